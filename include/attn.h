@@ -74,7 +74,9 @@ typedef enum {
                                        Hq not a multiple of Hkv, misalignment    */
     ATTN_ERR_UNSUPPORTED = 2,       /* D not 64/128, device is not sm_103        */
     ATTN_ERR_CUDA = 3,              /* a CUDA runtime/driver call failed          */
-    ATTN_ERR_DEVICE_TIMEOUT = 4     /* a kernel gave up on a bounded wait         */
+    ATTN_ERR_DEVICE_TIMEOUT = 4,    /* a kernel gave up on a bounded wait         */
+    ATTN_ERR_BAD_INDEX = 5          /* a kernel met a page number, a length or a
+                                       position outside its tensor (paged cache)  */
 } attn_status;
 
 /*
@@ -368,10 +370,115 @@ int attn_block_fwd(const void *x, const void *ln_gamma, const void *ln_beta, con
 size_t attn_block_workspace_bytes(int B, int S, int Hq, int Hkv, int D);
 
 /*
+ * The paged key/value cache. Keys and values live in pages of `page` tokens (a
+ * power of two, 16 to 256):
+ *   k_cache, v_cache   device, (n_pages, Hkv, page, D), contiguous, 16-byte
+ *               aligned. cache_kind ATTN_CACHE_16BIT: the type of k, v and q;
+ *               ATTN_CACHE_E4M3: 8-bit e4m3 codes of value / scale
+ *   k_scale, v_scale   device, FP32, (n_pages, Hkv): one scale per page and
+ *               K/V head (e4m3 only, else ignored and may be NULL)
+ *   block_table device, int32, (B, max_pages): page of tokens [j * page,
+ *               (j + 1) * page) of each sequence. Sequences may share pages that
+ *               are only read; a page that attn_kv_append writes must belong to
+ *               one sequence of the call
+ *   kv_lens     device, int32, (B): tokens of each sequence in the cache,
+ *               INCLUDING those of the current step, so that the append and the
+ *               attention of a step take the same tensor; at most
+ *               max_pages * page, itself at most 2^30
+ *   new_lens / q_lens  device, int32, (B): tokens of the step, 0 to S (Sq), or
+ *               NULL: S (Sq) each. Token s of sequence b sits at position
+ *               kv_lens[b] - new_lens[b] + s
+ * The lengths and page numbers are read on the device, so a captured graph can
+ * be replayed as they change. Out of range they fault nothing: the kernels
+ * leave out what they name (and hide the keys of such a page), and
+ * attn_last_status returns ATTN_ERR_BAD_INDEX.
+ */
+typedef enum {
+    ATTN_CACHE_16BIT = 0,
+    ATTN_CACHE_E4M3 = 1
+} attn_cache_kind;
+
+/*
+ * attn_kv_append / attn_kv_append_f16 — write a step's keys and values (bf16 /
+ * fp16) into the cache, the keys rotated to their positions on the way.
+ *   k, v        device, (B, S, Hkv, D), 16-byte aligned; D 64 or 128; a token's
+ *               (Hkv, D) values are contiguous and k_stride / v_stride (elements,
+ *               a multiple of 8, at least Hkv * D) lead from token to token of
+ *               the flattened (B, S): Hkv * D for contiguous tensors,
+ *               (Hq + 2 Hkv) * D inside a packed projection
+ *   rope_table, max_pos  the table of attn_rope_table for this D, or NULL: the
+ *               keys are stored as they come. A sequence with kv_lens > max_pos
+ *               is out of range
+ * 16-bit cache: rotated in FP32 and rounded once. e4m3: each page and head
+ * touched gets a scale 2^e, the smallest (>= 2^-100) with max |x| <= 448 * 2^e
+ * over its values; if the page held earlier tokens of the sequence and the new
+ * ones raise its scale, their codes are rescaled (exact but in e4m3's subnormal
+ * range). Rotated keys are quantised from FP32; infinities become +-448 codes
+ * and NaN stays NaN, neither sets the scale. A page whose slot 0 is written
+ * starts afresh, whatever its scale was. Slots behind the last token, pages the
+ * step does not touch and sequences with new_lens = 0 are left as they were.
+ */
+int attn_kv_append(const void *k, const void *v, long long k_stride, long long v_stride,
+                   void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                   const int *block_table, const int *kv_lens, const int *new_lens,
+                   int B, int S, int Hkv, int D, int page, int max_pages, int n_pages, int cache_kind,
+                   const float *rope_table, int max_pos, attn_stream_t stream);
+int attn_kv_append_f16(const void *k, const void *v, long long k_stride, long long v_stride,
+                       void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                       const int *block_table, const int *kv_lens, const int *new_lens,
+                       int B, int S, int Hkv, int D, int page, int max_pages, int n_pages, int cache_kind,
+                       const float *rope_table, int max_pos, attn_stream_t stream);
+
+/*
+ * attn_fwd_paged / attn_fwd_paged_f16 — attention of a step's queries over the
+ * cache, bf16 / fp16 Q and O. Query i of sequence b sits at position
+ * p = kv_lens[b] - q_lens[b] + i and sees the keys j <= p; with window > 0 only
+ * those with j > p - window or j < sinks (the first `sinks` tokens stay visible
+ * for good). One token per sequence, several draft tokens, or a chunk of a
+ * prompt. Slots behind kv_lens may hold anything. Keys that no query of the
+ * call sees are not read, or enter as zeros; a key that only some queries see
+ * must be finite in V, as for attn_fwd.
+ *   q           device, (B, Sq, Hq, D), 16-byte aligned, q_stride elements from
+ *               token to token (as k_stride above, at least Hq * D)
+ *   o, lse      device, (B, Sq, Hq, D) contiguous and FP32 (B, Hq, Sq). Rows with
+ *               no visible key get o = 0, lse = -inf; rows i >= q_lens[b] are not
+ *               written
+ *   scale       as for attn_fwd
+ *   window, sinks  >= 0; window 0: the whole past (sinks is then ignored)
+ *   rope_table, max_pos  as above: the queries are rotated to their positions
+ *               and rounded to their type, as attn_fwd_rope does; or NULL
+ *   workspace   device scratch of attn_paged_workspace_bytes(...) bytes, 256-byte
+ *               aligned, contents overwritten; its size does not depend on the
+ *               lengths. Calls, or replays of captured calls, that may run at the
+ *               same time need one each.
+ * Two launches: the attention, whose CTAs take equal shares of all visible keys,
+ * and the merge of the keys that several CTAs shared. Bound by the cache's reads
+ * up to 32 query rows (Sq * Hq / Hkv) a K/V head; more rows read it once per 32.
+ */
+int attn_fwd_paged(const void *q, long long q_stride, const void *k_cache, const void *v_cache,
+                   const float *k_scale, const float *v_scale,
+                   const int *block_table, const int *kv_lens, const int *q_lens, void *o, float *lse,
+                   int B, int Hq, int Hkv, int Sq, int D, int page, int max_pages, int n_pages, int cache_kind,
+                   float scale, int window, int sinks, const float *rope_table, int max_pos,
+                   void *workspace, size_t workspace_bytes, attn_stream_t stream);
+int attn_fwd_paged_f16(const void *q, long long q_stride, const void *k_cache, const void *v_cache,
+                       const float *k_scale, const float *v_scale,
+                       const int *block_table, const int *kv_lens, const int *q_lens, void *o, float *lse,
+                       int B, int Hq, int Hkv, int Sq, int D, int page, int max_pages, int n_pages, int cache_kind,
+                       float scale, int window, int sinks, const float *rope_table, int max_pos,
+                       void *workspace, size_t workspace_bytes, attn_stream_t stream);
+
+/* attn_paged_workspace_bytes — workspace bytes attn_fwd_paged needs for these
+ * sizes on the current device (host only; 0 for an empty problem or invalid
+ * sizes). */
+size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D);
+
+/*
  * attn_last_status — synchronises `stream`, then returns and clears the
  * current device's run-time status word: ATTN_OK, or ATTN_ERR_DEVICE_TIMEOUT
  * if any launch since the last call gave up on a bounded wait (the kernel then
- * stops early, leaves its outputs incomplete and releases what it holds), or
+ * stops early, leaves its outputs incomplete and releases what it holds),
+ * ATTN_ERR_BAD_INDEX if one met a page number, length or position out of range, or
  * ATTN_ERR_CUDA if the synchronisation itself failed.
  */
 int attn_last_status(attn_stream_t stream);

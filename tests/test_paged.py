@@ -1,0 +1,463 @@
+"""The paged key/value cache on the GPU: appending (rotation, 8-bit blocks, what stays untouched) and attention over
+the cache, against the plain 64-bit forms of paged_ref; bounds are derived there and beside each test."""
+import numpy as np
+import pytest
+import torch
+
+import paged_ref as R
+from transformer_attention_02_gb300 import attn as A
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda")
+BF, FP = torch.bfloat16, torch.float16
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def _status():
+    return A.attn_last_status(torch.cuda.current_stream().cuda_stream)
+
+
+def _rand(shape, dt, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(dt).to(DEV)
+
+
+class Cache:
+    """A cache with pages in shuffled order; 16-bit slots start as NaN, 8-bit ones as NaN codes."""
+
+    def __init__(self, B, Hkv, D, page, max_pages, dt, e4m3, seed=0, spare=2):
+        n = B * max_pages + spare
+        shape = (n, Hkv, page, D)
+        if e4m3:
+            self.k, self.v = (torch.full(shape, 0x7F, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+                              for _ in range(2))
+            self.ks, self.vs = (torch.full((n, Hkv), float("nan"), device=DEV) for _ in range(2))
+        else:
+            self.k, self.v = (torch.full(shape, float("nan"), dtype=dt, device=DEV) for _ in range(2))
+            self.ks = self.vs = None
+        perm = np.random.RandomState(seed).permutation(n)[:B * max_pages].reshape(B, max_pages)
+        self.table_np = perm.astype(np.int32)
+        self.table = _i32(self.table_np.tolist())
+        self.page = page
+
+    @property
+    def scales(self):
+        return dict(k_scale=self.ks, v_scale=self.vs)
+
+    def fill(self, b, n, seed):
+        """Random content for the first n tokens of sequence b; the rest stays NaN."""
+        page, (_, Hkv, _, D) = self.page, self.k.shape
+        g = np.random.RandomState(seed)
+        for t, s in ((self.k, self.ks), (self.v, self.vs)):
+            for j in range(-(-n // page)):
+                m = min(page, n - j * page)
+                x = torch.tensor(g.randn(Hkv, m, D) * 2.0 ** g.randint(-2, 3), dtype=torch.float32, device=DEV)
+                at = int(self.table_np[b, j])
+                if s is None:
+                    t[at, :, :m] = x.to(t.dtype)
+                else:
+                    sc = torch.tensor([R.block_scale(float(x[h].abs().max())) for h in range(Hkv)], device=DEV)
+                    s[at] = sc
+                    t.view(torch.uint8)[at, :, :m] = (x / sc[:, None, None]).to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+def _v_top(c, ids):
+    ids = torch.as_tensor(ids.astype(np.int64), device=DEV)
+    if c.vs is not None:
+        return float(torch.nan_to_num(c.vs[ids]).max()) * 448.0
+    return float(torch.nan_to_num(c.v[ids].float()).abs().max())
+
+
+def _check_attention(c, q, q_rot, o, lse, kv, ql, window=0, sinks=0, scale=None, label=""):
+    B, Sq, Hq, D = q.shape
+    p_step = R.step(q.dtype) if c.ks is None else R.step(FP)
+    sc = D ** -0.5 if scale is None else scale
+    for b in range(B):
+        n, L = ql[b], kv[b]
+        if n == 0:
+            continue
+        pos = np.arange(L - n, L)
+        k, v = (R.tokens(x, s, c.table_np[b], L, c.page) for x, s in ((c.k, c.ks), (c.v, c.vs)))
+        want = R.attend(R.f64(q_rot[b, :n]), k, v, pos, sc, window, sinks)
+        R.check_rows(R.f64(o[b, :n]), R.f64(lse[b, :, :n]), want, R.step(q.dtype), p_step, D, L,
+                     _v_top(c, c.table_np[b, :max(1, -(-L // c.page))]), f"{label} b={b}")
+
+
+# ------------------------------------------------------------------ append
+
+APPEND = [
+    # Hkv, D, page, tokens before per sequence, new per sequence, S, rope
+    (8, 128, 64, [0], [1], 1, True),                       # the very first token
+    (2, 64, 16, [15, 16, 17, 0], [1, 1, 1, 0], 1, True),   # last slot, fresh page, second slot, idle sequence
+    (3, 128, 32, [5, 0, 31], [70, 33, 1], 70, True),       # over several pages, ragged
+    (1, 64, 256, [100], [200], 200, False),                # not rotated
+    (4, 128, 16, [0, 7], [16, 9], 16, True),               # pages that end exactly full
+]
+
+
+@pytest.mark.parametrize("dt", [BF, FP], ids=["bf16", "f16"])
+@pytest.mark.parametrize("e4m3", [True, False], ids=["e4m3", "16bit"])
+@pytest.mark.parametrize("case", APPEND, ids=lambda c: f"H{c[0]}_D{c[1]}_p{c[2]}_{c[3]}+{c[4]}")
+def test_append(case, dt, e4m3):
+    Hkv, D, page, before, new, S, rope = case
+    B = len(before)
+    kv = [p + n for p, n in zip(before, new)]
+    max_pages = -(-max(kv) // page) + 1
+    c = Cache(B, Hkv, D, page, max_pages, dt, e4m3, seed=sum(kv))
+    for b in range(B):
+        c.fill(b, before[b], 100 + b)
+    was = {n: getattr(c, n).clone() for n in ("k", "v")}
+    was_s = None if not e4m3 else {"k": c.ks.clone(), "v": c.vs.clone()}
+    k, v = _rand((B, S, Hkv, D), dt, 1, 3.0), _rand((B, S, Hkv, D), dt, 2, 0.7)
+    table = A.rope_table(max_pages * page, D) if rope else None
+    A.kv_append(k, v, c.k, c.v, c.table, _i32(kv), new_lens=_i32(new), table=table, **c.scales)
+    assert _status() == A.ATTN_OK
+    touched = {"k": torch.zeros(c.k.shape[:3], dtype=torch.bool, device=DEV)}
+    for name, x, cache, scale in (("k", k, c.k, c.ks), ("v", v, c.v, c.vs)):
+        changed = torch.zeros(cache.shape[:3], dtype=torch.bool, device=DEV)
+        own_block = torch.zeros(cache.shape[:2], dtype=torch.bool, device=DEV)
+        for b in range(B):
+            pos = np.arange(before[b], kv[b])
+            x64 = R.f64(x[b, :new[b]])
+            want = R.rotate(x64, pos) if (rope and name == "k") else x64
+            # FP32 rotation: two products and a sum, each off by 2^-24 of the pair, and a table entry off by 2^-25
+            pair = np.repeat(np.abs(x64[..., 0::2]) + np.abs(x64[..., 1::2]), 2, axis=-1) * 2.0 ** -22
+            for j in sorted(set((pos // page).tolist())):
+                at, sel = int(c.table_np[b, j]), pos // page == j
+                slots = torch.as_tensor(pos[sel] % page, device=DEV)
+                for h in range(Hkv):
+                    got = R.f64(cache.float()[at, h][slots])
+                    w, e = want[sel][:, h], pair[sel][:, h]
+                    if e4m3:
+                        own_block[at, h] = True
+                        s = float(scale[at, h])
+                        need = R.block_scale(np.abs(w).max())
+                        old = int(pos[sel][0]) % page
+                        if old:
+                            s0 = float(was_s[name][at, h])
+                            need = max(need, s0)
+                            # earlier codes: moved by a power of two, exact but for half a subnormal step
+                            o0 = R.f64(was[name].float()[at, h, :old]) * s0
+                            o1 = R.f64(cache.float()[at, h, :old]) * s
+                            assert np.all(np.abs(o1 - o0) <= (0 if s == s0 else 2.0 ** -10 * s))
+                            changed[at, h, :old] = s != s0
+                        assert s == need, (name, b, j, h, s, need)
+                        tol = R.step(torch.float8_e4m3fn) * np.abs(w) + 2.0 ** -10 * s + e
+                        got = got * s
+                    else:
+                        tol = R.step(dt) * np.abs(w) + (e if name == "k" and rope else 0) + 2.0 ** -25
+                    assert np.all(np.abs(got - w) <= tol), (name, b, j, h)
+                changed[at, :, slots] = True
+        # everything else is as it was, byte for byte
+        same = cache.view(torch.uint8 if e4m3 else torch.int16) == was[name].view(torch.uint8 if e4m3 else torch.int16)
+        assert bool(same[~changed].all())
+        if e4m3:
+            assert bool((scale.view(torch.int32) == was_s[name].view(torch.int32))[~own_block].all())
+
+
+def test_append_grows_a_block_scale_and_keeps_earlier_values():
+    """Token magnitudes that double sixteen times within one page: every earlier code survives each growth until it
+    enters the subnormal range, where it loses at most half a subnormal step a growth."""
+    c = Cache(1, 1, 64, 32, 1, BF, True)
+    x = torch.stack([_rand((1, 64), BF, i) * 2.0 ** i for i in range(16)])[None]       # (1, 16, 1, 64)
+    for i in range(16):
+        A.kv_append(x[:, i:i + 1], x[:, i:i + 1], c.k, c.v, c.table, _i32([i + 1]), **c.scales)
+    s = float(c.vs[c.table_np[0, 0], 0])
+    got = R.f64(c.v.float()[c.table_np[0, 0], 0, :16]) * s
+    want = R.f64(x[0, :, 0])
+    # first quantisation, then half a subnormal step of each scale up to the last (their sum is below the last's step)
+    assert np.all(np.abs(got - want) <= 2.0 ** -4 * np.abs(want) + 2.0 ** -9 * s)
+    assert s == R.block_scale(np.abs(want).max())
+
+
+def test_append_of_zeros_infinities_and_nan():
+    c = Cache(1, 1, 64, 16, 1, BF, True)
+    x = torch.zeros((1, 3, 1, 64), dtype=BF, device=DEV)
+    x[0, 1, 0, :4] = torch.tensor([float("inf"), float("-inf"), float("nan"), 1.0])
+    A.kv_append(x[:, :1], x[:, :1], c.k, c.v, c.table, _i32([1]), **c.scales)
+    at = int(c.table_np[0, 0])
+    assert float(c.ks[at, 0]) == 2.0 ** -100 and bool((c.k.float()[at, 0, 0] == 0).all())
+    A.kv_append(x, x, c.k, c.v, c.table, _i32([3]), **c.scales)
+    assert float(c.ks[at, 0]) == R.block_scale(1.0) == float(c.vs[at, 0])
+    got = (c.k.float() * c.ks[:, :, None, None])[at, 0, 1, :4].cpu()
+    top = 448.0 * R.block_scale(1.0)
+    assert got[0] == top and got[1] == -top and torch.isnan(got[2]) and got[3] == 1.0
+
+
+def test_append_reads_slices_of_a_packed_projection():
+    B, S, Hq, Hkv, D = 3, 5, 4, 2, 64
+    qkv = _rand((B, S, (Hq + 2 * Hkv) * D), BF, 3)
+    k = qkv[..., Hq * D:(Hq + Hkv) * D].unflatten(-1, (Hkv, D))
+    v = qkv[..., (Hq + Hkv) * D:].unflatten(-1, (Hkv, D))
+    one, two = (Cache(B, Hkv, D, 16, 2, BF, True) for _ in range(2))
+    table, kv = A.rope_table(32, D), _i32([9, 20, 5])
+    A.kv_append(k, v, one.k, one.v, one.table, kv, table=table, **one.scales)
+    A.kv_append(k.contiguous(), v.contiguous(), two.k, two.v, two.table, kv, table=table, **two.scales)
+    assert torch.equal(one.k.view(torch.uint8), two.k.view(torch.uint8))
+    assert torch.equal(one.v.view(torch.uint8), two.v.view(torch.uint8))
+    last = k[:, 2:3], v[:, 2:3]                                            # one token each: the batch stride leads
+    A.kv_append(*last, one.k, one.v, one.table, kv, table=table, **one.scales)
+    A.kv_append(*(t.contiguous() for t in last), two.k, two.v, two.table, kv, table=table, **two.scales)
+    assert torch.equal(one.k.view(torch.uint8), two.k.view(torch.uint8))
+
+
+def test_append_leaves_out_what_is_out_of_range():
+    B, Hkv, D, page = 4, 2, 64, 16
+    c = Cache(B, Hkv, D, page, 2, FP, False)
+    c.table[1, 0] = c.k.shape[0]                                           # a page past the cache
+    c.table[2, 0] = -1
+    k = _rand((B, 3, Hkv, D), FP, 5)
+    was = c.k.clone()
+    A.kv_append(k, k, c.k, c.v, c.table, _i32([3, 3, 3, 33]))                # the last: longer than its table
+    assert _status() == A.ATTN_ERR_BAD_INDEX and _status() == A.ATTN_OK
+    at = int(c.table_np[0, 0])
+    assert torch.equal(c.k[at, :, :3], k[0].transpose(0, 1))
+    was[at] = c.k[at]
+    assert torch.equal(c.k.view(torch.int16), was.view(torch.int16))
+    A.kv_append(k, k, c.k, c.v, c.table, _i32([3, 0, 0, 2]), new_lens=_i32([0, 0, 0, 3]))   # more new than there are
+    assert _status() == A.ATTN_ERR_BAD_INDEX
+    assert torch.equal(c.k.view(torch.int16), was.view(torch.int16))
+
+
+# --------------------------------------------------------------- attention
+
+ATTEND = [
+    # Hq, Hkv, D, page, kv_lens, q_lens, Sq, window, sinks
+    (8, 2, 128, 64, [1], [1], 1, 0, 0),                            # one key
+    (32, 8, 128, 64, [500, 0, 129], [1, 1, 1], 1, 0, 0),           # an empty sequence among others
+    (4, 4, 64, 16, [77, 16, 17], [1, 1, 1], 1, 0, 0),              # MHA: one row a head
+    (7, 1, 128, 32, [1000, 31], [1, 1], 1, 0, 0),                  # a group of seven, MQA
+    (16, 1, 64, 128, [700], [1], 1, 0, 0),                         # sixteen rows
+    (64, 2, 128, 16, [300, 45], [1, 1], 1, 0, 0),                  # 32 rows
+    (6, 2, 128, 64, [900, 40, 5], [5, 3, 5], 5, 0, 0),             # several queries a sequence, ragged, 15 rows
+    (8, 2, 64, 32, [333, 20], [20, 20], 20, 0, 0),                 # 80 rows: three row blocks
+    (4, 1, 128, 16, [3, 9], [5, 9], 5 + 4, 0, 0),                  # more queries than keys: rows without a key
+    (8, 2, 128, 64, [2000, 1, 130], [1, 1, 1], 1, 100, 4),         # window and sinks, a gap between them
+    (8, 2, 128, 64, [2000, 600], [6, 2], 6, 300, 150),             # sinks past a unit
+    (4, 2, 64, 16, [513, 40], [3, 3], 3, 1, 0),                    # each query sees itself alone
+    (4, 2, 64, 256, [513, 40], [3, 0], 3, 1000000, 2),             # a window longer than the cache; an idle sequence
+]
+
+
+@pytest.mark.parametrize("dt", [BF, FP], ids=["bf16", "f16"])
+@pytest.mark.parametrize("e4m3", [True, False], ids=["e4m3", "16bit"])
+@pytest.mark.parametrize("case", ATTEND, ids=lambda c: "H{}-{}_D{}_p{}_{}_{}_w{}s{}".format(*c[:6], *c[7:]))
+def test_attention(case, dt, e4m3):
+    """Every slot no key occupies holds NaN, so a read of one shows."""
+    Hq, Hkv, D, page, kv, ql, Sq, window, sinks = case
+    B = len(kv)
+    c = Cache(B, Hkv, D, page, -(-max(kv) // page) + 1, dt, e4m3, seed=sum(kv))
+    for b in range(B):
+        c.fill(b, kv[b], b)
+    q = _rand((B, Sq, Hq, D), dt, 7)
+    o = torch.full_like(q, 5.0)
+    lse = torch.full((B, Hq, Sq), 5.0, device=DEV)
+    kw = dict(q_lens=_i32(ql), window=window, sinks=sinks, **c.scales)
+    A.attention_paged(q, c.k, c.v, c.table, _i32(kv), out=o, lse=lse, **kw)
+    assert _status() == A.ATTN_OK
+    for b in range(B):                                              # rows behind the last query are left alone
+        assert bool((o[b, ql[b]:] == 5.0).all()) and bool((lse[b, :, ql[b]:] == 5.0).all())
+    _check_attention(c, q, q, o, lse, kv, ql, window, sinks, label=str(case))
+    o2, lse2 = A.attention_paged(q, c.k, c.v, c.table, _i32(kv), out=o.clone(), lse=lse.clone(), **kw)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)            # and the same bits every time
+
+
+@pytest.mark.parametrize("e4m3", [True, False], ids=["e4m3", "16bit"])
+def test_attention_rotates_the_queries(e4m3):
+    kv, ql, Hq, Hkv, D = [300, 41, 3], [4, 4, 2], 8, 2, 128
+    c = Cache(3, Hkv, D, 32, 11, BF, e4m3)
+    for b in range(3):
+        c.fill(b, kv[b], b)
+    q, table = _rand((3, 4, Hq, D), BF, 8), A.rope_table(352, D)
+    o, lse = A.attention_paged(q, c.k, c.v, c.table, _i32(kv), q_lens=_i32(ql), table=table, **c.scales)
+    rot = q.clone()
+    for b in range(3):
+        rot[b, :ql[b]] = A.rope_apply(q[b:b + 1, :ql[b]].contiguous(), table, pos0=kv[b] - ql[b])[0]
+    _check_attention(c, q, rot, o, lse, kv, ql, label="rotated")
+
+
+@pytest.mark.parametrize("mag", [1e-20, 1e-5, 3e4])
+def test_attention_with_queries_of_any_magnitude(mag):
+    """bf16 queries far outside fp16's range over an 8-bit cache; the scale brings the logits back to order one."""
+    c = Cache(1, 2, 64, 16, 20, BF, True)
+    c.fill(0, 300, 3)
+    q = _rand((1, 1, 4, 64), BF, 9, mag)
+    q[0, 0, 3] = 0
+    sc = 0.1 / mag
+    o, lse = A.attention_paged(q, c.k, c.v, c.table, _i32([300]), scale=sc, **c.scales)
+    _check_attention(c, q, q, o, lse, [300], [1], scale=float(np.float32(sc)), label=str(mag))
+
+
+def test_attention_with_one_dominant_key_late_in_a_long_cache():
+    """The running maximum jumps by far more than the lazy threshold on the last page, and value scales differ by 2^40
+    between pages."""
+    c = Cache(1, 1, 128, 64, 64, BF, True)
+    c.fill(0, 4000, 4)
+    for j in range(63):
+        at = int(c.table_np[0, j])
+        c.vs[at] *= 2.0 ** ((j * 7) % 41 - 20)
+    q = _rand((1, 1, 8, 128), BF, 10, 6.0)
+    o, lse = A.attention_paged(q, c.k, c.v, c.table, _i32([4000]), **c.scales)
+    _check_attention(c, q, q, o, lse, [4000], [1], label="dominant")
+
+
+def test_attention_never_reads_hidden_values():
+    """Keys and values before the window hold NaN: one query a sequence, so no query sees them."""
+    c = Cache(2, 2, 128, 64, 12, FP, False)
+    for b, n in enumerate((700, 650)):
+        c.fill(b, n, b)
+    q = _rand((2, 1, 4, 128), FP, 11)
+    clean = A.attention_paged(q, c.k, c.v, c.table, _i32([700, 650]), window=77, sinks=3)
+    for b, n in enumerate((700, 650)):
+        for j in range(3, n - 77):
+            c.k[int(c.table_np[b, j // 64]), :, j % 64] = float("nan")
+            c.v[int(c.table_np[b, j // 64]), :, j % 64] = float("inf")
+    o, lse = A.attention_paged(q, c.k, c.v, c.table, _i32([700, 650]), window=77, sinks=3)
+    assert torch.equal(o, clean[0]) and torch.equal(lse, clean[1])
+
+
+def test_attention_hides_pages_out_of_range():
+    c = Cache(2, 2, 64, 16, 4, FP, False)
+    c.fill(0, 64, 0), c.fill(1, 64, 1)
+    q = _rand((2, 1, 4, 64), FP, 12)
+    kv = _i32([64, 64])
+    c.table[0, 1] = c.k.shape[0] + 5
+    o, lse = A.attention_paged(q, c.k, c.v, c.table, kv)
+    assert _status() == A.ATTN_ERR_BAD_INDEX and _status() == A.ATTN_OK
+    k, v = (R.tokens(x, None, c.table_np[0], 64, 16)[np.r_[0:16, 32:64]] for x in (c.k, c.v))
+    want = R.attend(R.f64(q[0]), k, v, np.array([47]), 64 ** -0.5, 0, 0)
+    R.check_rows(R.f64(o[0]), R.f64(lse[0]), want, R.step(FP), R.step(FP), 64, 64, _v_top(c, c.table_np[0]), "hidden page")
+    # a length past the table is cut to it, a negative one to nothing
+    c.table[0, 1] = int(c.table_np[0, 1])
+    full = A.attention_paged(q, c.k, c.v, c.table, kv)
+    o, lse = A.attention_paged(q, c.k, c.v, c.table, _i32([1 << 30, -4]))
+    assert _status() == A.ATTN_ERR_BAD_INDEX
+    assert torch.equal(o[0], full[0][0]) and bool((o[1] == 0).all()) and bool((lse[1] == float("-inf")).all())
+
+
+def test_sequences_may_share_read_pages():
+    c = Cache(2, 2, 64, 16, 4, BF, True)
+    c.fill(0, 60, 0)
+    c.table[1] = c.table[0]
+    q = _rand((1, 1, 4, 64), BF, 13).expand(2, -1, -1, -1).contiguous()
+    o, lse = A.attention_paged(q, c.k, c.v, c.table, _i32([60, 60]), **c.scales)
+    assert torch.equal(o[0], o[1]) and torch.equal(lse[0], lse[1])
+
+
+def test_offsets_past_32_bits():
+    """A cache of more than 2^32 bytes a tensor; the sequence's pages are its last ones."""
+    Hkv, page, D = 8, 256, 128
+    n = (1 << 32) // (Hkv * page * D) + 40
+    k = torch.empty((n, Hkv, page, D), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    v = torch.empty_like(k.view(torch.uint8)).view(torch.float8_e4m3fn)
+    ks, vs = torch.zeros((n, Hkv), device=DEV), torch.zeros((n, Hkv), device=DEV)
+    table, kv = _i32([[n - 1, n - 3]]), _i32([400])
+    x = _rand((1, 400, Hkv, D), BF, 14)
+    A.kv_append(x, x, k, v, table, kv, k_scale=ks, v_scale=vs)
+    q = _rand((1, 1, Hkv, D), BF, 15)
+    o, lse = A.attention_paged(q, k, v, table, kv, k_scale=ks, v_scale=vs)
+    small = [torch.stack([t[n - 1], t[n - 3]]).contiguous() for t in (k.view(torch.uint8), v.view(torch.uint8), ks, vs)]
+    o2, lse2 = A.attention_paged(q, small[0].view(torch.float8_e4m3fn), small[1].view(torch.float8_e4m3fn),
+                                 _i32([[0, 1]]), kv, k_scale=small[2], v_scale=small[3])
+    assert torch.equal(o, o2) and torch.equal(lse, lse2) and bool(torch.isfinite(lse).all())
+
+
+def test_large_ragged_batch_over_many_ctas():
+    """More segments than CTAs, lengths from 0 to several units, against a per-sequence call of its own."""
+    B, Hkv, Hq, D, page = 300, 2, 8, 64, 16
+    kv = [(37 * b) % 400 for b in range(B)]
+    c = Cache(B, Hkv, D, page, 26, BF, True)
+    c.k.view(torch.uint8).random_(0, 0x7E), c.v.view(torch.uint8).random_(0, 0x7E)
+    c.ks.uniform_(0.001, 0.01), c.vs.uniform_(0.001, 0.01)
+    q = _rand((B, 1, Hq, D), BF, 16)
+    o, lse = A.attention_paged(q, c.k, c.v, c.table, _i32(kv), **c.scales)
+    for b in range(0, B, 23):
+        _check_attention(_Row(c, b), q[b:b + 1], q[b:b + 1], o[b:b + 1], lse[b:b + 1], [kv[b]], [1], label=f"row {b}")
+
+
+class _Row:
+    def __init__(self, c, b):
+        self.k, self.v, self.ks, self.vs, self.page, self.table_np = c.k, c.v, c.ks, c.vs, c.page, c.table_np[b:b + 1]
+
+
+# ------------------------------------------------------------ used together
+
+def test_graph_of_a_decode_step_replays_as_lengths_and_pages_change():
+    B, Hq, Hkv, D, page, P = 3, 8, 2, 128, 16, 6
+    c = Cache(B, Hkv, D, page, P, BF, True)
+    table, kv = A.rope_table(P * page, D), _i32([0] * B)
+    x = [_rand((B, 40, H, D), BF, 20 + i) for i, H in enumerate((Hq, Hkv, Hkv))]
+    q, k, v = (torch.empty((B, 1, t.shape[2], D), dtype=BF, device=DEV) for t in x)
+    out, lse = torch.empty_like(q), torch.empty((B, Hq, 1), device=DEV)
+    ws = torch.empty(A.attn_paged_workspace_bytes(B, Hq, Hkv, 1, D), dtype=torch.uint8, device=DEV)
+
+    def step():
+        A.kv_append(k, v, c.k, c.v, c.table, kv, table=table, **c.scales)
+        A.attention_paged(q, c.k, c.v, c.table, kv, table=table, out=out, lse=lse, workspace=ws, **c.scales)
+
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):                                        # first use: module loading, outside the capture
+        kv.fill_(1), q.zero_(), k.zero_(), v.zero_()
+        step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for i in range(40):
+        for a, b in zip((q, k, v), x):
+            a.copy_(b[:, i:i + 1])
+        kv.fill_(i + 1)
+        g.replay()
+    torch.cuda.synchronize()
+    assert _status() == A.ATTN_OK
+    rot = torch.stack([A.rope_apply(q[b:b + 1], table, pos0=39)[0] for b in range(B)])
+    _check_attention(c, q, rot, out, lse, [40] * B, [1] * B, label="graph")
+    eager = Cache(B, Hkv, D, page, P, BF, True)
+    for i in range(40):
+        A.kv_append(x[1][:, i:i + 1], x[2][:, i:i + 1], eager.k, eager.v, eager.table, _i32([i + 1] * B), table=table,
+                    **eager.scales)
+    o2, l2 = A.attention_paged(q, eager.k, eager.v, eager.table, _i32([40] * B), table=table, **eager.scales)
+    assert torch.equal(o2, out) and torch.equal(l2, lse)
+
+
+def test_side_stream():
+    c = Cache(1, 2, 64, 16, 8, BF, True)
+    c.fill(0, 100, 0)
+    q = _rand((1, 1, 4, 64), BF, 30)
+    want = A.attention_paged(q, c.k, c.v, c.table, _i32([100]), **c.scales)
+    s, kv = torch.cuda.Stream(), _i32([100])
+    torch.cuda.synchronize()
+    o, lse = A.attention_paged(q, c.k, c.v, c.table, kv, stream=s, **c.scales)
+    assert A.attn_last_status(s.cuda_stream) == A.ATTN_OK
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("e4m3", [True, False], ids=["e4m3", "16bit"])
+def test_prompt_then_decode_steps(e4m3):
+    """A prompt enters the cache in two chunks, then tokens one at a time; each step's attention is checked over what the
+    cache holds, and with a 16-bit cache the prompt's against attention() on the contiguous rotated tensors."""
+    B, Hq, Hkv, D, page, n = 2, 8, 2, 128, 32, 150
+    c = Cache(B, Hkv, D, page, 6, BF, e4m3)
+    table = A.rope_table(6 * page, D)
+    q, k, v = (_rand((B, n, H, D), BF, 40 + i) for i, H in enumerate((Hq, Hkv, Hkv)))
+    at, outs = 0, []
+    for m in (70, 50) + (1,) * 30:
+        kv = _i32([at + m] * B)
+        A.kv_append(k[:, at:at + m].contiguous(), v[:, at:at + m].contiguous(), c.k, c.v, c.table, kv, table=table,
+                    **c.scales)
+        qs = q[:, at:at + m].contiguous()
+        o, lse = A.attention_paged(qs, c.k, c.v, c.table, kv, table=table, **c.scales)
+        if m > 1 or at == n - 1:
+            _check_attention(c, qs, A.rope_apply(qs, table, pos0=at), o, lse, [at + m] * B, [m] * B, label=f"at {at}")
+        outs.append(o)
+        at += m
+    if not e4m3:
+        dense, _ = A.attention(A.rope_apply(q, table), A.rope_apply(k, table), v, causal=True)
+        # the two paths round the same weights to bf16 separately: 2^-8 of sum p|v| each, and the outputs once each
+        d = (torch.cat(outs, 1).float() - dense.float()).abs()
+        bound = 2 * 2.0 ** -8 * dense.float().abs() + 2 * (2.0 ** -8 + 2.0 ** -14) * v.float().abs().amax()
+        assert bool((d <= bound).all())

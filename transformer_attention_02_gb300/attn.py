@@ -18,6 +18,8 @@ from . import build as _build
 
 MASK_NONE, MASK_CAUSAL, MASK_ADDITIVE, MASK_CAUSAL_ADDITIVE = 0, 1, 2, 3
 ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA, ATTN_ERR_DEVICE_TIMEOUT = 0, 1, 2, 3, 4
+ATTN_ERR_BAD_INDEX = 5
+CACHE_16BIT, CACHE_E4M3 = 0, 1
 
 _lib = None
 
@@ -80,6 +82,15 @@ def lib() -> ctypes.CDLL:
     L.attn_splitkv_num_splits.restype = I
     L.attn_splitkv_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
     L.attn_splitkv_workspace_bytes.restype = ctypes.c_size_t
+    LL, F = ctypes.c_longlong, ctypes.c_float
+    for f in (L.attn_kv_append, L.attn_kv_append_f16):
+        f.argtypes = [P, P, LL, LL, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, I, P]
+        f.restype = I
+    for f in (L.attn_fwd_paged, L.attn_fwd_paged_f16):
+        f.argtypes = [P, LL, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, I, I, P, I, P, ctypes.c_size_t, P]
+        f.restype = I
+    L.attn_paged_workspace_bytes.argtypes = [I, I, I, I, I]
+    L.attn_paged_workspace_bytes.restype = ctypes.c_size_t
     L.attn_last_status.argtypes = [P]
     L.attn_last_status.restype = I
     L.attn_status_string.argtypes = [I]
@@ -191,6 +202,40 @@ def attn_splitkv_num_splits(B, Hq, Hkv, Sq, Sk, num_splits=0) -> int:
 
 def attn_splitkv_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, num_splits=0) -> int:
     return int(lib().attn_splitkv_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, num_splits))
+
+
+def attn_kv_append(k, v, k_stride, v_stride, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, new_lens, B, S,
+                   Hkv, D, page, max_pages, n_pages, cache_kind, rope_table, max_pos, stream) -> int:
+    return lib().attn_kv_append(k, v, k_stride, v_stride, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens,
+                                new_lens, B, S, Hkv, D, page, max_pages, n_pages, cache_kind, rope_table, max_pos,
+                                stream)
+
+
+def attn_kv_append_f16(k, v, k_stride, v_stride, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, new_lens, B,
+                       S, Hkv, D, page, max_pages, n_pages, cache_kind, rope_table, max_pos, stream) -> int:
+    return lib().attn_kv_append_f16(k, v, k_stride, v_stride, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens,
+                                    new_lens, B, S, Hkv, D, page, max_pages, n_pages, cache_kind, rope_table, max_pos,
+                                    stream)
+
+
+def attn_fwd_paged(q, q_stride, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, q_lens, o, lse, B, Hq, Hkv,
+                   Sq, D, page, max_pages, n_pages, cache_kind, scale, window, sinks, rope_table, max_pos, workspace,
+                   workspace_bytes, stream) -> int:
+    return lib().attn_fwd_paged(q, q_stride, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, q_lens, o, lse,
+                                B, Hq, Hkv, Sq, D, page, max_pages, n_pages, cache_kind, scale, window, sinks,
+                                rope_table, max_pos, workspace, workspace_bytes, stream)
+
+
+def attn_fwd_paged_f16(q, q_stride, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, q_lens, o, lse, B, Hq,
+                       Hkv, Sq, D, page, max_pages, n_pages, cache_kind, scale, window, sinks, rope_table, max_pos,
+                       workspace, workspace_bytes, stream) -> int:
+    return lib().attn_fwd_paged_f16(q, q_stride, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, q_lens, o,
+                                    lse, B, Hq, Hkv, Sq, D, page, max_pages, n_pages, cache_kind, scale, window, sinks,
+                                    rope_table, max_pos, workspace, workspace_bytes, stream)
+
+
+def attn_paged_workspace_bytes(B, Hq, Hkv, Sq, D) -> int:
+    return int(lib().attn_paged_workspace_bytes(B, Hq, Hkv, Sq, D))
 
 
 def attn_last_status(stream) -> int:
@@ -519,3 +564,168 @@ def attention_block(x, ln_gamma, ln_beta, w_qkv, b_qkv, w_o, b_o, *, Hq: int, Hk
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_block_fwd")
     return out
+
+
+# ------------------------------------------------------- paged key/value cache
+
+def _token_stride(name, t, dev):
+    """Elements from token to token of a (B, S, H, D) tensor whose tokens are evenly spaced and contiguous inside
+    (a contiguous tensor, or a slice of a packed projection)."""
+    if t.dim() != 4:
+        raise ValueError(f"{name} must have 4 dimensions (B, S, H, D)")
+    if t.device != dev or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on the other tensors' device")
+    B, S, H, D = t.shape
+    if t.is_contiguous():
+        return H * D
+    sb, ss, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if S == 1:
+        return sb if B > 1 else max(ss, H * D)
+    if B > 1 and sb != S * ss:
+        raise ValueError(f"{name}: the tokens of the flattened (B, S) must be evenly spaced")
+    return ss
+
+
+def _int32(name, t, shape, dev):
+    import torch
+    if not (t.dtype == torch.int32 and t.device == dev and t.is_contiguous() and tuple(t.shape) == shape):
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of shape {shape} on the other tensors' device")
+    return t.data_ptr()
+
+
+def _cache_args(x, xname, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, lens, lens_name, table):
+    """Checks what the cache's calls share; returns their common arguments."""
+    import torch
+    dev = x.device
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"{xname} must be bf16 or fp16")
+    if not (k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype
+            and k_cache.device == dev and v_cache.device == dev and k_cache.is_contiguous()
+            and v_cache.is_contiguous()):
+        raise ValueError(f"k_cache and v_cache must be contiguous (n_pages, Hkv, page, D) tensors of one type on "
+                         f"{xname}'s device")
+    n_pages, Hkv, page, D = k_cache.shape
+    ks = vs = None
+    if k_cache.dtype == torch.float8_e4m3fn:
+        kind = CACHE_E4M3
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is None or not (t.dtype == torch.float32 and t.device == dev and t.is_contiguous()
+                                 and tuple(t.shape) == (n_pages, Hkv)):
+                raise ValueError(f"{name} must be a contiguous FP32 CUDA tensor of shape (n_pages, Hkv): an 8-bit cache "
+                                 "needs its scales")
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    elif k_cache.dtype == x.dtype:
+        kind = CACHE_16BIT
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("a 16-bit cache has no scales")
+    else:
+        raise ValueError(f"the cache must be float8_e4m3fn or of {xname}'s type")
+    B = x.shape[0]
+    if block_table.dim() != 2:
+        raise ValueError("block_table must have 2 dimensions (B, max_pages)")
+    max_pages = block_table.shape[1]
+    bt = _int32("block_table", block_table, (B, max_pages), dev)
+    kl = _int32("kv_lens", kv_lens, (B,), dev)
+    nl = None if lens is None else _int32(lens_name, lens, (B,), dev)
+    rope, max_pos = None, 0
+    if table is not None:
+        if not (table.dtype == torch.float32 and table.dim() == 3 and tuple(table.shape[1:]) == (D // 2, 2)
+                and table.device == dev and table.is_contiguous()):
+            raise ValueError("table must be the (max_pos, D/2, 2) FP32 CUDA tensor of rope_table() for this D")
+        rope, max_pos = table.data_ptr(), table.shape[0]
+    return kind, ks, vs, bt, kl, nl, Hkv, D, page, max_pages, n_pages, rope, max_pos
+
+
+class _on_device:
+    """Makes a tensor's device current for a call, if it is not (the C ABI works on the current device)."""
+
+    def __init__(self, dev):
+        self.dev, self.back = dev, None
+
+    def __enter__(self):
+        import torch
+        at = torch.cuda.current_device()
+        if self.dev.index is not None and self.dev.index != at:
+            self.back = at
+            torch.cuda.set_device(self.dev)
+
+    def __exit__(self, *exc):
+        import torch
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def kv_append(k, v, k_cache, v_cache, block_table, kv_lens, *, new_lens=None, k_scale=None, v_scale=None, table=None,
+              stream=None):
+    """Write a step's keys and values (B, S, Hkv, D) into a paged cache, in place.
+
+    k, v: bf16/fp16 CUDA tensors, contiguous or evenly spaced slices of a packed projection.
+    k_cache, v_cache: (n_pages, Hkv, page, D), of k's type or float8_e4m3fn; the latter with k_scale, v_scale
+    (n_pages, Hkv) FP32, which the call updates. block_table (B, max_pages), kv_lens (B) and new_lens (B, default S
+    each) are int32; kv_lens counts the step's tokens already: token s of sequence b goes to position
+    kv_lens[b] - new_lens[b] + s. table: rope_table() to rotate the keys to their positions, or None.
+    """
+    import torch
+    a = _cache_args(k, "k", k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, new_lens, "new_lens", table)
+    kind, ks, vs, bt, kl, nl, Hkv, D, page, max_pages, n_pages, rope, max_pos = a
+    if v.dtype != k.dtype or v.shape != k.shape or k.dim() != 4 or k.shape[2] != Hkv or k.shape[3] != D:
+        raise ValueError("k and v must be (B, S, Hkv, D) tensors of one type, with the cache's Hkv and D")
+    B, S = k.shape[0], k.shape[1]
+    k_stride, v_stride = _token_stride("k", k, k.device), _token_stride("v", v, k.device)
+    fn = attn_kv_append if k.dtype == torch.bfloat16 else attn_kv_append_f16
+    with _on_device(k.device):
+        rc = fn(k.data_ptr(), v.data_ptr(), k_stride, v_stride, k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, bt, kl,
+                nl, B, S, Hkv, D, page, max_pages, n_pages, kind, rope, max_pos, _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_kv_append")
+
+
+def attention_paged(q, k_cache, v_cache, block_table, kv_lens, *, q_lens=None, k_scale=None, v_scale=None, table=None,
+                    window: int = 0, sinks: int = 0, scale=None, out=None, lse=None, workspace=None, stream=None):
+    """O, LSE = causal attention of a step's queries (B, Sq, Hq, D) over a paged cache (see kv_append).
+
+    Query i of sequence b sits at position kv_lens[b] - q_lens[b] + i (q_lens: default Sq each) and sees the keys up
+    to it; window > 0: only the last `window` of them and the first `sinks` tokens. table: rope_table() to rotate the
+    queries to their positions, or None. Rows i >= q_lens[b] of out and lse are not written. workspace: optional
+    uint8 CUDA tensor of at least attn_paged_workspace_bytes bytes (allocated here when omitted).
+    """
+    import torch
+    a = _cache_args(q, "q", k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, q_lens, "q_lens", table)
+    kind, ks, vs, bt, kl, nl, Hkv, D, page, max_pages, n_pages, rope, max_pos = a
+    dev = q.device
+    q_stride = _token_stride("q", q, dev)
+    B, Sq, Hq = q.shape[0], q.shape[1], q.shape[2]
+    if q.shape[3] != D:
+        raise ValueError("q and the cache disagree on D")
+    with _on_device(dev):
+        made = []
+        if out is None:
+            out = torch.empty((B, Sq, Hq, D), dtype=q.dtype, device=dev)
+            made.append(out)
+        elif not (out.dtype == q.dtype and out.device == dev and tuple(out.shape) == (B, Sq, Hq, D)
+                  and out.is_contiguous()):
+            raise ValueError("out must be a contiguous (B, Sq, Hq, D) tensor of q's type and device")
+        if lse is None:
+            lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=dev)
+            made.append(lse)
+        elif not (lse.dtype == torch.float32 and lse.device == dev and tuple(lse.shape) == (B, Hq, Sq)
+                  and lse.is_contiguous()):
+            raise ValueError("lse must be a contiguous FP32 (B, Hq, Sq) tensor on q's device")
+        if workspace is None:
+            workspace = torch.empty(attn_paged_workspace_bytes(B, Hq, Hkv, Sq, D) or 1, dtype=torch.uint8, device=dev)
+            made.append(workspace)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
+        if stream is not None:
+            for t in made:                     # allocated on the current stream, used on another
+                t.record_stream(stream)
+        sc = float("nan") if scale is None else float(scale)
+        fn = attn_fwd_paged if q.dtype == torch.bfloat16 else attn_fwd_paged_f16
+        rc = fn(q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, bt, kl, nl, out.data_ptr(),
+                lse.data_ptr(), B, Hq, Hkv, Sq, D, page, max_pages, n_pages, kind, sc, int(window), int(sinks), rope,
+                max_pos, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_fwd_paged")
+    return out, lse

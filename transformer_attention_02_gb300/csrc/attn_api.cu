@@ -22,10 +22,11 @@
 #include "attn_kernel.cuh"
 #include "attn_launch.h"
 #include "block_params.h"
+#include "paged_params.h"
 
 namespace {
 
-constexpr int kAbiVersion = 5;
+constexpr int kAbiVersion = 6;
 constexpr unsigned long long kDefaultTimeoutNs = 2000000000ull;
 constexpr int kMaxContexts = 64;
 
@@ -49,6 +50,7 @@ struct DeviceInfo {
     bool smem_attr_set[2][4][2][3] = {};   // [D is 128][mask kind][bf16][plain, rotary, packed]
     bool gemm_attr_set = false;
     bool ln_attr_set[3] = {};
+    bool paged_attr_set[3][2][3] = {};     // [cache type][D is 128][rows of a block]
 };
 
 std::mutex g_mutex;
@@ -131,6 +133,16 @@ int attn::current_context_id(unsigned long long* id) {
     if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
     std::lock_guard<std::mutex> lock(g_mutex);
     return context_id_for(dev, id);
+}
+
+int attn::device_state(DeviceState* out) {
+    DeviceInfo* d = nullptr;
+    const int rc = device_info(&d);
+    if (rc != ATTN_OK) return rc;
+    out->num_sms = d->num_sms;
+    out->status = d->status;
+    out->paged_attr_set = d->paged_attr_set;
+    return ATTN_OK;
 }
 
 namespace {
@@ -318,6 +330,12 @@ int current_sm_count() {
     }
     return sms;
 }
+
+}  // namespace
+
+int attn::device_sm_count() { return current_sm_count(); }
+
+namespace {
 
 // Head packing (see tile_info): the query heads of a K/V group share each
 // tile's rows when the group is a power of two and the whole query sequence
@@ -871,7 +889,8 @@ int attn_last_status(attn_stream_t stream) {
     unsigned int word = 0, zero = 0;
     if (cudaMemcpyFromSymbol(&word, g_device_status, sizeof word) != cudaSuccess) return ATTN_ERR_CUDA;
     if (word != 0 && cudaMemcpyToSymbol(g_device_status, &zero, sizeof zero) != cudaSuccess) return ATTN_ERR_CUDA;
-    return (word & attn::kStatusTimeout) ? ATTN_ERR_DEVICE_TIMEOUT : ATTN_OK;
+    if (word & attn::kStatusTimeout) return ATTN_ERR_DEVICE_TIMEOUT;
+    return (word & attn::paged::kStatusBadIndex) ? ATTN_ERR_BAD_INDEX : ATTN_OK;
 }
 
 const char* attn_status_string(int code) {
@@ -881,6 +900,7 @@ const char* attn_status_string(int code) {
         case ATTN_ERR_UNSUPPORTED: return "ATTN_ERR_UNSUPPORTED";
         case ATTN_ERR_CUDA: return "ATTN_ERR_CUDA";
         case ATTN_ERR_DEVICE_TIMEOUT: return "ATTN_ERR_DEVICE_TIMEOUT";
+        case ATTN_ERR_BAD_INDEX: return "ATTN_ERR_BAD_INDEX";
         default: return "ATTN_UNKNOWN_STATUS";
     }
 }

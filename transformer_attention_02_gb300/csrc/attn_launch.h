@@ -29,4 +29,18 @@ int launch_fwd(bool& attr_set, const CUtensorMap& tq, const CUtensorMap& tk, con
 // library are keyed by it. Returns ATTN_OK or ATTN_ERR_CUDA.
 int current_context_id(unsigned long long* id);
 
+// What the entry points outside attn_api.cu need of the current context.
+struct DeviceState {
+    int num_sms;
+    unsigned int* status;                 // run-time status word
+    bool (*paged_attr_set)[2][3];         // [cache type]: see paged::launch_attend
+};
+
+// Fills `out` for the current context. Returns ATTN_OK, ATTN_ERR_UNSUPPORTED
+// (not an sm_103 device) or ATTN_ERR_CUDA.
+int device_state(DeviceState* out);
+
+// SM count of the current device (148 when it cannot be read, e.g. no GPU).
+int device_sm_count();
+
 }  // namespace attn

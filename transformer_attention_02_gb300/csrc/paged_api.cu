@@ -1,0 +1,216 @@
+// Entry points of the paged key/value cache (declared in include/attn.h):
+// argument checks, workspace layout and launches of the append and of the
+// attention over the cache.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/attn.h"
+#include "attn_launch.h"
+#include "paged_params.h"
+
+namespace {
+
+using namespace attn;
+
+bool aligned(const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
+
+constexpr size_t kWorkspaceAlign = 256;
+size_t align_up(size_t x) { return (x + kWorkspaceAlign - 1) / kWorkspaceAlign * kWorkspaceAlign; }
+
+// Sizes the append and the attention share. A page holds a power of two of
+// tokens, 16 to 256; every product that indexes memory fits its type.
+int check_cache(int B, int S, int Hkv, int D, int page, int max_pages, int n_pages, int cache) {
+    if (B < 0 || S < 0 || Hkv <= 0 || D <= 0 || max_pages <= 0 || n_pages <= 0) return ATTN_ERR_INVALID_ARG;
+    if (cache != ATTN_CACHE_16BIT && cache != ATTN_CACHE_E4M3) return ATTN_ERR_INVALID_ARG;
+    if (page < 16 || page > 256 || (page & (page - 1)) != 0) return ATTN_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)max_pages * page > (1 << 30) || S > (1 << 30)) return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+
+bool rope_ok(const float* table, int max_pos) { return !table || (aligned(table, 16) && max_pos > 0); }
+
+int page_shift_of(int page) {
+    int s = 0;
+    while ((1 << s) < page) ++s;
+    return s;
+}
+
+int kv_append_impl(const void* k, const void* v, long long k_stride, long long v_stride, void* k_cache, void* v_cache,
+                   float* k_scale, float* v_scale, const int* block_table, const int* kv_lens, const int* new_lens,
+                   int B, int S, int Hkv, int D, int page, int max_pages, int n_pages, int cache,
+                   const float* rope_table, int max_pos, cudaStream_t stream, bool bf16) {
+    int rc = check_cache(B, S, Hkv, D, page, max_pages, n_pages, cache);
+    if (rc != ATTN_OK) return rc;
+    if (B == 0 || S == 0) return ATTN_OK;
+    if (!k || !v || !k_cache || !v_cache || !block_table || !kv_lens) return ATTN_ERR_INVALID_ARG;
+    const bool e4m3 = cache == ATTN_CACHE_E4M3;
+    if (e4m3 && (!k_scale || !v_scale)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) ||
+        !aligned(v_scale, 4) || !aligned(block_table, 4) || !aligned(kv_lens, 4) || !aligned(new_lens, 4))
+        return ATTN_ERR_INVALID_ARG;
+    if (k_stride < (long long)Hkv * D || v_stride < (long long)Hkv * D || k_stride % 8 != 0 || v_stride % 8 != 0)
+        return ATTN_ERR_INVALID_ARG;
+    if (!rope_ok(rope_table, max_pos)) return ATTN_ERR_INVALID_ARG;
+    const int touched = (int)std::min<long long>(max_pages, ((long long)S + page - 2) / page + 1);
+    if ((long long)B * touched * Hkv * 2 > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+
+    DeviceState dev{};
+    rc = device_state(&dev);
+    if (rc != ATTN_OK) return rc;
+    paged::AppendParams p{};
+    p.k = static_cast<const uint16_t*>(k);
+    p.v = static_cast<const uint16_t*>(v);
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.block_table = block_table;
+    p.kv_lens = kv_lens;
+    p.new_lens = new_lens;
+    p.rope = rope_table;
+    p.max_pos = max_pos;
+    p.B = B;
+    p.S = S;
+    p.Hkv = Hkv;
+    p.D = D;
+    p.page_shift = page_shift_of(page);
+    p.max_pages = max_pages;
+    p.n_pages = n_pages;
+    p.touched = touched;
+    p.bf16 = bf16;
+    p.status = dev.status;
+    return paged::launch_append(p, e4m3 ? paged::kE4m3 : bf16 ? paged::kBf16 : paged::kF16, dev.num_sms, stream);
+}
+
+// Workspace of the attention: the first unit of every sequence, then two FP32
+// parts (unnormalised O, maximum, sum) for each CTA. Independent of the lengths.
+size_t attend_workspace(int B, int rows, int D, int sms, size_t* part_off) {
+    const int rb = paged::block_rows(rows);
+    *part_off = align_up((size_t)(B + 1) * sizeof(int));
+    return *part_off + (size_t)sms * paged::resident_ctas(rb) * 2 * rb * (D + 2) * sizeof(float);
+}
+
+int attend_impl(const void* q, long long q_stride, const void* k_cache, const void* v_cache, const float* k_scale,
+                const float* v_scale, const int* block_table, const int* kv_lens, const int* q_lens, void* o, float* lse,
+                int B, int Hq, int Hkv, int Sq, int D, int page, int max_pages, int n_pages, int cache, float scale,
+                int window, int sinks, const float* rope_table, int max_pos, void* workspace, size_t workspace_bytes,
+                cudaStream_t stream, bool bf16) {
+    int rc = check_cache(B, Sq, Hkv, D, page, max_pages, n_pages, cache);
+    if (rc != ATTN_OK) return rc;
+    if (Hq < 0 || Hq % Hkv != 0 || window < 0 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+    if (B == 0 || Sq == 0 || Hq == 0) return ATTN_OK;
+    if (!q || !k_cache || !v_cache || !block_table || !kv_lens || !o || !lse) return ATTN_ERR_INVALID_ARG;
+    const bool e4m3 = cache == ATTN_CACHE_E4M3;
+    if (e4m3 && (!k_scale || !v_scale)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(lse, 4) ||
+        !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(block_table, 4) || !aligned(kv_lens, 4) ||
+        !aligned(q_lens, 4))
+        return ATTN_ERR_INVALID_ARG;
+    if (q_stride < (long long)Hq * D || q_stride % 8 != 0) return ATTN_ERR_INVALID_ARG;
+    if (!rope_ok(rope_table, max_pos)) return ATTN_ERR_INVALID_ARG;
+    const long long rows = (long long)Sq * (Hq / Hkv);
+    if (rows > (1 << 30)) return ATTN_ERR_INVALID_ARG;
+    const int rb = paged::block_rows((int)rows);
+    const long long row_blocks = (rows + rb - 1) / rb;
+    const long long units = ((long long)max_pages * page + paged::kUnit - 1) / paged::kUnit + 1;
+    if ((long long)B * Hkv * row_blocks > 0x7fffffffLL / units) return ATTN_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, kWorkspaceAlign)) return ATTN_ERR_INVALID_ARG;
+    size_t part_off = 0;
+    if (workspace_bytes < attend_workspace(B, (int)rows, D, device_sm_count(), &part_off)) return ATTN_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !std::isfinite(scale)) scale = 1.0f / std::sqrt((float)D);
+
+    DeviceState dev{};
+    rc = device_state(&dev);
+    if (rc != ATTN_OK) return rc;
+    paged::AttendParams p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.q_stride = q_stride;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.block_table = block_table;
+    p.kv_lens = kv_lens;
+    p.q_lens = q_lens;
+    p.rope = rope_table;
+    p.o = static_cast<uint16_t*>(o);
+    p.lse = lse;
+    p.base = static_cast<int*>(workspace);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + part_off);
+    p.status = dev.status;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.max_pos = max_pos;
+    p.B = B;
+    p.Sq = Sq;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.group = Hq / Hkv;
+    p.rows = (int)rows;
+    p.row_blocks = (int)row_blocks;
+    p.page_shift = page_shift_of(page);
+    p.max_pages = max_pages;
+    p.n_pages = n_pages;
+    p.window = window;
+    p.sinks = sinks;
+    p.ctas = dev.num_sms * paged::resident_ctas(rb);
+    p.q_bf16 = bf16;
+    if (e4m3) return paged::launch_attend<paged::kE4m3>(dev.paged_attr_set[paged::kE4m3], p, D, stream);
+    return bf16 ? paged::launch_attend<paged::kBf16>(dev.paged_attr_set[paged::kBf16], p, D, stream)
+                : paged::launch_attend<paged::kF16>(dev.paged_attr_set[paged::kF16], p, D, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_kv_append(const void* k, const void* v, long long k_stride, long long v_stride, void* k_cache, void* v_cache,
+                   float* k_scale, float* v_scale, const int* block_table, const int* kv_lens, const int* new_lens,
+                   int B, int S, int Hkv, int D, int page, int max_pages, int n_pages, int cache_kind,
+                   const float* rope_table, int max_pos, attn_stream_t stream) {
+    return kv_append_impl(k, v, k_stride, v_stride, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, new_lens, B,
+                          S, Hkv, D, page, max_pages, n_pages, cache_kind, rope_table, max_pos,
+                          reinterpret_cast<cudaStream_t>(stream), true);
+}
+
+int attn_kv_append_f16(const void* k, const void* v, long long k_stride, long long v_stride, void* k_cache,
+                       void* v_cache, float* k_scale, float* v_scale, const int* block_table, const int* kv_lens,
+                       const int* new_lens, int B, int S, int Hkv, int D, int page, int max_pages, int n_pages,
+                       int cache_kind, const float* rope_table, int max_pos, attn_stream_t stream) {
+    return kv_append_impl(k, v, k_stride, v_stride, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, new_lens, B,
+                          S, Hkv, D, page, max_pages, n_pages, cache_kind, rope_table, max_pos,
+                          reinterpret_cast<cudaStream_t>(stream), false);
+}
+
+size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D) {
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Sq <= 0 || (D != 64 && D != 128)) return 0;
+    if ((long long)Sq * (Hq / Hkv) > (1 << 30)) return 0;
+    size_t part_off = 0;
+    return attend_workspace(B, Sq * (Hq / Hkv), D, device_sm_count(), &part_off);
+}
+
+int attn_fwd_paged(const void* q, long long q_stride, const void* k_cache, const void* v_cache, const float* k_scale,
+                   const float* v_scale, const int* block_table, const int* kv_lens, const int* q_lens, void* o,
+                   float* lse, int B, int Hq, int Hkv, int Sq, int D, int page, int max_pages, int n_pages,
+                   int cache_kind, float scale, int window, int sinks, const float* rope_table, int max_pos,
+                   void* workspace, size_t workspace_bytes, attn_stream_t stream) {
+    return attend_impl(q, q_stride, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, q_lens, o, lse, B, Hq, Hkv,
+                       Sq, D, page, max_pages, n_pages, cache_kind, scale, window, sinks, rope_table, max_pos, workspace,
+                       workspace_bytes, reinterpret_cast<cudaStream_t>(stream), true);
+}
+
+int attn_fwd_paged_f16(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
+                       const float* k_scale, const float* v_scale, const int* block_table, const int* kv_lens,
+                       const int* q_lens, void* o, float* lse, int B, int Hq, int Hkv, int Sq, int D, int page,
+                       int max_pages, int n_pages, int cache_kind, float scale, int window, int sinks,
+                       const float* rope_table, int max_pos, void* workspace, size_t workspace_bytes,
+                       attn_stream_t stream) {
+    return attend_impl(q, q_stride, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, q_lens, o, lse, B, Hq, Hkv,
+                       Sq, D, page, max_pages, n_pages, cache_kind, scale, window, sinks, rope_table, max_pos, workspace,
+                       workspace_bytes, reinterpret_cast<cudaStream_t>(stream), false);
+}
+
+}  // extern "C"

@@ -1,0 +1,87 @@
+// Host-visible parameters of the paged key/value cache's kernels (append,
+// attention, merge of key ranges) and their launchers, defined in
+// paged_append.cu and paged_attn_*.cu.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace attn {
+namespace paged {
+
+// Storage of the cache, with the type of the tensor-core operands it implies.
+constexpr int kBf16 = 0, kF16 = 1, kE4m3 = 2;
+
+// Device values that are out of range (page numbers, lengths, positions) set
+// this bit of the device status word; what they name is left out.
+constexpr unsigned int kStatusBadIndex = 2u;
+
+constexpr int kMinScaleExp = -100;      // smallest block scale of an 8-bit cache: 2^-100
+
+struct AppendParams {
+    const uint16_t* k;            // (B, S, Hkv, D) 16-bit, `k_stride` elements from token to token
+    const uint16_t* v;
+    long long k_stride, v_stride;
+    void* k_cache;                // (n_pages, Hkv, page, D)
+    void* v_cache;
+    float* k_scale;               // (n_pages, Hkv), 8-bit caches only
+    float* v_scale;
+    const int* block_table;       // (B, max_pages)
+    const int* kv_lens;           // (B) tokens in the cache, the step's included
+    const int* new_lens;          // (B) tokens of the step, or null: S
+    const float* rope;            // (max_pos, D/2, {cos, sin}) or null
+    int max_pos;
+    int B, S, Hkv, D;
+    int page_shift, max_pages, n_pages;
+    int touched;                  // pages a sequence's step may touch
+    bool bf16;                    // type of k and v
+    unsigned int* status;
+};
+
+// e4m3 or 16-bit cache by `cache`; ATTN_OK or ATTN_ERR_CUDA.
+int launch_append(const AppendParams& p, int cache, int num_sms, cudaStream_t stream);
+
+constexpr int kUnit = 128;        // keys of a scheduling unit
+
+struct AttendParams {
+    const uint16_t* q;            // (B, Sq, Hq, D) 16-bit, `q_stride` elements from token to token
+    long long q_stride;
+    const void* k_cache;          // (n_pages, Hkv, page, D)
+    const void* v_cache;
+    const float* k_scale;
+    const float* v_scale;
+    const int* block_table;       // (B, max_pages)
+    const int* kv_lens;           // (B)
+    const int* q_lens;            // (B) or null: Sq
+    const float* rope;            // or null
+    uint16_t* o;                  // (B, Sq, Hq, D)
+    float* lse;                   // (B, Hq, Sq)
+    float* part;                  // 2 slots per CTA of rows x (D + 2) FP32: unnormalised O, then maxima, then sums
+    int* base;                    // (B + 1) first unit of every sequence, written by CTA 0
+    unsigned int* status;
+    float scale_log2;             // scale * log2(e)
+    int max_pos;
+    int B, Sq, Hq, Hkv, group;
+    int rows;                     // Sq * group: query rows of a K/V head
+    int row_blocks;               // ceil(rows / rows of a block)
+    int page_shift, max_pages, n_pages;
+    int window, sinks;            // window 0: the whole past
+    int ctas;                     // grid of the attention kernel
+    bool q_bf16;                  // type of q and o (8-bit caches; 16-bit ones have q's type)
+};
+
+// Rows of a row block (8, 16 or 32) for `rows` query rows a K/V head.
+inline int block_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+
+// CTAs of the attention kernel that fit on an SM at once.
+inline int resident_ctas(int rows_per_block) { return rows_per_block <= 16 ? 2 : 1; }
+
+// The attention and the merge of its parts, for one cache type CT (kBf16,
+// kF16, kE4m3). attr_set caches, per context and instance [D is 128][rows of a
+// block 8, 16, 32], that the shared-memory attribute has been set.
+template <int CT>
+int launch_attend(bool (&attr_set)[2][3], const AttendParams& p, int D, cudaStream_t stream);
+
+}  // namespace paged
+}  // namespace attn
