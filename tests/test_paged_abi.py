@@ -69,11 +69,12 @@ def test_attention_arguments(kw, code):
 
 
 def test_workspace_size():
-    # 148 SMs assumed without a GPU: (B + 1) sequence offsets, then two parts of rows x (D + 2) FP32 per CTA, two CTAs
-    # an SM up to 16 query rows a K/V head and one above
+    # 148 SMs assumed without a GPU: (B + 1) sequence offsets, then two parts of rows x (D + 2) FP32 per CTA; rows
+    # come in blocks of 8, 16 or 32, two CTAs an SM unless a block holds 32 rows of 128
     assert A.attn_paged_workspace_bytes(16, 32, 8, 1, 128) == 256 + 148 * 2 * 2 * 8 * 130 * 4
     assert A.attn_paged_workspace_bytes(16, 32, 8, 4, 64) == 256 + 148 * 2 * 2 * 16 * 66 * 4
-    assert A.attn_paged_workspace_bytes(1, 32, 1, 9, 64) == 256 + 148 * 2 * 32 * 66 * 4
+    assert A.attn_paged_workspace_bytes(1, 32, 1, 9, 64) == 256 + 148 * 2 * 2 * 32 * 66 * 4
+    assert A.attn_paged_workspace_bytes(1, 32, 1, 9, 128) == 256 + 148 * 2 * 32 * 130 * 4
     assert A.attn_paged_workspace_bytes(0, 32, 8, 1, 128) == 0
     assert A.attn_paged_workspace_bytes(1, 30, 8, 1, 128) == 0
     assert A.attn_paged_workspace_bytes(1, 32, 8, 1, 96) == 0

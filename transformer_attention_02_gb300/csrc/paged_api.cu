@@ -91,7 +91,7 @@ int kv_append_impl(const void* k, const void* v, long long k_stride, long long v
 size_t attend_workspace(int B, int rows, int D, int sms, size_t* part_off) {
     const int rb = paged::block_rows(rows);
     *part_off = align_up((size_t)(B + 1) * sizeof(int));
-    return *part_off + (size_t)sms * paged::resident_ctas(rb) * 2 * rb * (D + 2) * sizeof(float);
+    return *part_off + (size_t)sms * paged::resident_ctas(D, rb) * 2 * rb * (D + 2) * sizeof(float);
 }
 
 int attend_impl(const void* q, long long q_stride, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -156,7 +156,7 @@ int attend_impl(const void* q, long long q_stride, const void* k_cache, const vo
     p.n_pages = n_pages;
     p.window = window;
     p.sinks = sinks;
-    p.ctas = dev.num_sms * paged::resident_ctas(rb);
+    p.ctas = dev.num_sms * paged::resident_ctas(D, rb);
     p.q_bf16 = bf16;
     if (e4m3) return paged::launch_attend<paged::kE4m3>(dev.paged_attr_set[paged::kE4m3], p, D, stream);
     return bf16 ? paged::launch_attend<paged::kBf16>(dev.paged_attr_set[paged::kBf16], p, D, stream)

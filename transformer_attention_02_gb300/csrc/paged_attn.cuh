@@ -42,34 +42,43 @@
 namespace attn {
 namespace paged {
 
+constexpr int kNoKey = 0x7fff0000;          // past every key (a sequence holds at most 2^30)
+constexpr float kNoLogit = -3e38f;          // the running maximum before any key
+
 template <int D, int CT, int NT>
 struct Cfg {
     static constexpr int kElt = CT == kE4m3 ? 1 : 2;
     static constexpr int kRowBytes = D * kElt;
     static constexpr int kChunks = kRowBytes / 16;
     static constexpr int kRows = 8 * NT;                         // query rows of a row block
-    static constexpr int kWarps = kRowBytes == 256 ? 4 : 8;
+    // Two CTAs a SM, or one when 32 rows of 128 dims take the registers of both.
+    static constexpr int kResident = resident_ctas(D, kRows);
+    static constexpr int kWarps = kResident == 2 && kRowBytes == 256 ? 4 : 8;
     static constexpr int kKeys = kRowBytes == 64 ? 32 : 16;      // keys of a stage
     static constexpr int kTiles = kKeys / 16;
+    static constexpr int kCopies = 16 * kChunks / 32;            // 16-byte copies a lane makes for 16 keys
     static constexpr int kStageBytes = 2 * kKeys * kRowBytes;
-    // Two CTAs a SM with three stages, or (32 rows: the accumulators take the
-    // registers of both) one with six.
-    static constexpr int kResident = NT <= 2 ? 2 : 1;
-    static constexpr int kStages = NT <= 2 ? 3 : 6;
+    static constexpr int kStages = kResident == 1 && kRowBytes == 128 ? 5 : 3;
     static constexpr int kRingBytes = kStages * kStageBytes;     // of one warp
-    static constexpr int kMergeStride = D + 4;                   // floats; breaks the bank alignment of the rows
     static constexpr bool kQShared = NT == 4;                    // Q fragments in shared memory, not registers
+    static constexpr int kQStride = D * 2 + 16;                  // bytes of a query row: conflict-free fragment reads
     static constexpr int kScaleOff = kWarps * kRingBytes;        // [warp][stage][tile]{k, v}
-    static constexpr int kStatOff = kScaleOff + kWarps * kStages * kTiles * 8;    // [warp][row]{max, sum}
+    static constexpr int kKeyOff = kScaleOff + kWarps * kStages * kTiles * 8;     // [warp][stage][tile] first key
+    static constexpr int kStatOff = kKeyOff + kWarps * kStages * kTiles * 4;      // [warp][row]{max, sum}
     static constexpr int kQOff = kStatOff + kWarps * kRows * 8;
-    static constexpr int kSmemBytes = kQOff + (kQShared ? kRows * D * 2 : 0);
-    static_assert(kRows * kMergeStride * 4 <= kRingBytes, "a warp's merge buffer reuses its ring");
+    static constexpr int kFragOff = kQOff + kRows * kQStride;
+    static constexpr int kSmemBytes = kFragOff + (kQShared ? kRows * D * 2 : 0);
+    static_assert(8 * D * 4 <= kStageBytes, "a warp merges eight rows at a time through one stage of its ring");
     static_assert(kUnit % kKeys == 0, "a stage lies inside one unit");
-    static_assert(kResident * (kSmemBytes + 1024) <= 232448, "shared memory budget");
+    static_assert(kQOff % 16 == 0 && kFragOff % 16 == 0, "16-byte accesses");
+    static_assert(kResident * (kSmemBytes + 1024 + 128) <= 233472, "shared memory budget");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -194,6 +203,38 @@ __device__ __forceinline__ int unit_owner(int total, int ctas, int x) {
     return (int)((((long long)x + 1) * ctas + total - 1) / total) - 1;
 }
 
+// One segment's share of a CTA: units [u0, u1) of the key list of row block rb
+// of K/V head hk of sequence b.
+struct Share {
+    int b, base;         // the sequence and the first unit of its segments
+    KeyList list;
+    int hk, rb, u0, u1;
+    int pos_lo, pos_hi;  // positions of the row block's first and last query
+    int kv_end;          // keys at or past it are hidden from every row
+    int w_lo;            // keys before it are hidden too, but for the sinks
+};
+
+// The share at unit x < x_end, searching onwards from s.b (whose list is s.list).
+template <int ROWS>
+__device__ __forceinline__ void locate(const AttendParams& p, int segs, int x, int x_end, Share& s) {
+    bool bad;
+    while (x >= s.base + s.list.units * segs) {                   // the sequence is done, or empty
+        s.base += s.list.units * segs;
+        s.list = key_list(p, ++s.b, bad);
+    }
+    const int seg = (x - s.base) / s.list.units;
+    s.u0 = x - s.base - seg * s.list.units;
+    s.u1 = min(s.list.units, s.u0 + x_end - x);
+    s.hk = seg / p.row_blocks;
+    s.rb = seg - s.hk * p.row_blocks;
+    const int r0 = s.rb * ROWS;
+    const int i0 = r0 / p.group, i1 = min(min(p.rows - 1, r0 + ROWS - 1) / p.group, s.list.ql - 1);
+    s.pos_lo = s.list.kv - s.list.ql + i0;
+    s.pos_hi = s.list.kv - s.list.ql + i1;
+    s.kv_end = i0 < s.list.ql ? max(0, s.pos_hi + 1) : 0;
+    s.w_lo = p.window > 0 ? s.pos_lo - p.window + 1 : 0;
+}
+
 template <int D, int CT, int NT>
 __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::kResident)
     paged_attend_kernel(const AttendParams p) {
@@ -201,17 +242,19 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     constexpr int kThreads = C::kWarps * 32;
     constexpr int kSteps = D / 16;                                // products of 16 dims
     constexpr bool kBf = CT == kBf16;                             // operand type of the products
-    extern __shared__ __align__(128) uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];          // the XOR of chunk offsets needs 256-byte stages
     __shared__ int s_scan[kThreads / 32 + 1];
     __shared__ int s_begin[2];                                    // the CTA's first sequence and its first unit
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    uint8_t* ring = smem_raw + warp * C::kRingBytes;
+    uint8_t* const ring = smem_raw + warp * C::kRingBytes;
     const uint32_t ring_a = ptx::smem_addr(ring);
     float* const scales = reinterpret_cast<float*>(smem_raw + C::kScaleOff) + warp * C::kStages * C::kTiles * 2;
     const uint32_t scales_a = ptx::smem_addr(scales);
+    volatile int* const keys_sh = reinterpret_cast<int*>(smem_raw + C::kKeyOff) + warp * C::kStages * C::kTiles;
     float2* const stats = reinterpret_cast<float2*>(smem_raw + C::kStatOff);
-    uint2* const q_sh = reinterpret_cast<uint2*>(smem_raw + C::kQOff);
+    uint8_t* const q_sh = smem_raw + C::kQOff;
+    uint2* const frag_sh = reinterpret_cast<uint2*>(smem_raw + C::kFragOff);
 
     // ---- where this CTA's range begins: a scan over the sequences' units
     const int segs = p.Hkv * p.row_blocks;                        // segments of a sequence
@@ -256,196 +299,232 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     }
     __syncthreads();
     if (x >= x_end) return;
-    int b = s_begin[0], b_base = s_begin[1];
+
+    // Where a lane's pieces lie in a swizzled stage. Copy c of a 16-key tile is
+    // chunk lane % kChunks of row c * (32 / kChunks) + lane / kChunks; the
+    // swizzle repeats every 8 rows (16 rows of 64 bytes), so a few offsets
+    // describe all copies. The ldmatrix rows likewise: chunk 2c is the XOR of
+    // c << 5 with chunk 0.
+    constexpr int kCopyRows = 32 / C::kChunks;                     // rows of one copy
+    constexpr int kPeriod = C::kRowBytes == 64 ? 16 : 8;
+    constexpr int kCopyKinds = kPeriod / kCopyRows;
+    uint32_t copy_off[kCopyKinds];
+#pragma unroll
+    for (int c = 0; c < kCopyKinds; ++c)
+        copy_off[c] = swizzled<C::kRowBytes>(c * kCopyRows + lane / C::kChunks, lane % C::kChunks);
+    auto copy_to = [&](int c) {
+        return copy_off[c % kCopyKinds] + (uint32_t)(c / kCopyKinds * kCopyKinds * kCopyRows * C::kRowBytes);
+    };
+    const uint32_t k_off = swizzled<C::kRowBytes>((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
+    const uint32_t v_off = swizzled<C::kRowBytes>((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
+    const int sinks = p.window > 0 ? p.sinks : 0;
+
+    // ---- the copies run ahead of the products, across segments: `ld` is the
+    // share they are in, ld_i its next stage. A segment then begins with its
+    // first stages already on their way, and the memory stays busy while the
+    // last segment's rows are merged.
+    Share ld;
+    ld.b = s_begin[0];
+    ld.base = s_begin[1];
+    {
+        bool bad;
+        ld.list = key_list(p, ld.b, bad);
+    }
+    int ld_x = x, ld_i = 0, ld_n = 0, ld_stage = 0;
+    int ids = 0;                                                  // page numbers of 32 / kTiles stages, one tile a lane
+    constexpr int kBatch = 32 / C::kTiles;
+    auto stages_of = [](int units) { return (units * kUnit + C::kWarps * C::kKeys - 1) / (C::kWarps * C::kKeys); };
+    auto key_at = [&](int off) {                                  // key at offset `off` of the share's list, or none
+        if (off >= (ld.u1 - ld.u0) * kUnit) return kNoKey;
+        const int u = ld.u0 + off / kUnit;
+        return (u < ld.list.sink_units ? u : u - ld.list.sink_units + ld.list.first) * kUnit + off % kUnit;
+    };
+    auto enter = [&]() {                                          // the share at ld_x
+        locate<C::kRows>(p, segs, ld_x, x_end, ld);
+        ld_i = 0;
+        ld_n = stages_of(ld.u1 - ld.u0);
+    };
+    enter();
+    auto issue = [&]() {
+        if (ld_x < x_end) {
+            if (ld_i % kBatch == 0) {
+                const int key = key_at(((ld_i + lane / C::kTiles) * C::kWarps + warp) * C::kKeys + lane % C::kTiles * 16);
+                ids = key < ld.kv_end ? __ldg(p.block_table + (size_t)ld.b * p.max_pages + (key >> p.page_shift)) : -1;
+            }
+            const int key0 = key_at((ld_i * C::kWarps + warp) * C::kKeys);
+#pragma unroll
+            for (int m = 0; m < C::kTiles; ++m) {
+                const int k0 = key0 + 16 * m;                     // (of no use past kv_end)
+                const int id = __shfl_sync(0xffffffffu, ids, ld_i % kBatch * C::kTiles + m);
+                const bool in = key0 < ld.kv_end && k0 < ld.kv_end, ok = in && (unsigned)id < (unsigned)p.n_pages;
+                if (lane == 0) {
+                    keys_sh[ld_stage * C::kTiles + m] = ok ? k0 : kNoKey;
+                    if (in && !ok) atomicOr(p.status, kStatusBadIndex);
+                }
+                if (!ok) continue;
+                const size_t block = (size_t)id * p.Hkv + ld.hk;
+                const size_t at =
+                    ((block << p.page_shift) + (size_t)(k0 & ((1 << p.page_shift) - 1))) * C::kRowBytes + lane * 16;
+                const uint8_t* ks = static_cast<const uint8_t*>(p.k_cache) + at;
+                const uint8_t* vs = static_cast<const uint8_t*>(p.v_cache) + at;
+                const uint32_t dst = ring_a + ld_stage * C::kStageBytes + m * 16 * C::kRowBytes;
+                if (k0 + 16 <= ld.kv_end && (k0 >= ld.w_lo || k0 + 16 <= sinks)) {
+#pragma unroll
+                    for (int c = 0; c < C::kCopies; ++c) {
+                        cp_async16(dst + copy_to(c), ks + c * 512);
+                        cp_async16(dst + C::kKeys * C::kRowBytes + copy_to(c), vs + c * 512);
+                    }
+                } else {
+                    // rows that no query of the block sees are filled with zeros
+#pragma unroll
+                    for (int c = 0; c < C::kCopies; ++c) {
+                        const int key = k0 + (c * 32 + lane) / C::kChunks;
+                        const bool take = key < ld.kv_end && (key >= ld.w_lo || key < sinks);
+                        cp_async16(dst + copy_to(c), ks + c * 512, take);
+                        cp_async16(dst + C::kKeys * C::kRowBytes + copy_to(c), vs + c * 512, take);
+                    }
+                }
+                if (CT == kE4m3 && lane < 2)
+                    cp_async4(scales_a + ((ld_stage * C::kTiles + m) * 2 + lane) * 4, (lane ? p.v_scale : p.k_scale) + block);
+            }
+            if (++ld_i == ld_n) {
+                ld_x += ld.u1 - ld.u0;
+                if (ld_x < x_end) enter();
+            }
+        }
+        cp_async_commit();
+        ld_stage = ld_stage + 1 == C::kStages ? 0 : ld_stage + 1;
+    };
+    Share cur = ld;
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) issue();
 
     uint32_t qf[C::kQShared ? 1 : kSteps][C::kQShared ? 1 : NT][2];
-
-    while (x < x_end) {
-        bool bad_len;
-        const KeyList list = key_list(p, b, bad_len);
-        if (list.units == 0 || x >= b_base + list.units * segs) {        // the sequence is done (or empty)
-            b_base += list.units * segs;
-            ++b;
-            continue;
-        }
-        const int seg = (x - b_base) / list.units;
-        const int u0 = x - b_base - seg * list.units;
-        const int u1 = min(list.units, u0 + x_end - x);
-        const int hk = seg / p.row_blocks, rb = seg - hk * p.row_blocks;
-        const int r0 = rb * C::kRows;
-        const int n_keys = (u1 - u0) * kUnit;
-
-        // Positions of the block's first and last valid rows, and what they see.
-        const int i0 = r0 / p.group;
-        const int i1 = min(min(p.rows - 1, r0 + C::kRows - 1) / p.group, list.ql - 1);
-        const int pos_lo = list.kv - list.ql + i0, pos_hi = list.kv - list.ql + i1;
-        const int kv_end = i0 < list.ql ? max(0, pos_hi + 1) : 0;        // keys at or past it: hidden from every row
-        const int w_lo = p.window > 0 ? pos_lo - p.window + 1 : 0;       // keys before it are hidden, but for the sinks
-        const int sinks = p.window > 0 ? p.sinks : 0;
-
-        const int* table = p.block_table + (size_t)b * p.max_pages;
-        uint32_t bad_tiles = 0;                                          // bit stage * kTiles + tile
-        auto key_of = [&](int i) {                                       // first key of this warp's i-th stage, or -1
-            const int off = (i * C::kWarps + warp) * C::kKeys;
-            if (off >= n_keys) return -1;
-            const int u = u0 + off / kUnit;
-            return (u < list.sink_units ? u : u - list.sink_units + list.first) * kUnit + off % kUnit;
-        };
-        auto issue = [&](int i) {
-            const int key0 = key_of(i);
-            if (key0 >= 0 && key0 < kv_end) {
-                const int s = i % C::kStages;
-#pragma unroll
-                for (int m = 0; m < C::kTiles; ++m) {
-                    const int k0 = key0 + 16 * m;
-                    int id = -1;
-                    if (k0 < kv_end) {
-                        id = __ldg(table + (k0 >> p.page_shift));
-                        if ((unsigned)id >= (unsigned)p.n_pages) {
-                            if (lane == 0) atomicOr(p.status, kStatusBadIndex);
-                            id = -1;
-                        }
+    int st = 0;                                                   // stage of the next products
+    for (;;) {
+        const int r0 = cur.rb * C::kRows, pos0 = cur.list.kv - cur.list.ql;
+        // ---- queries, rotated and rounded to their 16-bit type, in shared memory
+        const bool bf = CT == kE4m3 ? p.q_bf16 : kBf;
+        for (int w = tid; w < C::kRows * (D / 8); w += kThreads) {
+            const int r = w / (D / 8), d = (w - r * (D / 8)) * 8;
+            const int row = r0 + r, i = row / p.group;
+            uint32_t v[4] = {0u, 0u, 0u, 0u};
+            if (row < p.rows && i < cur.list.ql) {
+                const uint4 raw = *reinterpret_cast<const uint4*>(
+                    p.q + ((long long)cur.b * p.Sq + i) * p.q_stride +
+                    (long long)(cur.hk * p.group + (row - i * p.group)) * D + d);
+                v[0] = raw.x;
+                v[1] = raw.y;
+                v[2] = raw.z;
+                v[3] = raw.w;
+                if (p.rope) {
+                    int pos = pos0 + i;
+                    if (pos >= p.max_pos) {
+                        if (d == 0) atomicOr(p.status, kStatusBadIndex);
+                        pos = p.max_pos - 1;
                     }
-                    const uint32_t bit = 1u << (s * C::kTiles + m);
-                    bad_tiles = id < 0 ? bad_tiles | bit : bad_tiles & ~bit;
-                    const size_t row0 = id < 0 ? 0
-                                               : ((((size_t)id * p.Hkv + hk) << p.page_shift) +
-                                                  (size_t)(k0 & ((1 << p.page_shift) - 1)));
-                    const uint8_t* ks = static_cast<const uint8_t*>(p.k_cache) + row0 * C::kRowBytes;
-                    const uint8_t* vs = static_cast<const uint8_t*>(p.v_cache) + row0 * C::kRowBytes;
-                    const uint32_t dst = ring_a + s * C::kStageBytes;
-#pragma unroll
-                    for (int c = 0; c < 16 * C::kChunks / 32; ++c) {
-                        const int r = (c * 32 + lane) / C::kChunks, ch = lane % C::kChunks;
-                        const int key = k0 + r;
-                        const bool take = id >= 0 && key < kv_end && (key >= w_lo || key < sinks);
-                        const uint32_t to = swizzled<C::kRowBytes>(16 * m + r, ch);
-                        const size_t from = take ? (size_t)r * C::kRowBytes + ch * 16 : 0;
-                        cp_async16(dst + to, ks + from, take);
-                        cp_async16(dst + C::kKeys * C::kRowBytes + to, vs + from, take);
-                    }
-                    if (CT == kE4m3 && lane < 2) {
-                        const size_t at = id < 0 ? 0 : (size_t)id * p.Hkv + hk;
-                        cp_async4(scales_a + ((s * C::kTiles + m) * 2 + lane) * 4, (lane ? p.v_scale : p.k_scale) + at);
-                    }
+                    const float4* at = reinterpret_cast<const float4*>(p.rope) + (size_t)max(pos, 0) * (D / 4) + d / 4;
+                    const float4 a = __ldg(at), c = __ldg(at + 1);
+                    v[0] = bf ? rotate_pair<true>(v[0], a.x, a.y) : rotate_pair<false>(v[0], a.x, a.y);
+                    v[1] = bf ? rotate_pair<true>(v[1], a.z, a.w) : rotate_pair<false>(v[1], a.z, a.w);
+                    v[2] = bf ? rotate_pair<true>(v[2], c.x, c.y) : rotate_pair<false>(v[2], c.x, c.y);
+                    v[3] = bf ? rotate_pair<true>(v[3], c.z, c.w) : rotate_pair<false>(v[3], c.z, c.w);
                 }
             }
-            cp_async_commit();
-        };
-        const int n_it = (n_keys + C::kWarps * C::kKeys - 1) / (C::kWarps * C::kKeys);
-#pragma unroll
-        for (int i = 0; i < C::kStages - 1; ++i) issue(i);
-
-        // ---- queries: rotated, rounded to their 16-bit type, as B fragments.
-        // With an 8-bit cache they become f16 values, each row scaled by a
-        // power of two to lie in [-2, 2]: exact down to 2^-24 of the row's
-        // largest value, whatever the row's magnitude.
+            *reinterpret_cast<uint4*>(q_sh + r * C::kQStride + d * 2) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        __syncthreads();
+        // B fragments. With an 8-bit cache the queries become f16 values, each
+        // row scaled by a power of two to lie in [-2, 2]: exact down to 2^-24 of
+        // the row's largest value, whatever the row's magnitude.
         float cf[NT][2];                                          // log2 units per raw score, rows 2t and 2t + 1
-        auto load_q = [&](auto&& put) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int row = r0 + 8 * n + g;
-                const int i = row / p.group;
-                const bool there = row < p.rows && i < list.ql;
-                int pos = list.kv - list.ql + i;
-                if (p.rope && there && pos >= p.max_pos) {
-                    if (t == 0) atomicOr(p.status, kStatusBadIndex);
-                    pos = p.max_pos - 1;
-                }
-                pos = max(pos, 0);
-                const uint16_t* src =
-                    p.q + ((long long)b * p.Sq + i) * p.q_stride + (long long)(hk * p.group + (row - i * p.group)) * D;
-                const bool bf = CT == kE4m3 ? p.q_bf16 : kBf;
-                uint32_t w[kSteps][2];
-                float top = 0.f;
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        // dims of the fragment's register e: the keys' fragments hold the same ones
-                        const int d = CT == kE4m3 ? 16 * s + 4 * t + 2 * e : 16 * s + 8 * e + 2 * t;
-                        uint32_t v = there ? *reinterpret_cast<const uint32_t*>(src + d) : 0u;
-                        if (p.rope && there) {
-                            const float2 a =
-                                __ldg(reinterpret_cast<const float2*>(p.rope) + (size_t)pos * (D / 2) + d / 2);
-                            const float2 f = widen16(v, bf);
-                            const float y0 = f.x * a.x - f.y * a.y, y1 = f.y * a.x + f.x * a.y;
-                            v = bf ? ptx::pack_bf16x2(y0, y1) : ptx::pack_f16x2(y0, y1);
-                        }
-                        w[s][e] = v;
-                        if (CT == kE4m3) {
-                            const float2 f = widen16(v, bf);
-                            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-                        }
-                    }
-                }
-                float back = 1.f;
-                if (CT == kE4m3) {
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -120), 120);
-                    const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-                    back = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-                    for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float2 a = widen16(w[s][h], bf);
-                            w[s][h] = ptx::pack_f16x2(a.x * f, a.y * f);
-                        }
-                }
-                cf[n][0] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t);
-                cf[n][1] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t + 4);
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s) put(s, n, w[s][0], w[s][1]);
-            }
-        };
-        if constexpr (C::kQShared) {
-            load_q([&](int s, int n, uint32_t w0, uint32_t w1) {
-                if (warp == 0) q_sh[(s * NT + n) * 32 + lane] = make_uint2(w0, w1);
-            });
-            __syncthreads();
-        } else {
-            load_q([&](int s, int n, uint32_t w0, uint32_t w1) {
-                qf[s][n][0] = w0;
-                qf[s][n][1] = w1;
-            });
-        }
-
-        float acc[kSteps][NT][4];                                 // O^T
-        float m_used[NT][2], l_sum[NT][2];                        // rows 2t, 2t + 1 of each n-tile; the sum is this lane's
-        float v_ref = 0.f;                                        // largest value scale so far: acc is in units of it
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            m_used[n][0] = m_used[n][1] = -INFINITY;
+            uint32_t w[kSteps][2];
+            const uint8_t* src = q_sh + (8 * n + g) * C::kQStride;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                // the dims that the keys' fragments of the step hold
+                if (CT == kE4m3) {
+                    const uint2 v = *reinterpret_cast<const uint2*>(src + (16 * s + 4 * t) * 2);
+                    w[s][0] = v.x;
+                    w[s][1] = v.y;
+                } else {
+                    w[s][0] = *reinterpret_cast<const uint32_t*>(src + (16 * s + 2 * t) * 2);
+                    w[s][1] = *reinterpret_cast<const uint32_t*>(src + (16 * s + 8 + 2 * t) * 2);
+                }
+            }
+            cf[n][0] = cf[n][1] = p.scale_log2;
+            if (CT == kE4m3) {
+                float top = 0.f;
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 a = widen16(w[s][h], bf);
+                        top = fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y)));
+                    }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -120), 120);
+                const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+                const float back = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 a = widen16(w[s][h], bf);
+                        w[s][h] = ptx::pack_f16x2(a.x * f, a.y * f);
+                    }
+                cf[n][0] *= __shfl_sync(0xffffffffu, back, 8 * t);
+                cf[n][1] *= __shfl_sync(0xffffffffu, back, 8 * t + 4);
+            }
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                if constexpr (C::kQShared) {
+                    if (warp == 0) frag_sh[(s * NT + n) * 32 + lane] = make_uint2(w[s][0], w[s][1]);
+                } else {
+                    qf[s][n][0] = w[s][0];
+                    qf[s][n][1] = w[s][1];
+                }
+            }
+        }
+        if constexpr (C::kQShared) __syncthreads();
+
+        float acc[kSteps][NT][4];                                 // O^T
+        // Rows 2t, 2t + 1 of each n-tile: the maximum in use (log2 units; below
+        // any logit at first, so that no weight needs a special case) and this
+        // lane's part of the sum.
+        float m_used[NT][2], l_sum[NT][2];
+        float v_ref = 0.f, v_inv = 0.f;                           // largest value scale so far (acc is in units of it)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            m_used[n][0] = m_used[n][1] = kNoLogit;
             l_sum[n][0] = l_sum[n][1] = 0.f;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) acc[s][n][0] = acc[s][n][1] = acc[s][n][2] = acc[s][n][3] = 0.f;
         }
 
+        const int n_it = stages_of(cur.u1 - cur.u0);
         for (int i = 0; i < n_it; ++i) {
             cp_async_wait<C::kStages - 2>();
             __syncwarp();
-            issue(i + C::kStages - 1);
-            const int key0 = key_of(i);
-            if (key0 < 0 || key0 >= kv_end) continue;
-            const int st = i % C::kStages;
+            issue();
 #pragma unroll
             for (int m = 0; m < C::kTiles; ++m) {
-                const int k0 = key0 + 16 * m;
-                const bool bad = (bad_tiles >> (st * C::kTiles + m)) & 1u;
-                if (bad || k0 >= kv_end) continue;
-                const uint32_t ka = ring_a + st * C::kStageBytes, va = ka + C::kKeys * C::kRowBytes;
+                const int k0 = keys_sh[st * C::kTiles + m];
+                if (k0 == kNoKey) continue;                   // nothing there, or a page out of range
+                const uint32_t ka = ring_a + st * C::kStageBytes + m * 16 * C::kRowBytes + k_off;
+                const uint32_t va = ring_a + st * C::kStageBytes + (C::kKeys + m * 16) * C::kRowBytes + v_off;
                 // ---- S^T = K Q^T
                 float s[NT][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
                 {
-                    const int kr = 16 * m + (lane & 7) + ((lane >> 3) & 1) * 8, kc = lane >> 4;
 #pragma unroll
                     for (int c = 0; c < C::kChunks / 2; ++c) {
                         uint32_t r[4];
-                        ldmatrix4<false>(r, ka + swizzled<C::kRowBytes>(kr, 2 * c + kc));
+                        ldmatrix4<false>(r, ka ^ (uint32_t)(c << 5));
                         if (CT == kE4m3) {
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
@@ -455,7 +534,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                                 for (int n = 0; n < NT; ++n) {
                                     uint2 q2;
                                     if constexpr (C::kQShared)
-                                        q2 = q_sh[((2 * c + h) * NT + n) * 32 + lane];
+                                        q2 = frag_sh[((2 * c + h) * NT + n) * 32 + lane];
                                     else
                                         q2 = make_uint2(qf[2 * c + h][n][0], qf[2 * c + h][n][1]);
                                     mma16816<false>(s[n], a0, a1, a2, a3, q2.x, q2.y);
@@ -466,7 +545,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                             for (int n = 0; n < NT; ++n) {
                                 uint2 q2;
                                 if constexpr (C::kQShared)
-                                    q2 = q_sh[(c * NT + n) * 32 + lane];
+                                    q2 = frag_sh[(c * NT + n) * 32 + lane];
                                 else
                                     q2 = make_uint2(qf[c][n][0], qf[c][n][1]);
                                 mma16816<kBf>(s[n], r[0], r[1], r[2], r[3], q2.x, q2.y);
@@ -481,63 +560,72 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                     ks = kv2.x;
                     vs = kv2.y;
                 }
-                const bool whole = k0 + 15 <= pos_lo && (k0 >= pos_hi - p.window + 1 || p.window == 0 || k0 + 16 <= sinks);
-                bool grow = false;
+                const bool whole = k0 + 15 <= cur.pos_lo && (k0 >= cur.pos_hi - p.window + 1 || p.window == 0 || k0 + 16 <= sinks);
+                float f[NT][2];                                    // log2 units per value of s
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float f = cf[n][e] * ks;
-                        float z0 = s[n][e] * f, z1 = s[n][2 + e] * f;
-                        if (!whole) {
-                            const int pos = list.kv - list.ql + (r0 + 8 * n + 2 * t + e) / p.group;
+                    for (int e = 0; e < 2; ++e) f[n][e] = CT == kE4m3 ? cf[n][e] * ks : p.scale_log2;
+                if (!whole) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int pos = pos0 + (r0 + 8 * n + 2 * t + e) / p.group;
                             const int lo = p.window > 0 ? pos - p.window : -1;
                             const int j0 = k0 + g, j1 = j0 + 8;
-                            if (j0 > pos || (j0 <= lo && j0 >= sinks)) z0 = -INFINITY;
-                            if (j1 > pos || (j1 <= lo && j1 >= sinks)) z1 = -INFINITY;
+                            const bool h0 = j0 > pos || (j0 <= lo && j0 >= sinks), h1 = j1 > pos || (j1 <= lo && j1 >= sinks);
+                            s[n][e] = h0 ? -INFINITY : s[n][e] * f[n][e];
+                            s[n][2 + e] = h1 ? -INFINITY : s[n][2 + e] * f[n][e];
+                            f[n][e] = 1.f;
                         }
-                        s[n][e] = z0;
-                        s[n][2 + e] = z1;
-                        grow |= fmaxf(z0, z1) > m_used[n][e] + kRescaleThreshold;
-                    }
                 }
                 // The maximum in use may trail the true one by 2^8 (the weights
                 // then reach 2^8, far inside 16-bit range), so most tiles need
                 // one vote instead of the reduction and the rescaling.
-                if (__any_sync(0xffffffffu, grow) || vs > v_ref) {
-                    const float fv = vs > v_ref ? v_ref / vs : 1.f;
-                    v_ref = fmaxf(v_ref, vs);
+                bool grow = CT == kE4m3 && vs > v_ref;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        grow |= fmaf(fmaxf(s[n][e], s[n][2 + e]), f[n][e], -kRescaleThreshold) > m_used[n][e];
+                if (__any_sync(0xffffffffu, grow)) {
+                    float fv = 1.f;
+                    if (CT == kE4m3 && vs > v_ref) {
+                        fv = v_ref / vs;
+                        v_ref = vs;
+                        v_inv = vs > 1e-37f ? 1.f / vs : 0.f;
+                    }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float mx = fmaxf(s[n][e], s[n][2 + e]);
+                            float mx = fmaxf(s[n][e], s[n][2 + e]) * f[n][e];
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                             mx = fmaxf(mx, m_used[n][e]);
-                            const float alpha = mx == -INFINITY ? 1.f : ptx::ex2(m_used[n][e] - mx);
+                            const float alpha = ptx::ex2(m_used[n][e] - mx);
                             m_used[n][e] = mx;
                             l_sum[n][e] *= alpha;
-                            const float f = alpha * fv;
+                            const float fa = alpha * fv;
 #pragma unroll
                             for (int d = 0; d < kSteps; ++d) {
-                                acc[d][n][e] *= f;
-                                acc[d][n][2 + e] *= f;
+                                acc[d][n][e] *= fa;
+                                acc[d][n][2 + e] *= fa;
                             }
                         }
                     }
                 }
                 // ---- weights; P in f16 (bf16 for a bf16 cache), summed before that rounding
-                const float vf = CT == kE4m3 ? (v_ref > 0.f ? vs / v_ref : 0.f) : 1.f;
+                const float vf = vs * v_inv;
                 uint32_t pb[NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float w[4];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float nm = m_used[n][e] == -INFINITY ? 0.f : m_used[n][e];
-                        w[e] = ptx::ex2(s[n][e] - nm);
-                        w[2 + e] = ptx::ex2(s[n][2 + e] - nm);
+                        w[e] = ptx::ex2(fmaf(s[n][e], f[n][e], -m_used[n][e]));
+                        w[2 + e] = ptx::ex2(fmaf(s[n][2 + e], f[n][e], -m_used[n][e]));
                         l_sum[n][e] += w[e] + w[2 + e];
                     }
                     if (CT == kE4m3) {
@@ -549,11 +637,10 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                 }
                 // ---- O^T += V^T P^T
                 {
-                    const int vr = 16 * m + (lane & 7) + (lane >> 4) * 8, vc = (lane >> 3) & 1;
 #pragma unroll
                     for (int c = 0; c < C::kChunks / 2; ++c) {
                         uint32_t r[4];
-                        ldmatrix4<true>(r, va + swizzled<C::kRowBytes>(vr, 2 * c + vc));
+                        ldmatrix4<true>(r, va ^ (uint32_t)(c << 5));
                         if (CT == kE4m3) {
                             // Each register holds two keys of two neighbouring dims: the even
                             // dims of both chunks make one product, the odd ones the other.
@@ -574,96 +661,129 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                     }
                 }
             }
+            st = st + 1 == C::kStages ? 0 : st + 1;
         }
 
-        // ---- merge the warps: each leaves its O^T (times its value scale), its
-        // maximum and its sum in shared memory
-        cp_async_wait<0>();
+        // ---- merge the warps, eight rows at a time, through the stage that was
+        // read last (the others hold the next segment's keys)
         __syncwarp();
-        float* const mine_o = reinterpret_cast<float*>(ring);
+        const int m_stage = st == 0 ? C::kStages - 1 : st - 1;
+        float* const mine_o = reinterpret_cast<float*>(ring + m_stage * C::kStageBytes);
+        const bool full = cur.u0 == 0 && cur.u1 == cur.list.units;
+        float* slot = p.part + (size_t)(2 * blockIdx.x + (cur.u0 == 0 ? 1 : 0)) * C::kRows * (D + 2);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int col = 8 * n + 2 * t + e;
+                const int col = 2 * t + e;
                 float l = l_sum[n][e];
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-                if (g == 0) stats[warp * C::kRows + col] = make_float2(m_used[n][e], l);
+                if (g == 0) stats[warp * C::kRows + 8 * n + col] = make_float2(m_used[n][e], l);
                 const float f = CT == kE4m3 ? v_ref : 1.f;
 #pragma unroll
                 for (int d = 0; d < kSteps; ++d) {
                     const int da = CT == kE4m3 ? 32 * (d >> 1) + (d & 1) + 2 * g : 16 * d + g;
                     const int db = CT == kE4m3 ? da + 16 : da + 8;
-                    mine_o[col * C::kMergeStride + da] = acc[d][n][e] * f;
-                    mine_o[col * C::kMergeStride + db] = acc[d][n][2 + e] * f;
+                    mine_o[col * D + (da ^ (t << 3))] = acc[d][n][e] * f;      // XOR: spreads the rows over the banks
+                    mine_o[col * D + (db ^ (t << 3))] = acc[d][n][2 + e] * f;
                 }
             }
-        }
-        __syncthreads();
-        const bool full = u0 == 0 && u1 == list.units;
-        float* slot = p.part + (size_t)(2 * blockIdx.x + (u0 == 0 ? 1 : 0)) * C::kRows * (D + 2);
-        for (int w = tid; w < C::kRows * (D / 4); w += kThreads) {
-            const int col = w / (D / 4), d = (w - col * (D / 4)) * 4;
-            float mx = -INFINITY;
+            __syncthreads();
+            for (int w = tid; w < 8 * (D / 4); w += kThreads) {
+                const int c8 = w / (D / 4), d = (w - c8 * (D / 4)) * 4, col = 8 * n + c8;
+                float mx = kNoLogit;
 #pragma unroll
-            for (int v = 0; v < C::kWarps; ++v) mx = fmaxf(mx, stats[v * C::kRows + col].x);
-            float sum = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (mx != -INFINITY) {
+                for (int v = 0; v < C::kWarps; ++v) mx = fmaxf(mx, stats[v * C::kRows + col].x);
+                float sum = 0.f;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int v = 0; v < C::kWarps; ++v) {
                     const float2 st2 = stats[v * C::kRows + col];
-                    const float f = ptx::ex2(st2.x - mx);
+                    const float fm = ptx::ex2(st2.x - mx);
                     const float4 a = *reinterpret_cast<const float4*>(
-                        reinterpret_cast<const float*>(smem_raw + v * C::kRingBytes) + col * C::kMergeStride + d);
-                    if (st2.x != -INFINITY) {
-                        sum += st2.y * f;
-                        o.x = fmaf(a.x, f, o.x);
-                        o.y = fmaf(a.y, f, o.y);
-                        o.z = fmaf(a.z, f, o.z);
-                        o.w = fmaf(a.w, f, o.w);
+                        reinterpret_cast<const float*>(smem_raw + v * C::kRingBytes + m_stage * C::kStageBytes) + c8 * D +
+                        (d ^ ((c8 >> 1) << 3)));
+                    sum = fmaf(st2.y, fm, sum);
+                    o.x = fmaf(a.x, fm, o.x);
+                    o.y = fmaf(a.y, fm, o.y);
+                    o.z = fmaf(a.z, fm, o.z);
+                    o.w = fmaf(a.w, fm, o.w);
+                }
+                if (full) {
+                    const int row = r0 + col, i = row / p.group;
+                    if (row < p.rows && i < cur.list.ql) {
+                        const int h = cur.hk * p.group + (row - i * p.group);
+                        const float inv = sum != 0.f ? 1.f / sum : 0.f;       // 0: no key was visible
+                        uint2 r;
+                        r.x = bf ? ptx::pack_bf16x2(o.x * inv, o.y * inv) : ptx::pack_f16x2(o.x * inv, o.y * inv);
+                        r.y = bf ? ptx::pack_bf16x2(o.z * inv, o.w * inv) : ptx::pack_f16x2(o.z * inv, o.w * inv);
+                        *reinterpret_cast<uint2*>(p.o + (((size_t)cur.b * p.Sq + i) * p.Hq + h) * D + d) = r;
+                        if (d == 0)
+                            p.lse[((size_t)cur.b * p.Hq + h) * p.Sq + i] =
+                                sum != 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+                    }
+                } else {
+                    *reinterpret_cast<float4*>(slot + col * D + d) = o;
+                    if (d == 0) {
+                        slot[C::kRows * D + col] = mx;
+                        slot[C::kRows * (D + 1) + col] = sum;
                     }
                 }
             }
-            if (full) {
-                const int row = r0 + col, i = row / p.group;
-                if (row < p.rows && i < list.ql) {
-                    const int h = hk * p.group + (row - i * p.group);
-                    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-                    const bool bf = CT == kE4m3 ? p.q_bf16 : kBf;
-                    uint2 r;
-                    r.x = bf ? ptx::pack_bf16x2(o.x * inv, o.y * inv) : ptx::pack_f16x2(o.x * inv, o.y * inv);
-                    r.y = bf ? ptx::pack_bf16x2(o.z * inv, o.w * inv) : ptx::pack_f16x2(o.z * inv, o.w * inv);
-                    *reinterpret_cast<uint2*>(p.o + (((size_t)b * p.Sq + i) * p.Hq + h) * D + d) = r;
-                    if (d == 0)
-                        p.lse[((size_t)b * p.Hq + h) * p.Sq + i] =
-                            sum > 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-                }
-            } else {
-                *reinterpret_cast<float4*>(slot + col * D + d) = o;
-                if (d == 0) {
-                    slot[C::kRows * D + col] = mx;
-                    slot[C::kRows * (D + 1) + col] = sum;
-                }
-            }
+            __syncthreads();                                      // the stage is free again
         }
-        __syncthreads();                                          // the rings are free for the next segment
-        x += u1 - u0;
+        x += cur.u1 - cur.u0;
+        if (x >= x_end) break;
+        locate<C::kRows>(p, segs, x, x_end, cur);
     }
+    cp_async_wait<0>();
 }
 
 // Merges the parts of the segments that several CTAs share, and fills the rows
 // of sequences without a key. One warp per row; a lane holds D / 32 dims.
 template <int D, int RB>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const AttendParams p, bool bf16) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int kPer = D / 32;
+    __shared__ int s_scan[8], s_mine[2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int segs = p.Hkv * p.row_blocks;
     const int b = blockIdx.x / segs, seg = blockIdx.x - b * segs;
-    const int total = p.base[p.B], first = p.base[b];
-    const int units = (p.base[b + 1] - first) / segs;
+    int total, first, units;
+    if (p.B <= 256) {
+        // The sequences' units, one a thread: lengths are the step's inputs, so
+        // this needs nothing of the attention kernel and runs beside it.
+        bool bad;
+        const int mine = (int)threadIdx.x < p.B ? key_list(p, threadIdx.x, bad).units : 0;
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) s_scan[warp] = incl;
+        __syncthreads();
+        total = 0;
+        int before = incl - mine;
+        for (int w = 0; w < 8; ++w) {
+            if (w < warp) before += s_scan[w];
+            total += s_scan[w];
+        }
+        if ((int)threadIdx.x == b) {
+            s_mine[0] = before;
+            s_mine[1] = mine;
+        }
+        __syncthreads();
+        total *= segs;
+        first = s_mine[0] * segs;
+        units = s_mine[1];
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+    } else {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        total = p.base[p.B];
+        first = p.base[b];
+        units = (p.base[b + 1] - first) / segs;
+    }
     int c0 = 0, c1 = 0;
     if (units > 0) {
         const int ctas = working_ctas(p, total);
@@ -678,34 +798,51 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const AttendParams p, 
         const int row = rb * RB + col, i = row / p.group;
         if (row >= p.rows || i >= ql) continue;
         const int h = hk * p.group + (row - i * p.group);
-        float mx = -INFINITY, sum = 0.f, o[kPer];
+        float mx = kNoLogit, sum = 0.f, o[kPer];
 #pragma unroll
         for (int e = 0; e < kPer; ++e) o[e] = 0.f;
         if (units > 0) {
-            const size_t stride = (size_t)RB * (D + 2);
-            for (int c = c0 + lane; c <= c1; c += 32)
-                mx = fmaxf(mx, p.part[(size_t)(2 * c + (c == c0 ? 1 : 0)) * stride + RB * D + col]);
+            // Four parts at a time, their loads all in flight before any is used.
+            constexpr size_t kStride = (size_t)RB * (D + 2);
+            for (int c = c0; c <= c1; c += 4) {
+                float pm[4], pl[4], po[4][kPer];
 #pragma unroll
-            for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-            if (mx != -INFINITY) {
-#pragma unroll 4
-                for (int c = c0; c <= c1; ++c) {
-                    const float* slot = p.part + (size_t)(2 * c + (c == c0 ? 1 : 0)) * stride;
-                    const float f = ptx::ex2(slot[RB * D + col] - mx);
-                    sum = fmaf(slot[RB * (D + 1) + col], f, sum);
+                for (int j = 0; j < 4; ++j) {
+                    pm[j] = kNoLogit;
+                    pl[j] = 0.f;
 #pragma unroll
-                    for (int e = 0; e < kPer; ++e) o[e] = fmaf(slot[col * D + lane * kPer + e], f, o[e]);
+                    for (int e = 0; e < kPer; ++e) po[j][e] = 0.f;
+                    if (c + j <= c1) {
+                        const float* slot = p.part + (size_t)(2 * (c + j) + (c + j == c0 ? 1 : 0)) * kStride;
+                        pm[j] = slot[RB * D + col];
+                        pl[j] = slot[RB * (D + 1) + col];
+#pragma unroll
+                        for (int e = 0; e < kPer; ++e) po[j][e] = slot[col * D + lane * kPer + e];
+                    }
+                }
+                const float m4 = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), mx);
+                const float f0 = ptx::ex2(mx - m4);
+                mx = m4;
+                sum *= f0;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) o[e] *= f0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float f = ptx::ex2(pm[j] - mx);
+                    sum = fmaf(pl[j], f, sum);
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e) o[e] = fmaf(po[j][e], f, o[e]);
                 }
             }
         }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum != 0.f ? 1.f / sum : 0.f;         // 0: no key was visible
         uint16_t* dst = p.o + (((size_t)b * p.Sq + i) * p.Hq + h) * D + lane * kPer;
 #pragma unroll
         for (int e = 0; e < kPer; e += 2)
             *reinterpret_cast<uint32_t*>(dst + e) = bf16 ? ptx::pack_bf16x2(o[e] * inv, o[e + 1] * inv)
                                                          : ptx::pack_f16x2(o[e] * inv, o[e + 1] * inv);
         if (lane == 0)
-            p.lse[((size_t)b * p.Hq + h) * p.Sq + i] = sum > 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+            p.lse[((size_t)b * p.Hq + h) * p.Sq + i] = sum != 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
     }
 }
 
