@@ -50,7 +50,7 @@ struct DeviceInfo {
     bool smem_attr_set[2][4][2][3] = {};   // [D is 128][mask kind][bf16][plain, rotary, packed]
     bool gemm_attr_set = false;
     bool ln_attr_set[3] = {};
-    bool paged_attr_set[3][2][3] = {};     // [cache type][D is 128][rows of a block]
+    bool paged_attr_set[3][2][4] = {};     // [cache type][D is 128][rows of a block]
 };
 
 std::mutex g_mutex;

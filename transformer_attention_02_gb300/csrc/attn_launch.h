@@ -33,7 +33,7 @@ int current_context_id(unsigned long long* id);
 struct DeviceState {
     int num_sms;
     unsigned int* status;                 // run-time status word
-    bool (*paged_attr_set)[2][3];         // [cache type]: see paged::launch_attend
+    bool (*paged_attr_set)[2][4];         // [cache type]: see paged::launch_attend
 };
 
 // Fills `out` for the current context. Returns ATTN_OK, ATTN_ERR_UNSUPPORTED

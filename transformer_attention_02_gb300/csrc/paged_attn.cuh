@@ -42,6 +42,7 @@
 namespace attn {
 namespace paged {
 
+constexpr int kScanInMerge = 256;            // sequences whose units a merge CTA sums itself, one a thread
 constexpr int kNoKey = 0x7fff0000;          // past every key (a sequence holds at most 2^30)
 constexpr float kNoLogit = -3e38f;          // the running maximum before any key
 
@@ -60,14 +61,15 @@ struct Cfg {
     static constexpr int kStageBytes = 2 * kKeys * kRowBytes;
     static constexpr int kStages = kResident == 1 && kRowBytes == 128 ? 5 : 3;
     static constexpr int kRingBytes = kStages * kStageBytes;     // of one warp
-    static constexpr bool kQShared = NT == 4;                    // Q fragments in shared memory, not registers
+    static constexpr bool kQShared = D * NT >= 192;              // Q fragments in shared memory, not registers
     static constexpr int kQStride = D * 2 + 16;                  // bytes of a query row: conflict-free fragment reads
     static constexpr int kScaleOff = kWarps * kRingBytes;        // [warp][stage][tile]{k, v}
     static constexpr int kKeyOff = kScaleOff + kWarps * kStages * kTiles * 8;     // [warp][stage][tile] first key
     static constexpr int kStatOff = kKeyOff + kWarps * kStages * kTiles * 4;      // [warp][row]{max, sum}
     static constexpr int kQOff = kStatOff + kWarps * kRows * 8;
     static constexpr int kFragOff = kQOff + kRows * kQStride;
-    static constexpr int kSmemBytes = kFragOff + (kQShared ? kRows * D * 2 : 0);
+    static constexpr int kShareOff = kFragOff + (kQShared ? kRows * D * 2 : 0);   // [warp]{copies', products'}
+    static constexpr int kSmemBytes = kShareOff + kWarps * 2 * 64;
     static_assert(8 * D * 4 <= kStageBytes, "a warp merges eight rows at a time through one stage of its ring");
     static_assert(kUnit % kKeys == 0, "a stage lies inside one unit");
     static_assert(kQOff % 16 == 0 && kFragOff % 16 == 0, "16-byte accesses");
@@ -84,6 +86,9 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void prefetch_l2(const void* at) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(at) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -214,6 +219,8 @@ struct Share {
     int w_lo;            // keys before it are hidden too, but for the sinks
 };
 
+static_assert(sizeof(Share) <= 64, "the size the shared-memory layout gives it");
+
 // The share at unit x < x_end, searching onwards from s.b (whose list is s.list).
 template <int ROWS>
 __device__ __forceinline__ void locate(const AttendParams& p, int segs, int x, int x_end, Share& s) {
@@ -243,8 +250,8 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     constexpr int kSteps = D / 16;                                // products of 16 dims
     constexpr bool kBf = CT == kBf16;                             // operand type of the products
     extern __shared__ __align__(1024) uint8_t smem_raw[];          // the XOR of chunk offsets needs 256-byte stages
-    __shared__ int s_scan[kThreads / 32 + 1];
-    __shared__ int s_begin[2];                                    // the CTA's first sequence and its first unit
+    __shared__ int s_scan[C::kWarps];
+    __shared__ Share s_begin;                                     // (b, base, list) where the CTA's range begins
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     uint8_t* const ring = smem_raw + warp * C::kRingBytes;
@@ -260,10 +267,12 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     const int segs = p.Hkv * p.row_blocks;                        // segments of a sequence
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
+    KeyList list{};
     int mine = 0;
     for (int b = b_lo; b < b_hi; ++b) {
         bool bad;
-        mine += key_list(p, b, bad).units * segs;
+        list = key_list(p, b, bad);
+        mine += list.units * segs;
         if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
     }
     int incl = mine;
@@ -275,7 +284,8 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     if (lane == 31) s_scan[warp] = incl;
     __syncthreads();
     int before = incl - mine, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
+#pragma unroll
+    for (int w = 0; w < C::kWarps; ++w) {
         if (w < warp) before += s_scan[w];
         total += s_scan[w];
     }
@@ -283,19 +293,22 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     const bool works = (int)blockIdx.x < ctas;
     int x = works ? unit_start(total, ctas, blockIdx.x) : total;
     const int x_end = works ? unit_start(total, ctas, blockIdx.x + 1) : total;
-    if (blockIdx.x == 0 || (before <= x && x < before + mine)) {
+    const bool note = blockIdx.x == 0 && p.B > kScanInMerge;      // the merge reads the offsets of a large batch
+    if (note || (before <= x && x < before + mine)) {
         int at = before;
         for (int b = b_lo; b < b_hi; ++b) {
             bool bad;
-            const int n = key_list(p, b, bad).units * segs;
-            if (blockIdx.x == 0) p.base[b] = at;
+            if (per > 1) list = key_list(p, b, bad);
+            const int n = list.units * segs;
+            if (note) p.base[b] = at;
             if (at <= x && x < at + n) {
-                s_begin[0] = b;
-                s_begin[1] = at;
+                s_begin.b = b;
+                s_begin.base = at;
+                s_begin.list = list;
             }
             at += n;
         }
-        if (blockIdx.x == 0 && b_hi == p.B && b_lo < b_hi) p.base[p.B] = at;
+        if (note && b_hi == p.B && b_lo < b_hi) p.base[p.B] = at;
     }
     __syncthreads();
     if (x >= x_end) return;
@@ -323,13 +336,12 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     // share they are in, ld_i its next stage. A segment then begins with its
     // first stages already on their way, and the memory stays busy while the
     // last segment's rows are merged.
-    Share ld;
-    ld.b = s_begin[0];
-    ld.base = s_begin[1];
-    {
-        bool bad;
-        ld.list = key_list(p, ld.b, bad);
-    }
+    // Both shares stand in shared memory, one copy a warp: they would take some
+    // 25 registers.
+    Share& ld = reinterpret_cast<Share*>(smem_raw + C::kShareOff)[2 * warp];
+    Share& cur = reinterpret_cast<Share*>(smem_raw + C::kShareOff)[2 * warp + 1];
+    if (lane == 0) ld = s_begin;
+    __syncwarp();
     int ld_x = x, ld_i = 0, ld_n = 0, ld_stage = 0;
     int ids = 0;                                                  // page numbers of 32 / kTiles stages, one tile a lane
     constexpr int kBatch = 32 / C::kTiles;
@@ -340,9 +352,29 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
         return (u < ld.list.sink_units ? u : u - ld.list.sink_units + ld.list.first) * kUnit + off % kUnit;
     };
     auto enter = [&]() {                                          // the share at ld_x
-        locate<C::kRows>(p, segs, ld_x, x_end, ld);
+        Share s = ld;
+        locate<C::kRows>(p, segs, ld_x, x_end, s);
+        __syncwarp();
+        if (lane == 0) ld = s;
+        __syncwarp();
         ld_i = 0;
-        ld_n = stages_of(ld.u1 - ld.u0);
+        ld_n = stages_of(s.u1 - s.u0);
+        // The queries are read when the products get there; by then they are in L2.
+        if (warp == 0) {
+            const int r0 = s.rb * C::kRows, row = r0 + lane;
+            const int i = row / p.group;
+            if (lane < C::kRows && row < p.rows && i < s.list.ql) {
+                const uint16_t* q = p.q + ((long long)s.b * p.Sq + i) * p.q_stride +
+                                    (long long)(s.hk * p.group + (row - i * p.group)) * D;
+                const int pos = min(max(s.list.kv - s.list.ql + i, 0), p.max_pos - 1);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) prefetch_l2(q + 64 * c);
+                if (p.rope && row == max(r0, i * p.group)) {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) prefetch_l2(p.rope + (size_t)pos * D + 32 * c);
+                }
+            }
+        }
     };
     enter();
     auto issue = [&]() {
@@ -395,7 +427,8 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
         cp_async_commit();
         ld_stage = ld_stage + 1 == C::kStages ? 0 : ld_stage + 1;
     };
-    Share cur = ld;
+    if (lane == 0) cur = ld;
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) issue();
 
@@ -403,6 +436,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     int st = 0;                                                   // stage of the next products
     for (;;) {
         const int r0 = cur.rb * C::kRows, pos0 = cur.list.kv - cur.list.ql;
+        const int pos_lo = cur.pos_lo, pos_hi = cur.pos_hi;
         // ---- queries, rotated and rounded to their 16-bit type, in shared memory
         const bool bf = CT == kE4m3 ? p.q_bf16 : kBf;
         for (int w = tid; w < C::kRows * (D / 8); w += kThreads) {
@@ -560,7 +594,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                     ks = kv2.x;
                     vs = kv2.y;
                 }
-                const bool whole = k0 + 15 <= cur.pos_lo && (k0 >= cur.pos_hi - p.window + 1 || p.window == 0 || k0 + 16 <= sinks);
+                const bool whole = k0 + 15 <= pos_lo && (k0 >= pos_hi - p.window + 1 || p.window == 0 || k0 + 16 <= sinks);
                 float f[NT][2];                                    // log2 units per value of s
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -622,15 +656,15 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float w[4];
+                    ptx::fma2(w[0], w[1], s[n][0], s[n][1], f[n][0], f[n][1], -m_used[n][0], -m_used[n][1]);
+                    ptx::fma2(w[2], w[3], s[n][2], s[n][3], f[n][0], f[n][1], -m_used[n][0], -m_used[n][1]);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        w[e] = ptx::ex2(fmaf(s[n][e], f[n][e], -m_used[n][e]));
-                        w[2 + e] = ptx::ex2(fmaf(s[n][2 + e], f[n][e], -m_used[n][e]));
-                        l_sum[n][e] += w[e] + w[2 + e];
-                    }
+                    for (int e = 0; e < 4; ++e) w[e] = ptx::ex2(w[e]);
+                    ptx::add2(l_sum[n][0], l_sum[n][1], l_sum[n][0], l_sum[n][1], w[0], w[1]);
+                    ptx::add2(l_sum[n][0], l_sum[n][1], l_sum[n][0], l_sum[n][1], w[2], w[3]);
                     if (CT == kE4m3) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) w[e] *= vf;
+                        ptx::mul2(w[0], w[1], w[0], w[1], vf, vf);
+                        ptx::mul2(w[2], w[3], w[2], w[3], vf, vf);
                     }
                     pb[n][0] = transpose8x8(kBf ? ptx::pack_bf16x2(w[0], w[1]) : ptx::pack_f16x2(w[0], w[1]));
                     pb[n][1] = transpose8x8(kBf ? ptx::pack_bf16x2(w[2], w[3]) : ptx::pack_f16x2(w[2], w[3]));
@@ -735,7 +769,11 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
         }
         x += cur.u1 - cur.u0;
         if (x >= x_end) break;
-        locate<C::kRows>(p, segs, x, x_end, cur);
+        Share s = cur;
+        locate<C::kRows>(p, segs, x, x_end, s);
+        __syncwarp();
+        if (lane == 0) cur = s;
+        __syncwarp();
     }
     cp_async_wait<0>();
 }
@@ -750,7 +788,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const AttendParams p, 
     const int segs = p.Hkv * p.row_blocks;
     const int b = blockIdx.x / segs, seg = blockIdx.x - b * segs;
     int total, first, units;
-    if (p.B <= 256) {
+    if (p.B <= kScanInMerge) {
         // The sequences' units, one a thread: lengths are the step's inputs, so
         // this needs nothing of the attention kernel and runs beside it.
         bool bad;
@@ -802,12 +840,12 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const AttendParams p, 
 #pragma unroll
         for (int e = 0; e < kPer; ++e) o[e] = 0.f;
         if (units > 0) {
-            // Four parts at a time, their loads all in flight before any is used.
+            // Eight parts at a time, their loads all in flight before any is used.
             constexpr size_t kStride = (size_t)RB * (D + 2);
-            for (int c = c0; c <= c1; c += 4) {
-                float pm[4], pl[4], po[4][kPer];
+            for (int c = c0; c <= c1; c += 8) {
+                float pm[8], pl[8], po[8][kPer];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 8; ++j) {
                     pm[j] = kNoLogit;
                     pl[j] = 0.f;
 #pragma unroll
@@ -820,14 +858,16 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const AttendParams p, 
                         for (int e = 0; e < kPer; ++e) po[j][e] = slot[col * D + lane * kPer + e];
                     }
                 }
-                const float m4 = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), mx);
-                const float f0 = ptx::ex2(mx - m4);
-                mx = m4;
+                float m8 = mx;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m8 = fmaxf(m8, pm[j]);
+                const float f0 = ptx::ex2(mx - m8);
+                mx = m8;
                 sum *= f0;
 #pragma unroll
                 for (int e = 0; e < kPer; ++e) o[e] *= f0;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 8; ++j) {
                     const float f = ptx::ex2(pm[j] - mx);
                     sum = fmaf(pl[j], f, sum);
 #pragma unroll
@@ -872,15 +912,17 @@ int launch_instance(bool& attr_set, const AttendParams& p, cudaStream_t stream) 
 }
 
 template <int CT>
-int launch_attend(bool (&attr_set)[2][3], const AttendParams& p, int D, cudaStream_t stream) {
-    bool(&set)[3] = attr_set[D == 128];
+int launch_attend(bool (&attr_set)[2][4], const AttendParams& p, int D, cudaStream_t stream) {
+    bool(&set)[4] = attr_set[D == 128];
     switch (block_rows(p.rows)) {
         case 8:
             return D == 128 ? launch_instance<128, CT, 1>(set[0], p, stream) : launch_instance<64, CT, 1>(set[0], p, stream);
         case 16:
             return D == 128 ? launch_instance<128, CT, 2>(set[1], p, stream) : launch_instance<64, CT, 2>(set[1], p, stream);
+        case 24:
+            return D == 128 ? launch_instance<128, CT, 3>(set[2], p, stream) : launch_instance<64, CT, 3>(set[2], p, stream);
         default:
-            return D == 128 ? launch_instance<128, CT, 4>(set[2], p, stream) : launch_instance<64, CT, 4>(set[2], p, stream);
+            return D == 128 ? launch_instance<128, CT, 4>(set[3], p, stream) : launch_instance<64, CT, 4>(set[3], p, stream);
     }
 }
 

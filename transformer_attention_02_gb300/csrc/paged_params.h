@@ -71,17 +71,18 @@ struct AttendParams {
     bool q_bf16;                  // type of q and o (8-bit caches; 16-bit ones have q's type)
 };
 
-// Rows of a row block (8, 16 or 32) for `rows` query rows a K/V head.
-inline int block_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+// Rows of a row block for `rows` query rows a K/V head: a multiple of the
+// products' eight rows, at most 32.
+inline int block_rows(int rows) { return rows <= 24 ? (rows <= 8 ? 8 : rows <= 16 ? 16 : 24) : 32; }
 
 // CTAs of the attention kernel that fit on an SM at once.
 constexpr int resident_ctas(int D, int rows_per_block) { return D * rows_per_block <= 2048 ? 2 : 1; }
 
 // The attention and the merge of its parts, for one cache type CT (kBf16,
 // kF16, kE4m3). attr_set caches, per context and instance [D is 128][rows of a
-// block 8, 16, 32], that the shared-memory attribute has been set.
+// block 8, 16, 24, 32], that the shared-memory attribute has been set.
 template <int CT>
-int launch_attend(bool (&attr_set)[2][3], const AttendParams& p, int D, cudaStream_t stream);
+int launch_attend(bool (&attr_set)[2][4], const AttendParams& p, int D, cudaStream_t stream);
 
 }  // namespace paged
 }  // namespace attn
