@@ -568,12 +568,10 @@ def attention_block(x, ln_gamma, ln_beta, w_qkv, b_qkv, w_o, b_o, *, Hq: int, Hk
 
 # ------------------------------------------------------- paged key/value cache
 
-def _token_stride(name, t, dev):
-    """Elements from token to token of a (B, S, H, D) tensor whose tokens are evenly spaced and contiguous inside
-    (a contiguous tensor, or a slice of a packed projection)."""
-    if t.dim() != 4:
-        raise ValueError(f"{name} must have 4 dimensions (B, S, H, D)")
-    if t.device != dev or not t.is_cuda:
+def _token_stride(name, t, at):
+    """Elements from token to token of a (B, S, H, D) tensor on device `at` whose tokens are evenly spaced and
+    contiguous inside (a contiguous tensor, or a slice of a packed projection)."""
+    if at < 0 or t.get_device() != at:
         raise ValueError(f"{name} must be a CUDA tensor on the other tensors' device")
     B, S, H, D = t.shape
     if t.is_contiguous():
@@ -588,35 +586,42 @@ def _token_stride(name, t, dev):
     return ss
 
 
-def _int32(name, t, shape, dev):
+def _device_of(x, xname):
+    """Index of a CUDA tensor's device; checks its type and rank too."""
     import torch
-    if not (t.dtype == torch.int32 and t.device == dev and t.is_contiguous() and tuple(t.shape) == shape):
+    if x.dtype is not torch.bfloat16 and x.dtype is not torch.float16:
+        raise ValueError(f"{xname} must be bf16 or fp16")
+    if x.dim() != 4:
+        raise ValueError(f"{xname} must have 4 dimensions (B, S, H, D)")
+    return x.get_device()
+
+
+def _int32(name, t, shape, at):
+    import torch
+    if t.dtype is not torch.int32 or t.get_device() != at or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of shape {shape} on the other tensors' device")
     return t.data_ptr()
 
 
-def _cache_args(x, xname, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, lens, lens_name, table):
+def _cache_args(x, xname, at, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, lens, lens_name, table):
     """Checks what the cache's calls share; returns their common arguments."""
     import torch
-    dev = x.device
-    if x.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"{xname} must be bf16 or fp16")
-    if not (k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype
-            and k_cache.device == dev and v_cache.device == dev and k_cache.is_contiguous()
-            and v_cache.is_contiguous()):
+    shape, kind = k_cache.shape, k_cache.dtype
+    if (len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not kind or k_cache.get_device() != at
+            or v_cache.get_device() != at or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
         raise ValueError(f"k_cache and v_cache must be contiguous (n_pages, Hkv, page, D) tensors of one type on "
                          f"{xname}'s device")
-    n_pages, Hkv, page, D = k_cache.shape
+    n_pages, Hkv, page, D = shape
     ks = vs = None
-    if k_cache.dtype == torch.float8_e4m3fn:
+    if kind is torch.float8_e4m3fn:
         kind = CACHE_E4M3
-        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            if t is None or not (t.dtype == torch.float32 and t.device == dev and t.is_contiguous()
-                                 and tuple(t.shape) == (n_pages, Hkv)):
-                raise ValueError(f"{name} must be a contiguous FP32 CUDA tensor of shape (n_pages, Hkv): an 8-bit cache "
-                                 "needs its scales")
+        for t in (k_scale, v_scale):
+            if t is None or (t.dtype is not torch.float32 or t.get_device() != at or t.shape != (n_pages, Hkv)
+                             or not t.is_contiguous()):
+                raise ValueError("k_scale and v_scale must be contiguous FP32 CUDA tensors of shape (n_pages, Hkv): an "
+                                 "8-bit cache needs its scales")
         ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
-    elif k_cache.dtype == x.dtype:
+    elif kind is x.dtype:
         kind = CACHE_16BIT
         if k_scale is not None or v_scale is not None:
             raise ValueError("a 16-bit cache has no scales")
@@ -626,35 +631,35 @@ def _cache_args(x, xname, k_cache, v_cache, k_scale, v_scale, block_table, kv_le
     if block_table.dim() != 2:
         raise ValueError("block_table must have 2 dimensions (B, max_pages)")
     max_pages = block_table.shape[1]
-    bt = _int32("block_table", block_table, (B, max_pages), dev)
-    kl = _int32("kv_lens", kv_lens, (B,), dev)
-    nl = None if lens is None else _int32(lens_name, lens, (B,), dev)
+    bt = _int32("block_table", block_table, (B, max_pages), at)
+    kl = _int32("kv_lens", kv_lens, (B,), at)
+    nl = None if lens is None else _int32(lens_name, lens, (B,), at)
     rope, max_pos = None, 0
     if table is not None:
-        if not (table.dtype == torch.float32 and table.dim() == 3 and tuple(table.shape[1:]) == (D // 2, 2)
-                and table.device == dev and table.is_contiguous()):
+        if (table.dtype is not torch.float32 or table.dim() != 3 or table.shape[1:] != (D // 2, 2)
+                or table.get_device() != at or not table.is_contiguous()):
             raise ValueError("table must be the (max_pos, D/2, 2) FP32 CUDA tensor of rope_table() for this D")
         rope, max_pos = table.data_ptr(), table.shape[0]
     return kind, ks, vs, bt, kl, nl, Hkv, D, page, max_pages, n_pages, rope, max_pos
 
 
-class _on_device:
-    """Makes a tensor's device current for a call, if it is not (the C ABI works on the current device)."""
+def _enter_device(at):
+    """Makes device `at` current (the C ABI works on the current device); returns the one to go back to, or None."""
+    import torch
+    now = torch.cuda.current_device()
+    if now == at:
+        return None
+    torch.cuda.set_device(at)
+    return now
 
-    def __init__(self, dev):
-        self.dev, self.back = dev, None
 
-    def __enter__(self):
-        import torch
-        at = torch.cuda.current_device()
-        if self.dev.index is not None and self.dev.index != at:
-            self.back = at
-            torch.cuda.set_device(self.dev)
-
-    def __exit__(self, *exc):
-        import torch
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+def _stream_on(at, stream):
+    """Handle of `stream`, or of device `at`'s current stream."""
+    import torch
+    if stream is not None:
+        return stream.cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)      # current_stream() without making a Stream object
+    return torch.cuda.current_stream(at).cuda_stream if raw is None else raw(at)
 
 
 def kv_append(k, v, k_cache, v_cache, block_table, kv_lens, *, new_lens=None, k_scale=None, v_scale=None, table=None,
@@ -668,16 +673,23 @@ def kv_append(k, v, k_cache, v_cache, block_table, kv_lens, *, new_lens=None, k_
     kv_lens[b] - new_lens[b] + s. table: rope_table() to rotate the keys to their positions, or None.
     """
     import torch
-    a = _cache_args(k, "k", k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, new_lens, "new_lens", table)
-    kind, ks, vs, bt, kl, nl, Hkv, D, page, max_pages, n_pages, rope, max_pos = a
-    if v.dtype != k.dtype or v.shape != k.shape or k.dim() != 4 or k.shape[2] != Hkv or k.shape[3] != D:
+    at = _device_of(k, "k")
+    kind, ks, vs, bt, kl, nl, Hkv, D, page, max_pages, n_pages, rope, max_pos = _cache_args(
+        k, "k", at, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, new_lens, "new_lens", table)
+    shape = k.shape
+    B, S = shape[0], shape[1]
+    if v.dtype is not k.dtype or v.shape != shape or shape[2] != Hkv or shape[3] != D:
         raise ValueError("k and v must be (B, S, Hkv, D) tensors of one type, with the cache's Hkv and D")
-    B, S = k.shape[0], k.shape[1]
-    k_stride, v_stride = _token_stride("k", k, k.device), _token_stride("v", v, k.device)
-    fn = attn_kv_append if k.dtype == torch.bfloat16 else attn_kv_append_f16
-    with _on_device(k.device):
+    k_stride, v_stride = _token_stride("k", k, at), _token_stride("v", v, at)
+    L = lib()
+    fn = L.attn_kv_append if k.dtype is torch.bfloat16 else L.attn_kv_append_f16
+    back = _enter_device(at)
+    try:
         rc = fn(k.data_ptr(), v.data_ptr(), k_stride, v_stride, k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, bt, kl,
-                nl, B, S, Hkv, D, page, max_pages, n_pages, kind, rope, max_pos, _stream_handle(stream))
+                nl, B, S, Hkv, D, page, max_pages, n_pages, kind, rope, max_pos, _stream_on(at, stream))
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_kv_append")
 
@@ -692,40 +704,48 @@ def attention_paged(q, k_cache, v_cache, block_table, kv_lens, *, q_lens=None, k
     uint8 CUDA tensor of at least attn_paged_workspace_bytes bytes (allocated here when omitted).
     """
     import torch
-    a = _cache_args(q, "q", k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, q_lens, "q_lens", table)
-    kind, ks, vs, bt, kl, nl, Hkv, D, page, max_pages, n_pages, rope, max_pos = a
-    dev = q.device
-    q_stride = _token_stride("q", q, dev)
-    B, Sq, Hq = q.shape[0], q.shape[1], q.shape[2]
-    if q.shape[3] != D:
+    at = _device_of(q, "q")
+    kind, ks, vs, bt, kl, nl, Hkv, D, page, max_pages, n_pages, rope, max_pos = _cache_args(
+        q, "q", at, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, q_lens, "q_lens", table)
+    q_stride = _token_stride("q", q, at)
+    shape = q.shape
+    B, Sq, Hq, Dq = shape
+    if Dq != D:
         raise ValueError("q and the cache disagree on D")
-    with _on_device(dev):
+    L = lib()
+    back = _enter_device(at)
+    try:
         made = []
         if out is None:
-            out = torch.empty((B, Sq, Hq, D), dtype=q.dtype, device=dev)
+            out = torch.empty(shape, dtype=q.dtype, device=q.device)
             made.append(out)
-        elif not (out.dtype == q.dtype and out.device == dev and tuple(out.shape) == (B, Sq, Hq, D)
-                  and out.is_contiguous()):
+        elif out.dtype is not q.dtype or out.get_device() != at or out.shape != shape or not out.is_contiguous():
             raise ValueError("out must be a contiguous (B, Sq, Hq, D) tensor of q's type and device")
         if lse is None:
-            lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=dev)
+            lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
             made.append(lse)
-        elif not (lse.dtype == torch.float32 and lse.device == dev and tuple(lse.shape) == (B, Hq, Sq)
-                  and lse.is_contiguous()):
+        elif (lse.dtype is not torch.float32 or lse.get_device() != at or lse.shape != (B, Hq, Sq)
+              or not lse.is_contiguous()):
             raise ValueError("lse must be a contiguous FP32 (B, Hq, Sq) tensor on q's device")
         if workspace is None:
-            workspace = torch.empty(attn_paged_workspace_bytes(B, Hq, Hkv, Sq, D) or 1, dtype=torch.uint8, device=dev)
+            size = L.attn_paged_workspace_bytes(B, Hq, Hkv, Sq, D)
+            workspace = torch.empty(size or 1, dtype=torch.uint8, device=q.device)
             made.append(workspace)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
+        else:
+            if workspace.get_device() != at or not workspace.is_contiguous():
+                raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
+            size = workspace.numel() * workspace.element_size()
         if stream is not None:
             for t in made:                     # allocated on the current stream, used on another
                 t.record_stream(stream)
-        sc = float("nan") if scale is None else float(scale)
-        fn = attn_fwd_paged if q.dtype == torch.bfloat16 else attn_fwd_paged_f16
+        fn = L.attn_fwd_paged if q.dtype is torch.bfloat16 else L.attn_fwd_paged_f16
         rc = fn(q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, bt, kl, nl, out.data_ptr(),
-                lse.data_ptr(), B, Hq, Hkv, Sq, D, page, max_pages, n_pages, kind, sc, int(window), int(sinks), rope,
-                max_pos, workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream_handle(stream))
+                lse.data_ptr(), B, Hq, Hkv, Sq, D, page, max_pages, n_pages, kind,
+                float("nan") if scale is None else scale, window, sinks, rope, max_pos, workspace.data_ptr(), size,
+                _stream_on(at, stream))
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_fwd_paged")
     return out, lse
