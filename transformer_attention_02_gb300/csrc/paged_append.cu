@@ -15,6 +15,9 @@
 // range (below 2^-6 * scale); an arbitrary scale would round every code again
 // each time. e4m3 has the same relative precision under any scale, so the
 // power of two costs nothing else.
+#include <algorithm>
+#include <type_traits>
+
 #include "../../include/attn.h"
 #include "attn_kernel.cuh"
 #include "paged_params.h"
@@ -23,7 +26,11 @@ namespace attn {
 namespace paged {
 namespace {
 
-constexpr int kThreads = 128;
+// A block's new tokens as 16-byte pieces (eight values): HELD a thread. Steps of
+// few tokens have one piece a thread and up to 512 threads, prompts four and up
+// to 256, large pages eight and up to 512 (256 tokens of 16 pieces).
+__host__ __device__ constexpr int max_threads(int held) { return held == 4 ? 256 : 512; }
+__host__ __device__ constexpr int min_ctas(int held) { return held == 4 ? 3 : 1; }
 
 // Two floats to two e4m3 codes (round to nearest even, beyond +-448 to +-448,
 // NaN stays NaN); `lo` in the low byte.
@@ -43,9 +50,10 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t w) {
     return f;
 }
 
-__device__ __forceinline__ float2 widen(uint32_t w, bool bf16) {
+template <bool BF16>
+__device__ __forceinline__ float2 widen(uint32_t w) {
     float2 f;
-    if (bf16) {
+    if (BF16) {
         f.x = __uint_as_float(w << 16);
         f.y = __uint_as_float(w & 0xffff0000u);
     } else {
@@ -64,30 +72,25 @@ __device__ __forceinline__ float block_scale(float a) {
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-__device__ __forceinline__ float block_max(float v, float* red) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = red[0];
-#pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) v = fmaxf(v, red[w]);
-    return v;
-}
-
-// One CTA per (sequence, touched page, K/V head, keys or values).
-template <bool E4M3>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
-    __shared__ float red[kThreads / 32];
+// One CTA per (sequence, touched page, group of K/V heads, keys or values); it
+// takes the blocks of its heads one after the other, every thread holding the
+// same slots and dims of each, so that a page's table entries come from L1
+// after the first head. A block's new values stay in registers (FP32, rotated)
+// between the pass that finds their maximum and the one that writes them.
+// Bound by memory: each input is read and each code written once.
+template <bool E4M3, int HELD, bool BF16>
+__global__ void __launch_bounds__(max_threads(HELD), min_ctas(HELD)) append_kernel(const AppendParams p) {
+    __shared__ float red[2][max_threads(HELD) / 32];
     const int is_v = blockIdx.x & 1;
     long long u = blockIdx.x >> 1;
-    const int h = (int)(u % p.Hkv);
-    u /= p.Hkv;
+    const int groups = (p.Hkv + p.head_group - 1) / p.head_group;
+    const int h0 = (int)(u % groups) * p.head_group, h1 = min(p.Hkv, h0 + p.head_group);
+    u /= groups;
     const int j = (int)(u % p.touched);
     const int b = (int)(u / p.touched);
     const int page = 1 << p.page_shift;
 
-    int kv = p.kv_lens[b], n_new = p.new_lens ? p.new_lens[b] : p.S;
+    const int kv = p.kv_lens[b], n_new = p.new_lens ? p.new_lens[b] : p.S;
     if (n_new == 0) return;
     // Lengths the table or the step cannot hold: nothing of the sequence is written.
     if (n_new < 0 || n_new > p.S || kv < n_new || (kv - 1) >> p.page_shift >= p.max_pages ||
@@ -106,105 +109,152 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
     const int pos0 = max(first, pg << p.page_shift);   // the page's first new token, and one past its last
     const int pos1 = min(kv, (pg + 1) << p.page_shift);
     const int slot0 = pos0 & (page - 1);
-    const int chunks = p.D / 8;                        // 16-byte pieces (eight values) of a token
+    const int chunks = p.D / 8, cshift = p.D == 128 ? 4 : 3;   // pieces of a token
     const int n = (pos1 - pos0) * chunks;
-    const uint16_t* src = (is_v ? p.v : p.k) + ((long long)b * p.S + (pos0 - first)) * (is_v ? p.v_stride : p.k_stride) +
-                          (long long)h * p.D;
     const long long stride = is_v ? p.v_stride : p.k_stride;
+    const uint16_t* const src = (is_v ? p.v : p.k) + ((long long)b * p.S + (pos0 - first)) * stride;
     const bool turn = !is_v && p.rope != nullptr;
-    const size_t block = ((size_t)id * p.Hkv + h) << p.page_shift;
+    const float4* const table = reinterpret_cast<const float4*>(p.rope) + (size_t)pos0 * (p.D / 4);
 
-    auto load = [&](int c, float* x) {
-        const int t = c / chunks, g = c - t * chunks;
-        const uint4 w = *reinterpret_cast<const uint4*>(src + t * stride + 8 * g);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-        float4 a0 = make_float4(1.f, 0.f, 1.f, 0.f), a1 = a0;
-        if (turn) {
-            const float4* at = reinterpret_cast<const float4*>(p.rope) + (size_t)(pos0 + t) * (p.D / 4) + 2 * g;
-            a0 = __ldg(at);
-            a1 = __ldg(at + 1);
-        }
-        const float cs[4] = {a0.x, a0.z, a1.x, a1.z}, sn[4] = {a0.y, a0.w, a1.y, a1.w};
+    // A thread's pieces are whole tokens apart (the threads are a multiple of a
+    // token's pieces). Raw pieces of the next head are fetched while the current
+    // one is worked on.
+    const uint16_t* const src_t = src + (threadIdx.x >> cshift) * stride + 8 * (threadIdx.x & (chunks - 1));
+    const long long apart = (blockDim.x >> cshift) * stride;
+    uint4 w[HELD];
+    auto fetch = [&](int h) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = widen(ws[i], p.bf16);
-            x[2 * i] = turn ? f.x * cs[i] - f.y * sn[i] : f.x;
-            x[2 * i + 1] = turn ? f.y * cs[i] + f.x * sn[i] : f.y;
+        for (int i = 0; i < HELD; ++i) {
+            const int c = threadIdx.x + i * blockDim.x;
+            w[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (c < n) w[i] = __ldg(reinterpret_cast<const uint4*>(src_t + i * apart + h * p.D));
         }
     };
-
-    if (!E4M3) {
-        uint16_t* dst = static_cast<uint16_t*>(is_v ? p.v_cache : p.k_cache) + (block + slot0) * p.D;
-        for (int c = threadIdx.x; c < n; c += kThreads) {
-            float x[8];
-            load(c, x);
-            uint32_t w[4];
+    fetch(h0);
+    for (int h = h0; h < h1; ++h) {
+        const size_t block = ((size_t)id * p.Hkv + h) << p.page_shift;
+        float* const scale_at = E4M3 ? (is_v ? p.v_scale : p.k_scale) + (size_t)id * p.Hkv + h : nullptr;
+        const float before = E4M3 && slot0 > 0 ? *scale_at : 0.f;
+        float x[HELD][8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = p.bf16 ? ptx::pack_bf16x2(x[2 * i], x[2 * i + 1]) : ptx::pack_f16x2(x[2 * i], x[2 * i + 1]);
-            *reinterpret_cast<uint4*>(dst + 8 * (size_t)c) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        return;
-    }
-
-    float a = 0.f;
-    for (int c = threadIdx.x; c < n; c += kThreads) {
-        float x[8];
-        load(c, x);
+        for (int i = 0; i < HELD; ++i) {
+            const int c = threadIdx.x + i * blockDim.x;
+            const uint32_t ws[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float m = fabsf(x[i]);
-            a = fmaxf(a, m <= 3.402823466e38f ? m : 0.f);        // NaN and infinities do not set the scale
-        }
-    }
-    a = block_max(a, red);
-    uint8_t* blk = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + block * p.D;
-    float* scale_at = (is_v ? p.v_scale : p.k_scale) + (size_t)id * p.Hkv + h;
-    float scale = block_scale(a);
-    if (slot0 > 0) {
-        // Earlier tokens share the block: its scale only grows, and their codes move with it.
-        const float before = *scale_at;
-        scale = fmaxf(before, scale);
-        if (scale != before) {
-            const float f = before / scale;
-            uint2* old = reinterpret_cast<uint2*>(blk);
-            for (int c = threadIdx.x; c < slot0 * chunks; c += kThreads) {
-                uint2 w = old[c];
-                const uint32_t ws[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
-                uint32_t r[4];
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = widen<BF16>(ws[e]);
+                x[i][2 * e] = f.x;
+                x[i][2 * e + 1] = f.y;
+            }
+            if (turn && c < n) {
+                const float4 a0 = __ldg(table + 2 * c), a1 = __ldg(table + 2 * c + 1);
+                const float cs[4] = {a0.x, a0.z, a1.x, a1.z}, sn[4] = {a0.y, a0.w, a1.y, a1.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 v2 = from_e4m3x2(ws[i]);
-                    r[i] = to_e4m3x2(v2.x * f, v2.y * f);
+                for (int e = 0; e < 4; ++e) {
+                    const float f0 = x[i][2 * e], f1 = x[i][2 * e + 1];
+                    x[i][2 * e] = f0 * cs[e] - f1 * sn[e];
+                    x[i][2 * e + 1] = f1 * cs[e] + f0 * sn[e];
                 }
-                old[c] = make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
             }
         }
-    }
-    __syncthreads();                                   // every thread has read the old scale
-    if (threadIdx.x == 0) *scale_at = scale;
-    const float inv = 1.f / scale;                     // exact: a power of two in range
-    uint2* dst = reinterpret_cast<uint2*>(blk + (size_t)slot0 * p.D);
-    for (int c = threadIdx.x; c < n; c += kThreads) {
-        float x[8];
-        load(c, x);
-        uint32_t r[4];
+        if (h + 1 < h1) fetch(h + 1);
+        if (!E4M3) {
+            uint4* const dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_v ? p.v_cache : p.k_cache) +
+                                                        (block + slot0) * p.D);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = to_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
-        dst[c] = make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+            for (int i = 0; i < HELD; ++i) {
+                const int c = threadIdx.x + i * blockDim.x;
+                uint32_t r[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    r[e] = BF16 ? ptx::pack_bf16x2(x[i][2 * e], x[i][2 * e + 1])
+                                  : ptx::pack_f16x2(x[i][2 * e], x[i][2 * e + 1]);
+                if (c < n) dst[c] = make_uint4(r[0], r[1], r[2], r[3]);
+            }
+            continue;
+        }
+
+        float a = 0.f;
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(x[i][e]));      // (passes NaN over)
+        if (a > 3.402823466e38f) {                     // infinities do not set the scale
+            a = 0.f;
+#pragma unroll
+            for (int i = 0; i < HELD; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(x[i][e]) <= 3.402823466e38f ? fabsf(x[i][e]) : 0.f);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        float* const r2 = red[(h - h0) & 1];           // two in turn: one barrier a head
+        if ((threadIdx.x & 31) == 0) r2[threadIdx.x >> 5] = a;
+        __syncthreads();
+        for (int w = 0; w < (int)blockDim.x / 32; ++w) a = fmaxf(a, r2[w]);
+
+        uint8_t* const blk = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + block * p.D;
+        float scale = block_scale(a);
+        if (slot0 > 0) {
+            // Earlier tokens share the block: its scale only grows, and their codes move with it.
+            scale = fmaxf(before, scale);
+            if (scale != before) {
+                const float f = before / scale;
+                uint2* old = reinterpret_cast<uint2*>(blk);
+                for (int c = threadIdx.x; c < slot0 * chunks; c += blockDim.x) {
+                    const uint2 w = old[c];
+                    const uint32_t ws[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
+                    uint32_t r[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 v2 = from_e4m3x2(ws[i]);
+                        r[i] = to_e4m3x2(v2.x * f, v2.y * f);
+                    }
+                    old[c] = make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+                }
+            }
+        }
+        if (threadIdx.x == 0) *scale_at = scale;       // every thread read the old one before the barrier
+        const float inv = 1.f / scale;                 // exact: a power of two in range
+        uint2* const dst = reinterpret_cast<uint2*>(blk + (size_t)slot0 * p.D);
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) {
+            const int c = threadIdx.x + i * blockDim.x;
+            uint32_t r[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float y0, y1;
+                ptx::mul2(y0, y1, x[i][2 * e], x[i][2 * e + 1], inv, inv);
+                r[e] = to_e4m3x2(y0, y1);
+            }
+            if (c < n) dst[c] = make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+        }
     }
 }
 
 }  // namespace
 
-int launch_append(const AppendParams& p, int cache, int num_sms, cudaStream_t stream) {
-    (void)num_sms;
-    const unsigned grid = (unsigned)((long long)p.B * p.touched * p.Hkv * 2);
+int launch_append(AppendParams p, int cache, int num_sms, cudaStream_t stream) {
+    // Heads a CTA takes in turn: table entries are read once per group, but only
+    // where the blocks fill the SMs several times over without it.
+    const long long blocks = (long long)p.B * p.touched * p.Hkv * 2;
+    p.head_group = (int)std::max(1LL, std::min<long long>(std::min(p.Hkv, 8), blocks / (8LL * num_sms)));
+    const int groups = (p.Hkv + p.head_group - 1) / p.head_group;
+    const unsigned grid = (unsigned)((long long)p.B * p.touched * groups * 2);
+    const int pieces = std::min(p.S, 1 << p.page_shift) * (p.D / 8);
+    auto run = [&](auto kernel, int held) {
+        const int threads = ((pieces + held - 1) / held + 31) / 32 * 32;
+        kernel<<<grid, threads, 0, stream>>>(p);
+        return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    };
+    auto pick = [&](auto e4m3, auto bf16) {
+        constexpr bool kE = decltype(e4m3)::value, kB = decltype(bf16)::value;
+        if (pieces <= max_threads(1)) return run(append_kernel<kE, 1, kB>, 1);
+        return pieces <= 4 * max_threads(4) ? run(append_kernel<kE, 4, kB>, 4) : run(append_kernel<kE, 8, kB>, 8);
+    };
     if (cache == kE4m3)
-        append_kernel<true><<<grid, kThreads, 0, stream>>>(p);
-    else
-        append_kernel<false><<<grid, kThreads, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+        return p.bf16 ? pick(std::true_type{}, std::true_type{}) : pick(std::true_type{}, std::false_type{});
+    return p.bf16 ? pick(std::false_type{}, std::true_type{}) : pick(std::false_type{}, std::false_type{});
 }
 
 }  // namespace paged

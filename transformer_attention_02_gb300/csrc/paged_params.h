@@ -35,12 +35,13 @@ struct AppendParams {
     int B, S, Hkv, D;
     int page_shift, max_pages, n_pages;
     int touched;                  // pages a sequence's step may touch
+    int head_group;               // K/V heads a CTA takes in turn (set by the launcher)
     bool bf16;                    // type of k and v
     unsigned int* status;
 };
 
 // e4m3 or 16-bit cache by `cache`; ATTN_OK or ATTN_ERR_CUDA.
-int launch_append(const AppendParams& p, int cache, int num_sms, cudaStream_t stream);
+int launch_append(AppendParams p, int cache, int num_sms, cudaStream_t stream);
 
 constexpr int kUnit = 128;        // keys of a scheduling unit
 
