@@ -370,6 +370,27 @@ int attn_block_fwd(const void *x, const void *ln_gamma, const void *ln_beta, con
 size_t attn_block_workspace_bytes(int B, int S, int Hq, int Hkv, int D);
 
 /*
+ * attn_fwd_window / attn_fwd_window_f16 — causal attention with a sliding window
+ * and sinks, on contiguous tensors (prefill; the single-token form over a cache
+ * is attn_fwd_paged). Query i sits at position p = i + Sk - Sq and sees the keys
+ * j <= p with j > p - window (its own among them) or j < sinks: the first tokens
+ * that stay visible for good.
+ *   window      >= 1; sinks >= 0. A window or sinks of Sk or more hide nothing
+ *               (attn_fwd with the causal mask).
+ * Other arguments, layouts, results and errors as for attn_fwd / attn_fwd_f16;
+ * rows without a visible key get o = 0, lse = -inf. Blocks of 128 keys that no
+ * row of a 256-row tile sees are neither read nor computed, so the time grows
+ * with Sq * (window + sinks), not with Sq * Sk. As for attn_fwd, a key hidden
+ * from some rows of a tile only must be finite in V.
+ */
+int attn_fwd_window(const void *q, const void *k, const void *v, void *o, float *lse,
+                    int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                    float scale, int window, int sinks, attn_stream_t stream);
+int attn_fwd_window_f16(const void *q, const void *k, const void *v, void *o, float *lse,
+                        int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                        float scale, int window, int sinks, attn_stream_t stream);
+
+/*
  * The paged key/value cache. Keys and values live in pages of `page` tokens (a
  * power of two, 16 to 256):
  *   k_cache, v_cache   device, (n_pages, Hkv, page, D), contiguous, 16-byte

@@ -12,5 +12,6 @@ from .attn import (  # noqa: F401
     attention_splitkv, attn_fwd_rope, attn_fwd_rope_f16, attn_rope_table, attn_rope_apply, attn_rope_apply_f16,
     attention_rope, rope_table, rope_apply, attn_fwd_host, attn_fwd_host_f16, attn_fwd_host_workspace_bytes,
     attention_host, attn_linear, attn_layernorm, attn_fwd_qkvpacked, attn_block_fwd, attn_block_workspace_bytes,
-    linear, layernorm, attention_qkvpacked, attention_block, CACHE_16BIT, CACHE_E4M3, attn_kv_append,
+    linear, layernorm, attention_qkvpacked, attention_block, attn_fwd_window, attn_fwd_window_f16,
+    attention_window, CACHE_16BIT, CACHE_E4M3, attn_kv_append,
     attn_kv_append_f16, attn_fwd_paged, attn_fwd_paged_f16, attn_paged_workspace_bytes, kv_append, attention_paged)

@@ -82,6 +82,9 @@ def lib() -> ctypes.CDLL:
     L.attn_splitkv_num_splits.restype = I
     L.attn_splitkv_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
     L.attn_splitkv_workspace_bytes.restype = ctypes.c_size_t
+    for f in (L.attn_fwd_window, L.attn_fwd_window_f16):
+        f.argtypes = [P, P, P, P, P, I, I, I, I, I, I, ctypes.c_float, I, I, P]
+        f.restype = I
     LL, F = ctypes.c_longlong, ctypes.c_float
     for f in (L.attn_kv_append, L.attn_kv_append_f16):
         f.argtypes = [P, P, LL, LL, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, I, P]
@@ -202,6 +205,14 @@ def attn_splitkv_num_splits(B, Hq, Hkv, Sq, Sk, num_splits=0) -> int:
 
 def attn_splitkv_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, num_splits=0) -> int:
     return int(lib().attn_splitkv_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, num_splits))
+
+
+def attn_fwd_window(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, scale, window, sinks, stream) -> int:
+    return lib().attn_fwd_window(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, scale, window, sinks, stream)
+
+
+def attn_fwd_window_f16(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, scale, window, sinks, stream) -> int:
+    return lib().attn_fwd_window_f16(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, scale, window, sinks, stream)
 
 
 def attn_kv_append(k, v, k_stride, v_stride, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, new_lens, B, S,
@@ -566,7 +577,57 @@ def attention_block(x, ln_gamma, ln_beta, w_qkv, b_qkv, w_o, b_o, *, Hq: int, Hk
     return out
 
 
-# ------------------------------------------------------- paged key/value cache
+# ------------------------------------------- windows and the paged key/value cache
+
+def attention_window(q, k, v, *, window: int, sinks: int = 0, scale=None, out=None, lse=None, stream=None):
+    """O, LSE = causal attention with a sliding window on (B, S, H, D) bf16 or fp16 CUDA tensors.
+
+    The query at position p (its row plus Sk - Sq) sees the last `window` keys up to p, its own included, and the first
+    `sinks` keys. scale: None selects 1/sqrt(D). out/lse: optional preallocated outputs.
+    """
+    import torch
+    at = _device_of(q, "q")
+    qs, ks = q.shape, k.shape
+    B, Sq, Hq, D = qs
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if at < 0 or t.get_device() != at or t.dtype is not q.dtype or t.dim() != 4 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous 4-D CUDA tensor (B, S, H, D) of q's dtype and device")
+    if ks[0] != B or ks[3] != D or v.shape != ks:
+        raise ValueError("q, k, v shapes disagree")
+    L = lib()
+    back = _enter_device(at)
+    try:
+        out, lse = _outputs(q, at, out, lse, stream)
+        fn = L.attn_fwd_window if q.dtype is torch.bfloat16 else L.attn_fwd_window_f16
+        rc = fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, ks[2], Sq, ks[1], D,
+                float("nan") if scale is None else scale, window, sinks, _stream_on(at, stream))
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_fwd_window")
+    return out, lse
+
+
+def _outputs(q, at, out, lse, stream):
+    """The given outputs of an attention over q (B, Sq, Hq, D), checked, or new ones."""
+    import torch
+    shape = q.shape
+    B, Sq, Hq, _ = shape
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        if stream is not None:
+            out.record_stream(stream)              # allocated on the current stream, used on another
+    elif out.dtype is not q.dtype or out.get_device() != at or out.shape != shape or not out.is_contiguous():
+        raise ValueError("out must be a contiguous (B, Sq, Hq, D) tensor of q's type and device")
+    if lse is None:
+        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
+        if stream is not None:
+            lse.record_stream(stream)
+    elif (lse.dtype is not torch.float32 or lse.get_device() != at or lse.shape != (B, Hq, Sq)
+          or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous FP32 (B, Hq, Sq) tensor on q's device")
+    return out, lse
 
 def _token_stride(name, t, at):
     """Elements from token to token of a (B, S, H, D) tensor on device `at` whose tokens are evenly spaced and
@@ -715,29 +776,16 @@ def attention_paged(q, k_cache, v_cache, block_table, kv_lens, *, q_lens=None, k
     L = lib()
     back = _enter_device(at)
     try:
-        made = []
-        if out is None:
-            out = torch.empty(shape, dtype=q.dtype, device=q.device)
-            made.append(out)
-        elif out.dtype is not q.dtype or out.get_device() != at or out.shape != shape or not out.is_contiguous():
-            raise ValueError("out must be a contiguous (B, Sq, Hq, D) tensor of q's type and device")
-        if lse is None:
-            lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
-            made.append(lse)
-        elif (lse.dtype is not torch.float32 or lse.get_device() != at or lse.shape != (B, Hq, Sq)
-              or not lse.is_contiguous()):
-            raise ValueError("lse must be a contiguous FP32 (B, Hq, Sq) tensor on q's device")
+        out, lse = _outputs(q, at, out, lse, stream)
         if workspace is None:
             size = L.attn_paged_workspace_bytes(B, Hq, Hkv, Sq, D)
             workspace = torch.empty(size or 1, dtype=torch.uint8, device=q.device)
-            made.append(workspace)
+            if stream is not None:
+                workspace.record_stream(stream)
         else:
             if workspace.get_device() != at or not workspace.is_contiguous():
                 raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
             size = workspace.numel() * workspace.element_size()
-        if stream is not None:
-            for t in made:                     # allocated on the current stream, used on another
-                t.record_stream(stream)
         fn = L.attn_fwd_paged if q.dtype is torch.bfloat16 else L.attn_fwd_paged_f16
         rc = fn(q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, bt, kl, nl, out.data_ptr(),
                 lse.data_ptr(), B, Hq, Hkv, Sq, D, page, max_pages, n_pages, kind,

@@ -1,10 +1,10 @@
 """Build the CUDA library ``libattn.so`` in-tree with nvcc for sm_103a.
 
-Translation units (the host ABI, the host-buffer pipeline, the attention
+The translation units (the host ABI, the host-buffer pipeline, the attention
 block's GEMM and LayerNorm, the families of attention-kernel variants, the
-paged cache's append and attention) are compiled in parallel to objects under ``_build/`` and linked into one shared
-library; one -gencode, no cmake. The results sit next to this file and are
-git-ignored.
+paged cache's append and attention) are compiled in parallel to objects under
+``_build/`` and linked into one shared library; one -gencode, no cmake. The
+results sit next to this file and are git-ignored.
 """
 from __future__ import annotations
 
@@ -20,7 +20,8 @@ LIBRARY = os.path.join(HERE, "libattn.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = [os.path.join(CSRC, f) for f in
            ("attn_api.cu", "attn_host.cu", "block_kernels.cu", "fwd_bf16.cu", "fwd_f16.cu", "fwd_rope_bf16.cu",
-            "fwd_rope_f16.cu", "fwd_pack_bf16.cu", "fwd_pack_f16.cu", "paged_api.cu", "paged_append.cu",
+            "fwd_rope_f16.cu", "fwd_pack_bf16.cu", "fwd_pack_f16.cu", "fwd_window_bf16.cu",
+            "fwd_window_f16.cu", "paged_api.cu", "paged_append.cu",
             "paged_attn_bf16.cu", "paged_attn_f16.cu", "paged_attn_e4m3.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in
                      ("attn_kernel.cuh", "ptx.cuh", "attn_launch.h", "attn_fwd_inst.cuh", "block_params.h",

@@ -47,7 +47,7 @@ struct DeviceInfo {
     int num_sms = 0;
     unsigned int* status = nullptr;     // device address of g_device_status
     void* noalloc_scratch = nullptr;    // device address of the allocation-free scratch array
-    bool smem_attr_set[2][4][2][3] = {};   // [D is 128][mask kind][bf16][plain, rotary, packed]
+    bool smem_attr_set[2][4][2][4] = {};   // [D is 128][mask kind][bf16][plain, rotary, packed, windowed]
     bool gemm_attr_set = false;
     bool ln_attr_set[3] = {};
     bool paged_attr_set[3][2][4] = {};     // [cache type][D is 128][rows of a block]
@@ -235,6 +235,13 @@ int launch_d(DeviceInfo& dev, int mask_kind, const CUtensorMap& tq, const CUtens
     }
 }
 
+template <int D, bool BF16>
+int launch_window(DeviceInfo& dev, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                  const CUtensorMap& to, const attn::FwdParams& p, int grid, cudaStream_t stream) {
+    bool& attr = dev.smem_attr_set[D == 128][ATTN_MASK_CAUSAL][BF16 ? 1 : 0][3];
+    return attn::launch_fwd<D, true, false, BF16, false, false, true>(attr, tq, tk, tv, to, p, grid, stream);
+}
+
 template <bool BF16, bool ROPE, bool PACK>
 int launch_any(DeviceInfo& dev, int D, int mask_kind, const CUtensorMap& tq, const CUtensorMap& tk,
                const CUtensorMap& tv, const CUtensorMap& to, const attn::FwdParams& p, int grid,
@@ -384,6 +391,12 @@ struct RopeArgs {
     void* k_rot;          // receives the rotated keys, or null: k already holds rotated keys
 };
 
+// Sliding window of attn_fwd_window / attn_fwd_window_f16.
+struct WindowArgs {
+    int window;           // keys a query sees, its own included
+    int sinks;            // first tokens that stay visible
+};
+
 bool rope_args_ok(const RopeArgs& r, int Sq, int Sk) {
     if (!r.table || !aligned(r.table, 16) || r.max_pos <= 0) return false;
     if (r.q_pos0 < 0 || (long long)r.q_pos0 + Sq > r.max_pos) return false;
@@ -421,7 +434,7 @@ int launch_rope_apply(const void* x, void* y, int B, int S, int H, int D, const 
 // the workspace, which depends on the entry point). Nothing is enqueued.
 int check_fwd_args(const void* q, const void* k, const void* v, const void* o, const float* lse, int B, int Hq,
                    int Hkv, int Sq, int Sk, int D, int mask_kind, const float* mask, int num_splits,
-                   const RopeArgs* rope) {
+                   const RopeArgs* rope, bool windowed = false) {
     if (B < 0 || Hq < 0 || Hkv <= 0 || Sq < 0 || Sk < 0 || D <= 0) return ATTN_ERR_INVALID_ARG;
     if (mask_kind < ATTN_MASK_NONE || mask_kind > ATTN_MASK_CAUSAL_ADDITIVE) return ATTN_ERR_INVALID_ARG;
     const bool additive = mask_kind == ATTN_MASK_ADDITIVE || mask_kind == ATTN_MASK_CAUSAL_ADDITIVE;
@@ -438,12 +451,13 @@ int check_fwd_args(const void* q, const void* k, const void* v, const void* o, c
     if (Sq > (1 << 30) || Sk > (1 << 30)) return ATTN_ERR_INVALID_ARG;
     if (rope && !rope_args_ok(*rope, Sq, Sk)) return ATTN_ERR_INVALID_ARG;
     if (num_splits < 0) return ATTN_ERR_INVALID_ARG;
-    const int pack_shift = pack_shift_for(Hq, Hkv, Sq, rope != nullptr);
+    const bool unpacked = rope != nullptr || windowed;
+    const int pack_shift = pack_shift_for(Hq, Hkv, Sq, unpacked);
     const long long tile_heads = pack_shift ? Hkv : Hq;
     const long long rows_per_tile = attn::kRowsPerTile >> pack_shift;
     const long long n_mblk = ((long long)Sq + rows_per_tile - 1) / rows_per_tile;
     int split_blocks = 1;
-    const int splits = resolve_splits(B, Hq, Hkv, Sq, Sk, num_splits, rope != nullptr, &split_blocks);
+    const int splits = resolve_splits(B, Hq, Hkv, Sq, Sk, num_splits, unpacked, &split_blocks);
     if ((long long)B * tile_heads * n_mblk * splits > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
     return ATTN_OK;
 }
@@ -451,17 +465,19 @@ int check_fwd_args(const void* q, const void* k, const void* v, const void* o, c
 int attn_fwd_impl(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv,
                   int Sq, int Sk, int D, float scale, int mask_kind, const float* mask, cudaStream_t stream,
                   bool bf16, int num_splits = 1, void* workspace = nullptr, size_t workspace_bytes = 0,
-                  const RopeArgs* rope = nullptr, long long q_stride = 0, long long kv_stride = 0) {
+                  const RopeArgs* rope = nullptr, long long q_stride = 0, long long kv_stride = 0,
+                  const WindowArgs* win = nullptr) {
     // ---- arguments (host only, nothing enqueued yet)
-    int rc = check_fwd_args(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, mask_kind, mask, num_splits, rope);
+    int rc = check_fwd_args(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, mask_kind, mask, num_splits, rope, win != nullptr);
     if (rc != ATTN_OK) return rc;
+    const bool unpacked = rope != nullptr || win != nullptr;
     const bool additive = mask_kind == ATTN_MASK_ADDITIVE || mask_kind == ATTN_MASK_CAUSAL_ADDITIVE;
-    const int pack_shift = pack_shift_for(Hq, Hkv, Sq, rope != nullptr);
+    const int pack_shift = pack_shift_for(Hq, Hkv, Sq, unpacked);
     const long long tile_heads = pack_shift ? Hkv : Hq;
     const long long rows_per_tile = attn::kRowsPerTile >> pack_shift;
     const long long n_mblk = ((long long)Sq + rows_per_tile - 1) / rows_per_tile;
     int split_blocks = 1;
-    const int splits = resolve_splits(B, Hq, Hkv, Sq, Sk, num_splits, rope != nullptr, &split_blocks);
+    const int splits = resolve_splits(B, Hq, Hkv, Sq, Sk, num_splits, unpacked, &split_blocks);
     if (B == 0 || Hq == 0 || Sq == 0) return ATTN_OK;        // nothing to compute
     size_t lse_off = 0;
     if (splits > 1) {
@@ -528,13 +544,22 @@ int attn_fwd_impl(const void* q, const void* k, const void* v, void* o, float* l
     p.status = dev->status;
     p.rope = rope ? rope->table : nullptr;
     p.q_pos0 = rope ? rope->q_pos0 : 0;
+    if (win) {
+        p.q_pos0 = win->window;
+        p.mask_vec4 = win->sinks;
+    }
 
     // One CTA per work tile. At most one CTA fits on an SM; the running CTAs
     // take over the tiles of CTAs that have not started yet (cluster launch
     // control), so the grid behaves as a persistent one with a dynamic,
     // longest-first schedule.
     const int grid = p.n_tiles;
-    if (rope)
+    if (win)
+        rc = D == 128 ? (bf16 ? launch_window<128, true>(*dev, tq, tk, tv, to, p, grid, stream)
+                              : launch_window<128, false>(*dev, tq, tk, tv, to, p, grid, stream))
+                      : (bf16 ? launch_window<64, true>(*dev, tq, tk, tv, to, p, grid, stream)
+                              : launch_window<64, false>(*dev, tq, tk, tv, to, p, grid, stream));
+    else if (rope)
         rc = bf16 ? launch_any<true, true, false>(*dev, D, mask_kind, tq, tk, tv, to, p, grid, stream)
                   : launch_any<false, true, false>(*dev, D, mask_kind, tq, tk, tv, to, p, grid, stream);
     else if (pack_shift)
@@ -620,6 +645,36 @@ int attn_fwd_rope_f16(const void* q, const void* k, const void* v, void* o, floa
     const RopeArgs r{rope_table, max_pos, q_pos0, k_pos0, k_rot};
     return attn_fwd_impl(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, scale, mask_kind, mask,
                          reinterpret_cast<cudaStream_t>(stream), false, num_splits, workspace, workspace_bytes, &r);
+}
+
+}  // extern "C"
+
+namespace {
+
+int window_impl(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int Sq, int Sk,
+                int D, float scale, int window, int sinks, cudaStream_t stream, bool bf16) {
+    if (window <= 0 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+    // A window or sinks that reach every key hide none: the plain causal kernel.
+    const WindowArgs w{window, sinks};
+    const bool hides = window < Sk && sinks < Sk;
+    return attn_fwd_impl(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, scale, ATTN_MASK_CAUSAL, nullptr, stream, bf16, 1, nullptr,
+                         0, nullptr, 0, 0, hides ? &w : nullptr);
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int Sq,
+                    int Sk, int D, float scale, int window, int sinks, attn_stream_t stream) {
+    return window_impl(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, scale, window, sinks,
+                       reinterpret_cast<cudaStream_t>(stream), true);
+}
+
+int attn_fwd_window_f16(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int Sq,
+                        int Sk, int D, float scale, int window, int sinks, attn_stream_t stream) {
+    return window_impl(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, scale, window, sinks,
+                       reinterpret_cast<cudaStream_t>(stream), false);
 }
 
 int attn_rope_table(float* table, int max_pos, int D, double base, attn_stream_t stream) {

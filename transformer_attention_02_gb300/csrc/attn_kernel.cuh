@@ -63,13 +63,14 @@ struct FwdParams {
     float* o_part;            // split keys: FP32 O of each key range (n_splits, B, Hq, Sq, D), else null
     float* lse_part;          // split keys: FP32 LSE of each key range (n_splits, B, Hq, Sq)
     float scale_log2;         // scale * log2(e)
-    int mask_vec4;            // mask rows may be read with 32-byte (2) or 16-byte (1) loads, else 0
+    int mask_vec4;            // mask rows may be read with 32-byte (2) or 16-byte (1) loads, else 0;
+                              // windowed variants: tokens that stay visible (sinks)
     int flags;                // kFlagOVec8 | kFlagDebugStall
     int head_group;           // tile order: (b, head) slices per group (see tile_info)
     unsigned long long timeout_ns;
     unsigned int* status;     // device status word, bit 0 = a wait timed out
     const float* rope;        // rotary table (max_pos, D/2, {cos, sin}) FP32 (rotating variant only)
-    int q_pos0;               // position of query row 0 (rotating variant only)
+    int q_pos0;               // position of query row 0 (rotating variant); window length (windowed variants)
     // Kept last: inserting it earlier shifted the 64-bit fields after it and
     // measurably changed the code generated for the unpacked kernels.
     int pack_shift;           // > 0: the 2^pack_shift query heads of a K/V head share each tile's rows
@@ -162,8 +163,8 @@ struct TileCfg {
 
 struct TileInfo {
     int b, h, hk, m0;  // h: the (first) query head; m0: the first query row
-    int split;      // key range index
-    int kb0;        // first 128-key block of the key range
+    int split;      // key range index; windowed variants: key blocks before the gap
+    int kb0;        // first 128-key block of the key range; windowed variants: blocks in the gap
     int nb[2];      // KV blocks needed by query sub-tile t (rows m0+128t .. m0+128t+127)
     int n;          // max(nb[0], nb[1]): KV blocks streamed for the tile
 };
@@ -184,7 +185,13 @@ struct TileInfo {
 // all 2^pack_shift query heads of the group (row r of the sub-tile is query
 // row r >> pack_shift of head h + (r & (group - 1))), so the group's heads
 // share every K/V block instead of streaming it once each.
-template <bool CAUSAL, bool PACK>
+// Windowed variants (row at position i sees key j iff i - window < j <= i or
+// j < sinks): a tile streams the blocks of the sinks, then, past a gap, those
+// from the oldest key of its first row's window to its last row's own key.
+// Both sub-tiles walk the same list, so the upper one's first block of the
+// window may be hidden from it altogether (its rows' windows begin 128 keys
+// later): one block in window / 128 + 2.
+template <bool CAUSAL, bool PACK, bool WINDOW = false>
 __device__ __forceinline__ TileInfo tile_info(int tile, const FwdParams& p) {
     const int ps = PACK ? p.pack_shift : 0;
     const int heads = PACK ? p.Hkv : p.Hq;
@@ -222,6 +229,15 @@ __device__ __forceinline__ TileInfo tile_info(int tile, const FwdParams& p) {
     t.m0 = mb * 2 * sub_rows;
     t.split = split;
     t.kb0 = split * p.split_blocks;
+    int gap = 0;
+    if (WINDOW) {
+        const int low = max(0, t.m0 + (p.Sk - p.Sq) - p.q_pos0 + 1) / kBlockN;
+        const int sink_blocks = (min(p.mask_vec4, p.Sk) + kBlockN - 1) / kBlockN;
+        if (low > sink_blocks) {
+            t.split = sink_blocks;
+            gap = low - sink_blocks;
+        }
+    }
     const int range_begin = t.kb0 * kBlockN;
     const int range_end = min(p.Sk, range_begin + p.split_blocks * kBlockN);
 #pragma unroll
@@ -230,10 +246,17 @@ __device__ __forceinline__ TileInfo tile_info(int tile, const FwdParams& p) {
         const int last = min(first + sub_rows - 1, p.Sq - 1);
         int kv_end = range_begin;
         if (first < p.Sq) kv_end = CAUSAL ? min(range_end, max(0, last + (p.Sk - p.Sq) + 1)) : range_end;
-        t.nb[s] = kv_end > range_begin ? (kv_end - range_begin + kBlockN - 1) / kBlockN : 0;
+        t.nb[s] = kv_end > range_begin ? (kv_end - range_begin + kBlockN - 1) / kBlockN - gap : 0;
     }
+    if (WINDOW) t.kb0 = gap;
     t.n = max(t.nb[0], t.nb[1]);
     return t;
+}
+
+// Key block of the j-th block a tile streams.
+template <bool WINDOW>
+__device__ __forceinline__ int key_block(const TileInfo& t, int j) {
+    return WINDOW ? (j < t.split ? j : j + t.kb0) : t.kb0 + j;
 }
 
 struct SyncCtx {
@@ -325,7 +348,7 @@ __device__ __forceinline__ bool fetch_tile_warp(uint32_t full_bar, uint32_t empt
 // warp-uniform); lane 0 issues the copies. The K/V tiles enter the ring in the
 // order the MMA issuer takes them: K_0, then per block V_j and K_{j+1}. The
 // work tiles come from the tile ring.
-template <int D>
+template <int D, bool WINDOW>
 __device__ void role_tma(const CUtensorMap* tmK, const CUtensorMap* tmV, uint32_t smem, const uint8_t* smem_ptr,
                          const SyncCtx& sc) {
     using C = TileCfg<D>;
@@ -342,7 +365,7 @@ __device__ void role_tma(const CUtensorMap* tmK, const CUtensorMap* tmV, uint32_
             ptx::mbar_arrive_expect_tx(bar(C::bKVFull + slot), C::kTileBytes);
             for (int c = 0; c < C::kBoxes; ++c)
                 ptx::tma_load_4d(smem + C::kKVOff + slot * C::kTileBytes + c * C::kBoxBytes, map,
-                                 bar(C::bKVFull + slot), c * C::kBoxCols, t.hk, (t.kb0 + blk) * kBlockN, t.b);
+                                 bar(C::bKVFull + slot), c * C::kBoxCols, t.hk, key_block<WINDOW>(t, blk) * kBlockN, t.b);
         }
         ++kv_fill;
         return true;
@@ -498,7 +521,7 @@ __device__ void role_rope_q(const FwdParams& p, uint32_t smem, uint8_t* smem_ptr
 // tile's upper one is done, and its upper sub-tile while the current tile's
 // last key block runs. (In the rotary variant warps 12-15 rotate each
 // sub-tile after it lands.)
-template <int D, bool CAUSAL, bool ADDITIVE, bool BF16, bool ROPE, bool PACK>
+template <int D, bool CAUSAL, bool ADDITIVE, bool BF16, bool ROPE, bool PACK, bool WINDOW>
 __device__ void role_qload(const CUtensorMap* tmQ, const CUtensorMap* tmO, const FwdParams& p, uint32_t smem,
                            uint8_t* smem_ptr, const SyncCtx& sc) {
     using C = TileCfg<D>;
@@ -550,7 +573,7 @@ __device__ void role_qload(const CUtensorMap* tmQ, const CUtensorMap* tmO, const
         int tile = 0;
         const int found = next_tile_index(tile);
         if (found < 0) return -1;
-        if (found) t = tile_info<CAUSAL, PACK>(tile, p);
+        if (found) t = tile_info<CAUSAL, PACK, WINDOW>(tile, p);
         if (!found) {
             t.b = t.h = t.hk = t.m0 = t.split = t.kb0 = 0;
             t.nb[0] = t.nb[1] = t.n = -1;
@@ -802,7 +825,7 @@ __device__ void role_mma(const FwdParams& p, uint32_t smem, const uint8_t* smem_
 }
 
 // ------------------------------------------------ softmax / epilogue warpgroup
-template <int D, bool CAUSAL, bool ADDITIVE, bool BF16, bool PACK>
+template <int D, bool CAUSAL, bool ADDITIVE, bool BF16, bool PACK, bool WINDOW>
 __device__ void role_softmax(const FwdParams& p, uint32_t smem, uint8_t* smem_ptr, uint32_t tmem, int wg,
                              const SyncCtx& sc) {
     using C = TileCfg<D>;
@@ -874,7 +897,7 @@ __device__ void role_softmax(const FwdParams& p, uint32_t smem, uint8_t* smem_pt
             // Each warp waits on its own; the warpgroup agrees on whether to go
             // on at the one named barrier of the block (before the hand-off of
             // P), where a warp whose wait ran out votes to stop.
-            const int key0 = (ti.kb0 + j) * kBlockN;
+            const int key0 = key_block<WINDOW>(ti, j) * kBlockN;
             // x: raw scores, or (additive mask) logits in log2 units
             float x[kBlockN];
             if (ADDITIVE) {
@@ -932,6 +955,15 @@ __device__ void role_softmax(const FwdParams& p, uint32_t smem, uint8_t* smem_pt
 #pragma unroll
                     for (int c = 0; c < kBlockN; ++c)
                         if (c >= vis) x[c] = -INFINITY;
+                }
+                if (WINDOW) {
+                    // keys before the row's window are hidden, but for the sinks
+                    const int low = row + (p.Sk - p.Sq) - p.q_pos0 + 1 - key0, sink = p.mask_vec4 - key0;
+                    if (low > 0 && sink < kBlockN) {
+#pragma unroll
+                        for (int c = 0; c < kBlockN; ++c)
+                            if (c < low && c >= sink) x[c] = -INFINITY;
+                    }
                 }
                 float mA = fmaxf(x[0], x[1]), mB = fmaxf(x[2], x[3]);
                 float mC = fmaxf(x[4], x[5]), mD = fmaxf(x[6], x[7]);
@@ -1077,12 +1109,13 @@ __device__ void role_softmax(const FwdParams& p, uint32_t smem, uint8_t* smem_pt
 }
 
 // ------------------------------------------------------------------ kernel
-template <int D, bool CAUSAL, bool ADDITIVE, bool BF16, bool ROPE, bool PACK>
+template <int D, bool CAUSAL, bool ADDITIVE, bool BF16, bool ROPE, bool PACK, bool WINDOW = false>
 __global__ void __launch_bounds__(kernel_threads(ROPE), 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                     const FwdParams p) {
     using C = TileCfg<D>;
+    static_assert(!WINDOW || (CAUSAL && !ADDITIVE && !ROPE && !PACK), "the window reuses fields of the other variants");
     extern __shared__ uint8_t smem_raw[];
     // Swizzled TMA tiles and the MMA descriptors both assume 1024-byte alignment.
     const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -1122,15 +1155,15 @@ __global__ void __launch_bounds__(kernel_threads(ROPE), 1)
 
     if (warp < 8) {
         ptx::setmaxnreg_inc<softmax_regs(ROPE)>();
-        role_softmax<D, CAUSAL, ADDITIVE, BF16, PACK>(p, smem, smem_ptr, tmem, warp >> 2, sc);
+        role_softmax<D, CAUSAL, ADDITIVE, BF16, PACK, WINDOW>(p, smem, smem_ptr, tmem, warp >> 2, sc);
     } else if (warp < kRotateWarp0) {
         ptx::setmaxnreg_dec<control_regs(ROPE)>();
         if (warp == kMmaWarp)
             role_mma<D, BF16, ROPE>(p, smem, smem_ptr, tmem, sc);
         else if (warp == kTmaWarp)
-            role_tma<D>(&tmK, &tmV, smem, smem_ptr, sc);
+            role_tma<D, WINDOW>(&tmK, &tmV, smem, smem_ptr, sc);
         else if (warp == kQWarp)
-            role_qload<D, CAUSAL, ADDITIVE, BF16, ROPE, PACK>(&tmQ, &tmO, p, smem, smem_ptr, sc);
+            role_qload<D, CAUSAL, ADDITIVE, BF16, ROPE, PACK, WINDOW>(&tmQ, &tmO, p, smem, smem_ptr, sc);
         __syncwarp();
     } else {
         ptx::setmaxnreg_dec<kRotateRegs>();
