@@ -86,11 +86,11 @@ int kv_append_impl(const void* k, const void* v, long long k_stride, long long v
     return paged::launch_append(p, e4m3 ? paged::kE4m3 : bf16 ? paged::kBf16 : paged::kF16, dev.num_sms, stream);
 }
 
-// Workspace of the attention: the first unit of every sequence, then two FP32
+// Workspace of the attention: the place of every sequence in the schedule, then two FP32
 // parts (unnormalised O, maximum, sum) for each CTA. Independent of the lengths.
 size_t attend_workspace(int B, int rows, int D, int sms, size_t* part_off) {
     const int rb = paged::block_rows(rows);
-    *part_off = align_up((size_t)(B + 1) * sizeof(int));
+    *part_off = align_up((size_t)(B + 2) * sizeof(int));
     return *part_off + (size_t)sms * paged::resident_ctas(D, rb) * 2 * rb * (D + 2) * sizeof(float);
 }
 
@@ -116,7 +116,8 @@ int attend_impl(const void* q, long long q_stride, const void* k_cache, const vo
     if (rows > (1 << 30)) return ATTN_ERR_INVALID_ARG;
     const int rb = paged::block_rows((int)rows);
     const long long row_blocks = (rows + rb - 1) / rb;
-    const long long units = ((long long)max_pages * page + paged::kUnit - 1) / paged::kUnit + 1;
+    // (a segment's units, one more for the sinks, and its lead in the schedule)
+    const long long units = ((long long)max_pages * page + paged::kUnit - 1) / paged::kUnit + 4;
     if ((long long)B * Hkv * row_blocks > 0x7fffffffLL / units) return ATTN_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, kWorkspaceAlign)) return ATTN_ERR_INVALID_ARG;
     size_t part_off = 0;

@@ -69,7 +69,7 @@ struct Cfg {
     static constexpr int kQOff = kStatOff + kWarps * kRows * 8;
     static constexpr int kFragOff = kQOff + kRows * kQStride;
     static constexpr int kShareOff = kFragOff + (kQShared ? kRows * D * 2 : 0);   // [warp]{copies', products'}
-    static constexpr int kSmemBytes = kShareOff + kWarps * 2 * 64;
+    static constexpr int kSmemBytes = kShareOff + kWarps * 2 * 80;
     static_assert(8 * D * 4 <= kStageBytes, "a warp merges eight rows at a time through one stage of its ring");
     static_assert(kUnit % kKeys == 0, "a stage lies inside one unit");
     static_assert(kQOff % 16 == 0 && kFragOff % 16 == 0, "16-byte accesses");
@@ -199,11 +199,18 @@ __device__ __forceinline__ KeyList key_list(const AttendParams& p, int b, bool& 
     return l;
 }
 
-// CTAs that work on `total` units: no more than there are units, so that every
-// CTA between a segment's first and last one holds a part of it.
+// The schedule. Every non-empty segment counts its units and, where the CTAs
+// have several units each, kLead more for what a CTA pays to begin a segment
+// (its queries, the merge of the one before); CTA c takes the positions
+// [total c / ctas, total (c + 1) / ctas) of all segments end to end. With few
+// units there is no lead and no more CTAs than units. Either way every CTA
+// between a segment's first and last one holds a part of it.
+constexpr int kLead = 2;
+__device__ __forceinline__ int lead_of(const AttendParams& p, int units) { return units >= 8 * p.ctas ? kLead : 0; }
+__device__ __forceinline__ int span_of(int units, int lead) { return units > 0 ? units + lead : 0; }
 __device__ __forceinline__ int working_ctas(const AttendParams& p, int total) { return min(p.ctas, total); }
 __device__ __forceinline__ int unit_start(int total, int ctas, int cta) { return (int)((long long)total * cta / ctas); }
-// The CTA whose range holds unit x.
+// The CTA whose range holds position x.
 __device__ __forceinline__ int unit_owner(int total, int ctas, int x) {
     return (int)((((long long)x + 1) * ctas + total - 1) / total) - 1;
 }
@@ -214,24 +221,36 @@ struct Share {
     int b, base;         // the sequence and the first unit of its segments
     KeyList list;
     int hk, rb, u0, u1;
+    int next;            // position after the share
     int pos_lo, pos_hi;  // positions of the row block's first and last query
     int kv_end;          // keys at or past it are hidden from every row
     int w_lo;            // keys before it are hidden too, but for the sinks
 };
 
-static_assert(sizeof(Share) <= 64, "the size the shared-memory layout gives it");
+static_assert(sizeof(Share) <= 80, "the size the shared-memory layout gives it");
 
-// The share at unit x < x_end, searching onwards from s.b (whose list is s.list).
+// The first share with a unit in positions [x, x_end), searching onwards from
+// s.b (whose list is s.list); false if there is none.
 template <int ROWS>
-__device__ __forceinline__ void locate(const AttendParams& p, int segs, int x, int x_end, Share& s) {
+__device__ __forceinline__ bool locate(const AttendParams& p, int segs, int lead, int x, int x_end, Share& s) {
     bool bad;
-    while (x >= s.base + s.list.units * segs) {                   // the sequence is done, or empty
-        s.base += s.list.units * segs;
-        s.list = key_list(p, ++s.b, bad);
+    int seg;
+    for (;;) {
+        if (x >= x_end) return false;
+        const int span = span_of(s.list.units, lead);
+        if (x >= s.base + span * segs) {                          // the sequence is done, or empty
+            s.base += span * segs;
+            s.list = key_list(p, ++s.b, bad);
+            continue;
+        }
+        seg = (x - s.base) / span;
+        const int off = x - s.base - seg * span;
+        s.u0 = max(0, off - lead);
+        s.u1 = min(s.list.units, off + x_end - x - lead);
+        s.next = min(x_end, s.base + (seg + 1) * span);
+        if (s.u1 > s.u0) break;
+        x = s.next;
     }
-    const int seg = (x - s.base) / s.list.units;
-    s.u0 = x - s.base - seg * s.list.units;
-    s.u1 = min(s.list.units, s.u0 + x_end - x);
     s.hk = seg / p.row_blocks;
     s.rb = seg - s.hk * p.row_blocks;
     const int r0 = s.rb * ROWS;
@@ -240,6 +259,7 @@ __device__ __forceinline__ void locate(const AttendParams& p, int segs, int x, i
     s.pos_hi = s.list.kv - s.list.ql + i1;
     s.kv_end = i0 < s.list.ql ? max(0, s.pos_hi + 1) : 0;
     s.w_lo = p.window > 0 ? s.pos_lo - p.window + 1 : 0;
+    return true;
 }
 
 template <int D, int CT, int NT>
@@ -250,7 +270,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     constexpr int kSteps = D / 16;                                // products of 16 dims
     constexpr bool kBf = CT == kBf16;                             // operand type of the products
     extern __shared__ __align__(1024) uint8_t smem_raw[];          // the XOR of chunk offsets needs 256-byte stages
-    __shared__ int s_scan[C::kWarps];
+    __shared__ int2 s_scan[C::kWarps];
     __shared__ Share s_begin;                                     // (b, base, list) where the CTA's range begins
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -263,35 +283,47 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     uint8_t* const q_sh = smem_raw + C::kQOff;
     uint2* const frag_sh = reinterpret_cast<uint2*>(smem_raw + C::kFragOff);
 
+    // The page numbers come into L2 while the lengths are on their way (a line a
+    // thread; a table past that is fetched as it is needed).
+    {
+        const long long line = (long long)blockIdx.x * kThreads + tid;
+        if (line * 32 < (long long)p.B * p.max_pages) prefetch_l2(p.block_table + line * 32);
+    }
     // ---- where this CTA's range begins: a scan over the sequences' units
     const int segs = p.Hkv * p.row_blocks;                        // segments of a sequence
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
     KeyList list{};
-    int mine = 0;
+    int mine = 0, mine_n = 0;                                     // units, and sequences with any
     for (int b = b_lo; b < b_hi; ++b) {
         bool bad;
         list = key_list(p, b, bad);
-        mine += list.units * segs;
+        mine += list.units;
+        mine_n += list.units > 0;
         if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
     }
-    int incl = mine;
+    int incl = mine, incl_n = mine_n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        const int v = __shfl_up_sync(0xffffffffu, incl, o), n = __shfl_up_sync(0xffffffffu, incl_n, o);
+        if (lane >= o) incl += v, incl_n += n;
     }
-    if (lane == 31) s_scan[warp] = incl;
+    if (lane == 31) s_scan[warp] = make_int2(incl, incl_n);
     __syncthreads();
-    int before = incl - mine, total = 0;
+    int before = incl - mine, before_n = incl_n - mine_n, total = 0, total_n = 0;
 #pragma unroll
     for (int w = 0; w < C::kWarps; ++w) {
-        if (w < warp) before += s_scan[w];
-        total += s_scan[w];
+        const int2 v = s_scan[w];
+        if (w < warp) before += v.x, before_n += v.y;
+        total += v.x, total_n += v.y;
     }
+    const int lead = lead_of(p, total * segs);
+    before = (before + before_n * lead) * segs;
+    mine = (mine + mine_n * lead) * segs;
+    total = (total + total_n * lead) * segs;
     const int ctas = working_ctas(p, total);
     const bool works = (int)blockIdx.x < ctas;
-    int x = works ? unit_start(total, ctas, blockIdx.x) : total;
+    const int x = works ? unit_start(total, ctas, blockIdx.x) : total;
     const int x_end = works ? unit_start(total, ctas, blockIdx.x + 1) : total;
     const bool note = blockIdx.x == 0 && p.B > kScanInMerge;      // the merge reads the offsets of a large batch
     if (note || (before <= x && x < before + mine)) {
@@ -299,7 +331,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
         for (int b = b_lo; b < b_hi; ++b) {
             bool bad;
             if (per > 1) list = key_list(p, b, bad);
-            const int n = list.units * segs;
+            const int n = span_of(list.units, lead) * segs;
             if (note) p.base[b] = at;
             if (at <= x && x < at + n) {
                 s_begin.b = b;
@@ -308,7 +340,10 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
             }
             at += n;
         }
-        if (note && b_hi == p.B && b_lo < b_hi) p.base[p.B] = at;
+        if (note && b_hi == p.B && b_lo < b_hi) {
+            p.base[p.B] = at;
+            p.base[p.B + 1] = lead;
+        }
     }
     __syncthreads();
     if (x >= x_end) return;
@@ -343,6 +378,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     if (lane == 0) ld = s_begin;
     __syncwarp();
     int ld_x = x, ld_i = 0, ld_n = 0, ld_stage = 0;
+    bool ld_more = false;
     int ids = 0;                                                  // page numbers of 32 / kTiles stages, one tile a lane
     constexpr int kBatch = 32 / C::kTiles;
     auto stages_of = [](int units) { return (units * kUnit + C::kWarps * C::kKeys - 1) / (C::kWarps * C::kKeys); };
@@ -353,7 +389,8 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     };
     auto enter = [&]() {                                          // the share at ld_x
         Share s = ld;
-        locate<C::kRows>(p, segs, ld_x, x_end, s);
+        ld_more = locate<C::kRows>(p, segs, lead, ld_x, x_end, s);
+        if (!ld_more) return;
         __syncwarp();
         if (lane == 0) ld = s;
         __syncwarp();
@@ -377,8 +414,9 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
         }
     };
     enter();
+    if (!ld_more) return;                                         // nothing but leads in its range
     auto issue = [&]() {
-        if (ld_x < x_end) {
+        if (ld_more) {
             if (ld_i % kBatch == 0) {
                 const int key = key_at(((ld_i + lane / C::kTiles) * C::kWarps + warp) * C::kKeys + lane % C::kTiles * 16);
                 ids = key < ld.kv_end ? __ldg(p.block_table + (size_t)ld.b * p.max_pages + (key >> p.page_shift)) : -1;
@@ -420,8 +458,8 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                     cp_async4(scales_a + ((ld_stage * C::kTiles + m) * 2 + lane) * 4, (lane ? p.v_scale : p.k_scale) + block);
             }
             if (++ld_i == ld_n) {
-                ld_x += ld.u1 - ld.u0;
-                if (ld_x < x_end) enter();
+                ld_x = ld.next;
+                enter();
             }
         }
         cp_async_commit();
@@ -429,6 +467,54 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     };
     if (lane == 0) cur = ld;
     __syncwarp();
+
+    // ---- queries: fetched (a 16-byte piece and its angles, kQItems a thread)
+    // before the previous rows are merged, then rotated, rounded to their 16-bit
+    // type and put into shared memory.
+    constexpr int kQItems = (C::kRows * (D / 8) + kThreads - 1) / kThreads;
+    const bool bf = CT == kE4m3 ? p.q_bf16 : kBf;
+    uint4 q_raw[kQItems];
+    float4 q_turn[kQItems][2];
+    auto fetch_q = [&](const Share& s) {
+#pragma unroll
+        for (int j = 0; j < kQItems; ++j) {
+            const int w = tid + j * kThreads, r = w / (D / 8), d = (w - r * (D / 8)) * 8;
+            const int row = s.rb * C::kRows + r, i = row / p.group;
+            q_raw[j] = make_uint4(0u, 0u, 0u, 0u);
+            q_turn[j][0] = q_turn[j][1] = make_float4(1.f, 0.f, 1.f, 0.f);
+            if (r < C::kRows && row < p.rows && i < s.list.ql) {
+                q_raw[j] = *reinterpret_cast<const uint4*>(p.q + ((long long)s.b * p.Sq + i) * p.q_stride +
+                                                           (long long)(s.hk * p.group + (row - i * p.group)) * D + d);
+                if (p.rope) {
+                    int pos = s.list.kv - s.list.ql + i;
+                    if (pos >= p.max_pos) {
+                        if (d == 0) atomicOr(p.status, kStatusBadIndex);
+                        pos = p.max_pos - 1;
+                    }
+                    const float4* at = reinterpret_cast<const float4*>(p.rope) + (size_t)max(pos, 0) * (D / 4) + d / 4;
+                    q_turn[j][0] = __ldg(at);
+                    q_turn[j][1] = __ldg(at + 1);
+                }
+            }
+        }
+    };
+    auto store_q = [&]() {
+#pragma unroll
+        for (int j = 0; j < kQItems; ++j) {
+            const int w = tid + j * kThreads, r = w / (D / 8), d = (w - r * (D / 8)) * 8;
+            uint32_t v[4] = {q_raw[j].x, q_raw[j].y, q_raw[j].z, q_raw[j].w};
+            if (p.rope) {
+                const float4 a = q_turn[j][0], c = q_turn[j][1];
+                v[0] = bf ? rotate_pair<true>(v[0], a.x, a.y) : rotate_pair<false>(v[0], a.x, a.y);
+                v[1] = bf ? rotate_pair<true>(v[1], a.z, a.w) : rotate_pair<false>(v[1], a.z, a.w);
+                v[2] = bf ? rotate_pair<true>(v[2], c.x, c.y) : rotate_pair<false>(v[2], c.x, c.y);
+                v[3] = bf ? rotate_pair<true>(v[3], c.z, c.w) : rotate_pair<false>(v[3], c.z, c.w);
+            }
+            if (r < C::kRows)
+                *reinterpret_cast<uint4*>(q_sh + r * C::kQStride + d * 2) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    };
+    fetch_q(cur);
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) issue();
 
@@ -437,36 +523,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     for (;;) {
         const int r0 = cur.rb * C::kRows, pos0 = cur.list.kv - cur.list.ql;
         const int pos_lo = cur.pos_lo, pos_hi = cur.pos_hi;
-        // ---- queries, rotated and rounded to their 16-bit type, in shared memory
-        const bool bf = CT == kE4m3 ? p.q_bf16 : kBf;
-        for (int w = tid; w < C::kRows * (D / 8); w += kThreads) {
-            const int r = w / (D / 8), d = (w - r * (D / 8)) * 8;
-            const int row = r0 + r, i = row / p.group;
-            uint32_t v[4] = {0u, 0u, 0u, 0u};
-            if (row < p.rows && i < cur.list.ql) {
-                const uint4 raw = *reinterpret_cast<const uint4*>(
-                    p.q + ((long long)cur.b * p.Sq + i) * p.q_stride +
-                    (long long)(cur.hk * p.group + (row - i * p.group)) * D + d);
-                v[0] = raw.x;
-                v[1] = raw.y;
-                v[2] = raw.z;
-                v[3] = raw.w;
-                if (p.rope) {
-                    int pos = pos0 + i;
-                    if (pos >= p.max_pos) {
-                        if (d == 0) atomicOr(p.status, kStatusBadIndex);
-                        pos = p.max_pos - 1;
-                    }
-                    const float4* at = reinterpret_cast<const float4*>(p.rope) + (size_t)max(pos, 0) * (D / 4) + d / 4;
-                    const float4 a = __ldg(at), c = __ldg(at + 1);
-                    v[0] = bf ? rotate_pair<true>(v[0], a.x, a.y) : rotate_pair<false>(v[0], a.x, a.y);
-                    v[1] = bf ? rotate_pair<true>(v[1], a.z, a.w) : rotate_pair<false>(v[1], a.z, a.w);
-                    v[2] = bf ? rotate_pair<true>(v[2], c.x, c.y) : rotate_pair<false>(v[2], c.x, c.y);
-                    v[3] = bf ? rotate_pair<true>(v[3], c.z, c.w) : rotate_pair<false>(v[3], c.z, c.w);
-                }
-            }
-            *reinterpret_cast<uint4*>(q_sh + r * C::kQStride + d * 2) = make_uint4(v[0], v[1], v[2], v[3]);
-        }
+        store_q();
         __syncthreads();
         // B fragments. With an 8-bit cache the queries become f16 values, each
         // row scaled by a power of two to lie in [-2, 2]: exact down to 2^-24 of
@@ -698,13 +755,23 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
             st = st + 1 == C::kStages ? 0 : st + 1;
         }
 
+        // ---- the next share's queries set out
+        Share now = cur;
+        Share s = now;
+        const bool more = locate<C::kRows>(p, segs, lead, now.next, x_end, s);
+        if (more) {
+            __syncwarp();
+            if (lane == 0) cur = s;
+            __syncwarp();
+            if (NT == 1) fetch_q(s);
+        }
         // ---- merge the warps, eight rows at a time, through the stage that was
         // read last (the others hold the next segment's keys)
         __syncwarp();
         const int m_stage = st == 0 ? C::kStages - 1 : st - 1;
         float* const mine_o = reinterpret_cast<float*>(ring + m_stage * C::kStageBytes);
-        const bool full = cur.u0 == 0 && cur.u1 == cur.list.units;
-        float* slot = p.part + (size_t)(2 * blockIdx.x + (cur.u0 == 0 ? 1 : 0)) * C::kRows * (D + 2);
+        const bool full = now.u0 == 0 && now.u1 == now.list.units;
+        float* slot = p.part + (size_t)(2 * blockIdx.x + (now.u0 == 0 ? 1 : 0)) * C::kRows * (D + 2);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -746,15 +813,15 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                 }
                 if (full) {
                     const int row = r0 + col, i = row / p.group;
-                    if (row < p.rows && i < cur.list.ql) {
-                        const int h = cur.hk * p.group + (row - i * p.group);
+                    if (row < p.rows && i < now.list.ql) {
+                        const int h = now.hk * p.group + (row - i * p.group);
                         const float inv = sum != 0.f ? 1.f / sum : 0.f;       // 0: no key was visible
                         uint2 r;
                         r.x = bf ? ptx::pack_bf16x2(o.x * inv, o.y * inv) : ptx::pack_f16x2(o.x * inv, o.y * inv);
                         r.y = bf ? ptx::pack_bf16x2(o.z * inv, o.w * inv) : ptx::pack_f16x2(o.z * inv, o.w * inv);
-                        *reinterpret_cast<uint2*>(p.o + (((size_t)cur.b * p.Sq + i) * p.Hq + h) * D + d) = r;
+                        *reinterpret_cast<uint2*>(p.o + (((size_t)now.b * p.Sq + i) * p.Hq + h) * D + d) = r;
                         if (d == 0)
-                            p.lse[((size_t)cur.b * p.Hq + h) * p.Sq + i] =
+                            p.lse[((size_t)now.b * p.Hq + h) * p.Sq + i] =
                                 sum != 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
                     }
                 } else {
@@ -767,13 +834,8 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
             }
             __syncthreads();                                      // the stage is free again
         }
-        x += cur.u1 - cur.u0;
-        if (x >= x_end) break;
-        Share s = cur;
-        locate<C::kRows>(p, segs, x, x_end, s);
-        __syncwarp();
-        if (lane == 0) cur = s;
-        __syncwarp();
+        if (!more) break;
+        if (NT > 1) fetch_q(s);                                   // (earlier it would cost registers the sums need)
     }
     cp_async_wait<0>();
 }
@@ -783,50 +845,51 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
 template <int D, int RB>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const AttendParams p, bool bf16) {
     constexpr int kPer = D / 32;
-    __shared__ int s_scan[8], s_mine[2];
+    __shared__ int2 s_scan[8], s_mine;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int segs = p.Hkv * p.row_blocks;
     const int b = blockIdx.x / segs, seg = blockIdx.x - b * segs;
-    int total, first, units;
+    int total, first, units, lead;
     if (p.B <= kScanInMerge) {
         // The sequences' units, one a thread: lengths are the step's inputs, so
         // this needs nothing of the attention kernel and runs beside it.
         bool bad;
         const int mine = (int)threadIdx.x < p.B ? key_list(p, threadIdx.x, bad).units : 0;
-        int incl = mine;
+        int incl = mine, incl_n = mine > 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
+            const int v = __shfl_up_sync(0xffffffffu, incl, o), n = __shfl_up_sync(0xffffffffu, incl_n, o);
+            if (lane >= o) incl += v, incl_n += n;
         }
-        if (lane == 31) s_scan[warp] = incl;
+        if (lane == 31) s_scan[warp] = make_int2(incl, incl_n);
         __syncthreads();
+        int before = incl - mine, before_n = incl_n - (mine > 0), total_n = 0;
         total = 0;
-        int before = incl - mine;
         for (int w = 0; w < 8; ++w) {
-            if (w < warp) before += s_scan[w];
-            total += s_scan[w];
+            const int2 v = s_scan[w];
+            if (w < warp) before += v.x, before_n += v.y;
+            total += v.x, total_n += v.y;
         }
-        if ((int)threadIdx.x == b) {
-            s_mine[0] = before;
-            s_mine[1] = mine;
-        }
+        lead = lead_of(p, total * segs);
+        if ((int)threadIdx.x == b) s_mine = make_int2(before + before_n * lead, mine);
         __syncthreads();
-        total *= segs;
-        first = s_mine[0] * segs;
-        units = s_mine[1];
+        total = (total + total_n * lead) * segs;
+        first = s_mine.x * segs;
+        units = s_mine.y;
         asm volatile("griddepcontrol.wait;" ::: "memory");
     } else {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         total = p.base[p.B];
+        lead = p.base[p.B + 1];
         first = p.base[b];
-        units = (p.base[b + 1] - first) / segs;
+        const int span = (p.base[b + 1] - first) / segs;
+        units = span > 0 ? span - lead : 0;
     }
     int c0 = 0, c1 = 0;
     if (units > 0) {
-        const int ctas = working_ctas(p, total);
-        c0 = unit_owner(total, ctas, first + seg * units);
-        c1 = unit_owner(total, ctas, first + (seg + 1) * units - 1);
+        const int ctas = working_ctas(p, total), span = units + lead;
+        c0 = unit_owner(total, ctas, first + seg * span + lead);
+        c1 = unit_owner(total, ctas, first + (seg + 1) * span - 1);
         if (c0 == c1) return;
     }
     const int hk = seg / p.row_blocks, rb = seg - hk * p.row_blocks;

@@ -59,7 +59,7 @@ struct AttendParams {
     uint16_t* o;                  // (B, Sq, Hq, D)
     float* lse;                   // (B, Hq, Sq)
     float* part;                  // 2 slots per CTA of rows x (D + 2) FP32: unnormalised O, then maxima, then sums
-    int* base;                    // (B + 1) first unit of every sequence, written by CTA 0
+    int* base;                    // (B + 2) every sequence's first position in the schedule, its end, its lead
     unsigned int* status;
     float scale_log2;             // scale * log2(e)
     int max_pos;
