@@ -81,6 +81,8 @@ __device__ __forceinline__ float block_scale(float a) {
 template <bool E4M3, int HELD, bool BF16>
 __global__ void __launch_bounds__(max_threads(HELD), min_ctas(HELD)) append_kernel(const AppendParams p) {
     __shared__ float red[2][max_threads(HELD) / 32];
+    wait_for_inputs();
+    let_next_start();
     const int is_v = blockIdx.x & 1;
     long long u = blockIdx.x >> 1;
     const int groups = (p.Hkv + p.head_group - 1) / p.head_group;
@@ -244,7 +246,7 @@ int launch_append(AppendParams p, int cache, int num_sms, cudaStream_t stream) {
     const int pieces = std::min(p.S, 1 << p.page_shift) * (p.D / 8);
     auto run = [&](auto kernel, int held) {
         const int threads = ((pieces + held - 1) / held + 31) / 32 * 32;
-        kernel<<<grid, threads, 0, stream>>>(p);
+        if (launch_early(kernel, grid, threads, 0, stream, p) != cudaSuccess) return ATTN_ERR_CUDA;
         return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
     };
     auto pick = [&](auto e4m3, auto bf16) {

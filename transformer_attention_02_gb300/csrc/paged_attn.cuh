@@ -273,7 +273,8 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     __shared__ int2 s_scan[C::kWarps];
     __shared__ Share s_begin;                                     // (b, base, list) where the CTA's range begins
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    wait_for_inputs();
+    let_next_start();
     uint8_t* const ring = smem_raw + warp * C::kRingBytes;
     const uint32_t ring_a = ptx::smem_addr(ring);
     float* const scales = reinterpret_cast<float*>(smem_raw + C::kScaleOff) + warp * C::kStages * C::kTiles * 2;
@@ -876,15 +877,16 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const AttendParams p, 
         total = (total + total_n * lead) * segs;
         first = s_mine.x * segs;
         units = s_mine.y;
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        wait_for_inputs();
     } else {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
+        wait_for_inputs();
         total = p.base[p.B];
         lead = p.base[p.B + 1];
         first = p.base[b];
         const int span = (p.base[b + 1] - first) / segs;
         units = span > 0 ? span - lead : 0;
     }
+    let_next_start();
     int c0 = 0, c1 = 0;
     if (units > 0) {
         const int ctas = working_ctas(p, total), span = units + lead;
@@ -958,19 +960,11 @@ int launch_instance(bool& attr_set, const AttendParams& p, cudaStream_t stream) 
             return ATTN_ERR_CUDA;
         attr_set = true;
     }
-    kernel<<<p.ctas, C::kWarps * 32, C::kSmemBytes, stream>>>(p);
-    // The merge may become resident while the attention drains; it waits for its end itself.
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * p.row_blocks));
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
     const bool bf16 = CT == kBf16 || (CT == kE4m3 && p.q_bf16);
-    if (cudaLaunchKernelEx(&cfg, paged_merge_kernel<D, C::kRows>, p, bf16) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (launch_early(kernel, p.ctas, C::kWarps * 32, C::kSmemBytes, stream, p) != cudaSuccess ||
+        launch_early(paged_merge_kernel<D, C::kRows>, (unsigned)(p.B * p.Hkv * p.row_blocks), 256, 0, stream, p, bf16) !=
+            cudaSuccess)
+        return ATTN_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
