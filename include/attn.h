@@ -469,8 +469,8 @@ int attn_kv_append_f16(const void *k, const void *v, long long k_stride, long lo
  *   rope_table, max_pos  as above: the queries are rotated to their positions
  *               and rounded to their type, as attn_fwd_rope does; or NULL
  *   workspace   device scratch of attn_paged_workspace_bytes(...) bytes, 256-byte
- *               aligned, contents overwritten; its size does not depend on the
- *               lengths. Calls, or replays of captured calls, that may run at the
+ *               aligned, contents overwritten; its size does not depend on
+ *               kv_lens. Calls, or replays of captured calls, that may run at the
  *               same time need one each.
  * Two launches: the attention, whose CTAs take equal shares of all visible keys,
  * and the merge of the keys that several CTAs shared. Bound by the cache's reads
@@ -491,8 +491,9 @@ int attn_fwd_paged_f16(const void *q, long long q_stride, const void *k_cache, c
 
 /* attn_paged_workspace_bytes — workspace bytes attn_fwd_paged needs for these
  * sizes on the current device (host only; 0 for an empty problem or invalid
- * sizes). */
-size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D);
+ * sizes). max_keys: max_pages * page of the call, which bounds the work of short
+ * tables, or 0: enough for any table. */
+size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, long long max_keys);
 
 /*
  * attn_last_status — synchronises `stream`, then returns and clears the

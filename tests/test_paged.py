@@ -461,3 +461,80 @@ def test_prompt_then_decode_steps(e4m3):
         d = (torch.cat(outs, 1).float() - dense.float()).abs()
         bound = 2 * 2.0 ** -8 * dense.float().abs() + 2 * (2.0 ** -8 + 2.0 ** -14) * v.float().abs().amax()
         assert bool((d <= bound).all())
+
+
+def test_calls_that_may_overlap_do_not_share_a_workspace():
+    """Without a workspace argument: captured calls, side streams and threads use scratch of their own, so results are
+    those of calls made one after the other."""
+    import threading
+
+    c = Cache(4, 2, 128, 64, 40, BF, True)
+    for b in range(4):
+        c.fill(b, 2500 - 100 * b, b)
+    kv = [_i32([2500, 2400, 2300, 2200]), _i32([2000, 1, 1999, 64])]
+    q = [_rand((4, 1, 8, 128), BF, 60 + i) for i in range(2)]
+    want = [A.attention_paged(q[i], c.k, c.v, c.table, kv[i], **c.scales) for i in range(2)]
+    # two graphs captured alike, replayed side by side
+    outs, graphs = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(A.attention_paged(q[i], c.k, c.v, c.table, kv[i], **c.scales))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for got, w in zip(outs, want):
+        assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+    # two threads on the default stream, and a side stream beside them
+    bad = []
+
+    def loop(i, stream):
+        for _ in range(50):
+            o, l = A.attention_paged(q[i], c.k, c.v, c.table, kv[i], stream=stream, **c.scales)
+            (stream or torch.cuda.current_stream()).synchronize()
+            if not (torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])):
+                bad.append(i)
+
+    threads = [threading.Thread(target=loop, args=a) for a in ((0, None), (1, None), (1, streams[0]))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+@pytest.mark.parametrize("e4m3", [True, False], ids=["e4m3", "16bit"])
+@pytest.mark.parametrize("Hq,Hkv,D,Sq", [(8, 2, 64, 5), (8, 2, 128, 5), (3, 1, 64, 7), (4, 2, 128, 16), (8, 1, 64, 9)])
+def test_row_blocks_of_24_and_32(Hq, Hkv, D, Sq, e4m3):
+    """20, 21, 32 and 72 query rows a K/V head, over more keys than one CTA takes."""
+    kv = [3000, Sq]
+    c = Cache(2, Hkv, D, 64, 48, BF, e4m3)
+    for b in range(2):
+        c.fill(b, kv[b], b)
+    q = _rand((2, Sq, Hq, D), BF, 70)
+    o, lse = A.attention_paged(q, c.k, c.v, c.table, _i32(kv), **c.scales)
+    _check_attention(c, q, q, o, lse, kv, [Sq, Sq], label="row blocks")
+
+
+def test_batches_past_256_sequences_and_many_segments_a_cta():
+    """The merge reads the schedule from the workspace past 256 sequences; segments shorter and longer than a CTA's
+    range, with the lead that the schedule gives each when there are many."""
+    B, Hkv, Hq, D, page = 700, 4, 4, 64, 16
+    kv = [(977 * b) % 1500 for b in range(B)]
+    pages = 100
+    n = 5000
+    k, v = (torch.randint(0, 0x7E, (n, Hkv, page, D), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+            for _ in range(2))
+    ks, vs = (torch.rand((n, Hkv), device=DEV) * 0.01 for _ in range(2))
+    table = torch.randint(0, n, (B, pages), dtype=torch.int32, device=DEV)
+    q = _rand((B, 1, Hq, D), BF, 80)
+    o, lse = A.attention_paged(q, k, v, table, _i32(kv), k_scale=ks, v_scale=vs)
+    row = object.__new__(_Row)
+    row.k, row.v, row.ks, row.vs, row.page = k, v, ks, vs, page
+    for b in range(0, B, 41):
+        row.table_np = table[b:b + 1].cpu().numpy()
+        _check_attention(row, q[b:b + 1], q[b:b + 1], o[b:b + 1], lse[b:b + 1], [kv[b]], [1], label=f"row {b}")

@@ -75,6 +75,10 @@ def test_workspace_size():
     assert A.attn_paged_workspace_bytes(16, 32, 8, 4, 64) == 256 + 148 * 2 * 2 * 16 * 66 * 4
     assert A.attn_paged_workspace_bytes(1, 32, 1, 9, 64) == 256 + 148 * 2 * 2 * 32 * 66 * 4
     assert A.attn_paged_workspace_bytes(1, 32, 1, 9, 128) == 256 + 148 * 2 * 32 * 130 * 4
+    # a short table bounds the CTAs: 8 segments of 5 units (577 keys), one more for sinks, and the schedule's lead
+    assert A.attn_paged_workspace_bytes(1, 32, 8, 1, 128, 577) == 256 + 8 * (5 + 4) * 2 * 8 * 130 * 4
+    assert A.attn_paged_workspace_bytes(16, 32, 8, 1, 128, 8192) == A.attn_paged_workspace_bytes(16, 32, 8, 1, 128)
+    assert A.attn_paged_workspace_bytes(16, 32, 8, 1, 128, -1) == 0
     assert A.attn_paged_workspace_bytes(0, 32, 8, 1, 128) == 0
     assert A.attn_paged_workspace_bytes(1, 30, 8, 1, 128) == 0
     assert A.attn_paged_workspace_bytes(1, 32, 8, 1, 96) == 0

@@ -12,7 +12,9 @@ raises ``AttnError`` on a non-zero status.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import threading
 
 from . import build as _build
 
@@ -92,7 +94,7 @@ def lib() -> ctypes.CDLL:
     for f in (L.attn_fwd_paged, L.attn_fwd_paged_f16):
         f.argtypes = [P, LL, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, I, I, P, I, P, ctypes.c_size_t, P]
         f.restype = I
-    L.attn_paged_workspace_bytes.argtypes = [I, I, I, I, I]
+    L.attn_paged_workspace_bytes.argtypes = [I, I, I, I, I, LL]
     L.attn_paged_workspace_bytes.restype = ctypes.c_size_t
     L.attn_last_status.argtypes = [P]
     L.attn_last_status.restype = I
@@ -245,8 +247,8 @@ def attn_fwd_paged_f16(q, q_stride, k_cache, v_cache, k_scale, v_scale, block_ta
                                     rope_table, max_pos, workspace, workspace_bytes, stream)
 
 
-def attn_paged_workspace_bytes(B, Hq, Hkv, Sq, D) -> int:
-    return int(lib().attn_paged_workspace_bytes(B, Hq, Hkv, Sq, D))
+def attn_paged_workspace_bytes(B, Hq, Hkv, Sq, D, max_keys=0) -> int:
+    return int(lib().attn_paged_workspace_bytes(B, Hq, Hkv, Sq, D, max_keys))
 
 
 def attn_last_status(stream) -> int:
@@ -578,56 +580,20 @@ def attention_block(x, ln_gamma, ln_beta, w_qkv, b_qkv, w_o, b_o, *, Hq: int, Hk
 
 
 # ------------------------------------------- windows and the paged key/value cache
+# These wrappers run once per layer and decode step, so they are written for few
+# interpreter steps: one condition over everything, and the message sought only
+# once it has failed.
 
-def attention_window(q, k, v, *, window: int, sinks: int = 0, scale=None, out=None, lse=None, stream=None):
-    """O, LSE = causal attention with a sliding window on (B, S, H, D) bf16 or fp16 CUDA tensors.
+_torch = None
 
-    The query at position p (its row plus Sk - Sq) sees the last `window` keys up to p, its own included, and the first
-    `sinks` keys. scale: None selects 1/sqrt(D). out/lse: optional preallocated outputs.
-    """
+
+def _bind():
+    """torch, imported at first use (the C ABI above needs none)."""
+    global _torch
     import torch
-    at = _device_of(q, "q")
-    qs, ks = q.shape, k.shape
-    B, Sq, Hq, D = qs
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if at < 0 or t.get_device() != at or t.dtype is not q.dtype or t.dim() != 4 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous 4-D CUDA tensor (B, S, H, D) of q's dtype and device")
-    if ks[0] != B or ks[3] != D or v.shape != ks:
-        raise ValueError("q, k, v shapes disagree")
-    L = lib()
-    back = _enter_device(at)
-    try:
-        out, lse = _outputs(q, at, out, lse, stream)
-        fn = L.attn_fwd_window if q.dtype is torch.bfloat16 else L.attn_fwd_window_f16
-        rc = fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, ks[2], Sq, ks[1], D,
-                float("nan") if scale is None else scale, window, sinks, _stream_on(at, stream))
-    finally:
-        if back is not None:
-            torch.cuda.set_device(back)
-    if rc != ATTN_OK:
-        raise AttnError(rc, "attn_fwd_window")
-    return out, lse
+    _torch = torch
+    return torch
 
-
-def _outputs(q, at, out, lse, stream):
-    """The given outputs of an attention over q (B, Sq, Hq, D), checked, or new ones."""
-    import torch
-    shape = q.shape
-    B, Sq, Hq, _ = shape
-    if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
-        if stream is not None:
-            out.record_stream(stream)              # allocated on the current stream, used on another
-    elif out.dtype is not q.dtype or out.get_device() != at or out.shape != shape or not out.is_contiguous():
-        raise ValueError("out must be a contiguous (B, Sq, Hq, D) tensor of q's type and device")
-    if lse is None:
-        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
-        if stream is not None:
-            lse.record_stream(stream)
-    elif (lse.dtype is not torch.float32 or lse.get_device() != at or lse.shape != (B, Hq, Sq)
-          or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous FP32 (B, Hq, Sq) tensor on q's device")
-    return out, lse
 
 def _token_stride(name, t, at):
     """Elements from token to token of a (B, S, H, D) tensor on device `at` whose tokens are evenly spaced and
@@ -649,7 +615,7 @@ def _token_stride(name, t, at):
 
 def _device_of(x, xname):
     """Index of a CUDA tensor's device; checks its type and rank too."""
-    import torch
+    torch = _torch or _bind()
     if x.dtype is not torch.bfloat16 and x.dtype is not torch.float16:
         raise ValueError(f"{xname} must be bf16 or fp16")
     if x.dim() != 4:
@@ -657,70 +623,170 @@ def _device_of(x, xname):
     return x.get_device()
 
 
-def _int32(name, t, shape, at):
-    import torch
-    if t.dtype is not torch.int32 or t.get_device() != at or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of shape {shape} on the other tensors' device")
-    return t.data_ptr()
-
-
-def _cache_args(x, xname, at, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, lens, lens_name, table):
-    """Checks what the cache's calls share; returns their common arguments."""
-    import torch
-    shape, kind = k_cache.shape, k_cache.dtype
-    if (len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not kind or k_cache.get_device() != at
-            or v_cache.get_device() != at or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
-        raise ValueError(f"k_cache and v_cache must be contiguous (n_pages, Hkv, page, D) tensors of one type on "
-                         f"{xname}'s device")
-    n_pages, Hkv, page, D = shape
-    ks = vs = None
-    if kind is torch.float8_e4m3fn:
-        kind = CACHE_E4M3
-        for t in (k_scale, v_scale):
-            if t is None or (t.dtype is not torch.float32 or t.get_device() != at or t.shape != (n_pages, Hkv)
-                             or not t.is_contiguous()):
-                raise ValueError("k_scale and v_scale must be contiguous FP32 CUDA tensors of shape (n_pages, Hkv): an "
-                                 "8-bit cache needs its scales")
-        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
-    elif kind is x.dtype:
-        kind = CACHE_16BIT
-        if k_scale is not None or v_scale is not None:
-            raise ValueError("a 16-bit cache has no scales")
-    else:
-        raise ValueError(f"the cache must be float8_e4m3fn or of {xname}'s type")
-    B = x.shape[0]
-    if block_table.dim() != 2:
-        raise ValueError("block_table must have 2 dimensions (B, max_pages)")
-    max_pages = block_table.shape[1]
-    bt = _int32("block_table", block_table, (B, max_pages), at)
-    kl = _int32("kv_lens", kv_lens, (B,), at)
-    nl = None if lens is None else _int32(lens_name, lens, (B,), at)
-    rope, max_pos = None, 0
-    if table is not None:
-        if (table.dtype is not torch.float32 or table.dim() != 3 or table.shape[1:] != (D // 2, 2)
-                or table.get_device() != at or not table.is_contiguous()):
-            raise ValueError("table must be the (max_pos, D/2, 2) FP32 CUDA tensor of rope_table() for this D")
-        rope, max_pos = table.data_ptr(), table.shape[0]
-    return kind, ks, vs, bt, kl, nl, Hkv, D, page, max_pages, n_pages, rope, max_pos
-
-
 def _enter_device(at):
     """Makes device `at` current (the C ABI works on the current device); returns the one to go back to, or None."""
-    import torch
-    now = torch.cuda.current_device()
+    now = _torch.cuda.current_device()
     if now == at:
         return None
-    torch.cuda.set_device(at)
+    _torch.cuda.set_device(at)
     return now
 
 
 def _stream_on(at, stream):
     """Handle of `stream`, or of device `at`'s current stream."""
-    import torch
     if stream is not None:
         return stream.cuda_stream
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)      # current_stream() without making a Stream object
-    return torch.cuda.current_stream(at).cuda_stream if raw is None else raw(at)
+    raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)     # current_stream() without making a Stream object
+    return _torch.cuda.current_stream(at).cuda_stream if raw is None else raw(at)
+
+
+def _new(shape, dtype, like, stream):
+    t = _torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        t.record_stream(stream)                    # allocated on the current stream, used on another
+    return t
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_workspace_size(at, B, Hq, Hkv, Sq, D, max_keys):
+    return _lib.attn_paged_workspace_bytes(B, Hq, Hkv, Sq, D, max_keys) or 1      # (device `at` is current)
+
+
+class _Held(threading.local):
+    """Workspace of a thread's calls on a device's default stream, as {device: (tensor, address, bytes)}. Calls of one
+    thread on one stream run in order, so they may share it; another thread could enqueue between a call's two kernels,
+    another stream run beside them, and a captured call is replayed at any time, so all those get their own."""
+
+    def __init__(self):
+        self.by_device = {}
+
+
+_held = _Held()
+
+
+def _workspace(q, at, size, handle, stream):
+    """(address, bytes, the tensor to keep until the call is enqueued)."""
+    if handle or _torch.cuda.is_current_stream_capturing():
+        t = _new(size, _torch.uint8, q, stream)
+        return t.data_ptr(), size, t
+    held = _held.by_device.get(at)
+    if held is None or held[2] < size:
+        t = _torch.empty(size, dtype=_torch.uint8, device=q.device)
+        held = _held.by_device[at] = (t, t.data_ptr(), size)
+    return held[1], held[2], held[0]
+
+
+def _outputs(q, at, out, lse, stream):
+    """The given outputs of an attention over q (B, Sq, Hq, D), checked, or new ones."""
+    shape = q.shape
+    B, Sq, Hq, _ = shape
+    if out is None:
+        out = _new(shape, q.dtype, q, stream)
+    elif out.dtype is not q.dtype or out.get_device() != at or out.shape != shape or not out.is_contiguous():
+        raise ValueError("out must be a contiguous (B, Sq, Hq, D) tensor of q's type and device")
+    if lse is None:
+        lse = _new((B, Hq, Sq), _torch.float32, q, stream)
+    elif (lse.dtype is not _torch.float32 or lse.get_device() != at or lse.shape != (B, Hq, Sq)
+          or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous FP32 (B, Hq, Sq) tensor on q's device")
+    return out, lse
+
+
+def attention_window(q, k, v, *, window: int, sinks: int = 0, scale=None, out=None, lse=None, stream=None):
+    """O, LSE = causal attention with a sliding window on (B, S, H, D) bf16 or fp16 CUDA tensors.
+
+    The query at position p (its row plus Sk - Sq) sees the last `window` keys up to p, its own included, and the first
+    `sinks` keys. scale: None selects 1/sqrt(D). out/lse: optional preallocated outputs.
+    """
+    at = _device_of(q, "q")
+    qs, ks = q.shape, k.shape
+    B, Sq, Hq, D = qs
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if at < 0 or t.get_device() != at or t.dtype is not q.dtype or t.dim() != 4 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous 4-D CUDA tensor (B, S, H, D) of q's dtype and device")
+    if ks[0] != B or ks[3] != D or v.shape != ks:
+        raise ValueError("q, k, v shapes disagree")
+    L = lib()
+    back = _enter_device(at)
+    try:
+        out, lse = _outputs(q, at, out, lse, stream)
+        fn = L.attn_fwd_window if q.dtype is _torch.bfloat16 else L.attn_fwd_window_f16
+        rc = fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, ks[2], Sq, ks[1], D,
+                float("nan") if scale is None else scale, window, sinks, _stream_on(at, stream))
+    finally:
+        if back is not None:
+            _torch.cuda.set_device(back)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_fwd_window")
+    return out, lse
+
+
+def _cache_args(x, xname, at, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, lens, lens_name, table):
+    """Checks what the cache's calls share; returns their common arguments."""
+    torch = _torch
+    shape, dtype = k_cache.shape, k_cache.dtype
+    i32, f32 = torch.int32, torch.float32
+    B = x.shape[0]
+    ks = vs = nl = rope = None
+    max_pos = 0
+    if len(shape) == 4 and block_table.dim() == 2:
+        n_pages, Hkv, page, D = shape
+        max_pages = block_table.shape[1]
+        kind = CACHE_16BIT
+        ok = (v_cache.shape == shape and v_cache.dtype is dtype and k_cache.get_device() == at
+              and v_cache.get_device() == at and k_cache.is_contiguous() and v_cache.is_contiguous()
+              and block_table.dtype is i32 and block_table.shape[0] == B and block_table.get_device() == at
+              and block_table.is_contiguous()
+              and kv_lens.dtype is i32 and kv_lens.shape == (B,) and kv_lens.get_device() == at
+              and kv_lens.is_contiguous())
+        if dtype is torch.float8_e4m3fn:
+            kind, pair = CACHE_E4M3, (n_pages, Hkv)
+            ok = (ok and k_scale is not None and v_scale is not None
+                  and k_scale.dtype is f32 and k_scale.shape == pair and k_scale.get_device() == at
+                  and k_scale.is_contiguous()
+                  and v_scale.dtype is f32 and v_scale.shape == pair and v_scale.get_device() == at
+                  and v_scale.is_contiguous())
+            if ok:
+                ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+        else:
+            ok = ok and dtype is x.dtype and k_scale is None and v_scale is None
+        if lens is not None:
+            ok = (ok and lens.dtype is i32 and lens.shape == (B,) and lens.get_device() == at and lens.is_contiguous())
+            nl = lens.data_ptr()
+        if table is not None:
+            ok = (ok and table.dtype is f32 and table.dim() == 3 and table.shape[1] == D // 2 and table.shape[2] == 2
+                  and table.get_device() == at and table.is_contiguous())
+            rope, max_pos = table.data_ptr(), table.shape[0]
+        if ok:
+            return (kind, ks, vs, block_table.data_ptr(), kv_lens.data_ptr(), nl, Hkv, D, page, max_pages, n_pages, rope,
+                    max_pos)
+    raise ValueError(_cache_fault(x, xname, at, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, lens, lens_name,
+                                  table))
+
+
+def _cache_fault(x, xname, at, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, lens, lens_name, table):
+    """What is wrong with the arguments that _cache_args refuses."""
+    torch = _torch
+    if (k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype is not k_cache.dtype
+            or k_cache.get_device() != at or v_cache.get_device() != at or not k_cache.is_contiguous()
+            or not v_cache.is_contiguous()):
+        return f"k_cache and v_cache must be contiguous (n_pages, Hkv, page, D) tensors of one type on {xname}'s device"
+    B = x.shape[0]
+    for name, t, want in (("block_table", block_table, (B, block_table.shape[-1]) if block_table.dim() else (B, 1)),
+                          ("kv_lens", kv_lens, (B,)), (lens_name, lens, (B,))):
+        if t is not None and (t.dtype is not torch.int32 or tuple(t.shape) != want or t.get_device() != at
+                              or not t.is_contiguous()):
+            return f"{name} must be a contiguous int32 CUDA tensor of shape {want} on the other tensors' device"
+    if k_cache.dtype is not torch.float8_e4m3fn and k_cache.dtype is not x.dtype:
+        return f"the cache must be float8_e4m3fn or of {xname}'s type"
+    if k_cache.dtype is x.dtype and (k_scale is not None or v_scale is not None):
+        return "a 16-bit cache has no scales"
+    if table is not None and (table.dtype is not torch.float32 or table.dim() != 3
+                              or tuple(table.shape[1:]) != (k_cache.shape[3] // 2, 2) or table.get_device() != at
+                              or not table.is_contiguous()):
+        return "table must be the (max_pos, D/2, 2) FP32 CUDA tensor of rope_table() for this D"
+    return ("k_scale and v_scale must be contiguous FP32 CUDA tensors of shape (n_pages, Hkv): an 8-bit cache needs its "
+            "scales")
 
 
 def kv_append(k, v, k_cache, v_cache, block_table, kv_lens, *, new_lens=None, k_scale=None, v_scale=None, table=None,
@@ -733,26 +799,28 @@ def kv_append(k, v, k_cache, v_cache, block_table, kv_lens, *, new_lens=None, k_
     each) are int32; kv_lens counts the step's tokens already: token s of sequence b goes to position
     kv_lens[b] - new_lens[b] + s. table: rope_table() to rotate the keys to their positions, or None.
     """
-    import torch
     at = _device_of(k, "k")
     kind, ks, vs, bt, kl, nl, Hkv, D, page, max_pages, n_pages, rope, max_pos = _cache_args(
         k, "k", at, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, new_lens, "new_lens", table)
-    shape = k.shape
-    B, S = shape[0], shape[1]
-    if v.dtype is not k.dtype or v.shape != shape or shape[2] != Hkv or shape[3] != D:
+    shape, dtype = k.shape, k.dtype
+    B, S, H, Dk = shape
+    if v.dtype is not dtype or v.shape != shape or H != Hkv or Dk != D:
         raise ValueError("k and v must be (B, S, Hkv, D) tensors of one type, with the cache's Hkv and D")
     k_stride, v_stride = _token_stride("k", k, at), _token_stride("v", v, at)
-    L = lib()
-    fn = L.attn_kv_append if k.dtype is torch.bfloat16 else L.attn_kv_append_f16
+    L = _lib or lib()
+    fn = L.attn_kv_append if dtype is _torch.bfloat16 else L.attn_kv_append_f16
     back = _enter_device(at)
     try:
         rc = fn(k.data_ptr(), v.data_ptr(), k_stride, v_stride, k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, bt, kl,
                 nl, B, S, Hkv, D, page, max_pages, n_pages, kind, rope, max_pos, _stream_on(at, stream))
     finally:
         if back is not None:
-            torch.cuda.set_device(back)
-    if rc != ATTN_OK:
+            _torch.cuda.set_device(back)
+    if rc:
         raise AttnError(rc, "attn_kv_append")
+
+
+_NAN = float("nan")
 
 
 def attention_paged(q, k_cache, v_cache, block_table, kv_lens, *, q_lens=None, k_scale=None, v_scale=None, table=None,
@@ -762,38 +830,35 @@ def attention_paged(q, k_cache, v_cache, block_table, kv_lens, *, q_lens=None, k
     Query i of sequence b sits at position kv_lens[b] - q_lens[b] + i (q_lens: default Sq each) and sees the keys up
     to it; window > 0: only the last `window` of them and the first `sinks` tokens. table: rope_table() to rotate the
     queries to their positions, or None. Rows i >= q_lens[b] of out and lse are not written. workspace: optional
-    uint8 CUDA tensor of at least attn_paged_workspace_bytes bytes (allocated here when omitted).
+    uint8 CUDA tensor of at least attn_paged_workspace_bytes bytes; when omitted, one that the calling thread keeps for
+    the device's default stream, or, on another stream or under capture, a new one.
     """
-    import torch
     at = _device_of(q, "q")
     kind, ks, vs, bt, kl, nl, Hkv, D, page, max_pages, n_pages, rope, max_pos = _cache_args(
         q, "q", at, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, q_lens, "q_lens", table)
     q_stride = _token_stride("q", q, at)
-    shape = q.shape
-    B, Sq, Hq, Dq = shape
+    B, Sq, Hq, Dq = q.shape
     if Dq != D:
         raise ValueError("q and the cache disagree on D")
-    L = lib()
+    L = _lib or lib()
     back = _enter_device(at)
     try:
         out, lse = _outputs(q, at, out, lse, stream)
+        handle = _stream_on(at, stream)
         if workspace is None:
-            size = L.attn_paged_workspace_bytes(B, Hq, Hkv, Sq, D)
-            workspace = torch.empty(size or 1, dtype=torch.uint8, device=q.device)
-            if stream is not None:
-                workspace.record_stream(stream)
+            ws, size, keep = _workspace(q, at, _paged_workspace_size(at, B, Hq, Hkv, Sq, D, max_pages * page), handle,
+                                        stream)
         else:
             if workspace.get_device() != at or not workspace.is_contiguous():
                 raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
-            size = workspace.numel() * workspace.element_size()
-        fn = L.attn_fwd_paged if q.dtype is torch.bfloat16 else L.attn_fwd_paged_f16
+            ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        fn = L.attn_fwd_paged if q.dtype is _torch.bfloat16 else L.attn_fwd_paged_f16
         rc = fn(q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, bt, kl, nl, out.data_ptr(),
-                lse.data_ptr(), B, Hq, Hkv, Sq, D, page, max_pages, n_pages, kind,
-                float("nan") if scale is None else scale, window, sinks, rope, max_pos, workspace.data_ptr(), size,
-                _stream_on(at, stream))
+                lse.data_ptr(), B, Hq, Hkv, Sq, D, page, max_pages, n_pages, kind, _NAN if scale is None else scale,
+                window, sinks, rope, max_pos, ws, size, handle)
     finally:
         if back is not None:
-            torch.cuda.set_device(back)
-    if rc != ATTN_OK:
+            _torch.cuda.set_device(back)
+    if rc:
         raise AttnError(rc, "attn_fwd_paged")
     return out, lse

@@ -86,12 +86,25 @@ int kv_append_impl(const void* k, const void* v, long long k_stride, long long v
     return paged::launch_append(p, e4m3 ? paged::kE4m3 : bf16 ? paged::kBf16 : paged::kF16, dev.num_sms, stream);
 }
 
-// Workspace of the attention: the place of every sequence in the schedule, then two FP32
-// parts (unnormalised O, maximum, sum) for each CTA. Independent of the lengths.
-size_t attend_workspace(int B, int rows, int D, int sms, size_t* part_off) {
+// A segment's units in the schedule at most: its keys, one unit more for the
+// sinks, and its lead.
+long long span_bound(long long max_keys) { return (max_keys + paged::kUnit - 1) / paged::kUnit + 4; }
+
+// CTAs of the attention: as many as the device holds at once, or as the longest
+// lists could give work to (max_keys 0: any length).
+int attend_ctas(int B, int Hkv, int rows, int D, long long max_keys, int sms) {
     const int rb = paged::block_rows(rows);
+    const long long all = (long long)sms * paged::resident_ctas(D, rb);
+    if (max_keys <= 0) return (int)all;
+    const long long segments = (long long)B * Hkv * ((rows + rb - 1) / rb);
+    return (int)std::min(all, segments > all ? all : segments * span_bound(max_keys));
+}
+
+// Workspace of the attention: the place of every sequence in the schedule, then
+// two FP32 parts (unnormalised O, maximum, sum) for each CTA.
+size_t attend_workspace(int B, int rows, int D, int ctas, size_t* part_off) {
     *part_off = align_up((size_t)(B + 2) * sizeof(int));
-    return *part_off + (size_t)sms * paged::resident_ctas(D, rb) * 2 * rb * (D + 2) * sizeof(float);
+    return *part_off + (size_t)ctas * 2 * paged::block_rows(rows) * (D + 2) * sizeof(float);
 }
 
 int attend_impl(const void* q, long long q_stride, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -116,12 +129,12 @@ int attend_impl(const void* q, long long q_stride, const void* k_cache, const vo
     if (rows > (1 << 30)) return ATTN_ERR_INVALID_ARG;
     const int rb = paged::block_rows((int)rows);
     const long long row_blocks = (rows + rb - 1) / rb;
-    // (a segment's units, one more for the sinks, and its lead in the schedule)
-    const long long units = ((long long)max_pages * page + paged::kUnit - 1) / paged::kUnit + 4;
-    if ((long long)B * Hkv * row_blocks > 0x7fffffffLL / units) return ATTN_ERR_INVALID_ARG;
+    const long long max_keys = (long long)max_pages * page;
+    if ((long long)B * Hkv * row_blocks > 0x7fffffffLL / span_bound(max_keys)) return ATTN_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, kWorkspaceAlign)) return ATTN_ERR_INVALID_ARG;
     size_t part_off = 0;
-    if (workspace_bytes < attend_workspace(B, (int)rows, D, device_sm_count(), &part_off)) return ATTN_ERR_INVALID_ARG;
+    const int ctas = attend_ctas(B, Hkv, (int)rows, D, max_keys, device_sm_count());
+    if (workspace_bytes < attend_workspace(B, (int)rows, D, ctas, &part_off)) return ATTN_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !std::isfinite(scale)) scale = 1.0f / std::sqrt((float)D);
 
     DeviceState dev{};
@@ -157,7 +170,7 @@ int attend_impl(const void* q, long long q_stride, const void* k_cache, const vo
     p.n_pages = n_pages;
     p.window = window;
     p.sinks = sinks;
-    p.ctas = dev.num_sms * paged::resident_ctas(D, rb);
+    p.ctas = ctas;
     p.q_bf16 = bf16;
     if (e4m3) return paged::launch_attend<paged::kE4m3>(dev.paged_attr_set[paged::kE4m3], p, D, stream);
     return bf16 ? paged::launch_attend<paged::kBf16>(dev.paged_attr_set[paged::kBf16], p, D, stream)
@@ -186,11 +199,12 @@ int attn_kv_append_f16(const void* k, const void* v, long long k_stride, long lo
                           reinterpret_cast<cudaStream_t>(stream), false);
 }
 
-size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D) {
-    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Sq <= 0 || (D != 64 && D != 128)) return 0;
+size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, long long max_keys) {
+    if (max_keys < 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Sq <= 0 || (D != 64 && D != 128)) return 0;
     if ((long long)Sq * (Hq / Hkv) > (1 << 30)) return 0;
     size_t part_off = 0;
-    return attend_workspace(B, Sq * (Hq / Hkv), D, device_sm_count(), &part_off);
+    const int rows = Sq * (Hq / Hkv);
+    return attend_workspace(B, rows, D, attend_ctas(B, Hkv, rows, D, max_keys, device_sm_count()), &part_off);
 }
 
 int attn_fwd_paged(const void* q, long long q_stride, const void* k_cache, const void* v_cache, const float* k_scale,
