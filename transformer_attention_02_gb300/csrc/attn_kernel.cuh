@@ -163,8 +163,9 @@ struct TileCfg {
 
 struct TileInfo {
     int b, h, hk, m0;  // h: the (first) query head; m0: the first query row
-    int split;      // key range index; windowed variants: key blocks before the gap
-    int kb0;        // first 128-key block of the key range; windowed variants: blocks in the gap
+    int split;      // key range index; windowed variants: key blocks before the window's first
+    int kb0;        // first 128-key block of the key range; windowed variants: blocks left out before the
+                    // window's first, | kSkipsFirst: the upper sub-tile passes over that block
     int nb[2];      // KV blocks needed by query sub-tile t (rows m0+128t .. m0+128t+127)
     int n;          // max(nb[0], nb[1]): KV blocks streamed for the tile
 };
@@ -188,9 +189,9 @@ struct TileInfo {
 // Windowed variants (row at position i sees key j iff i - window < j <= i or
 // j < sinks): a tile streams the blocks of the sinks, then, past a gap, those
 // from the oldest key of its first row's window to its last row's own key.
-// Both sub-tiles walk the same list, so the upper one's first block of the
-// window may be hidden from it altogether (its rows' windows begin 128 keys
-// later): one block in window / 128 + 2.
+// Both sub-tiles walk the same list; the upper one, whose windows begin 128
+// keys later, passes over the window's first block unless sinks lie in it.
+constexpr int kSkipsFirst = 1 << 30;
 template <bool CAUSAL, bool PACK, bool WINDOW = false>
 __device__ __forceinline__ TileInfo tile_info(int tile, const FwdParams& p) {
     const int ps = PACK ? p.pack_shift : 0;
@@ -229,13 +230,15 @@ __device__ __forceinline__ TileInfo tile_info(int tile, const FwdParams& p) {
     t.m0 = mb * 2 * sub_rows;
     t.split = split;
     t.kb0 = split * p.split_blocks;
-    int gap = 0;
+    int gap = 0, skips = 0;
     if (WINDOW) {
-        const int low = max(0, t.m0 + (p.Sk - p.Sq) - p.q_pos0 + 1) / kBlockN;
+        const int first = t.m0 + (p.Sk - p.Sq) - p.q_pos0 + 1;     // oldest key of the first row's window
+        const int low = max(0, first) / kBlockN;
         const int sink_blocks = (min(p.mask_vec4, p.Sk) + kBlockN - 1) / kBlockN;
-        if (low > sink_blocks) {
+        if (low >= sink_blocks) {
             t.split = sink_blocks;
             gap = low - sink_blocks;
+            if (max(0, first + sub_rows) / kBlockN > low) skips = kSkipsFirst;
         }
     }
     const int range_begin = t.kb0 * kBlockN;
@@ -248,7 +251,7 @@ __device__ __forceinline__ TileInfo tile_info(int tile, const FwdParams& p) {
         if (first < p.Sq) kv_end = CAUSAL ? min(range_end, max(0, last + (p.Sk - p.Sq) + 1)) : range_end;
         t.nb[s] = kv_end > range_begin ? (kv_end - range_begin + kBlockN - 1) / kBlockN - gap : 0;
     }
-    if (WINDOW) t.kb0 = gap;
+    if (WINDOW) t.kb0 = gap | skips;
     t.n = max(t.nb[0], t.nb[1]);
     return t;
 }
@@ -256,7 +259,7 @@ __device__ __forceinline__ TileInfo tile_info(int tile, const FwdParams& p) {
 // Key block of the j-th block a tile streams.
 template <bool WINDOW>
 __device__ __forceinline__ int key_block(const TileInfo& t, int j) {
-    return WINDOW ? (j < t.split ? j : j + t.kb0) : t.kb0 + j;
+    return WINDOW ? (j < t.split ? j : j + (t.kb0 & ~kSkipsFirst)) : t.kb0 + j;
 }
 
 struct SyncCtx {
@@ -688,7 +691,7 @@ __device__ void role_qload(const CUtensorMap* tmQ, const CUtensorMap* tmO, const
 // two groups of MMAs can leave it idle. For the same reason the next K/V slot
 // is probed (without blocking) before a group is issued, and the wait after
 // the group is skipped when the probe already saw the slot full.
-template <int D, bool BF16, bool ROPE>
+template <int D, bool BF16, bool ROPE, bool WINDOW>
 __device__ void role_mma(const FwdParams& p, uint32_t smem, const uint8_t* smem_ptr, uint32_t tmem, const SyncCtx& sc) {
     using C = TileCfg<D>;
     const bool leader = (threadIdx.x & 31) == 0;
@@ -755,12 +758,14 @@ __device__ void role_mma(const FwdParams& p, uint32_t smem, const uint8_t* smem_
     if (p.flags & kFlagDebugStall) alive = wait_phase(bar(C::bStall), 0, sc);   // nothing ever arrives
     // Sizes of tile-ring entry k (the issuer reads only the block counts).
     const uint8_t* ring = smem_ptr + C::kTileOff;
+    int passed = -1;                    // windowed variants: the block the upper sub-tile passes over (never its last)
     auto fetch = [&](uint32_t k, int& nb0, int& nb1) -> bool {
         const uint32_t slot = k % kTileSlots;
         if (!wait_phase(bar(C::bTileFull + slot), (k / kTileSlots) & 1u, sc)) return false;
         const int4 c = reinterpret_cast<const int4*>(ring + 32 * slot)[1];
         nb0 = c.z;
         nb1 = c.w;
+        if (WINDOW) passed = (c.y & kSkipsFirst) ? c.x : -1;
         ptx::mbar_arrive(bar(C::bTileEmpty + slot));
         return true;
     };
@@ -782,7 +787,7 @@ __device__ void role_mma(const FwdParams& p, uint32_t smem, const uint8_t* smem_
         if (!wait_phase(bar(kQReady + q_buf[1]), use1 & 1u, sc)) { alive = false; break; }
         ptx::tc_fence_after_sync();
         ++nq;
-        if (n1 > 0) issue_qk(1, q_buf[1], ks);
+        if (n1 > 0 && !(WINDOW && passed == 0)) issue_qk(1, q_buf[1], ks);
         commit(C::bKVEmpty + ks);
         if (n0 <= 1) commit(C::bQEmpty + q_buf[0]);
         if (n1 <= 1) commit(C::bQEmpty + q_buf[1]);
@@ -803,15 +808,15 @@ __device__ void role_mma(const FwdParams& p, uint32_t smem, const uint8_t* smem_
                     if (j + 2 == n0) commit(C::bQEmpty + q_buf[0]);
                 }
             }
-            if (j < n1) {
+            if (j < n1 && !(WINDOW && j == passed)) {
                 if (!wait_p(1)) { alive = false; break; }
-                issue_pv(1, vs, j > 0);
+                issue_pv(1, vs, j > (WINDOW && passed == 0 ? 1 : 0));
                 if (j == n1 - 1) commit(C::bOFull + 1);
             }
             commit(C::bKVEmpty + vs);
             if (more) {
                 v_seen = probe_next();
-                if (j + 1 < n1) issue_qk(1, q_buf[1], ks);
+                if (j + 1 < n1 && !(WINDOW && j + 1 == passed)) issue_qk(1, q_buf[1], ks);
                 commit(C::bKVEmpty + ks);
                 if (j + 2 == n1) commit(C::bQEmpty + q_buf[1]);
             }
@@ -893,7 +898,10 @@ __device__ void role_softmax(const FwdParams& p, uint32_t smem, uint8_t* smem_pt
         float l_sum = 0.f;
         bool ok = true;
         const float sl = p.scale_log2;
+        const int passed = WINDOW && wg == 1 && (ti.kb0 & kSkipsFirst) ? ti.split : -1;
+        bool begun = false;
         for (int j = 0; j < nb; ++j) {
+            if (WINDOW && j == passed) continue;              // hidden from every row of this sub-tile
             // Each warp waits on its own; the warpgroup agrees on whether to go
             // on at the one named barrier of the block (before the hand-off of
             // P), where a warp whose wait ran out votes to stop.
@@ -959,7 +967,11 @@ __device__ void role_softmax(const FwdParams& p, uint32_t smem, uint8_t* smem_pt
                 if (WINDOW) {
                     // keys before the row's window are hidden, but for the sinks
                     const int low = row + (p.Sk - p.Sq) - p.q_pos0 + 1 - key0, sink = p.mask_vec4 - key0;
-                    if (low > 0 && sink < kBlockN) {
+                    if (low > 0 && sink <= 0) {
+#pragma unroll
+                        for (int c = 0; c < kBlockN; ++c)
+                            if (c < low) x[c] = -INFINITY;
+                    } else if (low > 0 && sink < kBlockN) {
 #pragma unroll
                         for (int c = 0; c < kBlockN; ++c)
                             if (c < low && c >= sink) x[c] = -INFINITY;
@@ -979,7 +991,8 @@ __device__ void role_softmax(const FwdParams& p, uint32_t smem, uint8_t* smem_pt
                 const float m_new = fmaxf(m_used, m_blk);
                 float alpha = 1.f;
                 bool rescale = false;
-                if (j == 0) {
+                if (WINDOW ? !begun : j == 0) {
+                    begun = true;
                     m_used = m_new;
                 } else {
                     const bool need = m_new > m_used + kRescaleThreshold;
@@ -1159,7 +1172,7 @@ __global__ void __launch_bounds__(kernel_threads(ROPE), 1)
     } else if (warp < kRotateWarp0) {
         ptx::setmaxnreg_dec<control_regs(ROPE)>();
         if (warp == kMmaWarp)
-            role_mma<D, BF16, ROPE>(p, smem, smem_ptr, tmem, sc);
+            role_mma<D, BF16, ROPE, WINDOW>(p, smem, smem_ptr, tmem, sc);
         else if (warp == kTmaWarp)
             role_tma<D, WINDOW>(&tmK, &tmV, smem, smem_ptr, sc);
         else if (warp == kQWarp)
