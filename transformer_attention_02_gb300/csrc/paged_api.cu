@@ -26,6 +26,7 @@ int check_cache(int B, int S, int Hkv, int D, int page, int max_pages, int n_pag
     if (page < 16 || page > 256 || (page & (page - 1)) != 0) return ATTN_ERR_INVALID_ARG;
     if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
     if ((long long)max_pages * page > (1 << 30) || S > (1 << 30)) return ATTN_ERR_INVALID_ARG;
+    if ((long long)Hkv * page * D > (1 << 30)) return ATTN_ERR_INVALID_ARG;          // bytes of a page in 32 bits
     return ATTN_OK;
 }
 

@@ -69,8 +69,10 @@ struct Cfg {
     static constexpr int kQOff = kStatOff + kWarps * kRows * 8;
     static constexpr int kFragOff = kQOff + kRows * kQStride;
     static constexpr int kShareOff = kFragOff + (kQShared ? kRows * D * 2 : 0);   // [warp]{copies', products'}
-    static constexpr int kSmemBytes = kShareOff + kWarps * 2 * 80;
-    static_assert(8 * D * 4 <= kStageBytes, "a warp merges eight rows at a time through one stage of its ring");
+    static constexpr int kRowOff = kShareOff + kWarps * 2 * 80;  // [row] score factor; [row]{max, sum} of the merge
+    static constexpr int kSmemBytes = kRowOff + kRows * 16;
+    static constexpr int kMergeTiles = kStageBytes / (8 * D * 4);    // n-tiles that a stage of the ring takes at once
+    static_assert(kMergeTiles >= 1, "a warp's rows are merged through one stage of its ring");
     static_assert(kUnit % kKeys == 0, "a stage lies inside one unit");
     static_assert(kQOff % 16 == 0 && kFragOff % 16 == 0, "16-byte accesses");
     static_assert(kResident * (kSmemBytes + 1024 + 128) <= 233472, "shared memory budget");
@@ -283,6 +285,8 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     float2* const stats = reinterpret_cast<float2*>(smem_raw + C::kStatOff);
     uint8_t* const q_sh = smem_raw + C::kQOff;
     uint2* const frag_sh = reinterpret_cast<uint2*>(smem_raw + C::kFragOff);
+    float* const row_sh = reinterpret_cast<float*>(smem_raw + C::kRowOff);
+    float2* const total_sh = reinterpret_cast<float2*>(smem_raw + C::kRowOff) + C::kRows;
 
     // The page numbers come into L2 while the lengths are on their way (a line a
     // thread; a table past that is fetched as it is needed).
@@ -380,6 +384,8 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     __syncwarp();
     int ld_x = x, ld_i = 0, ld_n = 0, ld_stage = 0;
     bool ld_more = false;
+    const uint32_t page_bytes = ((uint32_t)p.Hkv << p.page_shift) * C::kRowBytes;
+    uint32_t head_off = 0;                                        // of the share's head in a page, and the lane's chunk
     int ids = 0;                                                  // page numbers of 32 / kTiles stages, one tile a lane
     constexpr int kBatch = 32 / C::kTiles;
     auto stages_of = [](int units) { return (units * kUnit + C::kWarps * C::kKeys - 1) / (C::kWarps * C::kKeys); };
@@ -397,6 +403,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
         __syncwarp();
         ld_i = 0;
         ld_n = stages_of(s.u1 - s.u0);
+        head_off = ((uint32_t)s.hk << p.page_shift) * C::kRowBytes + lane * 16;
         // The queries are read when the products get there; by then they are in L2.
         if (warp == 0) {
             const int r0 = s.rb * C::kRows, row = r0 + lane;
@@ -433,9 +440,8 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                     if (in && !ok) atomicOr(p.status, kStatusBadIndex);
                 }
                 if (!ok) continue;
-                const size_t block = (size_t)id * p.Hkv + ld.hk;
-                const size_t at =
-                    ((block << p.page_shift) + (size_t)(k0 & ((1 << p.page_shift) - 1))) * C::kRowBytes + lane * 16;
+                const uint32_t slot = (uint32_t)(k0 & ((1 << p.page_shift) - 1));
+                const uint64_t at = (uint64_t)(uint32_t)id * page_bytes + (head_off + slot * C::kRowBytes);
                 const uint8_t* ks = static_cast<const uint8_t*>(p.k_cache) + at;
                 const uint8_t* vs = static_cast<const uint8_t*>(p.v_cache) + at;
                 const uint32_t dst = ring_a + ld_stage * C::kStageBytes + m * 16 * C::kRowBytes;
@@ -456,7 +462,8 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                     }
                 }
                 if (CT == kE4m3 && lane < 2)
-                    cp_async4(scales_a + ((ld_stage * C::kTiles + m) * 2 + lane) * 4, (lane ? p.v_scale : p.k_scale) + block);
+                    cp_async4(scales_a + ((ld_stage * C::kTiles + m) * 2 + lane) * 4,
+                              (lane ? p.v_scale : p.k_scale) + ((uint64_t)(uint32_t)id * (uint32_t)p.Hkv + ld.hk));
             }
             if (++ld_i == ld_n) {
                 ld_x = ld.next;
@@ -528,11 +535,10 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
         __syncthreads();
         // B fragments. With an 8-bit cache the queries become f16 values, each
         // row scaled by a power of two to lie in [-2, 2]: exact down to 2^-24 of
-        // the row's largest value, whatever the row's magnitude.
+        // the row's largest value, whatever the row's magnitude. Where the
+        // fragments stand in shared memory each n-tile is one warp's work.
         float cf[NT][2];                                          // log2 units per raw score, rows 2t and 2t + 1
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            uint32_t w[kSteps][2];
+        auto fragments = [&](int n, uint32_t (&w)[kSteps][2]) -> float {
             const uint8_t* src = q_sh + (8 * n + g) * C::kQStride;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
@@ -546,52 +552,66 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                     w[s][1] = *reinterpret_cast<const uint32_t*>(src + (16 * s + 8 + 2 * t) * 2);
                 }
             }
-            cf[n][0] = cf[n][1] = p.scale_log2;
-            if (CT == kE4m3) {
-                float top = 0.f;
+            if (CT != kE4m3) return 1.f;
+            float top = 0.f;
 #pragma unroll
-                for (int s = 0; s < kSteps; ++s)
+            for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float2 a = widen16(w[s][h], bf);
-                        top = fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y)));
-                    }
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -120), 120);
-                const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-                const float back = __uint_as_float((uint32_t)(127 + e) << 23);
+                for (int h = 0; h < 2; ++h) {
+                    const float2 a = widen16(w[s][h], bf);
+                    top = fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y)));
+                }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -120), 120);
+            const float f = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-                for (int s = 0; s < kSteps; ++s)
+            for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float2 a = widen16(w[s][h], bf);
-                        w[s][h] = ptx::pack_f16x2(a.x * f, a.y * f);
-                    }
-                cf[n][0] *= __shfl_sync(0xffffffffu, back, 8 * t);
-                cf[n][1] *= __shfl_sync(0xffffffffu, back, 8 * t + 4);
+                for (int h = 0; h < 2; ++h) {
+                    const float2 a = widen16(w[s][h], bf);
+                    w[s][h] = ptx::pack_f16x2(a.x * f, a.y * f);
+                }
+            return __uint_as_float((uint32_t)(127 + e) << 23);    // of row g
+        };
+        if constexpr (C::kQShared) {
+            if (warp < NT) {
+                uint32_t w[kSteps][2];
+                const float back = fragments(warp, w);
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) frag_sh[(s * NT + warp) * 32 + lane] = make_uint2(w[s][0], w[s][1]);
+                if (t == 0) row_sh[8 * warp + g] = p.scale_log2 * back;
             }
+            __syncthreads();
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                if constexpr (C::kQShared) {
-                    if (warp == 0) frag_sh[(s * NT + n) * 32 + lane] = make_uint2(w[s][0], w[s][1]);
-                } else {
+            for (int n = 0; n < NT; ++n) {
+                cf[n][0] = row_sh[8 * n + 2 * t];
+                cf[n][1] = row_sh[8 * n + 2 * t + 1];
+            }
+        } else {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                uint32_t w[kSteps][2];
+                const float back = fragments(n, w);
+                cf[n][0] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t);
+                cf[n][1] = p.scale_log2 * __shfl_sync(0xffffffffu, back, 8 * t + 4);
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) {
                     qf[s][n][0] = w[s][0];
                     qf[s][n][1] = w[s][1];
                 }
             }
         }
-        if constexpr (C::kQShared) __syncthreads();
 
         float acc[kSteps][NT][4];                                 // O^T
-        // Rows 2t, 2t + 1 of each n-tile: the maximum in use (log2 units; below
-        // any logit at first, so that no weight needs a special case) and this
-        // lane's part of the sum.
-        float m_used[NT][2], l_sum[NT][2];
+        // Rows 2t, 2t + 1 of each n-tile: minus the maximum in use (log2 units;
+        // below any logit at first, so that no weight needs a special case) and
+        // this lane's part of the sum.
+        float m_neg[NT][2], l_sum[NT][2];
         float v_ref = 0.f, v_inv = 0.f;                           // largest value scale so far (acc is in units of it)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            m_used[n][0] = m_used[n][1] = kNoLogit;
+            m_neg[n][0] = m_neg[n][1] = -kNoLogit;
             l_sum[n][0] = l_sum[n][1] = 0.f;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) acc[s][n][0] = acc[s][n][1] = acc[s][n][2] = acc[s][n][3] = 0.f;
@@ -602,7 +622,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
             cp_async_wait<C::kStages - 2>();
             __syncwarp();
             issue();
-#pragma unroll
+#pragma unroll 1
             for (int m = 0; m < C::kTiles; ++m) {
                 const int k0 = keys_sh[st * C::kTiles + m];
                 if (k0 == kNoKey) continue;                   // nothing there, or a page out of range
@@ -680,7 +700,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        grow |= fmaf(fmaxf(s[n][e], s[n][2 + e]), f[n][e], -kRescaleThreshold) > m_used[n][e];
+                        grow |= fmaf(fmaxf(s[n][e], s[n][2 + e]), f[n][e], m_neg[n][e]) > kRescaleThreshold;
                 if (__any_sync(0xffffffffu, grow)) {
                     float fv = 1.f;
                     if (CT == kE4m3 && vs > v_ref) {
@@ -695,9 +715,9 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                             float mx = fmaxf(s[n][e], s[n][2 + e]) * f[n][e];
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                            mx = fmaxf(mx, m_used[n][e]);
-                            const float alpha = ptx::ex2(m_used[n][e] - mx);
-                            m_used[n][e] = mx;
+                            mx = fmaxf(mx, -m_neg[n][e]);
+                            const float alpha = ptx::ex2(-m_neg[n][e] - mx);
+                            m_neg[n][e] = -mx;
                             l_sum[n][e] *= alpha;
                             const float fa = alpha * fv;
 #pragma unroll
@@ -714,8 +734,8 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float w[4];
-                    ptx::fma2(w[0], w[1], s[n][0], s[n][1], f[n][0], f[n][1], -m_used[n][0], -m_used[n][1]);
-                    ptx::fma2(w[2], w[3], s[n][2], s[n][3], f[n][0], f[n][1], -m_used[n][0], -m_used[n][1]);
+                    ptx::fma2(w[0], w[1], s[n][0], s[n][1], f[n][0], f[n][1], m_neg[n][0], m_neg[n][1]);
+                    ptx::fma2(w[2], w[3], s[n][2], s[n][3], f[n][0], f[n][1], m_neg[n][0], m_neg[n][1]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w[e] = ptx::ex2(w[e]);
                     ptx::add2(l_sum[n][0], l_sum[n][1], l_sum[n][0], l_sum[n][1], w[0], w[1]);
@@ -766,70 +786,89 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
             __syncwarp();
             if (NT == 1) fetch_q(s);
         }
-        // ---- merge the warps, eight rows at a time, through the stage that was
-        // read last (the others hold the next segment's keys)
-        __syncwarp();
+        // ---- merge the warps through the stage that was read last (the others
+        // hold the next segment's keys): first the maxima and sums, so that each
+        // warp can write its O^T in the units of the common maximum, then O^T,
+        // kMergeTiles n-tiles at a time.
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float l = l_sum[n][e];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                if (g == 0) stats[warp * C::kRows + 8 * n + 2 * t + e] = make_float2(-m_neg[n][e], l);
+            }
+        __syncthreads();
+        float to_common = 0.f;                                    // of row `lane`
+        if (lane < C::kRows) {
+            float mx = kNoLogit, sum = 0.f;
+#pragma unroll
+            for (int v = 0; v < C::kWarps; ++v) mx = fmaxf(mx, stats[v * C::kRows + lane].x);
+#pragma unroll
+            for (int v = 0; v < C::kWarps; ++v) {
+                const float2 s2 = stats[v * C::kRows + lane];
+                sum = fmaf(s2.y, ptx::ex2(s2.x - mx), sum);
+            }
+            to_common = ptx::ex2(stats[warp * C::kRows + lane].x - mx) * (CT == kE4m3 ? v_ref : 1.f);
+            if (warp == 0) total_sh[lane] = make_float2(mx, sum);
+        }
         const int m_stage = st == 0 ? C::kStages - 1 : st - 1;
         float* const mine_o = reinterpret_cast<float*>(ring + m_stage * C::kStageBytes);
         const bool full = now.u0 == 0 && now.u1 == now.list.units;
         float* slot = p.part + (size_t)(2 * blockIdx.x + (now.u0 == 0 ? 1 : 0)) * C::kRows * (D + 2);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int n0 = 0; n0 < NT; n0 += C::kMergeTiles) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int col = 2 * t + e;
-                float l = l_sum[n][e];
+            for (int n = n0; n < NT && n < n0 + C::kMergeTiles; ++n) {
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-                if (g == 0) stats[warp * C::kRows + 8 * n + col] = make_float2(m_used[n][e], l);
-                const float f = CT == kE4m3 ? v_ref : 1.f;
+                for (int e = 0; e < 2; ++e) {
+                    const float f = __shfl_sync(0xffffffffu, to_common, 8 * n + 2 * t + e);
+                    float* const row = mine_o + (8 * (n - n0) + 2 * t + e) * D;
 #pragma unroll
-                for (int d = 0; d < kSteps; ++d) {
-                    const int da = CT == kE4m3 ? 32 * (d >> 1) + (d & 1) + 2 * g : 16 * d + g;
-                    const int db = CT == kE4m3 ? da + 16 : da + 8;
-                    mine_o[col * D + (da ^ (t << 3))] = acc[d][n][e] * f;      // XOR: spreads the rows over the banks
-                    mine_o[col * D + (db ^ (t << 3))] = acc[d][n][2 + e] * f;
+                    for (int d = 0; d < kSteps; ++d) {
+                        const int da = CT == kE4m3 ? 32 * (d >> 1) + (d & 1) + 2 * g : 16 * d + g;
+                        const int db = CT == kE4m3 ? da + 16 : da + 8;
+                        row[da ^ (t << 3)] = acc[d][n][e] * f;    // XOR: spreads the rows over the banks
+                        row[db ^ (t << 3)] = acc[d][n][2 + e] * f;
+                    }
                 }
             }
             __syncthreads();
-            for (int w = tid; w < 8 * (D / 4); w += kThreads) {
-                const int c8 = w / (D / 4), d = (w - c8 * (D / 4)) * 4, col = 8 * n + c8;
-                float mx = kNoLogit;
-#pragma unroll
-                for (int v = 0; v < C::kWarps; ++v) mx = fmaxf(mx, stats[v * C::kRows + col].x);
-                float sum = 0.f;
+            constexpr int kItems = D / 4;                         // float4 of a row
+            const int rows = 8 * min(C::kMergeTiles, NT - n0);
+            for (int w = tid; w < rows * kItems; w += kThreads) {
+                const int c = w / kItems, d = (w - c * kItems) * 4, col = 8 * n0 + c;
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int v = 0; v < C::kWarps; ++v) {
-                    const float2 st2 = stats[v * C::kRows + col];
-                    const float fm = ptx::ex2(st2.x - mx);
                     const float4 a = *reinterpret_cast<const float4*>(
-                        reinterpret_cast<const float*>(smem_raw + v * C::kRingBytes + m_stage * C::kStageBytes) + c8 * D +
-                        (d ^ ((c8 >> 1) << 3)));
-                    sum = fmaf(st2.y, fm, sum);
-                    o.x = fmaf(a.x, fm, o.x);
-                    o.y = fmaf(a.y, fm, o.y);
-                    o.z = fmaf(a.z, fm, o.z);
-                    o.w = fmaf(a.w, fm, o.w);
+                        reinterpret_cast<const float*>(smem_raw + v * C::kRingBytes + m_stage * C::kStageBytes) + c * D +
+                        (d ^ (((c & 7) >> 1) << 3)));
+                    o.x += a.x;
+                    o.y += a.y;
+                    o.z += a.z;
+                    o.w += a.w;
                 }
+                const float2 ms = total_sh[col];
                 if (full) {
                     const int row = r0 + col, i = row / p.group;
                     if (row < p.rows && i < now.list.ql) {
                         const int h = now.hk * p.group + (row - i * p.group);
-                        const float inv = sum != 0.f ? 1.f / sum : 0.f;       // 0: no key was visible
+                        const float inv = ms.y != 0.f ? 1.f / ms.y : 0.f;     // 0: no key was visible
                         uint2 r;
                         r.x = bf ? ptx::pack_bf16x2(o.x * inv, o.y * inv) : ptx::pack_f16x2(o.x * inv, o.y * inv);
                         r.y = bf ? ptx::pack_bf16x2(o.z * inv, o.w * inv) : ptx::pack_f16x2(o.z * inv, o.w * inv);
                         *reinterpret_cast<uint2*>(p.o + (((size_t)now.b * p.Sq + i) * p.Hq + h) * D + d) = r;
                         if (d == 0)
                             p.lse[((size_t)now.b * p.Hq + h) * p.Sq + i] =
-                                sum != 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+                                ms.y != 0.f ? (ms.x + log2f(ms.y)) * 0.6931471805599453f : -INFINITY;
                     }
                 } else {
                     *reinterpret_cast<float4*>(slot + col * D + d) = o;
                     if (d == 0) {
-                        slot[C::kRows * D + col] = mx;
-                        slot[C::kRows * (D + 1) + col] = sum;
+                        slot[C::kRows * D + col] = ms.x;
+                        slot[C::kRows * (D + 1) + col] = ms.y;
                     }
                 }
             }
