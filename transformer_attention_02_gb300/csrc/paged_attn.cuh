@@ -69,7 +69,8 @@ struct Cfg {
     static constexpr int kQOff = kStatOff + kWarps * kRows * 8;
     static constexpr int kFragOff = kQOff + kRows * kQStride;
     static constexpr int kShareOff = kFragOff + (kQShared ? kRows * D * 2 : 0);   // [warp]{copies', products'}
-    static constexpr int kRowOff = kShareOff + kWarps * 2 * 80;  // [row] score factor; [row]{max, sum} of the merge
+    static constexpr int kIssueOff = kShareOff + kWarps * 2 * 80;    // [warp] what a stage's copies need of a share
+    static constexpr int kRowOff = kIssueOff + kWarps * 32;  // [row] score factor; [row]{max, sum} of the merge
     static constexpr int kSmemBytes = kRowOff + kRows * 16;
     static constexpr int kMergeTiles = kStageBytes / (8 * D * 4);    // n-tiles that a stage of the ring takes at once
     static_assert(kMergeTiles >= 1, "a warp's rows are merged through one stage of its ring");
@@ -83,9 +84,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void prefetch_l2(const void* at) {
@@ -280,7 +278,6 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     uint8_t* const ring = smem_raw + warp * C::kRingBytes;
     const uint32_t ring_a = ptx::smem_addr(ring);
     float* const scales = reinterpret_cast<float*>(smem_raw + C::kScaleOff) + warp * C::kStages * C::kTiles * 2;
-    const uint32_t scales_a = ptx::smem_addr(scales);
     volatile int* const keys_sh = reinterpret_cast<int*>(smem_raw + C::kKeyOff) + warp * C::kStages * C::kTiles;
     float2* const stats = reinterpret_cast<float2*>(smem_raw + C::kStatOff);
     uint8_t* const q_sh = smem_raw + C::kQOff;
@@ -386,20 +383,29 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     bool ld_more = false;
     const uint32_t page_bytes = ((uint32_t)p.Hkv << p.page_shift) * C::kRowBytes;
     uint32_t head_off = 0;                                        // of the share's head in a page, and the lane's chunk
-    int ids = 0;                                                  // page numbers of 32 / kTiles stages, one tile a lane
+    // What a stage's copies need of the share, as two vectors beside it: keys
+    // {count, offset of the gap, first before it, first past it (less the
+    // offset)}, {end, start of the window, sequence, head}.
+    int4* const ld_v = reinterpret_cast<int4*>(smem_raw + C::kIssueOff) + 2 * warp;
+    // Page numbers (-1: no key, or out of range) and scales of the next
+    // 32 / kTiles stages, one 16-key tile a lane.
     constexpr int kBatch = 32 / C::kTiles;
+    int ids = -1;
+    float2 sc = make_float2(0.f, 0.f);
+    int sc_slot = -1, sc_lane = 0;                                // the stage whose scales are still to be put down
     auto stages_of = [](int units) { return (units * kUnit + C::kWarps * C::kKeys - 1) / (C::kWarps * C::kKeys); };
-    auto key_at = [&](int off) {                                  // key at offset `off` of the share's list, or none
-        if (off >= (ld.u1 - ld.u0) * kUnit) return kNoKey;
-        const int u = ld.u0 + off / kUnit;
-        return (u < ld.list.sink_units ? u : u - ld.list.sink_units + ld.list.first) * kUnit + off % kUnit;
-    };
     auto enter = [&]() {                                          // the share at ld_x
         Share s = ld;
         ld_more = locate<C::kRows>(p, segs, lead, ld_x, x_end, s);
         if (!ld_more) return;
         __syncwarp();
-        if (lane == 0) ld = s;
+        if (lane == 0) {
+            ld = s;
+            const int gap = max(0, (s.list.sink_units - s.u0) * kUnit);
+            ld_v[0] = make_int4((s.u1 - s.u0) * kUnit, gap, s.u0 * kUnit,
+                                (s.u0 - s.list.sink_units + s.list.first) * kUnit);
+            ld_v[1] = make_int4(s.kv_end, s.w_lo, s.b, s.hk);
+        }
         __syncwarp();
         ld_i = 0;
         ld_n = stages_of(s.u1 - s.u0);
@@ -424,47 +430,60 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     enter();
     if (!ld_more) return;                                         // nothing but leads in its range
     auto issue = [&]() {
+        if (CT == kE4m3 && sc_slot >= 0) {
+            // (a stage late, when they have arrived; the products come later still)
+            if ((lane ^ sc_lane) < C::kTiles) reinterpret_cast<float2*>(scales)[sc_slot + (lane ^ sc_lane)] = sc;
+            sc_slot = -1;
+        }
         if (ld_more) {
+            const int4 u = ld_v[0], w = ld_v[1];
             if (ld_i % kBatch == 0) {
-                const int key = key_at(((ld_i + lane / C::kTiles) * C::kWarps + warp) * C::kKeys + lane % C::kTiles * 16);
-                ids = key < ld.kv_end ? __ldg(p.block_table + (size_t)ld.b * p.max_pages + (key >> p.page_shift)) : -1;
+                const int off = ((ld_i + lane / C::kTiles) * C::kWarps + warp) * C::kKeys + lane % C::kTiles * 16;
+                const int key = off + (off < u.y ? u.z : u.w);
+                ids = -1;
+                if (off < u.x && key < w.x) {
+                    ids = __ldg(p.block_table + (size_t)w.z * p.max_pages + (key >> p.page_shift));
+                    if ((unsigned)ids >= (unsigned)p.n_pages) {
+                        atomicOr(p.status, kStatusBadIndex);
+                        ids = -1;
+                    } else if (CT == kE4m3) {
+                        const uint64_t at = (uint64_t)(uint32_t)ids * (uint32_t)p.Hkv + w.w;
+                        sc = make_float2(__ldg(p.k_scale + at), __ldg(p.v_scale + at));
+                    }
+                }
             }
-            const int key0 = key_at((ld_i * C::kWarps + warp) * C::kKeys);
+            const int off0 = (ld_i * C::kWarps + warp) * C::kKeys, first = ld_i % kBatch * C::kTiles;
+            const uint32_t dst = ring_a + ld_stage * C::kStageBytes;
 #pragma unroll
             for (int m = 0; m < C::kTiles; ++m) {
-                const int k0 = key0 + 16 * m;                     // (of no use past kv_end)
-                const int id = __shfl_sync(0xffffffffu, ids, ld_i % kBatch * C::kTiles + m);
-                const bool in = key0 < ld.kv_end && k0 < ld.kv_end, ok = in && (unsigned)id < (unsigned)p.n_pages;
-                if (lane == 0) {
-                    keys_sh[ld_stage * C::kTiles + m] = ok ? k0 : kNoKey;
-                    if (in && !ok) atomicOr(p.status, kStatusBadIndex);
-                }
-                if (!ok) continue;
+                const int id = __shfl_sync(0xffffffffu, ids, first + m);
+                const int k0 = off0 + 16 * m + (off0 + 16 * m < u.y ? u.z : u.w);
+                if (lane == 0) keys_sh[ld_stage * C::kTiles + m] = id >= 0 ? k0 : kNoKey;
+                if (id < 0) continue;
                 const uint32_t slot = (uint32_t)(k0 & ((1 << p.page_shift) - 1));
                 const uint64_t at = (uint64_t)(uint32_t)id * page_bytes + (head_off + slot * C::kRowBytes);
                 const uint8_t* ks = static_cast<const uint8_t*>(p.k_cache) + at;
                 const uint8_t* vs = static_cast<const uint8_t*>(p.v_cache) + at;
-                const uint32_t dst = ring_a + ld_stage * C::kStageBytes + m * 16 * C::kRowBytes;
-                if (k0 + 16 <= ld.kv_end && (k0 >= ld.w_lo || k0 + 16 <= sinks)) {
+                const uint32_t kd = dst + m * 16 * C::kRowBytes, vd = kd + C::kKeys * C::kRowBytes;
+                if (k0 + 16 <= w.x && (k0 >= w.y || k0 + 16 <= sinks)) {
 #pragma unroll
                     for (int c = 0; c < C::kCopies; ++c) {
-                        cp_async16(dst + copy_to(c), ks + c * 512);
-                        cp_async16(dst + C::kKeys * C::kRowBytes + copy_to(c), vs + c * 512);
+                        cp_async16(kd + copy_to(c), ks + c * 512);
+                        cp_async16(vd + copy_to(c), vs + c * 512);
                     }
                 } else {
                     // rows that no query of the block sees are filled with zeros
 #pragma unroll
                     for (int c = 0; c < C::kCopies; ++c) {
                         const int key = k0 + (c * 32 + lane) / C::kChunks;
-                        const bool take = key < ld.kv_end && (key >= ld.w_lo || key < sinks);
-                        cp_async16(dst + copy_to(c), ks + c * 512, take);
-                        cp_async16(dst + C::kKeys * C::kRowBytes + copy_to(c), vs + c * 512, take);
+                        const bool take = key < w.x && (key >= w.y || key < sinks);
+                        cp_async16(kd + copy_to(c), ks + c * 512, take);
+                        cp_async16(vd + copy_to(c), vs + c * 512, take);
                     }
                 }
-                if (CT == kE4m3 && lane < 2)
-                    cp_async4(scales_a + ((ld_stage * C::kTiles + m) * 2 + lane) * 4,
-                              (lane ? p.v_scale : p.k_scale) + ((uint64_t)(uint32_t)id * (uint32_t)p.Hkv + ld.hk));
             }
+            sc_slot = ld_stage * C::kTiles;
+            sc_lane = first;
             if (++ld_i == ld_n) {
                 ld_x = ld.next;
                 enter();
