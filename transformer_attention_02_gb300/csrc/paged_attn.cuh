@@ -201,19 +201,25 @@ __device__ __forceinline__ KeyList key_list(const AttendParams& p, int b, bool& 
 
 // The schedule. Every non-empty segment counts its units and, where the CTAs
 // have several units each, kLead more for what a CTA pays to begin a segment
-// (its queries, the merge of the one before); CTA c takes the positions
-// [total c / ctas, total (c + 1) / ctas) of all segments end to end. With few
+// (its queries, the merge of the one before); each CTA takes an equal range of
+// the positions of all segments, end to end. With few
 // units there is no lead and no more CTAs than units. Either way every CTA
 // between a segment's first and last one holds a part of it.
-constexpr int kLead = 2;
+constexpr int kLead = 4;
 __device__ __forceinline__ int lead_of(const AttendParams& p, int units) { return units >= 8 * p.ctas ? kLead : 0; }
 __device__ __forceinline__ int span_of(int units, int lead) { return units > 0 ? units + lead : 0; }
 __device__ __forceinline__ int working_ctas(const AttendParams& p, int total) { return min(p.ctas, total); }
-__device__ __forceinline__ int unit_start(int total, int ctas, int cta) { return (int)((long long)total * cta / ctas); }
-// The CTA whose range holds position x.
-__device__ __forceinline__ int unit_owner(int total, int ctas, int x) {
-    return (int)((((long long)x + 1) * ctas + total - 1) / total) - 1;
-}
+// (32-bit divisions: they stand on the path to the first copy.)
+struct Ranges {
+    int each, more;      // positions of a CTA; the first `more` CTAs have one more
+    __device__ __forceinline__ Ranges(int total, int ctas) : each(total / ctas), more(total - each * ctas) {}
+    __device__ __forceinline__ int start(int cta) const { return cta * each + min(cta, more); }
+    // The CTA whose range holds position x.
+    __device__ __forceinline__ int owner(int x) const {
+        const int big = more * (each + 1);
+        return x < big ? x / (each + 1) : more + (x - big) / each;
+    }
+};
 
 // One segment's share of a CTA: units [u0, u1) of the key list of row block rb
 // of K/V head hk of sequence b.
@@ -251,10 +257,10 @@ __device__ __forceinline__ bool locate(const AttendParams& p, int segs, int lead
         if (s.u1 > s.u0) break;
         x = s.next;
     }
-    s.hk = seg / p.row_blocks;
+    s.hk = p.row_blocks == 1 ? seg : seg / p.row_blocks;
     s.rb = seg - s.hk * p.row_blocks;
     const int r0 = s.rb * ROWS;
-    const int i0 = r0 / p.group, i1 = min(min(p.rows - 1, r0 + ROWS - 1) / p.group, s.list.ql - 1);
+    const int i0 = r0 == 0 ? 0 : r0 / p.group, i1 = min(p.Sq == 1 ? 0 : min(p.rows - 1, r0 + ROWS - 1) / p.group, s.list.ql - 1);
     s.pos_lo = s.list.kv - s.list.ql + i0;
     s.pos_hi = s.list.kv - s.list.ql + i1;
     s.kv_end = i0 < s.list.ql ? max(0, s.pos_hi + 1) : 0;
@@ -324,9 +330,10 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     mine = (mine + mine_n * lead) * segs;
     total = (total + total_n * lead) * segs;
     const int ctas = working_ctas(p, total);
+    const Ranges ranges(total, max(ctas, 1));
     const bool works = (int)blockIdx.x < ctas;
-    const int x = works ? unit_start(total, ctas, blockIdx.x) : total;
-    const int x_end = works ? unit_start(total, ctas, blockIdx.x + 1) : total;
+    const int x = works ? ranges.start(blockIdx.x) : total;
+    const int x_end = works ? ranges.start(blockIdx.x + 1) : total;
     const bool note = blockIdx.x == 0 && p.B > kScanInMerge;      // the merge reads the offsets of a large batch
     if (note || (before <= x && x < before + mine)) {
         int at = before;
@@ -947,9 +954,10 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const AttendParams p, 
     let_next_start();
     int c0 = 0, c1 = 0;
     if (units > 0) {
-        const int ctas = working_ctas(p, total), span = units + lead;
-        c0 = unit_owner(total, ctas, first + seg * span + lead);
-        c1 = unit_owner(total, ctas, first + (seg + 1) * span - 1);
+        const int span = units + lead;
+        const Ranges ranges(total, working_ctas(p, total));
+        c0 = ranges.owner(first + seg * span + lead);
+        c1 = ranges.owner(first + (seg + 1) * span - 1);
         if (c0 == c1) return;
     }
     const int hk = seg / p.row_blocks, rb = seg - hk * p.row_blocks;
