@@ -93,9 +93,9 @@ long long span_bound(long long max_keys) { return (max_keys + paged::kUnit - 1) 
 
 // CTAs of the attention: as many as the device holds at once, or as the longest
 // lists could give work to (max_keys 0: any length).
-int attend_ctas(int B, int Hkv, int rows, int D, long long max_keys, int sms) {
+int attend_ctas(int B, int Hkv, int rows, int D, int cache, long long max_keys, int sms) {
     const int rb = paged::block_rows(rows);
-    const long long all = (long long)sms * paged::resident_ctas(D, rb);
+    const long long all = (long long)sms * paged::resident_ctas(D, rb, cache);
     if (max_keys <= 0) return (int)all;
     const long long segments = (long long)B * Hkv * ((rows + rb - 1) / rb);
     return (int)std::min(all, segments > all ? all : segments * span_bound(max_keys));
@@ -134,7 +134,8 @@ int attend_impl(const void* q, long long q_stride, const void* k_cache, const vo
     if ((long long)B * Hkv * row_blocks > 0x7fffffffLL / span_bound(max_keys)) return ATTN_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, kWorkspaceAlign)) return ATTN_ERR_INVALID_ARG;
     size_t part_off = 0;
-    const int ctas = attend_ctas(B, Hkv, (int)rows, D, max_keys, device_sm_count());
+    const int type = e4m3 ? paged::kE4m3 : bf16 ? paged::kBf16 : paged::kF16;
+    const int ctas = attend_ctas(B, Hkv, (int)rows, D, type, max_keys, device_sm_count());
     if (workspace_bytes < attend_workspace(B, (int)rows, D, ctas, &part_off)) return ATTN_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !std::isfinite(scale)) scale = 1.0f / std::sqrt((float)D);
 
@@ -205,7 +206,8 @@ size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, long lo
     if ((long long)Sq * (Hq / Hkv) > (1 << 30)) return 0;
     size_t part_off = 0;
     const int rows = Sq * (Hq / Hkv);
-    return attend_workspace(B, rows, D, attend_ctas(B, Hkv, rows, D, max_keys, device_sm_count()), &part_off);
+    // (the 16-bit cache's CTAs are the more, where the two differ)
+    return attend_workspace(B, rows, D, attend_ctas(B, Hkv, rows, D, paged::kBf16, max_keys, device_sm_count()), &part_off);
 }
 
 int attn_fwd_paged(const void* q, long long q_stride, const void* k_cache, const void* v_cache, const float* k_scale,

@@ -104,7 +104,9 @@ struct AttendParams {
 inline int block_rows(int rows) { return rows <= 24 ? (rows <= 8 ? 8 : rows <= 16 ? 16 : 24) : 32; }
 
 // CTAs of the attention kernel that fit on an SM at once.
-constexpr int resident_ctas(int D, int rows_per_block) { return D * rows_per_block <= 2048 ? 2 : 1; }
+constexpr int resident_ctas(int D, int rows_per_block, int cache) {
+    return (D == 64 ? rows_per_block <= 24 || cache != kE4m3 : rows_per_block <= 16) ? 2 : 1;
+}
 
 // The attention and the merge of its parts, for one cache type CT (kBf16,
 // kF16, kE4m3). attr_set caches, per context and instance [D is 128][rows of a
