@@ -32,11 +32,15 @@ namespace {
 __host__ __device__ constexpr int max_threads(int held) { return held == 4 ? 256 : 512; }
 __host__ __device__ constexpr int min_ctas(int held) { return held == 4 ? 3 : 1; }
 
-// Two floats to two e4m3 codes (round to nearest even, beyond +-448 to +-448,
-// NaN stays NaN); `lo` in the low byte.
-__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+// Four floats to four e4m3 codes (round to nearest even, beyond +-448 to
+// +-448, NaN stays NaN), the first in the low byte.
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
     return r;
 }
 
@@ -123,13 +127,15 @@ __global__ void __launch_bounds__(max_threads(HELD), min_ctas(HELD)) append_kern
     // one is worked on.
     const uint16_t* const src_t = src + (threadIdx.x >> cshift) * stride + 8 * (threadIdx.x & (chunks - 1));
     const long long apart = (blockDim.x >> cshift) * stride;
+    auto there = [&](int c) { return c < n; };
     uint4 w[HELD];
     auto fetch = [&](int h) {
+        const uint16_t* const at = src_t + h * p.D;
 #pragma unroll
         for (int i = 0; i < HELD; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
             w[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (c < n) w[i] = __ldg(reinterpret_cast<const uint4*>(src_t + i * apart + h * p.D));
+            if (there(c)) w[i] = __ldg(reinterpret_cast<const uint4*>(at + i * apart));
         }
     };
     fetch(h0);
@@ -148,7 +154,7 @@ __global__ void __launch_bounds__(max_threads(HELD), min_ctas(HELD)) append_kern
                 x[i][2 * e] = f.x;
                 x[i][2 * e + 1] = f.y;
             }
-            if (turn && c < n) {
+            if (turn && there(c)) {
                 const float4 a0 = __ldg(table + 2 * c), a1 = __ldg(table + 2 * c + 1);
                 const float cs[4] = {a0.x, a0.z, a1.x, a1.z}, sn[4] = {a0.y, a0.w, a1.y, a1.w};
 #pragma unroll
@@ -171,7 +177,7 @@ __global__ void __launch_bounds__(max_threads(HELD), min_ctas(HELD)) append_kern
                 for (int e = 0; e < 4; ++e)
                     r[e] = BF16 ? ptx::pack_bf16x2(x[i][2 * e], x[i][2 * e + 1])
                                   : ptx::pack_f16x2(x[i][2 * e], x[i][2 * e + 1]);
-                if (c < n) dst[c] = make_uint4(r[0], r[1], r[2], r[3]);
+                if (there(c)) dst[c] = make_uint4(r[0], r[1], r[2], r[3]);
             }
             continue;
         }
@@ -206,13 +212,11 @@ __global__ void __launch_bounds__(max_threads(HELD), min_ctas(HELD)) append_kern
                 for (int c = threadIdx.x; c < slot0 * chunks; c += blockDim.x) {
                     const uint2 w = old[c];
                     const uint32_t ws[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
-                    uint32_t r[4];
+                    float2 v2[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 v2 = from_e4m3x2(ws[i]);
-                        r[i] = to_e4m3x2(v2.x * f, v2.y * f);
-                    }
-                    old[c] = make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+                    for (int i = 0; i < 4; ++i) v2[i] = from_e4m3x2(ws[i]);
+                    old[c] = make_uint2(to_e4m3x4(v2[0].x * f, v2[0].y * f, v2[1].x * f, v2[1].y * f),
+                                        to_e4m3x4(v2[2].x * f, v2[2].y * f, v2[3].x * f, v2[3].y * f));
                 }
             }
         }
@@ -222,14 +226,11 @@ __global__ void __launch_bounds__(max_threads(HELD), min_ctas(HELD)) append_kern
 #pragma unroll
         for (int i = 0; i < HELD; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
-            uint32_t r[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float y0, y1;
-                ptx::mul2(y0, y1, x[i][2 * e], x[i][2 * e + 1], inv, inv);
-                r[e] = to_e4m3x2(y0, y1);
-            }
-            if (c < n) dst[c] = make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+            for (int e = 0; e < 8; e += 2) ptx::mul2(x[i][e], x[i][e + 1], x[i][e], x[i][e + 1], inv, inv);
+            if (there(c))
+                dst[c] = make_uint2(to_e4m3x4(x[i][0], x[i][1], x[i][2], x[i][3]),
+                                    to_e4m3x4(x[i][4], x[i][5], x[i][6], x[i][7]));
         }
     }
 }
@@ -240,7 +241,7 @@ int launch_append(AppendParams p, int cache, int num_sms, cudaStream_t stream) {
     // Heads a CTA takes in turn: table entries are read once per group, but only
     // where the blocks fill the SMs several times over without it.
     const long long blocks = (long long)p.B * p.touched * p.Hkv * 2;
-    p.head_group = (int)std::max(1LL, std::min<long long>(std::min(p.Hkv, 8), blocks / (8LL * num_sms)));
+    p.head_group = (int)std::max(1LL, std::min<long long>(std::min(p.Hkv, 4), blocks / (8LL * num_sms)));
     const int groups = (p.Hkv + p.head_group - 1) / p.head_group;
     const unsigned grid = (unsigned)((long long)p.B * p.touched * groups * 2);
     const int pieces = std::min(p.S, 1 << p.page_shift) * (p.D / 8);
