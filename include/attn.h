@@ -470,11 +470,18 @@ int attn_kv_append_f16(const void *k, const void *v, long long k_stride, long lo
  *               and rounded to their type, as attn_fwd_rope does; or NULL
  *   workspace   device scratch of attn_paged_workspace_bytes(...) bytes, 256-byte
  *               aligned, contents overwritten; its size does not depend on
- *               kv_lens. Calls, or replays of captured calls, that may run at the
+ *               kv_lens. A larger one is fine. Calls, or replays of captured calls, that may run at the
  *               same time need one each.
  * Two launches: the attention, whose CTAs take equal shares of all visible keys,
  * and the merge of the keys that several CTAs shared. Bound by the cache's reads
  * up to 32 query rows (Sq * Hq / Hkv) a K/V head; more rows read it once per 32.
+ * Long chunks (Sq of 128 and more, with B * Hq * ceil(Sq / 256) of 48 and more)
+ * go another way when the workspace holds the gathered tensors: the pages that
+ * are seen are copied into contiguous tensors of q's type (code * scale, rounded;
+ * exact in bf16 for the append's scales), and the fused kernel of attn_fwd reads
+ * those. Its weights are rounded to q's type, where the other path rounds them
+ * to fp16 over an 8-bit cache; keys of a page out of range read as zeros there,
+ * and are hidden here.
  */
 int attn_fwd_paged(const void *q, long long q_stride, const void *k_cache, const void *v_cache,
                    const float *k_scale, const float *v_scale,
@@ -491,8 +498,9 @@ int attn_fwd_paged_f16(const void *q, long long q_stride, const void *k_cache, c
 
 /* attn_paged_workspace_bytes — workspace bytes attn_fwd_paged needs for these
  * sizes on the current device (host only; 0 for an empty problem or invalid
- * sizes). max_keys: max_pages * page of the call, which bounds the work of short
- * tables, or 0: enough for any table. */
+ * sizes). max_keys: max_pages * page of the call. It bounds the work of short
+ * tables, and for long chunks the result then holds the gathered tensors (up to
+ * 4 GiB); 0: enough for any table, without them. */
 size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, long long max_keys);
 
 /*

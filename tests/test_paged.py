@@ -538,3 +538,95 @@ def test_batches_past_256_sequences_and_many_segments_a_cta():
     for b in range(0, B, 41):
         row.table_np = table[b:b + 1].cpu().numpy()
         _check_attention(row, q[b:b + 1], q[b:b + 1], o[b:b + 1], lse[b:b + 1], [kv[b]], [1], label=f"row {b}")
+
+
+# ------------------------------------------------------- long chunks of queries
+
+CHUNKS = [
+    # Hq, Hkv, D, page, kv_lens, q_lens, Sq, window, sinks, rope
+    (48, 8, 128, 64, [128], [128], 128, 0, 0, False),               # a prompt of its own
+    (8, 2, 64, 16, [700, 130, 0, 40], [300, 130, 0, 7], 300, 0, 0, True),    # ragged; tiles without a query
+    (12, 4, 128, 32, [1000, 333], [200, 333], 333, 150, 5, True),   # window and sinks
+    (8, 1, 64, 256, [100, 600], [140, 600], 600, 0, 0, False),      # more queries than keys: rows without one
+    (24, 8, 128, 16, [401, 500], [128, 200], 200, 129, 140, True),  # sinks over two blocks
+]
+
+
+@pytest.mark.parametrize("dt", [BF, FP], ids=["bf16", "f16"])
+@pytest.mark.parametrize("e4m3", [True, False], ids=["e4m3", "16bit"])
+@pytest.mark.parametrize("case", CHUNKS, ids=lambda c: "H{}-{}_D{}_p{}_{}_{}_w{}s{}".format(*c[:6], *c[7:9]))
+def test_long_chunks(case, dt, e4m3):
+    """By the gathered pages (the default workspace) and, with the small workspace, by the cache itself."""
+    Hq, Hkv, D, page, kv, ql, Sq, window, sinks, rope = case
+    B, pages = len(kv), -(-max(max(kv), Sq) // page) + 1
+    c = Cache(B, Hkv, D, page, pages, dt, e4m3, seed=sum(kv))
+    for b in range(B):
+        c.fill(b, kv[b], b)
+    q = _rand((B, Sq, Hq, D), dt, 90)
+    table = A.rope_table(pages * page, D) if rope else None
+    rot = q.clone()
+    for b in range(B):
+        if rope and ql[b]:
+            rot[b, :ql[b]] = A.rope_apply(q[b:b + 1, :ql[b]].contiguous(), table, pos0=kv[b] - ql[b])[0]
+    small = torch.empty(A.attn_paged_workspace_bytes(B, Hq, Hkv, Sq, D), dtype=torch.uint8, device=DEV)
+    full = A.attn_paged_workspace_bytes(B, Hq, Hkv, Sq, D, pages * page)
+    assert full >= 2 * B * pages * page * Hkv * D * 2
+    # the gathered path rounds the weights to the queries' type, the other one to fp16 over an 8-bit cache; a workspace
+    # that holds the gathered tensors takes the first
+    by_cache = R.step(dt) if c.ks is None or small.numel() >= full else R.step(FP)
+    for ws, p_step in ((None, R.step(dt)), (small, by_cache)):
+        o, lse = torch.full_like(q, 5.0), torch.full((B, Hq, Sq), 5.0, device=DEV)
+        A.attention_paged(q, c.k, c.v, c.table, _i32(kv), q_lens=_i32(ql), table=table, window=window, sinks=sinks, out=o,
+                          lse=lse, workspace=ws, **c.scales)
+        assert _status() == A.ATTN_OK
+        for b in range(B):
+            assert bool((o[b, ql[b]:] == 5.0).all()) and bool((lse[b, :, ql[b]:] == 5.0).all())
+            if ql[b]:
+                pos = np.arange(kv[b] - ql[b], kv[b])
+                k, v = (R.tokens(x, s, c.table_np[b], kv[b], page) for x, s in ((c.k, c.ks), (c.v, c.vs)))
+                want = R.attend(R.f64(rot[b, :ql[b]]), k, v, pos, D ** -0.5, window, sinks)
+                R.check_rows(R.f64(o[b, :ql[b]]), R.f64(lse[b, :, :ql[b]]), want, R.step(dt), p_step, D, kv[b],
+                             _v_top(c, c.table_np[b, :max(1, -(-kv[b] // page))]), f"{case} {ws is None} b={b}")
+
+
+def test_long_chunk_leaves_out_what_is_out_of_range():
+    c = Cache(2, 2, 64, 16, 20, FP, False)
+    c.fill(0, 300, 0), c.fill(1, 300, 1)
+    q = _rand((2, 128, 24, 64), FP, 91)
+    want = A.attention_paged(q, c.k, c.v, c.table, _i32([300, 300]))
+    c.table[1, 3] = -7
+    o, lse = A.attention_paged(q, c.k, c.v, c.table, _i32([300, 300]))
+    assert _status() == A.ATTN_ERR_BAD_INDEX and bool(torch.isfinite(o).all())
+    assert torch.equal(o[0], want[0][0]) and torch.equal(lse[0], want[1][0])
+    o, lse = A.attention_paged(q, c.k, c.v, c.table, _i32([-1, 1 << 29]), q_lens=_i32([128, 500]))
+    assert _status() == A.ATTN_ERR_BAD_INDEX
+    assert bool((o[0] == 0).all()) and bool((lse[0] == float("-inf")).all())
+
+
+def test_long_chunk_of_a_packed_projection_in_a_graph():
+    B, S, Hq, Hkv, D, page = 2, 160, 24, 2, 64, 32
+    c = Cache(B, Hkv, D, page, 16, BF, True)
+    table, kv = A.rope_table(512, D), _i32([160, 160])
+    qkv = _rand((B, S, (Hq + 2 * Hkv) * D), BF, 92)
+    q, k, v = (t.unflatten(-1, (-1, D)) for t in qkv.split([Hq * D, Hkv * D, Hkv * D], dim=-1))
+
+    def step():
+        A.kv_append(k, v, c.k, c.v, c.table, kv, table=table, **c.scales)
+        return A.attention_paged(q, c.k, c.v, c.table, kv, table=table, **c.scales)
+
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    kv.copy_(_i32([400, 161]))
+    for b in range(B):
+        c.fill(b, [240, 1][b], 50 + b)
+    g.replay()
+    torch.cuda.synchronize()
+    rot = torch.stack([A.rope_apply(q[b:b + 1].contiguous(), table, pos0=[240, 1][b])[0] for b in range(B)])
+    for b in range(B):
+        L = [400, 161][b]
+        kk, vv = (R.tokens(x, s, c.table_np[b], L, page) for x, s in ((c.k, c.ks), (c.v, c.vs)))
+        want = R.attend(R.f64(rot[b]), kk, vv, np.arange(L - S, L), D ** -0.5, 0, 0)
+        R.check_rows(R.f64(out[0][b]), R.f64(out[1][b]), want, R.step(BF), R.step(BF), D, L, _v_top(c, c.table_np[b, :13]),
+                     f"graph b={b}")

@@ -79,6 +79,13 @@ def test_workspace_size():
     assert A.attn_paged_workspace_bytes(1, 32, 8, 1, 128, 577) == 256 + 8 * (5 + 4) * 2 * 8 * 130 * 4
     assert A.attn_paged_workspace_bytes(16, 32, 8, 1, 128, 8192) == A.attn_paged_workspace_bytes(16, 32, 8, 1, 128)
     assert A.attn_paged_workspace_bytes(16, 32, 8, 1, 128, -1) == 0
+    # long chunks (128 queries, 48 tiles): gathered keys and values, then the queries; else, or past 4 GiB, as above
+    assert A.attn_paged_workspace_bytes(2, 32, 8, 128, 64, 1000 * 16) == 2 * (2 * 16000 * 8 * 64 * 2) + 2 * 128 * 32 * 64 * 2
+    few = 256 + 148 * 2 * 2 * 32 * 66 * 4
+    assert A.attn_paged_workspace_bytes(2, 32, 8, 128, 64) == few
+    assert A.attn_paged_workspace_bytes(2, 32, 8, 127, 64, 1000 * 16) == few
+    assert A.attn_paged_workspace_bytes(1, 32, 8, 256, 64, 1000 * 16) == few
+    assert A.attn_paged_workspace_bytes(64, 32, 8, 128, 64, 1 << 20) == few + 256       # (66 offsets: 512 bytes)
     assert A.attn_paged_workspace_bytes(0, 32, 8, 1, 128) == 0
     assert A.attn_paged_workspace_bytes(1, 30, 8, 1, 128) == 0
     assert A.attn_paged_workspace_bytes(1, 32, 8, 1, 96) == 0

@@ -652,6 +652,9 @@ def _paged_workspace_size(at, B, Hq, Hkv, Sq, D, max_keys):
     return _lib.attn_paged_workspace_bytes(B, Hq, Hkv, Sq, D, max_keys) or 1      # (device `at` is current)
 
 
+_HELD_BYTES = 32 << 20                              # larger workspaces (long chunks of queries) are a call's own
+
+
 class _Held(threading.local):
     """Workspace of a thread's calls on a device's default stream, as {device: (tensor, address, bytes)}. Calls of one
     thread on one stream run in order, so they may share it; another thread could enqueue between a call's two kernels,
@@ -666,7 +669,7 @@ _held = _Held()
 
 def _workspace(q, at, size, handle, stream):
     """(address, bytes, the tensor to keep until the call is enqueued)."""
-    if handle or _torch.cuda.is_current_stream_capturing():
+    if handle or size > _HELD_BYTES or _torch.cuda.is_current_stream_capturing():
         t = _new(size, _torch.uint8, q, stream)
         return t.data_ptr(), size, t
     held = _held.by_device.get(at)

@@ -21,7 +21,7 @@ OBJDIR = os.path.join(HERE, "_build")
 SOURCES = [os.path.join(CSRC, f) for f in
            ("attn_api.cu", "attn_host.cu", "block_kernels.cu", "fwd_bf16.cu", "fwd_f16.cu", "fwd_rope_bf16.cu",
             "fwd_rope_f16.cu", "fwd_pack_bf16.cu", "fwd_pack_f16.cu", "fwd_window_bf16.cu",
-            "fwd_window_f16.cu", "paged_api.cu", "paged_append.cu",
+            "fwd_window_f16.cu", "paged_api.cu", "paged_append.cu", "paged_gather.cu",
             "paged_attn_bf16.cu", "paged_attn_f16.cu", "paged_attn_e4m3.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in
                      ("attn_kernel.cuh", "ptx.cuh", "attn_launch.h", "attn_fwd_inst.cuh", "block_params.h",

@@ -47,7 +47,7 @@ struct DeviceInfo {
     int num_sms = 0;
     unsigned int* status = nullptr;     // device address of g_device_status
     void* noalloc_scratch = nullptr;    // device address of the allocation-free scratch array
-    bool smem_attr_set[2][4][2][4] = {};   // [D is 128][mask kind][bf16][plain, rotary, packed, windowed]
+    bool smem_attr_set[2][4][2][5] = {};   // [D is 128][mask kind][bf16][plain, rotary, packed, windowed, ragged]
     bool gemm_attr_set = false;
     bool ln_attr_set[3] = {};
     bool paged_attr_set[3][2][4] = {};     // [cache type][D is 128][rows of a block]
@@ -236,10 +236,11 @@ int launch_d(DeviceInfo& dev, int mask_kind, const CUtensorMap& tq, const CUtens
 }
 
 template <int D, bool BF16>
-int launch_window(DeviceInfo& dev, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+int launch_window(DeviceInfo& dev, bool ragged, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                   const CUtensorMap& to, const attn::FwdParams& p, int grid, cudaStream_t stream) {
-    bool& attr = dev.smem_attr_set[D == 128][ATTN_MASK_CAUSAL][BF16 ? 1 : 0][3];
-    return attn::launch_fwd<D, true, false, BF16, false, false, true>(attr, tq, tk, tv, to, p, grid, stream);
+    bool& attr = dev.smem_attr_set[D == 128][ATTN_MASK_CAUSAL][BF16 ? 1 : 0][ragged ? 4 : 3];
+    return ragged ? attn::launch_fwd<D, true, false, BF16, false, false, true, true>(attr, tq, tk, tv, to, p, grid, stream)
+                  : attn::launch_fwd<D, true, false, BF16, false, false, true>(attr, tq, tk, tv, to, p, grid, stream);
 }
 
 template <bool BF16, bool ROPE, bool PACK>
@@ -391,10 +392,13 @@ struct RopeArgs {
     void* k_rot;          // receives the rotated keys, or null: k already holds rotated keys
 };
 
-// Sliding window of attn_fwd_window / attn_fwd_window_f16.
+// Sliding window of attn_fwd_window / attn_fwd_window_f16, and the lengths of a
+// ragged batch.
 struct WindowArgs {
     int window;           // keys a query sees, its own included
     int sinks;            // first tokens that stay visible
+    const int* kv_lens = nullptr;      // (B) device, or null: Sk and Sq for every sequence
+    const int* q_lens = nullptr;       // (B) device, or null: Sq
 };
 
 bool rope_args_ok(const RopeArgs& r, int Sq, int Sk) {
@@ -547,6 +551,10 @@ int attn_fwd_impl(const void* q, const void* k, const void* v, void* o, float* l
     if (win) {
         p.q_pos0 = win->window;
         p.mask_vec4 = win->sinks;
+        if (win->kv_lens) {
+            p.mask = reinterpret_cast<const float*>(win->kv_lens);
+            p.rope = reinterpret_cast<const float*>(win->q_lens);
+        }
     }
 
     // One CTA per work tile. At most one CTA fits on an SM; the running CTAs
@@ -555,10 +563,10 @@ int attn_fwd_impl(const void* q, const void* k, const void* v, void* o, float* l
     // longest-first schedule.
     const int grid = p.n_tiles;
     if (win)
-        rc = D == 128 ? (bf16 ? launch_window<128, true>(*dev, tq, tk, tv, to, p, grid, stream)
-                              : launch_window<128, false>(*dev, tq, tk, tv, to, p, grid, stream))
-                      : (bf16 ? launch_window<64, true>(*dev, tq, tk, tv, to, p, grid, stream)
-                              : launch_window<64, false>(*dev, tq, tk, tv, to, p, grid, stream));
+        rc = D == 128 ? (bf16 ? launch_window<128, true>(*dev, win->kv_lens, tq, tk, tv, to, p, grid, stream)
+                              : launch_window<128, false>(*dev, win->kv_lens, tq, tk, tv, to, p, grid, stream))
+                      : (bf16 ? launch_window<64, true>(*dev, win->kv_lens, tq, tk, tv, to, p, grid, stream)
+                              : launch_window<64, false>(*dev, win->kv_lens, tq, tk, tv, to, p, grid, stream));
     else if (rope)
         rc = bf16 ? launch_any<true, true, false>(*dev, D, mask_kind, tq, tk, tv, to, p, grid, stream)
                   : launch_any<false, true, false>(*dev, D, mask_kind, tq, tk, tv, to, p, grid, stream);
@@ -662,6 +670,14 @@ int window_impl(const void* q, const void* k, const void* v, void* o, float* lse
 }
 
 }  // namespace
+
+int attn::launch_ragged(const void* q, long long q_stride, const void* k, const void* v, void* o, float* lse, int B, int Hq,
+                        int Hkv, int Sq, int Sk, int D, float scale, int window, int sinks, const int* kv_lens,
+                        const int* q_lens, cudaStream_t stream, bool bf16) {
+    const WindowArgs w{window, sinks, kv_lens, q_lens};
+    return attn_fwd_impl(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, scale, ATTN_MASK_CAUSAL, nullptr, stream, bf16, 1, nullptr,
+                         0, nullptr, q_stride, 0, &w);
+}
 
 extern "C" {
 

@@ -9,10 +9,10 @@
 
 namespace attn {
 
-template <int D, bool CAUSAL, bool ADDITIVE, bool BF16, bool ROPE, bool PACK, bool WINDOW>
+template <int D, bool CAUSAL, bool ADDITIVE, bool BF16, bool ROPE, bool PACK, bool WINDOW, bool RAGGED>
 int launch_fwd(bool& attr_set, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                const CUtensorMap& to, const FwdParams& p, int grid, cudaStream_t stream) {
-    auto kernel = attn_fwd_kernel<D, CAUSAL, ADDITIVE, BF16, ROPE, PACK, WINDOW>;
+    auto kernel = attn_fwd_kernel<D, CAUSAL, ADDITIVE, BF16, ROPE, PACK, WINDOW, RAGGED>;
     constexpr int smem = TileCfg<D>::kSmemBytes;
     if (!attr_set) {
         // The in-kernel register split assumes exactly launch_regs(ROPE) per thread at launch.
@@ -29,22 +29,23 @@ int launch_fwd(bool& attr_set, const CUtensorMap& tq, const CUtensorMap& tk, con
 
 }  // namespace attn
 
-#define ATTN_INSTANTIATE_ONE(D, CAUSAL, ADDITIVE, BF16, ROPE, PACK, WINDOW)                                      \
-    template int attn::launch_fwd<D, CAUSAL, ADDITIVE, BF16, ROPE, PACK, WINDOW>(                                \
+#define ATTN_INSTANTIATE_ONE(D, CAUSAL, ADDITIVE, BF16, ROPE, PACK, WINDOW, RAGGED)                              \
+    template int attn::launch_fwd<D, CAUSAL, ADDITIVE, BF16, ROPE, PACK, WINDOW, RAGGED>(                        \
         bool&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,                      \
         const attn::FwdParams&, int, cudaStream_t);
 
-#define ATTN_INSTANTIATE_FWD(BF16, ROPE, PACK)                         \
-    ATTN_INSTANTIATE_ONE(64, false, false, BF16, ROPE, PACK, false)    \
-    ATTN_INSTANTIATE_ONE(64, true, false, BF16, ROPE, PACK, false)    \
-    ATTN_INSTANTIATE_ONE(64, false, true, BF16, ROPE, PACK, false)    \
-    ATTN_INSTANTIATE_ONE(64, true, true, BF16, ROPE, PACK, false)    \
-    ATTN_INSTANTIATE_ONE(128, false, false, BF16, ROPE, PACK, false)    \
-    ATTN_INSTANTIATE_ONE(128, true, false, BF16, ROPE, PACK, false)    \
-    ATTN_INSTANTIATE_ONE(128, false, true, BF16, ROPE, PACK, false)    \
-    ATTN_INSTANTIATE_ONE(128, true, true, BF16, ROPE, PACK, false)
+#define ATTN_INSTANTIATE_FWD(BF16, ROPE, PACK)                                \
+    ATTN_INSTANTIATE_ONE(64, false, false, BF16, ROPE, PACK, false, false)  \
+    ATTN_INSTANTIATE_ONE(64, true, false, BF16, ROPE, PACK, false, false)  \
+    ATTN_INSTANTIATE_ONE(64, false, true, BF16, ROPE, PACK, false, false)  \
+    ATTN_INSTANTIATE_ONE(64, true, true, BF16, ROPE, PACK, false, false)  \
+    ATTN_INSTANTIATE_ONE(128, false, false, BF16, ROPE, PACK, false, false)  \
+    ATTN_INSTANTIATE_ONE(128, true, false, BF16, ROPE, PACK, false, false)  \
+    ATTN_INSTANTIATE_ONE(128, false, true, BF16, ROPE, PACK, false, false)  \
+    ATTN_INSTANTIATE_ONE(128, true, true, BF16, ROPE, PACK, false, false)
 
-// The windowed variants: causal with a sliding window and sinks.
-#define ATTN_INSTANTIATE_WINDOW(BF16)                                   \
-    ATTN_INSTANTIATE_ONE(64, true, false, BF16, false, false, true)     \
-    ATTN_INSTANTIATE_ONE(128, true, false, BF16, false, false, true)
+// The windowed variants: causal with a sliding window and sinks, over tensors of
+// one length or (RAGGED) with the lengths of every sequence read on the device.
+#define ATTN_INSTANTIATE_WINDOW(BF16, RAGGED)                                   \
+    ATTN_INSTANTIATE_ONE(64, true, false, BF16, false, false, true, RAGGED)     \
+    ATTN_INSTANTIATE_ONE(128, true, false, BF16, false, false, true, RAGGED)

@@ -53,7 +53,7 @@ namespace attn {
 struct FwdParams {
     void* o;                  // (B, Sq, Hq, D) 16-bit
     float* lse;               // (B, Hq, Sq)
-    const float* mask;        // (B, Sq, Sk) FP32 or null
+    const float* mask;        // (B, Sq, Sk) FP32 or null; ragged variants: int32 (B) keys of every sequence
     int B, Hq, Hkv, Sq, Sk;
     int group;                // Hq / Hkv
     int n_mblk;               // ceil(Sq / 256)
@@ -69,7 +69,8 @@ struct FwdParams {
     int head_group;           // tile order: (b, head) slices per group (see tile_info)
     unsigned long long timeout_ns;
     unsigned int* status;     // device status word, bit 0 = a wait timed out
-    const float* rope;        // rotary table (max_pos, D/2, {cos, sin}) FP32 (rotating variant only)
+    const float* rope;        // rotary table (max_pos, D/2, {cos, sin}) FP32 (rotating variant);
+                              // ragged variants: int32 (B) queries of every sequence, or null: Sq
     int q_pos0;               // position of query row 0 (rotating variant); window length (windowed variants)
     // Kept last: inserting it earlier shifted the 64-bit fields after it and
     // measurably changed the code generated for the unpacked kernels.
@@ -161,6 +162,20 @@ struct TileCfg {
     static_assert(kTmemSlotOff % 4 == 0 && kAbortOff % 4 == 0, "4-byte words");
 };
 
+// Ragged variants (over a paged cache gathered into contiguous tensors): keys
+// and queries of sequence b, read on the device and cut to what the tensors
+// hold; elsewhere every sequence has Sk and Sq.
+struct Lens {
+    int kv, q;
+};
+template <bool RAGGED>
+__device__ __forceinline__ Lens lens_of(const FwdParams& p, int b) {
+    if (!RAGGED) return Lens{p.Sk, p.Sq};
+    const int* kv = reinterpret_cast<const int*>(p.mask);
+    const int* ql = reinterpret_cast<const int*>(p.rope);
+    return Lens{min(max(__ldg(kv + b), 0), p.Sk), ql ? min(max(__ldg(ql + b), 0), p.Sq) : p.Sq};
+}
+
 struct TileInfo {
     int b, h, hk, m0;  // h: the (first) query head; m0: the first query row
     int split;      // key range index; windowed variants: key blocks before the window's first
@@ -192,7 +207,7 @@ struct TileInfo {
 // Both sub-tiles walk the same list; the upper one, whose windows begin 128
 // keys later, passes over the window's first block unless sinks lie in it.
 constexpr int kSkipsFirst = 1 << 30;
-template <bool CAUSAL, bool PACK, bool WINDOW = false>
+template <bool CAUSAL, bool PACK, bool WINDOW = false, bool RAGGED = false>
 __device__ __forceinline__ TileInfo tile_info(int tile, const FwdParams& p) {
     const int ps = PACK ? p.pack_shift : 0;
     const int heads = PACK ? p.Hkv : p.Hq;
@@ -224,6 +239,7 @@ __device__ __forceinline__ TileInfo tile_info(int tile, const FwdParams& p) {
     }
     TileInfo t;
     t.b = bh / heads;
+    const Lens len = lens_of<RAGGED>(p, t.b);
     const int hh = bh - t.b * heads;
     t.h = PACK ? hh * p.group : hh;
     t.hk = PACK ? hh : hh / p.group;
@@ -232,9 +248,9 @@ __device__ __forceinline__ TileInfo tile_info(int tile, const FwdParams& p) {
     t.kb0 = split * p.split_blocks;
     int gap = 0, skips = 0;
     if (WINDOW) {
-        const int first = t.m0 + (p.Sk - p.Sq) - p.q_pos0 + 1;     // oldest key of the first row's window
+        const int first = t.m0 + (len.kv - len.q) - p.q_pos0 + 1;     // oldest key of the first row's window
         const int low = max(0, first) / kBlockN;
-        const int sink_blocks = (min(p.mask_vec4, p.Sk) + kBlockN - 1) / kBlockN;
+        const int sink_blocks = (min(p.mask_vec4, len.kv) + kBlockN - 1) / kBlockN;
         if (low >= sink_blocks) {
             t.split = sink_blocks;
             gap = low - sink_blocks;
@@ -242,13 +258,13 @@ __device__ __forceinline__ TileInfo tile_info(int tile, const FwdParams& p) {
         }
     }
     const int range_begin = t.kb0 * kBlockN;
-    const int range_end = min(p.Sk, range_begin + p.split_blocks * kBlockN);
+    const int range_end = min(len.kv, range_begin + p.split_blocks * kBlockN);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         const int first = t.m0 + s * sub_rows;
-        const int last = min(first + sub_rows - 1, p.Sq - 1);
+        const int last = min(first + sub_rows - 1, len.q - 1);
         int kv_end = range_begin;
-        if (first < p.Sq) kv_end = CAUSAL ? min(range_end, max(0, last + (p.Sk - p.Sq) + 1)) : range_end;
+        if (first < len.q) kv_end = CAUSAL ? min(range_end, max(0, last + (len.kv - len.q) + 1)) : range_end;
         t.nb[s] = kv_end > range_begin ? (kv_end - range_begin + kBlockN - 1) / kBlockN - gap : 0;
     }
     if (WINDOW) t.kb0 = gap | skips;
@@ -524,7 +540,7 @@ __device__ void role_rope_q(const FwdParams& p, uint32_t smem, uint8_t* smem_ptr
 // tile's upper one is done, and its upper sub-tile while the current tile's
 // last key block runs. (In the rotary variant warps 12-15 rotate each
 // sub-tile after it lands.)
-template <int D, bool CAUSAL, bool ADDITIVE, bool BF16, bool ROPE, bool PACK, bool WINDOW>
+template <int D, bool CAUSAL, bool ADDITIVE, bool BF16, bool ROPE, bool PACK, bool WINDOW, bool RAGGED>
 __device__ void role_qload(const CUtensorMap* tmQ, const CUtensorMap* tmO, const FwdParams& p, uint32_t smem,
                            uint8_t* smem_ptr, const SyncCtx& sc) {
     using C = TileCfg<D>;
@@ -576,7 +592,7 @@ __device__ void role_qload(const CUtensorMap* tmQ, const CUtensorMap* tmO, const
         int tile = 0;
         const int found = next_tile_index(tile);
         if (found < 0) return -1;
-        if (found) t = tile_info<CAUSAL, PACK, WINDOW>(tile, p);
+        if (found) t = tile_info<CAUSAL, PACK, WINDOW, RAGGED>(tile, p);
         if (!found) {
             t.b = t.h = t.hk = t.m0 = t.split = t.kb0 = 0;
             t.nb[0] = t.nb[1] = t.n = -1;
@@ -830,7 +846,7 @@ __device__ void role_mma(const FwdParams& p, uint32_t smem, const uint8_t* smem_
 }
 
 // ------------------------------------------------ softmax / epilogue warpgroup
-template <int D, bool CAUSAL, bool ADDITIVE, bool BF16, bool PACK, bool WINDOW>
+template <int D, bool CAUSAL, bool ADDITIVE, bool BF16, bool PACK, bool WINDOW, bool RAGGED>
 __device__ void role_softmax(const FwdParams& p, uint32_t smem, uint8_t* smem_ptr, uint32_t tmem, int wg,
                              const SyncCtx& sc) {
     using C = TileCfg<D>;
@@ -866,7 +882,8 @@ __device__ void role_softmax(const FwdParams& p, uint32_t smem, uint8_t* smem_pt
         const int ps = PACK ? p.pack_shift : 0;
         const int row = ti.m0 + ((wg * kBlockM + r) >> ps);                   // query row
         const int hd = PACK ? ti.h + (r & ((1 << ps) - 1)) : ti.h;            // query head
-        const bool row_ok = row < p.Sq;
+        const Lens len = lens_of<RAGGED>(p, ti.b);
+        const bool row_ok = row < len.q;
         uint16_t* orow = reinterpret_cast<uint16_t*>(p.o) + (((size_t)ti.b * p.Sq + row) * p.Hq + hd) * D;
         float* lse_out = p.lse + ((size_t)ti.b * p.Hq + hd) * p.Sq + row;
         // With split keys this tile's result goes to the FP32 partial buffers.
@@ -889,8 +906,8 @@ __device__ void role_softmax(const FwdParams& p, uint32_t smem, uint8_t* smem_pt
             continue;
         }
         // keys [0, kv_lim) are visible to this row
-        int kv_lim = p.Sk;
-        if (CAUSAL) kv_lim = min(p.Sk, max(0, row + (p.Sk - p.Sq) + 1));
+        int kv_lim = len.kv;
+        if (CAUSAL) kv_lim = min(len.kv, max(0, row + (len.kv - len.q) + 1));
         const float* mrow = nullptr;
         if (ADDITIVE && row_ok) mrow = p.mask + ((size_t)ti.b * p.Sq + row) * p.Sk;
 
@@ -966,7 +983,7 @@ __device__ void role_softmax(const FwdParams& p, uint32_t smem, uint8_t* smem_pt
                 }
                 if (WINDOW) {
                     // keys before the row's window are hidden, but for the sinks
-                    const int low = row + (p.Sk - p.Sq) - p.q_pos0 + 1 - key0, sink = p.mask_vec4 - key0;
+                    const int low = row + (len.kv - len.q) - p.q_pos0 + 1 - key0, sink = p.mask_vec4 - key0;
                     if (low > 0 && sink <= 0) {
 #pragma unroll
                         for (int c = 0; c < kBlockN; ++c)
@@ -1122,12 +1139,14 @@ __device__ void role_softmax(const FwdParams& p, uint32_t smem, uint8_t* smem_pt
 }
 
 // ------------------------------------------------------------------ kernel
-template <int D, bool CAUSAL, bool ADDITIVE, bool BF16, bool ROPE, bool PACK, bool WINDOW = false>
+template <int D, bool CAUSAL, bool ADDITIVE, bool BF16, bool ROPE, bool PACK, bool WINDOW = false,
+          bool RAGGED = false>
 __global__ void __launch_bounds__(kernel_threads(ROPE), 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                     const FwdParams p) {
     using C = TileCfg<D>;
+    static_assert(!RAGGED || WINDOW, "the ragged variants are windowed ones");
     static_assert(!WINDOW || (CAUSAL && !ADDITIVE && !ROPE && !PACK), "the window reuses fields of the other variants");
     extern __shared__ uint8_t smem_raw[];
     // Swizzled TMA tiles and the MMA descriptors both assume 1024-byte alignment.
@@ -1168,7 +1187,7 @@ __global__ void __launch_bounds__(kernel_threads(ROPE), 1)
 
     if (warp < 8) {
         ptx::setmaxnreg_inc<softmax_regs(ROPE)>();
-        role_softmax<D, CAUSAL, ADDITIVE, BF16, PACK, WINDOW>(p, smem, smem_ptr, tmem, warp >> 2, sc);
+        role_softmax<D, CAUSAL, ADDITIVE, BF16, PACK, WINDOW, RAGGED>(p, smem, smem_ptr, tmem, warp >> 2, sc);
     } else if (warp < kRotateWarp0) {
         ptx::setmaxnreg_dec<control_regs(ROPE)>();
         if (warp == kMmaWarp)
@@ -1176,7 +1195,7 @@ __global__ void __launch_bounds__(kernel_threads(ROPE), 1)
         else if (warp == kTmaWarp)
             role_tma<D, WINDOW>(&tmK, &tmV, smem, smem_ptr, sc);
         else if (warp == kQWarp)
-            role_qload<D, CAUSAL, ADDITIVE, BF16, ROPE, PACK, WINDOW>(&tmQ, &tmO, p, smem, smem_ptr, sc);
+            role_qload<D, CAUSAL, ADDITIVE, BF16, ROPE, PACK, WINDOW, RAGGED>(&tmQ, &tmO, p, smem, smem_ptr, sc);
         __syncwarp();
     } else {
         ptx::setmaxnreg_dec<kRotateRegs>();

@@ -108,6 +108,25 @@ size_t attend_workspace(int B, int rows, int D, int ctas, size_t* part_off) {
     return *part_off + (size_t)ctas * 2 * paged::block_rows(rows) * (D + 2) * sizeof(float);
 }
 
+// Workspace of a long chunk: gathered keys and values, then rotated queries.
+struct ChunkLayout {
+    int cap = 0;                       // keys a sequence
+    size_t v_off = 0, q_off = 0, total = 0;
+};
+
+// False where the gathered path does not apply (few queries or tiles, or too large).
+bool chunk_layout(int B, int Hq, int Hkv, int Sq, int D, long long max_keys, ChunkLayout* c) {
+    if (Sq < paged::kChunkRows || max_keys <= 0) return false;
+    if ((long long)B * Hq * ((Sq + 255) / 256) < paged::kChunkTiles) return false;
+    c->cap = (int)max_keys;
+    const double kv = 2.0 * B * c->cap * Hkv * D, q = 2.0 * B * Sq * Hq * D;
+    if (2 * kv + q > (double)paged::kChunkLimit || (double)B * (c->cap / 128 + 1) * Hkv + q / 16 / 256 > 2e9) return false;
+    c->v_off = align_up((size_t)kv);
+    c->q_off = 2 * c->v_off;
+    c->total = c->q_off + align_up((size_t)q);
+    return true;
+}
+
 int attend_impl(const void* q, long long q_stride, const void* k_cache, const void* v_cache, const float* k_scale,
                 const float* v_scale, const int* block_table, const int* kv_lens, const int* q_lens, void* o, float* lse,
                 int B, int Hq, int Hkv, int Sq, int D, int page, int max_pages, int n_pages, int cache, float scale,
@@ -134,14 +153,53 @@ int attend_impl(const void* q, long long q_stride, const void* k_cache, const vo
     if ((long long)B * Hkv * row_blocks > 0x7fffffffLL / span_bound(max_keys)) return ATTN_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, kWorkspaceAlign)) return ATTN_ERR_INVALID_ARG;
     size_t part_off = 0;
+    ChunkLayout chunk;
+    const bool gathered = chunk_layout(B, Hq, Hkv, Sq, D, max_keys, &chunk) && workspace_bytes >= chunk.total;
     const int type = e4m3 ? paged::kE4m3 : bf16 ? paged::kBf16 : paged::kF16;
     const int ctas = attend_ctas(B, Hkv, (int)rows, D, type, max_keys, device_sm_count());
-    if (workspace_bytes < attend_workspace(B, (int)rows, D, ctas, &part_off)) return ATTN_ERR_INVALID_ARG;
+    if (!gathered && workspace_bytes < attend_workspace(B, (int)rows, D, ctas, &part_off)) return ATTN_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !std::isfinite(scale)) scale = 1.0f / std::sqrt((float)D);
 
     DeviceState dev{};
     rc = device_state(&dev);
     if (rc != ATTN_OK) return rc;
+    if (gathered) {
+        char* const ws = static_cast<char*>(workspace);
+        paged::GatherParams g{};
+        g.k_cache = k_cache;
+        g.v_cache = v_cache;
+        g.k_scale = k_scale;
+        g.v_scale = v_scale;
+        g.block_table = block_table;
+        g.kv_lens = kv_lens;
+        g.q_lens = q_lens;
+        g.k_out = reinterpret_cast<uint16_t*>(ws);
+        g.v_out = reinterpret_cast<uint16_t*>(ws + chunk.v_off);
+        g.q = static_cast<const uint16_t*>(q);
+        g.q_stride = q_stride;
+        g.q_out = reinterpret_cast<uint16_t*>(ws + chunk.q_off);
+        g.rope = rope_table;
+        g.max_pos = max_pos;
+        g.B = B;
+        g.Sq = Sq;
+        g.Hq = Hq;
+        g.Hkv = Hkv;
+        g.D = D;
+        g.cap = chunk.cap;
+        g.page_shift = page_shift_of(page);
+        g.max_pages = max_pages;
+        g.n_pages = n_pages;
+        g.window = window;
+        g.sinks = sinks;
+        g.bf16 = bf16;
+        g.status = dev.status;
+        rc = paged::launch_gather(g, type, stream);
+        if (rc != ATTN_OK) return rc;
+        constexpr int kNoWindow = 1 << 30;
+        return launch_ragged(rope_table ? g.q_out : q, rope_table ? (long long)Hq * D : q_stride, g.k_out, g.v_out, o, lse, B,
+                             Hq, Hkv, Sq, chunk.cap, D, scale, window > 0 ? std::min(window, kNoWindow) : kNoWindow,
+                             window > 0 ? sinks : 0, kv_lens, q_lens, stream, bf16);
+    }
     paged::AttendParams p{};
     p.q = static_cast<const uint16_t*>(q);
     p.q_stride = q_stride;
@@ -206,6 +264,8 @@ size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, long lo
     if ((long long)Sq * (Hq / Hkv) > (1 << 30)) return 0;
     size_t part_off = 0;
     const int rows = Sq * (Hq / Hkv);
+    ChunkLayout chunk;
+    if (chunk_layout(B, Hq, Hkv, Sq, D, max_keys, &chunk)) return chunk.total;
     // (the 16-bit cache's CTAs are the more, where the two differ)
     return attend_workspace(B, rows, D, attend_ctas(B, Hkv, rows, D, paged::kBf16, max_keys, device_sm_count()), &part_off);
 }

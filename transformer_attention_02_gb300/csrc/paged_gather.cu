@@ -1,0 +1,122 @@
+// Long chunks of queries over a paged cache: the pages that the queries see are
+// gathered into contiguous 16-bit tensors, with the queries rotated beside
+// them, and the fused tcgen05 kernel (its ragged variants) reads those.
+//
+// From kChunkRows queries a sequence the products outweigh the cache's reads,
+// and they belong on tcgen05: the kernel of paged_attn.cuh reaches some 200
+// TFLOP/s there (mma.sync, the cache read once per 32 rows), this path the
+// fused kernel's rate less one pass over the cache. Keys and values become
+// code * scale, exact in bf16 for power-of-two scales (four significant bits).
+// Bound by memory: each visible page is read once and written once at 16 bits.
+#include "../../include/attn.h"
+#include "attn_kernel.cuh"
+#include "paged_params.h"
+
+namespace attn {
+namespace paged {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int CT>
+__device__ __forceinline__ uint4 load_piece(const void* cache, size_t at, float scale, bool bf16) {
+    if (CT != kE4m3) return *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(cache) + at);
+    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(cache) + at);
+    const uint16_t pairs[4] = {(uint16_t)w.x, (uint16_t)(w.x >> 16), (uint16_t)w.y, (uint16_t)(w.y >> 16)};
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h;
+        float lo, hi;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(pairs[i]));
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+            : "=f"(lo), "=f"(hi)
+            : "r"(h));
+        r[i] = bf16 ? ptx::pack_bf16x2(lo * scale, hi * scale) : ptx::pack_f16x2(lo * scale, hi * scale);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// CTAs [0, p.copies): 128 keys of one K/V head of a sequence, zeros past its last
+// key (the products read whole blocks of 128). The others: 16-byte pieces of the
+// queries, rotated to their positions.
+template <int CT>
+__global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p) {
+    wait_for_inputs();
+    let_next_start();
+    const int chunks = p.D / 8, cshift = p.D == 128 ? 4 : 3;
+    if ((long long)blockIdx.x >= p.copies) {
+        const long long n = (long long)p.B * p.Sq * p.Hq * chunks;
+        const long long e = ((long long)blockIdx.x - p.copies) * kThreads + threadIdx.x;
+        if (e >= n) return;
+        const int g = (int)(e & (chunks - 1));
+        const long long row = e >> cshift;                        // (b * Sq + i) * Hq + h
+        const long long token = row / p.Hq;
+        const int h = (int)(row - token * p.Hq), b = (int)(token / p.Sq), i = (int)(token - (long long)b * p.Sq);
+        const int kv = min(max(p.kv_lens[b], 0), p.cap), ql = p.q_lens ? min(max(p.q_lens[b], 0), p.Sq) : p.Sq;
+        if (i >= ql) return;
+        int pos = kv - ql + i;
+        if (pos >= p.max_pos) {
+            if (g == 0) atomicOr(p.status, kStatusBadIndex);
+            pos = p.max_pos - 1;
+        }
+        const uint4 w = *reinterpret_cast<const uint4*>(p.q + token * p.q_stride + (long long)h * p.D + 8 * g);
+        const float4* at = reinterpret_cast<const float4*>(p.rope) + (size_t)max(pos, 0) * (p.D / 4) + 2 * g;
+        const float4 a = __ldg(at), c = __ldg(at + 1);
+        uint4 r;
+        if (p.bf16)
+            r = make_uint4(rotate_pair<true>(w.x, a.x, a.y), rotate_pair<true>(w.y, a.z, a.w),
+                           rotate_pair<true>(w.z, c.x, c.y), rotate_pair<true>(w.w, c.z, c.w));
+        else
+            r = make_uint4(rotate_pair<false>(w.x, a.x, a.y), rotate_pair<false>(w.y, a.z, a.w),
+                           rotate_pair<false>(w.z, c.x, c.y), rotate_pair<false>(w.w, c.z, c.w));
+        reinterpret_cast<uint4*>(p.q_out)[e] = r;
+        return;
+    }
+    long long u = blockIdx.x;
+    const int hk = (int)(u % p.Hkv);
+    u /= p.Hkv;
+    const int blocks = (p.cap + 127) / 128, kb = (int)(u % blocks), b = (int)(u / blocks);
+    const int raw_kv = p.kv_lens[b], raw_ql = p.q_lens ? p.q_lens[b] : p.Sq;
+    if (kb == 0 && hk == 0 && threadIdx.x == 0 && (raw_kv < 0 || raw_kv > p.cap || raw_ql < 0 || raw_ql > p.Sq))
+        atomicOr(p.status, kStatusBadIndex);
+    const int kv = min(max(raw_kv, 0), p.cap), ql = min(max(raw_ql, 0), p.Sq);
+    if (kb * 128 >= kv || ql == 0) return;
+    if (p.window > 0) {
+        const int low = max(0, kv - ql - p.window + 1);           // oldest key of the first query's window
+        if ((kb + 1) * 128 <= low && kb * 128 >= p.sinks) return; // no query sees a key of the block
+    }
+    for (int c = threadIdx.x; c < 128 << cshift; c += kThreads) {
+        const int key = kb * 128 + (c >> cshift), g = c & (chunks - 1);
+        if (key >= p.cap) break;                                  // (the tensor's end: loads past it read zeros)
+        uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
+        if (key < kv) {
+            const int id = __ldg(p.block_table + (size_t)b * p.max_pages + (key >> p.page_shift));
+            if ((unsigned)id < (unsigned)p.n_pages) {
+                const size_t block = (size_t)id * p.Hkv + hk;
+                const size_t at = ((block << p.page_shift) + (size_t)(key & ((1 << p.page_shift) - 1))) * p.D + 8 * g;
+                k = load_piece<CT>(p.k_cache, at, CT == kE4m3 ? __ldg(p.k_scale + block) : 1.f, p.bf16);
+                v = load_piece<CT>(p.v_cache, at, CT == kE4m3 ? __ldg(p.v_scale + block) : 1.f, p.bf16);
+            } else {
+                atomicOr(p.status, kStatusBadIndex);
+            }
+        }
+        const size_t to = (((size_t)b * p.cap + key) * p.Hkv + hk) * chunks + g;
+        reinterpret_cast<uint4*>(p.k_out)[to] = k;
+        reinterpret_cast<uint4*>(p.v_out)[to] = v;
+    }
+}
+
+}  // namespace
+
+int launch_gather(GatherParams p, int cache, cudaStream_t stream) {
+    p.copies = (long long)p.B * ((p.cap + 127) / 128) * p.Hkv;
+    const long long pieces = p.rope ? (long long)p.B * p.Sq * p.Hq * (p.D / 8) : 0;
+    const unsigned grid = (unsigned)(p.copies + (pieces + kThreads - 1) / kThreads);
+    auto kernel = cache == kE4m3 ? gather_kernel<kE4m3> : gather_kernel<kBf16>;
+    if (launch_early(kernel, grid, kThreads, 0, stream, p) != cudaSuccess) return ATTN_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace paged
+}  // namespace attn

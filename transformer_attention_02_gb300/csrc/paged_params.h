@@ -114,5 +114,40 @@ constexpr int resident_ctas(int D, int rows_per_block, int cache) {
 template <int CT>
 int launch_attend(bool (&attr_set)[2][4], const AttendParams& p, int D, cudaStream_t stream);
 
+// An attention goes by the gathered pages (paged_gather.cu) from kChunkRows
+// queries a sequence and kChunkTiles tiles of 256 rows of a head: a third of the
+// SMs. Measured over e4m3, 32/8 heads of 128, by the cache itself / gathered: 16
+// sequences of 8192 keys, 128 queries 1114 / 511 us, 256 queries 2194 / 559; one
+// sequence of 32768 keys, 128 queries (32 tiles) 272 / 406.
+constexpr int kChunkRows = 128;
+constexpr int kChunkTiles = 48;
+constexpr long long kChunkLimit = 4LL << 30;     // bytes of gathered tensors at most
+
+struct GatherParams {
+    const void* k_cache;          // (n_pages, Hkv, page, D)
+    const void* v_cache;
+    const float* k_scale;
+    const float* v_scale;
+    const int* block_table;
+    const int* kv_lens;
+    const int* q_lens;            // or null
+    uint16_t* k_out;              // (B, cap, Hkv, D)
+    uint16_t* v_out;
+    const uint16_t* q;            // (B, Sq, Hq, D), `q_stride` elements from token to token
+    long long q_stride;
+    uint16_t* q_out;              // (B, Sq, Hq, D), with a table only
+    const float* rope;            // or null: the queries are read where they are
+    int max_pos;
+    int B, Sq, Hq, Hkv, D;
+    int cap;                      // keys a sequence: max_pages * page
+    int page_shift, max_pages, n_pages;
+    int window, sinks;
+    long long copies;             // CTAs that gather (set by the launcher)
+    bool bf16;
+    unsigned int* status;
+};
+
+int launch_gather(GatherParams p, int cache, cudaStream_t stream);
+
 }  // namespace paged
 }  // namespace attn
