@@ -585,6 +585,7 @@ def attention_block(x, ln_gamma, ln_beta, w_qkv, b_qkv, w_o, b_o, *, Hq: int, Hk
 # once it has failed.
 
 _torch = None
+_NAN = float("nan")
 
 
 def _bind():
@@ -640,6 +641,16 @@ def _stream_on(at, stream):
     return _torch.cuda.current_stream(at).cuda_stream if raw is None else raw(at)
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _count(name, n):
+    """A window or a number of sinks as a C int: past its range it means all keys."""
+    if n < 0:
+        raise ValueError(f"{name} must not be negative")
+    return n if n <= _INT_MAX else _INT_MAX
+
+
 def _new(shape, dtype, like, stream):
     t = _torch.empty(shape, dtype=dtype, device=like.device)
     if stream is not None:
@@ -669,7 +680,7 @@ _held = _Held()
 
 def _workspace(q, at, size, handle, stream):
     """(address, bytes, the tensor to keep until the call is enqueued)."""
-    if handle or size > _HELD_BYTES or _torch.cuda.is_current_stream_capturing():
+    if stream is not None or handle or size > _HELD_BYTES or _torch.cuda.is_current_stream_capturing():
         t = _new(size, _torch.uint8, q, stream)
         return t.data_ptr(), size, t
     held = _held.by_device.get(at)
@@ -715,7 +726,8 @@ def attention_window(q, k, v, *, window: int, sinks: int = 0, scale=None, out=No
         out, lse = _outputs(q, at, out, lse, stream)
         fn = L.attn_fwd_window if q.dtype is _torch.bfloat16 else L.attn_fwd_window_f16
         rc = fn(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, ks[2], Sq, ks[1], D,
-                float("nan") if scale is None else scale, window, sinks, _stream_on(at, stream))
+                _NAN if scale is None else scale, _count("window", window), _count("sinks", sinks),
+                _stream_on(at, stream))
     finally:
         if back is not None:
             _torch.cuda.set_device(back)
@@ -823,9 +835,6 @@ def kv_append(k, v, k_cache, v_cache, block_table, kv_lens, *, new_lens=None, k_
         raise AttnError(rc, "attn_kv_append")
 
 
-_NAN = float("nan")
-
-
 def attention_paged(q, k_cache, v_cache, block_table, kv_lens, *, q_lens=None, k_scale=None, v_scale=None, table=None,
                     window: int = 0, sinks: int = 0, scale=None, out=None, lse=None, workspace=None, stream=None):
     """O, LSE = causal attention of a step's queries (B, Sq, Hq, D) over a paged cache (see kv_append).
@@ -858,7 +867,7 @@ def attention_paged(q, k_cache, v_cache, block_table, kv_lens, *, q_lens=None, k
         fn = L.attn_fwd_paged if q.dtype is _torch.bfloat16 else L.attn_fwd_paged_f16
         rc = fn(q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, bt, kl, nl, out.data_ptr(),
                 lse.data_ptr(), B, Hq, Hkv, Sq, D, page, max_pages, n_pages, kind, _NAN if scale is None else scale,
-                window, sinks, rope, max_pos, ws, size, handle)
+                _count("window", window), _count("sinks", sinks), rope, max_pos, ws, size, handle)
     finally:
         if back is not None:
             _torch.cuda.set_device(back)
