@@ -397,11 +397,12 @@ int attn_fwd_window_f16(const void *q, const void *k, const void *v, void *o, fl
  *               aligned. cache_kind ATTN_CACHE_16BIT: the type of k, v and q;
  *               ATTN_CACHE_E4M3: 8-bit e4m3 codes of value / scale
  *   k_scale, v_scale   device, FP32, (n_pages, Hkv): one scale per page and
- *               K/V head (e4m3 only, else ignored and may be NULL)
+ *               K/V head, from 2^-100 to 2^120 (e4m3 only, else ignored and may
+ *               be NULL)
  *   block_table device, int32, (B, max_pages): page of tokens [j * page,
  *               (j + 1) * page) of each sequence. Sequences may share pages that
- *               are only read; a page that attn_kv_append writes must belong to
- *               one sequence of the call
+ *               are only read; a page that attn_kv_append writes must stand
+ *               once in the table
  *   kv_lens     device, int32, (B): tokens of each sequence in the cache,
  *               INCLUDING those of the current step, so that the append and the
  *               attention of a step take the same tensor; at most
@@ -461,7 +462,8 @@ int attn_kv_append_f16(const void *k, const void *v, long long k_stride, long lo
  * must be finite in V, as for attn_fwd.
  *   q           device, (B, Sq, Hq, D), 16-byte aligned, q_stride elements from
  *               token to token (as k_stride above, at least Hq * D)
- *   o, lse      device, (B, Sq, Hq, D) contiguous and FP32 (B, Hq, Sq). Rows with
+ *   o, lse      device, (B, Sq, Hq, D) contiguous and FP32 (B, Hq, Sq), apart from
+ *               all inputs and the workspace. Rows with
  *               no visible key get o = 0, lse = -inf; rows i >= q_lens[b] are not
  *               written
  *   scale       as for attn_fwd
@@ -477,9 +479,9 @@ int attn_kv_append_f16(const void *k, const void *v, long long k_stride, long lo
  * up to 32 query rows (Sq * Hq / Hkv) a K/V head; more rows read it once per 32.
  * Long chunks (Sq of 128 and more, with B * Hq * ceil(Sq / 256) of 48 and more)
  * go another way when the workspace holds the gathered tensors: the pages that
- * are seen are copied into contiguous tensors of q's type (code * scale, rounded;
- * exact in bf16 for the append's scales), and the fused kernel of attn_fwd reads
- * those. Its weights are rounded to q's type, where the other path rounds them
+ * are seen are copied into contiguous tensors of q's type (code * scale, rounded
+ * and saturated; exact in bf16 for the append's scales), and the fused kernel of
+ * attn_fwd reads those. Its weights are rounded to q's type, where the other path rounds them
  * to fp16 over an 8-bit cache; keys of a page out of range read as zeros there,
  * and are hidden here.
  */

@@ -603,6 +603,21 @@ def test_long_chunk_leaves_out_what_is_out_of_range():
     assert bool((o[0] == 0).all()) and bool((lse[0] == float("-inf")).all())
 
 
+def test_long_chunk_over_codes_past_the_largest_half():
+    """The code of fp16's largest value stands for 2^16; gathered in fp16 it saturates and the rows stay finite."""
+    c = Cache(1, 2, 64, 16, 10, FP, True)
+    k, v = _rand((1, 130, 2, 64), FP, 93), _rand((1, 130, 2, 64), FP, 94)
+    v[0, 5, 0, 3], v[0, 5, 0, 4], k[0, 5, 0, 9] = 65504, -65504, 65504
+    q = _rand((1, 130, 48, 64), FP, 95)
+    q[..., 9] = 2.0 ** -14
+    A.kv_append(k, v, c.k, c.v, c.table, _i32([130]), **c.scales)
+    o, lse = A.attention_paged(q, c.k, c.v, c.table, _i32([130]), **c.scales)
+    kk, vv = (np.clip(R.tokens(x, s, c.table_np[0], 130, 16), -65504, 65504) for x, s in ((c.k, c.ks), (c.v, c.vs)))
+    assert np.abs(kk).max() == np.abs(vv).max() == 65504
+    want = R.attend(R.f64(q[0]), kk, vv, np.arange(130), 0.125, 0, 0)
+    R.check_rows(R.f64(o[0]), R.f64(lse[0]), want, R.step(FP), R.step(FP), 64, 130, 65504)
+
+
 def test_long_chunk_of_a_packed_projection_in_a_graph():
     B, S, Hq, Hkv, D, page = 2, 160, 24, 2, 64, 32
     c = Cache(B, Hkv, D, page, 16, BF, True)
@@ -630,3 +645,43 @@ def test_long_chunk_of_a_packed_projection_in_a_graph():
         want = R.attend(R.f64(rot[b]), kk, vv, np.arange(L - S, L), D ** -0.5, 0, 0)
         R.check_rows(R.f64(out[0][b]), R.f64(out[1][b]), want, R.step(BF), R.step(BF), D, L, _v_top(c, c.table_np[b, :13]),
                      f"graph b={b}")
+
+
+def _scaled_pages(rel_log2, logit_log2, seed):
+    """A one-head e4m3 cache of pages whose value scales are 2^rel_log2[j] and whose keys all have logits near
+    logit_log2[j] * ln 2 for the query of ones / 64: (cache, query, keys)."""
+    D, page = 64, 16
+    n = len(rel_log2)
+    c = Cache(1, 1, D, page, n, BF, True, seed=seed)
+    c.fill(0, n * page, seed)
+    q = torch.ones((1, 1, 1, D), dtype=BF, device=DEV)
+    for j in range(n):
+        at = int(c.table_np[0, j])
+        c.vs[at] = 2.0 ** rel_log2[j]
+        # K = +-code, D of them alike: q . K scale / 8 = logit
+        c.k.view(torch.uint8)[at] = torch.ones((1, page, D), device=DEV).to(torch.float8_e4m3fn).view(torch.uint8)
+        c.ks[at] = logit_log2[j] * np.log(2.0) / (D * D ** -0.5) if logit_log2[j] else 1e-30
+    return c, q, n * page
+
+
+@pytest.mark.parametrize("rel_log2,logit_log2", [
+    ([0, 0, 40, 0], [0, 0, -80, 0]),            # enormous values of no weight
+    ([40, 0, 0, 0], [-80, 0, 0, 0]),            # ... met first
+    ([30, 0, 0], [0, 60, 90]),                  # large values that later keys outweigh
+    ([-100, -100, -100], [0, 1, 0]),            # values of nothing (a block of zeros has this scale)
+    ([0, -100, 3], [0, 10, 2]),                 # most of the weight on values of nothing
+    ([120, 118, 0], [0, 1, 3]),                 # values near the end of bf16
+])
+def test_value_scales_far_apart(rel_log2, logit_log2):
+    """Each page's contribution counts by weight times scale, scales below 2^-72 as 2^-72. What the 16-bit products lose
+    is relative to the largest such contribution: n 2^-24 of 448 max_j p_j max(scale_j, 2^-72) (half a subnormal step,
+    2^-25, twice for the sum's side)."""
+    c, q, n = _scaled_pages(rel_log2, logit_log2, 5)
+    o, lse = A.attention_paged(q, c.k, c.v, c.table, _i32([n]), **c.scales)
+    k, v = (R.tokens(x, s, c.table_np[0], n, 16) for x, s in ((c.k, c.ks), (c.v, c.vs)))
+    want = R.attend(R.f64(q[0]), k, v, np.array([n - 1]), 64 ** -0.5, 0, 0)
+    z = 64 ** -0.5 * k[:, 0].sum(-1)
+    w = np.exp(z - z.max())
+    w /= w.sum()
+    top = float((w * np.repeat(2.0 ** np.maximum(np.array(rel_log2, float), -72), 16)).max() * 448)
+    R.check_rows(R.f64(o[0]), R.f64(lse[0]), want, R.step(BF), R.step(FP), 64, n, top, f"{rel_log2} {logit_log2}")

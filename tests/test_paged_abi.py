@@ -79,6 +79,8 @@ def test_workspace_size():
     assert A.attn_paged_workspace_bytes(1, 32, 8, 1, 128, 577) == 256 + 8 * (5 + 4) * 2 * 8 * 130 * 4
     assert A.attn_paged_workspace_bytes(16, 32, 8, 1, 128, 8192) == A.attn_paged_workspace_bytes(16, 32, 8, 1, 128)
     assert A.attn_paged_workspace_bytes(16, 32, 8, 1, 128, -1) == 0
+    assert A.attn_paged_workspace_bytes(16, 32, 8, 128, 128, (1 << 30) + 1) == 0
+    assert A.attn_paged_workspace_bytes(16, 32, 8, 128, 128, (1 << 32) + 16) == 0
     # long chunks (128 queries, 48 tiles): gathered keys and values, then the queries; else, or past 4 GiB, as above
     assert A.attn_paged_workspace_bytes(2, 32, 8, 128, 64, 1000 * 16) == 2 * (2 * 16000 * 8 * 64 * 2) + 2 * 128 * 32 * 64 * 2
     few = 256 + 148 * 2 * 2 * 32 * 66 * 4

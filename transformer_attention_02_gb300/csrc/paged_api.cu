@@ -159,6 +159,8 @@ int attend_impl(const void* q, long long q_stride, const void* k_cache, const vo
     const int ctas = attend_ctas(B, Hkv, (int)rows, D, type, max_keys, device_sm_count());
     if (!gathered && workspace_bytes < attend_workspace(B, (int)rows, D, ctas, &part_off)) return ATTN_ERR_INVALID_ARG;
     if (!(scale > 0.f) || !std::isfinite(scale)) scale = 1.0f / std::sqrt((float)D);
+    constexpr int kAllKeys = 1 << 30;                     // a longer window hides nothing; differences stay in 32 bits
+    window = std::min(window, kAllKeys);
 
     DeviceState dev{};
     rc = device_state(&dev);
@@ -195,9 +197,8 @@ int attend_impl(const void* q, long long q_stride, const void* k_cache, const vo
         g.status = dev.status;
         rc = paged::launch_gather(g, type, stream);
         if (rc != ATTN_OK) return rc;
-        constexpr int kNoWindow = 1 << 30;
         return launch_ragged(rope_table ? g.q_out : q, rope_table ? (long long)Hq * D : q_stride, g.k_out, g.v_out, o, lse, B,
-                             Hq, Hkv, Sq, chunk.cap, D, scale, window > 0 ? std::min(window, kNoWindow) : kNoWindow,
+                             Hq, Hkv, Sq, chunk.cap, D, scale, window > 0 ? window : kAllKeys,
                              window > 0 ? sinks : 0, kv_lens, q_lens, stream, bf16);
     }
     paged::AttendParams p{};
@@ -260,7 +261,7 @@ int attn_kv_append_f16(const void* k, const void* v, long long k_stride, long lo
 }
 
 size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, long long max_keys) {
-    if (max_keys < 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Sq <= 0 || (D != 64 && D != 128)) return 0;
+    if (max_keys < 0 || max_keys > (1 << 30) || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Sq <= 0 || (D != 64 && D != 128)) return 0;
     if ((long long)Sq * (Hq / Hkv) > (1 << 30)) return 0;
     size_t part_off = 0;
     const int rows = Sq * (Hq / Hkv);

@@ -44,7 +44,8 @@ namespace paged {
 
 constexpr int kScanInMerge = 256;            // sequences whose units a merge CTA sums itself, one a thread
 constexpr int kNoKey = 0x7fff0000;          // past every key (a sequence holds at most 2^30)
-constexpr float kNoLogit = -3e38f;          // the running maximum before any key
+constexpr float kNoLogit = -3e38f;          // the reference before any key
+constexpr float kShift = 20.f, kShiftDown = 0x1p-20f;     // 8-bit caches: see m_neg
 
 template <int D, int CT, int NT>
 struct Cfg {
@@ -249,7 +250,8 @@ __device__ __forceinline__ bool locate(const AttendParams& p, int segs, int lead
         const int span = span_of(s.list.units, lead);
         if (x >= s.base + span * segs) {                          // the sequence is done, or empty
             s.base += span * segs;
-            s.list = key_list(p, ++s.b, bad);
+            if (++s.b >= p.B) return false;                       // (only if the lengths changed under the call)
+            s.list = key_list(p, s.b, bad);
             continue;
         }
         seg = (x - s.base) / span;
@@ -633,11 +635,15 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
         }
 
         float acc[kSteps][NT][4];                                 // O^T
-        // Rows 2t, 2t + 1 of each n-tile: minus the maximum in use (log2 units;
-        // below any logit at first, so that no weight needs a special case) and
-        // this lane's part of the sum.
+        // Rows 2t, 2t + 1 of each n-tile: minus the reference in use (log2 units)
+        // and this lane's part of the sum of 2^(logit - reference). Over an 8-bit
+        // cache the reference follows logit + log2(value scale), so that what goes
+        // to the tensor cores, weight * scale, is largest where it matters most,
+        // whatever the scales of other pages. The weights alone then reach
+        // 2^(8 + kShift) / scale: FP32 holds them and their sum for scales from
+        // 2^-72 to 2^120 (values under smaller scales, below 2^-63, fade to zero).
+        // Below any logit at first, so that no weight needs a special case.
         float m_neg[NT][2], l_sum[NT][2];
-        float v_ref = 0.f, v_inv = 0.f;                           // largest value scale so far (acc is in units of it)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             m_neg[n][0] = m_neg[n][1] = -kNoLogit;
@@ -695,11 +701,12 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                     }
                 }
                 // ---- logits in log2 units; hidden keys to -inf
-                float ks = 1.f, vs = 1.f;
+                float ks = 1.f, vs = 1.f, lv = 0.f;
                 if (CT == kE4m3) {
                     const float2 kv2 = *reinterpret_cast<const float2*>(scales + (st * C::kTiles + m) * 2);
                     ks = kv2.x;
-                    vs = kv2.y;
+                    vs = kv2.y * kShiftDown;
+                    lv = fminf(fmaxf(__log2f(fabsf(kv2.y)), -72.f), 120.f) - kShift;
                 }
                 const bool whole = k0 + 15 <= pos_lo && (k0 >= pos_hi - p.window + 1 || p.window == 0 || k0 + 16 <= sinks);
                 float f[NT][2];                                    // log2 units per value of s
@@ -721,22 +728,16 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                             f[n][e] = 1.f;
                         }
                 }
-                // The maximum in use may trail the true one by 2^8 (the weights
+                // The reference may trail the true maximum by 2^8 (the weights
                 // then reach 2^8, far inside 16-bit range), so most tiles need
                 // one vote instead of the reduction and the rescaling.
-                bool grow = CT == kE4m3 && vs > v_ref;
+                bool grow = false;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        grow |= fmaf(fmaxf(s[n][e], s[n][2 + e]), f[n][e], m_neg[n][e]) > kRescaleThreshold;
+                        grow |= fmaf(fmaxf(s[n][e], s[n][2 + e]), f[n][e], m_neg[n][e]) > kRescaleThreshold - lv;
                 if (__any_sync(0xffffffffu, grow)) {
-                    float fv = 1.f;
-                    if (CT == kE4m3 && vs > v_ref) {
-                        fv = v_ref / vs;
-                        v_ref = vs;
-                        v_inv = vs > 1e-37f ? 1.f / vs : 0.f;
-                    }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -744,21 +745,19 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                             float mx = fmaxf(s[n][e], s[n][2 + e]) * f[n][e];
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                            mx = fmaxf(mx, -m_neg[n][e]);
+                            mx = fmaxf(mx + lv, -m_neg[n][e]);
                             const float alpha = ptx::ex2(-m_neg[n][e] - mx);
                             m_neg[n][e] = -mx;
                             l_sum[n][e] *= alpha;
-                            const float fa = alpha * fv;
 #pragma unroll
                             for (int d = 0; d < kSteps; ++d) {
-                                acc[d][n][e] *= fa;
-                                acc[d][n][2 + e] *= fa;
+                                acc[d][n][e] *= alpha;
+                                acc[d][n][2 + e] *= alpha;
                             }
                         }
                     }
                 }
                 // ---- weights; P in f16 (bf16 for a bf16 cache), summed before that rounding
-                const float vf = vs * v_inv;
                 uint32_t pb[NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -770,8 +769,8 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                     ptx::add2(l_sum[n][0], l_sum[n][1], l_sum[n][0], l_sum[n][1], w[0], w[1]);
                     ptx::add2(l_sum[n][0], l_sum[n][1], l_sum[n][0], l_sum[n][1], w[2], w[3]);
                     if (CT == kE4m3) {
-                        ptx::mul2(w[0], w[1], w[0], w[1], vf, vf);
-                        ptx::mul2(w[2], w[3], w[2], w[3], vf, vf);
+                        ptx::mul2(w[0], w[1], w[0], w[1], vs, vs);
+                        ptx::mul2(w[2], w[3], w[2], w[3], vs, vs);
                     }
                     pb[n][0] = transpose8x8(kBf ? ptx::pack_bf16x2(w[0], w[1]) : ptx::pack_f16x2(w[0], w[1]));
                     pb[n][1] = transpose8x8(kBf ? ptx::pack_bf16x2(w[2], w[3]) : ptx::pack_f16x2(w[2], w[3]));
@@ -839,7 +838,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                 const float2 s2 = stats[v * C::kRows + lane];
                 sum = fmaf(s2.y, ptx::ex2(s2.x - mx), sum);
             }
-            to_common = ptx::ex2(stats[warp * C::kRows + lane].x - mx) * (CT == kE4m3 ? v_ref : 1.f);
+            to_common = ptx::ex2(stats[warp * C::kRows + lane].x - mx + (CT == kE4m3 ? kShift : 0.f));
             if (warp == 0) total_sh[lane] = make_float2(mx, sum);
         }
         const int m_stage = st == 0 ? C::kStages - 1 : st - 1;
@@ -960,7 +959,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const AttendParams p, 
         const int span = units + lead;
         const Ranges ranges(total, working_ctas(p, total));
         c0 = ranges.owner(first + seg * span + lead);
-        c1 = ranges.owner(first + (seg + 1) * span - 1);
+        c1 = min(ranges.owner(first + (seg + 1) * span - 1), p.ctas - 1);     // (as above)
         if (c0 == c1) return;
     }
     const int hk = seg / p.row_blocks, rb = seg - hk * p.row_blocks;

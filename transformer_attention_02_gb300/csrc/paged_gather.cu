@@ -32,7 +32,12 @@ __device__ __forceinline__ uint4 load_piece(const void* cache, size_t at, float 
         asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
             : "=f"(lo), "=f"(hi)
             : "r"(h));
-        r[i] = bf16 ? ptx::pack_bf16x2(lo * scale, hi * scale) : ptx::pack_f16x2(lo * scale, hi * scale);
+        // Saturating: the code of a value near the type's largest may lie above it.
+        lo *= scale, hi *= scale;
+        if (bf16)
+            asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r[i]) : "f"(hi), "f"(lo));
+        else
+            asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r[i]) : "f"(hi), "f"(lo));
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
