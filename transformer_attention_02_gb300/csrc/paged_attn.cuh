@@ -112,6 +112,16 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
                      : "memory");
 }
 
+// Two 16x16 matrices of bytes, transposed: lanes 0..15 and 16..31 give the rows
+// of each. Lane 4g + t receives bytes 4t..4t+3 of column g in r[0] (second
+// matrix: r[2]) and of column g + 8 in r[1] (r[3]).
+__device__ __forceinline__ void ldmatrix_bytes_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
 // Transposes an 8x8 matrix of 16-bit values held as an accumulator fragment.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     uint32_t r;
@@ -161,14 +171,27 @@ __device__ __forceinline__ float2 widen16(uint32_t w, bool bf16) {
     return f;
 }
 
-// Byte offset of 16-byte chunk c of row r in a swizzled stage.
-template <int ROWB>
+// The key of a 16-key tile that stands in row m of the products. An 8-bit tile's
+// values come from ldmatrix with four consecutive keys a lane, which are the
+// products' columns 2t, 2t + 1, 2t + 8 and 2t + 9: so those rows hold the keys
+// 4t..4t+3.
+template <bool E4M3>
+__device__ __forceinline__ int key_of_row(int m) {
+    return E4M3 ? ((m & 6) << 1) + (m & 1) + ((m >> 2) & 2) : m;
+}
+
+// Byte offset of 16-byte chunk c of row r in a swizzled stage. The eight rows
+// that one step of an ldmatrix reads lie in different banks: rows 0..7 or 8..15,
+// and for an 8-bit tile's keys also those of key_of_row, {0, 1, 4, 5, 8, ...}
+// and {2, 3, 6, 7, 10, ...}.
+template <int ROWB, bool E4M3>
 __device__ __forceinline__ uint32_t swizzled(int r, int c) {
     if (ROWB == 64) {                                            // two rows share a 128-byte line
-        const int line = r >> 1;
-        return (uint32_t)(line * 128 + (((((r & 1) << 2) + c) ^ (line & 7)) << 4));
+        const int line = r >> 1, x = ((line >> 1) & 1) | (((line ^ (line >> 2)) & 1) << 1);
+        return (uint32_t)(line * 128 + (((((r & 1) << 2) + c) ^ x) << 4));
     }
-    return (uint32_t)(r * ROWB + ((c ^ (r & 7)) << 4));
+    const int x = E4M3 ? (r & 1) | ((r >> 1) & 2) | (((r << 1) ^ (r >> 1)) & 4) : r & 7;
+    return (uint32_t)(r * ROWB + ((c ^ x) << 4));
 }
 
 // What a sequence's queries see, as a list of 128-key units: the units of the
@@ -364,21 +387,23 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
 
     // Where a lane's pieces lie in a swizzled stage. Copy c of a 16-key tile is
     // chunk lane % kChunks of row c * (32 / kChunks) + lane / kChunks; the
-    // swizzle repeats every 8 rows (16 rows of 64 bytes), so a few offsets
+    // swizzle repeats every 8 rows (16 rows of 8-bit values), so a few offsets
     // describe all copies. The ldmatrix rows likewise: chunk 2c is the XOR of
     // c << 5 with chunk 0.
     constexpr int kCopyRows = 32 / C::kChunks;                     // rows of one copy
-    constexpr int kPeriod = C::kRowBytes == 64 ? 16 : 8;
+    constexpr int kPeriod = CT == kE4m3 ? 16 : 8;
     constexpr int kCopyKinds = kPeriod / kCopyRows;
     uint32_t copy_off[kCopyKinds];
 #pragma unroll
     for (int c = 0; c < kCopyKinds; ++c)
-        copy_off[c] = swizzled<C::kRowBytes>(c * kCopyRows + lane / C::kChunks, lane % C::kChunks);
+        copy_off[c] = swizzled<C::kRowBytes, CT == kE4m3>(c * kCopyRows + lane / C::kChunks, lane % C::kChunks);
     auto copy_to = [&](int c) {
         return copy_off[c % kCopyKinds] + (uint32_t)(c / kCopyKinds * kCopyKinds * kCopyRows * C::kRowBytes);
     };
-    const uint32_t k_off = swizzled<C::kRowBytes>((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
-    const uint32_t v_off = swizzled<C::kRowBytes>((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
+    const uint32_t k_off = swizzled<C::kRowBytes, CT == kE4m3>(key_of_row<CT == kE4m3>(lane & 15), lane >> 4);
+    const uint32_t v_off = CT == kE4m3
+                               ? swizzled<C::kRowBytes, true>(lane & 15, lane >> 4)
+                               : swizzled<C::kRowBytes, false>((lane & 7) + (lane >> 4) * 8, (lane >> 3) & 1);
     const int sinks = p.window > 0 ? p.sinks : 0;
 
     // ---- the copies run ahead of the products, across segments: `ld` is the
@@ -721,7 +746,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                         for (int e = 0; e < 2; ++e) {
                             const int pos = pos0 + (r0 + 8 * n + 2 * t + e) / p.group;
                             const int lo = p.window > 0 ? pos - p.window : -1;
-                            const int j0 = k0 + g, j1 = j0 + 8;
+                            const int j0 = k0 + key_of_row<CT == kE4m3>(g), j1 = j0 + (CT == kE4m3 ? 2 : 8);
                             const bool h0 = j0 > pos || (j0 <= lo && j0 >= sinks), h1 = j1 > pos || (j1 <= lo && j1 >= sinks);
                             s[n][e] = h0 ? -INFINITY : s[n][e] * f[n][e];
                             s[n][2 + e] = h1 ? -INFINITY : s[n][2 + e] * f[n][e];
@@ -780,20 +805,18 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
 #pragma unroll
                     for (int c = 0; c < C::kChunks / 2; ++c) {
                         uint32_t r[4];
-                        ldmatrix4<true>(r, va ^ (uint32_t)(c << 5));
                         if (CT == kE4m3) {
-                            // Each register holds two keys of two neighbouring dims: the even
-                            // dims of both chunks make one product, the odd ones the other.
+                            ldmatrix_bytes_trans(r, va ^ (uint32_t)(c << 5));
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) r[j] = __byte_perm(r[j], 0u, 0x3120);
-                            const uint32_t e0 = e4m3_lo(r[0]), e1 = e4m3_lo(r[1]), e2 = e4m3_lo(r[2]), e3 = e4m3_lo(r[3]);
-                            const uint32_t o0 = e4m3_hi(r[0]), o1 = e4m3_hi(r[1]), o2 = e4m3_hi(r[2]), o3 = e4m3_hi(r[3]);
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t a0 = e4m3_lo(r[2 * h]), a1 = e4m3_lo(r[2 * h + 1]),
+                                               a2 = e4m3_hi(r[2 * h]), a3 = e4m3_hi(r[2 * h + 1]);
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                mma16816<false>(acc[2 * c][n], e0, e1, e2, e3, pb[n][0], pb[n][1]);
-                                mma16816<false>(acc[2 * c + 1][n], o0, o1, o2, o3, pb[n][0], pb[n][1]);
+                                for (int n = 0; n < NT; ++n)
+                                    mma16816<false>(acc[2 * c + h][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
                             }
                         } else {
+                            ldmatrix4<true>(r, va ^ (uint32_t)(c << 5));
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
                                 mma16816<kBf>(acc[c][n], r[0], r[1], r[2], r[3], pb[n][0], pb[n][1]);
@@ -855,10 +878,8 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                     float* const row = mine_o + (8 * (n - n0) + 2 * t + e) * D;
 #pragma unroll
                     for (int d = 0; d < kSteps; ++d) {
-                        const int da = CT == kE4m3 ? 32 * (d >> 1) + (d & 1) + 2 * g : 16 * d + g;
-                        const int db = CT == kE4m3 ? da + 16 : da + 8;
-                        row[da ^ (t << 3)] = acc[d][n][e] * f;    // XOR: spreads the rows over the banks
-                        row[db ^ (t << 3)] = acc[d][n][2 + e] * f;
+                        row[(16 * d + g) ^ (t << 3)] = acc[d][n][e] * f;     // XOR: spreads the rows over the banks
+                        row[(16 * d + 8 + g) ^ (t << 3)] = acc[d][n][2 + e] * f;
                     }
                 }
             }
