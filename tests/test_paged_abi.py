@@ -70,11 +70,11 @@ def test_attention_arguments(kw, code):
 
 def test_workspace_size():
     # 148 SMs assumed without a GPU: (B + 1) sequence offsets, then two parts of rows x (D + 2) FP32 per CTA; rows
-    # come in blocks of 8, 16 or 32, two CTAs an SM unless a block holds 32 rows of 128
+    # come in blocks of 8, 16, 24 or 32, two CTAs an SM, three for blocks of 24 and 32 rows of 64 over an 8-bit cache
     assert A.attn_paged_workspace_bytes(16, 32, 8, 1, 128) == 256 + 148 * 2 * 2 * 8 * 130 * 4
     assert A.attn_paged_workspace_bytes(16, 32, 8, 4, 64) == 256 + 148 * 2 * 2 * 16 * 66 * 4
-    assert A.attn_paged_workspace_bytes(1, 32, 1, 9, 64) == 256 + 148 * 2 * 2 * 32 * 66 * 4
-    assert A.attn_paged_workspace_bytes(1, 32, 1, 9, 128) == 256 + 148 * 2 * 32 * 130 * 4
+    assert A.attn_paged_workspace_bytes(1, 32, 1, 9, 64) == 256 + 148 * 3 * 2 * 32 * 66 * 4
+    assert A.attn_paged_workspace_bytes(1, 32, 1, 9, 128) == 256 + 148 * 2 * 2 * 32 * 130 * 4
     # a short table bounds the CTAs: 8 segments of 5 units (577 keys), one more for sinks, and the schedule's lead
     assert A.attn_paged_workspace_bytes(1, 32, 8, 1, 128, 577) == 256 + 8 * (5 + 4) * 2 * 8 * 130 * 4
     assert A.attn_paged_workspace_bytes(16, 32, 8, 1, 128, 8192) == A.attn_paged_workspace_bytes(16, 32, 8, 1, 128)
@@ -83,7 +83,7 @@ def test_workspace_size():
     assert A.attn_paged_workspace_bytes(16, 32, 8, 128, 128, (1 << 32) + 16) == 0
     # long chunks (128 queries, 48 tiles): gathered keys and values, then the queries; else, or past 4 GiB, as above
     assert A.attn_paged_workspace_bytes(2, 32, 8, 128, 64, 1000 * 16) == 2 * (2 * 16000 * 8 * 64 * 2) + 2 * 128 * 32 * 64 * 2
-    few = 256 + 148 * 2 * 2 * 32 * 66 * 4
+    few = 256 + 148 * 3 * 2 * 32 * 66 * 4
     assert A.attn_paged_workspace_bytes(2, 32, 8, 128, 64) == few
     assert A.attn_paged_workspace_bytes(2, 32, 8, 127, 64, 1000 * 16) == few
     assert A.attn_paged_workspace_bytes(1, 32, 8, 256, 64, 1000 * 16) == few

@@ -267,8 +267,8 @@ size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, long lo
     const int rows = Sq * (Hq / Hkv);
     ChunkLayout chunk;
     if (chunk_layout(B, Hq, Hkv, Sq, D, max_keys, &chunk)) return chunk.total;
-    // (the 16-bit cache's CTAs are the more, where the two differ)
-    return attend_workspace(B, rows, D, attend_ctas(B, Hkv, rows, D, paged::kBf16, max_keys, device_sm_count()), &part_off);
+    // (the 8-bit cache's CTAs are the more, where the two differ)
+    return attend_workspace(B, rows, D, attend_ctas(B, Hkv, rows, D, paged::kE4m3, max_keys, device_sm_count()), &part_off);
 }
 
 int attn_fwd_paged(const void* q, long long q_stride, const void* k_cache, const void* v_cache, const float* k_scale,

@@ -53,17 +53,21 @@ struct Cfg {
     static constexpr int kRowBytes = D * kElt;
     static constexpr int kChunks = kRowBytes / 16;
     static constexpr int kRows = 8 * NT;                         // query rows of a row block
-    // Two CTAs a SM of eight warps (four with 256-byte rows, whose stages are as
-    // large again), or one when the sums take the registers of both. 32 rows of
-    // 64 dims over e4m3 lie between: one CTA of twelve warps (16 x 8192 keys, 8
-    // K/V heads: 56.5 us; two of eight spill registers: 88.8).
+    // Sixteen warps an SM, in two CTAs, while 128 registers hold a warp's sums;
+    // else eight to twelve, in CTAs of four where their rings fit, because the
+    // CTAs cover one another's change of segment (barriers, merge, queries).
+    // Measured over e4m3, 8 K/V heads, 256 x 512 keys / 16 x 8192: 20 rows of
+    // 128: one CTA of eight warps 140.0 / 70.3 us, two of four 104.5 / 64.3;
+    // 20 rows of 64: two of eight (spilling) 78.9 / 46.5, three of four 70.2 /
+    // 47.0; 4 rows of 128: two of eight 63.5 / 49.0, four of four 56.6 / 50.7
+    // (not taken: long contexts are the more usual).
     static constexpr int kResident = resident_ctas(D, kRows, CT);
-    static constexpr int kWarps = kResident == 2 && kRowBytes == 256 ? 4 : kResident == 1 && D == 64 ? 12 : 8;
+    static constexpr int kWarps = kResident == 3 || (kResident == 2 && (kRowBytes == 256 || (D == 128 && NT >= 3))) ? 4 : 8;
     static constexpr int kKeys = kRowBytes == 64 ? 32 : 16;      // keys of a stage
     static constexpr int kTiles = kKeys / 16;
     static constexpr int kCopies = 16 * kChunks / 32;            // 16-byte copies a lane makes for 16 keys
     static constexpr int kStageBytes = 2 * kKeys * kRowBytes;
-    static constexpr int kStages = kResident == 1 && kRowBytes == 128 ? 5 : 3;      // (as many as fit)
+    static constexpr int kStages = CT == kE4m3 && D == 128 && NT >= 3 ? 5 : 3;    // (as many as fit)
     static constexpr int kRingBytes = kStages * kStageBytes;     // of one warp
     static constexpr bool kQShared = D * NT >= 192;              // Q fragments in shared memory, not registers
     static constexpr int kQStride = D * 2 + 16;                  // bytes of a query row: conflict-free fragment reads
