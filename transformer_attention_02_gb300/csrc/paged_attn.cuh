@@ -78,7 +78,7 @@ struct Cfg {
     static constexpr int kFragOff = kQOff + kRows * kQStride;
     static constexpr int kShareOff = kFragOff + (kQShared ? kRows * D * 2 : 0);   // [warp]{copies', products'}
     static constexpr int kIssueOff = kShareOff + kWarps * 2 * 80;    // [warp] what a stage's copies need of a share
-    static constexpr int kRowOff = kIssueOff + kWarps * 32;  // [row] score factor; [row]{max, sum} of the merge
+    static constexpr int kRowOff = kIssueOff + kWarps * 32;  // [row] score factor; [row]{factor, place in O} of the merge
     static constexpr int kSmemBytes = kRowOff + kRows * 16;
     static constexpr int kMergeTiles = kStageBytes / (8 * D * 4);    // n-tiles that a stage of the ring takes at once
     static_assert(kMergeTiles >= 1, "a warp's rows are merged through one stage of its ring");
@@ -855,23 +855,39 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                 if (g == 0) stats[warp * C::kRows + 8 * n + 2 * t + e] = make_float2(-m_neg[n][e], l);
             }
         __syncthreads();
+        const bool full = now.u0 == 0 && now.u1 == now.list.units;
+        float* slot = p.part + (size_t)(2 * blockIdx.x + (now.u0 == 0 ? 1 : 0)) * C::kRows * (D + 2);
         float to_common = 0.f;                                    // of row `lane`
         if (lane < C::kRows) {
-            float mx = kNoLogit, sum = 0.f;
+            float mx = kNoLogit;
 #pragma unroll
             for (int v = 0; v < C::kWarps; ++v) mx = fmaxf(mx, stats[v * C::kRows + lane].x);
-#pragma unroll
-            for (int v = 0; v < C::kWarps; ++v) {
-                const float2 s2 = stats[v * C::kRows + lane];
-                sum = fmaf(s2.y, ptx::ex2(s2.x - mx), sum);
-            }
             to_common = ptx::ex2(stats[warp * C::kRows + lane].x - mx + (CT == kE4m3 ? kShift : 0.f));
-            if (warp == 0) total_sh[lane] = make_float2(mx, sum);
+            if (warp == 0) {
+                // The row's factor and place in the output (-1: none); its sum.
+                float sum = 0.f, inv = 1.f;
+#pragma unroll
+                for (int v = 0; v < C::kWarps; ++v) {
+                    const float2 s2 = stats[v * C::kRows + lane];
+                    sum = fmaf(s2.y, ptx::ex2(s2.x - mx), sum);
+                }
+                const int row = r0 + lane, i = row / p.group;
+                const bool live = row < p.rows && i < now.list.ql;
+                const int h = now.hk * p.group + (row - i * p.group);
+                if (!full) {
+                    slot[C::kRows * D + lane] = mx;
+                    slot[C::kRows * (D + 1) + lane] = sum;
+                } else if (live) {
+                    inv = sum != 0.f ? 1.f / sum : 0.f;               // 0: no key was visible
+                    p.lse[((size_t)now.b * p.Hq + h) * p.Sq + i] =
+                        sum != 0.f ? (mx + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+                }
+                total_sh[lane] = make_float2(inv, __int_as_float(live ? i * p.Hq + h : -1));
+            }
         }
         const int m_stage = st == 0 ? C::kStages - 1 : st - 1;
         float* const mine_o = reinterpret_cast<float*>(ring + m_stage * C::kStageBytes);
-        const bool full = now.u0 == 0 && now.u1 == now.list.units;
-        float* slot = p.part + (size_t)(2 * blockIdx.x + (now.u0 == 0 ? 1 : 0)) * C::kRows * (D + 2);
+        uint16_t* const out = p.o + (size_t)now.b * p.Sq * p.Hq * D;
 #pragma unroll
         for (int n0 = 0; n0 < NT; n0 += C::kMergeTiles) {
 #pragma unroll
@@ -903,29 +919,22 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                     o.z += a.z;
                     o.w += a.w;
                 }
-                const float2 ms = total_sh[col];
                 if (full) {
-                    const int row = r0 + col, i = row / p.group;
-                    if (row < p.rows && i < now.list.ql) {
-                        const int h = now.hk * p.group + (row - i * p.group);
-                        const float inv = ms.y != 0.f ? 1.f / ms.y : 0.f;     // 0: no key was visible
+                    const float2 ri = total_sh[col];
+                    const int at = __float_as_int(ri.y);
+                    if (at >= 0) {
                         uint2 r;
-                        r.x = bf ? ptx::pack_bf16x2(o.x * inv, o.y * inv) : ptx::pack_f16x2(o.x * inv, o.y * inv);
-                        r.y = bf ? ptx::pack_bf16x2(o.z * inv, o.w * inv) : ptx::pack_f16x2(o.z * inv, o.w * inv);
-                        *reinterpret_cast<uint2*>(p.o + (((size_t)now.b * p.Sq + i) * p.Hq + h) * D + d) = r;
-                        if (d == 0)
-                            p.lse[((size_t)now.b * p.Hq + h) * p.Sq + i] =
-                                ms.y != 0.f ? (ms.x + log2f(ms.y)) * 0.6931471805599453f : -INFINITY;
+                        r.x = bf ? ptx::pack_bf16x2(o.x * ri.x, o.y * ri.x) : ptx::pack_f16x2(o.x * ri.x, o.y * ri.x);
+                        r.y = bf ? ptx::pack_bf16x2(o.z * ri.x, o.w * ri.x) : ptx::pack_f16x2(o.z * ri.x, o.w * ri.x);
+                        *reinterpret_cast<uint2*>(out + (size_t)at * D + d) = r;
                     }
                 } else {
                     *reinterpret_cast<float4*>(slot + col * D + d) = o;
-                    if (d == 0) {
-                        slot[C::kRows * D + col] = ms.x;
-                        slot[C::kRows * (D + 1) + col] = ms.y;
-                    }
                 }
             }
-            __syncthreads();                                      // the stage is free again
+            // The stage is free for the next tiles; after the last ones, for the
+            // copies, which come after the barrier below.
+            if (n0 + C::kMergeTiles < NT) __syncthreads();
         }
         if (!more) break;
         if (NT > 1) fetch_q(s);                                   // (earlier it would cost registers the sums need)

@@ -105,7 +105,8 @@ inline int block_rows(int rows) { return rows <= 24 ? (rows <= 8 ? 8 : rows <= 1
 
 // CTAs of the attention kernel that fit on an SM at once.
 constexpr int resident_ctas(int D, int rows_per_block, int cache) {
-    return D == 64 && cache == kE4m3 && rows_per_block >= 24 ? 3 : D == 64 || cache == kE4m3 || rows_per_block <= 16 ? 2 : 1;
+    if (D == 64) return rows_per_block == 32 || (rows_per_block == 24 && cache == kE4m3) ? 3 : 2;
+    return cache == kE4m3 || rows_per_block <= 16 ? 2 : 1;
 }
 
 // The attention and the merge of its parts, for one cache type CT (kBf16,
