@@ -685,3 +685,75 @@ def test_value_scales_far_apart(rel_log2, logit_log2):
     w /= w.sum()
     top = float((w * np.repeat(2.0 ** np.maximum(np.array(rel_log2, float), -72), 16)).max() * 448)
     R.check_rows(R.f64(o[0]), R.f64(lse[0]), want, R.step(BF), R.step(FP), 64, n, top, f"{rel_log2} {logit_log2}")
+
+
+def test_the_native_module_and_the_wrappers_own_checks_agree(monkeypatch):
+    """The usual call goes through the native module, others through the wrappers' checks: the same bits, the same
+    refusals."""
+    class Sub(torch.Tensor):
+        pass
+
+    def step(q, k, v, **kw):
+        c = Cache(2, 2, 64, 16, 10, BF, True)
+        c.fill(0, 130, 0), c.fill(1, 40, 1)
+        A.kv_append(k, v, c.k, c.v, c.table, _i32([131, 41]), **c.scales)
+        o, lse = A.attention_paged(q, c.k, c.v, c.table, _i32([131, 41]), **c.scales, **kw)
+        w = A.attention_window(q.repeat(1, 9, 1, 1), k.repeat(1, 9, 1, 1), v.repeat(1, 9, 1, 1), window=3)
+        return [c.k.view(torch.uint8), c.ks.view(torch.int32), c.v.view(torch.uint8), c.vs.view(torch.int32), o, lse, *w]
+
+    q, k, v = _rand((2, 1, 8, 64), BF, 1), _rand((2, 1, 2, 64), BF, 2), _rand((2, 1, 2, 64), BF, 3)
+    want = step(q, k, v)
+    assert A._native is not None
+    c = Cache(1, 2, 64, 16, 10, BF, True)
+    for native in (A._native, None):
+        monkeypatch.setattr(A, "_native", native)
+        for got in (step(q, k, v), step(q.as_subclass(Sub), k.as_subclass(Sub), v),
+                    step(q, k, v, window=2 ** 40, sinks=2 ** 40, scale=0.125),
+                    step(q, k, v, workspace=torch.empty(1 << 22, dtype=torch.uint8, device=DEV)),
+                    step(q, k, v, out=torch.empty_like(q), lse=torch.empty(2, 8, 1, device=DEV))):
+            for a, b in zip(got, want):
+                assert a.shape == b.shape and a.dtype == b.dtype and torch.equal(a, b)
+        with pytest.raises(A.AttnError) as e:
+            A.attention_paged(q[:1], c.k, c.v, c.table, _i32([3]), **c.scales,
+                              workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+        assert e.value.code == A.ATTN_ERR_INVALID_ARG
+        with pytest.raises(A.AttnError):
+            A.kv_append(k[:1], v[:1], c.k[:, :, :8].contiguous(), c.v[:, :, :8].contiguous(), c.table, _i32([3]), **c.scales)
+        with pytest.raises(A.AttnError):
+            A.attention_window(q, k, v, window=0)
+        for kw in (dict(window=-1), dict(out=torch.empty(1, 1, 8, 64, device=DEV)), dict(q_lens=_i32([1, 1])),
+                   dict(k_scale=c.ks[:1]), dict(table=torch.zeros(9, 64, 2, device=DEV)),
+                   dict(table=torch.zeros(0, 32, 2, device=DEV))):
+            with pytest.raises(ValueError):
+                A.attention_paged(q[:1], c.k, c.v, c.table, _i32([3]), **{**c.scales, **kw})
+        with pytest.raises(ValueError):
+            A.kv_append(k[:1], v, c.k, c.v, c.table, _i32([3]), **c.scales)
+        with pytest.raises(ValueError):
+            A.attention_window(q, k, v[:, :, :1], window=3)
+    assert _status() == A.ATTN_OK
+
+
+def test_native_calls_of_threads_and_streams_keep_apart():
+    """Threads and side streams that call at once, through the native module."""
+    import threading
+    c = Cache(3, 2, 128, 16, 300, BF, True)
+    for b in range(3):
+        c.fill(b, [4700, 4000, 1][b], b)
+    kv = _i32([4700, 4000, 1])
+    qs = [_rand((3, 1, 8, 128), BF, 70 + i) for i in range(4)]
+    want = [A.attention_paged(q, c.k, c.v, c.table, kv, **c.scales) for q in qs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        s = torch.cuda.Stream() if i % 2 else torch.cuda.current_stream()
+        with torch.cuda.stream(s):
+            for _ in range(50):
+                o, lse = A.attention_paged(qs[i], c.k, c.v, c.table, kv, **c.scales)
+                s.synchronize()
+                if not (torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])):
+                    bad.append(i)
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    [x.start() for x in ts], [x.join() for x in ts]
+    assert not bad

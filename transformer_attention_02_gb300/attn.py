@@ -1,7 +1,8 @@
 """Python binding of the C ABI declared in ``include/attn.h``.
 
 Argument marshalling only: every step of the attention runs in the CUDA
-library ``libattn.so``. There is no fallback of any kind; if the library has
+library ``libattn.so`` (the calls of a decode step reach it through the native
+module ``_binding``, the others through ctypes). There is no fallback of any kind; if the library has
 not been built, or the device is not an sm_103 GPU, the calls fail loudly.
 
 ``attn_fwd`` and the other functions keep the C names and take raw device
@@ -580,18 +581,27 @@ def attention_block(x, ln_gamma, ln_beta, w_qkv, b_qkv, w_o, b_o, *, Hq: int, Hk
 
 
 # ------------------------------------------- windows and the paged key/value cache
-# These wrappers run once per layer and decode step, so they are written for few
-# interpreter steps: one condition over everything, and the message sought only
-# once it has failed.
+# These wrappers run once per layer and decode step, so the usual call (tensors as
+# they should be, on the current device and stream) goes through the native module
+# _binding, from one interpreter step to the C ABI. What it leaves alone comes to
+# the checks here: one condition over everything, and the message sought only once
+# it has failed.
 
 _torch = None
+_native = None
 _NAN = float("nan")
 
 
 def _bind():
-    """torch, imported at first use (the C ABI above needs none)."""
-    global _torch
+    """torch and the native module, imported at first use (the C ABI above needs neither)."""
+    global _torch, _native
     import torch
+    lib()
+    if not os.path.exists(_build.BINDING):
+        raise RuntimeError(
+            f"{_build.BINDING} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
+    from . import _binding
+    _native = _binding
     _torch = torch
     return torch
 
@@ -667,9 +677,9 @@ _HELD_BYTES = 32 << 20                              # larger workspaces (long ch
 
 
 class _Held(threading.local):
-    """Workspace of a thread's calls on a device's default stream, as {device: (tensor, address, bytes)}. Calls of one
-    thread on one stream run in order, so they may share it; another thread could enqueue between a call's two kernels,
-    another stream run beside them, and a captured call is replayed at any time, so all those get their own."""
+    """Workspace of a thread's calls on a device's default stream, as {device: tensor}. Calls of one thread on
+    one stream run in order, so they may share it; another thread could enqueue between a call's two kernels, another
+    stream run beside them, and a captured call is replayed at any time, so all those get their own."""
 
     def __init__(self):
         self.by_device = {}
@@ -684,10 +694,9 @@ def _workspace(q, at, size, handle, stream):
         t = _new(size, _torch.uint8, q, stream)
         return t.data_ptr(), size, t
     held = _held.by_device.get(at)
-    if held is None or held[2] < size:
-        t = _torch.empty(size, dtype=_torch.uint8, device=q.device)
-        held = _held.by_device[at] = (t, t.data_ptr(), size)
-    return held[1], held[2], held[0]
+    if held is None or held.numel() < size:
+        held = _held.by_device[at] = _torch.empty(size, dtype=_torch.uint8, device=q.device)
+    return held.data_ptr(), held.numel(), held
 
 
 def _outputs(q, at, out, lse, stream):
@@ -712,6 +721,12 @@ def attention_window(q, k, v, *, window: int, sinks: int = 0, scale=None, out=No
     The query at position p (its row plus Sk - Sq) sees the last `window` keys up to p, its own included, and the first
     `sinks` keys. scale: None selects 1/sqrt(D). out/lse: optional preallocated outputs.
     """
+    if _native is not None and stream is None:
+        done = _native.attention_window(q, k, v, window, sinks, scale, out, lse)
+        if done is not None:
+            if done.__class__ is int:
+                raise AttnError(done, "attn_fwd_window")
+            return done
     at = _device_of(q, "q")
     qs, ks = q.shape, k.shape
     B, Sq, Hq, D = qs
@@ -770,7 +785,7 @@ def _cache_args(x, xname, at, k_cache, v_cache, k_scale, v_scale, block_table, k
             nl = lens.data_ptr()
         if table is not None:
             ok = (ok and table.dtype is f32 and table.dim() == 3 and table.shape[1] == D // 2 and table.shape[2] == 2
-                  and table.get_device() == at and table.is_contiguous())
+                  and table.shape[0] > 0 and table.get_device() == at and table.is_contiguous())
             rope, max_pos = table.data_ptr(), table.shape[0]
         if ok:
             return (kind, ks, vs, block_table.data_ptr(), kv_lens.data_ptr(), nl, Hkv, D, page, max_pages, n_pages, rope,
@@ -797,7 +812,8 @@ def _cache_fault(x, xname, at, k_cache, v_cache, k_scale, v_scale, block_table, 
     if k_cache.dtype is x.dtype and (k_scale is not None or v_scale is not None):
         return "a 16-bit cache has no scales"
     if table is not None and (table.dtype is not torch.float32 or table.dim() != 3
-                              or tuple(table.shape[1:]) != (k_cache.shape[3] // 2, 2) or table.get_device() != at
+                              or tuple(table.shape[1:]) != (k_cache.shape[3] // 2, 2) or table.shape[0] == 0
+                              or table.get_device() != at
                               or not table.is_contiguous()):
         return "table must be the (max_pos, D/2, 2) FP32 CUDA tensor of rope_table() for this D"
     return ("k_scale and v_scale must be contiguous FP32 CUDA tensors of shape (n_pages, Hkv): an 8-bit cache needs its "
@@ -814,6 +830,12 @@ def kv_append(k, v, k_cache, v_cache, block_table, kv_lens, *, new_lens=None, k_
     each) are int32; kv_lens counts the step's tokens already: token s of sequence b goes to position
     kv_lens[b] - new_lens[b] + s. table: rope_table() to rotate the keys to their positions, or None.
     """
+    if _native is not None and stream is None:
+        rc = _native.kv_append(k, v, k_cache, v_cache, block_table, kv_lens, new_lens, k_scale, v_scale, table)
+        if rc is not None:
+            if rc:
+                raise AttnError(rc, "attn_kv_append")
+            return
     at = _device_of(k, "k")
     kind, ks, vs, bt, kl, nl, Hkv, D, page, max_pages, n_pages, rope, max_pos = _cache_args(
         k, "k", at, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, new_lens, "new_lens", table)
@@ -845,6 +867,13 @@ def attention_paged(q, k_cache, v_cache, block_table, kv_lens, *, q_lens=None, k
     uint8 CUDA tensor of at least attn_paged_workspace_bytes bytes; when omitted, one that the calling thread keeps for
     the device's default stream, or, on another stream or under capture, a new one.
     """
+    if _native is not None and stream is None:
+        done = _native.attention_paged(q, k_cache, v_cache, block_table, kv_lens, q_lens, k_scale, v_scale, table, window,
+                                       sinks, scale, out, lse, workspace, _held.by_device.get(q.get_device()), _HELD_BYTES)
+        if done is not None:
+            if done.__class__ is int:
+                raise AttnError(done, "attn_fwd_paged")
+            return done
     at = _device_of(q, "q")
     kind, ks, vs, bt, kl, nl, Hkv, D, page, max_pages, n_pages, rope, max_pos = _cache_args(
         q, "q", at, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, q_lens, "q_lens", table)
