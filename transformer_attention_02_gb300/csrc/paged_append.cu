@@ -81,7 +81,13 @@ __device__ __forceinline__ float block_scale(float a) {
 // same slots and dims of each, so that a page's table entries come from L1
 // after the first head. A block's new values stay in registers (FP32, rotated)
 // between the pass that finds their maximum and the one that writes them.
-// Bound by memory: each input is read and each code written once.
+// Bound by memory: each input is read and each code written once. Measured: 4 x
+// 2048 tokens of 32 heads of 128 into e4m3 pages of 64 (bf16, rotated) 41 us,
+// 5.0 TB/s of the 6.70 a copy reaches; the conversions and the block's maximum
+// stand between a block's loads and its stores, and the next block's loads
+// overlap only in part (staging them by asynchronous copies: 43 to 47 us). Few
+// tokens are bound by latency: one token of 64 sequences 2.4 us, 8 x 500 tokens
+// into 16-bit pages 4.1 us.
 template <bool E4M3, int HELD, bool BF16>
 __global__ void __launch_bounds__(max_threads(HELD), min_ctas(HELD)) append_kernel(const AppendParams p) {
     __shared__ float red[2][max_threads(HELD) / 32];
@@ -239,7 +245,8 @@ __global__ void __launch_bounds__(max_threads(HELD), min_ctas(HELD)) append_kern
 
 int launch_append(AppendParams p, int cache, int num_sms, cudaStream_t stream) {
     // Heads a CTA takes in turn: table entries are read once per group, but only
-    // where the blocks fill the SMs several times over without it.
+    // where the blocks fill the SMs several times over without it. (4 x 2048
+    // tokens, 32 heads into e4m3: 1, 2, 3, 4 heads 56, 44.7, 41.9, 40.8 us.)
     const long long blocks = (long long)p.B * p.touched * p.Hkv * 2;
     p.head_group = (int)std::max(1LL, std::min<long long>(std::min(p.Hkv, 4), blocks / (8LL * num_sms)));
     const int groups = (p.Hkv + p.head_group - 1) / p.head_group;

@@ -103,7 +103,7 @@ struct AttendParams {
 // products' eight rows, at most 32.
 inline int block_rows(int rows) { return rows <= 24 ? (rows <= 8 ? 8 : rows <= 16 ? 16 : 24) : 32; }
 
-// CTAs of the attention kernel that fit on an SM at once.
+// CTAs of the attention kernel on an SM at once (the reasons stand at Cfg).
 constexpr int resident_ctas(int D, int rows_per_block, int cache) {
     if (D == 64) return rows_per_block == 32 || (rows_per_block == 24 && cache == kE4m3) ? 3 : 2;
     return cache == kE4m3 || rows_per_block <= 16 ? 2 : 1;
@@ -118,8 +118,8 @@ int launch_attend(bool (&attr_set)[2][4], const AttendParams& p, int D, cudaStre
 // An attention goes by the gathered pages (paged_gather.cu) from kChunkRows
 // queries a sequence and kChunkTiles tiles of 256 rows of a head: a third of the
 // SMs. Measured over e4m3, 32/8 heads of 128, by the cache itself / gathered: 16
-// sequences of 8192 keys, 128 queries 1114 / 511 us, 256 queries 2194 / 559; one
-// sequence of 32768 keys, 128 queries (32 tiles) 272 / 406.
+// sequences of 8192 keys, 128 queries 1048 / 512 us, 256 queries 2065 / 561; one
+// sequence of 32768 keys, 128 queries (32 tiles) 256 / 406.
 constexpr int kChunkRows = 128;
 constexpr int kChunkTiles = 48;
 constexpr long long kChunkLimit = 4LL << 30;     // bytes of gathered tensors at most
