@@ -30,7 +30,7 @@ SOURCES = [os.path.join(CSRC, f) for f in
             "paged_attn_bf16.cu", "paged_attn_f16.cu", "paged_attn_e4m3.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in
                      ("attn_kernel.cuh", "ptx.cuh", "attn_launch.h", "attn_fwd_inst.cuh", "block_params.h",
-                      "gemm_kernel.cuh", "paged_params.h", "paged_attn.cuh")] + [
+                      "gemm_kernel.cuh", "early_launch.h", "paged_params.h", "paged_attn.cuh")] + [
     os.path.join(ROOT, "include", "attn.h")]
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

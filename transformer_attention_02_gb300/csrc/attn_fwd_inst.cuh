@@ -23,7 +23,13 @@ int launch_fwd(bool& attr_set, const CUtensorMap& tq, const CUtensorMap& tk, con
             return ATTN_ERR_CUDA;
         attr_set = true;
     }
-    kernel<<<grid, kernel_threads(ROPE), smem, stream>>>(tq, tk, tv, to, p);
+    if constexpr (WINDOW) {
+        if (launch_early(kernel, (unsigned)grid, (unsigned)kernel_threads(ROPE), (size_t)smem, stream, tq, tk, tv, to,
+                                p) != cudaSuccess)
+            return ATTN_ERR_CUDA;
+    } else {
+        kernel<<<grid, kernel_threads(ROPE), smem, stream>>>(tq, tk, tv, to, p);
+    }
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -46,6 +46,7 @@
 #include <cuda_fp16.h>
 #include <cstdint>
 
+#include "early_launch.h"
 #include "ptx.cuh"
 
 namespace attn {
@@ -206,11 +207,11 @@ struct TileInfo {
 // from the oldest key of its first row's window to its last row's own key.
 // Both sub-tiles walk the same list; the upper one, whose windows begin 128
 // keys later, passes over the window's first block unless sinks lie in it.
-// Measured: 16384 tokens, 32/8 heads of 128, window 4096 and 4 sinks, bf16: 711
-// us, 1354 TFLOP/s of visible pairs (0.69 of a large library product; the plain
+// Measured: 16384 tokens, 32/8 heads of 128, window 4096 and 4 sinks, bf16: 709
+// us, 1358 TFLOP/s of visible pairs (0.69 of a large library product; the plain
 // causal variant reaches 0.72 to 0.77). Narrow windows are bound by the softmax
 // of whole blocks and by the tiles' ends: 4 x 2048 tokens, 32 heads of 64,
-// window 512, fp16: 75 us, five blocks a row for four visible ones.
+// window 512, fp16: 72 us, five blocks a row for four visible ones.
 constexpr int kSkipsFirst = 1 << 30;
 template <bool CAUSAL, bool PACK, bool WINDOW = false, bool RAGGED = false>
 __device__ __forceinline__ TileInfo tile_info(int tile, const FwdParams& p) {
@@ -1189,6 +1190,12 @@ __global__ void __launch_bounds__(kernel_threads(ROPE), 1)
     ptx::tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const SyncCtx sc{abort_flag, p.status, p.timeout_ns};
+    if (WINDOW) {
+        // Launched while the kernel before it drains: nothing above touches
+        // global memory, nothing below starts before everything earlier is done.
+        wait_for_inputs();
+        let_next_start();
+    }
 
     if (warp < 8) {
         ptx::setmaxnreg_inc<softmax_regs(ROPE)>();

@@ -34,7 +34,7 @@
 // Measured (attention and merge, graph replay; the copy bandwidth of the same
 // GPU is 6.70 TB/s): 16 sequences of 8192 keys, 8 K/V heads of 128, 4 query rows
 // a head: e4m3 49.4 us, 5.43 TB/s, 16-bit 85.5 us, 6.27 TB/s; 32 heads of one
-// row over 16-bit keys (8 x 8192, 1.07 GB) 161 us, 6.67 TB/s. About 9 us of each
+// row over 16-bit keys (16 x 4096, 1.07 GB) 161 us, 6.67 TB/s. About 9 us of each
 // are the ends: the chain lengths - page numbers - first keys (4), the last
 // stages and their merge (3), the second kernel (2). More rows over e4m3: 16
 // rows 54.6 us, 24 64.4, 32 77.3; there the tensor cores and the conversions

@@ -7,38 +7,13 @@
 
 #include <cstdint>
 
+#include "early_launch.h"
+
 namespace attn {
 namespace paged {
 
 // Storage of the cache, with the type of the tensor-core operands it implies.
 constexpr int kBf16 = 0, kF16 = 1, kE4m3 = 2;
-
-// Launches a kernel that may become resident while the kernel before it in the
-// stream drains (programmatic dependent launch). Such a kernel begins with
-// wait_for_inputs(): nothing of it touches memory before everything earlier in
-// the stream has finished and is visible. Saves most of the launch latency
-// between the steps of a decode loop.
-template <typename... Params, typename... Args>
-cudaError_t launch_early(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
-                         Args... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-#ifdef __CUDACC__
-__device__ __forceinline__ void wait_for_inputs() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// The next kernel of the stream may become resident from here on.
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-#endif
 
 // Device values that are out of range (page numbers, lengths, positions) set
 // this bit of the device status word; what they name is left out.
@@ -118,8 +93,8 @@ int launch_attend(bool (&attr_set)[2][4], const AttendParams& p, int D, cudaStre
 // An attention goes by the gathered pages (paged_gather.cu) from kChunkRows
 // queries a sequence and kChunkTiles tiles of 256 rows of a head: a third of the
 // SMs. Measured over e4m3, 32/8 heads of 128, by the cache itself / gathered: 16
-// sequences of 8192 keys, 128 queries 1048 / 512 us, 256 queries 2065 / 561; one
-// sequence of 32768 keys, 128 queries (32 tiles) 256 / 406.
+// sequences of 8192 keys, 128 queries 939 / 507 us, 256 queries 1853 / 564; one
+// sequence of 32768 keys, 128 queries (32 tiles) 242 / 406.
 constexpr int kChunkRows = 128;
 constexpr int kChunkTiles = 48;
 constexpr long long kChunkLimit = 4LL << 30;     // bytes of gathered tensors at most
