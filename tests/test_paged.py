@@ -757,3 +757,59 @@ def test_native_calls_of_threads_and_streams_keep_apart():
     ts = [threading.Thread(target=work, args=(i,)) for i in range(4)]
     [x.start() for x in ts], [x.join() for x in ts]
     assert not bad
+
+
+@pytest.mark.parametrize("native", [True, False])
+def test_empty_problems(native, monkeypatch):
+    """No sequence, no token, no page: nothing is launched or written, and shapes come back."""
+    c = Cache(2, 2, 64, 16, 3, BF, True)
+    c.fill(0, 20, 0), c.fill(1, 5, 1)
+    A.attention_paged(_rand((2, 1, 8, 64), BF, 0), c.k, c.v, c.table, _i32([20, 5]), **c.scales)
+    if not native:
+        monkeypatch.setattr(A, "_native", None)
+    was = [t.clone() for t in (c.k.view(torch.uint8), c.v.view(torch.uint8), c.ks.view(torch.int32))]
+    for B, S in ((0, 1), (2, 0), (0, 0)):
+        table, lens = c.table[:B].contiguous(), _i32([20, 5][:B])
+        k = torch.empty((B, S, 2, 64), dtype=BF, device=DEV)
+        A.kv_append(k, k, c.k, c.v, table, lens, **c.scales)
+        o, lse = A.attention_paged(torch.empty((B, S, 8, 64), dtype=BF, device=DEV), c.k, c.v, table, lens, **c.scales)
+        assert o.shape == (B, S, 8, 64) and lse.shape == (B, 8, S)
+        w, wl = A.attention_window(torch.empty((B, S, 8, 64), dtype=BF, device=DEV), k, k, window=4)
+        assert w.shape == (B, S, 8, 64) and wl.shape == (B, 8, S)
+    with pytest.raises(A.AttnError):
+        A.attention_paged(_rand((2, 1, 8, 64), BF, 0), c.k, c.v, c.table[:, :0].contiguous(), _i32([20, 5]), **c.scales)
+    o, lse = A.attention_window(_rand((1, 3, 2, 64), BF, 1), *[torch.empty((1, 0, 1, 64), dtype=BF, device=DEV)] * 2, window=2)
+    assert bool((o == 0).all()) and bool((lse == float("-inf")).all())
+    assert all(torch.equal(a, b) for a, b in zip(was, (c.k.view(torch.uint8), c.v.view(torch.uint8), c.ks.view(torch.int32))))
+    assert _status() == A.ATTN_OK
+
+
+def test_a_windowed_prompt_follows_the_kernel_that_makes_its_inputs():
+    """The windowed kernel starts while its producer drains: a chain of producers and windows in a graph and eagerly."""
+    B, S, H, D = 2, 700, 8, 128
+    x = _rand((B, S, H, D), BF, 5)
+    table = A.rope_table(2048, D)
+
+    def chain(x):
+        for i in range(6):
+            q = A.rope_apply(x, table, pos0=i)
+            o, _ = A.attention_window(q, q, x, window=100 + i, sinks=3)
+            x = (o + x).contiguous()
+        return x
+
+    want = x
+    for i in range(6):                                   # the same with a synchronisation at every step
+        q = A.rope_apply(want, table, pos0=i)
+        torch.cuda.synchronize()
+        o, _ = A.attention_window(q, q, want, window=100 + i, sinks=3)
+        torch.cuda.synchronize()
+        want = (o + want).contiguous()
+    assert torch.equal(chain(x), want)
+    static = x.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = chain(static)
+    for _ in range(5):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
