@@ -70,9 +70,9 @@ def test_attention_arguments(kw, code):
 
 def test_workspace_size():
     # 148 SMs assumed without a GPU: (B + 1) sequence offsets, then two parts of rows x (D + 2) FP32 per CTA; rows
-    # come in blocks of 8, 16, 24 or 32, two CTAs an SM, three for blocks of 24 (8-bit) and 32 rows of 64
-    assert A.attn_paged_workspace_bytes(16, 32, 8, 1, 128) == 256 + 148 * 2 * 2 * 8 * 130 * 4
-    assert A.attn_paged_workspace_bytes(16, 32, 8, 4, 64) == 256 + 148 * 2 * 2 * 16 * 66 * 4
+    # come in blocks of 8, 16, 24 or 32, three CTAs an SM, two for blocks of 24 and 32 rows of 128
+    assert A.attn_paged_workspace_bytes(16, 32, 8, 1, 128) == 256 + 148 * 3 * 2 * 8 * 130 * 4
+    assert A.attn_paged_workspace_bytes(16, 32, 8, 4, 64) == 256 + 148 * 3 * 2 * 16 * 66 * 4
     assert A.attn_paged_workspace_bytes(1, 32, 1, 9, 64) == 256 + 148 * 3 * 2 * 32 * 66 * 4
     assert A.attn_paged_workspace_bytes(1, 32, 1, 9, 128) == 256 + 148 * 2 * 2 * 32 * 130 * 4
     # a short table bounds the CTAs: 8 segments of 5 units (577 keys), one more for sinks, and the schedule's lead

@@ -95,7 +95,7 @@ long long span_bound(long long max_keys) { return (max_keys + paged::kUnit - 1) 
 // lists could give work to (max_keys 0: any length).
 int attend_ctas(int B, int Hkv, int rows, int D, int cache, long long max_keys, int sms) {
     const int rb = paged::block_rows(rows);
-    const long long all = (long long)sms * paged::resident_ctas(D, rb, cache);
+    const long long all = (long long)sms * paged::plan_of(D, rb, cache).ctas;
     if (max_keys <= 0) return (int)all;
     const long long segments = (long long)B * Hkv * ((rows + rb - 1) / rb);
     return (int)std::min(all, segments > all ? all : segments * span_bound(max_keys));
@@ -267,8 +267,10 @@ size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, long lo
     const int rows = Sq * (Hq / Hkv);
     ChunkLayout chunk;
     if (chunk_layout(B, Hq, Hkv, Sq, D, max_keys, &chunk)) return chunk.total;
-    // (the 8-bit cache's CTAs are the more, where the two differ)
-    return attend_workspace(B, rows, D, attend_ctas(B, Hkv, rows, D, paged::kE4m3, max_keys, device_sm_count()), &part_off);
+    // (enough for either kind of cache)
+    const int sms = device_sm_count(), ctas = std::max(attend_ctas(B, Hkv, rows, D, paged::kE4m3, max_keys, sms),
+                                                       attend_ctas(B, Hkv, rows, D, paged::kBf16, max_keys, sms));
+    return attend_workspace(B, rows, D, ctas, &part_off);
 }
 
 int attn_fwd_paged(const void* q, long long q_stride, const void* k_cache, const void* v_cache, const float* k_scale,

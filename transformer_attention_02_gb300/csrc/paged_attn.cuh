@@ -33,12 +33,12 @@
 //
 // Measured (attention and merge, graph replay; the copy bandwidth of the same
 // GPU is 6.70 TB/s): 16 sequences of 8192 keys, 8 K/V heads of 128, 4 query rows
-// a head: e4m3 49.4 us, 5.43 TB/s, 16-bit 85.5 us, 6.27 TB/s; 32 heads of one
-// row over 16-bit keys (16 x 4096, 1.07 GB) 161 us, 6.67 TB/s. About 9 us of each
-// are the ends: the chain lengths - page numbers - first keys (4), the last
-// stages and their merge (3), the second kernel (2). More rows over e4m3: 16
-// rows 54.6 us, 24 64.4, 32 77.3; there the tensor cores and the conversions
-// before them (417 instructions for 16 keys and 24 rows) wait on one another.
+// a head: e4m3 47.2 us, 5.69 TB/s, 16-bit 85.4 us, 6.28 TB/s; 32 heads of one
+// row over 16-bit keys (16 x 4096, 1.07 GB) 161 us, 6.67 TB/s. What is left are
+// the ends: the chain lengths - page numbers - first keys (2 us), SMs that finish
+// 3 to 4 us apart, the second kernel (2). More rows over e4m3: 16 rows 52.8 us,
+// 24 58.9, 32 69.0; there the tensor cores, the conversions before them and the
+// softmax of a stage wait on one another.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -62,21 +62,24 @@ struct Cfg {
     static constexpr int kRowBytes = D * kElt;
     static constexpr int kChunks = kRowBytes / 16;
     static constexpr int kRows = 8 * NT;                         // query rows of a row block
-    // Sixteen warps an SM, in two CTAs, while 128 registers hold a warp's sums;
-    // else eight to twelve, in CTAs of four where their rings fit, because the
-    // CTAs cover one another's change of segment (barriers, merge, queries).
-    // Measured over e4m3, 8 K/V heads, 256 x 512 keys / 16 x 8192: 20 rows of
-    // 128: one CTA of eight warps 140.0 / 70.3 us, two of four 104.5 / 64.3;
-    // 20 rows of 64: two of eight (spilling) 78.9 / 46.5, three of four 70.2 /
-    // 47.0; 4 rows of 128: two of eight 63.5 / 49.0, four of four 56.6 / 50.7
-    // (not taken: long contexts are the more usual).
-    static constexpr int kResident = resident_ctas(D, kRows, CT);
-    static constexpr int kWarps = kResident == 3 || (kResident == 2 && (kRowBytes == 256 || (D == 128 && NT >= 3))) ? 4 : 8;
-    static constexpr int kKeys = kRowBytes == 64 ? 32 : 16;      // keys of a stage
+    // Eight to twelve warps an SM hold a wide block's sums in registers; CTAs of
+    // four warps cover one another's change of segment (barriers, merge, queries),
+    // and stages of 32 keys (64 of 64 8-bit dims) spend one look at the queries'
+    // fragments, one vote and one turn of the loop on two (four) tiles. Measured
+    // over e4m3, 8 K/V heads, 16 x 8192 keys / 256 x 512:
+    //   4 rows of 128   two CTAs of eight warps, 16 keys 49.5 / 62.6 us, three of four, 32 keys 47.3 / 57.6
+    //   16 rows of 128  two of eight, 16 keys 54.6 / 86.5, two of four, 32 keys 53.3 / 76.5, three of four 52.9 / 71.4
+    //   20 rows of 128  one of eight, 16 keys 70.3 / 140.0, two of four 63.4 / 96.6, 32 keys 58.0 / 91.2
+    //   32 rows of 128  two of four, 16 keys 77.0 / 116.5, 32 keys 69.0 / 108.5
+    //   4 rows of 64    two of eight, 32 keys 29.1 / 46.6, three of four, 64 keys 28.5 / 39.3
+    //   20 rows of 64   three of four, tile by tile 47.0 / 67.5, both tiles of 32 keys together 39.1 / 60.3
+    // 16-bit caches, 16 x 8192: 4 rows of 64 two of eight, 16 keys 46.8, three of
+    // four, 32 keys 46.1; 24 rows of 128 one of eight 92.3, two of four 94.7.
+    static constexpr Plan kPlan = plan_of(D, kRows, CT);
+    static constexpr int kResident = kPlan.ctas, kWarps = kPlan.warps, kKeys = kPlan.keys, kStages = kPlan.stages;
     static constexpr int kTiles = kKeys / 16;
     static constexpr int kCopies = 16 * kChunks / 32;            // 16-byte copies a lane makes for 16 keys
     static constexpr int kStageBytes = 2 * kKeys * kRowBytes;
-    static constexpr int kStages = CT == kE4m3 && D == 128 && NT >= 3 ? 5 : 3;    // (as many as fit)
     static constexpr int kRingBytes = kStages * kStageBytes;     // of one warp
     static constexpr bool kQShared = D * NT >= 192;              // Q fragments in shared memory, not registers
     static constexpr int kQStride = D * 2 + 16;                  // bytes of a query row: conflict-free fragment reads
@@ -491,6 +494,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                 const int off = ((ld_i + lane / C::kTiles) * C::kWarps + warp) * C::kKeys + lane % C::kTiles * 16;
                 const int key = off + (off < u.y ? u.z : u.w);
                 ids = -1;
+                sc = make_float2(1.f, 1.f);
                 if (off < u.x && key < w.x) {
                     ids = __ldg(p.block_table + (size_t)w.z * p.max_pages + (key >> p.page_shift));
                     if ((unsigned)ids >= (unsigned)p.n_pages) {
@@ -509,13 +513,13 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                 const int id = __shfl_sync(0xffffffffu, ids, first + m);
                 const int k0 = off0 + 16 * m + (off0 + 16 * m < u.y ? u.z : u.w);
                 if (lane == 0) keys_sh[ld_stage * C::kTiles + m] = id >= 0 ? k0 : kNoKey;
-                if (id < 0) continue;
+                if (C::kTiles == 1 && id < 0) continue;       // (its stage is passed over)
                 const uint32_t slot = (uint32_t)(k0 & ((1 << p.page_shift) - 1));
-                const uint64_t at = (uint64_t)(uint32_t)id * page_bytes + (head_off + slot * C::kRowBytes);
+                const uint64_t at = (uint64_t)(uint32_t)max(id, 0) * page_bytes + (head_off + slot * C::kRowBytes);
                 const uint8_t* ks = static_cast<const uint8_t*>(p.k_cache) + at;
                 const uint8_t* vs = static_cast<const uint8_t*>(p.v_cache) + at;
                 const uint32_t kd = dst + m * 16 * C::kRowBytes, vd = kd + C::kKeys * C::kRowBytes;
-                if (k0 + 16 <= w.x && (k0 >= w.y || k0 + 16 <= sinks)) {
+                if ((C::kTiles == 1 || id >= 0) && k0 + 16 <= w.x && (k0 >= w.y || k0 + 16 <= sinks)) {
 #pragma unroll
                     for (int c = 0; c < C::kCopies; ++c) {
                         cp_async16(kd + copy_to(c), ks + c * 512);
@@ -526,7 +530,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
 #pragma unroll
                     for (int c = 0; c < C::kCopies; ++c) {
                         const int key = k0 + (c * 32 + lane) / C::kChunks;
-                        const bool take = key < w.x && (key >= w.y || key < sinks);
+                        const bool take = id >= 0 && key < w.x && (key >= w.y || key < sinks);
                         cp_async16(kd + copy_to(c), ks + c * 512, take);
                         cp_async16(vd + copy_to(c), vs + c * 512, take);
                     }
@@ -695,63 +699,87 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
             cp_async_wait<C::kStages - 2>();
             __syncwarp();
             issue();
-#pragma unroll 1
-            for (int m = 0; m < C::kTiles; ++m) {
-                const int k0 = keys_sh[st * C::kTiles + m];
-                if (k0 == kNoKey) continue;                   // nothing there, or a page out of range
-                const uint32_t ka = ring_a + st * C::kStageBytes + m * 16 * C::kRowBytes + k_off;
-                const uint32_t va = ring_a + st * C::kStageBytes + (C::kKeys + m * 16) * C::kRowBytes + v_off;
+            // All tiles of a stage together: one look at the queries' fragments, one
+            // vote. The first key of each; kNoKey: nothing there, or a page out of
+            // range (its rows are zeros, and hidden).
+            constexpr int M = C::kTiles;
+            int k0[M];
+            bool none = true, whole = true;
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                k0[m] = keys_sh[st * M + m];
+                none &= k0[m] == kNoKey;
+                whole &= k0[m] + 15 <= pos_lo && (k0[m] >= pos_hi - p.window + 1 || p.window == 0 || k0[m] + 16 <= sinks);
+            }
+            if (!none) {
+                const uint32_t ka = ring_a + st * C::kStageBytes + k_off;
+                const uint32_t va = ring_a + st * C::kStageBytes + C::kKeys * C::kRowBytes + v_off;
                 // ---- S^T = K Q^T
-                float s[NT][4];
+                float s[M][NT][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-                {
+                for (int m = 0; m < M; ++m)
 #pragma unroll
-                    for (int c = 0; c < C::kChunks / 2; ++c) {
-                        uint32_t r[4];
-                        ldmatrix4<false>(r, ka ^ (uint32_t)(c << 5));
-                        if (CT == kE4m3) {
+                    for (int n = 0; n < NT; ++n) s[m][n][0] = s[m][n][1] = s[m][n][2] = s[m][n][3] = 0.f;
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const uint32_t a0 = e4m3_lo(r[2 * h]), a1 = e4m3_lo(r[2 * h + 1]),
-                                               a2 = e4m3_hi(r[2 * h]), a3 = e4m3_hi(r[2 * h + 1]);
+                for (int c = 0; c < C::kChunks / 2; ++c) {
+                    uint32_t r[M][4];
 #pragma unroll
-                                for (int n = 0; n < NT; ++n) {
-                                    uint2 q2;
-                                    if constexpr (C::kQShared)
-                                        q2 = frag_sh[((2 * c + h) * NT + n) * 32 + lane];
-                                    else
-                                        q2 = make_uint2(qf[2 * c + h][n][0], qf[2 * c + h][n][1]);
-                                    mma16816<false>(s[n], a0, a1, a2, a3, q2.x, q2.y);
-                                }
+                    for (int m = 0; m < M; ++m) ldmatrix4<false>(r[m], (ka ^ (uint32_t)(c << 5)) + m * 16 * C::kRowBytes);
+                    if (CT == kE4m3) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t a[M][4];
+#pragma unroll
+                            for (int m = 0; m < M; ++m) {
+                                a[m][0] = e4m3_lo(r[m][2 * h]);
+                                a[m][1] = e4m3_lo(r[m][2 * h + 1]);
+                                a[m][2] = e4m3_hi(r[m][2 * h]);
+                                a[m][3] = e4m3_hi(r[m][2 * h + 1]);
                             }
-                        } else {
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
                                 uint2 q2;
                                 if constexpr (C::kQShared)
-                                    q2 = frag_sh[(c * NT + n) * 32 + lane];
+                                    q2 = frag_sh[((2 * c + h) * NT + n) * 32 + lane];
                                 else
-                                    q2 = make_uint2(qf[c][n][0], qf[c][n][1]);
-                                mma16816<kBf>(s[n], r[0], r[1], r[2], r[3], q2.x, q2.y);
+                                    q2 = make_uint2(qf[2 * c + h][n][0], qf[2 * c + h][n][1]);
+#pragma unroll
+                                for (int m = 0; m < M; ++m)
+                                    mma16816<false>(s[m][n], a[m][0], a[m][1], a[m][2], a[m][3], q2.x, q2.y);
                             }
+                        }
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            uint2 q2;
+                            if constexpr (C::kQShared)
+                                q2 = frag_sh[(c * NT + n) * 32 + lane];
+                            else
+                                q2 = make_uint2(qf[c][n][0], qf[c][n][1]);
+#pragma unroll
+                            for (int m = 0; m < M; ++m)
+                                mma16816<kBf>(s[m][n], r[m][0], r[m][1], r[m][2], r[m][3], q2.x, q2.y);
                         }
                     }
                 }
                 // ---- logits in log2 units; hidden keys to -inf
-                float ks = 1.f, vs = 1.f, lv = 0.f;
-                if (CT == kE4m3) {
-                    const float2 kv2 = *reinterpret_cast<const float2*>(scales + (st * C::kTiles + m) * 2);
-                    ks = kv2.x;
-                    vs = kv2.y * kShiftDown;
-                    lv = fminf(fmaxf(__log2f(fabsf(kv2.y)), -72.f), 120.f) - kShift;
+                float vs[M], lv[M], f[M][NT][2];                   // f: log2 units per value of s
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    float ks = 1.f;
+                    vs[m] = 1.f;
+                    lv[m] = 0.f;
+                    if (CT == kE4m3) {
+                        const float2 kv2 = *reinterpret_cast<const float2*>(scales + (st * M + m) * 2);
+                        ks = kv2.x;
+                        vs[m] = kv2.y * kShiftDown;
+                        lv[m] = fminf(fmaxf(__log2f(fabsf(kv2.y)), -72.f), 120.f) - kShift;
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) f[m][n][e] = CT == kE4m3 ? cf[n][e] * ks : p.scale_log2;
                 }
-                const bool whole = k0 + 15 <= pos_lo && (k0 >= pos_hi - p.window + 1 || p.window == 0 || k0 + 16 <= sinks);
-                float f[NT][2];                                    // log2 units per value of s
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) f[n][e] = CT == kE4m3 ? cf[n][e] * ks : p.scale_log2;
                 if (!whole) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
@@ -759,31 +787,39 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                         for (int e = 0; e < 2; ++e) {
                             const int pos = pos0 + (r0 + 8 * n + 2 * t + e) / p.group;
                             const int lo = p.window > 0 ? pos - p.window : -1;
-                            const int j0 = k0 + key_of_row<CT == kE4m3>(g), j1 = j0 + (CT == kE4m3 ? 2 : 8);
-                            const bool h0 = j0 > pos || (j0 <= lo && j0 >= sinks), h1 = j1 > pos || (j1 <= lo && j1 >= sinks);
-                            s[n][e] = h0 ? -INFINITY : s[n][e] * f[n][e];
-                            s[n][2 + e] = h1 ? -INFINITY : s[n][2 + e] * f[n][e];
-                            f[n][e] = 1.f;
+#pragma unroll
+                            for (int m = 0; m < M; ++m) {
+                                const int j0 = k0[m] + key_of_row<CT == kE4m3>(g), j1 = j0 + (CT == kE4m3 ? 2 : 8);
+                                const bool h0 = j0 > pos || (j0 <= lo && j0 >= sinks), h1 = j1 > pos || (j1 <= lo && j1 >= sinks);
+                                s[m][n][e] = h0 ? -INFINITY : s[m][n][e] * f[m][n][e];
+                                s[m][n][2 + e] = h1 ? -INFINITY : s[m][n][2 + e] * f[m][n][e];
+                                f[m][n][e] = 1.f;
+                            }
                         }
                 }
                 // The reference may trail the true maximum by 2^8 (the weights
-                // then reach 2^8, far inside 16-bit range), so most tiles need
+                // then reach 2^8, far inside 16-bit range), so most stages need
                 // one vote instead of the reduction and the rescaling.
                 bool grow = false;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int m = 0; m < M; ++m)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        grow |= fmaf(fmaxf(s[n][e], s[n][2 + e]), f[n][e], m_neg[n][e]) > kRescaleThreshold - lv;
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            grow |= fmaf(fmaxf(s[m][n][e], s[m][n][2 + e]), f[m][n][e], m_neg[n][e]) > kRescaleThreshold - lv[m];
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float mx = fmaxf(s[n][e], s[n][2 + e]) * f[n][e];
+                            float mx = fmaxf(s[0][n][e], s[0][n][2 + e]) * f[0][n][e] + lv[0];
+#pragma unroll
+                            for (int m = 1; m < M; ++m)
+                                mx = fmaxf(mx, fmaxf(s[m][n][e], s[m][n][2 + e]) * f[m][n][e] + lv[m]);
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                            mx = fmaxf(mx + lv, -m_neg[n][e]);
+                            mx = fmaxf(mx, -m_neg[n][e]);
                             const float alpha = ptx::ex2(-m_neg[n][e] - mx);
                             m_neg[n][e] = -mx;
                             l_sum[n][e] *= alpha;
@@ -796,46 +832,50 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                     }
                 }
                 // ---- weights; P in f16 (bf16 for a bf16 cache), summed before that rounding
-                uint32_t pb[NT][2];
+                uint32_t pb[M][NT][2];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float w[4];
-                    ptx::fma2(w[0], w[1], s[n][0], s[n][1], f[n][0], f[n][1], m_neg[n][0], m_neg[n][1]);
-                    ptx::fma2(w[2], w[3], s[n][2], s[n][3], f[n][0], f[n][1], m_neg[n][0], m_neg[n][1]);
+                for (int m = 0; m < M; ++m)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = ptx::ex2(w[e]);
-                    ptx::add2(l_sum[n][0], l_sum[n][1], l_sum[n][0], l_sum[n][1], w[0], w[1]);
-                    ptx::add2(l_sum[n][0], l_sum[n][1], l_sum[n][0], l_sum[n][1], w[2], w[3]);
-                    if (CT == kE4m3) {
-                        ptx::mul2(w[0], w[1], w[0], w[1], vs, vs);
-                        ptx::mul2(w[2], w[3], w[2], w[3], vs, vs);
+                    for (int n = 0; n < NT; ++n) {
+                        float w[4];
+                        float(&x)[4] = s[m][n];
+                        ptx::fma2(w[0], w[1], x[0], x[1], f[m][n][0], f[m][n][1], m_neg[n][0], m_neg[n][1]);
+                        ptx::fma2(w[2], w[3], x[2], x[3], f[m][n][0], f[m][n][1], m_neg[n][0], m_neg[n][1]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[e] = ptx::ex2(w[e]);
+                        ptx::add2(l_sum[n][0], l_sum[n][1], l_sum[n][0], l_sum[n][1], w[0], w[1]);
+                        ptx::add2(l_sum[n][0], l_sum[n][1], l_sum[n][0], l_sum[n][1], w[2], w[3]);
+                        if (CT == kE4m3) {
+                            ptx::mul2(w[0], w[1], w[0], w[1], vs[m], vs[m]);
+                            ptx::mul2(w[2], w[3], w[2], w[3], vs[m], vs[m]);
+                        }
+                        pb[m][n][0] = transpose8x8(kBf ? ptx::pack_bf16x2(w[0], w[1]) : ptx::pack_f16x2(w[0], w[1]));
+                        pb[m][n][1] = transpose8x8(kBf ? ptx::pack_bf16x2(w[2], w[3]) : ptx::pack_f16x2(w[2], w[3]));
                     }
-                    pb[n][0] = transpose8x8(kBf ? ptx::pack_bf16x2(w[0], w[1]) : ptx::pack_f16x2(w[0], w[1]));
-                    pb[n][1] = transpose8x8(kBf ? ptx::pack_bf16x2(w[2], w[3]) : ptx::pack_f16x2(w[2], w[3]));
-                }
                 // ---- O^T += V^T P^T
-                {
+#pragma unroll
+                for (int m = 0; m < M; ++m)
 #pragma unroll
                     for (int c = 0; c < C::kChunks / 2; ++c) {
+                        const uint32_t at = (va ^ (uint32_t)(c << 5)) + m * 16 * C::kRowBytes;
                         uint32_t r[4];
                         if (CT == kE4m3) {
-                            ldmatrix_bytes_trans(r, va ^ (uint32_t)(c << 5));
+                            ldmatrix_bytes_trans(r, at);
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 const uint32_t a0 = e4m3_lo(r[2 * h]), a1 = e4m3_lo(r[2 * h + 1]),
                                                a2 = e4m3_hi(r[2 * h]), a3 = e4m3_hi(r[2 * h + 1]);
 #pragma unroll
                                 for (int n = 0; n < NT; ++n)
-                                    mma16816<false>(acc[2 * c + h][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                                    mma16816<false>(acc[2 * c + h][n], a0, a1, a2, a3, pb[m][n][0], pb[m][n][1]);
                             }
                         } else {
-                            ldmatrix4<true>(r, va ^ (uint32_t)(c << 5));
+                            ldmatrix4<true>(r, at);
 #pragma unroll
                             for (int n = 0; n < NT; ++n)
-                                mma16816<kBf>(acc[c][n], r[0], r[1], r[2], r[3], pb[n][0], pb[n][1]);
+                                mma16816<kBf>(acc[c][n], r[0], r[1], r[2], r[3], pb[m][n][0], pb[m][n][1]);
                         }
                     }
-                }
             }
             st = st + 1 == C::kStages ? 0 : st + 1;
         }

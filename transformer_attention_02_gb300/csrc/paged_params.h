@@ -78,10 +78,19 @@ struct AttendParams {
 // products' eight rows, at most 32.
 inline int block_rows(int rows) { return rows <= 24 ? (rows <= 8 ? 8 : rows <= 16 ? 16 : 24) : 32; }
 
-// CTAs of the attention kernel on an SM at once (the reasons stand at Cfg).
-constexpr int resident_ctas(int D, int rows_per_block, int cache) {
-    if (D == 64) return rows_per_block == 32 || (rows_per_block == 24 && cache == kE4m3) ? 3 : 2;
-    return cache == kE4m3 || rows_per_block <= 16 ? 2 : 1;
+// How the attention kernel fills an SM: CTAs at once, their warps, the keys of a
+// warp's stage (16 a tile) and the stages of its ring. (The reasons stand at Cfg.)
+struct Plan {
+    int ctas, warps, keys, stages;
+};
+constexpr Plan plan_of(int D, int rows_per_block, int cache) {
+    const bool wide = rows_per_block > 16;
+    if (cache == kE4m3) {
+        if (D == 128) return !wide ? Plan{3, 4, 32, 2} : rows_per_block == 24 ? Plan{2, 4, 32, 3} : Plan{2, 4, 32, 2};
+        return rows_per_block == 8 ? Plan{3, 4, 64, 2} : rows_per_block == 32 ? Plan{2, 4, 32, 3} : Plan{3, 4, 32, 3};
+    }
+    if (D == 128) return !wide ? Plan{2, 4, 16, 3} : Plan{1, 8, 16, 3};
+    return rows_per_block == 32 ? Plan{3, 4, 16, 3} : Plan{3, 4, 32, 2};
 }
 
 // The attention and the merge of its parts, for one cache type CT (kBf16,
