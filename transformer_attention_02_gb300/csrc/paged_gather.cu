@@ -3,7 +3,7 @@
 // them, and the fused tcgen05 kernel (its ragged variants) reads those.
 //
 // From kChunkRows queries a sequence the products outweigh the cache's reads,
-// and they belong on tcgen05: the kernel of paged_attn.cuh reaches some 290
+// and they belong on tcgen05: the kernel of paged_attn.cuh reaches some 330
 // TFLOP/s there (mma.sync, the cache read once per 32 rows), this path the
 // fused kernel's rate less one pass over the cache: 16 x 256 queries over 8192
 // e4m3 keys (32/8 heads of 128) 561 us, 964 TFLOP/s; one chunk of 2048 over 16384
