@@ -699,6 +699,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
             cp_async_wait<C::kStages - 2>();
             __syncwarp();
             issue();
+            if (C::kStages == 2) __syncwarp();                // (it puts down this stage's scales)
             // All tiles of a stage together: one look at the queries' fragments, one
             // vote. The first key of each; kNoKey: nothing there, or a page out of
             // range (its rows are zeros, and hidden).
