@@ -813,3 +813,36 @@ def test_a_windowed_prompt_follows_the_kernel_that_makes_its_inputs():
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Sq", [(2, 1), (8, 3), (8, 5), (16, 4)])
+@pytest.mark.parametrize("e4m3", [True, False], ids=["e4m3", "16bit"])
+def test_pages_of_one_tile(e4m3, Hq, Sq, D):
+    """Pages of 16 tokens: every tile of a stage has a page and scales of its own, some out of range (their keys are
+    hidden), some wholly before the window, the last one ragged."""
+    Hkv, page, n = 2 if Hq < 16 else 1, 16, 16 * 70 + 5
+    c = Cache(1, Hkv, D, page, 72, BF, e4m3, seed=D + Hq)
+    c.fill(0, n, 3)
+    if e4m3:
+        for j in range(0, 71, 3):
+            c.vs[int(c.table_np[0, j])] *= 2.0 ** (j % 7)
+    gone = [5, 6, 17, 40, 63]
+    table = c.table.clone()
+    for i, j in enumerate(gone):
+        table[0, j] = [-1, 1 << 30, -(1 << 31), 74 + 0, 1000][i]
+    q = _rand((1, Sq, Hq, D), BF, 7)
+    keep = np.array([t // page not in gone for t in range(n)])
+    for window, sinks in ((0, 0), (600, 70), (33, 0)):
+        o, lse = A.attention_paged(q, c.k, c.v, table, _i32([n]), window=window, sinks=sinks, **c.scales)
+        bad = _status()
+        k, v = (R.tokens(x, s, c.table_np[0], n, page) for x, s in ((c.k, c.ks), (c.v, c.vs)))
+        pos = np.arange(n - Sq, n)
+        for i in range(Sq):
+            t = np.arange(n)
+            see = keep & (t <= pos[i]) & (True if not window else (t > pos[i] - window) | (t < sinks))
+            ks, vs = k[see], v[see]
+            want = R.attend(R.f64(q[0, i:i + 1]), ks, vs, np.array([len(ks) - 1]), D ** -0.5, 0, 0)
+            R.check_rows(R.f64(o[0, i:i + 1]), R.f64(lse[0, :, i:i + 1]), want, R.step(BF),
+                         R.step(FP) if e4m3 else R.step(BF), D, n, _v_top(c, c.table_np[0, :71]), f"{window} {i}")
+        assert bad == (A.ATTN_OK if window == 33 else A.ATTN_ERR_BAD_INDEX)
