@@ -10,6 +10,8 @@
 // 424 us, 1216 TFLOP/s. Keys and values become
 // code * scale, exact in bf16 for power-of-two scales (four significant bits).
 // Bound by memory: each visible page is read once and written once at 16 bits.
+#include <type_traits>
+
 #include "../../include/attn.h"
 #include "attn_kernel.cuh"
 #include "paged_params.h"
@@ -20,10 +22,13 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Eight values as they stand in the cache.
 template <int CT>
-__device__ __forceinline__ uint4 load_piece(const void* cache, size_t at, float scale, bool bf16) {
-    if (CT != kE4m3) return *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(cache) + at);
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(cache) + at);
+using Raw = std::conditional_t<CT == kE4m3, uint2, uint4>;
+
+// code * scale in 16 bits, saturating: the code of a value near the type's
+// largest may lie above it.
+__device__ __forceinline__ uint4 widen_piece(uint2 w, float scale, bool bf16) {
     const uint16_t pairs[4] = {(uint16_t)w.x, (uint16_t)(w.x >> 16), (uint16_t)w.y, (uint16_t)(w.y >> 16)};
     uint32_t r[4];
 #pragma unroll
@@ -34,7 +39,6 @@ __device__ __forceinline__ uint4 load_piece(const void* cache, size_t at, float 
         asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
             : "=f"(lo), "=f"(hi)
             : "r"(h));
-        // Saturating: the code of a value near the type's largest may lie above it.
         lo *= scale, hi *= scale;
         if (bf16)
             asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r[i]) : "f"(hi), "f"(lo));
@@ -43,6 +47,7 @@ __device__ __forceinline__ uint4 load_piece(const void* cache, size_t at, float 
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
+__device__ __forceinline__ uint4 widen_piece(uint4 w, float, bool) { return w; }
 
 // CTAs [0, p.copies): 128 keys of one K/V head of a sequence, zeros past its last
 // key (the products read whole blocks of 128). The others: 16-byte pieces of the
@@ -93,24 +98,42 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p) 
         const int low = max(0, kv - ql - p.window + 1);           // oldest key of the first query's window
         if ((kb + 1) * 128 <= low && kb * 128 >= p.sinks) return; // no query sees a key of the block
     }
-    for (int c = threadIdx.x; c < 128 << cshift; c += kThreads) {
-        const int key = kb * 128 + (c >> cshift), g = c & (chunks - 1);
-        if (key >= p.cap) break;                                  // (the tensor's end: loads past it read zeros)
-        uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
-        if (key < kv) {
-            const int id = __ldg(p.block_table + (size_t)b * p.max_pages + (key >> p.page_shift));
-            if ((unsigned)id < (unsigned)p.n_pages) {
-                const size_t block = (size_t)id * p.Hkv + hk;
-                const size_t at = ((block << p.page_shift) + (size_t)(key & ((1 << p.page_shift) - 1))) * p.D + 8 * g;
-                k = load_piece<CT>(p.k_cache, at, CT == kE4m3 ? __ldg(p.k_scale + block) : 1.f, p.bf16);
-                v = load_piece<CT>(p.v_cache, at, CT == kE4m3 ? __ldg(p.v_scale + block) : 1.f, p.bf16);
-            } else {
-                atomicOr(p.status, kStatusBadIndex);
+    // kBatch pieces a thread are loaded before any is stored.
+    constexpr int kBatch = 4;
+    static_assert(128 * 8 % (kThreads * kBatch) == 0, "whole batches");
+    for (int c0 = threadIdx.x; c0 < 128 << cshift; c0 += kBatch * kThreads) {
+        Raw<CT> k[kBatch], v[kBatch];
+        float ks[kBatch], vs[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int c = c0 + i * kThreads, key = kb * 128 + (c >> cshift), g = c & (chunks - 1);
+            k[i] = v[i] = Raw<CT>{};
+            ks[i] = vs[i] = 1.f;
+            if (key < kv) {
+                const int id = __ldg(p.block_table + (size_t)b * p.max_pages + (key >> p.page_shift));
+                if ((unsigned)id < (unsigned)p.n_pages) {
+                    const size_t block = (size_t)id * p.Hkv + hk;
+                    const size_t at = ((block << p.page_shift) + (size_t)(key & ((1 << p.page_shift) - 1))) * chunks + g;
+                    k[i] = __ldg(static_cast<const Raw<CT>*>(p.k_cache) + at);
+                    v[i] = __ldg(static_cast<const Raw<CT>*>(p.v_cache) + at);
+                    if (CT == kE4m3) {
+                        ks[i] = __ldg(p.k_scale + block);
+                        vs[i] = __ldg(p.v_scale + block);
+                    }
+                } else {
+                    atomicOr(p.status, kStatusBadIndex);
+                }
             }
         }
-        const size_t to = (((size_t)b * p.cap + key) * p.Hkv + hk) * chunks + g;
-        reinterpret_cast<uint4*>(p.k_out)[to] = k;
-        reinterpret_cast<uint4*>(p.v_out)[to] = v;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int c = c0 + i * kThreads, key = kb * 128 + (c >> cshift), g = c & (chunks - 1);
+            if (key < p.cap) {                                    // (the tensor's end: loads past it read zeros)
+                const size_t to = (((size_t)b * p.cap + key) * p.Hkv + hk) * chunks + g;
+                reinterpret_cast<uint4*>(p.k_out)[to] = widen_piece(k[i], ks[i], p.bf16);
+                reinterpret_cast<uint4*>(p.v_out)[to] = widen_piece(v[i], vs[i], p.bf16);
+            }
+        }
     }
 }
 
