@@ -475,7 +475,7 @@ int attn_kv_append_f16(const void *k, const void *v, long long k_stride, long lo
  *               kv_lens. A larger one is fine. Calls, or replays of captured calls, that may run at the
  *               same time need one each.
  * Two launches: the attention, whose CTAs take equal shares of all visible keys,
- * and the merge of the keys that several CTAs shared. Bound by the cache's reads
+ * and the merge of the keys that several CTAs shared; one over short tables. Bound by the cache's reads
  * up to 32 query rows (Sq * Hq / Hkv) a K/V head; more rows read it once per 32.
  * Long chunks (Sq of 128 and more, with B * Hq * ceil(Sq / 256) of 48 and more)
  * go another way when the workspace holds the gathered tensors: the pages that

@@ -846,3 +846,29 @@ def test_pages_of_one_tile(e4m3, Hq, Sq, D):
             R.check_rows(R.f64(o[0, i:i + 1]), R.f64(lse[0, :, i:i + 1]), want, R.step(BF),
                          R.step(FP) if e4m3 else R.step(BF), D, n, _v_top(c, c.table_np[0, :71]), f"{window} {i}")
         assert bad == (A.ATTN_OK if window == 33 else A.ATTN_ERR_BAD_INDEX)
+
+
+@pytest.mark.parametrize("e4m3", [True, False], ids=["e4m3", "16bit"])
+@pytest.mark.parametrize("Hq,Hkv,D,Sq", [(8, 2, 128, 1), (8, 8, 64, 1), (7, 1, 128, 5), (16, 2, 64, 3), (12, 2, 128, 20)])
+def test_short_tables(Hq, Hkv, D, Sq, e4m3):
+    """Tables that a CTA takes whole (256 keys): empty sequences, no queries, more queries than keys, lengths out of
+    range; and the same lengths under a table that goes by the schedule."""
+    kv, ql = [256, 0, 17, 1, 200, 130, 5], [Sq, Sq, max(Sq - 1, 0), Sq, 0, Sq, Sq]
+    B, page = len(kv), 32
+    c = Cache(B, Hkv, D, page, 8, FP, e4m3, seed=Hq * D)
+    for b in range(B):
+        c.fill(b, kv[b], b)
+    q = _rand((B, Sq, Hq, D), FP, 8)
+    wide = torch.cat([c.table, torch.full((B, 100), -1, dtype=torch.int32, device=DEV)], 1).contiguous()
+    for window, sinks in ((0, 0), (20, 3)):
+        for table in (c.table, wide):
+            o, lse = torch.full_like(q, 5.0), torch.full((B, Hq, Sq), 5.0, device=DEV)
+            A.attention_paged(q, c.k, c.v, table, _i32(kv), q_lens=_i32(ql), window=window, sinks=sinks, out=o, lse=lse,
+                              **c.scales)
+            assert _status() == A.ATTN_OK
+            _check_attention(c, q, q, o, lse, kv, ql, window, sinks, label=f"{window} {table.shape}")
+            for b in range(B):
+                assert bool((o[b, ql[b]:] == 5.0).all()) and bool((lse[b, :, ql[b]:] == 5.0).all())
+    o, lse = A.attention_paged(q, c.k, c.v, c.table, _i32([-1, 300, 17, 1, 200, 130, 5]), **c.scales)
+    assert _status() == A.ATTN_ERR_BAD_INDEX
+    assert bool((o[0] == 0).all()) and bool((lse[0] == float("-inf")).all()) and bool(torch.isfinite(o[2:]).all())

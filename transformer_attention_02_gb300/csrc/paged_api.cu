@@ -231,7 +231,10 @@ int attend_impl(const void* q, long long q_stride, const void* k_cache, const vo
     p.n_pages = n_pages;
     p.window = window;
     p.sinks = sinks;
-    p.ctas = ctas;
+    const long long segments = (long long)B * Hkv * row_blocks;
+    p.whole = paged::takes_whole(segments, (long long)dev.num_sms * paged::plan_of(D, rb, type).ctas,
+                                 (max_keys + paged::kUnit - 1) / paged::kUnit);
+    p.ctas = p.whole ? (int)segments : ctas;
     p.q_bf16 = bf16;
     if (e4m3) return paged::launch_attend<paged::kE4m3>(dev.paged_attr_set[paged::kE4m3], p, D, stream);
     return bf16 ? paged::launch_attend<paged::kBf16>(dev.paged_attr_set[paged::kBf16], p, D, stream)

@@ -23,7 +23,8 @@
 // every SM alike. A CTA that holds only part of a segment leaves its FP32
 // result (unnormalised O, row maximum, row sum) in the workspace, and a second
 // kernel, launched while the first one drains, merges the parts. All lengths
-// are read on the device.
+// are read on the device. Over short tables a CTA takes one segment whole, and the
+// merge is left out (takes_whole).
 //
 // Memory: each warp owns a ring of stages filled by 16-byte asynchronous copies
 // (16 or 32 keys and their values a stage); rows that no query sees are filled
@@ -37,7 +38,7 @@
 // row over 16-bit keys (16 x 4096, 1.07 GB) 161 us, 6.67 TB/s. What is left are
 // the ends: the chain lengths - page numbers - first keys (2 us), SMs that finish
 // 3 to 4 us apart, the second kernel (2). More rows over e4m3: 16 rows 52.8 us,
-// 24 58.9, 32 69.0; there the tensor cores, the conversions before them and the
+// 24 59.4, 32 69.8; there the tensor cores, the conversions before them and the
 // softmax of a stage wait on one another.
 #pragma once
 
@@ -312,6 +313,19 @@ __device__ __forceinline__ bool locate(const AttendParams& p, int segs, int lead
     return true;
 }
 
+// Rows of a segment without any key: o = 0, lse = -inf.
+template <int D, int ROWS, int THREADS>
+__device__ __forceinline__ void fill_rows(const AttendParams& p, int b, int seg, int ql, int tid) {
+    const int hk = seg / p.row_blocks, r0 = (seg - hk * p.row_blocks) * ROWS;
+    for (int w = tid; w < ROWS * (D / 8); w += THREADS) {
+        const int row = r0 + w / (D / 8), c = w % (D / 8), i = row / p.group;
+        if (row >= p.rows || i >= ql) continue;
+        const int h = hk * p.group + (row - i * p.group);
+        reinterpret_cast<uint4*>(p.o)[(((size_t)b * p.Sq + i) * p.Hq + h) * (D / 8) + c] = make_uint4(0u, 0u, 0u, 0u);
+        if (c == 0) p.lse[((size_t)b * p.Hq + h) * p.Sq + i] = -INFINITY;
+    }
+}
+
 template <int D, int CT, int NT>
 __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::kResident)
     paged_attend_kernel(const AttendParams p) {
@@ -322,6 +336,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     extern __shared__ __align__(1024) uint8_t smem_raw[];          // the XOR of chunk offsets needs 256-byte stages
     __shared__ int2 s_scan[C::kWarps];
     __shared__ Share s_begin;                                     // (b, base, list) where the CTA's range begins
+    __shared__ int s_range[2];                                    // the schedule's lead, the range's end
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     wait_for_inputs();
     let_next_start();
@@ -343,59 +358,84 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     }
     // ---- where this CTA's range begins: a scan over the sequences' units
     const int segs = p.Hkv * p.row_blocks;                        // segments of a sequence
-    const int per = (p.B + kThreads - 1) / kThreads;
-    const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
-    KeyList list{};
-    int mine = 0, mine_n = 0;                                     // units, and sequences with any
-    for (int b = b_lo; b < b_hi; ++b) {
+    int x, x_end;
+    if (p.whole) {
+        const int b = blockIdx.x / segs, seg = blockIdx.x - b * segs;
         bool bad;
-        list = key_list(p, b, bad);
-        mine += list.units;
-        mine_n += list.units > 0;
-        if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
-    }
-    int incl = mine, incl_n = mine_n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o), n = __shfl_up_sync(0xffffffffu, incl_n, o);
-        if (lane >= o) incl += v, incl_n += n;
-    }
-    if (lane == 31) s_scan[warp] = make_int2(incl, incl_n);
-    __syncthreads();
-    int before = incl - mine, before_n = incl_n - mine_n, total = 0, total_n = 0;
-#pragma unroll
-    for (int w = 0; w < C::kWarps; ++w) {
-        const int2 v = s_scan[w];
-        if (w < warp) before += v.x, before_n += v.y;
-        total += v.x, total_n += v.y;
-    }
-    const int lead = lead_of(p, total * segs);
-    before = (before + before_n * lead) * segs;
-    mine = (mine + mine_n * lead) * segs;
-    total = (total + total_n * lead) * segs;
-    const int ctas = working_ctas(p, total);
-    const Ranges ranges(total, max(ctas, 1));
-    const bool works = (int)blockIdx.x < ctas;
-    const int x = works ? ranges.start(blockIdx.x) : total;
-    const int x_end = works ? ranges.start(blockIdx.x + 1) : total;
-    const bool note = blockIdx.x == 0 && p.B > kScanInMerge;      // the merge reads the offsets of a large batch
-    if (note || (before <= x && x < before + mine)) {
-        int at = before;
+        const KeyList list = key_list(p, b, bad);
+        if (bad && seg == 0 && tid == 0) atomicOr(p.status, kStatusBadIndex);
+        if (list.units == 0) {
+            fill_rows<D, C::kRows, kThreads>(p, b, seg, list.ql, tid);
+            return;
+        }
+        x = seg * list.units;
+        x_end = x + list.units;
+        if (tid == 0) {
+            s_begin.b = b;
+            s_begin.base = 0;
+            s_begin.list = list;
+            s_range[0] = 0;
+            s_range[1] = x_end;
+        }
+    } else {
+        const int per = (p.B + kThreads - 1) / kThreads;
+        const int b_lo = min(p.B, tid * per), b_hi = min(p.B, b_lo + per);
+        KeyList list{};
+        int mine = 0, mine_n = 0;                                     // units, and sequences with any
         for (int b = b_lo; b < b_hi; ++b) {
             bool bad;
-            if (per > 1) list = key_list(p, b, bad);
-            const int n = span_of(list.units, lead) * segs;
-            if (note) p.base[b] = at;
-            if (at <= x && x < at + n) {
-                s_begin.b = b;
-                s_begin.base = at;
-                s_begin.list = list;
-            }
-            at += n;
+            list = key_list(p, b, bad);
+            mine += list.units;
+            mine_n += list.units > 0;
+            if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadIndex);
         }
-        if (note && b_hi == p.B && b_lo < b_hi) {
-            p.base[p.B] = at;
-            p.base[p.B + 1] = lead;
+        int incl = mine, incl_n = mine_n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o), n = __shfl_up_sync(0xffffffffu, incl_n, o);
+            if (lane >= o) incl += v, incl_n += n;
+        }
+        if (lane == 31) s_scan[warp] = make_int2(incl, incl_n);
+        __syncthreads();
+        int before = incl - mine, before_n = incl_n - mine_n, total = 0, total_n = 0;
+#pragma unroll
+        for (int w = 0; w < C::kWarps; ++w) {
+            const int2 v = s_scan[w];
+            if (w < warp) before += v.x, before_n += v.y;
+            total += v.x, total_n += v.y;
+        }
+        const int lead = lead_of(p, total * segs);
+        before = (before + before_n * lead) * segs;
+        mine = (mine + mine_n * lead) * segs;
+        total = (total + total_n * lead) * segs;
+        const int ctas = working_ctas(p, total);
+        const Ranges ranges(total, max(ctas, 1));
+        const bool works = (int)blockIdx.x < ctas;
+        x = works ? ranges.start(blockIdx.x) : total;
+        x_end = works ? ranges.start(blockIdx.x + 1) : total;
+        if (tid == 0) {
+            s_range[0] = lead;
+            s_range[1] = x_end;
+        }
+        const bool note = blockIdx.x == 0 && p.B > kScanInMerge;      // the merge reads the offsets of a large batch
+        if (note || (before <= x && x < before + mine)) {
+            int at = before;
+            for (int b = b_lo; b < b_hi; ++b) {
+                bool bad;
+                if (per > 1) list = key_list(p, b, bad);
+                const int n = span_of(list.units, lead) * segs;
+                if (note) p.base[b] = at;
+                if (at <= x && x < at + n) {
+                    s_begin.b = b;
+                    s_begin.base = at;
+                    s_begin.list = list;
+                }
+                at += n;
+            }
+            if (note && b_hi == p.B && b_lo < b_hi) {
+                p.base[p.B] = at;
+                p.base[p.B + 1] = lead;
+            }
         }
     }
     __syncthreads();
@@ -449,7 +489,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     auto stages_of = [](int units) { return (units * kUnit + C::kWarps * C::kKeys - 1) / (C::kWarps * C::kKeys); };
     auto enter = [&]() {                                          // the share at ld_x
         Share s = ld;
-        ld_more = locate<C::kRows>(p, segs, lead, ld_x, x_end, s);
+        ld_more = locate<C::kRows>(p, segs, s_range[0], ld_x, s_range[1], s);
         if (!ld_more) return;
         __syncwarp();
         if (lane == 0) {
@@ -884,7 +924,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
         // ---- the next share's queries set out
         Share now = cur;
         Share s = now;
-        const bool more = locate<C::kRows>(p, segs, lead, now.next, x_end, s);
+        const bool more = locate<C::kRows>(p, segs, s_range[0], now.next, s_range[1], s);
         if (more) {
             __syncwarp();
             if (lane == 0) cur = s;
@@ -1117,7 +1157,8 @@ int launch_instance(bool& attr_set, const AttendParams& p, cudaStream_t stream) 
         attr_set = true;
     }
     const bool bf16 = CT == kBf16 || (CT == kE4m3 && p.q_bf16);
-    if (launch_early(kernel, p.ctas, C::kWarps * 32, C::kSmemBytes, stream, p) != cudaSuccess ||
+    if (launch_early(kernel, p.ctas, C::kWarps * 32, C::kSmemBytes, stream, p) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (!p.whole &&
         launch_early(paged_merge_kernel<D, C::kRows>, (unsigned)(p.B * p.Hkv * p.row_blocks), 256, 0, stream, p, bf16) !=
             cudaSuccess)
         return ATTN_ERR_CUDA;
