@@ -174,7 +174,7 @@ __device__ __forceinline__ Lens lens_of(const FwdParams& p, int b) {
     if (!RAGGED) return Lens{p.Sk, p.Sq};
     const int* kv = reinterpret_cast<const int*>(p.mask);
     const int* ql = reinterpret_cast<const int*>(p.rope);
-    return Lens{min(max(__ldg(kv + b), 0), p.Sk), ql ? min(max(__ldg(ql + b), 0), p.Sq) : p.Sq};
+    return Lens{min(max(kv[b], 0), p.Sk), ql ? min(max(ql[b], 0), p.Sq) : p.Sq};
 }
 
 struct TileInfo {

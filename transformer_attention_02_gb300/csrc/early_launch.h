@@ -11,6 +11,11 @@ namespace attn {
 // wait_for_inputs(): nothing of it touches memory before everything earlier in
 // the stream has finished and is visible. Saves most of the launch latency
 // between the steps of a decode loop.
+// Visible to ordinary loads, that is. The non-coherent ones (__ldg) are for data
+// that nothing writes as long as the kernel lives, and it lives while the kernel
+// before it still writes: they read rotation tables only, which no kernel that lets
+// its successor start early makes. Data of the stream is read by plain loads, or, where
+// it is read once or a neighbour's line may be in L1, by __ldcg from L2.
 template <typename... Params, typename... Args>
 cudaError_t launch_early(void (*kernel)(Params...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
                          Args... args) {

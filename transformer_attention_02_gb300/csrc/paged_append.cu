@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(max_threads(HELD), min_ctas(HELD)) append_kern
         for (int i = 0; i < HELD; ++i) {
             const int c = threadIdx.x + i * blockDim.x;
             w[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (there(c)) w[i] = __ldg(reinterpret_cast<const uint4*>(at + i * apart));
+            if (there(c)) w[i] = __ldcg(reinterpret_cast<const uint4*>(at + i * apart));
         }
     };
     fetch(h0);

@@ -536,13 +536,13 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                 ids = -1;
                 sc = make_float2(1.f, 1.f);
                 if (off < u.x && key < w.x) {
-                    ids = __ldg(p.block_table + (size_t)w.z * p.max_pages + (key >> p.page_shift));
+                    ids = p.block_table[(size_t)w.z * p.max_pages + (key >> p.page_shift)];
                     if ((unsigned)ids >= (unsigned)p.n_pages) {
                         atomicOr(p.status, kStatusBadIndex);
                         ids = -1;
                     } else if (CT == kE4m3) {
                         const uint64_t at = (uint64_t)(uint32_t)ids * (uint32_t)p.Hkv + w.w;
-                        sc = make_float2(__ldg(p.k_scale + at), __ldg(p.v_scale + at));
+                        sc = make_float2(__ldcg(p.k_scale + at), __ldcg(p.v_scale + at));
                     }
                 }
             }

@@ -110,15 +110,15 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p) 
             k[i] = v[i] = Raw<CT>{};
             ks[i] = vs[i] = 1.f;
             if (key < kv) {
-                const int id = __ldg(p.block_table + (size_t)b * p.max_pages + (key >> p.page_shift));
+                const int id = p.block_table[(size_t)b * p.max_pages + (key >> p.page_shift)];
                 if ((unsigned)id < (unsigned)p.n_pages) {
                     const size_t block = (size_t)id * p.Hkv + hk;
                     const size_t at = ((block << p.page_shift) + (size_t)(key & ((1 << p.page_shift) - 1))) * chunks + g;
-                    k[i] = __ldg(static_cast<const Raw<CT>*>(p.k_cache) + at);
-                    v[i] = __ldg(static_cast<const Raw<CT>*>(p.v_cache) + at);
+                    k[i] = __ldcg(static_cast<const Raw<CT>*>(p.k_cache) + at);
+                    v[i] = __ldcg(static_cast<const Raw<CT>*>(p.v_cache) + at);
                     if (CT == kE4m3) {
-                        ks[i] = __ldg(p.k_scale + block);
-                        vs[i] = __ldg(p.v_scale + block);
+                        ks[i] = __ldcg(p.k_scale + block);
+                        vs[i] = __ldcg(p.v_scale + block);
                     }
                 } else {
                     atomicOr(p.status, kStatusBadIndex);
