@@ -28,7 +28,8 @@
 //
 // Memory: each warp owns a ring of stages filled by 16-byte asynchronous copies
 // (16 or 32 keys and their values a stage); rows that no query sees are filled
-// with zeros, so whatever their slots hold never enters a product. 16-byte
+// with zeros and tiles of such rows alone passed over, scales and all, so whatever
+// stands there never enters a product. 16-byte
 // chunks are XOR-swizzled by the row, which makes the ldmatrix reads of eight
 // rows conflict-free.
 //
@@ -480,8 +481,11 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
     // {count, offset of the gap, first before it, first past it (less the
     // offset)}, {end, start of the window, sequence, head}.
     int4* const ld_v = reinterpret_cast<int4*>(smem_raw + C::kIssueOff) + 2 * warp;
-    // Page numbers (-1: no key, or out of range) and scales of the next
-    // 32 / kTiles stages, one 16-key tile a lane.
+    // Page numbers (-1: no key that a query of the block sees, or out of range)
+    // and scales of the next 32 / kTiles stages, one 16-key tile a lane. A unit at
+    // either end of the window may hold tiles that nobody sees: neither their page
+    // numbers nor their scales are looked at (a scale multiplies weights of zero
+    // too, and a page behind the window may have left the table).
     constexpr int kBatch = 32 / C::kTiles;
     int ids = -1;
     float2 sc = make_float2(0.f, 0.f);
@@ -535,7 +539,7 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
                 const int key = off + (off < u.y ? u.z : u.w);
                 ids = -1;
                 sc = make_float2(1.f, 1.f);
-                if (off < u.x && key < w.x) {
+                if (off < u.x && key < w.x && (key + 16 > w.y || key < sinks)) {
                     ids = p.block_table[(size_t)w.z * p.max_pages + (key >> p.page_shift)];
                     if ((unsigned)ids >= (unsigned)p.n_pages) {
                         atomicOr(p.status, kStatusBadIndex);
