@@ -88,3 +88,23 @@ CASES = [
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "H{}-{}_D{}_p{}_{}_{}_w{}s{}".format(*c[:6], *c[7:]))
 def test_unseen_pages(case, e4m3, dt):
     _agree(case, dt, e4m3, [None])
+
+
+CHUNKS = [
+    (24, 2, 128, 16, [700, 650], [130, 130], 130, 200, 4),
+    (24, 2, 128, 64, [1100, 333], [200, 7], 200, 300, 0),     # a chunk beside a few tokens
+    (12, 4, 64, 16, [1000, 900, 0, 777], [128, 140, 0, 1], 140, 129, 140),
+    (24, 8, 64, 256, [1500, 1027], [128, 130], 130, 290, 19),
+]
+
+
+@pytest.mark.parametrize("dt", [BF, FP], ids=["bf16", "f16"])
+@pytest.mark.parametrize("e4m3", [True, False], ids=["e4m3", "16bit"])
+@pytest.mark.parametrize("case", CHUNKS, ids=lambda c: "H{}-{}_D{}_p{}_{}_{}_w{}s{}".format(*c[:6], *c[7:]))
+def test_unseen_pages_of_a_long_chunk(case, e4m3, dt):
+    """By the gathered pages (the default workspace) and, with the small workspace, by the cache itself."""
+    Hq, Hkv, D, page, kv, _, Sq = case[:7]
+    keys = 8192                                             # (a table for which the gathered tensors are the larger scratch)
+    small = A.attn_paged_workspace_bytes(len(kv), Hq, Hkv, Sq, D)
+    assert small < A.attn_paged_workspace_bytes(len(kv), Hq, Hkv, Sq, D, keys)
+    _agree(case, dt, e4m3, [None, torch.empty(small, dtype=torch.uint8, device=DEV)], keys)
