@@ -727,7 +727,9 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
         // to the tensor cores, weight * scale, is largest where it matters most,
         // whatever the scales of other pages. The weights alone then reach
         // 2^(8 + kShift) / scale: FP32 holds them and their sum for scales from
-        // 2^-72 to 2^120 (values under smaller scales, below 2^-63, fade to zero).
+        // 2^-72 to 2^120 (values under smaller scales, below 2^-63, fade to zero),
+        // and where it is brought to a higher reference the factor, down to 2^-220,
+        // is applied as its root twice; alone it would leave FP32's range.
         // Below any logit at first, so that no weight needs a special case.
         float m_neg[NT][2], l_sum[NT][2];
 #pragma unroll
@@ -865,9 +867,10 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                             mx = fmaxf(mx, -m_neg[n][e]);
-                            const float alpha = ptx::ex2(-m_neg[n][e] - mx);
+                            // (the root of the factor, twice: see m_neg)
+                            const float root = ptx::ex2(0.5f * (-m_neg[n][e] - mx)), alpha = root * root;
                             m_neg[n][e] = -mx;
-                            l_sum[n][e] *= alpha;
+                            l_sum[n][e] = l_sum[n][e] * root * root;
 #pragma unroll
                             for (int d = 0; d < kSteps; ++d) {
                                 acc[d][n][e] *= alpha;
@@ -963,7 +966,8 @@ __global__ void __launch_bounds__(Cfg<D, CT, NT>::kWarps * 32, Cfg<D, CT, NT>::k
 #pragma unroll
                 for (int v = 0; v < C::kWarps; ++v) {
                     const float2 s2 = stats[v * C::kRows + lane];
-                    sum = fmaf(s2.y, ptx::ex2(s2.x - mx), sum);
+                    const float root = ptx::ex2(0.5f * (s2.x - mx));
+                    sum = fmaf(s2.y * root, root, sum);
                 }
                 const int row = r0 + lane, i = row / p.group;
                 const bool live = row < p.rows && i < now.list.ql;
@@ -1126,15 +1130,15 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const AttendParams p, 
                 float m8 = mx;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) m8 = fmaxf(m8, pm[j]);
-                const float f0 = ptx::ex2(mx - m8);
+                const float r0 = ptx::ex2(0.5f * (mx - m8)), f0 = r0 * r0;      // (see m_neg)
                 mx = m8;
-                sum *= f0;
+                sum = sum * r0 * r0;
 #pragma unroll
                 for (int e = 0; e < kPer; ++e) o[e] *= f0;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float f = ptx::ex2(pm[j] - mx);
-                    sum = fmaf(pl[j], f, sum);
+                    const float r = ptx::ex2(0.5f * (pm[j] - mx)), f = r * r;
+                    sum = fmaf(pl[j] * r, r, sum);
 #pragma unroll
                     for (int e = 0; e < kPer; ++e) o[e] = fmaf(po[j][e], f, o[e]);
                 }
