@@ -481,9 +481,8 @@ int attn_kv_append_f16(const void *k, const void *v, long long k_stride, long lo
  * go another way when the workspace holds the gathered tensors: the pages that
  * are seen are copied into contiguous tensors of q's type (code * scale, rounded
  * and saturated; exact in bf16 for the append's scales), and the fused kernel of
- * attn_fwd reads those. Its weights are rounded to q's type, where the other path rounds them
- * to fp16 over an 8-bit cache; keys of a page out of range read as zeros there,
- * and are hidden here.
+ * attn_fwd reads those. Its weights are rounded to q's type, where the other path
+ * rounds them to fp16 over an 8-bit cache.
  */
 int attn_fwd_paged(const void *q, long long q_stride, const void *k_cache, const void *v_cache,
                    const float *k_scale, const float *v_scale,

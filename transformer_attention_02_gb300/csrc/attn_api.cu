@@ -399,6 +399,8 @@ struct WindowArgs {
     int sinks;            // first tokens that stay visible
     const int* kv_lens = nullptr;      // (B) device, or null: Sk and Sq for every sequence
     const int* q_lens = nullptr;       // (B) device, or null: Sq
+    const int* block_table = nullptr;  // with kv_lens: (B, Sk >> page_shift) device, the pages the keys come from
+    int page_shift = 0, n_pages = 0;
 };
 
 bool rope_args_ok(const RopeArgs& r, int Sq, int Sk) {
@@ -554,6 +556,9 @@ int attn_fwd_impl(const void* q, const void* k, const void* v, void* o, float* l
         if (win->kv_lens) {
             p.mask = reinterpret_cast<const float*>(win->kv_lens);
             p.rope = reinterpret_cast<const float*>(win->q_lens);
+            p.o_part = reinterpret_cast<float*>(const_cast<int*>(win->block_table));
+            p.pack_shift = win->page_shift;
+            p.split_blocks = win->n_pages;
         }
     }
 
@@ -673,8 +678,9 @@ int window_impl(const void* q, const void* k, const void* v, void* o, float* lse
 
 int attn::launch_ragged(const void* q, long long q_stride, const void* k, const void* v, void* o, float* lse, int B, int Hq,
                         int Hkv, int Sq, int Sk, int D, float scale, int window, int sinks, const int* kv_lens,
-                        const int* q_lens, cudaStream_t stream, bool bf16) {
-    const WindowArgs w{window, sinks, kv_lens, q_lens};
+                        const int* q_lens, const int* block_table, int page_shift, int n_pages, cudaStream_t stream,
+                        bool bf16) {
+    const WindowArgs w{window, sinks, kv_lens, q_lens, block_table, page_shift, n_pages};
     return attn_fwd_impl(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, scale, ATTN_MASK_CAUSAL, nullptr, stream, bf16, 1, nullptr,
                          0, nullptr, q_stride, 0, &w);
 }

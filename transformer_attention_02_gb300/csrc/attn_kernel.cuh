@@ -59,9 +59,10 @@ struct FwdParams {
     int group;                // Hq / Hkv
     int n_mblk;               // ceil(Sq / 256)
     int n_splits;             // key ranges per (b, h, query block); 1 = keys not split
-    int split_blocks;         // 128-key blocks per key range
+    int split_blocks;         // 128-key blocks per key range; ragged variants: pages of the cache
     int n_tiles;              // B * Hq * n_mblk * n_splits
-    float* o_part;            // split keys: FP32 O of each key range (n_splits, B, Hq, Sq, D), else null
+    float* o_part;            // split keys: FP32 O of each key range (n_splits, B, Hq, Sq, D), else null; ragged
+                              // variants: int32 (B, Sk >> pack_shift) pages of every sequence
     float* lse_part;          // split keys: FP32 LSE of each key range (n_splits, B, Hq, Sq)
     float scale_log2;         // scale * log2(e)
     int mask_vec4;            // mask rows may be read with 32-byte (2) or 16-byte (1) loads, else 0;
@@ -75,7 +76,8 @@ struct FwdParams {
     int q_pos0;               // position of query row 0 (rotating variant); window length (windowed variants)
     // Kept last: inserting it earlier shifted the 64-bit fields after it and
     // measurably changed the code generated for the unpacked kernels.
-    int pack_shift;           // > 0: the 2^pack_shift query heads of a K/V head share each tile's rows
+    int pack_shift;           // > 0: the 2^pack_shift query heads of a K/V head share each tile's rows; ragged
+                              // variants: a page holds 2^pack_shift keys
 };
 // Kept at 128 bytes, with the 64-bit fields where they are: appending two int
 // fields (136 bytes) made the kernel 5% slower on the Llama-2-7B-shaped
@@ -177,11 +179,20 @@ __device__ __forceinline__ Lens lens_of(const FwdParams& p, int b) {
     return Lens{min(max(kv[b], 0), p.Sk), ql ? min(max(ql[b], 0), p.Sq) : p.Sq};
 }
 
+// Ragged variants: page of key `key` of sequence b, and whether the cache has it
+// (pages hold 16 keys at least). The keys of one that it has not are hidden; in the
+// gathered tensors they are zeros.
+__device__ __forceinline__ int page_at(const FwdParams& p, int b, int key) {
+    return reinterpret_cast<const int*>(p.o_part)[(size_t)b * (p.Sk >> p.pack_shift) + (key >> p.pack_shift)];
+}
+__device__ __forceinline__ bool page_there(const FwdParams& p, int page) { return (unsigned)page < (unsigned)p.split_blocks; }
+
 struct TileInfo {
     int b, h, hk, m0;  // h: the (first) query head; m0: the first query row
     int split;      // key range index; windowed variants: key blocks before the window's first
     int kb0;        // first 128-key block of the key range; windowed variants: blocks left out before the
-                    // window's first, | kSkipsFirst: the upper sub-tile passes over that block
+                    // window's first, | kSkipsFirst: the upper sub-tile passes over that block, |
+                    // kMissingPages (ragged variants): some keys of the list are not there
     int nb[2];      // KV blocks needed by query sub-tile t (rows m0+128t .. m0+128t+127)
     int n;          // max(nb[0], nb[1]): KV blocks streamed for the tile
 };
@@ -212,7 +223,7 @@ struct TileInfo {
 // causal variant reaches 0.72 to 0.77). Narrow windows are bound by the softmax
 // of whole blocks and by the tiles' ends: 4 x 2048 tokens, 32 heads of 64,
 // window 512, fp16: 72 us, five blocks a row for four visible ones.
-constexpr int kSkipsFirst = 1 << 30;
+constexpr int kSkipsFirst = 1 << 30, kMissingPages = 1 << 29;      // above every count of blocks (2^23)
 template <bool CAUSAL, bool PACK, bool WINDOW = false, bool RAGGED = false>
 __device__ __forceinline__ TileInfo tile_info(int tile, const FwdParams& p) {
     const int ps = PACK ? p.pack_shift : 0;
@@ -251,7 +262,7 @@ __device__ __forceinline__ TileInfo tile_info(int tile, const FwdParams& p) {
     t.hk = PACK ? hh : hh / p.group;
     t.m0 = mb * 2 * sub_rows;
     t.split = split;
-    t.kb0 = split * p.split_blocks;
+    t.kb0 = RAGGED ? 0 : split * p.split_blocks;
     int gap = 0, skips = 0;
     if (WINDOW) {
         const int first = t.m0 + (len.kv - len.q) - p.q_pos0 + 1;     // oldest key of the first row's window
@@ -264,7 +275,7 @@ __device__ __forceinline__ TileInfo tile_info(int tile, const FwdParams& p) {
         }
     }
     const int range_begin = t.kb0 * kBlockN;
-    const int range_end = min(len.kv, range_begin + p.split_blocks * kBlockN);
+    const int range_end = RAGGED ? len.kv : min(len.kv, range_begin + p.split_blocks * kBlockN);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         const int first = t.m0 + s * sub_rows;
@@ -281,7 +292,22 @@ __device__ __forceinline__ TileInfo tile_info(int tile, const FwdParams& p) {
 // Key block of the j-th block a tile streams.
 template <bool WINDOW>
 __device__ __forceinline__ int key_block(const TileInfo& t, int j) {
-    return WINDOW ? (j < t.split ? j : j + (t.kb0 & ~kSkipsFirst)) : t.kb0 + j;
+    return WINDOW ? (j < t.split ? j : j + (t.kb0 & (kMissingPages - 1))) : t.kb0 + j;
+}
+
+// Ragged variants: whether a page of the tile's key blocks is missing from the
+// cache. One warp looks up all of them, once a tile and tiles ahead of the products
+// (in the softmax, a block at a time, it cost 1 to 2% of a chunk's time).
+__device__ __forceinline__ bool misses_pages(const FwdParams& p, const TileInfo& t) {
+    const int kv = lens_of<true>(p, t.b).kv;
+    const int shift = min(p.pack_shift, 7), per = 7 - shift;      // 2^per pages a block
+    bool all = true;
+#pragma unroll 4
+    for (int i = threadIdx.x & 31; i < t.n << per; i += 32) {
+        const int key = key_block<true>(t, i >> per) * kBlockN + ((i & ((1 << per) - 1)) << shift);
+        if (key < kv) all &= page_there(p, page_at(p, t.b, key));
+    }
+    return !__all_sync(0xffffffffu, all);
 }
 
 struct SyncCtx {
@@ -599,6 +625,7 @@ __device__ void role_qload(const CUtensorMap* tmQ, const CUtensorMap* tmO, const
         const int found = next_tile_index(tile);
         if (found < 0) return -1;
         if (found) t = tile_info<CAUSAL, PACK, WINDOW, RAGGED>(tile, p);
+        if (RAGGED && found && misses_pages(p, t)) t.kb0 |= kMissingPages;
         if (!found) {
             t.b = t.h = t.hk = t.m0 = t.split = t.kb0 = 0;
             t.nb[0] = t.nb[1] = t.n = -1;
@@ -893,7 +920,7 @@ __device__ void role_softmax(const FwdParams& p, uint32_t smem, uint8_t* smem_pt
         uint16_t* orow = reinterpret_cast<uint16_t*>(p.o) + (((size_t)ti.b * p.Sq + row) * p.Hq + hd) * D;
         float* lse_out = p.lse + ((size_t)ti.b * p.Hq + hd) * p.Sq + row;
         // With split keys this tile's result goes to the FP32 partial buffers.
-        const bool part = p.o_part != nullptr;
+        const bool part = !RAGGED && p.o_part != nullptr;
         const size_t prow_index = (((size_t)ti.split * p.B + ti.b) * p.Hq + hd) * p.Sq + row;
         float* prow = part ? p.o_part + prow_index * D : nullptr;
         if (part) lse_out = p.lse_part + prow_index;
@@ -986,6 +1013,15 @@ __device__ void role_softmax(const FwdParams& p, uint32_t smem, uint8_t* smem_pt
 #pragma unroll
                     for (int c = 0; c < kBlockN; ++c)
                         if (c >= vis) x[c] = -INFINITY;
+                }
+                if (RAGGED && (ti.kb0 & kMissingPages)) {
+                    // the pages of the block's eight 16-key tiles, one a lane
+                    const int key = key0 + 16 * (threadIdx.x & 7);
+                    const uint32_t seen =
+                        __ballot_sync(0xffffffffu, key >= len.kv || page_there(p, page_at(p, ti.b, key)));
+#pragma unroll
+                    for (int c = 0; c < kBlockN; ++c)
+                        if (!(seen >> (c / 16) & 1u)) x[c] = -INFINITY;
                 }
                 if (WINDOW) {
                     // keys before the row's window are hidden, but for the sinks

@@ -45,10 +45,12 @@ int device_state(DeviceState* out);
 // tensors of capacity Sk whose lengths differ by sequence and are read on the
 // device: kv_lens (B), and q_lens (B) or null. Rows at or past a sequence's
 // queries are not written; V must be finite up to the next multiple of 128 keys.
+// The keys come from pages of 2^page_shift: those whose entry in block_table (B, Sk >>
+// page_shift) is not one of n_pages are hidden.
 // Other arguments as for attn_fwd.
 int launch_ragged(const void* q, long long q_stride, const void* k, const void* v, void* o, float* lse, int B, int Hq,
                   int Hkv, int Sq, int Sk, int D, float scale, int window, int sinks, const int* kv_lens,
-                  const int* q_lens, cudaStream_t stream, bool bf16);
+                  const int* q_lens, const int* block_table, int page_shift, int n_pages, cudaStream_t stream, bool bf16);
 
 // SM count of the current device (148 when it cannot be read, e.g. no GPU).
 int device_sm_count();

@@ -199,7 +199,8 @@ int attend_impl(const void* q, long long q_stride, const void* k_cache, const vo
         if (rc != ATTN_OK) return rc;
         return launch_ragged(rope_table ? g.q_out : q, rope_table ? (long long)Hq * D : q_stride, g.k_out, g.v_out, o, lse, B,
                              Hq, Hkv, Sq, chunk.cap, D, scale, window > 0 ? window : kAllKeys,
-                             window > 0 ? sinks : 0, kv_lens, q_lens, stream, bf16);
+                             window > 0 ? sinks : 0, kv_lens, q_lens, block_table, page_shift_of(page), n_pages, stream,
+                             bf16);
     }
     paged::AttendParams p{};
     p.q = static_cast<const uint16_t*>(q);

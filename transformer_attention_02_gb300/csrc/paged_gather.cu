@@ -50,7 +50,8 @@ __device__ __forceinline__ uint4 widen_piece(uint2 w, float scale, bool bf16) {
 __device__ __forceinline__ uint4 widen_piece(uint4 w, float, bool) { return w; }
 
 // CTAs [0, p.copies): 128 keys of one K/V head of a sequence, zeros for those that
-// no query sees and past its last key (the products read whole blocks of 128). The
+// no query sees, past its last key (the products read whole blocks of 128) and in
+// pages out of range (which the products' kernel hides: it has the table). The
 // others: 16-byte pieces of the queries, rotated to their positions. 8-bit pages in
 // five CTAs an SM, 48 registers (four: 16 x 256 queries over 8192 keys 573 us, five 568).
 template <int CT>
