@@ -380,8 +380,9 @@ size_t attn_block_workspace_bytes(int B, int S, int Hq, int Hkv, int D);
  * Other arguments, layouts, results and errors as for attn_fwd / attn_fwd_f16;
  * rows without a visible key get o = 0, lse = -inf. Blocks of 128 keys that no
  * row of a 256-row tile sees are neither read nor computed, so the time grows
- * with Sq * (window + sinks), not with Sq * Sk. As for attn_fwd, a key hidden
- * from some rows of a tile only must be finite in V.
+ * with Sq * (window + sinks), not with Sq * Sk. V must be finite at every key of a
+ * block that is read, hidden ones among them: as in attn_fwd, they enter with
+ * weights of zero.
  */
 int attn_fwd_window(const void *q, const void *k, const void *v, void *o, float *lse,
                     int B, int Hq, int Hkv, int Sq, int Sk, int D,
@@ -398,7 +399,8 @@ int attn_fwd_window_f16(const void *q, const void *k, const void *v, void *o, fl
  *               ATTN_CACHE_E4M3: 8-bit e4m3 codes of value / scale
  *   k_scale, v_scale   device, FP32, (n_pages, Hkv): one scale per page and
  *               K/V head, from 2^-100 to 2^120 (e4m3 only, else ignored and may
- *               be NULL)
+ *               be NULL). The attention counts values by weight times scale, scales
+ *               below 2^-72 as 2^-72: values under 2^-63 lose bits and fade to zero
  *   block_table device, int32, (B, max_pages): page of tokens [j * page,
  *               (j + 1) * page) of each sequence. Sequences may share pages that
  *               are only read; a page that attn_kv_append writes must stand
@@ -458,8 +460,9 @@ int attn_kv_append_f16(const void *k, const void *v, long long k_stride, long lo
  * those with j > p - window or j < sinks (the first `sinks` tokens stay visible
  * for good). One token per sequence, several draft tokens, or a chunk of a
  * prompt. Slots behind kv_lens may hold anything. Keys that no query of the
- * call sees are not read, or enter as zeros; a key that only some queries see
- * must be finite in V, as for attn_fwd.
+ * call sees are not read, or enter as zeros, and the numbers and scales of pages
+ * that hold no other are not looked at; a key that only some queries see
+ * must be finite in V.
  *   q           device, (B, Sq, Hq, D), 16-byte aligned, q_stride elements from
  *               token to token (as k_stride above, at least Hq * D)
  *   o, lse      device, (B, Sq, Hq, D) contiguous and FP32 (B, Hq, Sq), apart from

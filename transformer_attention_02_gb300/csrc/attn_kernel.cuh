@@ -218,11 +218,11 @@ struct TileInfo {
 // from the oldest key of its first row's window to its last row's own key.
 // Both sub-tiles walk the same list; the upper one, whose windows begin 128
 // keys later, passes over the window's first block unless sinks lie in it.
-// Measured: 16384 tokens, 32/8 heads of 128, window 4096 and 4 sinks, bf16: 709
-// us, 1358 TFLOP/s of visible pairs (0.69 of a large library product; the plain
+// Measured: 16384 tokens, 32/8 heads of 128, window 4096 and 4 sinks, bf16: 712
+// us, 1352 TFLOP/s of visible pairs (0.69 of a large library product; the plain
 // causal variant reaches 0.72 to 0.77). Narrow windows are bound by the softmax
 // of whole blocks and by the tiles' ends: 4 x 2048 tokens, 32 heads of 64,
-// window 512, fp16: 72 us, five blocks a row for four visible ones.
+// window 512, fp16: 72.6 us, five blocks a row for four visible ones.
 constexpr int kSkipsFirst = 1 << 30, kMissingPages = 1 << 29;      // above every count of blocks (2^23)
 template <bool CAUSAL, bool PACK, bool WINDOW = false, bool RAGGED = false>
 __device__ __forceinline__ TileInfo tile_info(int tile, const FwdParams& p) {

@@ -28,7 +28,9 @@ namespace {
 
 // A block's new tokens as 16-byte pieces (eight values): HELD a thread. Steps of
 // few tokens have one piece a thread and up to 512 threads, prompts four and up
-// to 256, large pages eight and up to 512 (256 tokens of 16 pieces).
+// to 256, large pages eight and up to 512 (256 tokens of 16 pieces). (4 x 2048
+// tokens, 32 heads of 128 into e4m3 pages of 16, 64, 128, 256: 65.6, 41.0, 47.6, 68.2
+// us; over e4m3 four pieces spill 24 bytes a thread, eight 92 to 120.)
 __host__ __device__ constexpr int max_threads(int held) { return held == 4 ? 256 : 512; }
 __host__ __device__ constexpr int min_ctas(int held) { return held == 4 ? 3 : 1; }
 

@@ -35,11 +35,11 @@
 //
 // Measured (attention and merge, graph replay; the copy bandwidth of the same
 // GPU is 6.70 TB/s): 16 sequences of 8192 keys, 8 K/V heads of 128, 4 query rows
-// a head: e4m3 47.2 us, 5.69 TB/s, 16-bit 85.4 us, 6.28 TB/s; 32 heads of one
-// row over 16-bit keys (16 x 4096, 1.07 GB) 161 us, 6.67 TB/s. What is left are
+// a head: e4m3 47.6 us, 5.65 TB/s, 16-bit 85.6 us, 6.28 TB/s; 32 heads of one
+// row over 16-bit keys (16 x 4096, 1.07 GB) 162 us, 6.62 TB/s. What is left are
 // the ends: the chain lengths - page numbers - first keys (2 us), SMs that finish
-// 3 to 4 us apart, the second kernel (2). More rows over e4m3: 16 rows 52.8 us,
-// 24 59.4, 32 69.8; there the tensor cores, the conversions before them and the
+// 3 to 4 us apart, the second kernel (2). More rows over e4m3: 16 rows 53.0 us,
+// 24 60.1, 32 70.3; there the tensor cores, the conversions before them and the
 // softmax of a stage wait on one another.
 #pragma once
 
@@ -68,7 +68,8 @@ struct Cfg {
     // four warps cover one another's change of segment (barriers, merge, queries),
     // and stages of 32 keys (64 of 64 8-bit dims) spend one look at the queries'
     // fragments, one vote and one turn of the loop on two (four) tiles. Measured
-    // over e4m3, 8 K/V heads, 16 x 8192 keys / 256 x 512:
+    // over e4m3, 8 K/V heads, 16 x 8192 keys / 256 x 512 (side by side, before row
+    // sums were rescaled by a root twice, which costs blocks of 20 rows and more 1%):
     //   4 rows of 128   two CTAs of eight warps, 16 keys 49.5 / 62.6 us, three of four, 32 keys 47.3 / 57.6
     //   16 rows of 128  two of eight, 16 keys 54.6 / 86.5, two of four, 32 keys 53.3 / 76.5, three of four 52.9 / 71.4
     //   20 rows of 128  one of eight, 16 keys 70.3 / 140.0, two of four 63.4 / 96.6, 32 keys 58.0 / 91.2

@@ -6,8 +6,8 @@
 // and they belong on tcgen05: the kernel of paged_attn.cuh reaches some 330
 // TFLOP/s there (mma.sync, the cache read once per 32 rows), this path the
 // fused kernel's rate less one pass over the cache: 16 x 256 queries over 8192
-// e4m3 keys (32/8 heads of 128) 561 us, 964 TFLOP/s; one chunk of 2048 over 16384
-// 424 us, 1216 TFLOP/s. Keys and values become
+// e4m3 keys (32/8 heads of 128) 566 us, 956 TFLOP/s; one chunk of 2048 over 16384
+// 428 us, 1204 TFLOP/s. Keys and values become
 // code * scale, exact in bf16 for power-of-two scales (four significant bits).
 // Bound by memory: each visible page is read once and written once at 16 bits.
 #include <type_traits>

@@ -113,9 +113,9 @@ int launch_attend(bool (&attr_set)[2][4], const AttendParams& p, int D, cudaStre
 // An attention goes by the gathered pages (paged_gather.cu) from kChunkRows
 // queries a sequence and kChunkTiles tiles of 256 rows of a head: a third of the
 // SMs. Measured over e4m3, 32/8 heads of 128, by the cache itself / gathered: 16
-// sequences of 8192 keys, 128 queries 838 / 508 us, 256 queries 1655 / 566; two,
-// 128 queries (64 tiles, half filled) 119 / 116; one sequence of 32768 keys, 128
-// queries (32 tiles) 212 / 406.
+// sequences of 8192 keys, 128 queries 850 / 514 us, 256 queries 1675 / 566; two,
+// 128 queries (64 tiles, half filled) 121 / 116; one sequence of 32768 keys, 128
+// queries (32 tiles) 215 / 406.
 constexpr int kChunkRows = 128;
 constexpr int kChunkTiles = 48;
 constexpr long long kChunkLimit = 4LL << 30;     // bytes of gathered tensors at most
