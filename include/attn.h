@@ -508,6 +508,59 @@ int attn_fwd_paged_f16(const void *q, long long q_stride, const void *k_cache, c
 size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, long long max_keys);
 
 /*
+ * attn_bwd / attn_bwd_f16 — backward pass of attn_fwd, attn_fwd_window and
+ * attn_fwd_qkvpacked: the gradients of Q, K and V from the gradient of O. With
+ * P = softmax of the scaled and masked logits, recomputed block by block,
+ *     dV = P^T dO,  dS = P o (dO V^T - rowsum(dO o O)),
+ *     dQ = scale dS K,  dK = scale dS^T Q,
+ * dK and dV summed over the query heads of a K/V head. bf16 / fp16 tensors, FP32
+ * sums and statistics; P and dS are rounded to the tensors' type as operands.
+ * With rotated queries and keys pass those; their gradients turn back by
+ * the rotation with the opposite angle.
+ *   d_o, o      device, (B, Sq, Hq, D) contiguous: the output's gradient, and the
+ *               output as the forward pass wrote it; 16-byte aligned like all
+ *               tensors here
+ *   lse         device, FP32, (B, Hq, Sq), as the forward pass wrote it
+ *   q, dq       device, (B, Sq, Hq, D); a token's (H, D) values are contiguous and
+ *               q_stride / dq_stride (elements, a multiple of 8, at least Hq * D)
+ *               lead from token to token of the flattened (B, S), so that they may
+ *               be slices of a packed projection
+ *   k, v, dk, dv  device, (B, Sk, Hkv, D), with strides of their own
+ *               The gradients are written whole and overlap no input and no
+ *               other tensor, but may interleave in one packed tensor.
+ *   scale, mask_kind, mask  as for attn_fwd. The mask has no gradient. Mask values
+ *               below -2.3e38 hide a key as -inf does. With an additive mask the
+ *               rows' statistics are found anew, in one more pass over the
+ *               keys: a mask of large values leaves lse without the logits' bits.
+ *   window, sinks  window > 0 (causal mask only): as for attn_fwd_window; 0: none
+ *   workspace   device scratch of attn_bwd_workspace_bytes(...) bytes, 256-byte
+ *               aligned, contents overwritten. Calls that may run at the same
+ *               time need one each.
+ * A row without a visible key gives no gradient: its dQ is 0 and it adds nothing
+ * to dK and dV. With Sq or Sk of 0 the gradients that exist are 0. Blocks of 128
+ * keys and 128 queries that hide all of their pairs are not computed. Q, K, V and dO
+ * must be finite in the others, hidden pairs included: those enter with weights of
+ * zero. Results do not depend on the order of execution (no atomics).
+ * Errors as for attn_fwd.
+ */
+int attn_bwd(const void *d_o, const void *q, const void *k, const void *v, const void *o, const float *lse,
+             void *dq, void *dk, void *dv, long long q_stride, long long k_stride, long long v_stride,
+             long long dq_stride, long long dk_stride, long long dv_stride,
+             int B, int Hq, int Hkv, int Sq, int Sk, int D,
+             float scale, int mask_kind, const float *mask, int window, int sinks,
+             void *workspace, size_t workspace_bytes, attn_stream_t stream);
+int attn_bwd_f16(const void *d_o, const void *q, const void *k, const void *v, const void *o, const float *lse,
+                 void *dq, void *dk, void *dv, long long q_stride, long long k_stride, long long v_stride,
+                 long long dq_stride, long long dk_stride, long long dv_stride,
+                 int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                 float scale, int mask_kind, const float *mask, int window, int sinks,
+                 void *workspace, size_t workspace_bytes, attn_stream_t stream);
+
+/* attn_bwd_workspace_bytes — workspace bytes attn_bwd needs for these sizes
+ * (host only; 0 for an empty problem or invalid sizes). */
+size_t attn_bwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D, int mask_kind);
+
+/*
  * attn_last_status — synchronises `stream`, then returns and clears the
  * current device's run-time status word: ATTN_OK, or ATTN_ERR_DEVICE_TIMEOUT
  * if any launch since the last call gave up on a bounded wait (the kernel then

@@ -97,6 +97,11 @@ def lib() -> ctypes.CDLL:
         f.restype = I
     L.attn_paged_workspace_bytes.argtypes = [I, I, I, I, I, LL]
     L.attn_paged_workspace_bytes.restype = ctypes.c_size_t
+    for f in (L.attn_bwd, L.attn_bwd_f16):
+        f.argtypes = [P] * 9 + [LL] * 6 + [I] * 6 + [F, I, P, I, I, P, ctypes.c_size_t, P]
+        f.restype = I
+    L.attn_bwd_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
+    L.attn_bwd_workspace_bytes.restype = ctypes.c_size_t
     L.attn_last_status.argtypes = [P]
     L.attn_last_status.restype = I
     L.attn_status_string.argtypes = [I]
@@ -250,6 +255,23 @@ def attn_fwd_paged_f16(q, q_stride, k_cache, v_cache, k_scale, v_scale, block_ta
 
 def attn_paged_workspace_bytes(B, Hq, Hkv, Sq, D, max_keys=0) -> int:
     return int(lib().attn_paged_workspace_bytes(B, Hq, Hkv, Sq, D, max_keys))
+
+
+def attn_bwd(d_o, q, k, v, o, lse, dq, dk, dv, q_stride, k_stride, v_stride, dq_stride, dk_stride, dv_stride, B, Hq, Hkv,
+             Sq, Sk, D, scale, mask_kind, mask, window, sinks, workspace, workspace_bytes, stream) -> int:
+    return lib().attn_bwd(d_o, q, k, v, o, lse, dq, dk, dv, q_stride, k_stride, v_stride, dq_stride, dk_stride, dv_stride,
+                          B, Hq, Hkv, Sq, Sk, D, scale, mask_kind, mask, window, sinks, workspace, workspace_bytes, stream)
+
+
+def attn_bwd_f16(d_o, q, k, v, o, lse, dq, dk, dv, q_stride, k_stride, v_stride, dq_stride, dk_stride, dv_stride, B, Hq,
+                 Hkv, Sq, Sk, D, scale, mask_kind, mask, window, sinks, workspace, workspace_bytes, stream) -> int:
+    return lib().attn_bwd_f16(d_o, q, k, v, o, lse, dq, dk, dv, q_stride, k_stride, v_stride, dq_stride, dk_stride,
+                              dv_stride, B, Hq, Hkv, Sq, Sk, D, scale, mask_kind, mask, window, sinks, workspace,
+                              workspace_bytes, stream)
+
+
+def attn_bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, mask_kind=0) -> int:
+    return int(lib().attn_bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, mask_kind))
 
 
 def attn_last_status(stream) -> int:
@@ -903,3 +925,86 @@ def attention_paged(q, k_cache, v_cache, block_table, kv_lens, *, q_lens=None, k
     if rc:
         raise AttnError(rc, "attn_fwd_paged")
     return out, lse
+
+
+# ------------------------------------------------------------ the backward pass
+
+def _mask_arg(mask, at, shape):
+    """Address of an additive mask, checked, or None."""
+    if mask is None:
+        return None
+    if mask.dtype is not _torch.float32 or mask.get_device() != at or mask.shape != shape or not mask.is_contiguous():
+        raise ValueError("mask must be a contiguous FP32 CUDA tensor of shape (B, Sq, Sk) on q's device")
+    return mask.data_ptr()
+
+
+def _gradient(name, t, like, at, stream):
+    """(tensor, token stride): the given gradient, checked, or a new contiguous one of `like`'s shape and type."""
+    if t is None:
+        t = _new(like.shape, like.dtype, like, stream)
+    elif t.dtype is not like.dtype or t.get_device() != at or t.shape != like.shape:
+        raise ValueError(f"{name} must be a tensor of the shape, type and device of what it is the gradient of")
+    return t, _token_stride(name, t, at)
+
+
+def _own_workspace(workspace, size, like, at, stream):
+    """The given workspace, checked, or a new one of `size` bytes."""
+    if workspace is None:
+        return _new((max(size, 1),), _torch.uint8, like, stream)
+    if workspace.get_device() != at or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on q's device")
+    return workspace
+
+
+def _attention_mask(causal, mask, window):
+    """The mask kind of a backward pass; a window needs a causal one."""
+    if window and (not causal or mask is not None):
+        raise ValueError("a window needs causal=True and no additive mask")
+    return (MASK_CAUSAL if causal else MASK_NONE) + (MASK_ADDITIVE if mask is not None else 0)
+
+
+def attention_backward(d_o, q, k, v, o, lse, *, causal: bool = False, mask=None, window: int = 0, sinks: int = 0,
+                       scale=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """dQ, dK, dV = the gradients of attention(), attention_qkvpacked() or, with window > 0, attention_window().
+
+    d_o: the gradient of the output, and o (B, Sq, Hq, D) and lse (B, Hq, Sq) as the forward call returned them. q
+    (B, Sq, Hq, D), k, v (B, Sk, Hkv, D): bf16 or fp16 CUDA tensors, contiguous or evenly spaced slices of a packed
+    projection; so may be dq, dk, dv (new contiguous tensors by default), which overlap no input. causal, mask, window,
+    sinks, scale: those of the forward call; the mask has no gradient. workspace: optional uint8 CUDA tensor of at least
+    attn_bwd_workspace_bytes bytes.
+    """
+    at = _device_of(q, "q")
+    for name, t in (("k", k), ("v", v), ("o", o), ("d_o", d_o)):
+        if t.dtype is not q.dtype or t.dim() != 4:
+            raise ValueError(f"{name} must be a 4-D tensor (B, S, H, D) of q's type")
+    q_stride, k_stride, v_stride = _token_stride("q", q, at), _token_stride("k", k, at), _token_stride("v", v, at)
+    B, Sq, Hq, D = q.shape
+    Sk, Hkv = k.shape[1], k.shape[2]
+    if k.shape[0] != B or k.shape[3] != D or v.shape != k.shape:
+        raise ValueError("q, k, v shapes disagree")
+    for name, t in (("o", o), ("d_o", d_o)):
+        if t.shape != q.shape or t.get_device() != at or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor of q's shape and device")
+    if (lse.dtype is not _torch.float32 or lse.get_device() != at or lse.shape != (B, Hq, Sq)
+            or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous FP32 (B, Hq, Sq) tensor on q's device")
+    window, sinks = _count("window", window), _count("sinks", sinks)
+    kind = _attention_mask(causal, mask, window)
+    L = _lib or lib()
+    back = _enter_device(at)
+    try:
+        dq, dq_stride = _gradient("dq", dq, q, at, stream)
+        dk, dk_stride = _gradient("dk", dk, k, at, stream)
+        dv, dv_stride = _gradient("dv", dv, v, at, stream)
+        ws = _own_workspace(workspace, L.attn_bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, kind), q, at, stream)
+        fn = L.attn_bwd if q.dtype is _torch.bfloat16 else L.attn_bwd_f16
+        rc = fn(d_o.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dq.data_ptr(),
+                dk.data_ptr(), dv.data_ptr(), q_stride, k_stride, v_stride, dq_stride, dk_stride, dv_stride, B, Hq, Hkv, Sq,
+                Sk, D, _NAN if scale is None else scale, kind, _mask_arg(mask, at, (B, Sq, Sk)), window, sinks,
+                ws.data_ptr(), ws.numel() * ws.element_size(), _stream_on(at, stream))
+    finally:
+        if back is not None:
+            _torch.cuda.set_device(back)
+    if rc:
+        raise AttnError(rc, "attn_bwd")
+    return dq, dk, dv

@@ -26,7 +26,7 @@
 
 namespace {
 
-constexpr int kAbiVersion = 6;
+constexpr int kAbiVersion = 7;
 constexpr unsigned long long kDefaultTimeoutNs = 2000000000ull;
 constexpr int kMaxContexts = 64;
 
@@ -51,6 +51,7 @@ struct DeviceInfo {
     bool gemm_attr_set = false;
     bool ln_attr_set[3] = {};
     bool paged_attr_set[3][2][4] = {};     // [cache type][D is 128][rows of a block]
+    bool bwd_attr_set[2][2][2][2] = {};    // [D is 128][bf16][additive mask][dQ, dK and dV]
 };
 
 std::mutex g_mutex;
@@ -142,6 +143,9 @@ int attn::device_state(DeviceState* out) {
     out->num_sms = d->num_sms;
     out->status = d->status;
     out->paged_attr_set = d->paged_attr_set;
+    out->bwd_attr_set = d->bwd_attr_set;
+    out->timeout_ns = g_timeout_ns.load();
+    out->stall = g_debug_stall.load() != 0;
     return ATTN_OK;
 }
 
@@ -165,6 +169,14 @@ int encode_bshd(CUtensorMap* map, const void* base, int B, int S, int H, int D, 
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
+
+}  // namespace
+
+int attn::encode_tokens(CUtensorMap* map, const void* base, int B, int S, int H, int D, bool bf16, long long token_stride) {
+    return encode_bshd(map, base, B, S, H, D, bf16, token_stride);
+}
+
+namespace {
 
 __global__ void fill_empty_rows_kernel(uint16_t* o, size_t n_o, float* lse, size_t n_lse) {
     const size_t stride = (size_t)gridDim.x * blockDim.x;

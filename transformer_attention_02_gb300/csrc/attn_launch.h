@@ -35,11 +35,19 @@ struct DeviceState {
     int num_sms;
     unsigned int* status;                 // run-time status word
     bool (*paged_attr_set)[2][4];         // [cache type]: see paged::launch_attend
+    bool (*bwd_attr_set)[2][2][2];        // [D is 128]: see the backward pass's launchers
+    unsigned long long timeout_ns;        // limit of every wait
+    bool stall;                           // failure-detection test hook
 };
 
 // Fills `out` for the current context. Returns ATTN_OK, ATTN_ERR_UNSUPPORTED
 // (not an sm_103 device) or ATTN_ERR_CUDA.
 int device_state(DeviceState* out);
+
+// Tensor map of a (B, S, H, D) 16-bit tensor, token_stride elements from token to
+// token: boxes of 64 columns x 128 tokens of one head, 128-byte swizzle.
+// device_state() has been called. Returns ATTN_OK or ATTN_ERR_CUDA.
+int encode_tokens(CUtensorMap* map, const void* base, int B, int S, int H, int D, bool bf16, long long token_stride);
 
 // Causal attention with a window (at most 2^30; sinks >= 0) over contiguous
 // tensors of capacity Sk whose lengths differ by sequence and are read on the

@@ -1,0 +1,189 @@
+// Entry points of the attention's backward pass (declared in include/attn.h):
+// argument checks, workspace layout and launches.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/attn.h"
+#include "attn_launch.h"
+#include "bwd_params.h"
+
+namespace {
+
+using namespace attn;
+
+bool aligned(const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0; }
+
+constexpr size_t kWorkspaceAlign = 256;
+size_t align_up(size_t x) { return (x + kWorkspaceAlign - 1) / kWorkspaceAlign * kWorkspaceAlign; }
+
+bool is_additive(int mask_kind) { return mask_kind == ATTN_MASK_ADDITIVE || mask_kind == ATTN_MASK_CAUSAL_ADDITIVE; }
+
+// Three rows of statistics for every query row, the third with an additive mask only.
+size_t stat_bytes(int B, int Hq, int Sq) { return align_up((size_t)B * Hq * bwd::padded_rows(Sq) * sizeof(float)); }
+size_t bwd_workspace(int B, int Hq, int Sq, int mask_kind) { return stat_bytes(B, Hq, Sq) * (is_additive(mask_kind) ? 3 : 2); }
+
+// A tensor of tokens: pointer, distance of tokens, H * D values a token. Null only where it is empty.
+bool tokens_ok(const void* ptr, long long stride, int B, int S, int H, int D) {
+    if ((long long)B * S * H == 0) return true;
+    // (the distances of a tensor map have 40 bits)
+    return ptr && aligned(ptr, 16) && stride >= (long long)H * D && stride % 8 == 0 && stride < (1LL << 39) / std::max(1, S);
+}
+
+int check_sizes(int B, int Hq, int Hkv, int Sq, int Sk, int D) {
+    if (B < 0 || Hq < 0 || Hkv <= 0 || Sq < 0 || Sk < 0 || D <= 0 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+    if (Sq > (1 << 30) || Sk > (1 << 30)) return ATTN_ERR_INVALID_ARG;
+    const long long nq = bwd::padded_rows(Sq) / bwd::kBlock, nk = bwd::padded_rows(Sk) / bwd::kBlock;
+    if ((double)B * Hq * nq > 2147483647.0 || (double)B * Hkv * nk > 2147483647.0 || (double)nq * (Hq / Hkv) > 2147483647.0)
+        return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+
+int zero_tokens(void* ptr, long long stride, int B, int S, int H, int D, cudaStream_t stream) {
+    if ((long long)B * S * H == 0) return ATTN_OK;
+    return cudaMemset2DAsync(ptr, (size_t)stride * 2, 0, (size_t)H * D * 2, (size_t)B * S, stream) == cudaSuccess
+               ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+template <int D, bool BF16, bool ADDITIVE>
+int launch_both(const DeviceState& dev, const CUtensorMap* maps, bwd::BwdParams& p, cudaStream_t stream) {
+    bool* attr = dev.bwd_attr_set[D == 128][BF16][ADDITIVE];
+    p.n_tiles = p.B * p.Hq * p.n_qb;
+    int rc = bwd::launch_dq<D, BF16, ADDITIVE>(attr[0], maps[0], maps[1], maps[2], maps[3], p,
+                                               std::min(p.n_tiles, dev.num_sms), stream);
+    if (rc != ATTN_OK) return rc;
+    p.n_tiles = p.B * p.Hkv * p.n_kb;
+    return bwd::launch_dkv<D, BF16, ADDITIVE>(attr[1], maps[0], maps[1], maps[2], maps[3], p,
+                                              std::min(p.n_tiles, dev.num_sms), stream);
+}
+
+int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const void* o, const float* lse, void* dq,
+             void* dk, void* dv, long long q_stride, long long k_stride, long long v_stride, long long dq_stride,
+             long long dk_stride, long long dv_stride, int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale,
+             int mask_kind, const float* mask, int window, int sinks, void* workspace, size_t workspace_bytes,
+             cudaStream_t stream, bool bf16) {
+    int rc = check_sizes(B, Hq, Hkv, Sq, Sk, D);
+    if (rc != ATTN_OK) return rc;
+    if (mask_kind < ATTN_MASK_NONE || mask_kind > ATTN_MASK_CAUSAL_ADDITIVE || window < 0 || sinks < 0)
+        return ATTN_ERR_INVALID_ARG;
+    if (window > 0 && mask_kind != ATTN_MASK_CAUSAL) return ATTN_ERR_INVALID_ARG;
+    const long long q_values = (long long)B * Sq * Hq, kv_values = (long long)B * Sk;
+    if (!tokens_ok(q, q_stride, B, Sq, Hq, D) || !tokens_ok(k, k_stride, B, Sk, Hkv, D) ||
+        !tokens_ok(v, v_stride, B, Sk, Hkv, D) || !tokens_ok(dq, dq_stride, B, Sq, Hq, D) ||
+        !tokens_ok(dk, dk_stride, B, Sk, Hkv, D) || !tokens_ok(dv, dv_stride, B, Sk, Hkv, D) ||
+        !tokens_ok(d_o, (long long)Hq * D, B, Sq, Hq, D) || !tokens_ok(o, (long long)Hq * D, B, Sq, Hq, D))
+        return ATTN_ERR_INVALID_ARG;
+    const bool additive = is_additive(mask_kind);
+    if (q_values > 0 && (!lse || !aligned(lse, 4))) return ATTN_ERR_INVALID_ARG;
+    if (additive && q_values > 0 && kv_values > 0 && (!mask || !aligned(mask, 4))) return ATTN_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !std::isfinite(scale)) scale = 1.0f / std::sqrt((float)D);
+    if (q_values == 0 || kv_values == 0) {                        // no pair of a query and a key: no gradients
+        if (q_values == 0 && kv_values == 0) return ATTN_OK;
+        DeviceState dev{};
+        if ((rc = device_state(&dev)) != ATTN_OK || (rc = zero_tokens(dq, dq_stride, B, Sq, Hq, D, stream)) != ATTN_OK ||
+            (rc = zero_tokens(dk, dk_stride, B, Sk, Hkv, D, stream)) != ATTN_OK)
+            return rc;
+        return zero_tokens(dv, dv_stride, B, Sk, Hkv, D, stream);
+    }
+    if (!workspace || !aligned(workspace, kWorkspaceAlign) || workspace_bytes < bwd_workspace(B, Hq, Sq, mask_kind))
+        return ATTN_ERR_INVALID_ARG;
+
+    DeviceState dev{};
+    rc = device_state(&dev);
+    if (rc != ATTN_OK) return rc;
+    CUtensorMap maps[4];
+    if (encode_tokens(&maps[0], q, B, Sq, Hq, D, bf16, q_stride) != ATTN_OK ||
+        encode_tokens(&maps[1], k, B, Sk, Hkv, D, bf16, k_stride) != ATTN_OK ||
+        encode_tokens(&maps[2], v, B, Sk, Hkv, D, bf16, v_stride) != ATTN_OK ||
+        encode_tokens(&maps[3], d_o, B, Sq, Hq, D, bf16, (long long)Hq * D) != ATTN_OK)
+        return ATTN_ERR_CUDA;
+    const size_t stat = stat_bytes(B, Hq, Sq);
+    char* const ws = static_cast<char*>(workspace);
+
+    bwd::PrepParams pp{};
+    pp.o = static_cast<const uint16_t*>(o);
+    pp.d_o = static_cast<const uint16_t*>(d_o);
+    pp.lse = additive ? nullptr : lse;
+    pp.neg_lse = reinterpret_cast<float*>(ws);
+    pp.neg_delta = reinterpret_cast<float*>(ws + stat);
+    pp.B = B;
+    pp.Hq = Hq;
+    pp.Sq = Sq;
+    pp.Sp = (int)bwd::padded_rows(Sq);
+    pp.D = D;
+    rc = bwd::launch_prep(pp, bf16, dev.num_sms, stream);
+    if (rc != ATTN_OK) return rc;
+
+    constexpr int kAllKeys = 1 << 30;                     // a longer window hides nothing; differences stay in 32 bits
+    bwd::BwdParams p{};
+    p.neg_lse = pp.neg_lse;
+    p.neg_delta = pp.neg_delta;
+    p.inv_sum = additive ? reinterpret_cast<float*>(ws + 2 * stat) : nullptr;
+    p.mask = additive ? mask : nullptr;
+    p.dq = dq;
+    p.dk = dk;
+    p.dv = dv;
+    p.dq_stride = dq_stride;
+    p.dk_stride = dk_stride;
+    p.dv_stride = dv_stride;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.Sq = Sq;
+    p.Sk = Sk;
+    p.Sp = pp.Sp;
+    p.group = Hq / Hkv;
+    p.n_qb = pp.Sp / bwd::kBlock;
+    p.n_kb = (int)(bwd::padded_rows(Sk) / bwd::kBlock);
+    p.off = Sk - Sq;
+    p.causal = mask_kind == ATTN_MASK_CAUSAL || mask_kind == ATTN_MASK_CAUSAL_ADDITIVE;
+    p.window = std::min(window, kAllKeys);
+    p.sinks = window > 0 ? std::min(sinks, kAllKeys) : 0;
+    p.vec8 = aligned(dq, 32) && aligned(dk, 32) && aligned(dv, 32) && dq_stride % 16 == 0 && dk_stride % 16 == 0 &&
+             dv_stride % 16 == 0;
+    p.stall = dev.stall;
+    p.scale = scale;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.timeout_ns = dev.timeout_ns;
+    p.status = dev.status;
+    if (D == 128) {
+        if (additive) return bf16 ? launch_both<128, true, true>(dev, maps, p, stream) : launch_both<128, false, true>(dev, maps, p, stream);
+        return bf16 ? launch_both<128, true, false>(dev, maps, p, stream) : launch_both<128, false, false>(dev, maps, p, stream);
+    }
+    if (additive) return bf16 ? launch_both<64, true, true>(dev, maps, p, stream) : launch_both<64, false, true>(dev, maps, p, stream);
+    return bf16 ? launch_both<64, true, false>(dev, maps, p, stream) : launch_both<64, false, false>(dev, maps, p, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_bwd(const void* d_o, const void* q, const void* k, const void* v, const void* o, const float* lse, void* dq,
+             void* dk, void* dv, long long q_stride, long long k_stride, long long v_stride, long long dq_stride,
+             long long dk_stride, long long dv_stride, int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale,
+             int mask_kind, const float* mask, int window, int sinks, void* workspace, size_t workspace_bytes,
+             attn_stream_t stream) {
+    return bwd_impl(d_o, q, k, v, o, lse, dq, dk, dv, q_stride, k_stride, v_stride, dq_stride, dk_stride, dv_stride, B, Hq,
+                    Hkv, Sq, Sk, D, scale, mask_kind, mask, window, sinks, workspace, workspace_bytes,
+                    reinterpret_cast<cudaStream_t>(stream), true);
+}
+
+int attn_bwd_f16(const void* d_o, const void* q, const void* k, const void* v, const void* o, const float* lse, void* dq,
+                 void* dk, void* dv, long long q_stride, long long k_stride, long long v_stride, long long dq_stride,
+                 long long dk_stride, long long dv_stride, int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale,
+                 int mask_kind, const float* mask, int window, int sinks, void* workspace, size_t workspace_bytes,
+                 attn_stream_t stream) {
+    return bwd_impl(d_o, q, k, v, o, lse, dq, dk, dv, q_stride, k_stride, v_stride, dq_stride, dk_stride, dv_stride, B, Hq,
+                    Hkv, Sq, Sk, D, scale, mask_kind, mask, window, sinks, workspace, workspace_bytes,
+                    reinterpret_cast<cudaStream_t>(stream), false);
+}
+
+size_t attn_bwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D, int mask_kind) {
+    if (check_sizes(B, Hq, Hkv, Sq, Sk, D) != ATTN_OK || mask_kind < ATTN_MASK_NONE || mask_kind > ATTN_MASK_CAUSAL_ADDITIVE)
+        return 0;
+    if ((long long)B * Sq * Hq == 0 || Sk == 0) return 0;
+    return bwd_workspace(B, Hq, Sq, mask_kind);
+}
+
+}  // extern "C"

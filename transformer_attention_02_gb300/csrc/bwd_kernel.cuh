@@ -1,0 +1,851 @@
+// Backward pass of the fused attention for sm_103a. With G = Hq / Hkv,
+//   P_ij  = exp(scale <q_i, k_j> + mask_ij - lse_i)     (recomputed, never stored)
+//   dV_j  = sum_i P_ij dO_i
+//   dP_ij = <dO_i, v_j>
+//   dS_ij = P_ij (dP_ij - delta_i),   delta_i = <dO_i, O_i>
+//   dQ_i  = scale sum_j dS_ij k_j,    dK_j = scale sum_i dS_ij q_i
+// where the sums for dK and dV run over the G query heads of a K/V head too.
+//
+// Two kernels, of which each owns what it writes:
+//   bwd_dkv_kernel  a tile is (b, K/V head, 128 keys); it walks the queries that
+//                   see the keys, of all G heads, and holds dK and dV in TMEM;
+//   bwd_dq_kernel   a tile is (b, query head, 128 queries); it walks the keys
+//                   that they see and holds dQ in TMEM.
+// S and dP are computed in both, so seven products run where five would do. One
+// kernel with five would have to add dQ up in device memory from all key blocks,
+// with atomics (whose order changes the result) or behind a lock, 4 bytes x D a
+// query and key block; and dK, dV, dQ, S and dP of 128 x 128 x 128 tiles do not fit
+// TMEM together. With two kernels nothing is atomic, and results are the same
+// from run to run.
+//
+// Both are bound by the tensor cores: four (three) products of 512 cycles at D =
+// 128 stand against one exponential a pair (512 cycles of the SM's 32 a cycle).
+// Roles of a CTA (384 threads): warps 0-7 take the S and dP tiles from TMEM and
+// put P and dS back in 16 bits (warps 0-3 columns 0-63 of each, warps 4-7 the
+// others; a warp's lanes are 32 rows), warp 8 issues the products, warp 9 the
+// loads.
+//
+// P enters its product in the inputs' 16-bit type, as in the forward pass, and
+// so does dS: the tensor cores take both operands in one type. Each is rounded
+// once, from FP32, so that a term is off by half a step of that type, as the
+// inputs themselves are; sums are FP32.
+#pragma once
+
+#include "../../include/attn.h"
+#include "attn_kernel.cuh"
+#include "bwd_params.h"
+
+namespace attn {
+namespace bwd {
+
+constexpr int kThreads = 384;
+constexpr int kIssueWarp = 8;
+constexpr int kLoadWarp = 9;
+constexpr uint32_t kRowBytes = kBlock * sizeof(float);     // 128 row statistics
+constexpr float kLog2E = 1.4426950408889634f;
+
+// ------------------------------------------------------------ shared pieces
+
+// The 128 x D tiles: boxes of 64 columns, 128-byte rows, 128-byte swizzle.
+template <int D>
+struct Tile {
+    static constexpr int kBoxes = D / 64;
+    static constexpr int kBoxBytes = 128 * 128;
+    static constexpr int kBytes = kBoxes * kBoxBytes;
+};
+
+template <int D>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar, int h, int row, int b) {
+#pragma unroll
+    for (int c = 0; c < Tile<D>::kBoxes; ++c)
+        ptx::tma_load_4d(dst + c * Tile<D>::kBoxBytes, map, bar, c * 64, h, row, b);
+}
+
+// D(tmem) = A B^T of two tiles, summed over the head dimension.
+template <int D, bool BF16>
+__device__ __forceinline__ void product_over_d(uint32_t d, uint32_t a, uint32_t b) {
+    constexpr uint32_t kIdesc = ptx::idesc_f16(kBlock, kBlock, BF16, false, false);
+    const uint64_t ad = ptx::sdesc_kmajor_sw128(a), bd = ptx::sdesc_kmajor_sw128(b);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t off = (uint64_t)(((kk >> 2) * Tile<D>::kBoxBytes + (kk & 3) * 32) >> 4);
+        ptx::mma_ss(d, ad + off, bd + off, kIdesc, kk > 0 ? 1u : 0u);
+    }
+}
+
+// D(tmem) (+)= A B, A 128 x 128 in TMEM as its two halves stand (16-bit pairs, columns 0-31 and 64-95 from `a`), B a tile.
+template <int D, bool BF16>
+__device__ __forceinline__ void product_over_rows(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
+    constexpr uint32_t kIdesc = ptx::idesc_f16(kBlock, D, BF16, false, true);
+    const uint64_t bd = ptx::sdesc_mnmajor_sw128(b, Tile<D>::kBoxBytes);
+#pragma unroll
+    for (int kk = 0; kk < kBlock / 16; ++kk)
+        ptx::mma_ts(d, a + (uint32_t)((kk >> 2) * 64 + (kk & 3) * 8), bd + (uint64_t)((kk * 16 * 128) >> 4), kIdesc,
+                    (accumulate || kk > 0) ? 1u : 0u);
+}
+
+__device__ __forceinline__ void load64(uint32_t taddr, float* x) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(x);
+    ptx::tmem_ld32(taddr, r);
+    ptx::tmem_ld32(taddr + 32, r + 32);
+    ptx::tmem_ld_wait();
+    ptx::reg_fence32(r);
+    ptx::reg_fence32(r + 32);
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+    return BF16 ? ptx::pack_bf16x2(a, b) : ptx::pack_f16x2(a, b);
+}
+
+// A warp is through with something: one arrival for its 32 lanes.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(bar);
+}
+
+// The same after TMEM loads or stores, which the products issued next must find done.
+__device__ __forceinline__ void warp_arrive_tmem(uint32_t bar) {
+    ptx::tc_fence_before_sync();
+    warp_arrive(bar);
+}
+
+// N accumulated values of a row, times `factor`, to 16 bits in device memory.
+template <int N, bool BF16>
+__device__ __forceinline__ void store_row(uint32_t taddr, uint16_t* row, float factor, bool there, bool vec8, bool zero) {
+#pragma unroll
+    for (int c = 0; c < N / 32; ++c) {
+        uint32_t v[32], w[16];
+        if (!zero) {
+            ptx::tmem_ld32(taddr + 32 * c, v);
+            ptx::tmem_ld_wait();
+            ptx::reg_fence32(v);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            w[i] = zero ? 0u : pack<BF16>(__uint_as_float(v[2 * i]) * factor, __uint_as_float(v[2 * i + 1]) * factor);
+        if (there) {
+            if (vec8) {
+                ptx::st_global_v8(row + 32 * c, w);
+                ptx::st_global_v8(row + 32 * c + 16, w + 8);
+            } else {
+                uint4* dst = reinterpret_cast<uint4*>(row + 32 * c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ dK, dV
+//
+// TMEM: S^T and then P^T in columns 0-127, dP^T and then dS^T in 128-255, dV from
+// 256, dK behind it. A query block i of the walk takes, in the tensor cores' order,
+//   dV += P_i^T dO_i,  S_{i+1}^T = K Q_{i+1}^T,  dK += dS_i^T Q_i,  dP_{i+1}^T = V dO_{i+1}^T
+// so that the warps find P's work under the last two products of a block and dS's
+// under the first two. S^T of the next block overwrites P^T, whose product was
+// issued before it by the same thread: the tensor cores run one thread's products
+// in order. Rows are keys here, so that P^T and dS^T are operands as they stand.
+
+template <int D, bool ADDITIVE>
+struct KvCfg {
+    using T = Tile<D>;
+    // Q stays until the last product of its block, dO until the first.
+    static constexpr int kQ = D == 128 ? (ADDITIVE ? 2 : 3) : 5, kG = D == 128 ? 2 : 4;
+    static constexpr int kKOff = 0, kVOff = T::kBytes, kQOff = 2 * T::kBytes, kGOff = kQOff + kQ * T::kBytes;
+    static constexpr int kRowOff = kGOff + kG * T::kBytes;                  // [kQ] -lse, [kG] -delta, [kQ] 1 / sum
+    static constexpr int kDeltaOff = kRowOff + kQ * (int)kRowBytes;
+    static constexpr int kSumOff = kDeltaOff + kG * (int)kRowBytes;
+    static constexpr int kBarOff = kSumOff + (ADDITIVE ? kQ * (int)kRowBytes : 0);
+    static constexpr int bK = 0, bV = 1, bKVEmpty = 2, bS = 3, bP = 4, bDP = 5, bDS = 6, bAcc = 7, bAccEmpty = 8,
+                         bDrain = 9, bStall = 10, bQ = 11, bQEmpty = bQ + kQ, bG = bQEmpty + kQ, bGEmpty = bG + kG,
+                         kNumBars = bGEmpty + kG;
+    static constexpr int kTmemSlotOff = kBarOff + 8 * kNumBars;
+    static constexpr int kAbortOff = kTmemSlotOff + 4;
+    static constexpr int kSmemBytes = kAbortOff + 4;
+    static constexpr uint32_t cS = 0, cDP = 128, cDV = 256, cDK = 256 + D;
+    static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+struct KvTile {
+    int b, hk, k0;
+    int lo, per_head;       // first query block that sees a key of the tile, and how many do
+    int n;                  // blocks of the walk: those of every head
+};
+
+// Tiles of a K/V head follow each other, so that its queries come from L2; with
+// a causal mask the first keys, which most queries see, come first.
+__device__ __forceinline__ KvTile kv_tile(int t, const BwdParams& p) {
+    KvTile w;
+    const int bh = t / p.n_kb;
+    w.k0 = (t - bh * p.n_kb) * kBlock;
+    w.b = bh / p.Hkv;
+    w.hk = bh - w.b * p.Hkv;
+    int lo = 0, hi = p.Sq;                                     // queries
+    if (p.causal) lo = max(0, w.k0 - p.off);
+    if (p.window && w.k0 >= p.sinks) hi = (int)min((long long)p.Sq, (long long)w.k0 + kBlock - 1 - p.off + p.window);
+    w.lo = lo / kBlock;
+    w.per_head = hi > lo ? (hi + kBlock - 1) / kBlock - w.lo : 0;
+    w.n = w.per_head * p.group;
+    return w;
+}
+
+template <int D, bool BF16, bool ADDITIVE>
+__global__ void __launch_bounds__(kThreads, 1)
+    bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG, const BwdParams p) {
+    using C = KvCfg<D, ADDITIVE>;
+    using T = Tile<D>;
+    extern __shared__ __align__(1024) uint8_t smem_ptr[];
+    const uint32_t smem = ptx::smem_addr(smem_ptr);
+    if (smem & 1023u) {                               // swizzled tiles: the linker aligns the array, never seen otherwise
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem_ptr + C::kAbortOff);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_ptr + C::kTmemSlotOff);
+    auto bar = [&](int i) { return smem + C::kBarOff + 8u * (uint32_t)i; };
+
+    if (warp == kLoadWarp && lane == 0) {
+        for (int i = 0; i < C::kNumBars; ++i) {
+            uint32_t count = 1;
+            if (i == C::bP || i == C::bDS || i == C::bAccEmpty) count = 8;
+            // a block's tile is free once its last product has run and the eight warps have its statistics
+            if ((i >= C::bQEmpty && i < C::bQEmpty + C::kQ) || (i >= C::bGEmpty && i < C::bGEmpty + C::kG)) count = 9;
+            ptx::mbar_init(bar(i), count);
+        }
+        *abort_flag = 0u;
+        ptx::fence_barrier_init();
+        ptx::fence_proxy_async_shared();
+        ptx::prefetch_tensormap(&tmQ);
+        ptx::prefetch_tensormap(&tmK);
+        ptx::prefetch_tensormap(&tmV);
+        ptx::prefetch_tensormap(&tmG);
+    }
+    if (warp == kIssueWarp) {
+        ptx::tmem_alloc(ptx::smem_addr(tmem_slot), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const SyncCtx sc{abort_flag, p.status, p.timeout_ns};
+
+    if (warp == kLoadWarp) {
+        // ------------------------------------------------------------ loads
+        uint32_t tiles = 0, fills = 0;                         // tiles with work, blocks
+        bool alive = true;
+        for (int t = blockIdx.x; t < p.n_tiles && alive; t += gridDim.x) {
+            const KvTile w = kv_tile(t, p);
+            if (w.n == 0) continue;
+            if (tiles > 0 && !warp_wait(bar(C::bKVEmpty), (tiles - 1) & 1u, sc)) break;
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(bar(C::bK), T::kBytes);
+                load_tile<D>(smem + C::kKOff, &tmK, bar(C::bK), w.hk, w.k0, w.b);
+                ptx::mbar_arrive_expect_tx(bar(C::bV), T::kBytes);
+                load_tile<D>(smem + C::kVOff, &tmV, bar(C::bV), w.hk, w.k0, w.b);
+            }
+            ++tiles;
+            int h = w.hk * p.group, i = w.lo;
+            for (int it = 0; it < w.n; ++it, ++fills) {
+                const uint32_t qs = fills % C::kQ, gs = fills % C::kG;
+                const size_t row = ((size_t)w.b * p.Hq + h) * p.Sp + (size_t)i * kBlock;
+                if (fills >= (uint32_t)C::kQ && !warp_wait(bar(C::bQEmpty + qs), (fills / C::kQ - 1) & 1u, sc)) {
+                    alive = false;
+                    break;
+                }
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(bar(C::bQ + qs), T::kBytes + kRowBytes * (ADDITIVE ? 2 : 1));
+                    load_tile<D>(smem + C::kQOff + qs * T::kBytes, &tmQ, bar(C::bQ + qs), h, i * kBlock, w.b);
+                    ptx::bulk_load(smem + C::kRowOff + qs * kRowBytes, p.neg_lse + row, kRowBytes, bar(C::bQ + qs));
+                    if (ADDITIVE)
+                        ptx::bulk_load(smem + C::kSumOff + qs * kRowBytes, p.inv_sum + row, kRowBytes, bar(C::bQ + qs));
+                }
+                if (fills >= (uint32_t)C::kG && !warp_wait(bar(C::bGEmpty + gs), (fills / C::kG - 1) & 1u, sc)) {
+                    // (the Q tile of this block is in flight: it counts for the shutdown)
+                    if (lane == 0) drain_phase(bar(C::bQ + qs), (fills / C::kQ) & 1u, sc);
+                    alive = false;
+                    break;
+                }
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(bar(C::bG + gs), T::kBytes + kRowBytes);
+                    load_tile<D>(smem + C::kGOff + gs * T::kBytes, &tmG, bar(C::bG + gs), h, i * kBlock, w.b);
+                    ptx::bulk_load(smem + C::kDeltaOff + gs * kRowBytes, p.neg_delta + row, kRowBytes, bar(C::bG + gs));
+                }
+                if (++i == w.lo + w.per_head) {
+                    i = w.lo;
+                    ++h;
+                }
+            }
+        }
+        // Shut down: every copy has landed.
+        if (tiles > 0) {
+            drain_phase(bar(C::bK), (tiles - 1) & 1u, sc);
+            drain_phase(bar(C::bV), (tiles - 1) & 1u, sc);
+        }
+        for (uint32_t s = 0; s < (uint32_t)C::kQ; ++s)
+            if (fills > s) drain_phase(bar(C::bQ + s), ((fills - 1 - s) / C::kQ) & 1u, sc);
+        for (uint32_t s = 0; s < (uint32_t)C::kG; ++s)
+            if (fills > s) drain_phase(bar(C::bG + s), ((fills - 1 - s) / C::kG) & 1u, sc);
+    } else if (warp == kIssueWarp) {
+        // --------------------------------------------------------- products
+        if (lane == 0) {
+            uint32_t tiles = 0, use = 0;
+            bool alive = true, issued = false;
+            if (p.stall) alive = wait_phase(bar(C::bStall), 0, sc);          // nothing ever arrives
+            for (int t = blockIdx.x; t < p.n_tiles && alive; t += gridDim.x) {
+                const KvTile w = kv_tile(t, p);
+                if (w.n == 0) continue;
+                auto issue_s = [&](uint32_t u) -> bool {
+                    const uint32_t s = u % C::kQ;
+                    if (!wait_phase(bar(C::bQ + s), (u / C::kQ) & 1u, sc)) return false;
+                    ptx::tc_fence_after_sync();
+                    product_over_d<D, BF16>(tmem + C::cS, smem + C::kKOff, smem + C::kQOff + s * T::kBytes);
+                    ptx::tc_commit(bar(C::bS));
+                    return issued = true;
+                };
+                auto issue_dp = [&](uint32_t u) -> bool {
+                    const uint32_t s = u % C::kG;
+                    if (!wait_phase(bar(C::bG + s), (u / C::kG) & 1u, sc)) return false;
+                    ptx::tc_fence_after_sync();
+                    product_over_d<D, BF16>(tmem + C::cDP, smem + C::kVOff, smem + C::kGOff + s * T::kBytes);
+                    ptx::tc_commit(bar(C::bDP));
+                    return true;
+                };
+                alive = wait_phase(bar(C::bK), tiles & 1u, sc) && issue_s(use) && wait_phase(bar(C::bV), tiles & 1u, sc) &&
+                        issue_dp(use);
+                if (alive && w.n == 1) ptx::tc_commit(bar(C::bKVEmpty));
+                for (int it = 0; it < w.n && alive; ++it, ++use) {
+                    const bool more = it + 1 < w.n;
+                    const uint32_t qs = use % C::kQ, gs = use % C::kG;
+                    alive = wait_phase(bar(C::bP), use & 1u, sc);
+                    // the warps have the last tile's dK and dV
+                    if (alive && it == 0 && tiles > 0) alive = wait_phase(bar(C::bAccEmpty), (tiles - 1) & 1u, sc);
+                    if (!alive) break;
+                    ptx::tc_fence_after_sync();
+                    product_over_rows<D, BF16>(tmem + C::cDV, tmem + C::cS, smem + C::kGOff + gs * T::kBytes, it > 0);
+                    ptx::tc_commit(bar(C::bGEmpty + gs));
+                    if (more && !(alive = issue_s(use + 1))) break;
+                    if (!(alive = wait_phase(bar(C::bDS), use & 1u, sc))) break;
+                    ptx::tc_fence_after_sync();
+                    product_over_rows<D, BF16>(tmem + C::cDK, tmem + C::cDP, smem + C::kQOff + qs * T::kBytes, it > 0);
+                    ptx::tc_commit(bar(C::bQEmpty + qs));
+                    if (more) {
+                        if (!(alive = issue_dp(use + 1))) break;
+                        if (it + 2 == w.n) ptx::tc_commit(bar(C::bKVEmpty));
+                    }
+                }
+                if (!alive) break;
+                ptx::tc_commit(bar(C::bAcc));
+                ++tiles;
+            }
+            if (issued) {                                     // TMEM is freed after every product has run
+                ptx::tc_commit(bar(C::bDrain));
+                drain_phase(bar(C::bDrain), 0, sc);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        // ------------------------------------------------------- P^T and dS^T
+        const int wg = warp >> 2, r = (warp & 3) * 32 + lane;     // key of the tile; columns 64 wg ..
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_base + C::cS + 64 * wg, tDP = tmem + lane_base + C::cDP + 64 * wg;
+        const float sl = p.scale_log2;
+        uint32_t tiles = 0, use = 0;
+        bool alive = true;
+        for (int t = blockIdx.x; t < p.n_tiles && alive; t += gridDim.x) {
+            const KvTile w = kv_tile(t, p);
+            const int key = w.k0 + r;
+            // queries [see, end) see this key
+            const int see = p.causal ? key - p.off : 0;
+            const int end = p.window && key >= p.sinks
+                                ? (int)min((long long)INT_MAX, (long long)key - p.off + p.window) : INT_MAX;
+            // blocks that begin at or after all_see and end at or before all_end hide nothing
+            const int all_see = p.causal ? w.k0 + kBlock - 1 - p.off : 0;
+            const int all_end = p.window && w.k0 + kBlock > p.sinks
+                                    ? (int)min((long long)INT_MAX, (long long)max(w.k0, p.sinks) - p.off + p.window) : INT_MAX;
+            int i = w.lo;
+            for (int it = 0; it < w.n; ++it, ++use) {
+                const int m0 = i * kBlock + 64 * wg;              // this warp's first query
+                const uint32_t qs = use % C::kQ, gs = use % C::kG;
+                float x[64];
+                if (ADDITIVE) {
+                    // a warp's lanes are neighbouring keys: each load is one line of the mask
+                    const float* at = p.mask + ((size_t)w.b * p.Sq + m0) * p.Sk + key;
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) x[c] = (key < p.Sk && m0 + c < p.Sq) ? __ldg(at + (size_t)c * p.Sk) : 0.f;
+                }
+                alive = warp_wait(bar(C::bQ + qs), (use / C::kQ) & 1u, sc) && warp_wait(bar(C::bS), use & 1u, sc);
+                if (!alive) break;
+                ptx::tc_fence_after_sync();
+                const float4* nl = reinterpret_cast<const float4*>(smem_ptr + C::kRowOff + qs * kRowBytes) + 16 * wg;
+                if (ADDITIVE) {
+                    const float4* is = reinterpret_cast<const float4*>(smem_ptr + C::kSumOff + qs * kRowBytes) + 16 * wg;
+#pragma unroll
+                    for (int c = 0; c < 64; c += 32) {
+                        uint32_t s[32];
+                        ptx::tmem_ld32(tS + c, s);
+                        ptx::tmem_ld_wait();
+                        ptx::reg_fence32(s);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 n = nl[(c + e) / 4], u = is[(c + e) / 4];
+                            const float nn[4] = {n.x, n.y, n.z, n.w}, uu[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                            for (int d = 0; d < 4; ++d) {
+                                float y = fmaf(x[c + e + d], kLog2E, __uint_as_float(s[e + d]) * sl);
+                                if (m0 + c + e + d < see) y = -INFINITY;
+                                x[c + e + d] = ptx::ex2(y + nn[d]) * uu[d];
+                            }
+                        }
+                    }
+                } else {
+                    load64(tS, x);
+#pragma unroll
+                    for (int c = 0; c < 64; c += 4) {
+                        const float4 n = nl[c / 4];
+                        ptx::fma2(x[c], x[c + 1], x[c], x[c + 1], sl, sl, n.x, n.y);
+                        ptx::fma2(x[c + 2], x[c + 3], x[c + 2], x[c + 3], sl, sl, n.z, n.w);
+                    }
+                    const int base = i * kBlock;
+                    if (base < all_see || base > all_end - kBlock) {
+                        const int c0 = see - m0, c1 = end - m0;
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            if (c < c0 || c >= c1) x[c] = -INFINITY;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) x[c] = ptx::ex2(x[c]);
+                }
+                {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) pk[c] = pack<BF16>(x[2 * c], x[2 * c + 1]);
+                    ptx::tmem_st32(tS, pk);
+                    ptx::tmem_st_wait();
+                }
+                warp_arrive_tmem(bar(C::bP));
+                if (lane == 0) ptx::mbar_arrive(bar(C::bQEmpty + qs));
+                // ---- dS = P (dP - delta)
+                alive = warp_wait(bar(C::bG + gs), (use / C::kG) & 1u, sc) && warp_wait(bar(C::bDP), use & 1u, sc);
+                if (!alive) break;
+                ptx::tc_fence_after_sync();
+                const float4* nd = reinterpret_cast<const float4*>(smem_ptr + C::kDeltaOff + gs * kRowBytes) + 16 * wg;
+                {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int c = 0; c < 64; c += 32) {
+                        uint32_t d[32];
+                        ptx::tmem_ld32(tDP + c, d);
+                        ptx::tmem_ld_wait();
+                        ptx::reg_fence32(d);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 n = nd[(c + e) / 4];
+                            float a0, a1, a2, a3;
+                            ptx::add2(a0, a1, __uint_as_float(d[e]), __uint_as_float(d[e + 1]), n.x, n.y);
+                            ptx::add2(a2, a3, __uint_as_float(d[e + 2]), __uint_as_float(d[e + 3]), n.z, n.w);
+                            ptx::mul2(a0, a1, a0, a1, x[c + e], x[c + e + 1]);
+                            ptx::mul2(a2, a3, a2, a3, x[c + e + 2], x[c + e + 3]);
+                            pk[(c + e) / 2] = pack<BF16>(a0, a1);
+                            pk[(c + e) / 2 + 1] = pack<BF16>(a2, a3);
+                        }
+                    }
+                    ptx::tmem_st32(tDP, pk);
+                    ptx::tmem_st_wait();
+                }
+                warp_arrive_tmem(bar(C::bDS));
+                if (lane == 0) ptx::mbar_arrive(bar(C::bGEmpty + gs));
+                if (++i == w.lo + w.per_head) i = w.lo;
+            }
+            if (!alive) break;
+            // ---- warps 0-3 write dV, warps 4-7 dK
+            if (w.n > 0 && !(alive = warp_wait(bar(C::bAcc), tiles & 1u, sc))) break;
+            ptx::tc_fence_after_sync();
+            uint16_t* row = static_cast<uint16_t*>(wg ? p.dk : p.dv) +
+                            ((long long)w.b * p.Sk + key) * (wg ? p.dk_stride : p.dv_stride) + w.hk * D;
+            store_row<D, BF16>(tmem + lane_base + (wg ? C::cDK : C::cDV), row, wg ? p.scale : 1.f, key < p.Sk, p.vec8,
+                               w.n == 0);
+            if (w.n > 0) {
+                warp_arrive_tmem(bar(C::bAccEmpty));
+                ++tiles;
+            }
+        }
+    }
+
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kIssueWarp) {
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------- dQ
+//
+// TMEM: dQ from column 0, S of even blocks of the walk and then their dS in
+// 128-255, of odd blocks in 256-383, dP in 384-511. A key block j takes, in the
+// tensor cores' order,
+//   dP_{j+1} = dO V_{j+1}^T,  dQ += dS_j K_j,  S_{j+2} = Q K_{j+2}^T
+// the first as soon as the warps hold dP_j in registers. With an additive mask
+// the keys are walked twice: first for the rows' maximum and sum, since a mask of
+// large values leaves lse without the logits' bits; both go to the other kernel.
+
+template <int D>
+struct QCfg {
+    using T = Tile<D>;
+    static constexpr int kK = D == 128 ? 3 : 5, kV = D == 128 ? 2 : 4;
+    static constexpr int kQOff = 0, kGOff = T::kBytes, kKOff = 2 * T::kBytes, kVOff = kKOff + kK * T::kBytes;
+    static constexpr int kBarOff = kVOff + kV * T::kBytes;
+    static constexpr int bQ = 0, bQEmpty = 1, bS = 2, bDP = 4, bDPFree = 5, bDS = 6, bAcc = 8, bAccEmpty = 9, bDrain = 10,
+                         bStall = 11, bHalf = 12, bWhole = 13, bK = 14, bKEmpty = bK + kK, bV = bKEmpty + kK, bVEmpty = bV + kV,
+                         kNumBars = bVEmpty + kV;
+    static constexpr int kTmemSlotOff = kBarOff + 8 * kNumBars;
+    static constexpr int kAbortOff = kTmemSlotOff + 4;
+    static constexpr int kStatOff = (kAbortOff + 4 + 15) / 16 * 16;      // additive mask: [128] {maximum, sum} of a half
+    static constexpr int kSmemBytes = kStatOff + 128 * 8;
+    static constexpr uint32_t cDQ = 0, cS = 128, cDP = 384;
+    static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+struct QTile {
+    int b, h, hk, m0;
+    int first, gap;         // key blocks of the walk: 0 .. first - 1 (sinks), then on from first + gap
+    int n;
+    __device__ __forceinline__ int block(int j) const { return j < first ? j : j + gap; }
+};
+
+// Tiles of a head follow each other; with a causal mask the last queries, which see most keys, come first.
+__device__ __forceinline__ QTile q_tile(int t, const BwdParams& p) {
+    QTile w;
+    const int bh = t / p.n_qb, m = t - bh * p.n_qb;
+    w.m0 = (p.causal ? p.n_qb - 1 - m : m) * kBlock;
+    w.b = bh / p.Hq;
+    w.h = bh - w.b * p.Hq;
+    w.hk = w.h / p.group;
+    int hi = p.Sk;
+    if (p.causal) hi = min(p.Sk, max(0, min(w.m0 + kBlock, p.Sq) + p.off));
+    w.n = (hi + kBlock - 1) / kBlock;
+    w.first = w.gap = 0;
+    if (p.window) {
+        const int low = max(0, w.m0 + p.off - p.window + 1) / kBlock, sinks = (min(p.sinks, hi) + kBlock - 1) / kBlock;
+        if (low > sinks && low <= w.n) {
+            w.first = sinks;
+            w.gap = low - sinks;
+            w.n -= w.gap;
+        }
+    }
+    return w;
+}
+
+template <int D, bool BF16, bool ADDITIVE>
+__global__ void __launch_bounds__(kThreads, 1)
+    bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG, const BwdParams p) {
+    using C = QCfg<D>;
+    using T = Tile<D>;
+    extern __shared__ __align__(1024) uint8_t smem_ptr[];
+    const uint32_t smem = ptx::smem_addr(smem_ptr);
+    if (smem & 1023u) {                               // swizzled tiles: the linker aligns the array, never seen otherwise
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem_ptr + C::kAbortOff);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_ptr + C::kTmemSlotOff);
+    auto bar = [&](int i) { return smem + C::kBarOff + 8u * (uint32_t)i; };
+
+    if (warp == kLoadWarp && lane == 0) {
+        for (int i = 0; i < C::kNumBars; ++i) {
+            uint32_t count = 1;
+            if (i == C::bDPFree || i == C::bDS || i == C::bDS + 1 || i == C::bAccEmpty) count = 8;
+            if (i == C::bHalf || i == C::bWhole) count = 4;
+            ptx::mbar_init(bar(i), count);
+        }
+        *abort_flag = 0u;
+        ptx::fence_barrier_init();
+        ptx::fence_proxy_async_shared();
+        ptx::prefetch_tensormap(&tmQ);
+        ptx::prefetch_tensormap(&tmK);
+        ptx::prefetch_tensormap(&tmV);
+        ptx::prefetch_tensormap(&tmG);
+    }
+    if (warp == kIssueWarp) {
+        ptx::tmem_alloc(ptx::smem_addr(tmem_slot), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    ptx::tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const SyncCtx sc{abort_flag, p.status, p.timeout_ns};
+
+    if (warp == kLoadWarp) {
+        // ------------------------------------------------------------ loads
+        uint32_t tiles = 0, kf = 0, vf = 0;
+        bool alive = true;
+        for (int t = blockIdx.x; t < p.n_tiles && alive; t += gridDim.x) {
+            const QTile w = q_tile(t, p);
+            if (w.n == 0) continue;
+            if (tiles > 0 && !warp_wait(bar(C::bQEmpty), (tiles - 1) & 1u, sc)) break;
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(bar(C::bQ), 2 * T::kBytes);
+                load_tile<D>(smem + C::kQOff, &tmQ, bar(C::bQ), w.h, w.m0, w.b);
+                load_tile<D>(smem + C::kGOff, &tmG, bar(C::bQ), w.h, w.m0, w.b);
+            }
+            ++tiles;
+            auto load_k = [&](int j) -> bool {
+                const uint32_t s = kf % C::kK;
+                if (kf >= (uint32_t)C::kK && !warp_wait(bar(C::bKEmpty + s), (kf / C::kK - 1) & 1u, sc)) return false;
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(bar(C::bK + s), T::kBytes);
+                    load_tile<D>(smem + C::kKOff + s * T::kBytes, &tmK, bar(C::bK + s), w.hk, w.block(j) * kBlock, w.b);
+                }
+                ++kf;
+                return true;
+            };
+            auto load_v = [&](int j) -> bool {
+                const uint32_t s = vf % C::kV;
+                if (vf >= (uint32_t)C::kV && !warp_wait(bar(C::bVEmpty + s), (vf / C::kV - 1) & 1u, sc)) return false;
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(bar(C::bV + s), T::kBytes);
+                    load_tile<D>(smem + C::kVOff + s * T::kBytes, &tmV, bar(C::bV + s), w.hk, w.block(j) * kBlock, w.b);
+                }
+                ++vf;
+                return true;
+            };
+            if (ADDITIVE)
+                for (int j = 0; j < w.n && alive; ++j) alive = load_k(j);
+            // in the order in which the products take them: K_0, V_0, K_1, V_1, ...
+            for (int j = 0; j < w.n && alive; ++j) alive = load_k(j) && load_v(j);
+        }
+        if (tiles > 0) drain_phase(bar(C::bQ), (tiles - 1) & 1u, sc);
+        for (uint32_t s = 0; s < (uint32_t)C::kK; ++s)
+            if (kf > s) drain_phase(bar(C::bK + s), ((kf - 1 - s) / C::kK) & 1u, sc);
+        for (uint32_t s = 0; s < (uint32_t)C::kV; ++s)
+            if (vf > s) drain_phase(bar(C::bV + s), ((vf - 1 - s) / C::kV) & 1u, sc);
+    } else if (warp == kIssueWarp) {
+        // --------------------------------------------------------- products
+        if (lane == 0) {
+            // su: S tiles issued, and K tiles whose first use that was; ds: dS (or freed S) tiles taken; dp: dP tiles issued
+            uint32_t tiles = 0, su = 0, ds = 0, dp = 0;
+            bool alive = true, issued = false;
+            if (p.stall) alive = wait_phase(bar(C::bStall), 0, sc);          // nothing ever arrives
+            auto issue_s = [&]() -> bool {
+                const uint32_t s = su % C::kK;
+                if (!wait_phase(bar(C::bK + s), (su / C::kK) & 1u, sc)) return false;
+                ptx::tc_fence_after_sync();
+                product_over_d<D, BF16>(tmem + C::cS + 128 * (su & 1u), smem + C::kQOff, smem + C::kKOff + s * T::kBytes);
+                ptx::tc_commit(bar(C::bS + (su & 1u)));
+                ++su;
+                return issued = true;
+            };
+            auto issue_dp = [&]() -> bool {
+                const uint32_t s = dp % C::kV;
+                if (!wait_phase(bar(C::bV + s), (dp / C::kV) & 1u, sc)) return false;
+                if (dp > 0 && !wait_phase(bar(C::bDPFree), (dp - 1) & 1u, sc)) return false;
+                ptx::tc_fence_after_sync();
+                product_over_d<D, BF16>(tmem + C::cDP, smem + C::kGOff, smem + C::kVOff + s * T::kBytes);
+                ptx::tc_commit(bar(C::bDP));
+                ptx::tc_commit(bar(C::bVEmpty + s));
+                ++dp;
+                return true;
+            };
+            auto wait_ds = [&]() -> bool {
+                const bool ok = wait_phase(bar(C::bDS + (ds & 1u)), (ds >> 1) & 1u, sc);
+                if (ok) ptx::tc_fence_after_sync();
+                return ok;
+            };
+            for (int t = blockIdx.x; t < p.n_tiles && alive; t += gridDim.x) {
+                const QTile w = q_tile(t, p);
+                if (w.n == 0) continue;
+                if (!(alive = wait_phase(bar(C::bQ), tiles & 1u, sc))) break;
+                if (ADDITIVE) {
+                    // S alone: a buffer is used again once the warps have read it
+                    alive = issue_s() && (w.n == 1 || issue_s());
+                    for (int j = 0; j < w.n && alive; ++j, ++ds) {
+                        if (!(alive = wait_ds())) break;
+                        ptx::tc_commit(bar(C::bKEmpty + ds % C::kK));
+                        if (j + 2 < w.n) alive = issue_s();
+                    }
+                }
+                // (Q and dO are free after S and dP of the last block)
+                alive = alive && issue_s() && issue_dp() && (w.n == 1 || issue_s());
+                if (alive && w.n == 1) ptx::tc_commit(bar(C::bQEmpty));
+                for (int j = 0; j < w.n && alive; ++j, ++ds) {
+                    if (j + 1 < w.n && !(alive = issue_dp())) break;
+                    if (j + 2 == w.n) ptx::tc_commit(bar(C::bQEmpty));
+                    if (!(alive = wait_ds())) break;
+                    if (j == 0 && tiles > 0 && !(alive = wait_phase(bar(C::bAccEmpty), (tiles - 1) & 1u, sc))) break;
+                    ptx::tc_fence_after_sync();
+                    const uint32_t s = ds % C::kK;
+                    product_over_rows<D, BF16>(tmem + C::cDQ, tmem + C::cS + 128 * (ds & 1u), smem + C::kKOff + s * T::kBytes,
+                                               j > 0);
+                    ptx::tc_commit(bar(C::bKEmpty + s));
+                    if (j + 2 < w.n) alive = issue_s();
+                }
+                if (!alive) break;
+                ptx::tc_commit(bar(C::bAcc));
+                ++tiles;
+            }
+            if (issued) {
+                ptx::tc_commit(bar(C::bDrain));
+                drain_phase(bar(C::bDrain), 0, sc);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        // ---------------------------------------------------------------- dS
+        const int wg = warp >> 2, r = (warp & 3) * 32 + lane;     // query of the tile; columns 64 wg ..
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_base + C::cS + 64 * wg, tDP = tmem + lane_base + C::cDP + 64 * wg;
+        const float sl = p.scale_log2;
+        float2* stat = reinterpret_cast<float2*>(smem_ptr + C::kStatOff);
+        uint32_t tiles = 0, su = 0, dp = 0, seen = 0;
+        bool alive = true;
+        for (int t = blockIdx.x; t < p.n_tiles && alive; t += gridDim.x) {
+            const QTile w = q_tile(t, p);
+            const int row = w.m0 + r;
+            const bool there = row < p.Sq;
+            const size_t at = ((size_t)w.b * p.Hq + w.h) * p.Sp + row;
+            // keys [low, lim) are visible, and those before sinks
+            const int lim = p.causal ? min(p.Sk, max(0, row + p.off + 1)) : p.Sk;
+            const int low = p.window ? row + p.off - p.window + 1 : 0;
+            const float* mrow = ADDITIVE && there ? p.mask + ((size_t)w.b * p.Sq + row) * p.Sk : nullptr;
+            float nl = 0.f, is = 0.f;
+            const float nd = p.neg_delta[at];
+            if (!ADDITIVE) nl = p.neg_lse[at];
+
+            // logits in log2 units of block j: S in the buffer of `su`, scaled, masked, hidden keys at -inf
+            auto logits = [&](int j, float* x) -> bool {
+                const int key0 = w.block(j) * kBlock + 64 * wg;
+                if (ADDITIVE) {
+                    const bool vec = mrow != nullptr && key0 + 64 <= p.Sk && p.Sk % 4 == 0 &&
+                                     (reinterpret_cast<uintptr_t>(p.mask) & 15) == 0;
+                    if (vec) {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 4) {
+                            const float4 m = ptx::ld_global_nc_v4(mrow + key0 + c);
+                            x[c] = m.x, x[c + 1] = m.y, x[c + 2] = m.z, x[c + 3] = m.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) x[c] = mrow != nullptr && key0 + c < p.Sk ? __ldg(mrow + key0 + c) : 0.f;
+                    }
+                }
+                if (!warp_wait(bar(C::bS + (su & 1u)), (su >> 1) & 1u, sc)) return false;
+                ptx::tc_fence_after_sync();
+                if (ADDITIVE) {
+#pragma unroll
+                    for (int c = 0; c < 64; c += 32) {
+                        uint32_t s[32];
+                        ptx::tmem_ld32(tS + 128 * (su & 1u) + c, s);
+                        ptx::tmem_ld_wait();
+                        ptx::reg_fence32(s);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[c + e] = fmaf(x[c + e], kLog2E, __uint_as_float(s[e]) * sl);
+                    }
+                } else {
+                    load64(tS + 128 * (su & 1u), x);
+#pragma unroll
+                    for (int c = 0; c < 64; c += 2) ptx::fma2(x[c], x[c + 1], x[c], x[c + 1], sl, sl, nl, nl);
+                }
+                const int c1 = lim - key0, c0 = low - key0, cs = p.sinks - key0;
+                if (c1 < 64 || (p.window && c0 > 0 && cs < 64)) {
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        if (c >= c1 || (p.window && c < c0 && c >= cs)) x[c] = -INFINITY;
+                }
+                return true;
+            };
+
+            if (ADDITIVE) {
+                float m = -INFINITY, l = 0.f;
+                for (int j = 0; j < w.n; ++j, ++su) {
+                    float x[64];
+                    if (!(alive = logits(j, x))) break;
+                    warp_arrive_tmem(bar(C::bDS + (su & 1u)));
+                    float top = m;
+#pragma unroll
+                    for (int c = 0; c < 64; c += 2) top = ptx::max3(top, x[c], x[c + 1]);
+                    if (top != -INFINITY) {
+                        l *= ptx::ex2(m - top);
+                        m = top;
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) l += ptx::ex2(x[c] - top);
+                    }
+                }
+                if (!alive) break;
+                // join the two halves of the row
+                if (wg) {
+                    stat[r] = make_float2(m, l);
+                    warp_arrive(bar(C::bHalf));
+                    if (!(alive = warp_wait(bar(C::bWhole), seen & 1u, sc))) break;
+                } else {
+                    if (!(alive = warp_wait(bar(C::bHalf), seen & 1u, sc))) break;
+                    const float2 o = stat[r];
+                    const float top = fmaxf(m, o.x);
+                    if (top != -INFINITY) l = l * ptx::ex2(m - top) + o.y * ptx::ex2(o.x - top);
+                    const bool any = there && l > 0.f;
+                    stat[r] = make_float2(any ? -top : 0.f, any ? 1.f / l : 0.f);
+                    p.neg_lse[at] = stat[r].x;
+                    p.inv_sum[at] = stat[r].y;
+                    warp_arrive(bar(C::bWhole));
+                }
+                ++seen;
+                nl = stat[r].x;
+                is = stat[r].y;
+            }
+            for (int j = 0; j < w.n; ++j, ++su, ++dp) {
+                float x[64];
+                if (!(alive = logits(j, x))) break;
+#pragma unroll
+                for (int c = 0; c < 64; ++c) x[c] = ptx::ex2(ADDITIVE ? x[c] + nl : x[c]);
+                if (!(alive = warp_wait(bar(C::bDP), dp & 1u, sc))) break;
+                ptx::tc_fence_after_sync();
+                uint32_t pk[32];
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                    uint32_t d[32];
+                    ptx::tmem_ld32(tDP + c, d);
+                    ptx::tmem_ld_wait();
+                    ptx::reg_fence32(d);
+                    if (c == 32) warp_arrive_tmem(bar(C::bDPFree));
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float a0, a1;
+                        ptx::add2(a0, a1, __uint_as_float(d[e]), __uint_as_float(d[e + 1]), nd, nd);
+                        if (ADDITIVE) ptx::mul2(a0, a1, a0, a1, is, is);
+                        ptx::mul2(a0, a1, a0, a1, x[c + e], x[c + e + 1]);
+                        pk[(c + e) / 2] = pack<BF16>(a0, a1);
+                    }
+                }
+                ptx::tmem_st32(tS + 128 * (su & 1u), pk);
+                ptx::tmem_st_wait();
+                warp_arrive_tmem(bar(C::bDS + (su & 1u)));
+            }
+            if (!alive) break;
+            // ---- each half of the warps writes half of the row
+            if (w.n > 0 && !(alive = warp_wait(bar(C::bAcc), tiles & 1u, sc))) break;
+            ptx::tc_fence_after_sync();
+            uint16_t* out = static_cast<uint16_t*>(p.dq) + ((long long)w.b * p.Sq + row) * p.dq_stride + w.h * D + wg * (D / 2);
+            store_row<D / 2, BF16>(tmem + lane_base + C::cDQ + wg * (D / 2), out, p.scale, there, p.vec8, w.n == 0);
+            if (w.n > 0) {
+                warp_arrive_tmem(bar(C::bAccEmpty));
+                ++tiles;
+            }
+        }
+    }
+
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    if (warp == kIssueWarp) {
+        ptx::tc_fence_after_sync();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace bwd
+}  // namespace attn

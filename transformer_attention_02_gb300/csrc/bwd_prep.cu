@@ -1,0 +1,114 @@
+// Row statistics of the attention's backward pass: for every query row
+//   delta = sum_d dO[d] O[d]      (= sum_j P_j dP_j, since O = P V),
+// and the row's log-sum-exp in log2 units, both negated, as (B, Hq, Sp) with
+// the rows of a head next to each other and padded to whole blocks, so that the
+// products' kernels fetch 128 of them with one bulk copy. Rows that are none,
+// and rows without a visible key (lse = -inf), get -inf: their probabilities
+// become 2^-inf = 0.
+// Bound by memory: O and dO are read once. Eight 16-byte pieces of a row a lane
+// group, rows in the order in which they lie in memory.
+#include <algorithm>
+
+#include "../../include/attn.h"
+#include "attn_kernel.cuh"
+#include "bwd_params.h"
+
+namespace attn {
+namespace bwd {
+namespace {
+
+template <bool BF16>
+__device__ __forceinline__ float2 widen(uint32_t w) {
+    float2 f;
+    if (BF16) {
+        f.x = __uint_as_float(w << 16);
+        f.y = __uint_as_float(w & 0xffff0000u);
+    } else {
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+            : "=f"(f.x), "=f"(f.y)
+            : "r"(w));
+    }
+    return f;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 u = widen<BF16>(x[i]), v = widen<BF16>(y[i]);
+        s0 = fmaf(u.x, v.x, s0);
+        s1 = fmaf(u.y, v.y, s1);
+    }
+    return s0 + s1;
+}
+
+constexpr int kRows = 4;            // rows of a lane group in flight
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) bwd_prep_kernel(const PrepParams p) {
+    constexpr int kLanes = D / 8;                        // lanes of a row
+    const long long rows = (long long)p.B * p.Sq * p.Hq;
+    const int lane = threadIdx.x % kLanes;
+    const long long groups = (long long)gridDim.x * (256 / kLanes);
+    const long long g0 = (long long)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
+    const uint4* o = reinterpret_cast<const uint4*>(p.o) + lane;
+    const uint4* g = reinterpret_cast<const uint4*>(p.d_o) + lane;
+    // (whole warps stay in the loop: its bound is a warp's first group)
+    for (long long r0 = g0; r0 - threadIdx.x % 32 / kLanes < rows; r0 += groups * kRows) {
+        uint4 a[kRows], b[kRows];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const long long r = r0 + u * groups;
+            a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows) {
+                a[u] = __ldcg(o + r * kLanes);
+                b[u] = __ldcg(g + r * kLanes);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const long long r = r0 + u * groups;
+            float s = dot8<BF16>(a[u], b[u]);
+#pragma unroll
+            for (int m = kLanes / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+            if (lane == 0 && r < rows) {
+                const int h = (int)(r % p.Hq);
+                const long long t = r / p.Hq;
+                const int i = (int)(t % p.Sq);
+                const long long bh = t / p.Sq * p.Hq + h;
+                p.neg_delta[bh * p.Sp + i] = -s;
+                if (p.lse) {
+                    const float l = p.lse[bh * p.Sq + i];
+                    p.neg_lse[bh * p.Sp + i] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
+                }
+            }
+        }
+    }
+    // rows that are none
+    const int pad = p.Sp - p.Sq;
+    const long long n = (long long)p.B * p.Hq * pad;
+    for (long long e = (long long)blockIdx.x * 256 + threadIdx.x; e < n; e += (long long)gridDim.x * 256) {
+        const long long at = e / pad * p.Sp + p.Sq + e % pad;
+        p.neg_delta[at] = 0.f;
+        if (p.lse) p.neg_lse[at] = -INFINITY;
+    }
+}
+
+}  // namespace
+
+int launch_prep(const PrepParams& p, bool bf16, int num_sms, cudaStream_t stream) {
+    const long long per_block = 256 / (p.D / 8) * kRows;
+    const long long rows = (long long)p.B * p.Sq * p.Hq;
+    const unsigned grid = (unsigned)std::max(1LL, std::min((rows + per_block - 1) / per_block, 6LL * num_sms));
+    auto run = [&](auto kernel) {
+        kernel<<<grid, 256, 0, stream>>>(p);
+        return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    };
+    if (p.D == 128) return bf16 ? run(bwd_prep_kernel<128, true>) : run(bwd_prep_kernel<128, false>);
+    return bf16 ? run(bwd_prep_kernel<64, true>) : run(bwd_prep_kernel<64, false>);
+}
+
+}  // namespace bwd
+}  // namespace attn

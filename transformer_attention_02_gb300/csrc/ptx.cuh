@@ -115,6 +115,13 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// Plain copy of `bytes` (a multiple of 16; both addresses 16-byte aligned) completing on an mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 // 4-D tiled store shared -> global (coordinates innermost first), tracked in
 // the issuing thread's bulk async-group; rows past the tensor's extent are not
 // written.
