@@ -22,7 +22,7 @@ int launch(bool& attr_set, Kernel kernel, int smem, const CUtensorMap& q, const 
 template <int D, bool BF16, bool ADDITIVE>
 int launch_dq(bool& attr_set, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& d_o,
               const BwdParams& p, int grid, cudaStream_t stream) {
-    return launch(attr_set, bwd_dq_kernel<D, BF16, ADDITIVE>, QCfg<D>::kSmemBytes, q, k, v, d_o, p, grid, stream);
+    return launch(attr_set, bwd_dq_kernel<D, BF16, ADDITIVE>, QCfg<D, ADDITIVE>::kSmemBytes, q, k, v, d_o, p, grid, stream);
 }
 
 template <int D, bool BF16, bool ADDITIVE>

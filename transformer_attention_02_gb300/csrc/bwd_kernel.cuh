@@ -20,10 +20,9 @@
 //
 // Both are bound by the tensor cores: four (three) products of 512 cycles at D =
 // 128 stand against one exponential a pair (512 cycles of the SM's 32 a cycle).
-// Roles of a CTA (384 threads): warps 0-7 take the S and dP tiles from TMEM and
-// put P and dS back in 16 bits (warps 0-3 columns 0-63 of each, warps 4-7 the
-// others; a warp's lanes are 32 rows), warp 8 issues the products, warp 9 the
-// loads.
+// Roles of a CTA (640 threads): warps 0-15 take the S and dP tiles from TMEM and
+// put P and dS back in 16 bits (four warpgroups of 32 columns each; a warp's
+// lanes are 32 rows), warp 16 issues the products, warp 17 the loads.
 //
 // P enters its product in the inputs' 16-bit type, as in the forward pass, and
 // so does dS: the tensor cores take both operands in one type. Each is rounded
@@ -38,9 +37,10 @@
 namespace attn {
 namespace bwd {
 
-constexpr int kThreads = 384;
-constexpr int kIssueWarp = 8;
-constexpr int kLoadWarp = 9;
+constexpr int kThreads = 640;
+constexpr int kGroups = 4, kCols = kBlock / kGroups;       // warpgroups of the element-wise work, columns of each
+constexpr int kWarps = 4 * kGroups;
+constexpr int kIssueWarp = kWarps, kLoadWarp = kWarps + 1;
 constexpr uint32_t kRowBytes = kBlock * sizeof(float);     // 128 row statistics
 constexpr float kLog2E = 1.4426950408889634f;
 
@@ -73,24 +73,22 @@ __device__ __forceinline__ void product_over_d(uint32_t d, uint32_t a, uint32_t 
     }
 }
 
-// D(tmem) (+)= A B, A 128 x 128 in TMEM as its two halves stand (16-bit pairs, columns 0-31 and 64-95 from `a`), B a tile.
+// D(tmem) (+)= A B, A 128 x 128 in TMEM as the warpgroups leave it: 16-bit pairs, each in the first half of its own columns.
 template <int D, bool BF16>
 __device__ __forceinline__ void product_over_rows(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
     constexpr uint32_t kIdesc = ptx::idesc_f16(kBlock, D, BF16, false, true);
     const uint64_t bd = ptx::sdesc_mnmajor_sw128(b, Tile<D>::kBoxBytes);
 #pragma unroll
     for (int kk = 0; kk < kBlock / 16; ++kk)
-        ptx::mma_ts(d, a + (uint32_t)((kk >> 2) * 64 + (kk & 3) * 8), bd + (uint64_t)((kk * 16 * 128) >> 4), kIdesc,
+        ptx::mma_ts(d, a + (uint32_t)((kk >> 1) * kCols + (kk & 1) * 8), bd + (uint64_t)((kk * 16 * 128) >> 4), kIdesc,
                     (accumulate || kk > 0) ? 1u : 0u);
 }
 
-__device__ __forceinline__ void load64(uint32_t taddr, float* x) {
+__device__ __forceinline__ void load32(uint32_t taddr, float* x) {
     uint32_t* r = reinterpret_cast<uint32_t*>(x);
     ptx::tmem_ld32(taddr, r);
-    ptx::tmem_ld32(taddr + 32, r + 32);
     ptx::tmem_ld_wait();
     ptx::reg_fence32(r);
-    ptx::reg_fence32(r + 32);
 }
 
 template <bool BF16>
@@ -110,31 +108,38 @@ __device__ __forceinline__ void warp_arrive_tmem(uint32_t bar) {
     warp_arrive(bar);
 }
 
-// N accumulated values of a row, times `factor`, to 16 bits in device memory.
+// N accumulated values of a row, times `factor`, to 16 bits in device memory. `freed`: a barrier to arrive on once they
+// are in registers.
 template <int N, bool BF16>
-__device__ __forceinline__ void store_row(uint32_t taddr, uint16_t* row, float factor, bool there, bool vec8, bool zero) {
+__device__ __forceinline__ void store_row(uint32_t taddr, uint32_t freed, uint16_t* row, float factor, bool there, bool vec8) {
+    uint32_t v[N];
 #pragma unroll
-    for (int c = 0; c < N / 32; ++c) {
-        uint32_t v[32], w[16];
-        if (!zero) {
-            ptx::tmem_ld32(taddr + 32 * c, v);
-            ptx::tmem_ld_wait();
-            ptx::reg_fence32(v);
-        }
+    for (int c = 0; c < N; c += 32) ptx::tmem_ld32(taddr + c, v + c);
+    ptx::tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            w[i] = zero ? 0u : pack<BF16>(__uint_as_float(v[2 * i]) * factor, __uint_as_float(v[2 * i + 1]) * factor);
-        if (there) {
-            if (vec8) {
-                ptx::st_global_v8(row + 32 * c, w);
-                ptx::st_global_v8(row + 32 * c + 16, w + 8);
-            } else {
-                uint4* dst = reinterpret_cast<uint4*>(row + 32 * c);
+    for (int c = 0; c < N; c += 32) ptx::reg_fence32(v + c);
+    warp_arrive_tmem(freed);
+    if (!there) return;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-            }
+    for (int c = 0; c < N; c += 16) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i] = pack<BF16>(__uint_as_float(v[c + 2 * i]) * factor, __uint_as_float(v[c + 2 * i + 1]) * factor);
+        if (vec8) {
+            ptx::st_global_v8(row + c, w);
+        } else {
+            reinterpret_cast<uint4*>(row + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(row + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
     }
+}
+
+template <int N>
+__device__ __forceinline__ void zero_row(uint16_t* row, bool there) {
+#pragma unroll
+    for (int c = 0; c < N; c += 8)
+        if (there) *reinterpret_cast<uint4*>(row + c) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // ------------------------------------------------------------------ dK, dV
@@ -210,9 +215,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kLoadWarp && lane == 0) {
         for (int i = 0; i < C::kNumBars; ++i) {
             uint32_t count = 1;
-            if (i == C::bP || i == C::bDS || i == C::bAccEmpty) count = 8;
-            // a block's tile is free once its last product has run and the eight warps have its statistics
-            if ((i >= C::bQEmpty && i < C::bQEmpty + C::kQ) || (i >= C::bGEmpty && i < C::bGEmpty + C::kG)) count = 9;
+            if (i == C::bP || i == C::bDS || i == C::bAccEmpty) count = kWarps;
+            // a block's tile is free once its last product has run and the warps have its statistics
+            if ((i >= C::bQEmpty && i < C::bQEmpty + C::kQ) || (i >= C::bGEmpty && i < C::bGEmpty + C::kG)) count = kWarps + 1;
             ptx::mbar_init(bar(i), count);
         }
         *abort_flag = 0u;
@@ -291,67 +296,73 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (fills > s) drain_phase(bar(C::bG + s), ((fills - 1 - s) / C::kG) & 1u, sc);
     } else if (warp == kIssueWarp) {
         // --------------------------------------------------------- products
-        if (lane == 0) {
-            uint32_t tiles = 0, use = 0;
-            bool alive = true, issued = false;
-            if (p.stall) alive = wait_phase(bar(C::bStall), 0, sc);          // nothing ever arrives
-            for (int t = blockIdx.x; t < p.n_tiles && alive; t += gridDim.x) {
-                const KvTile w = kv_tile(t, p);
-                if (w.n == 0) continue;
-                auto issue_s = [&](uint32_t u) -> bool {
-                    const uint32_t s = u % C::kQ;
-                    if (!wait_phase(bar(C::bQ + s), (u / C::kQ) & 1u, sc)) return false;
-                    ptx::tc_fence_after_sync();
+        uint32_t tiles = 0, use = 0;
+        bool alive = true, issued = false;
+        if (p.stall) alive = warp_wait(bar(C::bStall), 0, sc);               // nothing ever arrives
+        for (int t = blockIdx.x; t < p.n_tiles && alive; t += gridDim.x) {
+            const KvTile w = kv_tile(t, p);
+            if (w.n == 0) continue;
+            auto issue_s = [&](uint32_t u) -> bool {
+                const uint32_t s = u % C::kQ;
+                if (!warp_wait(bar(C::bQ + s), (u / C::kQ) & 1u, sc)) return false;
+                ptx::tc_fence_after_sync();
+                if (ptx::elect_one()) {
                     product_over_d<D, BF16>(tmem + C::cS, smem + C::kKOff, smem + C::kQOff + s * T::kBytes);
                     ptx::tc_commit(bar(C::bS));
-                    return issued = true;
-                };
-                auto issue_dp = [&](uint32_t u) -> bool {
-                    const uint32_t s = u % C::kG;
-                    if (!wait_phase(bar(C::bG + s), (u / C::kG) & 1u, sc)) return false;
-                    ptx::tc_fence_after_sync();
+                }
+                return issued = true;
+            };
+            auto issue_dp = [&](uint32_t u) -> bool {
+                const uint32_t s = u % C::kG;
+                if (!warp_wait(bar(C::bG + s), (u / C::kG) & 1u, sc)) return false;
+                ptx::tc_fence_after_sync();
+                if (ptx::elect_one()) {
                     product_over_d<D, BF16>(tmem + C::cDP, smem + C::kVOff, smem + C::kGOff + s * T::kBytes);
                     ptx::tc_commit(bar(C::bDP));
-                    return true;
-                };
-                alive = wait_phase(bar(C::bK), tiles & 1u, sc) && issue_s(use) && wait_phase(bar(C::bV), tiles & 1u, sc) &&
-                        issue_dp(use);
-                if (alive && w.n == 1) ptx::tc_commit(bar(C::bKVEmpty));
-                for (int it = 0; it < w.n && alive; ++it, ++use) {
-                    const bool more = it + 1 < w.n;
-                    const uint32_t qs = use % C::kQ, gs = use % C::kG;
-                    alive = wait_phase(bar(C::bP), use & 1u, sc);
-                    // the warps have the last tile's dK and dV
-                    if (alive && it == 0 && tiles > 0) alive = wait_phase(bar(C::bAccEmpty), (tiles - 1) & 1u, sc);
-                    if (!alive) break;
-                    ptx::tc_fence_after_sync();
+                }
+                return true;
+            };
+            alive = warp_wait(bar(C::bK), tiles & 1u, sc) && issue_s(use) && warp_wait(bar(C::bV), tiles & 1u, sc) &&
+                    issue_dp(use);
+            if (alive && w.n == 1 && ptx::elect_one()) ptx::tc_commit(bar(C::bKVEmpty));
+            for (int it = 0; it < w.n && alive; ++it, ++use) {
+                const bool more = it + 1 < w.n;
+                const uint32_t qs = use % C::kQ, gs = use % C::kG;
+                alive = warp_wait(bar(C::bP), use & 1u, sc);
+                // the warps have the last tile's dK and dV
+                if (alive && it == 0 && tiles > 0) alive = warp_wait(bar(C::bAccEmpty), (tiles - 1) & 1u, sc);
+                if (!alive) break;
+                ptx::tc_fence_after_sync();
+                if (ptx::elect_one()) {
                     product_over_rows<D, BF16>(tmem + C::cDV, tmem + C::cS, smem + C::kGOff + gs * T::kBytes, it > 0);
                     ptx::tc_commit(bar(C::bGEmpty + gs));
-                    if (more && !(alive = issue_s(use + 1))) break;
-                    if (!(alive = wait_phase(bar(C::bDS), use & 1u, sc))) break;
-                    ptx::tc_fence_after_sync();
+                }
+                if (more && !(alive = issue_s(use + 1))) break;
+                if (!(alive = warp_wait(bar(C::bDS), use & 1u, sc))) break;
+                ptx::tc_fence_after_sync();
+                if (ptx::elect_one()) {
                     product_over_rows<D, BF16>(tmem + C::cDK, tmem + C::cDP, smem + C::kQOff + qs * T::kBytes, it > 0);
                     ptx::tc_commit(bar(C::bQEmpty + qs));
-                    if (more) {
-                        if (!(alive = issue_dp(use + 1))) break;
-                        if (it + 2 == w.n) ptx::tc_commit(bar(C::bKVEmpty));
-                    }
                 }
-                if (!alive) break;
-                ptx::tc_commit(bar(C::bAcc));
-                ++tiles;
+                if (more) {
+                    if (!(alive = issue_dp(use + 1))) break;
+                    if (it + 2 == w.n && ptx::elect_one()) ptx::tc_commit(bar(C::bKVEmpty));
+                }
             }
-            if (issued) {                                     // TMEM is freed after every product has run
-                ptx::tc_commit(bar(C::bDrain));
-                drain_phase(bar(C::bDrain), 0, sc);
-            }
+            if (!alive) break;
+            if (ptx::elect_one()) ptx::tc_commit(bar(C::bAcc));
+            ++tiles;
+        }
+        if (issued) {                                         // TMEM is freed after every product has run
+            if (ptx::elect_one()) ptx::tc_commit(bar(C::bDrain));
+            drain_phase(bar(C::bDrain), 0, sc);
         }
         __syncwarp();
-    } else if (warp < 8) {
+    } else if (warp < kWarps) {
         // ------------------------------------------------------- P^T and dS^T
-        const int wg = warp >> 2, r = (warp & 3) * 32 + lane;     // key of the tile; columns 64 wg ..
+        const int wg = warp >> 2, r = (warp & 3) * 32 + lane;     // key of the tile; columns kCols wg ..
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + lane_base + C::cS + 64 * wg, tDP = tmem + lane_base + C::cDP + 64 * wg;
+        const uint32_t tS = tmem + lane_base + C::cS + kCols * wg, tDP = tmem + lane_base + C::cDP + kCols * wg;
         const float sl = p.scale_log2;
         uint32_t tiles = 0, use = 0;
         bool alive = true;
@@ -368,43 +379,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     ? (int)min((long long)INT_MAX, (long long)max(w.k0, p.sinks) - p.off + p.window) : INT_MAX;
             int i = w.lo;
             for (int it = 0; it < w.n; ++it, ++use) {
-                const int m0 = i * kBlock + 64 * wg;              // this warp's first query
+                const int m0 = i * kBlock + kCols * wg;              // this warp's first query
                 const uint32_t qs = use % C::kQ, gs = use % C::kG;
-                float x[64];
+                float x[kCols];
                 if (ADDITIVE) {
                     // a warp's lanes are neighbouring keys: each load is one line of the mask
                     const float* at = p.mask + ((size_t)w.b * p.Sq + m0) * p.Sk + key;
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) x[c] = (key < p.Sk && m0 + c < p.Sq) ? __ldg(at + (size_t)c * p.Sk) : 0.f;
+                    for (int c = 0; c < kCols; ++c) x[c] = (key < p.Sk && m0 + c < p.Sq) ? __ldg(at + (size_t)c * p.Sk) : 0.f;
                 }
                 alive = warp_wait(bar(C::bQ + qs), (use / C::kQ) & 1u, sc) && warp_wait(bar(C::bS), use & 1u, sc);
                 if (!alive) break;
                 ptx::tc_fence_after_sync();
-                const float4* nl = reinterpret_cast<const float4*>(smem_ptr + C::kRowOff + qs * kRowBytes) + 16 * wg;
+                const float4* nl = reinterpret_cast<const float4*>(smem_ptr + C::kRowOff + qs * kRowBytes) + kCols / 4 * wg;
                 if (ADDITIVE) {
-                    const float4* is = reinterpret_cast<const float4*>(smem_ptr + C::kSumOff + qs * kRowBytes) + 16 * wg;
+                    const float4* is = reinterpret_cast<const float4*>(smem_ptr + C::kSumOff + qs * kRowBytes) + kCols / 4 * wg;
+                    float s[kCols];
+                    load32(tS, s);
 #pragma unroll
-                    for (int c = 0; c < 64; c += 32) {
-                        uint32_t s[32];
-                        ptx::tmem_ld32(tS + c, s);
-                        ptx::tmem_ld_wait();
-                        ptx::reg_fence32(s);
+                    for (int c = 0; c < kCols; c += 4) {
+                        const float4 n = nl[c / 4], u = is[c / 4];
+                        const float nn[4] = {n.x, n.y, n.z, n.w}, uu[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 n = nl[(c + e) / 4], u = is[(c + e) / 4];
-                            const float nn[4] = {n.x, n.y, n.z, n.w}, uu[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                            for (int d = 0; d < 4; ++d) {
-                                float y = fmaf(x[c + e + d], kLog2E, __uint_as_float(s[e + d]) * sl);
-                                if (m0 + c + e + d < see) y = -INFINITY;
-                                x[c + e + d] = ptx::ex2(y + nn[d]) * uu[d];
-                            }
+                        for (int d = 0; d < 4; ++d) {
+                            float y = fmaf(x[c + d], kLog2E, s[c + d] * sl);
+                            if (m0 + c + d < see) y = -INFINITY;
+                            x[c + d] = ptx::ex2(y + nn[d]) * uu[d];
                         }
                     }
                 } else {
-                    load64(tS, x);
+                    load32(tS, x);
 #pragma unroll
-                    for (int c = 0; c < 64; c += 4) {
+                    for (int c = 0; c < kCols; c += 4) {
                         const float4 n = nl[c / 4];
                         ptx::fma2(x[c], x[c + 1], x[c], x[c + 1], sl, sl, n.x, n.y);
                         ptx::fma2(x[c + 2], x[c + 3], x[c + 2], x[c + 3], sl, sl, n.z, n.w);
@@ -413,17 +419,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (base < all_see || base > all_end - kBlock) {
                         const int c0 = see - m0, c1 = end - m0;
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
+                        for (int c = 0; c < kCols; ++c)
                             if (c < c0 || c >= c1) x[c] = -INFINITY;
                     }
 #pragma unroll
-                    for (int c = 0; c < 64; ++c) x[c] = ptx::ex2(x[c]);
+                    for (int c = 0; c < kCols; ++c) x[c] = ptx::ex2(x[c]);
                 }
                 {
-                    uint32_t pk[32];
+                    uint32_t pk[kCols / 2];
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) pk[c] = pack<BF16>(x[2 * c], x[2 * c + 1]);
-                    ptx::tmem_st32(tS, pk);
+                    for (int c = 0; c < kCols / 2; ++c) pk[c] = pack<BF16>(x[2 * c], x[2 * c + 1]);
+                    ptx::tmem_st16(tS, pk);
                     ptx::tmem_st_wait();
                 }
                 warp_arrive_tmem(bar(C::bP));
@@ -432,28 +438,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 alive = warp_wait(bar(C::bG + gs), (use / C::kG) & 1u, sc) && warp_wait(bar(C::bDP), use & 1u, sc);
                 if (!alive) break;
                 ptx::tc_fence_after_sync();
-                const float4* nd = reinterpret_cast<const float4*>(smem_ptr + C::kDeltaOff + gs * kRowBytes) + 16 * wg;
+                const float4* nd = reinterpret_cast<const float4*>(smem_ptr + C::kDeltaOff + gs * kRowBytes) + kCols / 4 * wg;
                 {
-                    uint32_t pk[32];
+                    float d[kCols];
+                    uint32_t pk[kCols / 2];
+                    load32(tDP, d);
 #pragma unroll
-                    for (int c = 0; c < 64; c += 32) {
-                        uint32_t d[32];
-                        ptx::tmem_ld32(tDP + c, d);
-                        ptx::tmem_ld_wait();
-                        ptx::reg_fence32(d);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 n = nd[(c + e) / 4];
-                            float a0, a1, a2, a3;
-                            ptx::add2(a0, a1, __uint_as_float(d[e]), __uint_as_float(d[e + 1]), n.x, n.y);
-                            ptx::add2(a2, a3, __uint_as_float(d[e + 2]), __uint_as_float(d[e + 3]), n.z, n.w);
-                            ptx::mul2(a0, a1, a0, a1, x[c + e], x[c + e + 1]);
-                            ptx::mul2(a2, a3, a2, a3, x[c + e + 2], x[c + e + 3]);
-                            pk[(c + e) / 2] = pack<BF16>(a0, a1);
-                            pk[(c + e) / 2 + 1] = pack<BF16>(a2, a3);
-                        }
+                    for (int c = 0; c < kCols; c += 4) {
+                        const float4 n = nd[c / 4];
+                        ptx::add2(d[c], d[c + 1], d[c], d[c + 1], n.x, n.y);
+                        ptx::add2(d[c + 2], d[c + 3], d[c + 2], d[c + 3], n.z, n.w);
+                        ptx::mul2(d[c], d[c + 1], d[c], d[c + 1], x[c], x[c + 1]);
+                        ptx::mul2(d[c + 2], d[c + 3], d[c + 2], d[c + 3], x[c + 2], x[c + 3]);
+                        pk[c / 2] = pack<BF16>(d[c], d[c + 1]);
+                        pk[c / 2 + 1] = pack<BF16>(d[c + 2], d[c + 3]);
                     }
-                    ptx::tmem_st32(tDP, pk);
+                    ptx::tmem_st16(tDP, pk);
                     ptx::tmem_st_wait();
                 }
                 warp_arrive_tmem(bar(C::bDS));
@@ -461,17 +461,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (++i == w.lo + w.per_head) i = w.lo;
             }
             if (!alive) break;
-            // ---- warps 0-3 write dV, warps 4-7 dK
-            if (w.n > 0 && !(alive = warp_wait(bar(C::bAcc), tiles & 1u, sc))) break;
-            ptx::tc_fence_after_sync();
-            uint16_t* row = static_cast<uint16_t*>(wg ? p.dk : p.dv) +
-                            ((long long)w.b * p.Sk + key) * (wg ? p.dk_stride : p.dv_stride) + w.hk * D;
-            store_row<D, BF16>(tmem + lane_base + (wg ? C::cDK : C::cDV), row, wg ? p.scale : 1.f, key < p.Sk, p.vec8,
-                               w.n == 0);
-            if (w.n > 0) {
-                warp_arrive_tmem(bar(C::bAccEmpty));
-                ++tiles;
+            // ---- two warpgroups write dV, two dK, each half of the row
+            const bool is_k = wg >= 2;
+            const int col = (wg & 1) * (D / 2);
+            uint16_t* row = static_cast<uint16_t*>(is_k ? p.dk : p.dv) +
+                            ((long long)w.b * p.Sk + key) * (is_k ? p.dk_stride : p.dv_stride) + w.hk * D + col;
+            if (w.n == 0) {
+                zero_row<D / 2>(row, key < p.Sk);
+                continue;
             }
+            if (!(alive = warp_wait(bar(C::bAcc), tiles & 1u, sc))) break;
+            ptx::tc_fence_after_sync();
+            store_row<D / 2, BF16>(tmem + lane_base + (is_k ? C::cDK : C::cDV) + col, bar(C::bAccEmpty), row,
+                                   is_k ? p.scale : 1.f, key < p.Sk, p.vec8);
+            ++tiles;
         }
     }
 
@@ -493,19 +496,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the keys are walked twice: first for the rows' maximum and sum, since a mask of
 // large values leaves lse without the logits' bits; both go to the other kernel.
 
-template <int D>
+template <int D, bool ADDITIVE>
 struct QCfg {
     using T = Tile<D>;
-    static constexpr int kK = D == 128 ? 3 : 5, kV = D == 128 ? 2 : 4;
+    static constexpr int kK = D == 128 ? (ADDITIVE ? 2 : 3) : 5, kV = D == 128 ? 2 : 4;
     static constexpr int kQOff = 0, kGOff = T::kBytes, kKOff = 2 * T::kBytes, kVOff = kKOff + kK * T::kBytes;
     static constexpr int kBarOff = kVOff + kV * T::kBytes;
     static constexpr int bQ = 0, bQEmpty = 1, bS = 2, bDP = 4, bDPFree = 5, bDS = 6, bAcc = 8, bAccEmpty = 9, bDrain = 10,
-                         bStall = 11, bHalf = 12, bWhole = 13, bK = 14, bKEmpty = bK + kK, bV = bKEmpty + kK, bVEmpty = bV + kV,
+                         bStall = 11, bParts = 12, bWhole = 13, bK = 14, bKEmpty = bK + kK, bV = bKEmpty + kK, bVEmpty = bV + kV,
                          kNumBars = bVEmpty + kV;
     static constexpr int kTmemSlotOff = kBarOff + 8 * kNumBars;
     static constexpr int kAbortOff = kTmemSlotOff + 4;
-    static constexpr int kStatOff = (kAbortOff + 4 + 15) / 16 * 16;      // additive mask: [128] {maximum, sum} of a half
-    static constexpr int kSmemBytes = kStatOff + 128 * 8;
+    static constexpr int kStatOff = (kAbortOff + 4 + 15) / 16 * 16;      // additive mask: [kGroups][128] {maximum, sum}
+    static constexpr int kSmemBytes = kStatOff + (ADDITIVE ? kGroups * 128 * 8 : 0);
     static constexpr uint32_t cDQ = 0, cS = 128, cDP = 384;
     static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
@@ -544,7 +547,7 @@ template <int D, bool BF16, bool ADDITIVE>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG, const BwdParams p) {
-    using C = QCfg<D>;
+    using C = QCfg<D, ADDITIVE>;
     using T = Tile<D>;
     extern __shared__ __align__(1024) uint8_t smem_ptr[];
     const uint32_t smem = ptx::smem_addr(smem_ptr);
@@ -560,8 +563,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kLoadWarp && lane == 0) {
         for (int i = 0; i < C::kNumBars; ++i) {
             uint32_t count = 1;
-            if (i == C::bDPFree || i == C::bDS || i == C::bDS + 1 || i == C::bAccEmpty) count = 8;
-            if (i == C::bHalf || i == C::bWhole) count = 4;
+            if (i == C::bDPFree || i == C::bDS || i == C::bDS + 1 || i == C::bAccEmpty) count = kWarps;
+            if (i == C::bParts) count = kWarps - 4;
+            if (i == C::bWhole) count = 4;
             ptx::mbar_init(bar(i), count);
         }
         *abort_flag = 0u;
@@ -628,79 +632,83 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (vf > s) drain_phase(bar(C::bV + s), ((vf - 1 - s) / C::kV) & 1u, sc);
     } else if (warp == kIssueWarp) {
         // --------------------------------------------------------- products
-        if (lane == 0) {
-            // su: S tiles issued, and K tiles whose first use that was; ds: dS (or freed S) tiles taken; dp: dP tiles issued
-            uint32_t tiles = 0, su = 0, ds = 0, dp = 0;
-            bool alive = true, issued = false;
-            if (p.stall) alive = wait_phase(bar(C::bStall), 0, sc);          // nothing ever arrives
-            auto issue_s = [&]() -> bool {
-                const uint32_t s = su % C::kK;
-                if (!wait_phase(bar(C::bK + s), (su / C::kK) & 1u, sc)) return false;
-                ptx::tc_fence_after_sync();
+        // su: S tiles issued, and K tiles whose first use that was; ds: dS (or freed S) tiles taken; dp: dP tiles issued
+        uint32_t tiles = 0, su = 0, ds = 0, dp = 0;
+        bool alive = true, issued = false;
+        if (p.stall) alive = warp_wait(bar(C::bStall), 0, sc);          // nothing ever arrives
+        auto issue_s = [&]() -> bool {
+            const uint32_t s = su % C::kK;
+            if (!warp_wait(bar(C::bK + s), (su / C::kK) & 1u, sc)) return false;
+            ptx::tc_fence_after_sync();
+            if (ptx::elect_one()) {
                 product_over_d<D, BF16>(tmem + C::cS + 128 * (su & 1u), smem + C::kQOff, smem + C::kKOff + s * T::kBytes);
                 ptx::tc_commit(bar(C::bS + (su & 1u)));
-                ++su;
-                return issued = true;
-            };
-            auto issue_dp = [&]() -> bool {
-                const uint32_t s = dp % C::kV;
-                if (!wait_phase(bar(C::bV + s), (dp / C::kV) & 1u, sc)) return false;
-                if (dp > 0 && !wait_phase(bar(C::bDPFree), (dp - 1) & 1u, sc)) return false;
-                ptx::tc_fence_after_sync();
+            }
+            ++su;
+            return issued = true;
+        };
+        auto issue_dp = [&]() -> bool {
+            const uint32_t s = dp % C::kV;
+            if (!warp_wait(bar(C::bV + s), (dp / C::kV) & 1u, sc)) return false;
+            if (dp > 0 && !warp_wait(bar(C::bDPFree), (dp - 1) & 1u, sc)) return false;
+            ptx::tc_fence_after_sync();
+            if (ptx::elect_one()) {
                 product_over_d<D, BF16>(tmem + C::cDP, smem + C::kGOff, smem + C::kVOff + s * T::kBytes);
                 ptx::tc_commit(bar(C::bDP));
                 ptx::tc_commit(bar(C::bVEmpty + s));
-                ++dp;
-                return true;
-            };
-            auto wait_ds = [&]() -> bool {
-                const bool ok = wait_phase(bar(C::bDS + (ds & 1u)), (ds >> 1) & 1u, sc);
-                if (ok) ptx::tc_fence_after_sync();
-                return ok;
-            };
-            for (int t = blockIdx.x; t < p.n_tiles && alive; t += gridDim.x) {
-                const QTile w = q_tile(t, p);
-                if (w.n == 0) continue;
-                if (!(alive = wait_phase(bar(C::bQ), tiles & 1u, sc))) break;
-                if (ADDITIVE) {
-                    // S alone: a buffer is used again once the warps have read it
-                    alive = issue_s() && (w.n == 1 || issue_s());
-                    for (int j = 0; j < w.n && alive; ++j, ++ds) {
-                        if (!(alive = wait_ds())) break;
-                        ptx::tc_commit(bar(C::bKEmpty + ds % C::kK));
-                        if (j + 2 < w.n) alive = issue_s();
-                    }
-                }
-                // (Q and dO are free after S and dP of the last block)
-                alive = alive && issue_s() && issue_dp() && (w.n == 1 || issue_s());
-                if (alive && w.n == 1) ptx::tc_commit(bar(C::bQEmpty));
+            }
+            ++dp;
+            return true;
+        };
+        auto wait_ds = [&]() -> bool {
+            const bool ok = warp_wait(bar(C::bDS + (ds & 1u)), (ds >> 1) & 1u, sc);
+            if (ok) ptx::tc_fence_after_sync();
+            return ok;
+        };
+        for (int t = blockIdx.x; t < p.n_tiles && alive; t += gridDim.x) {
+            const QTile w = q_tile(t, p);
+            if (w.n == 0) continue;
+            if (!(alive = warp_wait(bar(C::bQ), tiles & 1u, sc))) break;
+            if (ADDITIVE) {
+                // S alone: a buffer is used again once the warps have read it
+                alive = issue_s() && (w.n == 1 || issue_s());
                 for (int j = 0; j < w.n && alive; ++j, ++ds) {
-                    if (j + 1 < w.n && !(alive = issue_dp())) break;
-                    if (j + 2 == w.n) ptx::tc_commit(bar(C::bQEmpty));
                     if (!(alive = wait_ds())) break;
-                    if (j == 0 && tiles > 0 && !(alive = wait_phase(bar(C::bAccEmpty), (tiles - 1) & 1u, sc))) break;
-                    ptx::tc_fence_after_sync();
-                    const uint32_t s = ds % C::kK;
+                    if (ptx::elect_one()) ptx::tc_commit(bar(C::bKEmpty + ds % C::kK));
+                    if (j + 2 < w.n) alive = issue_s();
+                }
+            }
+            // (Q and dO are free after S and dP of the last block)
+            alive = alive && issue_s() && issue_dp() && (w.n == 1 || issue_s());
+            if (alive && w.n == 1 && ptx::elect_one()) ptx::tc_commit(bar(C::bQEmpty));
+            for (int j = 0; j < w.n && alive; ++j, ++ds) {
+                if (j + 1 < w.n && !(alive = issue_dp())) break;
+                if (j + 2 == w.n && ptx::elect_one()) ptx::tc_commit(bar(C::bQEmpty));
+                if (!(alive = wait_ds())) break;
+                if (j == 0 && tiles > 0 && !(alive = warp_wait(bar(C::bAccEmpty), (tiles - 1) & 1u, sc))) break;
+                ptx::tc_fence_after_sync();
+                const uint32_t s = ds % C::kK;
+                if (ptx::elect_one()) {
                     product_over_rows<D, BF16>(tmem + C::cDQ, tmem + C::cS + 128 * (ds & 1u), smem + C::kKOff + s * T::kBytes,
                                                j > 0);
                     ptx::tc_commit(bar(C::bKEmpty + s));
-                    if (j + 2 < w.n) alive = issue_s();
                 }
-                if (!alive) break;
-                ptx::tc_commit(bar(C::bAcc));
-                ++tiles;
+                if (j + 2 < w.n) alive = issue_s();
             }
-            if (issued) {
-                ptx::tc_commit(bar(C::bDrain));
-                drain_phase(bar(C::bDrain), 0, sc);
-            }
+            if (!alive) break;
+            if (ptx::elect_one()) ptx::tc_commit(bar(C::bAcc));
+            ++tiles;
+        }
+        if (issued) {
+            if (ptx::elect_one()) ptx::tc_commit(bar(C::bDrain));
+            drain_phase(bar(C::bDrain), 0, sc);
         }
         __syncwarp();
-    } else if (warp < 8) {
+    } else if (warp < kWarps) {
         // ---------------------------------------------------------------- dS
-        const int wg = warp >> 2, r = (warp & 3) * 32 + lane;     // query of the tile; columns 64 wg ..
+        const int wg = warp >> 2, r = (warp & 3) * 32 + lane;     // query of the tile; columns kCols wg ..
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + lane_base + C::cS + 64 * wg, tDP = tmem + lane_base + C::cDP + 64 * wg;
+        const uint32_t tS = tmem + lane_base + C::cS + kCols * wg, tDP = tmem + lane_base + C::cDP + kCols * wg;
         const float sl = p.scale_log2;
         float2* stat = reinterpret_cast<float2*>(smem_ptr + C::kStatOff);
         uint32_t tiles = 0, su = 0, dp = 0, seen = 0;
@@ -720,42 +728,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 
             // logits in log2 units of block j: S in the buffer of `su`, scaled, masked, hidden keys at -inf
             auto logits = [&](int j, float* x) -> bool {
-                const int key0 = w.block(j) * kBlock + 64 * wg;
+                const int key0 = w.block(j) * kBlock + kCols * wg;
                 if (ADDITIVE) {
-                    const bool vec = mrow != nullptr && key0 + 64 <= p.Sk && p.Sk % 4 == 0 &&
+                    const bool vec = mrow != nullptr && key0 + kCols <= p.Sk && p.Sk % 4 == 0 &&
                                      (reinterpret_cast<uintptr_t>(p.mask) & 15) == 0;
                     if (vec) {
 #pragma unroll
-                        for (int c = 0; c < 64; c += 4) {
+                        for (int c = 0; c < kCols; c += 4) {
                             const float4 m = ptx::ld_global_nc_v4(mrow + key0 + c);
                             x[c] = m.x, x[c + 1] = m.y, x[c + 2] = m.z, x[c + 3] = m.w;
                         }
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c) x[c] = mrow != nullptr && key0 + c < p.Sk ? __ldg(mrow + key0 + c) : 0.f;
+                        for (int c = 0; c < kCols; ++c) x[c] = mrow != nullptr && key0 + c < p.Sk ? __ldg(mrow + key0 + c) : 0.f;
                     }
                 }
                 if (!warp_wait(bar(C::bS + (su & 1u)), (su >> 1) & 1u, sc)) return false;
                 ptx::tc_fence_after_sync();
                 if (ADDITIVE) {
+                    float s[kCols];
+                    load32(tS + 128 * (su & 1u), s);
 #pragma unroll
-                    for (int c = 0; c < 64; c += 32) {
-                        uint32_t s[32];
-                        ptx::tmem_ld32(tS + 128 * (su & 1u) + c, s);
-                        ptx::tmem_ld_wait();
-                        ptx::reg_fence32(s);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) x[c + e] = fmaf(x[c + e], kLog2E, __uint_as_float(s[e]) * sl);
-                    }
+                    for (int c = 0; c < kCols; ++c) x[c] = fmaf(x[c], kLog2E, s[c] * sl);
                 } else {
-                    load64(tS + 128 * (su & 1u), x);
+                    load32(tS + 128 * (su & 1u), x);
 #pragma unroll
-                    for (int c = 0; c < 64; c += 2) ptx::fma2(x[c], x[c + 1], x[c], x[c + 1], sl, sl, nl, nl);
+                    for (int c = 0; c < kCols; c += 2) ptx::fma2(x[c], x[c + 1], x[c], x[c + 1], sl, sl, nl, nl);
                 }
                 const int c1 = lim - key0, c0 = low - key0, cs = p.sinks - key0;
-                if (c1 < 64 || (p.window && c0 > 0 && cs < 64)) {
+                if (c1 < kCols || (p.window && c0 > 0 && cs < kCols)) {
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
+                    for (int c = 0; c < kCols; ++c)
                         if (c >= c1 || (p.window && c < c0 && c >= cs)) x[c] = -INFINITY;
                 }
                 return true;
@@ -764,32 +767,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ADDITIVE) {
                 float m = -INFINITY, l = 0.f;
                 for (int j = 0; j < w.n; ++j, ++su) {
-                    float x[64];
+                    float x[kCols];
                     if (!(alive = logits(j, x))) break;
                     warp_arrive_tmem(bar(C::bDS + (su & 1u)));
                     float top = m;
 #pragma unroll
-                    for (int c = 0; c < 64; c += 2) top = ptx::max3(top, x[c], x[c + 1]);
+                    for (int c = 0; c < kCols; c += 2) top = ptx::max3(top, x[c], x[c + 1]);
                     if (top != -INFINITY) {
                         l *= ptx::ex2(m - top);
                         m = top;
 #pragma unroll
-                        for (int c = 0; c < 64; ++c) l += ptx::ex2(x[c] - top);
+                        for (int c = 0; c < kCols; ++c) l += ptx::ex2(x[c] - top);
                     }
                 }
                 if (!alive) break;
-                // join the two halves of the row
+                // the first warpgroup joins the parts of the row
                 if (wg) {
-                    stat[r] = make_float2(m, l);
-                    warp_arrive(bar(C::bHalf));
+                    stat[128 * wg + r] = make_float2(m, l);
+                    warp_arrive(bar(C::bParts));
                     if (!(alive = warp_wait(bar(C::bWhole), seen & 1u, sc))) break;
                 } else {
-                    if (!(alive = warp_wait(bar(C::bHalf), seen & 1u, sc))) break;
-                    const float2 o = stat[r];
-                    const float top = fmaxf(m, o.x);
-                    if (top != -INFINITY) l = l * ptx::ex2(m - top) + o.y * ptx::ex2(o.x - top);
+                    if (!(alive = warp_wait(bar(C::bParts), seen & 1u, sc))) break;
+#pragma unroll
+                    for (int g = 1; g < kGroups; ++g) {
+                        const float2 o = stat[128 * g + r];
+                        const float top = fmaxf(m, o.x);
+                        if (top != -INFINITY) l = l * ptx::ex2(m - top) + o.y * ptx::ex2(o.x - top);
+                        m = top;
+                    }
                     const bool any = there && l > 0.f;
-                    stat[r] = make_float2(any ? -top : 0.f, any ? 1.f / l : 0.f);
+                    stat[r] = make_float2(any ? -m : 0.f, any ? 1.f / l : 0.f);
                     p.neg_lse[at] = stat[r].x;
                     p.inv_sum[at] = stat[r].y;
                     warp_arrive(bar(C::bWhole));
@@ -799,43 +806,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 is = stat[r].y;
             }
             for (int j = 0; j < w.n; ++j, ++su, ++dp) {
-                float x[64];
+                float x[kCols];
                 if (!(alive = logits(j, x))) break;
 #pragma unroll
-                for (int c = 0; c < 64; ++c) x[c] = ptx::ex2(ADDITIVE ? x[c] + nl : x[c]);
+                for (int c = 0; c < kCols; ++c) x[c] = ptx::ex2(ADDITIVE ? x[c] + nl : x[c]);
                 if (!(alive = warp_wait(bar(C::bDP), dp & 1u, sc))) break;
                 ptx::tc_fence_after_sync();
-                uint32_t pk[32];
+                float d[kCols];
+                uint32_t pk[kCols / 2];
+                load32(tDP, d);
+                warp_arrive_tmem(bar(C::bDPFree));
 #pragma unroll
-                for (int c = 0; c < 64; c += 32) {
-                    uint32_t d[32];
-                    ptx::tmem_ld32(tDP + c, d);
-                    ptx::tmem_ld_wait();
-                    ptx::reg_fence32(d);
-                    if (c == 32) warp_arrive_tmem(bar(C::bDPFree));
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float a0, a1;
-                        ptx::add2(a0, a1, __uint_as_float(d[e]), __uint_as_float(d[e + 1]), nd, nd);
-                        if (ADDITIVE) ptx::mul2(a0, a1, a0, a1, is, is);
-                        ptx::mul2(a0, a1, a0, a1, x[c + e], x[c + e + 1]);
-                        pk[(c + e) / 2] = pack<BF16>(a0, a1);
-                    }
+                for (int c = 0; c < kCols; c += 2) {
+                    ptx::add2(d[c], d[c + 1], d[c], d[c + 1], nd, nd);
+                    if (ADDITIVE) ptx::mul2(d[c], d[c + 1], d[c], d[c + 1], is, is);
+                    ptx::mul2(d[c], d[c + 1], d[c], d[c + 1], x[c], x[c + 1]);
+                    pk[c / 2] = pack<BF16>(d[c], d[c + 1]);
                 }
-                ptx::tmem_st32(tS + 128 * (su & 1u), pk);
+                ptx::tmem_st16(tS + 128 * (su & 1u), pk);
                 ptx::tmem_st_wait();
                 warp_arrive_tmem(bar(C::bDS + (su & 1u)));
             }
             if (!alive) break;
-            // ---- each half of the warps writes half of the row
-            if (w.n > 0 && !(alive = warp_wait(bar(C::bAcc), tiles & 1u, sc))) break;
-            ptx::tc_fence_after_sync();
-            uint16_t* out = static_cast<uint16_t*>(p.dq) + ((long long)w.b * p.Sq + row) * p.dq_stride + w.h * D + wg * (D / 2);
-            store_row<D / 2, BF16>(tmem + lane_base + C::cDQ + wg * (D / 2), out, p.scale, there, p.vec8, w.n == 0);
-            if (w.n > 0) {
-                warp_arrive_tmem(bar(C::bAccEmpty));
-                ++tiles;
+            // ---- each warpgroup writes 32 columns
+            const bool writes = 32 * wg < D;
+            uint16_t* out = static_cast<uint16_t*>(p.dq) + ((long long)w.b * p.Sq + row) * p.dq_stride + w.h * D + 32 * wg;
+            if (w.n == 0) {
+                zero_row<32>(out, there && writes);
+                continue;
             }
+            if (!(alive = warp_wait(bar(C::bAcc), tiles & 1u, sc))) break;
+            ptx::tc_fence_after_sync();
+            if (writes)
+                store_row<32, BF16>(tmem + lane_base + C::cDQ + 32 * wg, bar(C::bAccEmpty), out, p.scale, there, p.vec8);
+            else
+                warp_arrive(bar(C::bAccEmpty));
+            ++tiles;
         }
     }
 
