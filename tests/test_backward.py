@@ -345,7 +345,7 @@ def test_refusals_on_the_host(fn, kw, code):
 
 
 def test_workspace_sizes():
-    assert A.attn_bwd_workspace_bytes(2, 4, 2, 100, 300, 64, 1) == 2 * 2 * 4 * 128 * 4
-    assert A.attn_bwd_workspace_bytes(2, 4, 2, 100, 300, 64, 2) == 3 * 2 * 4 * 128 * 4
+    assert A.attn_bwd_workspace_bytes(2, 4, 2, 100, 300, 64, 1) == 256 + 2 * 2 * 4 * 128 * 4
+    assert A.attn_bwd_workspace_bytes(2, 4, 2, 100, 300, 64, 2) == 256 + 3 * 2 * 4 * 128 * 4
     assert A.attn_bwd_workspace_bytes(2, 4, 3, 100, 300, 64, 1) == 0
     assert A.attn_bwd_workspace_bytes(2, 4, 2, 0, 300, 64, 1) == 0

@@ -19,9 +19,11 @@ size_t align_up(size_t x) { return (x + kWorkspaceAlign - 1) / kWorkspaceAlign *
 
 bool is_additive(int mask_kind) { return mask_kind == ATTN_MASK_ADDITIVE || mask_kind == ATTN_MASK_CAUSAL_ADDITIVE; }
 
-// Three rows of statistics for every query row, the third with an additive mask only.
+// Two tile counters, then three statistics for every query row, the third with an additive mask only.
 size_t stat_bytes(int B, int Hq, int Sq) { return align_up((size_t)B * Hq * bwd::padded_rows(Sq) * sizeof(float)); }
-size_t bwd_workspace(int B, int Hq, int Sq, int mask_kind) { return stat_bytes(B, Hq, Sq) * (is_additive(mask_kind) ? 3 : 2); }
+size_t bwd_workspace(int B, int Hq, int Sq, int mask_kind) {
+    return kWorkspaceAlign + stat_bytes(B, Hq, Sq) * (is_additive(mask_kind) ? 3 : 2);
+}
 
 // A tensor of tokens: pointer, distance of tokens, H * D values a token. Null only where it is empty.
 bool tokens_ok(const void* ptr, long long stride, int B, int S, int H, int D) {
@@ -47,13 +49,15 @@ int zero_tokens(void* ptr, long long stride, int B, int S, int H, int D, cudaStr
 }
 
 template <int D, bool BF16, bool ADDITIVE>
-int launch_both(const DeviceState& dev, const CUtensorMap* maps, bwd::BwdParams& p, cudaStream_t stream) {
+int launch_both(const DeviceState& dev, const CUtensorMap* maps, bwd::BwdParams& p, unsigned int* counters, cudaStream_t stream) {
     bool* attr = dev.bwd_attr_set[D == 128][BF16][ADDITIVE];
     p.n_tiles = p.B * p.Hq * p.n_qb;
+    p.counter = counters;
     int rc = bwd::launch_dq<D, BF16, ADDITIVE>(attr[0], maps[0], maps[1], maps[2], maps[3], p,
                                                std::min(p.n_tiles, dev.num_sms), stream);
     if (rc != ATTN_OK) return rc;
     p.n_tiles = p.B * p.Hkv * p.n_kb;
+    p.counter = counters + 1;
     return bwd::launch_dkv<D, BF16, ADDITIVE>(attr[1], maps[0], maps[1], maps[2], maps[3], p,
                                               std::min(p.n_tiles, dev.num_sms), stream);
 }
@@ -99,7 +103,8 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
         encode_tokens(&maps[3], d_o, B, Sq, Hq, D, bf16, (long long)Hq * D) != ATTN_OK)
         return ATTN_ERR_CUDA;
     const size_t stat = stat_bytes(B, Hq, Sq);
-    char* const ws = static_cast<char*>(workspace);
+    unsigned int* const counters = static_cast<unsigned int*>(workspace);
+    char* const ws = static_cast<char*>(workspace) + kWorkspaceAlign;
 
     bwd::PrepParams pp{};
     pp.o = static_cast<const uint16_t*>(o);
@@ -107,6 +112,7 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
     pp.lse = additive ? nullptr : lse;
     pp.neg_lse = reinterpret_cast<float*>(ws);
     pp.neg_delta = reinterpret_cast<float*>(ws + stat);
+    pp.counters = counters;
     pp.B = B;
     pp.Hq = Hq;
     pp.Sq = Sq;
@@ -148,11 +154,11 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
     p.timeout_ns = dev.timeout_ns;
     p.status = dev.status;
     if (D == 128) {
-        if (additive) return bf16 ? launch_both<128, true, true>(dev, maps, p, stream) : launch_both<128, false, true>(dev, maps, p, stream);
-        return bf16 ? launch_both<128, true, false>(dev, maps, p, stream) : launch_both<128, false, false>(dev, maps, p, stream);
+        if (additive) return bf16 ? launch_both<128, true, true>(dev, maps, p, counters, stream) : launch_both<128, false, true>(dev, maps, p, counters, stream);
+        return bf16 ? launch_both<128, true, false>(dev, maps, p, counters, stream) : launch_both<128, false, false>(dev, maps, p, counters, stream);
     }
-    if (additive) return bf16 ? launch_both<64, true, true>(dev, maps, p, stream) : launch_both<64, false, true>(dev, maps, p, stream);
-    return bf16 ? launch_both<64, true, false>(dev, maps, p, stream) : launch_both<64, false, false>(dev, maps, p, stream);
+    if (additive) return bf16 ? launch_both<64, true, true>(dev, maps, p, counters, stream) : launch_both<64, false, true>(dev, maps, p, counters, stream);
+    return bf16 ? launch_both<64, true, false>(dev, maps, p, counters, stream) : launch_both<64, false, false>(dev, maps, p, counters, stream);
 }
 
 }  // namespace

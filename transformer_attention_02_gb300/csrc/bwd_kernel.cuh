@@ -96,6 +96,13 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
     return BF16 ? ptx::pack_bf16x2(a, b) : ptx::pack_f16x2(a, b);
 }
 
+// Waits for two phases; the probes of both are under way together.
+__device__ __forceinline__ bool warp_wait2(uint32_t bar_a, uint32_t parity_a, uint32_t bar_b, uint32_t parity_b, const SyncCtx& sc) {
+    const bool a = ptx::mbar_try_wait(bar_a, parity_a), b = ptx::mbar_try_wait(bar_b, parity_b);
+    if (__all_sync(0xffffffffu, a && b)) return true;
+    return warp_wait(bar_a, parity_a, sc) && warp_wait(bar_b, parity_b, sc);
+}
+
 // A warp is through with something: one arrival for its 32 lanes.
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
     __syncwarp();
@@ -142,6 +149,50 @@ __device__ __forceinline__ void zero_row(uint16_t* row, bool there) {
         if (there) *reinterpret_cast<uint4*>(row + c) = make_uint4(0u, 0u, 0u, 0u);
 }
 
+// Work tiles are handed out in order: a CTA's first is its own index, each further one comes from a counter in the
+// workspace when the CTA is about to load it, so that CTAs with short tiles take more of them. (Which CTA computes a tile
+// changes nothing in it.) The loading warp publishes them in a ring of two entries; every other warp takes a copy.
+struct TileRing {
+    uint32_t full, empty;           // barriers, two each
+    volatile int* entry;
+};
+constexpr int kRing = 2;
+constexpr uint32_t kRingReaders = kWarps + 1;
+
+// The k-th tile of the CTA, or -1 at the end (or where a wait ran out).
+__device__ __forceinline__ int take_tile(uint32_t k, const BwdParams& p, const TileRing& ring, const SyncCtx& sc) {
+    const uint32_t s = k % kRing;
+    if (k >= kRing && !warp_wait(ring.empty + 8 * s, (k / kRing - 1) & 1u, sc)) return -1;
+    int t = 0;
+    if ((threadIdx.x & 31) == 0) {
+        t = k == 0 ? (int)blockIdx.x : (int)min((long long)gridDim.x + atomicAdd(p.counter, 1u), (long long)p.n_tiles);
+        if (t >= p.n_tiles) t = -1;
+        ring.entry[s] = t;
+        ptx::mbar_arrive(ring.full + 8 * s);
+    }
+    return __shfl_sync(0xffffffffu, t, 0);
+}
+
+__device__ __forceinline__ int next_tile(uint32_t k, const TileRing& ring, const SyncCtx& sc) {
+    const uint32_t s = k % kRing;
+    if (!warp_wait(ring.full + 8 * s, (k / kRing) & 1u, sc)) return -1;
+    const int t = ring.entry[s];
+    warp_arrive(ring.empty + 8 * s);
+    return t;
+}
+
+// A place in a ring of N buffers: which buffer, and how often it was used before (its barriers' parity).
+template <int N>
+struct Place {
+    uint32_t at = 0, round = 0;
+    __device__ __forceinline__ uint32_t parity() const { return round & 1u; }
+    __device__ __forceinline__ Place next() const {
+        Place n = *this;
+        if (++n.at == N) n.at = 0, ++n.round;
+        return n;
+    }
+};
+
 // ------------------------------------------------------------------ dK, dV
 //
 // TMEM: S^T and then P^T in columns 0-127, dP^T and then dS^T in 128-255, dV from
@@ -162,12 +213,13 @@ struct KvCfg {
     static constexpr int kDeltaOff = kRowOff + kQ * (int)kRowBytes;
     static constexpr int kSumOff = kDeltaOff + kG * (int)kRowBytes;
     static constexpr int kBarOff = kSumOff + (ADDITIVE ? kQ * (int)kRowBytes : 0);
-    static constexpr int bK = 0, bV = 1, bKVEmpty = 2, bS = 3, bP = 4, bDP = 5, bDS = 6, bAcc = 7, bAccEmpty = 8,
-                         bDrain = 9, bStall = 10, bQ = 11, bQEmpty = bQ + kQ, bG = bQEmpty + kQ, bGEmpty = bG + kG,
-                         kNumBars = bGEmpty + kG;
+    static constexpr int bK = 0, bV = 1, bKVEmpty = 2, bP = 3, bDS = 4, bAcc = 5, bAccEmpty = 6, bDrain = 7, bStall = 8,
+                         bS = 9, bDP = 10, bTile = 11, bTileEmpty = bTile + kRing, bQ = bTileEmpty + kRing, bQEmpty = bQ + kQ,
+                         bG = bQEmpty + kQ, bGEmpty = bG + kG, kNumBars = bGEmpty + kG;
     static constexpr int kTmemSlotOff = kBarOff + 8 * kNumBars;
     static constexpr int kAbortOff = kTmemSlotOff + 4;
-    static constexpr int kSmemBytes = kAbortOff + 4;
+    static constexpr int kTileOff = kAbortOff + 4;
+    static constexpr int kSmemBytes = kTileOff + 4 * kRing;
     static constexpr uint32_t cS = 0, cDP = 128, cDV = 256, cDK = 256 + D;
     static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
@@ -211,10 +263,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem_ptr + C::kAbortOff);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_ptr + C::kTmemSlotOff);
     auto bar = [&](int i) { return smem + C::kBarOff + 8u * (uint32_t)i; };
+    const TileRing ring{bar(C::bTile), bar(C::bTileEmpty), reinterpret_cast<volatile int*>(smem_ptr + C::kTileOff)};
 
     if (warp == kLoadWarp && lane == 0) {
         for (int i = 0; i < C::kNumBars; ++i) {
             uint32_t count = 1;
+            if (i >= C::bTileEmpty && i < C::bTileEmpty + kRing) count = kRingReaders;
             if (i == C::bP || i == C::bDS || i == C::bAccEmpty) count = kWarps;
             // a block's tile is free once its last product has run and the warps have its statistics
             if ((i >= C::bQEmpty && i < C::bQEmpty + C::kQ) || (i >= C::bGEmpty && i < C::bGEmpty + C::kG)) count = kWarps + 1;
@@ -241,8 +295,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
         uint32_t tiles = 0, fills = 0;                         // tiles with work, blocks
+        Place<C::kQ> q;
+        Place<C::kG> g;
         bool alive = true;
-        for (int t = blockIdx.x; t < p.n_tiles && alive; t += gridDim.x) {
+        for (uint32_t k = 0; alive; ++k) {
+            const int t = take_tile(k, p, ring, sc);
+            if (t < 0) break;
             const KvTile w = kv_tile(t, p);
             if (w.n == 0) continue;
             if (tiles > 0 && !warp_wait(bar(C::bKVEmpty), (tiles - 1) & 1u, sc)) break;
@@ -254,30 +312,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++tiles;
             int h = w.hk * p.group, i = w.lo;
-            for (int it = 0; it < w.n; ++it, ++fills) {
-                const uint32_t qs = fills % C::kQ, gs = fills % C::kG;
+            for (int it = 0; it < w.n; ++it, ++fills, q = q.next(), g = g.next()) {
                 const size_t row = ((size_t)w.b * p.Hq + h) * p.Sp + (size_t)i * kBlock;
-                if (fills >= (uint32_t)C::kQ && !warp_wait(bar(C::bQEmpty + qs), (fills / C::kQ - 1) & 1u, sc)) {
-                    alive = false;
-                    break;
-                }
+                alive = (q.round == 0 || warp_wait(bar(C::bQEmpty + q.at), (q.round - 1) & 1u, sc)) &&
+                        (g.round == 0 || warp_wait(bar(C::bGEmpty + g.at), (g.round - 1) & 1u, sc));
+                if (!alive) break;
                 if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(bar(C::bQ + qs), T::kBytes + kRowBytes * (ADDITIVE ? 2 : 1));
-                    load_tile<D>(smem + C::kQOff + qs * T::kBytes, &tmQ, bar(C::bQ + qs), h, i * kBlock, w.b);
-                    ptx::bulk_load(smem + C::kRowOff + qs * kRowBytes, p.neg_lse + row, kRowBytes, bar(C::bQ + qs));
+                    ptx::mbar_arrive_expect_tx(bar(C::bQ + q.at), T::kBytes + kRowBytes * (ADDITIVE ? 2 : 1));
+                    load_tile<D>(smem + C::kQOff + q.at * T::kBytes, &tmQ, bar(C::bQ + q.at), h, i * kBlock, w.b);
+                    ptx::bulk_load(smem + C::kRowOff + q.at * kRowBytes, p.neg_lse + row, kRowBytes, bar(C::bQ + q.at));
                     if (ADDITIVE)
-                        ptx::bulk_load(smem + C::kSumOff + qs * kRowBytes, p.inv_sum + row, kRowBytes, bar(C::bQ + qs));
-                }
-                if (fills >= (uint32_t)C::kG && !warp_wait(bar(C::bGEmpty + gs), (fills / C::kG - 1) & 1u, sc)) {
-                    // (the Q tile of this block is in flight: it counts for the shutdown)
-                    if (lane == 0) drain_phase(bar(C::bQ + qs), (fills / C::kQ) & 1u, sc);
-                    alive = false;
-                    break;
-                }
-                if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(bar(C::bG + gs), T::kBytes + kRowBytes);
-                    load_tile<D>(smem + C::kGOff + gs * T::kBytes, &tmG, bar(C::bG + gs), h, i * kBlock, w.b);
-                    ptx::bulk_load(smem + C::kDeltaOff + gs * kRowBytes, p.neg_delta + row, kRowBytes, bar(C::bG + gs));
+                        ptx::bulk_load(smem + C::kSumOff + q.at * kRowBytes, p.inv_sum + row, kRowBytes, bar(C::bQ + q.at));
+                    ptx::mbar_arrive_expect_tx(bar(C::bG + g.at), T::kBytes + kRowBytes);
+                    load_tile<D>(smem + C::kGOff + g.at * T::kBytes, &tmG, bar(C::bG + g.at), h, i * kBlock, w.b);
+                    ptx::bulk_load(smem + C::kDeltaOff + g.at * kRowBytes, p.neg_delta + row, kRowBytes, bar(C::bG + g.at));
                 }
                 if (++i == w.lo + w.per_head) {
                     i = w.lo;
@@ -297,55 +345,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kIssueWarp) {
         // --------------------------------------------------------- products
         uint32_t tiles = 0, use = 0;
+        Place<C::kQ> q;
+        Place<C::kG> g;
         bool alive = true, issued = false;
         if (p.stall) alive = warp_wait(bar(C::bStall), 0, sc);               // nothing ever arrives
-        for (int t = blockIdx.x; t < p.n_tiles && alive; t += gridDim.x) {
+        for (uint32_t k = 0; alive; ++k) {
+            const int t = next_tile(k, ring, sc);
+            if (t < 0) break;
             const KvTile w = kv_tile(t, p);
             if (w.n == 0) continue;
-            auto issue_s = [&](uint32_t u) -> bool {
-                const uint32_t s = u % C::kQ;
-                if (!warp_wait(bar(C::bQ + s), (u / C::kQ) & 1u, sc)) return false;
+            auto issue_s = [&](const Place<C::kQ>& at) -> bool {
+                if (!warp_wait(bar(C::bQ + at.at), at.parity(), sc)) return false;
                 ptx::tc_fence_after_sync();
                 if (ptx::elect_one()) {
-                    product_over_d<D, BF16>(tmem + C::cS, smem + C::kKOff, smem + C::kQOff + s * T::kBytes);
+                    product_over_d<D, BF16>(tmem + C::cS, smem + C::kKOff, smem + C::kQOff + at.at * T::kBytes);
                     ptx::tc_commit(bar(C::bS));
                 }
                 return issued = true;
             };
-            auto issue_dp = [&](uint32_t u) -> bool {
-                const uint32_t s = u % C::kG;
-                if (!warp_wait(bar(C::bG + s), (u / C::kG) & 1u, sc)) return false;
+            auto issue_dp = [&](const Place<C::kG>& at) -> bool {
+                if (!warp_wait(bar(C::bG + at.at), at.parity(), sc)) return false;
                 ptx::tc_fence_after_sync();
                 if (ptx::elect_one()) {
-                    product_over_d<D, BF16>(tmem + C::cDP, smem + C::kVOff, smem + C::kGOff + s * T::kBytes);
+                    product_over_d<D, BF16>(tmem + C::cDP, smem + C::kVOff, smem + C::kGOff + at.at * T::kBytes);
                     ptx::tc_commit(bar(C::bDP));
                 }
                 return true;
             };
-            alive = warp_wait(bar(C::bK), tiles & 1u, sc) && issue_s(use) && warp_wait(bar(C::bV), tiles & 1u, sc) &&
-                    issue_dp(use);
+            alive = warp_wait(bar(C::bK), tiles & 1u, sc) && issue_s(q) && warp_wait(bar(C::bV), tiles & 1u, sc) && issue_dp(g);
             if (alive && w.n == 1 && ptx::elect_one()) ptx::tc_commit(bar(C::bKVEmpty));
-            for (int it = 0; it < w.n && alive; ++it, ++use) {
+            for (int it = 0; it < w.n && alive; ++it, ++use, q = q.next(), g = g.next()) {
                 const bool more = it + 1 < w.n;
-                const uint32_t qs = use % C::kQ, gs = use % C::kG;
                 alive = warp_wait(bar(C::bP), use & 1u, sc);
                 // the warps have the last tile's dK and dV
                 if (alive && it == 0 && tiles > 0) alive = warp_wait(bar(C::bAccEmpty), (tiles - 1) & 1u, sc);
                 if (!alive) break;
                 ptx::tc_fence_after_sync();
                 if (ptx::elect_one()) {
-                    product_over_rows<D, BF16>(tmem + C::cDV, tmem + C::cS, smem + C::kGOff + gs * T::kBytes, it > 0);
-                    ptx::tc_commit(bar(C::bGEmpty + gs));
+                    product_over_rows<D, BF16>(tmem + C::cDV, tmem + C::cS, smem + C::kGOff + g.at * T::kBytes, it > 0);
+                    ptx::tc_commit(bar(C::bGEmpty + g.at));
                 }
-                if (more && !(alive = issue_s(use + 1))) break;
+                if (more && !(alive = issue_s(q.next()))) break;
                 if (!(alive = warp_wait(bar(C::bDS), use & 1u, sc))) break;
                 ptx::tc_fence_after_sync();
                 if (ptx::elect_one()) {
-                    product_over_rows<D, BF16>(tmem + C::cDK, tmem + C::cDP, smem + C::kQOff + qs * T::kBytes, it > 0);
-                    ptx::tc_commit(bar(C::bQEmpty + qs));
+                    product_over_rows<D, BF16>(tmem + C::cDK, tmem + C::cDP, smem + C::kQOff + q.at * T::kBytes, it > 0);
+                    ptx::tc_commit(bar(C::bQEmpty + q.at));
                 }
                 if (more) {
-                    if (!(alive = issue_dp(use + 1))) break;
+                    if (!(alive = issue_dp(g.next()))) break;
                     if (it + 2 == w.n && ptx::elect_one()) ptx::tc_commit(bar(C::bKVEmpty));
                 }
             }
@@ -365,8 +413,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tS = tmem + lane_base + C::cS + kCols * wg, tDP = tmem + lane_base + C::cDP + kCols * wg;
         const float sl = p.scale_log2;
         uint32_t tiles = 0, use = 0;
+        Place<C::kQ> q;
+        Place<C::kG> g;
         bool alive = true;
-        for (int t = blockIdx.x; t < p.n_tiles && alive; t += gridDim.x) {
+        for (uint32_t k = 0; alive; ++k) {
+            const int t = next_tile(k, ring, sc);
+            if (t < 0) break;
             const KvTile w = kv_tile(t, p);
             const int key = w.k0 + r;
             // queries [see, end) see this key
@@ -378,9 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int all_end = p.window && w.k0 + kBlock > p.sinks
                                     ? (int)min((long long)INT_MAX, (long long)max(w.k0, p.sinks) - p.off + p.window) : INT_MAX;
             int i = w.lo;
-            for (int it = 0; it < w.n; ++it, ++use) {
+            for (int it = 0; it < w.n; ++it, ++use, q = q.next(), g = g.next()) {
                 const int m0 = i * kBlock + kCols * wg;              // this warp's first query
-                const uint32_t qs = use % C::kQ, gs = use % C::kG;
                 float x[kCols];
                 if (ADDITIVE) {
                     // a warp's lanes are neighbouring keys: each load is one line of the mask
@@ -388,12 +439,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < kCols; ++c) x[c] = (key < p.Sk && m0 + c < p.Sq) ? __ldg(at + (size_t)c * p.Sk) : 0.f;
                 }
-                alive = warp_wait(bar(C::bQ + qs), (use / C::kQ) & 1u, sc) && warp_wait(bar(C::bS), use & 1u, sc);
+                alive = warp_wait2(bar(C::bQ + q.at), q.parity(), bar(C::bS), use & 1u, sc);
                 if (!alive) break;
                 ptx::tc_fence_after_sync();
-                const float4* nl = reinterpret_cast<const float4*>(smem_ptr + C::kRowOff + qs * kRowBytes) + kCols / 4 * wg;
+                const float4* nl = reinterpret_cast<const float4*>(smem_ptr + C::kRowOff + q.at * kRowBytes) + kCols / 4 * wg;
                 if (ADDITIVE) {
-                    const float4* is = reinterpret_cast<const float4*>(smem_ptr + C::kSumOff + qs * kRowBytes) + kCols / 4 * wg;
+                    const float4* is = reinterpret_cast<const float4*>(smem_ptr + C::kSumOff + q.at * kRowBytes) + kCols / 4 * wg;
                     float s[kCols];
                     load32(tS, s);
 #pragma unroll
@@ -433,12 +484,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tmem_st_wait();
                 }
                 warp_arrive_tmem(bar(C::bP));
-                if (lane == 0) ptx::mbar_arrive(bar(C::bQEmpty + qs));
+                if (lane == 0) ptx::mbar_arrive(bar(C::bQEmpty + q.at));
                 // ---- dS = P (dP - delta)
-                alive = warp_wait(bar(C::bG + gs), (use / C::kG) & 1u, sc) && warp_wait(bar(C::bDP), use & 1u, sc);
+                alive = warp_wait2(bar(C::bG + g.at), g.parity(), bar(C::bDP), use & 1u, sc);
                 if (!alive) break;
                 ptx::tc_fence_after_sync();
-                const float4* nd = reinterpret_cast<const float4*>(smem_ptr + C::kDeltaOff + gs * kRowBytes) + kCols / 4 * wg;
+                const float4* nd = reinterpret_cast<const float4*>(smem_ptr + C::kDeltaOff + g.at * kRowBytes) + kCols / 4 * wg;
                 {
                     float d[kCols];
                     uint32_t pk[kCols / 2];
@@ -457,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tmem_st_wait();
                 }
                 warp_arrive_tmem(bar(C::bDS));
-                if (lane == 0) ptx::mbar_arrive(bar(C::bGEmpty + gs));
+                if (lane == 0) ptx::mbar_arrive(bar(C::bGEmpty + g.at));
                 if (++i == w.lo + w.per_head) i = w.lo;
             }
             if (!alive) break;
@@ -503,11 +554,13 @@ struct QCfg {
     static constexpr int kQOff = 0, kGOff = T::kBytes, kKOff = 2 * T::kBytes, kVOff = kKOff + kK * T::kBytes;
     static constexpr int kBarOff = kVOff + kV * T::kBytes;
     static constexpr int bQ = 0, bQEmpty = 1, bS = 2, bDP = 4, bDPFree = 5, bDS = 6, bAcc = 8, bAccEmpty = 9, bDrain = 10,
-                         bStall = 11, bParts = 12, bWhole = 13, bK = 14, bKEmpty = bK + kK, bV = bKEmpty + kK, bVEmpty = bV + kV,
+                         bStall = 11, bParts = 12, bWhole = 13, bTile = 14,
+                         bTileEmpty = bTile + kRing, bK = bTileEmpty + kRing, bKEmpty = bK + kK, bV = bKEmpty + kK, bVEmpty = bV + kV,
                          kNumBars = bVEmpty + kV;
     static constexpr int kTmemSlotOff = kBarOff + 8 * kNumBars;
     static constexpr int kAbortOff = kTmemSlotOff + 4;
-    static constexpr int kStatOff = (kAbortOff + 4 + 15) / 16 * 16;      // additive mask: [kGroups][128] {maximum, sum}
+    static constexpr int kTileOff = kAbortOff + 4;
+    static constexpr int kStatOff = (kTileOff + 4 * kRing + 15) / 16 * 16;      // additive mask: [kGroups][128] {maximum, sum}
     static constexpr int kSmemBytes = kStatOff + (ADDITIVE ? kGroups * 128 * 8 : 0);
     static constexpr uint32_t cDQ = 0, cS = 128, cDP = 384;
     static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -559,10 +612,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem_ptr + C::kAbortOff);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_ptr + C::kTmemSlotOff);
     auto bar = [&](int i) { return smem + C::kBarOff + 8u * (uint32_t)i; };
+    const TileRing ring{bar(C::bTile), bar(C::bTileEmpty), reinterpret_cast<volatile int*>(smem_ptr + C::kTileOff)};
 
     if (warp == kLoadWarp && lane == 0) {
         for (int i = 0; i < C::kNumBars; ++i) {
             uint32_t count = 1;
+            if (i >= C::bTileEmpty && i < C::bTileEmpty + kRing) count = kRingReaders;
             if (i == C::bDPFree || i == C::bDS || i == C::bDS + 1 || i == C::bAccEmpty) count = kWarps;
             if (i == C::bParts) count = kWarps - 4;
             if (i == C::bWhole) count = 4;
@@ -590,7 +645,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ loads
         uint32_t tiles = 0, kf = 0, vf = 0;
         bool alive = true;
-        for (int t = blockIdx.x; t < p.n_tiles && alive; t += gridDim.x) {
+        for (uint32_t k = 0; alive; ++k) {
+            const int t = take_tile(k, p, ring, sc);
+            if (t < 0) break;
             const QTile w = q_tile(t, p);
             if (w.n == 0) continue;
             if (tiles > 0 && !warp_wait(bar(C::bQEmpty), (tiles - 1) & 1u, sc)) break;
@@ -665,7 +722,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) ptx::tc_fence_after_sync();
             return ok;
         };
-        for (int t = blockIdx.x; t < p.n_tiles && alive; t += gridDim.x) {
+        for (uint32_t k = 0; alive; ++k) {
+            const int t = next_tile(k, ring, sc);
+            if (t < 0) break;
             const QTile w = q_tile(t, p);
             if (w.n == 0) continue;
             if (!(alive = warp_wait(bar(C::bQ), tiles & 1u, sc))) break;
@@ -713,7 +772,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         float2* stat = reinterpret_cast<float2*>(smem_ptr + C::kStatOff);
         uint32_t tiles = 0, su = 0, dp = 0, seen = 0;
         bool alive = true;
-        for (int t = blockIdx.x; t < p.n_tiles && alive; t += gridDim.x) {
+        for (uint32_t k = 0; alive; ++k) {
+            const int t = next_tile(k, ring, sc);
+            if (t < 0) break;
             const QTile w = q_tile(t, p);
             const int row = w.m0 + r;
             const bool there = row < p.Sq;

@@ -29,6 +29,7 @@ struct BwdParams {
     int off;                        // Sk - Sq: query i sits at position i + off
     int causal, window, sinks;      // window 0: none (causal with it)
     int n_tiles;
+    unsigned int* counter;          // tiles handed out beyond each CTA's first; the statistics' kernel sets it to 0
     int vec8;                       // gradients may be written with 32-byte stores
     int stall;                      // failure-detection test hook, as in the forward kernel
     float scale, scale_log2;
@@ -40,6 +41,7 @@ struct PrepParams {
     const uint16_t *o, *d_o;        // (B, Sq, Hq, D) contiguous
     const float* lse;               // (B, Hq, Sq) or null (additive mask: the dQ kernel finds its own statistics)
     float *neg_lse, *neg_delta;
+    unsigned int* counters;         // [2]
     int B, Hq, Sq, Sp, D;
 };
 

@@ -49,6 +49,7 @@ constexpr int kRows = 4;            // rows of a lane group in flight
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(const PrepParams p) {
     constexpr int kLanes = D / 8;                        // lanes of a row
+    if (blockIdx.x == 0 && threadIdx.x < 2) p.counters[threadIdx.x] = 0u;
     const long long rows = (long long)p.B * p.Sq * p.Hq;
     const int lane = threadIdx.x % kLanes;
     const long long groups = (long long)gridDim.x * (256 / kLanes);
