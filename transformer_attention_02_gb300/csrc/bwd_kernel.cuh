@@ -61,27 +61,54 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
         ptx::tma_load_4d(dst + c * Tile<D>::kBoxBytes, map, bar, c * 64, h, row, b);
 }
 
+// The products below are issued in two halves, `between` in between: the tensor cores' queue is full there, so that a
+// probe of what the next product waits for costs nothing.
+
 // D(tmem) = A B^T of two tiles, summed over the head dimension.
-template <int D, bool BF16>
-__device__ __forceinline__ void product_over_d(uint32_t d, uint32_t a, uint32_t b) {
+template <int D, bool BF16, typename Between>
+__device__ __forceinline__ void product_over_d(uint32_t d, uint32_t a, uint32_t b, Between between) {
     constexpr uint32_t kIdesc = ptx::idesc_f16(kBlock, kBlock, BF16, false, false);
+    constexpr int kSteps = D / 16;
     const uint64_t ad = ptx::sdesc_kmajor_sw128(a), bd = ptx::sdesc_kmajor_sw128(b);
+    auto part = [&](int from, int to) {
+        if (!ptx::elect_one()) return;
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t off = (uint64_t)(((kk >> 2) * Tile<D>::kBoxBytes + (kk & 3) * 32) >> 4);
-        ptx::mma_ss(d, ad + off, bd + off, kIdesc, kk > 0 ? 1u : 0u);
-    }
+        for (int kk = from; kk < to; ++kk) {
+            const uint64_t off = (uint64_t)(((kk >> 2) * Tile<D>::kBoxBytes + (kk & 3) * 32) >> 4);
+            ptx::mma_ss(d, ad + off, bd + off, kIdesc, kk > 0 ? 1u : 0u);
+        }
+    };
+    part(0, kSteps / 2);
+    between();
+    part(kSteps / 2, kSteps);
 }
 
 // D(tmem) (+)= A B, A 128 x 128 in TMEM as the warpgroups leave it: 16-bit pairs, each in the first half of its own columns.
-template <int D, bool BF16>
-__device__ __forceinline__ void product_over_rows(uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
+template <int D, bool BF16, typename Between>
+__device__ __forceinline__ void product_over_rows(uint32_t d, uint32_t a, uint32_t b, bool accumulate, Between between) {
     constexpr uint32_t kIdesc = ptx::idesc_f16(kBlock, D, BF16, false, true);
+    constexpr int kSteps = kBlock / 16;
     const uint64_t bd = ptx::sdesc_mnmajor_sw128(b, Tile<D>::kBoxBytes);
+    auto part = [&](int from, int to) {
+        if (!ptx::elect_one()) return;
 #pragma unroll
-    for (int kk = 0; kk < kBlock / 16; ++kk)
-        ptx::mma_ts(d, a + (uint32_t)((kk >> 1) * kCols + (kk & 1) * 8), bd + (uint64_t)((kk * 16 * 128) >> 4), kIdesc,
-                    (accumulate || kk > 0) ? 1u : 0u);
+        for (int kk = from; kk < to; ++kk)
+            ptx::mma_ts(d, a + (uint32_t)((kk >> 1) * kCols + (kk & 1) * 8), bd + (uint64_t)((kk * 16 * 128) >> 4), kIdesc,
+                        (accumulate || kk > 0) ? 1u : 0u);
+    };
+    part(0, kSteps / 2);
+    between();
+    part(kSteps / 2, kSteps);
+}
+
+// What was issued so far arrives on `bar` when it is done.
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if (ptx::elect_one()) ptx::tc_commit(bar);
+}
+
+// A phase that was seen complete, or is waited for.
+__device__ __forceinline__ bool warp_wait_unless(bool seen, uint32_t bar, uint32_t parity, const SyncCtx& sc) {
+    return __all_sync(0xffffffffu, seen) || warp_wait(bar, parity, sc);
 }
 
 __device__ __forceinline__ void load32(uint32_t taddr, float* x) {
@@ -354,51 +381,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (t < 0) break;
             const KvTile w = kv_tile(t, p);
             if (w.n == 0) continue;
-            auto issue_s = [&](const Place<C::kQ>& at) -> bool {
-                if (!warp_wait(bar(C::bQ + at.at), at.parity(), sc)) return false;
-                ptx::tc_fence_after_sync();
-                if (ptx::elect_one()) {
-                    product_over_d<D, BF16>(tmem + C::cS, smem + C::kKOff, smem + C::kQOff + at.at * T::kBytes);
-                    ptx::tc_commit(bar(C::bS));
-                }
-                return issued = true;
-            };
-            auto issue_dp = [&](const Place<C::kG>& at) -> bool {
-                if (!warp_wait(bar(C::bG + at.at), at.parity(), sc)) return false;
-                ptx::tc_fence_after_sync();
-                if (ptx::elect_one()) {
-                    product_over_d<D, BF16>(tmem + C::cDP, smem + C::kVOff, smem + C::kGOff + at.at * T::kBytes);
-                    ptx::tc_commit(bar(C::bDP));
-                }
-                return true;
-            };
-            alive = warp_wait(bar(C::bK), tiles & 1u, sc) && issue_s(q) && warp_wait(bar(C::bV), tiles & 1u, sc) && issue_dp(g);
-            if (alive && w.n == 1 && ptx::elect_one()) ptx::tc_commit(bar(C::bKVEmpty));
-            for (int it = 0; it < w.n && alive; ++it, ++use, q = q.next(), g = g.next()) {
+            // What the next product waits for, probed while the one before it is issued.
+            bool seen = false;
+            auto probe = [&](uint32_t b, uint32_t parity) { seen = ptx::mbar_test_wait(b, parity); };
+            alive = warp_wait2(bar(C::bK), tiles & 1u, bar(C::bQ + q.at), q.parity(), sc);
+            if (!alive) break;
+            issued = true;
+            ptx::tc_fence_after_sync();
+            product_over_d<D, BF16>(tmem + C::cS, smem + C::kKOff, smem + C::kQOff + q.at * T::kBytes, [] {});
+            commit(bar(C::bS));
+            alive = warp_wait2(bar(C::bV), tiles & 1u, bar(C::bG + g.at), g.parity(), sc);
+            if (!alive) break;
+            ptx::tc_fence_after_sync();
+            product_over_d<D, BF16>(tmem + C::cDP, smem + C::kVOff, smem + C::kGOff + g.at * T::kBytes, [] {});
+            commit(bar(C::bDP));
+            if (w.n == 1) commit(bar(C::bKVEmpty));
+            for (int it = 0; it < w.n; ++it, ++use, q = q.next(), g = g.next()) {
                 const bool more = it + 1 < w.n;
-                alive = warp_wait(bar(C::bP), use & 1u, sc);
+                const Place<C::kQ> q1 = q.next();
+                const Place<C::kG> g1 = g.next();
+                alive = warp_wait_unless(seen, bar(C::bP), use & 1u, sc);
                 // the warps have the last tile's dK and dV
                 if (alive && it == 0 && tiles > 0) alive = warp_wait(bar(C::bAccEmpty), (tiles - 1) & 1u, sc);
                 if (!alive) break;
                 ptx::tc_fence_after_sync();
-                if (ptx::elect_one()) {
-                    product_over_rows<D, BF16>(tmem + C::cDV, tmem + C::cS, smem + C::kGOff + g.at * T::kBytes, it > 0);
-                    ptx::tc_commit(bar(C::bGEmpty + g.at));
-                }
-                if (more && !(alive = issue_s(q.next()))) break;
-                if (!(alive = warp_wait(bar(C::bDS), use & 1u, sc))) break;
-                ptx::tc_fence_after_sync();
-                if (ptx::elect_one()) {
-                    product_over_rows<D, BF16>(tmem + C::cDK, tmem + C::cDP, smem + C::kQOff + q.at * T::kBytes, it > 0);
-                    ptx::tc_commit(bar(C::bQEmpty + q.at));
-                }
+                product_over_rows<D, BF16>(tmem + C::cDV, tmem + C::cS, smem + C::kGOff + g.at * T::kBytes, it > 0,
+                                           [&] { probe(bar(C::bQ + q1.at), q1.parity()); });
+                commit(bar(C::bGEmpty + g.at));
                 if (more) {
-                    if (!(alive = issue_dp(g.next()))) break;
-                    if (it + 2 == w.n && ptx::elect_one()) ptx::tc_commit(bar(C::bKVEmpty));
+                    if (!(alive = warp_wait_unless(seen, bar(C::bQ + q1.at), q1.parity(), sc))) break;
+                    ptx::tc_fence_after_sync();
+                    product_over_d<D, BF16>(tmem + C::cS, smem + C::kKOff, smem + C::kQOff + q1.at * T::kBytes,
+                                            [&] { probe(bar(C::bDS), use & 1u); });
+                    commit(bar(C::bS));
+                } else {
+                    seen = false;
+                }
+                if (!(alive = warp_wait_unless(seen, bar(C::bDS), use & 1u, sc))) break;
+                ptx::tc_fence_after_sync();
+                product_over_rows<D, BF16>(tmem + C::cDK, tmem + C::cDP, smem + C::kQOff + q.at * T::kBytes, it > 0,
+                                           [&] { probe(bar(C::bG + g1.at), g1.parity()); });
+                commit(bar(C::bQEmpty + q.at));
+                if (more) {
+                    if (!(alive = warp_wait_unless(seen, bar(C::bG + g1.at), g1.parity(), sc))) break;
+                    ptx::tc_fence_after_sync();
+                    product_over_d<D, BF16>(tmem + C::cDP, smem + C::kVOff, smem + C::kGOff + g1.at * T::kBytes,
+                                            [&] { probe(bar(C::bP), (use + 1) & 1u); });
+                    commit(bar(C::bDP));
+                    if (it + 2 == w.n) commit(bar(C::bKVEmpty));
                 }
             }
             if (!alive) break;
-            if (ptx::elect_one()) ptx::tc_commit(bar(C::bAcc));
+            commit(bar(C::bAcc));
             ++tiles;
         }
         if (issued) {                                         // TMEM is freed after every product has run
@@ -439,11 +473,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < kCols; ++c) x[c] = (key < p.Sk && m0 + c < p.Sq) ? __ldg(at + (size_t)c * p.Sk) : 0.f;
                 }
-                alive = warp_wait2(bar(C::bQ + q.at), q.parity(), bar(C::bS), use & 1u, sc);
-                if (!alive) break;
-                ptx::tc_fence_after_sync();
+                if (!(alive = warp_wait(bar(C::bQ + q.at), q.parity(), sc))) break;
                 const float4* nl = reinterpret_cast<const float4*>(smem_ptr + C::kRowOff + q.at * kRowBytes) + kCols / 4 * wg;
                 if (ADDITIVE) {
+                    if (!(alive = warp_wait(bar(C::bS), use & 1u, sc))) break;
+                    ptx::tc_fence_after_sync();
                     const float4* is = reinterpret_cast<const float4*>(smem_ptr + C::kSumOff + q.at * kRowBytes) + kCols / 4 * wg;
                     float s[kCols];
                     load32(tS, s);
@@ -459,13 +493,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 } else {
-                    load32(tS, x);
+                    float s[kCols];
 #pragma unroll
                     for (int c = 0; c < kCols; c += 4) {
                         const float4 n = nl[c / 4];
-                        ptx::fma2(x[c], x[c + 1], x[c], x[c + 1], sl, sl, n.x, n.y);
-                        ptx::fma2(x[c + 2], x[c + 3], x[c + 2], x[c + 3], sl, sl, n.z, n.w);
+                        x[c] = n.x, x[c + 1] = n.y, x[c + 2] = n.z, x[c + 3] = n.w;
                     }
+                    if (!(alive = warp_wait(bar(C::bS), use & 1u, sc))) break;
+                    ptx::tc_fence_after_sync();
+                    load32(tS, s);
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 2) ptx::fma2(x[c], x[c + 1], s[c], s[c + 1], sl, sl, x[c], x[c + 1]);
                     const int base = i * kBlock;
                     if (base < all_see || base > all_end - kBlock) {
                         const int c0 = see - m0, c1 = end - m0;
@@ -689,38 +727,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (vf > s) drain_phase(bar(C::bV + s), ((vf - 1 - s) / C::kV) & 1u, sc);
     } else if (warp == kIssueWarp) {
         // --------------------------------------------------------- products
-        // su: S tiles issued, and K tiles whose first use that was; ds: dS (or freed S) tiles taken; dp: dP tiles issued
+        // su, ds, dp: S tiles issued, dS (or freed S) tiles taken, dP tiles issued; ka, kb: the K tiles of the first two, v: V
         uint32_t tiles = 0, su = 0, ds = 0, dp = 0;
+        Place<C::kK> ka, kb;
+        Place<C::kV> v;
         bool alive = true, issued = false;
-        if (p.stall) alive = warp_wait(bar(C::bStall), 0, sc);          // nothing ever arrives
-        auto issue_s = [&]() -> bool {
-            const uint32_t s = su % C::kK;
-            if (!warp_wait(bar(C::bK + s), (su / C::kK) & 1u, sc)) return false;
+        if (p.stall) alive = warp_wait(bar(C::bStall), 0, sc);               // nothing ever arrives
+        // What the next product waits for, probed while the one before it is issued.
+        bool seen = false;
+        auto probe = [&](uint32_t b, uint32_t parity) { seen = ptx::mbar_test_wait(b, parity); };
+        auto issue_s = [&](bool k_seen, auto between) -> bool {
+            if (!warp_wait_unless(k_seen, bar(C::bK + ka.at), ka.parity(), sc)) return false;
             ptx::tc_fence_after_sync();
-            if (ptx::elect_one()) {
-                product_over_d<D, BF16>(tmem + C::cS + 128 * (su & 1u), smem + C::kQOff, smem + C::kKOff + s * T::kBytes);
-                ptx::tc_commit(bar(C::bS + (su & 1u)));
-            }
+            product_over_d<D, BF16>(tmem + C::cS + 128 * (su & 1u), smem + C::kQOff, smem + C::kKOff + ka.at * T::kBytes,
+                                    between);
+            commit(bar(C::bS + (su & 1u)));
             ++su;
+            ka = ka.next();
             return issued = true;
         };
-        auto issue_dp = [&]() -> bool {
-            const uint32_t s = dp % C::kV;
-            if (!warp_wait(bar(C::bV + s), (dp / C::kV) & 1u, sc)) return false;
+        auto issue_dp = [&](bool v_seen, auto between) -> bool {
+            if (!warp_wait_unless(v_seen, bar(C::bV + v.at), v.parity(), sc)) return false;
             if (dp > 0 && !warp_wait(bar(C::bDPFree), (dp - 1) & 1u, sc)) return false;
             ptx::tc_fence_after_sync();
-            if (ptx::elect_one()) {
-                product_over_d<D, BF16>(tmem + C::cDP, smem + C::kGOff, smem + C::kVOff + s * T::kBytes);
-                ptx::tc_commit(bar(C::bDP));
-                ptx::tc_commit(bar(C::bVEmpty + s));
-            }
+            product_over_d<D, BF16>(tmem + C::cDP, smem + C::kGOff, smem + C::kVOff + v.at * T::kBytes, between);
+            commit(bar(C::bDP));
+            commit(bar(C::bVEmpty + v.at));
             ++dp;
+            v = v.next();
             return true;
-        };
-        auto wait_ds = [&]() -> bool {
-            const bool ok = warp_wait(bar(C::bDS + (ds & 1u)), (ds >> 1) & 1u, sc);
-            if (ok) ptx::tc_fence_after_sync();
-            return ok;
         };
         for (uint32_t k = 0; alive; ++k) {
             const int t = next_tile(k, ring, sc);
@@ -730,36 +765,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(alive = warp_wait(bar(C::bQ), tiles & 1u, sc))) break;
             if (ADDITIVE) {
                 // S alone: a buffer is used again once the warps have read it
-                alive = issue_s() && (w.n == 1 || issue_s());
-                for (int j = 0; j < w.n && alive; ++j, ++ds) {
-                    if (!(alive = wait_ds())) break;
-                    if (ptx::elect_one()) ptx::tc_commit(bar(C::bKEmpty + ds % C::kK));
-                    if (j + 2 < w.n) alive = issue_s();
+                alive = issue_s(false, [] {}) && (w.n == 1 || issue_s(false, [] {}));
+                for (int j = 0; j < w.n && alive; ++j, ++ds, kb = kb.next()) {
+                    if (!(alive = warp_wait(bar(C::bDS + (ds & 1u)), (ds >> 1) & 1u, sc))) break;
+                    commit(bar(C::bKEmpty + kb.at));
+                    if (j + 2 < w.n) alive = issue_s(false, [] {});
                 }
             }
-            // (Q and dO are free after S and dP of the last block)
-            alive = alive && issue_s() && issue_dp() && (w.n == 1 || issue_s());
-            if (alive && w.n == 1 && ptx::elect_one()) ptx::tc_commit(bar(C::bQEmpty));
-            for (int j = 0; j < w.n && alive; ++j, ++ds) {
-                if (j + 1 < w.n && !(alive = issue_dp())) break;
-                if (j + 2 == w.n && ptx::elect_one()) ptx::tc_commit(bar(C::bQEmpty));
-                if (!(alive = wait_ds())) break;
+            alive = alive && issue_s(false, [] {}) && issue_dp(false, [] {}) && (w.n == 1 || issue_s(false, [] {}));
+            if (!alive) break;
+            if (w.n == 1) commit(bar(C::bQEmpty));                           // (S and dP of the last block have Q and dO last)
+            bool v_seen = false;
+            for (int j = 0; j < w.n; ++j, ++ds, kb = kb.next()) {
+                const uint32_t ds_bar = bar(C::bDS + (ds & 1u)), ds_parity = (ds >> 1) & 1u;
+                seen = false;
+                if (j + 1 < w.n && !(alive = issue_dp(v_seen, [&] { probe(ds_bar, ds_parity); }))) break;
+                if (j + 2 == w.n) commit(bar(C::bQEmpty));
+                if (!(alive = warp_wait_unless(seen, ds_bar, ds_parity, sc))) break;
                 if (j == 0 && tiles > 0 && !(alive = warp_wait(bar(C::bAccEmpty), (tiles - 1) & 1u, sc))) break;
                 ptx::tc_fence_after_sync();
-                const uint32_t s = ds % C::kK;
-                if (ptx::elect_one()) {
-                    product_over_rows<D, BF16>(tmem + C::cDQ, tmem + C::cS + 128 * (ds & 1u), smem + C::kKOff + s * T::kBytes,
-                                               j > 0);
-                    ptx::tc_commit(bar(C::bKEmpty + s));
+                product_over_rows<D, BF16>(tmem + C::cDQ, tmem + C::cS + 128 * (ds & 1u), smem + C::kKOff + kb.at * T::kBytes,
+                                           j > 0, [&] { probe(bar(C::bK + ka.at), ka.parity()); });
+                commit(bar(C::bKEmpty + kb.at));
+                if (j + 2 < w.n) {
+                    if (!(alive = issue_s(seen, [&] { v_seen = ptx::mbar_test_wait(bar(C::bV + v.at), v.parity()); }))) break;
+                } else {
+                    v_seen = false;
                 }
-                if (j + 2 < w.n) alive = issue_s();
             }
             if (!alive) break;
-            if (ptx::elect_one()) ptx::tc_commit(bar(C::bAcc));
+            commit(bar(C::bAcc));
             ++tiles;
         }
         if (issued) {
-            if (ptx::elect_one()) ptx::tc_commit(bar(C::bDrain));
+            commit(bar(C::bDrain));
             drain_phase(bar(C::bDrain), 0, sc);
         }
         __syncwarp();
