@@ -61,44 +61,55 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
         ptx::tma_load_4d(dst + c * Tile<D>::kBoxBytes, map, bar, c * 64, h, row, b);
 }
 
-// The products below are issued in two halves, `between` in between: the tensor cores' queue is full there, so that a
-// probe of what the next product waits for costs nothing.
+// Products are issued by one lane and in halves. The tensor cores take a product's instructions little faster than they run
+// them, so every cycle between two products is theirs lost: a product's second half and the next one's first go out in one
+// piece of code, and what the next one waits for is probed, and all bookkeeping done, between a product's halves.
 
-// D(tmem) = A B^T of two tiles, summed over the head dimension.
-template <int D, bool BF16, typename Between>
-__device__ __forceinline__ void product_over_d(uint32_t d, uint32_t a, uint32_t b, Between between) {
+// Half of D(tmem) = A B^T of two tiles, summed over the head dimension.
+template <int D, bool BF16>
+__device__ __forceinline__ void half_over_d(int half, uint32_t d, uint32_t a, uint32_t b) {
     constexpr uint32_t kIdesc = ptx::idesc_f16(kBlock, kBlock, BF16, false, false);
-    constexpr int kSteps = D / 16;
+    constexpr int kSteps = D / 32;
     const uint64_t ad = ptx::sdesc_kmajor_sw128(a), bd = ptx::sdesc_kmajor_sw128(b);
-    auto part = [&](int from, int to) {
-        if (!ptx::elect_one()) return;
 #pragma unroll
-        for (int kk = from; kk < to; ++kk) {
-            const uint64_t off = (uint64_t)(((kk >> 2) * Tile<D>::kBoxBytes + (kk & 3) * 32) >> 4);
-            ptx::mma_ss(d, ad + off, bd + off, kIdesc, kk > 0 ? 1u : 0u);
-        }
-    };
-    part(0, kSteps / 2);
-    between();
-    part(kSteps / 2, kSteps);
+    for (int i = 0; i < kSteps; ++i) {
+        const int kk = half * kSteps + i;
+        const uint64_t off = (uint64_t)(((kk >> 2) * Tile<D>::kBoxBytes + (kk & 3) * 32) >> 4);
+        ptx::mma_ss(d, ad + off, bd + off, kIdesc, kk > 0 ? 1u : 0u);
+    }
 }
 
-// D(tmem) (+)= A B, A 128 x 128 in TMEM as the warpgroups leave it: 16-bit pairs, each in the first half of its own columns.
-template <int D, bool BF16, typename Between>
-__device__ __forceinline__ void product_over_rows(uint32_t d, uint32_t a, uint32_t b, bool accumulate, Between between) {
+// Half of D(tmem) (+)= A B, A 128 x 128 in TMEM as the warpgroups leave it: 16-bit pairs, each in the first half of its own
+// columns.
+template <int D, bool BF16>
+__device__ __forceinline__ void half_over_rows(int half, uint32_t d, uint32_t a, uint32_t b, bool accumulate) {
     constexpr uint32_t kIdesc = ptx::idesc_f16(kBlock, D, BF16, false, true);
-    constexpr int kSteps = kBlock / 16;
+    constexpr int kSteps = kBlock / 32;
     const uint64_t bd = ptx::sdesc_mnmajor_sw128(b, Tile<D>::kBoxBytes);
-    auto part = [&](int from, int to) {
-        if (!ptx::elect_one()) return;
 #pragma unroll
-        for (int kk = from; kk < to; ++kk)
-            ptx::mma_ts(d, a + (uint32_t)((kk >> 1) * kCols + (kk & 1) * 8), bd + (uint64_t)((kk * 16 * 128) >> 4), kIdesc,
-                        (accumulate || kk > 0) ? 1u : 0u);
-    };
-    part(0, kSteps / 2);
-    between();
-    part(kSteps / 2, kSteps);
+    for (int i = 0; i < kSteps; ++i) {
+        const int kk = half * kSteps + i;
+        ptx::mma_ts(d, a + (uint32_t)((kk >> 1) * kCols + (kk & 1) * 8), bd + (uint64_t)((kk * 16 * 128) >> 4), kIdesc,
+                    (accumulate || kk > 0) ? 1u : 0u);
+    }
+}
+
+// The rest of one product and the beginning of the next, which is free to go (`seen`, the same in all lanes) or waits first.
+template <typename Wait, typename Tail, typename Head>
+__device__ __forceinline__ bool follow(bool seen, Wait wait, Tail tail, Head head) {
+    if (seen) {
+        ptx::tc_fence_after_sync();
+        if (ptx::elect_one()) {
+            tail();
+            head();
+        }
+        return true;
+    }
+    if (ptx::elect_one()) tail();
+    if (!wait()) return false;
+    ptx::tc_fence_after_sync();
+    if (ptx::elect_one()) head();
+    return true;
 }
 
 // What was issued so far arrives on `bar` when it is done.
@@ -106,9 +117,13 @@ __device__ __forceinline__ void commit(uint32_t bar) {
     if (ptx::elect_one()) ptx::tc_commit(bar);
 }
 
-// A phase that was seen complete, or is waited for.
-__device__ __forceinline__ bool warp_wait_unless(bool seen, uint32_t bar, uint32_t parity, const SyncCtx& sc) {
-    return __all_sync(0xffffffffu, seen) || warp_wait(bar, parity, sc);
+// Whether two phases are complete.
+__device__ __forceinline__ bool warp_test2(uint32_t bar_a, uint32_t parity_a, uint32_t bar_b, uint32_t parity_b) {
+    const bool a = ptx::mbar_test_wait(bar_a, parity_a), b = ptx::mbar_test_wait(bar_b, parity_b);
+    return __all_sync(0xffffffffu, a && b);
+}
+__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, ptx::mbar_test_wait(bar, parity));
 }
 
 __device__ __forceinline__ void load32(uint32_t taddr, float* x) {
@@ -142,29 +157,27 @@ __device__ __forceinline__ void warp_arrive_tmem(uint32_t bar) {
     warp_arrive(bar);
 }
 
-// N accumulated values of a row, times `factor`, to 16 bits in device memory. `freed`: a barrier to arrive on once they
-// are in registers.
+// N accumulated values of a row, times `factor`, to 16 bits in device memory. `freed`: a barrier to arrive on once the last
+// of them are in registers.
 template <int N, bool BF16>
 __device__ __forceinline__ void store_row(uint32_t taddr, uint32_t freed, uint16_t* row, float factor, bool there, bool vec8) {
-    uint32_t v[N];
 #pragma unroll
-    for (int c = 0; c < N; c += 32) ptx::tmem_ld32(taddr + c, v + c);
-    ptx::tmem_ld_wait();
+    for (int c = 0; c < N; c += 32) {
+        float v[32];
+        uint32_t w[16];
+        load32(taddr + c, v);
+        if (c + 32 >= N) warp_arrive_tmem(freed);
 #pragma unroll
-    for (int c = 0; c < N; c += 32) ptx::reg_fence32(v + c);
-    warp_arrive_tmem(freed);
-    if (!there) return;
+        for (int i = 0; i < 16; ++i) w[i] = pack<BF16>(v[2 * i] * factor, v[2 * i + 1] * factor);
+        if (there) {
+            if (vec8) {
+                ptx::st_global_v8(row + c, w);
+                ptx::st_global_v8(row + c + 16, w + 8);
+            } else {
+                uint4* dst = reinterpret_cast<uint4*>(row + c);
 #pragma unroll
-    for (int c = 0; c < N; c += 16) {
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            w[i] = pack<BF16>(__uint_as_float(v[c + 2 * i]) * factor, __uint_as_float(v[c + 2 * i + 1]) * factor);
-        if (vec8) {
-            ptx::st_global_v8(row + c, w);
-        } else {
-            reinterpret_cast<uint4*>(row + c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            reinterpret_cast<uint4*>(row + c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            }
         }
     }
 }
@@ -240,8 +253,8 @@ struct KvCfg {
     static constexpr int kDeltaOff = kRowOff + kQ * (int)kRowBytes;
     static constexpr int kSumOff = kDeltaOff + kG * (int)kRowBytes;
     static constexpr int kBarOff = kSumOff + (ADDITIVE ? kQ * (int)kRowBytes : 0);
-    static constexpr int bK = 0, bV = 1, bKVEmpty = 2, bP = 3, bDS = 4, bAcc = 5, bAccEmpty = 6, bDrain = 7, bStall = 8,
-                         bS = 9, bDP = 10, bTile = 11, bTileEmpty = bTile + kRing, bQ = bTileEmpty + kRing, bQEmpty = bQ + kQ,
+    static constexpr int bK = 0, bV = 1, bKEmpty = 2, bVEmpty = 3, bP = 4, bDS = 5, bAcc = 6, bAccEmpty = 7, bDrain = 8,
+                         bStall = 9, bS = 10, bDP = 11, bTile = 12, bTileEmpty = bTile + kRing, bQ = bTileEmpty + kRing, bQEmpty = bQ + kQ,
                          bG = bQEmpty + kQ, bGEmpty = bG + kG, kNumBars = bGEmpty + kG;
     static constexpr int kTmemSlotOff = kBarOff + 8 * kNumBars;
     static constexpr int kAbortOff = kTmemSlotOff + 4;
@@ -286,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
         return;
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // (known to be uniform)
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem_ptr + C::kAbortOff);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_ptr + C::kTmemSlotOff);
     auto bar = [&](int i) { return smem + C::kBarOff + 8u * (uint32_t)i; };
@@ -321,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
-        uint32_t tiles = 0, fills = 0;                         // tiles with work, blocks
+        uint32_t tiles = 0, v_fills = 0, fills = 0;            // K and V tiles, blocks
         Place<C::kQ> q;
         Place<C::kG> g;
         bool alive = true;
@@ -330,12 +343,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (t < 0) break;
             const KvTile w = kv_tile(t, p);
             if (w.n == 0) continue;
-            if (tiles > 0 && !warp_wait(bar(C::bKVEmpty), (tiles - 1) & 1u, sc)) break;
+            if (tiles > 0 && !warp_wait(bar(C::bKEmpty), (tiles - 1) & 1u, sc)) break;
             if (lane == 0) {
                 ptx::mbar_arrive_expect_tx(bar(C::bK), T::kBytes);
                 load_tile<D>(smem + C::kKOff, &tmK, bar(C::bK), w.hk, w.k0, w.b);
-                ptx::mbar_arrive_expect_tx(bar(C::bV), T::kBytes);
-                load_tile<D>(smem + C::kVOff, &tmV, bar(C::bV), w.hk, w.k0, w.b);
             }
             ++tiles;
             int h = w.hk * p.group, i = w.lo;
@@ -354,6 +365,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     load_tile<D>(smem + C::kGOff + g.at * T::kBytes, &tmG, bar(C::bG + g.at), h, i * kBlock, w.b);
                     ptx::bulk_load(smem + C::kDeltaOff + g.at * kRowBytes, p.neg_delta + row, kRowBytes, bar(C::bG + g.at));
                 }
+                if (it == 0) {
+                    if (v_fills > 0 && !(alive = warp_wait(bar(C::bVEmpty), (v_fills - 1) & 1u, sc))) {
+                        ++fills;
+                        break;
+                    }
+                    if (lane == 0) {
+                        ptx::mbar_arrive_expect_tx(bar(C::bV), T::kBytes);
+                        load_tile<D>(smem + C::kVOff, &tmV, bar(C::bV), w.hk, w.k0, w.b);
+                    }
+                    ++v_fills;
+                }
                 if (++i == w.lo + w.per_head) {
                     i = w.lo;
                     ++h;
@@ -361,79 +383,115 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         // Shut down: every copy has landed.
-        if (tiles > 0) {
-            drain_phase(bar(C::bK), (tiles - 1) & 1u, sc);
-            drain_phase(bar(C::bV), (tiles - 1) & 1u, sc);
-        }
+        if (tiles > 0) drain_phase(bar(C::bK), (tiles - 1) & 1u, sc);
+        if (v_fills > 0) drain_phase(bar(C::bV), (v_fills - 1) & 1u, sc);
         for (uint32_t s = 0; s < (uint32_t)C::kQ; ++s)
             if (fills > s) drain_phase(bar(C::bQ + s), ((fills - 1 - s) / C::kQ) & 1u, sc);
         for (uint32_t s = 0; s < (uint32_t)C::kG; ++s)
             if (fills > s) drain_phase(bar(C::bG + s), ((fills - 1 - s) / C::kG) & 1u, sc);
     } else if (warp == kIssueWarp) {
         // --------------------------------------------------------- products
-        uint32_t tiles = 0, use = 0;
+        // One walk over the blocks of all tiles: a tile's first S and dP are issued before the last tile's last dK.
+        uint32_t k = 0, tiles = 0, use = 0;                   // ring entries, tiles with work, blocks
         Place<C::kQ> q;
         Place<C::kG> g;
         bool alive = true, issued = false;
-        if (p.stall) alive = warp_wait(bar(C::bStall), 0, sc);               // nothing ever arrives
-        for (uint32_t k = 0; alive; ++k) {
-            const int t = next_tile(k, ring, sc);
-            if (t < 0) break;
-            const KvTile w = kv_tile(t, p);
-            if (w.n == 0) continue;
-            // What the next product waits for, probed while the one before it is issued.
-            bool seen = false;
-            auto probe = [&](uint32_t b, uint32_t parity) { seen = ptx::mbar_test_wait(b, parity); };
-            alive = warp_wait2(bar(C::bK), tiles & 1u, bar(C::bQ + q.at), q.parity(), sc);
-            if (!alive) break;
-            issued = true;
-            ptx::tc_fence_after_sync();
-            product_over_d<D, BF16>(tmem + C::cS, smem + C::kKOff, smem + C::kQOff + q.at * T::kBytes, [] {});
-            commit(bar(C::bS));
-            alive = warp_wait2(bar(C::bV), tiles & 1u, bar(C::bG + g.at), g.parity(), sc);
-            if (!alive) break;
-            ptx::tc_fence_after_sync();
-            product_over_d<D, BF16>(tmem + C::cDP, smem + C::kVOff, smem + C::kGOff + g.at * T::kBytes, [] {});
-            commit(bar(C::bDP));
-            if (w.n == 1) commit(bar(C::bKVEmpty));
-            for (int it = 0; it < w.n; ++it, ++use, q = q.next(), g = g.next()) {
-                const bool more = it + 1 < w.n;
-                const Place<C::kQ> q1 = q.next();
-                const Place<C::kG> g1 = g.next();
-                alive = warp_wait_unless(seen, bar(C::bP), use & 1u, sc);
-                // the warps have the last tile's dK and dV
-                if (alive && it == 0 && tiles > 0) alive = warp_wait(bar(C::bAccEmpty), (tiles - 1) & 1u, sc);
-                if (!alive) break;
-                ptx::tc_fence_after_sync();
-                product_over_rows<D, BF16>(tmem + C::cDV, tmem + C::cS, smem + C::kGOff + g.at * T::kBytes, it > 0,
-                                           [&] { probe(bar(C::bQ + q1.at), q1.parity()); });
-                commit(bar(C::bGEmpty + g.at));
-                if (more) {
-                    if (!(alive = warp_wait_unless(seen, bar(C::bQ + q1.at), q1.parity(), sc))) break;
-                    ptx::tc_fence_after_sync();
-                    product_over_d<D, BF16>(tmem + C::cS, smem + C::kKOff, smem + C::kQOff + q1.at * T::kBytes,
-                                            [&] { probe(bar(C::bDS), use & 1u); });
-                    commit(bar(C::bS));
-                } else {
-                    seen = false;
-                }
-                if (!(alive = warp_wait_unless(seen, bar(C::bDS), use & 1u, sc))) break;
-                ptx::tc_fence_after_sync();
-                product_over_rows<D, BF16>(tmem + C::cDK, tmem + C::cDP, smem + C::kQOff + q.at * T::kBytes, it > 0,
-                                           [&] { probe(bar(C::bG + g1.at), g1.parity()); });
-                commit(bar(C::bQEmpty + q.at));
-                if (more) {
-                    if (!(alive = warp_wait_unless(seen, bar(C::bG + g1.at), g1.parity(), sc))) break;
-                    ptx::tc_fence_after_sync();
-                    product_over_d<D, BF16>(tmem + C::cDP, smem + C::kVOff, smem + C::kGOff + g1.at * T::kBytes,
-                                            [&] { probe(bar(C::bP), (use + 1) & 1u); });
-                    commit(bar(C::bDP));
-                    if (it + 2 == w.n) commit(bar(C::bKVEmpty));
-                }
+        // Blocks of the next tile with work; 0: there is none.
+        auto next_work = [&]() -> int {
+            for (;;) {
+                const int t = next_tile(k++, ring, sc);
+                if (t < 0) return 0;
+                const int n = kv_tile(t, p).n;
+                if (n > 0) return n;
             }
+        };
+        auto s_half = [&](int half, uint32_t at) {
+            half_over_d<D, BF16>(half, tmem + C::cS, smem + C::kKOff, smem + C::kQOff + at * T::kBytes);
+        };
+        auto dp_half = [&](int half, uint32_t at) {
+            half_over_d<D, BF16>(half, tmem + C::cDP, smem + C::kVOff, smem + C::kGOff + at * T::kBytes);
+        };
+        if (p.stall) alive = warp_wait(bar(C::bStall), 0, sc);               // nothing ever arrives
+        int n = alive ? next_work() : 0, it = 0;
+        if (n > 0) {
+            alive = warp_wait2(bar(C::bK), 0, bar(C::bQ + q.at), q.parity(), sc);
+            if (alive) {
+                issued = true;
+                ptx::tc_fence_after_sync();
+                if (ptx::elect_one()) {
+                    s_half(0, q.at);
+                    s_half(1, q.at);
+                    ptx::tc_commit(bar(C::bS));
+                    if (n == 1) ptx::tc_commit(bar(C::bKEmpty));
+                }
+                alive = warp_wait2(bar(C::bV), 0, bar(C::bG + g.at), g.parity(), sc);
+            }
+            if (alive) {
+                ptx::tc_fence_after_sync();
+                if (ptx::elect_one()) dp_half(0, g.at);
+            }
+        }
+        while (alive && n > 0) {
+            // (dP of this block is half issued)
+            const bool last = it + 1 == n, drained = it > 0 || tiles == 0;
+            const uint32_t acc_parity = (tiles - 1) & 1u;     // the warps have the last tile's dK and dV
+            alive = follow(
+                drained ? warp_test(bar(C::bP), use & 1u)
+                        : warp_test2(bar(C::bP), use & 1u, bar(C::bAccEmpty), acc_parity),
+                [&] { return warp_wait(bar(C::bP), use & 1u, sc) && (drained || warp_wait(bar(C::bAccEmpty), acc_parity, sc)); },
+                [&] {
+                    dp_half(1, g.at);
+                    ptx::tc_commit(bar(C::bDP));
+                    if (last) ptx::tc_commit(bar(C::bVEmpty));
+                },
+                [&] { half_over_rows<D, BF16>(0, tmem + C::cDV, tmem + C::cS, smem + C::kGOff + g.at * T::kBytes, it > 0); });
             if (!alive) break;
-            commit(bar(C::bAcc));
-            ++tiles;
+            auto dv_rest = [&] {
+                half_over_rows<D, BF16>(1, tmem + C::cDV, tmem + C::cS, smem + C::kGOff + g.at * T::kBytes, true);
+                ptx::tc_commit(bar(C::bGEmpty + g.at));
+            };
+            auto dk_begin = [&] {
+                half_over_rows<D, BF16>(0, tmem + C::cDK, tmem + C::cDP, smem + C::kQOff + q.at * T::kBytes, it > 0);
+            };
+            auto dk_rest = [&] {
+                half_over_rows<D, BF16>(1, tmem + C::cDK, tmem + C::cDP, smem + C::kQOff + q.at * T::kBytes, true);
+                ptx::tc_commit(bar(C::bQEmpty + q.at));
+                if (last) ptx::tc_commit(bar(C::bAcc));
+            };
+            auto wait_ds = [&] { return warp_wait(bar(C::bDS), use & 1u, sc); };
+            // the block after this one: number i1 of n1 of its tile
+            const Place<C::kQ> q1 = q.next();
+            const Place<C::kG> g1 = g.next();
+            const int n1 = last ? next_work() : n, i1 = last ? 0 : it + 1;
+            if (n1 == 0) {
+                alive = follow(false, wait_ds, dv_rest, [&] { dk_begin(); dk_rest(); });
+                break;
+            }
+            const uint32_t kv_parity = (tiles + 1) & 1u;      // of a new tile's K and V
+            alive = follow(
+                last ? warp_test2(bar(C::bQ + q1.at), q1.parity(), bar(C::bK), kv_parity) : warp_test(bar(C::bQ + q1.at), q1.parity()),
+                [&] { return warp_wait(bar(C::bQ + q1.at), q1.parity(), sc) && (!last || warp_wait(bar(C::bK), kv_parity, sc)); },
+                dv_rest, [&] { s_half(0, q1.at); });
+            if (!alive) break;
+            alive = follow(
+                warp_test(bar(C::bDS), use & 1u), wait_ds,
+                [&] {
+                    s_half(1, q1.at);
+                    ptx::tc_commit(bar(C::bS));
+                    if (i1 + 1 == n1) ptx::tc_commit(bar(C::bKEmpty));
+                },
+                dk_begin);
+            if (!alive) break;
+            alive = follow(
+                last ? warp_test2(bar(C::bG + g1.at), g1.parity(), bar(C::bV), kv_parity) : warp_test(bar(C::bG + g1.at), g1.parity()),
+                [&] { return warp_wait(bar(C::bG + g1.at), g1.parity(), sc) && (!last || warp_wait(bar(C::bV), kv_parity, sc)); },
+                dk_rest, [&] { dp_half(0, g1.at); });
+            tiles += last;
+            n = n1;
+            it = i1;
+            ++use;
+            q = q1;
+            g = g1;
         }
         if (issued) {                                         // TMEM is freed after every product has run
             if (ptx::elect_one()) ptx::tc_commit(bar(C::bDrain));
@@ -450,6 +508,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         Place<C::kQ> q;
         Place<C::kG> g;
         bool alive = true;
+        // Two warpgroups write dV, two dK, each half of the row: of the tile before, once the first P of the next one is done
+        const bool is_k = wg >= 2;
+        const int col = (wg & 1) * (D / 2);
+        uint16_t* done_row = nullptr;
+        bool done_there = false;
+        auto finish = [&]() -> bool {
+            if (!done_row) return true;
+            if (!warp_wait(bar(C::bAcc), tiles & 1u, sc)) return false;
+            ptx::tc_fence_after_sync();
+            store_row<D / 2, BF16>(tmem + lane_base + (is_k ? C::cDK : C::cDV) + col, bar(C::bAccEmpty), done_row,
+                                   is_k ? p.scale : 1.f, done_there, p.vec8);
+            done_row = nullptr;
+            ++tiles;
+            return true;
+        };
         for (uint32_t k = 0; alive; ++k) {
             const int t = next_tile(k, ring, sc);
             if (t < 0) break;
@@ -523,6 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 warp_arrive_tmem(bar(C::bP));
                 if (lane == 0) ptx::mbar_arrive(bar(C::bQEmpty + q.at));
+                if (it == 0 && !(alive = finish())) break;
                 // ---- dS = P (dP - delta)
                 alive = warp_wait2(bar(C::bG + g.at), g.parity(), bar(C::bDP), use & 1u, sc);
                 if (!alive) break;
@@ -550,21 +624,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (++i == w.lo + w.per_head) i = w.lo;
             }
             if (!alive) break;
-            // ---- two warpgroups write dV, two dK, each half of the row
-            const bool is_k = wg >= 2;
-            const int col = (wg & 1) * (D / 2);
             uint16_t* row = static_cast<uint16_t*>(is_k ? p.dk : p.dv) +
                             ((long long)w.b * p.Sk + key) * (is_k ? p.dk_stride : p.dv_stride) + w.hk * D + col;
             if (w.n == 0) {
                 zero_row<D / 2>(row, key < p.Sk);
-                continue;
+            } else {
+                done_row = row;
+                done_there = key < p.Sk;
             }
-            if (!(alive = warp_wait(bar(C::bAcc), tiles & 1u, sc))) break;
-            ptx::tc_fence_after_sync();
-            store_row<D / 2, BF16>(tmem + lane_base + (is_k ? C::cDK : C::cDV) + col, bar(C::bAccEmpty), row,
-                                   is_k ? p.scale : 1.f, key < p.Sk, p.vec8);
-            ++tiles;
         }
+        if (alive) finish();
     }
 
     ptx::tc_fence_before_sync();
@@ -592,7 +661,7 @@ struct QCfg {
     static constexpr int kQOff = 0, kGOff = T::kBytes, kKOff = 2 * T::kBytes, kVOff = kKOff + kK * T::kBytes;
     static constexpr int kBarOff = kVOff + kV * T::kBytes;
     static constexpr int bQ = 0, bQEmpty = 1, bS = 2, bDP = 4, bDPFree = 5, bDS = 6, bAcc = 8, bAccEmpty = 9, bDrain = 10,
-                         bStall = 11, bParts = 12, bWhole = 13, bTile = 14,
+                         bStall = 11, bParts = 12, bWhole = 13, bG = 14, bGEmpty = 15, bTile = 16,
                          bTileEmpty = bTile + kRing, bK = bTileEmpty + kRing, bKEmpty = bK + kK, bV = bKEmpty + kK, bVEmpty = bV + kV,
                          kNumBars = bVEmpty + kV;
     static constexpr int kTmemSlotOff = kBarOff + 8 * kNumBars;
@@ -646,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
         return;
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // (known to be uniform)
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem_ptr + C::kAbortOff);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_ptr + C::kTmemSlotOff);
     auto bar = [&](int i) { return smem + C::kBarOff + 8u * (uint32_t)i; };
@@ -681,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
-        uint32_t tiles = 0, kf = 0, vf = 0;
+        uint32_t tiles = 0, g_fills = 0, kf = 0, vf = 0;
         bool alive = true;
         for (uint32_t k = 0; alive; ++k) {
             const int t = take_tile(k, p, ring, sc);
@@ -690,11 +759,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (w.n == 0) continue;
             if (tiles > 0 && !warp_wait(bar(C::bQEmpty), (tiles - 1) & 1u, sc)) break;
             if (lane == 0) {
-                ptx::mbar_arrive_expect_tx(bar(C::bQ), 2 * T::kBytes);
+                ptx::mbar_arrive_expect_tx(bar(C::bQ), T::kBytes);
                 load_tile<D>(smem + C::kQOff, &tmQ, bar(C::bQ), w.h, w.m0, w.b);
-                load_tile<D>(smem + C::kGOff, &tmG, bar(C::bQ), w.h, w.m0, w.b);
             }
             ++tiles;
+            auto load_g = [&]() -> bool {
+                if (g_fills > 0 && !warp_wait(bar(C::bGEmpty), (g_fills - 1) & 1u, sc)) return false;
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(bar(C::bG), T::kBytes);
+                    load_tile<D>(smem + C::kGOff, &tmG, bar(C::bG), w.h, w.m0, w.b);
+                }
+                ++g_fills;
+                return true;
+            };
             auto load_k = [&](int j) -> bool {
                 const uint32_t s = kf % C::kK;
                 if (kf >= (uint32_t)C::kK && !warp_wait(bar(C::bKEmpty + s), (kf / C::kK - 1) & 1u, sc)) return false;
@@ -717,86 +794,155 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             if (ADDITIVE)
                 for (int j = 0; j < w.n && alive; ++j) alive = load_k(j);
-            // in the order in which the products take them: K_0, V_0, K_1, V_1, ...
-            for (int j = 0; j < w.n && alive; ++j) alive = load_k(j) && load_v(j);
+            // in the order in which the products take them: K_0, dO, V_0, K_1, V_1, ...
+            for (int j = 0; j < w.n && alive; ++j) alive = load_k(j) && (j > 0 || load_g()) && load_v(j);
         }
         if (tiles > 0) drain_phase(bar(C::bQ), (tiles - 1) & 1u, sc);
+        if (g_fills > 0) drain_phase(bar(C::bG), (g_fills - 1) & 1u, sc);
         for (uint32_t s = 0; s < (uint32_t)C::kK; ++s)
             if (kf > s) drain_phase(bar(C::bK + s), ((kf - 1 - s) / C::kK) & 1u, sc);
         for (uint32_t s = 0; s < (uint32_t)C::kV; ++s)
             if (vf > s) drain_phase(bar(C::bV + s), ((vf - 1 - s) / C::kV) & 1u, sc);
     } else if (warp == kIssueWarp) {
         // --------------------------------------------------------- products
-        // su, ds, dp: S tiles issued, dS (or freed S) tiles taken, dP tiles issued; ka, kb: the K tiles of the first two, v: V
-        uint32_t tiles = 0, su = 0, ds = 0, dp = 0;
-        Place<C::kK> ka, kb;
+        // One walk over the blocks of all tiles (with an additive mask each tile's keys come twice, the first time for S
+        // alone), with three places in it: dQ, dP one block ahead, S two blocks ahead. A place is a tile's number, the
+        // block and the number of blocks; lane t % 32 keeps that of tile t for the places behind the first.
+        struct At {
+            uint32_t tile = 0;
+            int j = 0, n = 0;
+        };
+        constexpr int kWalks = ADDITIVE ? 2 : 1;
+        uint32_t k = 0, su = 0, ds = 0, dp = 0;               // ring entries, S issued, dS (or freed S) taken, dP issued
+        At at_s, at_dp, at_dq;
+        Place<C::kK> ka, kb;                                  // K of S, of dQ
         Place<C::kV> v;
         bool alive = true, issued = false;
-        if (p.stall) alive = warp_wait(bar(C::bStall), 0, sc);               // nothing ever arrives
-        // What the next product waits for, probed while the one before it is issued.
-        bool seen = false;
-        auto probe = [&](uint32_t b, uint32_t parity) { seen = ptx::mbar_test_wait(b, parity); };
-        auto issue_s = [&](bool k_seen, auto between) -> bool {
-            if (!warp_wait_unless(k_seen, bar(C::bK + ka.at), ka.parity(), sc)) return false;
-            ptx::tc_fence_after_sync();
-            product_over_d<D, BF16>(tmem + C::cS + 128 * (su & 1u), smem + C::kQOff, smem + C::kKOff + ka.at * T::kBytes,
-                                    between);
-            commit(bar(C::bS + (su & 1u)));
+        int kept = 0;
+        auto next_work = [&]() {                              // at_s: the next tile with work, n = 0 behind the last
+            at_s.n = 0;
+            for (int t; at_s.n == 0 && (t = next_tile(k, ring, sc)) >= 0; ++k) at_s.n = kWalks * q_tile(t, p).n;
+            at_s.j = 0;
+            if (lane == (int)(at_s.tile & 31u)) kept = at_s.n;
+        };
+        auto go_on = [&](At& a) {
+            if (++a.j < a.n) return;
+            ++a.tile;
+            a.j = 0;
+            a.n = __shfl_sync(0xffffffffu, kept, (int)(a.tile & 31u));
+        };
+        // Second halves of the products that are half issued: of S (s_open), with its buffers and what follows it, of dP, dQ
+        bool s_open = false, s_ends = false, dp_open = false, dp_ends = false, dq_open = false, dq_ends = false;
+        uint32_t s_tile = 0, s_buf = 0, dp_tile = 0, dq_tile = 0, dq_buf = 0;
+        auto rest = [&] {
+            if (s_open) {
+                half_over_d<D, BF16>(1, tmem + C::cS + 128 * s_buf, smem + C::kQOff, smem + C::kKOff + s_tile * T::kBytes);
+                ptx::tc_commit(bar(C::bS + s_buf));
+                if (s_ends) ptx::tc_commit(bar(C::bQEmpty));
+            }
+            if (dp_open) {
+                half_over_d<D, BF16>(1, tmem + C::cDP, smem + C::kGOff, smem + C::kVOff + dp_tile * T::kBytes);
+                ptx::tc_commit(bar(C::bDP));
+                ptx::tc_commit(bar(C::bVEmpty + dp_tile));
+                if (dp_ends) ptx::tc_commit(bar(C::bGEmpty));
+            }
+            if (dq_open) {
+                half_over_rows<D, BF16>(1, tmem + C::cDQ, tmem + C::cS + 128 * dq_buf, smem + C::kKOff + dq_tile * T::kBytes, true);
+                ptx::tc_commit(bar(C::bKEmpty + dq_tile));
+                if (dq_ends) ptx::tc_commit(bar(C::bAcc));
+            }
+        };
+        auto close = [&] { s_open = dp_open = dq_open = false; };
+        auto begin_s = [&]() -> bool {
+            const uint32_t b = bar(C::bK + ka.at), par = ka.parity(), qb = bar(C::bQ), qpar = at_s.tile & 1u;
+            const bool first = at_s.j == 0;
+            if (!follow(
+                    first ? warp_test2(b, par, qb, qpar) : warp_test(b, par),
+                    [&] { return warp_wait(b, par, sc) && (!first || warp_wait(qb, qpar, sc)); }, rest,
+                    [&] {
+                        half_over_d<D, BF16>(0, tmem + C::cS + 128 * (su & 1u), smem + C::kQOff, smem + C::kKOff + ka.at * T::kBytes);
+                    }))
+                return false;
+            close();
+            s_open = issued = true;
+            s_tile = ka.at;
+            s_buf = su & 1u;
+            s_ends = at_s.j + 1 == at_s.n;
             ++su;
             ka = ka.next();
-            return issued = true;
-        };
-        auto issue_dp = [&](bool v_seen, auto between) -> bool {
-            if (!warp_wait_unless(v_seen, bar(C::bV + v.at), v.parity(), sc)) return false;
-            if (dp > 0 && !warp_wait(bar(C::bDPFree), (dp - 1) & 1u, sc)) return false;
-            ptx::tc_fence_after_sync();
-            product_over_d<D, BF16>(tmem + C::cDP, smem + C::kGOff, smem + C::kVOff + v.at * T::kBytes, between);
-            commit(bar(C::bDP));
-            commit(bar(C::bVEmpty + v.at));
-            ++dp;
-            v = v.next();
+            if (s_ends) {
+                // the loads of a further tile wait for this product, whose end may wait for nothing then
+                if (ptx::elect_one()) rest();
+                close();
+                ++at_s.tile;
+                next_work();
+            } else {
+                ++at_s.j;
+            }
             return true;
         };
-        for (uint32_t k = 0; alive; ++k) {
-            const int t = next_tile(k, ring, sc);
-            if (t < 0) break;
-            const QTile w = q_tile(t, p);
-            if (w.n == 0) continue;
-            if (!(alive = warp_wait(bar(C::bQ), tiles & 1u, sc))) break;
-            if (ADDITIVE) {
-                // S alone: a buffer is used again once the warps have read it
-                alive = issue_s(false, [] {}) && (w.n == 1 || issue_s(false, [] {}));
-                for (int j = 0; j < w.n && alive; ++j, ++ds, kb = kb.next()) {
-                    if (!(alive = warp_wait(bar(C::bDS + (ds & 1u)), (ds >> 1) & 1u, sc))) break;
-                    commit(bar(C::bKEmpty + kb.at));
-                    if (j + 2 < w.n) alive = issue_s(false, [] {});
-                }
+        auto begin_dp = [&]() -> bool {
+            if (!ADDITIVE || 2 * at_dp.j >= at_dp.n) {
+                const uint32_t b = bar(C::bV + v.at), par = v.parity(), fb = bar(C::bDPFree), fpar = (dp - 1) & 1u;
+                const bool first = at_dp.j == at_dp.n - at_dp.n / kWalks;
+                const uint32_t gpar = at_dp.tile & 1u;
+                if (!follow(
+                        dp > 0 && !first && warp_test2(b, par, fb, fpar),
+                        [&] {
+                            return warp_wait(b, par, sc) && (dp == 0 || warp_wait(fb, fpar, sc)) &&
+                                   (!first || warp_wait(bar(C::bG), gpar, sc));
+                        },
+                        rest,
+                        [&] { half_over_d<D, BF16>(0, tmem + C::cDP, smem + C::kGOff, smem + C::kVOff + v.at * T::kBytes); }))
+                    return false;
+                close();
+                dp_open = true;
+                dp_tile = v.at;
+                dp_ends = at_dp.j + 1 == at_dp.n;
+                ++dp;
+                v = v.next();
             }
-            alive = alive && issue_s(false, [] {}) && issue_dp(false, [] {}) && (w.n == 1 || issue_s(false, [] {}));
-            if (!alive) break;
-            if (w.n == 1) commit(bar(C::bQEmpty));                           // (S and dP of the last block have Q and dO last)
-            bool v_seen = false;
-            for (int j = 0; j < w.n; ++j, ++ds, kb = kb.next()) {
-                const uint32_t ds_bar = bar(C::bDS + (ds & 1u)), ds_parity = (ds >> 1) & 1u;
-                seen = false;
-                if (j + 1 < w.n && !(alive = issue_dp(v_seen, [&] { probe(ds_bar, ds_parity); }))) break;
-                if (j + 2 == w.n) commit(bar(C::bQEmpty));
-                if (!(alive = warp_wait_unless(seen, ds_bar, ds_parity, sc))) break;
-                if (j == 0 && tiles > 0 && !(alive = warp_wait(bar(C::bAccEmpty), (tiles - 1) & 1u, sc))) break;
-                ptx::tc_fence_after_sync();
-                product_over_rows<D, BF16>(tmem + C::cDQ, tmem + C::cS + 128 * (ds & 1u), smem + C::kKOff + kb.at * T::kBytes,
-                                           j > 0, [&] { probe(bar(C::bK + ka.at), ka.parity()); });
+            go_on(at_dp);
+            return true;
+        };
+        auto begin_dq = [&]() -> bool {
+            const uint32_t b = bar(C::bDS + (ds & 1u)), par = (ds >> 1) & 1u;
+            if (ADDITIVE && 2 * at_dq.j < at_dq.n) {          // S alone, which the warps have read
+                if (ptx::elect_one()) rest();
+                close();
+                if (!warp_wait(b, par, sc)) return false;
                 commit(bar(C::bKEmpty + kb.at));
-                if (j + 2 < w.n) {
-                    if (!(alive = issue_s(seen, [&] { v_seen = ptx::mbar_test_wait(bar(C::bV + v.at), v.parity()); }))) break;
-                } else {
-                    v_seen = false;
-                }
+            } else {
+                const bool first = at_dq.j == at_dq.n - at_dq.n / kWalks, drained = !first || at_dq.tile == 0;
+                const uint32_t apar = (at_dq.tile - 1) & 1u;  // the warps have the last tile's dQ
+                if (!follow(
+                        drained ? warp_test(b, par) : warp_test2(b, par, bar(C::bAccEmpty), apar),
+                        [&] { return warp_wait(b, par, sc) && (drained || warp_wait(bar(C::bAccEmpty), apar, sc)); }, rest,
+                        [&] {
+                            half_over_rows<D, BF16>(0, tmem + C::cDQ, tmem + C::cS + 128 * (ds & 1u),
+                                                    smem + C::kKOff + kb.at * T::kBytes, !first);
+                        }))
+                    return false;
+                close();
+                dq_open = true;
+                dq_tile = kb.at;
+                dq_buf = ds & 1u;
+                dq_ends = at_dq.j + 1 == at_dq.n;
             }
-            if (!alive) break;
-            commit(bar(C::bAcc));
-            ++tiles;
+            ++ds;
+            kb = kb.next();
+            go_on(at_dq);
+            return true;
+        };
+        if (p.stall) alive = warp_wait(bar(C::bStall), 0, sc);               // nothing ever arrives
+        if (alive) {
+            next_work();
+            at_dp.n = at_dq.n = at_s.n;
+            alive = at_s.n == 0 || (begin_s() && begin_dp() && (at_s.n == 0 || begin_s()));
         }
+        while (alive && at_dq.n > 0)
+            alive = (at_dp.n == 0 || begin_dp()) && begin_dq() && (at_s.n == 0 || begin_s());
+        if (alive && ptx::elect_one()) rest();
         if (issued) {
             commit(bar(C::bDrain));
             drain_phase(bar(C::bDrain), 0, sc);
@@ -811,6 +957,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         float2* stat = reinterpret_cast<float2*>(smem_ptr + C::kStatOff);
         uint32_t tiles = 0, su = 0, dp = 0, seen = 0;
         bool alive = true;
+        // Each warpgroup writes 32 columns of dQ: of the tile before, once the first block of the next one is in registers
+        const bool writes = 32 * wg < D;
+        uint16_t* done_row = nullptr;
+        bool done_there = false;
+        auto finish = [&]() -> bool {
+            if (!done_row) return true;
+            if (!warp_wait(bar(C::bAcc), tiles & 1u, sc)) return false;
+            ptx::tc_fence_after_sync();
+            if (writes)
+                store_row<32, BF16>(tmem + lane_base + C::cDQ + 32 * wg, bar(C::bAccEmpty), done_row, p.scale, done_there,
+                                    p.vec8);
+            else
+                warp_arrive(bar(C::bAccEmpty));
+            done_row = nullptr;
+            ++tiles;
+            return true;
+        };
         for (uint32_t k = 0; alive; ++k) {
             const int t = next_tile(k, ring, sc);
             if (t < 0) break;
@@ -870,6 +1033,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float x[kCols];
                     if (!(alive = logits(j, x))) break;
                     warp_arrive_tmem(bar(C::bDS + (su & 1u)));
+                    if (j == 0 && !(alive = finish())) break;
                     float top = m;
 #pragma unroll
                     for (int c = 0; c < kCols; c += 2) top = ptx::max3(top, x[c], x[c + 1]);
@@ -910,6 +1074,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(alive = logits(j, x))) break;
 #pragma unroll
                 for (int c = 0; c < kCols; ++c) x[c] = ptx::ex2(ADDITIVE ? x[c] + nl : x[c]);
+                if (!ADDITIVE && j == 0 && !(alive = finish())) break;
                 if (!(alive = warp_wait(bar(C::bDP), dp & 1u, sc))) break;
                 ptx::tc_fence_after_sync();
                 float d[kCols];
@@ -928,21 +1093,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 warp_arrive_tmem(bar(C::bDS + (su & 1u)));
             }
             if (!alive) break;
-            // ---- each warpgroup writes 32 columns
-            const bool writes = 32 * wg < D;
             uint16_t* out = static_cast<uint16_t*>(p.dq) + ((long long)w.b * p.Sq + row) * p.dq_stride + w.h * D + 32 * wg;
             if (w.n == 0) {
                 zero_row<32>(out, there && writes);
-                continue;
+            } else {
+                done_row = out;
+                done_there = there;
             }
-            if (!(alive = warp_wait(bar(C::bAcc), tiles & 1u, sc))) break;
-            ptx::tc_fence_after_sync();
-            if (writes)
-                store_row<32, BF16>(tmem + lane_base + C::cDQ + 32 * wg, bar(C::bAccEmpty), out, p.scale, there, p.vec8);
-            else
-                warp_arrive(bar(C::bAccEmpty));
-            ++tiles;
         }
+        if (alive) finish();
     }
 
     ptx::tc_fence_before_sync();
