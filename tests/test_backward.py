@@ -205,6 +205,16 @@ def test_empty_sizes_give_zero_gradients():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("masked", [False, True])
+def test_many_tiles_without_a_pair(masked):
+    """Several in a row for every CTA: queries before all keys, keys that no window reaches."""
+    mask = _mask("bias", 4, 1000, 100) if masked else None
+    _check(*_inputs(4, 32, 16, 1000, 100, 64, BF16, seed=15), causal=True, mask=mask)
+    if not masked:
+        _check(*_inputs(4, 32, 32, 50, 2000, 128, BF16, seed=16), causal=True, window=20)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("scale", [0.02, 1.0, 3.0])
 def test_scales(scale):
     _check(*_inputs(1, 2, 1, 200, 200, 128, BF16, seed=9), causal=True, scale=scale)

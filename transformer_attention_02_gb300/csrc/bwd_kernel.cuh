@@ -61,9 +61,11 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
         ptx::tma_load_4d(dst + c * Tile<D>::kBoxBytes, map, bar, c * 64, h, row, b);
 }
 
-// Products are issued by one lane and in halves. The tensor cores take a product's instructions little faster than they run
-// them, so every cycle between two products is theirs lost: a product's second half and the next one's first go out in one
-// piece of code, and what the next one waits for is probed, and all bookkeeping done, between a product's halves.
+// Products are issued by one lane. The tensor cores take a product's instructions little faster than they run them, so every
+// cycle between two products is theirs lost, and a look at a barrier costs the issuing warp 100 of them beside busy warps.
+// So products go out in bursts with one look for everything a burst needs, made, like all bookkeeping, while the last
+// product of the burst before it is half issued. Within a burst there is no branch (it would move every operand out of the
+// uniform registers): blocks inside a tile take that way, the others, where a tile begins or ends, a slower one.
 
 // Half of D(tmem) = A B^T of two tiles, summed over the head dimension.
 template <int D, bool BF16>
@@ -182,16 +184,18 @@ __device__ __forceinline__ void store_row(uint32_t taddr, uint32_t freed, uint16
     }
 }
 
-template <int N>
-__device__ __forceinline__ void zero_row(uint16_t* row, bool there) {
-#pragma unroll
-    for (int c = 0; c < N; c += 8)
-        if (there) *reinterpret_cast<uint4*>(row + c) = make_uint4(0u, 0u, 0u, 0u);
+// One warp writes zeros over rows row0 .. of a tile: `rows` of them, D values each, `stride` apart.
+template <int D>
+__device__ __forceinline__ void zero_rows(uint16_t* at, long long stride, int rows) {
+    constexpr int kPer = D / 8;                               // 16-byte pieces of a row
+    for (int e = threadIdx.x & 31; e < rows * kPer; e += 32)
+        *reinterpret_cast<uint4*>(at + (e / kPer) * stride + 8 * (e % kPer)) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // Work tiles are handed out in order: a CTA's first is its own index, each further one comes from a counter in the
 // workspace when the CTA is about to load it, so that CTAs with short tiles take more of them. (Which CTA computes a tile
-// changes nothing in it.) The loading warp publishes them in a ring of two entries; every other warp takes a copy.
+// changes nothing in it.) The loading warp publishes them in a ring of two entries; every other warp takes a copy. Tiles
+// without a visible pair are not published: the loading warp writes their zeros.
 struct TileRing {
     uint32_t full, empty;           // barriers, two each
     volatile int* entry;
@@ -199,26 +203,35 @@ struct TileRing {
 constexpr int kRing = 2;
 constexpr uint32_t kRingReaders = kWarps + 1;
 
-// The k-th tile of the CTA, or -1 at the end (or where a wait ran out).
-__device__ __forceinline__ int take_tile(uint32_t k, const BwdParams& p, const TileRing& ring, const SyncCtx& sc) {
-    const uint32_t s = k % kRing;
-    if (k >= kRing && !warp_wait(ring.empty + 8 * s, (k / kRing - 1) & 1u, sc)) return -1;
+// Loading warp: the CTA's next tile, or -1 behind the last. `taken`: tiles taken so far.
+__device__ __forceinline__ int take_tile(uint32_t& taken, const BwdParams& p) {
     int t = 0;
     if ((threadIdx.x & 31) == 0) {
-        t = k == 0 ? (int)blockIdx.x : (int)min((long long)gridDim.x + atomicAdd(p.counter, 1u), (long long)p.n_tiles);
+        t = taken == 0 ? (int)blockIdx.x : (int)min((long long)gridDim.x + atomicAdd(p.counter, 1u), (long long)p.n_tiles);
         if (t >= p.n_tiles) t = -1;
-        ring.entry[s] = t;
-        ptx::mbar_arrive(ring.full + 8 * s);
     }
+    ++taken;
     return __shfl_sync(0xffffffffu, t, 0);
 }
 
+// Loading warp: publishes tile t (-1: the end) as the ring's k-th entry. False where a wait ran out.
+__device__ __forceinline__ bool publish_tile(uint32_t k, int t, const TileRing& ring, const SyncCtx& sc) {
+    const uint32_t s = k % kRing;
+    if (k >= kRing && !warp_wait(ring.empty + 8 * s, (k / kRing - 1) & 1u, sc)) return false;
+    if ((threadIdx.x & 31) == 0) {
+        ring.entry[s] = t;
+        ptx::mbar_arrive(ring.full + 8 * s);
+    }
+    return true;
+}
+
+// The k-th entry of the ring: a tile, or -1 at the end (or where a wait ran out).
 __device__ __forceinline__ int next_tile(uint32_t k, const TileRing& ring, const SyncCtx& sc) {
     const uint32_t s = k % kRing;
     if (!warp_wait(ring.full + 8 * s, (k / kRing) & 1u, sc)) return -1;
     const int t = ring.entry[s];
     warp_arrive(ring.empty + 8 * s);
-    return t;
+    return __shfl_sync(0xffffffffu, t, 0);                    // (known to be uniform, and with it what follows from it)
 }
 
 // A place in a ring of N buffers: which buffer, and how often it was used before (its barriers' parity).
@@ -329,20 +342,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_before_sync();
     __syncthreads();
     ptx::tc_fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const SyncCtx sc{abort_flag, p.status, p.timeout_ns};
 
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
-        uint32_t tiles = 0, v_fills = 0, fills = 0;            // K and V tiles, blocks
+        uint32_t taken = 0, tiles = 0, v_fills = 0, q_fills = 0, g_fills = 0;
         Place<C::kQ> q;
         Place<C::kG> g;
-        bool alive = true;
-        for (uint32_t k = 0; alive; ++k) {
-            const int t = take_tile(k, p, ring, sc);
-            if (t < 0) break;
-            const KvTile w = kv_tile(t, p);
-            if (w.n == 0) continue;
+        for (bool alive = true; alive;) {
+            const int t = take_tile(taken, p);
+            const KvTile w = kv_tile(max(t, 0), p);
+            if (t >= 0 && w.n == 0) {
+                const long long token = (long long)w.b * p.Sk + w.k0;
+                const int rows = min(kBlock, p.Sk - w.k0);
+                zero_rows<D>(static_cast<uint16_t*>(p.dk) + token * p.dk_stride + w.hk * D, p.dk_stride, rows);
+                zero_rows<D>(static_cast<uint16_t*>(p.dv) + token * p.dv_stride + w.hk * D, p.dv_stride, rows);
+                continue;
+            }
+            if (!publish_tile(tiles, t, ring, sc) || t < 0) break;
             if (tiles > 0 && !warp_wait(bar(C::bKEmpty), (tiles - 1) & 1u, sc)) break;
             if (lane == 0) {
                 ptx::mbar_arrive_expect_tx(bar(C::bK), T::kBytes);
@@ -350,26 +368,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++tiles;
             int h = w.hk * p.group, i = w.lo;
-            for (int it = 0; it < w.n; ++it, ++fills, q = q.next(), g = g.next()) {
+            for (int it = 0; it < w.n; ++it) {
                 const size_t row = ((size_t)w.b * p.Hq + h) * p.Sp + (size_t)i * kBlock;
-                alive = (q.round == 0 || warp_wait(bar(C::bQEmpty + q.at), (q.round - 1) & 1u, sc)) &&
-                        (g.round == 0 || warp_wait(bar(C::bGEmpty + g.at), (g.round - 1) & 1u, sc));
-                if (!alive) break;
+                if (q.round > 0 && !(alive = warp_wait(bar(C::bQEmpty + q.at), (q.round - 1) & 1u, sc))) break;
                 if (lane == 0) {
                     ptx::mbar_arrive_expect_tx(bar(C::bQ + q.at), T::kBytes + kRowBytes * (ADDITIVE ? 2 : 1));
                     load_tile<D>(smem + C::kQOff + q.at * T::kBytes, &tmQ, bar(C::bQ + q.at), h, i * kBlock, w.b);
                     ptx::bulk_load(smem + C::kRowOff + q.at * kRowBytes, p.neg_lse + row, kRowBytes, bar(C::bQ + q.at));
                     if (ADDITIVE)
                         ptx::bulk_load(smem + C::kSumOff + q.at * kRowBytes, p.inv_sum + row, kRowBytes, bar(C::bQ + q.at));
+                }
+                ++q_fills;
+                q = q.next();
+                if (g.round > 0 && !(alive = warp_wait(bar(C::bGEmpty + g.at), (g.round - 1) & 1u, sc))) break;
+                if (lane == 0) {
                     ptx::mbar_arrive_expect_tx(bar(C::bG + g.at), T::kBytes + kRowBytes);
                     load_tile<D>(smem + C::kGOff + g.at * T::kBytes, &tmG, bar(C::bG + g.at), h, i * kBlock, w.b);
                     ptx::bulk_load(smem + C::kDeltaOff + g.at * kRowBytes, p.neg_delta + row, kRowBytes, bar(C::bG + g.at));
                 }
+                ++g_fills;
+                g = g.next();
                 if (it == 0) {
-                    if (v_fills > 0 && !(alive = warp_wait(bar(C::bVEmpty), (v_fills - 1) & 1u, sc))) {
-                        ++fills;
-                        break;
-                    }
+                    if (v_fills > 0 && !(alive = warp_wait(bar(C::bVEmpty), (v_fills - 1) & 1u, sc))) break;
                     if (lane == 0) {
                         ptx::mbar_arrive_expect_tx(bar(C::bV), T::kBytes);
                         load_tile<D>(smem + C::kVOff, &tmV, bar(C::bV), w.hk, w.k0, w.b);
@@ -386,24 +406,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tiles > 0) drain_phase(bar(C::bK), (tiles - 1) & 1u, sc);
         if (v_fills > 0) drain_phase(bar(C::bV), (v_fills - 1) & 1u, sc);
         for (uint32_t s = 0; s < (uint32_t)C::kQ; ++s)
-            if (fills > s) drain_phase(bar(C::bQ + s), ((fills - 1 - s) / C::kQ) & 1u, sc);
+            if (q_fills > s) drain_phase(bar(C::bQ + s), ((q_fills - 1 - s) / C::kQ) & 1u, sc);
         for (uint32_t s = 0; s < (uint32_t)C::kG; ++s)
-            if (fills > s) drain_phase(bar(C::bG + s), ((fills - 1 - s) / C::kG) & 1u, sc);
+            if (g_fills > s) drain_phase(bar(C::bG + s), ((g_fills - 1 - s) / C::kG) & 1u, sc);
     } else if (warp == kIssueWarp) {
         // --------------------------------------------------------- products
         // One walk over the blocks of all tiles: a tile's first S and dP are issued before the last tile's last dK.
-        uint32_t k = 0, tiles = 0, use = 0;                   // ring entries, tiles with work, blocks
+        uint32_t k = 0, tiles = 0, use = 0;                   // ring entries, tiles done, blocks
         Place<C::kQ> q;
         Place<C::kG> g;
         bool alive = true, issued = false;
-        // Blocks of the next tile with work; 0: there is none.
+        // Blocks of the next tile; 0: there is none.
         auto next_work = [&]() -> int {
-            for (;;) {
-                const int t = next_tile(k++, ring, sc);
-                if (t < 0) return 0;
-                const int n = kv_tile(t, p).n;
-                if (n > 0) return n;
-            }
+            const int t = next_tile(k++, ring, sc);
+            return t < 0 ? 0 : kv_tile(t, p).n;
         };
         auto s_half = [&](int half, uint32_t at) {
             half_over_d<D, BF16>(half, tmem + C::cS, smem + C::kKOff, smem + C::kQOff + at * T::kBytes);
@@ -626,12 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!alive) break;
             uint16_t* row = static_cast<uint16_t*>(is_k ? p.dk : p.dv) +
                             ((long long)w.b * p.Sk + key) * (is_k ? p.dk_stride : p.dv_stride) + w.hk * D + col;
-            if (w.n == 0) {
-                zero_row<D / 2>(row, key < p.Sk);
-            } else {
-                done_row = row;
-                done_there = key < p.Sk;
-            }
+            done_row = row;
+            done_there = key < p.Sk;
         }
         if (alive) finish();
     }
@@ -650,14 +662,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 // 128-255, of odd blocks in 256-383, dP in 384-511. A key block j takes, in the
 // tensor cores' order,
 //   dP_{j+1} = dO V_{j+1}^T,  dQ += dS_j K_j,  S_{j+2} = Q K_{j+2}^T
-// the first as soon as the warps hold dP_j in registers. With an additive mask
+// in one burst once the warps have left dS_j. With an additive mask
 // the keys are walked twice: first for the rows' maximum and sum, since a mask of
 // large values leaves lse without the logits' bits; both go to the other kernel.
 
 template <int D, bool ADDITIVE>
 struct QCfg {
     using T = Tile<D>;
-    static constexpr int kK = D == 128 ? (ADDITIVE ? 2 : 3) : 5, kV = D == 128 ? 2 : 4;
+    // K stays from its S to its dQ, two blocks later
+    static constexpr int kK = D == 128 ? 3 : 5, kV = D == 128 ? (ADDITIVE ? 1 : 2) : 4;
     static constexpr int kQOff = 0, kGOff = T::kBytes, kKOff = 2 * T::kBytes, kVOff = kKOff + kK * T::kBytes;
     static constexpr int kBarOff = kVOff + kV * T::kBytes;
     static constexpr int bQ = 0, bQEmpty = 1, bS = 2, bDP = 4, bDPFree = 5, bDS = 6, bAcc = 8, bAccEmpty = 9, bDrain = 10,
@@ -745,18 +758,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_before_sync();
     __syncthreads();
     ptx::tc_fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const SyncCtx sc{abort_flag, p.status, p.timeout_ns};
 
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
-        uint32_t tiles = 0, g_fills = 0, kf = 0, vf = 0;
-        bool alive = true;
-        for (uint32_t k = 0; alive; ++k) {
-            const int t = take_tile(k, p, ring, sc);
-            if (t < 0) break;
-            const QTile w = q_tile(t, p);
-            if (w.n == 0) continue;
+        uint32_t taken = 0, tiles = 0, g_fills = 0, kf = 0, vf = 0;
+        for (bool alive = true; alive;) {
+            const int t = take_tile(taken, p);
+            const QTile w = q_tile(max(t, 0), p);
+            if (t >= 0 && w.n == 0) {
+                zero_rows<D>(static_cast<uint16_t*>(p.dq) + ((long long)w.b * p.Sq + w.m0) * p.dq_stride + w.h * D, p.dq_stride,
+                             min(kBlock, p.Sq - w.m0));
+                if (ADDITIVE) {                                   // the other kernel passes over these rows too
+                    const size_t at = ((size_t)w.b * p.Hq + w.h) * p.Sp + w.m0;
+                    for (int e = lane; e < kBlock; e += 32) p.neg_lse[at + e] = p.inv_sum[at + e] = 0.f;
+                }
+                continue;
+            }
+            if (!publish_tile(tiles, t, ring, sc) || t < 0) break;
             if (tiles > 0 && !warp_wait(bar(C::bQEmpty), (tiles - 1) & 1u, sc)) break;
             if (lane == 0) {
                 ptx::mbar_arrive_expect_tx(bar(C::bQ), T::kBytes);
@@ -807,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // --------------------------------------------------------- products
         // One walk over the blocks of all tiles (with an additive mask each tile's keys come twice, the first time for S
         // alone), with three places in it: dQ, dP one block ahead, S two blocks ahead. A place is a tile's number, the
-        // block and the number of blocks; lane t % 32 keeps that of tile t for the places behind the first.
+        // block and the number of blocks; those of the last four tiles are kept for the places behind the first.
         struct At {
             uint32_t tile = 0;
             int j = 0, n = 0;
@@ -818,18 +838,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         Place<C::kK> ka, kb;                                  // K of S, of dQ
         Place<C::kV> v;
         bool alive = true, issued = false;
-        int kept = 0;
-        auto next_work = [&]() {                              // at_s: the next tile with work, n = 0 behind the last
-            at_s.n = 0;
-            for (int t; at_s.n == 0 && (t = next_tile(k, ring, sc)) >= 0; ++k) at_s.n = kWalks * q_tile(t, p).n;
+        int kept0 = 0, kept1 = 0, kept2 = 0, kept3 = 0;
+        auto next_work = [&]() {                              // at_s: the next tile, n = 0 behind the last
+            const int t = next_tile(k++, ring, sc);
+            at_s.n = t < 0 ? 0 : kWalks * q_tile(t, p).n;
             at_s.j = 0;
-            if (lane == (int)(at_s.tile & 31u)) kept = at_s.n;
+            const uint32_t i = at_s.tile & 3u;
+            kept0 = i == 0 ? at_s.n : kept0;
+            kept1 = i == 1 ? at_s.n : kept1;
+            kept2 = i == 2 ? at_s.n : kept2;
+            kept3 = i == 3 ? at_s.n : kept3;
         };
         auto go_on = [&](At& a) {
             if (++a.j < a.n) return;
             ++a.tile;
             a.j = 0;
-            a.n = __shfl_sync(0xffffffffu, kept, (int)(a.tile & 31u));
+            const uint32_t i = a.tile & 3u;
+            a.n = i == 0 ? kept0 : i == 1 ? kept1 : i == 2 ? kept2 : kept3;
         };
         // Second halves of the products that are half issued: of S (s_open), with its buffers and what follows it, of dP, dQ
         bool s_open = false, s_ends = false, dp_open = false, dp_ends = false, dq_open = false, dq_ends = false;
@@ -1094,12 +1119,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!alive) break;
             uint16_t* out = static_cast<uint16_t*>(p.dq) + ((long long)w.b * p.Sq + row) * p.dq_stride + w.h * D + 32 * wg;
-            if (w.n == 0) {
-                zero_row<32>(out, there && writes);
-            } else {
-                done_row = out;
-                done_there = there;
-            }
+            done_row = out;
+            done_there = there;
         }
         if (alive) finish();
     }
