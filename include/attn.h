@@ -561,6 +561,99 @@ int attn_bwd_f16(const void *d_o, const void *q, const void *k, const void *v, c
 size_t attn_bwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D, int mask_kind);
 
 /*
+ * attn_rope_axes / attn_rope_axes_f16 — rotary positions with several axes (time,
+ * height and width of images and video) for the queries and keys of a step, in
+ * one launch. The D/2 pairs (x[2i], x[2i+1]) of a head vector are dealt out to
+ * the axes in order, sections[a] of them to axis a; pair i of axis a turns by the
+ * angle of the table's entry (positions[token][a], i).
+ *   q, q_out    device, (B, S, Hq, D) bf16 / fp16, 16-byte aligned; a token's (H, D)
+ *               values are contiguous and the strides (elements, a multiple of 8,
+ *               at least H * D) lead from token to token of the flattened (B, S),
+ *               so that they may be slices of a packed projection. q_out may be q
+ *               (in place); otherwise inputs and outputs do not overlap
+ *   k, k_out    the same with Hkv heads. Either pair may be NULL with no heads
+ *   D           a multiple of 8, at most 1024
+ *   rope_table, max_pos  device, FP32, (max_pos, D/2, {cos, sin}), 8-byte aligned: of
+ *               attn_rope_table (the frequency goes by the pair's number in the
+ *               head vector) or attn_rope_axes_table (by its number in the axis)
+ *   positions   device, int32, (B * S, n_axes): read on the device, so a captured
+ *               graph can be replayed as they change. A token with one outside
+ *               [0, max_pos) is not written, and attn_last_status returns
+ *               ATTN_ERR_BAD_INDEX
+ *   sections    HOST, int, (n_axes): non-negative, D/2 together; 1 to 4 axes
+ *   inverse     != 0: the opposite angle, which turns a vector back and is the
+ *               way of a gradient through the rotation
+ * FP32 arithmetic, rounded once. Bound by memory: one read and one write.
+ */
+int attn_rope_axes(const void *q, void *q_out, long long q_stride, long long q_out_stride,
+                   const void *k, void *k_out, long long k_stride, long long k_out_stride,
+                   int B, int S, int Hq, int Hkv, int D, const float *rope_table, int max_pos,
+                   const int *positions, const int *sections, int n_axes, int inverse, attn_stream_t stream);
+int attn_rope_axes_f16(const void *q, void *q_out, long long q_stride, long long q_out_stride,
+                       const void *k, void *k_out, long long k_stride, long long k_out_stride,
+                       int B, int S, int Hq, int Hkv, int D, const float *rope_table, int max_pos,
+                       const int *positions, const int *sections, int n_axes, int inverse, attn_stream_t stream);
+
+/*
+ * attn_rope_axes_table — fills `table` (device, FP32, max_pos x P x 2, 16-byte
+ * aligned, P = the sum of sections, at most 512) with {cos, sin} of
+ * pos * base^(-j/n) for pair j of an axis of n pairs: each axis has the
+ * frequencies of a head of its own size. In double, rounded to FP32. base > 1,
+ * max_pos * P <= 2^30.
+ */
+int attn_rope_axes_table(float *table, int max_pos, const int *sections, int n_axes, double base, attn_stream_t stream);
+
+/*
+ * Activation checkpoints in 8 bits: a (B, S, H, D) tensor (D 64 or 128) as e4m3
+ * codes of value / scale, with one scale 2^e for each head vector, the smallest
+ * (>= 2^-100) with max |x| <= 448 * 2^e, as in the paged cache. Infinities become
+ * +-448 codes and NaN stays NaN; neither sets the scale.
+ *   x           device, bf16 / fp16, 16-byte aligned, x_stride elements from token to
+ *               token (a multiple of 8, at least H * D)
+ *   codes, scale  device, (B, S, H, D) bytes, 16-byte aligned, and FP32 (B, S, H);
+ *               contiguous
+ * attn_checkpoint_store writes codes and scale, attn_checkpoint_load writes x:
+ * code * scale, exact in bf16; in fp16 rounded, and cut to +-65504.
+ */
+int attn_checkpoint_store(const void *x, long long x_stride, void *codes, float *scale, int B, int S, int H, int D,
+                          attn_stream_t stream);
+int attn_checkpoint_store_f16(const void *x, long long x_stride, void *codes, float *scale, int B, int S, int H, int D,
+                              attn_stream_t stream);
+int attn_checkpoint_load(const void *codes, const float *scale, void *x, long long x_stride, int B, int S, int H, int D,
+                         attn_stream_t stream);
+int attn_checkpoint_load_f16(const void *codes, const float *scale, void *x, long long x_stride, int B, int S, int H,
+                             int D, attn_stream_t stream);
+
+/*
+ * attn_bwd_checkpoint / attn_bwd_checkpoint_f16 — attn_bwd from 8-bit checkpoints
+ * of Q, K and V alone: they are widened into the workspace, the forward pass
+ * computes O and lse again, and the backward pass runs on those. The gradients are
+ * those of the attention of the widened tensors, exactly as if the caller had made
+ * the three calls.
+ *   q8, k8, v8, q_scale, k_scale, v_scale  codes and scales as of attn_checkpoint_store:
+ *               (B, Sq, Hq, D), (B, Sk, Hkv, D) and (B, Sq, Hq), (B, Sk, Hkv)
+ *   workspace   device scratch of attn_bwd_checkpoint_workspace_bytes(...) bytes,
+ *               256-byte aligned
+ * Other arguments and errors as for attn_bwd.
+ */
+int attn_bwd_checkpoint(const void *d_o, const void *q8, const void *k8, const void *v8,
+                        const float *q_scale, const float *k_scale, const float *v_scale,
+                        void *dq, void *dk, void *dv, long long dq_stride, long long dk_stride, long long dv_stride,
+                        int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                        float scale, int mask_kind, const float *mask, int window, int sinks,
+                        void *workspace, size_t workspace_bytes, attn_stream_t stream);
+int attn_bwd_checkpoint_f16(const void *d_o, const void *q8, const void *k8, const void *v8,
+                            const float *q_scale, const float *k_scale, const float *v_scale,
+                            void *dq, void *dk, void *dv, long long dq_stride, long long dk_stride, long long dv_stride,
+                            int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                            float scale, int mask_kind, const float *mask, int window, int sinks,
+                            void *workspace, size_t workspace_bytes, attn_stream_t stream);
+
+/* attn_bwd_checkpoint_workspace_bytes — workspace bytes attn_bwd_checkpoint needs for
+ * these sizes (host only; 0 for an empty problem or invalid sizes). */
+size_t attn_bwd_checkpoint_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D, int mask_kind);
+
+/*
  * attn_last_status — synchronises `stream`, then returns and clears the
  * current device's run-time status word: ATTN_OK, or ATTN_ERR_DEVICE_TIMEOUT
  * if any launch since the last call gave up on a bounded wait (the kernel then

@@ -99,7 +99,7 @@ def backward(d_o, q, k, v, *, causal=False, mask=None, window=0, sinks=0, scale=
 
 
 def check(got, want, bounds, label=""):
-    for name, a, w, b in zip(("dq", "dk", "dv"), got, want, bounds):
+    for name, a, w, b in zip(("dq", "dk", "dv") if len(got) == 3 else ("gradient",), got, want, bounds):
         assert bool(torch.isfinite(a).all()), f"{label} {name}: not finite"
         err = (a.double() - w).abs()
         worst = float((err / b.clamp(min=1e-300)).max()) if err.numel() else 0.0

@@ -15,4 +15,7 @@ from .attn import (  # noqa: F401
     linear, layernorm, attention_qkvpacked, attention_block, attn_fwd_window, attn_fwd_window_f16,
     attention_window, CACHE_16BIT, CACHE_E4M3, attn_kv_append,
     attn_kv_append_f16, attn_fwd_paged, attn_fwd_paged_f16, attn_paged_workspace_bytes, kv_append, attention_paged,
-    attn_bwd, attn_bwd_f16, attn_bwd_workspace_bytes, attention_backward)
+    attn_bwd, attn_bwd_f16, attn_bwd_workspace_bytes, attention_backward, attn_rope_axes, attn_rope_axes_f16,
+    attn_rope_axes_table, rope_axes, rope_axes_table, attn_checkpoint_store, attn_checkpoint_store_f16,
+    attn_checkpoint_load, attn_checkpoint_load_f16, checkpoint_store, checkpoint_load, attn_bwd_checkpoint,
+    attn_bwd_checkpoint_f16, attn_bwd_checkpoint_workspace_bytes, attention_backward_checkpoint)

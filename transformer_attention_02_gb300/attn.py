@@ -102,6 +102,22 @@ def lib() -> ctypes.CDLL:
         f.restype = I
     L.attn_bwd_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
     L.attn_bwd_workspace_bytes.restype = ctypes.c_size_t
+    for f in (L.attn_rope_axes, L.attn_rope_axes_f16):
+        f.argtypes = [P, P, LL, LL] * 2 + [I] * 5 + [P, I, P, P, I, I, P]
+        f.restype = I
+    L.attn_rope_axes_table.argtypes = [P, I, P, I, ctypes.c_double, P]
+    L.attn_rope_axes_table.restype = I
+    for f in (L.attn_checkpoint_store, L.attn_checkpoint_store_f16):
+        f.argtypes = [P, LL, P, P, I, I, I, I, P]
+        f.restype = I
+    for f in (L.attn_checkpoint_load, L.attn_checkpoint_load_f16):
+        f.argtypes = [P, P, P, LL, I, I, I, I, P]
+        f.restype = I
+    for f in (L.attn_bwd_checkpoint, L.attn_bwd_checkpoint_f16):
+        f.argtypes = [P] * 10 + [LL] * 3 + [I] * 6 + [F, I, P, I, I, P, ctypes.c_size_t, P]
+        f.restype = I
+    L.attn_bwd_checkpoint_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
+    L.attn_bwd_checkpoint_workspace_bytes.restype = ctypes.c_size_t
     L.attn_last_status.argtypes = [P]
     L.attn_last_status.restype = I
     L.attn_status_string.argtypes = [I]
@@ -272,6 +288,57 @@ def attn_bwd_f16(d_o, q, k, v, o, lse, dq, dk, dv, q_stride, k_stride, v_stride,
 
 def attn_bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, mask_kind=0) -> int:
     return int(lib().attn_bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, mask_kind))
+
+
+def attn_rope_axes(q, q_out, q_stride, q_out_stride, k, k_out, k_stride, k_out_stride, B, S, Hq, Hkv, D, rope_table,
+                   max_pos, positions, sections, n_axes, inverse, stream) -> int:
+    return lib().attn_rope_axes(q, q_out, q_stride, q_out_stride, k, k_out, k_stride, k_out_stride, B, S, Hq, Hkv, D,
+                                rope_table, max_pos, positions, sections, n_axes, inverse, stream)
+
+
+def attn_rope_axes_f16(q, q_out, q_stride, q_out_stride, k, k_out, k_stride, k_out_stride, B, S, Hq, Hkv, D,
+                       rope_table, max_pos, positions, sections, n_axes, inverse, stream) -> int:
+    return lib().attn_rope_axes_f16(q, q_out, q_stride, q_out_stride, k, k_out, k_stride, k_out_stride, B, S, Hq, Hkv,
+                                    D, rope_table, max_pos, positions, sections, n_axes, inverse, stream)
+
+
+def attn_rope_axes_table(table, max_pos, sections, n_axes, base, stream) -> int:
+    return lib().attn_rope_axes_table(table, max_pos, sections, n_axes, float(base), stream)
+
+
+def attn_checkpoint_store(x, x_stride, codes, scale, B, S, H, D, stream) -> int:
+    return lib().attn_checkpoint_store(x, x_stride, codes, scale, B, S, H, D, stream)
+
+
+def attn_checkpoint_store_f16(x, x_stride, codes, scale, B, S, H, D, stream) -> int:
+    return lib().attn_checkpoint_store_f16(x, x_stride, codes, scale, B, S, H, D, stream)
+
+
+def attn_checkpoint_load(codes, scale, x, x_stride, B, S, H, D, stream) -> int:
+    return lib().attn_checkpoint_load(codes, scale, x, x_stride, B, S, H, D, stream)
+
+
+def attn_checkpoint_load_f16(codes, scale, x, x_stride, B, S, H, D, stream) -> int:
+    return lib().attn_checkpoint_load_f16(codes, scale, x, x_stride, B, S, H, D, stream)
+
+
+def attn_bwd_checkpoint(d_o, q8, k8, v8, q_scale, k_scale, v_scale, dq, dk, dv, dq_stride, dk_stride, dv_stride, B,
+                        Hq, Hkv, Sq, Sk, D, scale, mask_kind, mask, window, sinks, workspace, workspace_bytes, stream) -> int:
+    return lib().attn_bwd_checkpoint(d_o, q8, k8, v8, q_scale, k_scale, v_scale, dq, dk, dv, dq_stride, dk_stride,
+                                     dv_stride, B, Hq, Hkv, Sq, Sk, D, scale, mask_kind, mask, window, sinks,
+                                     workspace, workspace_bytes, stream)
+
+
+def attn_bwd_checkpoint_f16(d_o, q8, k8, v8, q_scale, k_scale, v_scale, dq, dk, dv, dq_stride, dk_stride, dv_stride,
+                            B, Hq, Hkv, Sq, Sk, D, scale, mask_kind, mask, window, sinks, workspace, workspace_bytes,
+                            stream) -> int:
+    return lib().attn_bwd_checkpoint_f16(d_o, q8, k8, v8, q_scale, k_scale, v_scale, dq, dk, dv, dq_stride, dk_stride,
+                                         dv_stride, B, Hq, Hkv, Sq, Sk, D, scale, mask_kind, mask, window, sinks,
+                                         workspace, workspace_bytes, stream)
+
+
+def attn_bwd_checkpoint_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, mask_kind=0) -> int:
+    return int(lib().attn_bwd_checkpoint_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, mask_kind))
 
 
 def attn_last_status(stream) -> int:
@@ -943,7 +1010,7 @@ def _gradient(name, t, like, at, stream):
     if t is None:
         t = _new(like.shape, like.dtype, like, stream)
     elif t.dtype is not like.dtype or t.get_device() != at or t.shape != like.shape:
-        raise ValueError(f"{name} must be a tensor of the shape, type and device of what it is the gradient of")
+        raise ValueError(f"{name} must have the shape, type and device of the tensor it belongs to")
     return t, _token_stride(name, t, at)
 
 
@@ -1007,4 +1074,200 @@ def attention_backward(d_o, q, k, v, o, lse, *, causal: bool = False, mask=None,
             _torch.cuda.set_device(back)
     if rc:
         raise AttnError(rc, "attn_bwd")
+    return dq, dk, dv
+
+
+# --------------------------------------- rotary positions with several axes
+
+def _sections(sections):
+    """The pairs of each axis as a C array (kept alive by the caller), and their number."""
+    sections = tuple(sections)
+    if not 1 <= len(sections) <= 4 or any(not 0 <= n <= 512 for n in sections):
+        raise ValueError("sections must be 1 to 4 numbers of pairs, each 0 to 512")
+    return (ctypes.c_int * len(sections))(*sections), len(sections)
+
+
+def rope_axes_table(max_pos: int, sections, base: float = 10000.0, *, device=None, stream=None):
+    """FP32 (max_pos, sum(sections), 2) table of {cos, sin}(pos * base^(-j/n)) for pair j of an axis of n pairs.
+
+    Each axis has the frequencies of a head of its own size; rope_table() is the table of the other kind, in which a
+    pair's frequency goes by its number in the head vector.
+    """
+    torch = _torch or _bind()
+    axes, n = _sections(sections)
+    device = torch.device(device or "cuda")
+    at = torch.cuda.current_device() if device.index is None else device.index
+    back = _enter_device(at)
+    try:
+        table = _new((max_pos, sum(axes), 2), torch.float32, torch.empty(0, device=device), stream)
+        rc = attn_rope_axes_table(table.data_ptr(), max_pos, axes, n, base, _stream_on(at, stream))
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
+    if rc:
+        raise AttnError(rc, "attn_rope_axes_table")
+    return table
+
+
+def rope_axes(q, k, table, positions, sections, *, inverse: bool = False, q_out=None, k_out=None, stream=None):
+    """Turn queries (B, S, Hq, D) and keys (B, S, Hkv, D) to positions of several axes; k may be None.
+
+    sections: pairs of a head vector that each axis turns, in order (D/2 together); positions: int32 CUDA tensor
+    (B, S, len(sections)); table: rope_table() or rope_axes_table() for this D. inverse: by the opposite angle, the way
+    of a gradient. q, k: bf16 or fp16, contiguous or evenly spaced slices of a packed projection; so may be q_out and
+    k_out (new contiguous tensors by default; q and k themselves: in place). Returns (q_out, k_out), or q_out without k.
+    """
+    at = _device_of(q, "q")
+    torch = _torch
+    B, S, Hq, D = q.shape
+    axes, n = _sections(sections)
+    if sum(axes) * 2 != D:
+        raise ValueError("sections must add up to D/2")
+    if (positions.dtype is not torch.int32 or positions.shape != (B, S, n) or positions.get_device() != at
+            or not positions.is_contiguous()):
+        raise ValueError("positions must be a contiguous int32 CUDA tensor of shape (B, S, len(sections)) on q's device")
+    if (table.dtype is not torch.float32 or table.dim() != 3 or tuple(table.shape[1:]) != (D // 2, 2)
+            or table.shape[0] == 0 or table.get_device() != at or not table.is_contiguous()):
+        raise ValueError("table must be the (max_pos, D/2, 2) FP32 CUDA tensor of rope_table() or rope_axes_table() for this D")
+    q_stride, Hkv, k_stride, ko_stride, k_in = _token_stride("q", q, at), 0, 0, 0, None
+    if k is not None:
+        if k.dtype is not q.dtype or k.dim() != 4 or k.shape[0] != B or k.shape[1] != S or k.shape[3] != D:
+            raise ValueError("k must be a (B, S, Hkv, D) tensor of q's type, B, S and D")
+        Hkv, k_stride, k_in = k.shape[2], _token_stride("k", k, at), k.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    fn = attn_rope_axes if q.dtype is torch.bfloat16 else attn_rope_axes_f16
+    back = _enter_device(at)
+    try:
+        q_out, qo_stride = _gradient("q_out", q_out, q, at, stream)
+        if k is not None:
+            k_out, ko_stride = _gradient("k_out", k_out, k, at, stream)
+        rc = fn(q.data_ptr(), q_out.data_ptr(), q_stride, qo_stride, k_in, None if k is None else k_out.data_ptr(), k_stride,
+                ko_stride, B, S, Hq, Hkv, D, table.data_ptr(), table.shape[0], positions.data_ptr(), axes, n,
+                1 if inverse else 0, _stream_on(at, stream))
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
+    if rc:
+        raise AttnError(rc, "attn_rope_axes")
+    return q_out if k is None else (q_out, k_out)
+
+
+# ------------------------------------------------- activation checkpoints in 8 bits
+
+def checkpoint_store(x, *, codes=None, scale=None, stream=None):
+    """(codes, scale) of a bf16 or fp16 CUDA tensor x (B, S, H, D), contiguous or an evenly spaced slice.
+
+    codes: float8_e4m3fn (B, S, H, D), value / scale; scale: FP32 (B, S, H), a power of two for each head vector, the
+    smallest with max |x| <= 448 * scale.
+    """
+    at = _device_of(x, "x")
+    torch = _torch
+    B, S, H, D = x.shape
+    x_stride = _token_stride("x", x, at)
+    if codes is not None and (codes.dtype is not torch.float8_e4m3fn or codes.shape != x.shape or codes.get_device() != at
+                              or not codes.is_contiguous()):
+        raise ValueError("codes must be a contiguous float8_e4m3fn tensor of x's shape and device")
+    if scale is not None and (scale.dtype is not torch.float32 or scale.shape != (B, S, H) or scale.get_device() != at
+                              or not scale.is_contiguous()):
+        raise ValueError("scale must be a contiguous FP32 (B, S, H) tensor on x's device")
+    fn = attn_checkpoint_store if x.dtype is torch.bfloat16 else attn_checkpoint_store_f16
+    back = _enter_device(at)
+    try:
+        if codes is None:
+            codes = _new((B, S, H, D), torch.float8_e4m3fn, x, stream)
+        if scale is None:
+            scale = _new((B, S, H), torch.float32, x, stream)
+        rc = fn(x.data_ptr(), x_stride, codes.data_ptr(), scale.data_ptr(), B, S, H, D, _stream_on(at, stream))
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
+    if rc:
+        raise AttnError(rc, "attn_checkpoint_store")
+    return codes, scale
+
+
+def _checkpoint(name, pair, at, shape=None):
+    """(codes, scale) of a checkpoint, checked; `at` None: any device."""
+    torch = _torch
+    codes, scale = pair
+    if (codes.dtype is not torch.float8_e4m3fn or codes.dim() != 4 or (shape is not None and codes.shape != shape)
+            or codes.get_device() < 0 or (at is not None and codes.get_device() != at) or not codes.is_contiguous()):
+        raise ValueError(f"{name}: codes must be a contiguous float8_e4m3fn CUDA tensor (B, S, H, D)")
+    if (scale.dtype is not torch.float32 or scale.shape != codes.shape[:3] or scale.get_device() != codes.get_device()
+            or not scale.is_contiguous()):
+        raise ValueError(f"{name}: scale must be a contiguous FP32 (B, S, H) tensor on the codes' device")
+    return codes, scale
+
+
+def checkpoint_load(codes, scale, dtype=None, *, out=None, stream=None):
+    """The tensor (B, S, H, D) of a checkpoint in bf16 (the default) or fp16: code * scale."""
+    torch = _torch or _bind()
+    codes, scale = _checkpoint("checkpoint", (codes, scale), None)
+    at = codes.get_device()
+    dtype = (torch.bfloat16 if out is None else out.dtype) if dtype is None else dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError("dtype must be bf16 or fp16")
+    if out is not None and (out.dtype is not dtype or out.shape != codes.shape):
+        raise ValueError("out must be a tensor of the codes' shape and of dtype")
+    B, S, H, D = codes.shape
+    fn = attn_checkpoint_load if dtype is torch.bfloat16 else attn_checkpoint_load_f16
+    back = _enter_device(at)
+    try:
+        if out is None:
+            out = _new((B, S, H, D), dtype, codes, stream)
+        rc = fn(codes.data_ptr(), scale.data_ptr(), out.data_ptr(), _token_stride("out", out, at), B, S, H, D,
+                _stream_on(at, stream))
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
+    if rc:
+        raise AttnError(rc, "attn_checkpoint_load")
+    return out
+
+
+def attention_backward_checkpoint(d_o, q, k, v, *, causal: bool = False, mask=None, window: int = 0, sinks: int = 0,
+                                  scale=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """attention_backward() from 8-bit checkpoints: q, k, v are the (codes, scale) pairs of checkpoint_store().
+
+    They are widened to d_o's type, o and lse are computed again, and the gradients are those at the widened tensors.
+    workspace: optional uint8 CUDA tensor of at least attn_bwd_checkpoint_workspace_bytes bytes; it holds all of that.
+    Other arguments as for attention_backward().
+    """
+    at = _device_of(d_o, "d_o")
+    torch = _torch
+    if at < 0 or not d_o.is_contiguous():
+        raise ValueError("d_o must be a contiguous CUDA tensor (B, Sq, Hq, D)")
+    q8, qs = _checkpoint("q", q, at, d_o.shape)
+    k8, ks = _checkpoint("k", k, at)
+    B, Sq, Hq, D = d_o.shape
+    Sk, Hkv = k8.shape[1], k8.shape[2]
+    if k8.shape[0] != B or k8.shape[3] != D:
+        raise ValueError("q, k, v shapes disagree")
+    v8, vs = _checkpoint("v", v, at, k8.shape)
+    window, sinks = _count("window", window), _count("sinks", sinks)
+    kind = _attention_mask(causal, mask, window)
+    L = _lib or lib()
+    back = _enter_device(at)
+    try:
+        dq, dq_stride = _gradient("dq", dq, d_o, at, stream)
+        pair = []
+        for name, t in (("dk", dk), ("dv", dv)):
+            if t is None:
+                t = _new(k8.shape, d_o.dtype, d_o, stream)
+            elif t.dtype is not d_o.dtype or t.get_device() != at or t.shape != k8.shape:
+                raise ValueError(f"{name} must be a (B, Sk, Hkv, D) tensor of d_o's type and device")
+            pair.append((t, _token_stride(name, t, at)))
+        (dk, dk_stride), (dv, dv_stride) = pair
+        ws = _own_workspace(workspace, L.attn_bwd_checkpoint_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, kind), d_o, at, stream)
+        fn = L.attn_bwd_checkpoint if d_o.dtype is torch.bfloat16 else L.attn_bwd_checkpoint_f16
+        rc = fn(d_o.data_ptr(), q8.data_ptr(), k8.data_ptr(), v8.data_ptr(), qs.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+                dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dq_stride, dk_stride, dv_stride, B, Hq, Hkv, Sq, Sk, D,
+                _NAN if scale is None else scale, kind, _mask_arg(mask, at, (B, Sq, Sk)), window, sinks, ws.data_ptr(),
+                ws.numel() * ws.element_size(), _stream_on(at, stream))
+    finally:
+        if back is not None:
+            torch.cuda.set_device(back)
+    if rc:
+        raise AttnError(rc, "attn_bwd_checkpoint")
     return dq, dk, dv

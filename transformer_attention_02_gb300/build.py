@@ -2,7 +2,7 @@
 
 The translation units (the host ABI, the host-buffer pipeline, the attention
 block's GEMM and LayerNorm, the families of attention-kernel variants, the
-paged cache's append and attention, the backward pass) are compiled in parallel to objects under
+paged cache's append and attention, the backward pass, checkpoints, rotary axes) are compiled in parallel to objects under
 ``_build/`` and linked into one shared library; one -gencode, no cmake. Beside
 it stands ``_binding.so``, a small Python module over that library for the calls
 of a decode step (g++, against PyTorch's headers). The results sit next to this
@@ -28,11 +28,12 @@ SOURCES = [os.path.join(CSRC, f) for f in
             "fwd_rope_f16.cu", "fwd_pack_bf16.cu", "fwd_pack_f16.cu", "fwd_window_bf16.cu",
             "fwd_window_f16.cu", "paged_api.cu", "paged_append.cu", "paged_gather.cu",
             "paged_attn_bf16.cu", "paged_attn_f16.cu", "paged_attn_e4m3.cu", "bwd_api.cu", "bwd_prep.cu",
-            "bwd_bf16_d64.cu", "bwd_bf16_d128.cu", "bwd_f16_d64.cu", "bwd_f16_d128.cu")]
+            "bwd_bf16_d64.cu", "bwd_bf16_d128.cu", "bwd_f16_d64.cu", "bwd_f16_d128.cu",
+            "checkpoint.cu", "rope_axes.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in
                      ("attn_kernel.cuh", "ptx.cuh", "attn_launch.h", "attn_fwd_inst.cuh", "block_params.h",
                       "gemm_kernel.cuh", "early_launch.h", "paged_params.h", "paged_attn.cuh", "bwd_params.h",
-                      "bwd_kernel.cuh", "bwd_inst.cuh")] + [
+                      "bwd_kernel.cuh", "bwd_inst.cuh", "checkpoint_params.h", "e4m3.cuh")] + [
     os.path.join(ROOT, "include", "attn.h")]
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -7,6 +7,7 @@
 #include "../../include/attn.h"
 #include "attn_launch.h"
 #include "bwd_params.h"
+#include "checkpoint_params.h"
 
 namespace {
 
@@ -66,7 +67,7 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
              void* dk, void* dv, long long q_stride, long long k_stride, long long v_stride, long long dq_stride,
              long long dk_stride, long long dv_stride, int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale,
              int mask_kind, const float* mask, int window, int sinks, void* workspace, size_t workspace_bytes,
-             cudaStream_t stream, bool bf16) {
+             cudaStream_t stream, bool bf16, bool check_only = false) {
     int rc = check_sizes(B, Hq, Hkv, Sq, Sk, D);
     if (rc != ATTN_OK) return rc;
     if (mask_kind < ATTN_MASK_NONE || mask_kind > ATTN_MASK_CAUSAL_ADDITIVE || window < 0 || sinks < 0)
@@ -92,6 +93,7 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
     }
     if (!workspace || !aligned(workspace, kWorkspaceAlign) || workspace_bytes < bwd_workspace(B, Hq, Sq, mask_kind))
         return ATTN_ERR_INVALID_ARG;
+    if (check_only) return ATTN_OK;
 
     DeviceState dev{};
     rc = device_state(&dev);
@@ -161,9 +163,147 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
     return bf16 ? launch_both<64, true, false>(dev, maps, p, counters, stream) : launch_both<64, false, false>(dev, maps, p, counters, stream);
 }
 
+// ----------------------------------------------------- 8-bit checkpoints
+
+int check_vectors(const void* x, long long stride, const void* codes, const float* scale, int B, int S, int H, int D) {
+    if (B < 0 || S < 0 || H < 0 || D <= 0) return ATTN_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)B * S * H == 0) return ATTN_OK;
+    if (!x || !codes || !scale || !aligned(x, 16) || !aligned(codes, 16) || !aligned(scale, 4)) return ATTN_ERR_INVALID_ARG;
+    return stride >= (long long)H * D && stride % 8 == 0 ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+}
+
+checkpoint::Tensor vectors_of(const void* x, long long stride, const void* codes, const float* scale, int B, int S, int H) {
+    checkpoint::Tensor t;
+    t.x = static_cast<uint16_t*>(const_cast<void*>(x));
+    t.codes = static_cast<uint8_t*>(const_cast<void*>(codes));
+    t.scale = const_cast<float*>(scale);
+    t.stride = stride;
+    t.tokens = (long long)B * S;
+    t.H = H;
+    return t;
+}
+
+int convert(bool store, const void* x, long long stride, const void* codes, const float* scale, int B, int S, int H, int D,
+            cudaStream_t stream, bool bf16) {
+    int rc = check_vectors(x, stride, codes, scale, B, S, H, D);
+    if (rc != ATTN_OK || (long long)B * S * H == 0) return rc;
+    DeviceState dev{};
+    if ((rc = device_state(&dev)) != ATTN_OK) return rc;
+    const checkpoint::Tensor t = vectors_of(x, stride, codes, scale, B, S, H);
+    return store ? checkpoint::launch_store(t, D, bf16, dev.num_sms, stream)
+                 : checkpoint::launch_load(&t, 1, D, bf16, dev.num_sms, stream);
+}
+
+// Workspace of a backward pass from checkpoints: Q, K, V and O in 16 bits, lse, then the backward pass's own.
+struct CheckpointLayout {
+    size_t k = 0, v = 0, o = 0, lse = 0, bwd = 0, total = 0;
+};
+CheckpointLayout checkpoint_layout(int B, int Hq, int Hkv, int Sq, int Sk, int D, int mask_kind) {
+    CheckpointLayout l;
+    const size_t q = align_up((size_t)B * Sq * Hq * D * 2), kv = align_up((size_t)B * Sk * Hkv * D * 2);
+    l.k = q;
+    l.v = l.k + kv;
+    l.o = l.v + kv;
+    l.lse = l.o + q;
+    l.bwd = l.lse + align_up((size_t)B * Hq * Sq * sizeof(float));
+    l.total = l.bwd + bwd_workspace(B, Hq, Sq, mask_kind);
+    return l;
+}
+
+int bwd_checkpoint_impl(const void* d_o, const void* q8, const void* k8, const void* v8, const float* q_scale,
+                        const float* k_scale, const float* v_scale, void* dq, void* dk, void* dv, long long dq_stride,
+                        long long dk_stride, long long dv_stride, int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale,
+                        int mask_kind, const float* mask, int window, int sinks, void* workspace, size_t workspace_bytes,
+                        cudaStream_t stream, bool bf16) {
+    int rc = check_sizes(B, Hq, Hkv, Sq, Sk, D);
+    if (rc != ATTN_OK) return rc;
+    const long long qs = (long long)Hq * D, ks = (long long)Hkv * D;
+    char* const ws = static_cast<char*>(workspace);
+    const bool empty = (long long)B * Sq * Hq == 0 || (long long)B * Sk == 0;
+    if (empty)                                            // (no pair of a query and a key: nothing is read)
+        return bwd_impl(d_o, q8, k8, v8, d_o, q_scale, dq, dk, dv, qs, ks, ks, dq_stride, dk_stride, dv_stride, B, Hq, Hkv, Sq,
+                        Sk, D, scale, mask_kind, mask, window, sinks, workspace, workspace_bytes, stream, bf16);
+    if ((rc = check_vectors(q8, qs, q8, q_scale, B, Sq, Hq, D)) != ATTN_OK ||
+        (rc = check_vectors(k8, ks, k8, k_scale, B, Sk, Hkv, D)) != ATTN_OK ||
+        (rc = check_vectors(v8, ks, v8, v_scale, B, Sk, Hkv, D)) != ATTN_OK)
+        return rc;
+    if (!workspace || !aligned(workspace, kWorkspaceAlign)) return ATTN_ERR_INVALID_ARG;
+    if (mask_kind < ATTN_MASK_NONE || mask_kind > ATTN_MASK_CAUSAL_ADDITIVE) return ATTN_ERR_INVALID_ARG;
+    const CheckpointLayout l = checkpoint_layout(B, Hq, Hkv, Sq, Sk, D, mask_kind);
+    if (workspace_bytes < l.total) return ATTN_ERR_INVALID_ARG;
+    float* const lse = reinterpret_cast<float*>(ws + l.lse);
+    // Everything is checked before the first launch: the backward pass's own arguments here, the forward pass's are among them.
+    rc = bwd_impl(d_o, ws, ws + l.k, ws + l.v, ws + l.o, lse, dq, dk, dv, qs, ks, ks, dq_stride, dk_stride, dv_stride, B, Hq, Hkv,
+                  Sq, Sk, D, scale, mask_kind, mask, window, sinks, ws + l.bwd, l.total - l.bwd, stream, bf16, true);
+    if (rc != ATTN_OK) return rc;
+    DeviceState dev{};
+    if ((rc = device_state(&dev)) != ATTN_OK) return rc;
+    const checkpoint::Tensor t[3] = {vectors_of(ws, qs, q8, q_scale, B, Sq, Hq), vectors_of(ws + l.k, ks, k8, k_scale, B, Sk, Hkv),
+                                     vectors_of(ws + l.v, ks, v8, v_scale, B, Sk, Hkv)};
+    rc = checkpoint::launch_load(t, 3, D, bf16, dev.num_sms, stream);
+    if (rc != ATTN_OK) return rc;
+    const attn_stream_t s = reinterpret_cast<attn_stream_t>(stream);
+    if (window > 0)
+        rc = (bf16 ? attn_fwd_window : attn_fwd_window_f16)(ws, ws + l.k, ws + l.v, ws + l.o, lse, B, Hq, Hkv, Sq, Sk, D, scale,
+                                                            window, sinks, s);
+    else
+        rc = (bf16 ? attn_fwd : attn_fwd_f16)(ws, ws + l.k, ws + l.v, ws + l.o, lse, B, Hq, Hkv, Sq, Sk, D, scale, mask_kind, mask, s);
+    if (rc != ATTN_OK) return rc;
+    return bwd_impl(d_o, ws, ws + l.k, ws + l.v, ws + l.o, lse, dq, dk, dv, qs, ks, ks, dq_stride, dk_stride, dv_stride, B, Hq, Hkv,
+                    Sq, Sk, D, scale, mask_kind, mask, window, sinks, ws + l.bwd, l.total - l.bwd, stream, bf16);
+}
+
 }  // namespace
 
 extern "C" {
+
+int attn_checkpoint_store(const void* x, long long x_stride, void* codes, float* scale, int B, int S, int H, int D,
+                          attn_stream_t stream) {
+    return convert(true, x, x_stride, codes, scale, B, S, H, D, reinterpret_cast<cudaStream_t>(stream), true);
+}
+
+int attn_checkpoint_store_f16(const void* x, long long x_stride, void* codes, float* scale, int B, int S, int H, int D,
+                              attn_stream_t stream) {
+    return convert(true, x, x_stride, codes, scale, B, S, H, D, reinterpret_cast<cudaStream_t>(stream), false);
+}
+
+int attn_checkpoint_load(const void* codes, const float* scale, void* x, long long x_stride, int B, int S, int H, int D,
+                         attn_stream_t stream) {
+    return convert(false, x, x_stride, codes, scale, B, S, H, D, reinterpret_cast<cudaStream_t>(stream), true);
+}
+
+int attn_checkpoint_load_f16(const void* codes, const float* scale, void* x, long long x_stride, int B, int S, int H, int D,
+                             attn_stream_t stream) {
+    return convert(false, x, x_stride, codes, scale, B, S, H, D, reinterpret_cast<cudaStream_t>(stream), false);
+}
+
+int attn_bwd_checkpoint(const void* d_o, const void* q8, const void* k8, const void* v8, const float* q_scale,
+                        const float* k_scale, const float* v_scale, void* dq, void* dk, void* dv, long long dq_stride,
+                        long long dk_stride, long long dv_stride, int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale,
+                        int mask_kind, const float* mask, int window, int sinks, void* workspace, size_t workspace_bytes,
+                        attn_stream_t stream) {
+    return bwd_checkpoint_impl(d_o, q8, k8, v8, q_scale, k_scale, v_scale, dq, dk, dv, dq_stride, dk_stride, dv_stride, B, Hq,
+                               Hkv, Sq, Sk, D, scale, mask_kind, mask, window, sinks, workspace, workspace_bytes,
+                               reinterpret_cast<cudaStream_t>(stream), true);
+}
+
+int attn_bwd_checkpoint_f16(const void* d_o, const void* q8, const void* k8, const void* v8, const float* q_scale,
+                            const float* k_scale, const float* v_scale, void* dq, void* dk, void* dv, long long dq_stride,
+                            long long dk_stride, long long dv_stride, int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                            float scale, int mask_kind, const float* mask, int window, int sinks, void* workspace,
+                            size_t workspace_bytes, attn_stream_t stream) {
+    return bwd_checkpoint_impl(d_o, q8, k8, v8, q_scale, k_scale, v_scale, dq, dk, dv, dq_stride, dk_stride, dv_stride, B, Hq,
+                               Hkv, Sq, Sk, D, scale, mask_kind, mask, window, sinks, workspace, workspace_bytes,
+                               reinterpret_cast<cudaStream_t>(stream), false);
+}
+
+size_t attn_bwd_checkpoint_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D, int mask_kind) {
+    if (check_sizes(B, Hq, Hkv, Sq, Sk, D) != ATTN_OK || mask_kind < ATTN_MASK_NONE || mask_kind > ATTN_MASK_CAUSAL_ADDITIVE)
+        return 0;
+    if ((long long)B * Sq * Hq == 0 || Sk == 0) return 0;
+    return checkpoint_layout(B, Hq, Hkv, Sq, Sk, D, mask_kind).total;
+}
 
 int attn_bwd(const void* d_o, const void* q, const void* k, const void* v, const void* o, const float* lse, void* dq,
              void* dk, void* dv, long long q_stride, long long k_stride, long long v_stride, long long dq_stride,

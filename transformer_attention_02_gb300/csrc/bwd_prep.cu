@@ -12,24 +12,11 @@
 #include "../../include/attn.h"
 #include "attn_kernel.cuh"
 #include "bwd_params.h"
+#include "e4m3.cuh"
 
 namespace attn {
 namespace bwd {
 namespace {
-
-template <bool BF16>
-__device__ __forceinline__ float2 widen(uint32_t w) {
-    float2 f;
-    if (BF16) {
-        f.x = __uint_as_float(w << 16);
-        f.y = __uint_as_float(w & 0xffff0000u);
-    } else {
-        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
-            : "=f"(f.x), "=f"(f.y)
-            : "r"(w));
-    }
-    return f;
-}
 
 template <bool BF16>
 __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
@@ -48,8 +35,8 @@ constexpr int kRows = 4;            // rows of a lane group in flight
 constexpr int kSteps = 4;           // times a lane group takes kRows rows of its block's stretch
 
 // A block takes stretches of consecutive rows, so that a row's place (b, i, h) is the stretch's first one, found by 64-bit
-// divisions once, and small steps from it. Measured: 4 x 2048 tokens of 32 heads of 128 26 us (134 MB, 5.2 TB/s); with
-// 64-bit divisions for every row 45 us.
+// divisions once, and small steps from it. Measured: 4 x 2048 tokens of 32 heads of 128 33 us, 8 x 4096 tokens 98
+// us (5.5 TB/s); with 64-bit divisions for every row 45 and 160.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256, 4) bwd_prep_kernel(const PrepParams p) {
     constexpr int kLanes = D / 8;                        // lanes of a row
