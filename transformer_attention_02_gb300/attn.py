@@ -1040,6 +1040,12 @@ def attention_backward(d_o, q, k, v, o, lse, *, causal: bool = False, mask=None,
     sinks, scale: those of the forward call; the mask has no gradient. workspace: optional uint8 CUDA tensor of at least
     attn_bwd_workspace_bytes bytes.
     """
+    if _native is not None and stream is None:
+        done = _native.attention_backward(d_o, q, k, v, o, lse, causal, mask, window, sinks, scale, dq, dk, dv, workspace)
+        if done is not None:
+            if done.__class__ is int:
+                raise AttnError(done, "attn_bwd")
+            return done
     at = _device_of(q, "q")
     for name, t in (("k", k), ("v", v), ("o", o), ("d_o", d_o)):
         if t.dtype is not q.dtype or t.dim() != 4:
@@ -1117,6 +1123,12 @@ def rope_axes(q, k, table, positions, sections, *, inverse: bool = False, q_out=
     of a gradient. q, k: bf16 or fp16, contiguous or evenly spaced slices of a packed projection; so may be q_out and
     k_out (new contiguous tensors by default; q and k themselves: in place). Returns (q_out, k_out), or q_out without k.
     """
+    if _native is not None and stream is None:
+        done = _native.rope_axes(q, k, table, positions, sections, inverse, q_out, k_out)
+        if done is not None:
+            if done.__class__ is int:
+                raise AttnError(done, "attn_rope_axes")
+            return done
     at = _device_of(q, "q")
     torch = _torch
     B, S, Hq, D = q.shape
@@ -1161,6 +1173,12 @@ def checkpoint_store(x, *, codes=None, scale=None, stream=None):
     codes: float8_e4m3fn (B, S, H, D), value / scale; scale: FP32 (B, S, H), a power of two for each head vector, the
     smallest with max |x| <= 448 * scale.
     """
+    if _native is not None and stream is None:
+        done = _native.checkpoint_store(x, codes, scale)
+        if done is not None:
+            if done.__class__ is int:
+                raise AttnError(done, "attn_checkpoint_store")
+            return done
     at = _device_of(x, "x")
     torch = _torch
     B, S, H, D = x.shape

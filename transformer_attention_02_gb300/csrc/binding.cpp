@@ -1,4 +1,5 @@
-// The per-step calls (kv_append, attention_paged, attention_window) from Python
+// The per-step calls (kv_append, attention_paged, attention_window, rope_axes, and
+// those of a short training step: attention_backward, checkpoint_store) from Python
 // tensors to the C ABI without the interpreter in between. A decode step makes
 // two such calls a layer, each of a few microseconds on the GPU: the checks of
 // a call cost 3 us in Python and its conversion by ctypes 2 us, 0.5 us here.
@@ -263,12 +264,186 @@ PyObject* attention_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// A result of `like`'s shape and type on device `at`: the given one or a new one, and its token stride.
+bool result(PyObject* o, const Tensor& like, int at, Tensor* t, long long* stride) {
+    if (o == Py_None) {
+        *t = at::empty(like.sizes(), at::TensorOptions().dtype(like.scalar_type()).device(like.device()));
+    } else {
+        const Tensor* g = plain(o);
+        if (!g || !g->defined() || !g->is_cuda() || g->device().index() != at || g->scalar_type() != like.scalar_type() ||
+            g->sizes() != like.sizes())
+            return false;
+        *t = *g;
+    }
+    return (*stride = token_stride(*t)) >= 0;
+}
+
+// A 4-D tensor of x's type and device with even tokens.
+bool tokens(const Tensor* t, const Tensor& x, int at, long long* stride) {
+    return t && t->defined() && t->is_cuda() && t->device().index() == at && t->scalar_type() == x.scalar_type() &&
+           t->dim() == 4 && fits(t->sizes()) && (*stride = token_stride(*t)) >= 0;
+}
+
+PyObject* given(PyObject* o, const Tensor& t) { return o != Py_None ? Py_NewRef(o) : THPVariable_Wrap(t); }
+
+// attention_backward(d_o, q, k, v, o, lse, causal, mask, window, sinks, scale, dq, dk, dv, workspace): (dq, dk, dv), a
+// status, or None
+PyObject* attention_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 15) Py_RETURN_NONE;
+    const Tensor *g = plain(a[0]), *q = plain(a[1]), *k = plain(a[2]), *v = plain(a[3]), *o = plain(a[4]), *l = plain(a[5]);
+    int at = -1, window, sinks;
+    float scale;
+    cudaStream_t stream;
+    long long st[6];
+    if (!begin(q, &at, &stream) || !tokens(q, *q, at, st) || !tokens(k, *q, at, st + 1) || !tokens(v, *q, at, st + 2))
+        Py_RETURN_NONE;
+    for (const Tensor* t : {g, o})
+        if (!good(t, q->scalar_type(), at) || t->sizes() != q->sizes()) Py_RETURN_NONE;
+    const int B = (int)q->size(0), Sq = (int)q->size(1), Hq = (int)q->size(2), D = (int)q->size(3);
+    const int Sk = (int)k->size(1), Hkv = (int)k->size(2);
+    if (k->size(0) != B || k->size(3) != D || v->sizes() != k->sizes()) Py_RETURN_NONE;
+    if (!good(l, at::kFloat, at) || l->dim() != 3 || l->size(0) != B || l->size(1) != Hq || l->size(2) != Sq) Py_RETURN_NONE;
+    if ((a[6] != Py_True && a[6] != Py_False) || !count(a[8], &window) || !count(a[9], &sinks) || !scale_of(a[10], &scale))
+        Py_RETURN_NONE;
+    const bool causal = a[6] == Py_True;
+    const float* mask = nullptr;
+    if (a[7] != Py_None) {
+        const Tensor* m = plain(a[7]);
+        if (!good(m, at::kFloat, at) || m->dim() != 3 || m->size(0) != B || m->size(1) != Sq || m->size(2) != Sk) Py_RETURN_NONE;
+        mask = static_cast<const float*>(m->data_ptr());
+    }
+    if (window > 0 && (!causal || a[7] != Py_None)) Py_RETURN_NONE;
+    const int kind = (causal ? ATTN_MASK_CAUSAL : ATTN_MASK_NONE) + (a[7] != Py_None ? ATTN_MASK_ADDITIVE : 0);
+    Tensor ws;
+    if (a[14] != Py_None) {
+        const Tensor* t = plain(a[14]);
+        if (!t || !t->defined() || !t->is_cuda() || t->device().index() != at || !t->is_contiguous()) Py_RETURN_NONE;
+        ws = *t;
+    }
+    Tensor dq, dk, dv;
+    if (!result(a[11], *q, at, &dq, st + 3) || !result(a[12], *k, at, &dk, st + 4) || !result(a[13], *k, at, &dv, st + 5))
+        Py_RETURN_NONE;
+    if (a[14] == Py_None) {
+        const size_t size = std::max<size_t>(1, attn_bwd_workspace_bytes(B, Hq, Hkv, Sq, Sk, D, kind));
+        ws = at::empty({(int64_t)size}, at::TensorOptions().dtype(at::kByte).device(q->device()));
+    }
+    const void *gp = g->data_ptr(), *qp = q->data_ptr(), *kp = k->data_ptr(), *vp = v->data_ptr(), *op = o->data_ptr();
+    const float* lp = static_cast<const float*>(l->data_ptr());
+    void *dqp = dq.data_ptr(), *dkp = dk.data_ptr(), *dvp = dv.data_ptr(), *wp = ws.data_ptr();
+    const size_t bytes = ws.nbytes();
+    const auto fn = q->scalar_type() == at::kBFloat16 ? attn_bwd : attn_bwd_f16;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = fn(gp, qp, kp, vp, op, lp, dqp, dkp, dvp, st[0], st[1], st[2], st[3], st[4], st[5], B, Hq, Hkv, Sq, Sk, D, scale, kind,
+            mask, window, sinks, wp, bytes, reinterpret_cast<attn_stream_t>(stream));
+    Py_END_ALLOW_THREADS
+    if (rc != ATTN_OK) return PyLong_FromLong(rc);
+    PyObject* r = PyTuple_New(3);
+    if (!r) return nullptr;
+    PyTuple_SET_ITEM(r, 0, given(a[11], dq));
+    PyTuple_SET_ITEM(r, 1, given(a[12], dk));
+    PyTuple_SET_ITEM(r, 2, given(a[13], dv));
+    return r;
+    END_HANDLE_TH_ERRORS
+}
+
+// rope_axes(q, k, table, positions, sections, inverse, q_out, k_out): (q_out, k_out), q_out without k, a status, or None
+PyObject* rope_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 8) Py_RETURN_NONE;
+    const Tensor *q = plain(a[0]), *table = plain(a[2]), *pos = plain(a[3]);
+    int at = -1, sections[4], axes = 0;
+    cudaStream_t stream;
+    long long qs, ks = 0, qos, kos = 0;
+    if (!begin(q, &at, &stream) || !tokens(q, *q, at, &qs)) Py_RETURN_NONE;
+    const int B = (int)q->size(0), S = (int)q->size(1), Hq = (int)q->size(2), D = (int)q->size(3);
+    if (!PyTuple_CheckExact(a[4]) && !PyList_CheckExact(a[4])) Py_RETURN_NONE;
+    const Py_ssize_t parts = PySequence_Fast_GET_SIZE(a[4]);
+    long long pairs = 0;
+    for (; axes < parts && axes < 4; ++axes) {
+        if (!count(PySequence_Fast_GET_ITEM(a[4], axes), sections + axes) || sections[axes] > 512) Py_RETURN_NONE;
+        pairs += sections[axes];
+    }
+    if (parts < 1 || parts > 4 || 2 * pairs != D) Py_RETURN_NONE;
+    if (!good(pos, at::kInt, at) || pos->dim() != 3 || pos->size(0) != B || pos->size(1) != S || pos->size(2) != axes) Py_RETURN_NONE;
+    if (!good(table, at::kFloat, at) || table->dim() != 3 || table->size(1) != D / 2 || table->size(2) != 2 ||
+        table->size(0) == 0 || table->size(0) > INT_MAX || (a[5] != Py_True && a[5] != Py_False))
+        Py_RETURN_NONE;
+    const Tensor* k = nullptr;
+    if (a[1] != Py_None) {
+        k = plain(a[1]);
+        if (!tokens(k, *q, at, &ks) || k->size(0) != B || k->size(1) != S || k->size(3) != D) Py_RETURN_NONE;
+    } else if (a[7] != Py_None) {
+        Py_RETURN_NONE;
+    }
+    Tensor qo, ko;
+    if (!result(a[6], *q, at, &qo, &qos) || (k && !result(a[7], *k, at, &ko, &kos))) Py_RETURN_NONE;
+    const void *qp = q->data_ptr(), *kp = k ? k->data_ptr() : nullptr;
+    void *qop = qo.data_ptr(), *kop = k ? ko.data_ptr() : nullptr;
+    const float* tp = static_cast<const float*>(table->data_ptr());
+    const int *pp = static_cast<const int*>(pos->data_ptr()), max_pos = (int)table->size(0), Hkv = k ? (int)k->size(2) : 0;
+    const auto fn = q->scalar_type() == at::kBFloat16 ? attn_rope_axes : attn_rope_axes_f16;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = fn(qp, qop, qs, qos, kp, kop, ks, kos, B, S, Hq, Hkv, D, tp, max_pos, pp, sections, axes, a[5] == Py_True,
+            reinterpret_cast<attn_stream_t>(stream));
+    Py_END_ALLOW_THREADS
+    if (rc != ATTN_OK) return PyLong_FromLong(rc);
+    if (!k) return given(a[6], qo);
+    PyObject* r = PyTuple_New(2);
+    if (!r) return nullptr;
+    PyTuple_SET_ITEM(r, 0, given(a[6], qo));
+    PyTuple_SET_ITEM(r, 1, given(a[7], ko));
+    return r;
+    END_HANDLE_TH_ERRORS
+}
+
+// checkpoint_store(x, codes, scale): (codes, scale), a status, or None
+PyObject* checkpoint_store(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (n != 3) Py_RETURN_NONE;
+    const Tensor* x = plain(a[0]);
+    int at = -1;
+    cudaStream_t stream;
+    long long xs;
+    if (!begin(x, &at, &stream) || !tokens(x, *x, at, &xs)) Py_RETURN_NONE;
+    const int B = (int)x->size(0), S = (int)x->size(1), H = (int)x->size(2), D = (int)x->size(3);
+    Tensor codes, scale;
+    if (a[1] != Py_None) {
+        const Tensor* t = plain(a[1]);
+        if (!good(t, at::kFloat8_e4m3fn, at) || t->sizes() != x->sizes()) Py_RETURN_NONE;
+        codes = *t;
+    }
+    if (a[2] != Py_None) {
+        const Tensor* t = plain(a[2]);
+        if (!good(t, at::kFloat, at) || t->dim() != 3 || t->size(0) != B || t->size(1) != S || t->size(2) != H) Py_RETURN_NONE;
+        scale = *t;
+    }
+    if (a[1] == Py_None) codes = at::empty(x->sizes(), at::TensorOptions().dtype(at::kFloat8_e4m3fn).device(x->device()));
+    if (a[2] == Py_None) scale = at::empty({B, S, H}, at::TensorOptions().dtype(at::kFloat).device(x->device()));
+    const void* xp = x->data_ptr();
+    void* cp = codes.data_ptr();
+    float* sp = static_cast<float*>(scale.data_ptr());
+    const auto fn = x->scalar_type() == at::kBFloat16 ? attn_checkpoint_store : attn_checkpoint_store_f16;
+    int rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = fn(xp, xs, cp, sp, B, S, H, D, reinterpret_cast<attn_stream_t>(stream));
+    Py_END_ALLOW_THREADS
+    return rc != ATTN_OK ? PyLong_FromLong(rc) : pair(a[1], a[2], codes, scale);
+    END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
     {"kv_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_append)), METH_FASTCALL, nullptr},
     {"attention_paged", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention_paged)), METH_FASTCALL,
      nullptr},
     {"attention_window", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention_window)), METH_FASTCALL,
      nullptr},
+    {"attention_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention_backward)), METH_FASTCALL,
+     nullptr},
+    {"rope_axes", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope_axes)), METH_FASTCALL, nullptr},
+    {"checkpoint_store", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(checkpoint_store)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

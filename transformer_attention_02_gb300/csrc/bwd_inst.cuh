@@ -15,8 +15,8 @@ int launch(bool& attr_set, Kernel kernel, int smem, const CUtensorMap& q, const 
             return ATTN_ERR_CUDA;
         attr_set = true;
     }
-    kernel<<<grid, kThreads, smem, stream>>>(q, k, v, d_o, p);
-    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    return launch_early(kernel, (unsigned)grid, (unsigned)kThreads, (size_t)smem, stream, q, k, v, d_o, p) == cudaSuccess
+               ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 template <int D, bool BF16, bool ADDITIVE>

@@ -344,6 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const SyncCtx sc{abort_flag, p.status, p.timeout_ns};
+    wait_for_inputs();                                // nothing above touches global memory
+    let_next_start();
 
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
@@ -560,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // a warp's lanes are neighbouring keys: each load is one line of the mask
                     const float* at = p.mask + ((size_t)w.b * p.Sq + m0) * p.Sk + key;
 #pragma unroll
-                    for (int c = 0; c < kCols; ++c) x[c] = (key < p.Sk && m0 + c < p.Sq) ? __ldg(at + (size_t)c * p.Sk) : 0.f;
+                    for (int c = 0; c < kCols; ++c) x[c] = (key < p.Sk && m0 + c < p.Sq) ? at[(size_t)c * p.Sk] : 0.f;
                 }
                 if (!(alive = warp_wait(bar(C::bQ + q.at), q.parity(), sc))) break;
                 const float4* nl = reinterpret_cast<const float4*>(smem_ptr + C::kRowOff + q.at * kRowBytes) + kCols / 4 * wg;
@@ -760,6 +762,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const SyncCtx sc{abort_flag, p.status, p.timeout_ns};
+    wait_for_inputs();                                // nothing above touches global memory
+    let_next_start();
 
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
@@ -1023,12 +1027,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (vec) {
 #pragma unroll
                         for (int c = 0; c < kCols; c += 4) {
-                            const float4 m = ptx::ld_global_nc_v4(mrow + key0 + c);
+                            const float4 m = *reinterpret_cast<const float4*>(mrow + key0 + c);
                             x[c] = m.x, x[c + 1] = m.y, x[c + 2] = m.z, x[c + 3] = m.w;
                         }
                     } else {
 #pragma unroll
-                        for (int c = 0; c < kCols; ++c) x[c] = mrow != nullptr && key0 + c < p.Sk ? __ldg(mrow + key0 + c) : 0.f;
+                        for (int c = 0; c < kCols; ++c) x[c] = mrow != nullptr && key0 + c < p.Sk ? mrow[key0 + c] : 0.f;
                     }
                 }
                 if (!warp_wait(bar(C::bS + (su & 1u)), (su >> 1) & 1u, sc)) return false;

@@ -42,6 +42,8 @@ __global__ void __launch_bounds__(256, 4) bwd_prep_kernel(const PrepParams p) {
     constexpr int kLanes = D / 8;                        // lanes of a row
     constexpr int kGroups = 256 / kLanes;
     constexpr int kStretch = kGroups * kRows * kSteps;
+    wait_for_inputs();
+    let_next_start();
     if (blockIdx.x == 0 && threadIdx.x < 2) p.counters[threadIdx.x] = 0u;
     const long long rows = (long long)p.B * p.Sq * p.Hq;
     const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
@@ -100,8 +102,7 @@ int launch_prep(const PrepParams& p, bool bf16, int num_sms, cudaStream_t stream
     const long long rows = (long long)p.B * p.Sq * p.Hq;
     const unsigned grid = (unsigned)std::max(1LL, std::min((rows + per_block - 1) / per_block, 4LL * num_sms));
     auto run = [&](auto kernel) {
-        kernel<<<grid, 256, 0, stream>>>(p);
-        return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+        return launch_early(kernel, grid, 256u, (size_t)0, stream, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
     };
     if (p.D == 128) return bf16 ? run(bwd_prep_kernel<128, true>) : run(bwd_prep_kernel<128, false>);
     return bf16 ? run(bwd_prep_kernel<64, true>) : run(bwd_prep_kernel<64, false>);

@@ -53,6 +53,8 @@ __device__ __forceinline__ float finite_abs(float x) {
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) store_kernel(const Tensor t) {
+    wait_for_inputs();
+    let_next_start();
     constexpr int kLanes = D / 16;
     const int lane = threadIdx.x % kLanes;
     const long long vectors = t.tokens * t.H;
@@ -106,6 +108,8 @@ struct Tensors {
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) load_kernel(const __grid_constant__ Tensors p) {
+    wait_for_inputs();
+    let_next_start();
     constexpr int kLanes = D / 16;
     const int b1 = p.blocks[0], b2 = p.blocks[0] + p.blocks[1];
     const int which = (int)blockIdx.x < b1 ? 0 : (int)blockIdx.x < b2 ? 1 : 2;
@@ -152,8 +156,8 @@ int blocks_for(const Tensor& t, int D, int most) {
 
 int launch_store(const Tensor& t, int D, bool bf16, int num_sms, cudaStream_t stream) {
     return for_type(D, bf16, [&](auto d, auto b) {
-        store_kernel<decltype(d)::value, decltype(b)::value><<<std::max(1, blocks_for(t, D, 5 * num_sms)), 256, 0, stream>>>(t);
-        return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+        return launch_early(store_kernel<decltype(d)::value, decltype(b)::value>, (unsigned)std::max(1, blocks_for(t, D, 5 * num_sms)),
+                            256u, (size_t)0, stream, t) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
     });
 }
 
@@ -164,8 +168,8 @@ int launch_load(const Tensor* t, int n, int D, bool bf16, int num_sms, cudaStrea
         p.blocks[i] = blocks_for(t[i], D, 5 * num_sms);
     }
     return for_type(D, bf16, [&](auto d, auto b) {
-        load_kernel<decltype(d)::value, decltype(b)::value><<<p.blocks[0] + p.blocks[1] + p.blocks[2], 256, 0, stream>>>(p);
-        return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+        return launch_early(load_kernel<decltype(d)::value, decltype(b)::value>, (unsigned)(p.blocks[0] + p.blocks[1] + p.blocks[2]),
+                            256u, (size_t)0, stream, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
     });
 }
 

@@ -69,6 +69,8 @@ __device__ __forceinline__ uint4 turn(const uint4& w, const Angles& a) {
 // FIXED: the pieces of a head vector divide 32.
 template <bool BF16, bool FIXED>
 __global__ void __launch_bounds__(256) rope_axes_kernel(const AxesParams p) {
+    wait_for_inputs();
+    let_next_start();
     const int lane = threadIdx.x & 31;
     const int pieces = p.D / 8;                               // of a head vector
     const long long units = p.tokens * p.parts;
@@ -200,8 +202,7 @@ int rope_axes_impl(const void* q, void* q_out, long long q_stride, long long q_o
     const long long units = tokens * p.parts;
     const unsigned grid = (unsigned)std::max(1LL, std::min((units + 7) / 8, 8LL * dev.num_sms));
     auto run = [&](auto kernel) {
-        kernel<<<grid, 256, 0, stream>>>(p);
-        return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+        return launch_early(kernel, grid, 256u, (size_t)0, stream, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
     };
     const bool fixed = 32 % (D / 8) == 0;
     while ((8 << p.shift) < D) ++p.shift;
