@@ -108,25 +108,15 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
     unsigned int* const counters = static_cast<unsigned int*>(workspace);
     char* const ws = static_cast<char*>(workspace) + kWorkspaceAlign;
 
-    bwd::PrepParams pp{};
-    pp.o = static_cast<const uint16_t*>(o);
-    pp.d_o = static_cast<const uint16_t*>(d_o);
-    pp.lse = additive ? nullptr : lse;
-    pp.neg_lse = reinterpret_cast<float*>(ws);
-    pp.neg_delta = reinterpret_cast<float*>(ws + stat);
-    pp.counters = counters;
-    pp.B = B;
-    pp.Hq = Hq;
-    pp.Sq = Sq;
-    pp.Sp = (int)bwd::padded_rows(Sq);
-    pp.D = D;
-    rc = bwd::launch_prep(pp, bf16, dev.num_sms, stream);
+    rc = bwd::launch_begin(counters, stream);
     if (rc != ATTN_OK) return rc;
 
     constexpr int kAllKeys = 1 << 30;                     // a longer window hides nothing; differences stay in 32 bits
     bwd::BwdParams p{};
-    p.neg_lse = pp.neg_lse;
-    p.neg_delta = pp.neg_delta;
+    p.o = static_cast<const uint16_t*>(o);
+    p.lse = lse;
+    p.neg_lse = reinterpret_cast<float*>(ws);
+    p.neg_delta = reinterpret_cast<float*>(ws + stat);
     p.inv_sum = additive ? reinterpret_cast<float*>(ws + 2 * stat) : nullptr;
     p.mask = additive ? mask : nullptr;
     p.dq = dq;
@@ -140,9 +130,9 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
     p.Hkv = Hkv;
     p.Sq = Sq;
     p.Sk = Sk;
-    p.Sp = pp.Sp;
+    p.Sp = (int)bwd::padded_rows(Sq);
     p.group = Hq / Hkv;
-    p.n_qb = pp.Sp / bwd::kBlock;
+    p.n_qb = p.Sp / bwd::kBlock;
     p.n_kb = (int)(bwd::padded_rows(Sk) / bwd::kBlock);
     p.off = Sk - Sq;
     p.causal = mask_kind == ATTN_MASK_CAUSAL || mask_kind == ATTN_MASK_CAUSAL_ADDITIVE;

@@ -24,6 +24,10 @@
 // put P and dS back in 16 bits (four warpgroups of 32 columns each; a warp's
 // lanes are 32 rows), warp 16 issues the products, warp 17 the loads.
 //
+// delta and the log-sum-exp in log2 units, negated, are left for the other kernel by bwd_dq_kernel, which has dO at hand: as
+// (B, Hq, Sp) with the rows of a head next to each other and padded to whole blocks, so that 128 of them are one bulk copy.
+// Rows that are none, and rows without a visible key (lse = -inf), get -inf: their probabilities become 2^-inf = 0.
+//
 // P enters its product in the inputs' 16-bit type, as in the forward pass, and
 // so does dS: the tensor cores take both operands in one type. Each is rounded
 // once, from FP32, so that a term is off by half a step of that type, as the
@@ -33,6 +37,9 @@
 #include "../../include/attn.h"
 #include "attn_kernel.cuh"
 #include "bwd_params.h"
+#include "e4m3.cuh"
+
+#include <type_traits>
 
 namespace attn {
 namespace bwd {
@@ -676,14 +683,15 @@ struct QCfg {
     static constexpr int kQOff = 0, kGOff = T::kBytes, kKOff = 2 * T::kBytes, kVOff = kKOff + kK * T::kBytes;
     static constexpr int kBarOff = kVOff + kV * T::kBytes;
     static constexpr int bQ = 0, bQEmpty = 1, bS = 2, bDP = 4, bDPFree = 5, bDS = 6, bAcc = 8, bAccEmpty = 9, bDrain = 10,
-                         bStall = 11, bParts = 12, bWhole = 13, bG = 14, bGEmpty = 15, bTile = 16,
+                         bStall = 11, bParts = 12, bWhole = 13, bG = 14, bGEmpty = 15, bDelta = 16, bTile = 17,
                          bTileEmpty = bTile + kRing, bK = bTileEmpty + kRing, bKEmpty = bK + kK, bV = bKEmpty + kK, bVEmpty = bV + kV,
                          kNumBars = bVEmpty + kV;
     static constexpr int kTmemSlotOff = kBarOff + 8 * kNumBars;
     static constexpr int kAbortOff = kTmemSlotOff + 4;
     static constexpr int kTileOff = kAbortOff + 4;
     static constexpr int kStatOff = (kTileOff + 4 * kRing + 15) / 16 * 16;      // additive mask: [kGroups][128] {maximum, sum}
-    static constexpr int kSmemBytes = kStatOff + (ADDITIVE ? kGroups * 128 * 8 : 0);
+    static constexpr int kDeltaOff = kStatOff + (ADDITIVE ? kGroups * 128 * 8 : 0);       // [128] -delta
+    static constexpr int kSmemBytes = kDeltaOff + 128 * 4;
     static constexpr uint32_t cDQ = 0, cS = 128, cDP = 384;
     static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
@@ -740,7 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < C::kNumBars; ++i) {
             uint32_t count = 1;
             if (i >= C::bTileEmpty && i < C::bTileEmpty + kRing) count = kRingReaders;
-            if (i == C::bDPFree || i == C::bDS || i == C::bDS + 1 || i == C::bAccEmpty) count = kWarps;
+            if (i == C::bDPFree || i == C::bDS || i == C::bDS + 1 || i == C::bAccEmpty || i == C::bDelta) count = kWarps;
+            if (i == C::bGEmpty) count = kWarps + 1;              // the last dP has run, and the warps have delta
             if (i == C::bParts) count = kWarps - 4;
             if (i == C::bWhole) count = 4;
             ptx::mbar_init(bar(i), count);
@@ -774,13 +783,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (t >= 0 && w.n == 0) {
                 zero_rows<D>(static_cast<uint16_t*>(p.dq) + ((long long)w.b * p.Sq + w.m0) * p.dq_stride + w.h * D, p.dq_stride,
                              min(kBlock, p.Sq - w.m0));
-                if (ADDITIVE) {                                   // the other kernel passes over these rows too
-                    const size_t at = ((size_t)w.b * p.Hq + w.h) * p.Sp + w.m0;
-                    for (int e = lane; e < kBlock; e += 32) p.neg_lse[at + e] = p.inv_sum[at + e] = 0.f;
+                // the other kernel passes over these rows too
+                const size_t at = ((size_t)w.b * p.Hq + w.h) * p.Sp + w.m0;
+                for (int e = lane; e < kBlock; e += 32) {
+                    p.neg_delta[at + e] = 0.f;
+                    p.neg_lse[at + e] = ADDITIVE ? 0.f : -INFINITY;
+                    if (ADDITIVE) p.inv_sum[at + e] = 0.f;
                 }
                 continue;
             }
             if (!publish_tile(tiles, t, ring, sc) || t < 0) break;
+            for (int e = lane; e < min(kBlock, p.Sq - w.m0); e += 32) {       // O, for delta: on its way to L2
+                const char* o = reinterpret_cast<const char*>(p.o + (((size_t)w.b * p.Sq + w.m0 + e) * p.Hq + w.h) * D);
+#pragma unroll
+                for (int c = 0; c < 2 * D; c += 128) ptx::prefetch_l2(o + c);
+            }
             if (tiles > 0 && !warp_wait(bar(C::bQEmpty), (tiles - 1) & 1u, sc)) break;
             if (lane == 0) {
                 ptx::mbar_arrive_expect_tx(bar(C::bQ), T::kBytes);
@@ -1014,9 +1031,53 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int lim = p.causal ? min(p.Sk, max(0, row + p.off + 1)) : p.Sk;
             const int low = p.window ? row + p.off - p.window + 1 : 0;
             const float* mrow = ADDITIVE && there ? p.mask + ((size_t)w.b * p.Sq + row) * p.Sk : nullptr;
-            float nl = 0.f, is = 0.f;
-            const float nd = p.neg_delta[at];
-            if (!ADDITIVE) nl = p.neg_lse[at];
+            float nl = 0.f, is = 0.f, nd = 0.f;
+            if (!ADDITIVE) {
+                const float l = there ? p.lse[((size_t)w.b * p.Hq + w.h) * p.Sq + row] : -INFINITY;
+                nl = l == -INFINITY ? -INFINITY : -l * kLog2E;
+            }
+            // delta of the tile's rows, eight a warp, O from device memory (whole lines of it) and dO from its tile
+            constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kPasses = 8 / kAtOnce;              // lanes of a row
+            const int r0 = 8 * warp + lane / kLanes, piece = lane % kLanes;
+            auto fetch_o = [&](uint4 (&o)[kPasses]) {
+                const uint16_t* at_o = p.o + (((size_t)w.b * p.Sq + w.m0 + r0) * p.Hq + w.h) * D + 8 * piece;
+#pragma unroll
+                for (int e = 0; e < kPasses; ++e)
+                    o[e] = w.m0 + r0 + kAtOnce * e < p.Sq
+                               ? __ldcg(reinterpret_cast<const uint4*>(at_o + (size_t)(kAtOnce * e) * p.Hq * D))
+                               : make_uint4(0u, 0u, 0u, 0u);
+            };
+            auto find_delta = [&](const uint4 (&o)[kPasses]) -> bool {
+                if (!warp_wait(bar(C::bG), k & 1u, sc)) return false;
+                float* delta = reinterpret_cast<float*>(smem_ptr + C::kDeltaOff);
+#pragma unroll
+                for (int e = 0; e < kPasses; ++e) {
+                    const int i = r0 + kAtOnce * e;
+                    const uint4 g = *reinterpret_cast<const uint4*>(smem_ptr + C::kGOff + (piece >> 3) * T::kBoxBytes + i * 128 +
+                                                                    (((piece & 7) ^ (i & 7)) << 4));
+                    const uint32_t a[4] = {o[e].x, o[e].y, o[e].z, o[e].w}, c[4] = {g.x, g.y, g.z, g.w};
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        const float2 x = widen<BF16>(a[f]), y = widen<BF16>(c[f]);
+                        s0 = fmaf(x.x, y.x, s0);
+                        s1 = fmaf(x.y, y.y, s1);
+                    }
+                    s0 += s1;
+#pragma unroll
+                    for (int m = kLanes / 2; m > 0; m >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, m);
+                    if (piece == 0) delta[i] = -s0;
+                }
+                warp_arrive(bar(C::bDelta));
+                if (!warp_wait(bar(C::bDelta), k & 1u, sc)) return false;
+                nd = delta[r];
+                warp_arrive(bar(C::bGEmpty));                     // (the next tile's are written after its dO has come)
+                if (wg == 0) {
+                    p.neg_delta[at] = nd;
+                    if (!ADDITIVE) p.neg_lse[at] = nl;
+                }
+                return true;
+            };
 
             // logits in log2 units of block j: S in the buffer of `su`, scaled, masked, hidden keys at -inf
             auto logits = [&](int j, float* x) -> bool {
@@ -1098,13 +1159,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 nl = stat[r].x;
                 is = stat[r].y;
             }
-            for (int j = 0; j < w.n; ++j, ++su, ++dp) {
+            // The first block of a tile is a copy of its own: it has the last tile's dQ and delta to see to.
+            auto block = [&](int j, auto begins) -> bool {
                 float x[kCols];
-                if (!(alive = logits(j, x))) break;
+                uint4 o[kPasses];
+                if constexpr (decltype(begins)::value) fetch_o(o);
+                if (!logits(j, x)) return false;
 #pragma unroll
                 for (int c = 0; c < kCols; ++c) x[c] = ptx::ex2(ADDITIVE ? x[c] + nl : x[c]);
-                if (!ADDITIVE && j == 0 && !(alive = finish())) break;
-                if (!(alive = warp_wait(bar(C::bDP), dp & 1u, sc))) break;
+                if constexpr (decltype(begins)::value) {
+                    if (!ADDITIVE && !finish()) return false;
+                    if (!find_delta(o)) return false;
+                }
+                if (!warp_wait(bar(C::bDP), dp & 1u, sc)) return false;
                 ptx::tc_fence_after_sync();
                 float d[kCols];
                 uint32_t pk[kCols / 2];
@@ -1120,7 +1187,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tmem_st16(tS + 128 * (su & 1u), pk);
                 ptx::tmem_st_wait();
                 warp_arrive_tmem(bar(C::bDS + (su & 1u)));
-            }
+                ++su;
+                ++dp;
+                return true;
+            };
+            alive = block(0, std::true_type{});
+            for (int j = 1; j < w.n && alive; ++j) alive = block(j, std::false_type{});
             if (!alive) break;
             uint16_t* out = static_cast<uint16_t*>(p.dq) + ((long long)w.b * p.Sq + row) * p.dq_stride + w.h * D + 32 * wg;
             done_row = out;

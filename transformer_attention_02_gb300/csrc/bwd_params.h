@@ -1,5 +1,5 @@
 // Host-visible parameters of the attention's backward kernels and their
-// launchers (bwd_prep.cu, bwd_inst.cuh).
+// launchers (bwd_begin.cu, bwd_inst.cuh).
 #pragma once
 
 #include <cuda.h>
@@ -16,10 +16,12 @@ constexpr int kBlock = 128;         // queries and keys of a tile
 inline long long padded_rows(int Sq) { return ((long long)Sq + kBlock - 1) / kBlock * kBlock; }
 
 struct BwdParams {
-    // (B, Hq, Sp) FP32, Sp = padded_rows(Sq), from bwd_prep_kernel; a row that is none holds -inf and 0
-    float* neg_lse;                 // -lse in log2 units; with an additive mask: -(row maximum), from the dQ kernel
+    const uint16_t* o;              // (B, Sq, Hq, D) contiguous
+    const float* lse;               // (B, Hq, Sq)
+    // (B, Hq, Sp) FP32, Sp = padded_rows(Sq), from the dQ kernel to the other one; a row that is none holds -inf and 0
+    float* neg_lse;                 // -lse in log2 units; with an additive mask: -(row maximum)
     float* neg_delta;               // -sum_d dO O
-    float* inv_sum;                 // additive mask only: 1 / row sum, from the dQ kernel
+    float* inv_sum;                 // additive mask only: 1 / row sum
     const float* mask;              // (B, Sq, Sk) FP32 or null
     void *dq, *dk, *dv;             // gradients in the inputs' type
     long long dq_stride, dk_stride, dv_stride;   // elements from token to token
@@ -29,7 +31,7 @@ struct BwdParams {
     int off;                        // Sk - Sq: query i sits at position i + off
     int causal, window, sinks;      // window 0: none (causal with it)
     int n_tiles;
-    unsigned int* counter;          // tiles handed out beyond each CTA's first; the statistics' kernel sets it to 0
+    unsigned int* counter;          // tiles handed out beyond each CTA's first; launch_begin sets it to 0
     int vec8;                       // gradients may be written with 32-byte stores
     int stall;                      // failure-detection test hook, as in the forward kernel
     float scale, scale_log2;
@@ -37,16 +39,8 @@ struct BwdParams {
     unsigned int* status;
 };
 
-struct PrepParams {
-    const uint16_t *o, *d_o;        // (B, Sq, Hq, D) contiguous
-    const float* lse;               // (B, Hq, Sq) or null (additive mask: the dQ kernel finds its own statistics)
-    float *neg_lse, *neg_delta;
-    unsigned int* counters;         // [2]
-    int B, Hq, Sq, Sp, D;
-};
-
 // Launchers; ATTN_OK or ATTN_ERR_CUDA. attr_set: per context and variant, that the kernel's shared memory is set.
-int launch_prep(const PrepParams& p, bool bf16, int num_sms, cudaStream_t stream);
+int launch_begin(unsigned int* counters, cudaStream_t stream);        // two of them to 0
 template <int D, bool BF16, bool ADDITIVE>
 int launch_dq(bool& attr_set, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& d_o,
               const BwdParams& p, int grid, cudaStream_t stream);

@@ -156,7 +156,7 @@ int blocks_for(const Tensor& t, int D, int most) {
 
 int launch_store(const Tensor& t, int D, bool bf16, int num_sms, cudaStream_t stream) {
     return for_type(D, bf16, [&](auto d, auto b) {
-        return launch_early(store_kernel<decltype(d)::value, decltype(b)::value>, (unsigned)std::max(1, blocks_for(t, D, 5 * num_sms)),
+        return launch_early(store_kernel<decltype(d)::value, decltype(b)::value>, (unsigned)std::max(1, blocks_for(t, D, 32 * num_sms)),
                             256u, (size_t)0, stream, t) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
     });
 }
@@ -165,7 +165,7 @@ int launch_load(const Tensor* t, int n, int D, bool bf16, int num_sms, cudaStrea
     Tensors p{};
     for (int i = 0; i < n && i < 3; ++i) {
         p.t[i] = t[i];
-        p.blocks[i] = blocks_for(t[i], D, 5 * num_sms);
+        p.blocks[i] = blocks_for(t[i], D, 32 * num_sms);
     }
     return for_type(D, bf16, [&](auto d, auto b) {
         return launch_early(load_kernel<decltype(d)::value, decltype(b)::value>, (unsigned)(p.blocks[0] + p.blocks[1] + p.blocks[2]),
