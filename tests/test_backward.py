@@ -68,6 +68,11 @@ SHAPES = [
     (1, 8, 2, 700, 700, 128),
     (2, 40, 40, 130, 259, 64),
     (1, 2, 2, 2000, 2100, 128),
+    # few tiles, long walks: cut into parts whose sums are joined
+    (1, 8, 1, 1500, 1500, 64),
+    (1, 1, 1, 40, 6000, 128),
+    (1, 16, 1, 700, 100, 64),
+    (2, 3, 1, 1, 3000, 128),
 ]
 
 
@@ -89,6 +94,7 @@ def test_gradients(shape, causal, dtype):
     ((1, 1, 1, 640, 640, 128), 128, 128),
     ((1, 2, 1, 400, 400, 128), 10 ** 12, 10 ** 12),
     ((1, 2, 1, 1, 1000, 128), 7, 3),
+    ((1, 8, 1, 2000, 2000, 64), 700, 5),
 ])
 def test_windows(shape, window, sinks):
     w = dict(causal=True, window=min(window, 1 << 30), sinks=min(sinks, 1 << 30))
@@ -355,7 +361,10 @@ def test_refusals_on_the_host(fn, kw, code):
 
 
 def test_workspace_sizes():
+    # (8 and 12 tiles of dQ and of dK, dV, too short to be cut)
     assert A.attn_bwd_workspace_bytes(2, 4, 2, 100, 300, 64, 1) == 256 + 2 * 2 * 4 * 128 * 4
     assert A.attn_bwd_workspace_bytes(2, 4, 2, 100, 300, 64, 2) == 256 + 3 * 2 * 4 * 128 * 4
+    # one tile of 64 blocks of 128 keys: 16 parts of dQ of 1 x 128 x 64 FP32 values; the longer walk of dK and dV has one block
+    assert A.attn_bwd_workspace_bytes(1, 1, 1, 128, 8192, 64, 1) == 256 + 2 * 128 * 4 + 16 * 128 * 64 * 4
     assert A.attn_bwd_workspace_bytes(2, 4, 3, 100, 300, 64, 1) == 0
     assert A.attn_bwd_workspace_bytes(2, 4, 2, 0, 300, 64, 1) == 0

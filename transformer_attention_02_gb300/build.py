@@ -27,7 +27,7 @@ SOURCES = [os.path.join(CSRC, f) for f in
            ("attn_api.cu", "attn_host.cu", "block_kernels.cu", "fwd_bf16.cu", "fwd_f16.cu", "fwd_rope_bf16.cu",
             "fwd_rope_f16.cu", "fwd_pack_bf16.cu", "fwd_pack_f16.cu", "fwd_window_bf16.cu",
             "fwd_window_f16.cu", "paged_api.cu", "paged_append.cu", "paged_gather.cu",
-            "paged_attn_bf16.cu", "paged_attn_f16.cu", "paged_attn_e4m3.cu", "bwd_api.cu", "bwd_begin.cu",
+            "paged_attn_bf16.cu", "paged_attn_f16.cu", "paged_attn_e4m3.cu", "bwd_api.cu", "bwd_small.cu",
             "bwd_bf16_d64.cu", "bwd_bf16_d128.cu", "bwd_f16_d64.cu", "bwd_f16_d128.cu",
             "checkpoint.cu", "rope_axes.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in

@@ -51,7 +51,7 @@ struct DeviceInfo {
     bool gemm_attr_set = false;
     bool ln_attr_set[3] = {};
     bool paged_attr_set[3][2][4] = {};     // [cache type][D is 128][rows of a block]
-    bool bwd_attr_set[2][2][2][2] = {};    // [D is 128][bf16][additive mask][dQ, dK and dV]
+    bool bwd_attr_set[2][2][2][2][2] = {};    // [D is 128][bf16][additive mask][dQ, dK and dV][whole, parts]
 };
 
 std::mutex g_mutex;

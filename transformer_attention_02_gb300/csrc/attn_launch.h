@@ -35,7 +35,7 @@ struct DeviceState {
     int num_sms;
     unsigned int* status;                 // run-time status word
     bool (*paged_attr_set)[2][4];         // [cache type]: see paged::launch_attend
-    bool (*bwd_attr_set)[2][2][2];        // [D is 128]: see the backward pass's launchers
+    bool (*bwd_attr_set)[2][2][2][2];     // [D is 128]: see the backward pass's launchers
     unsigned long long timeout_ns;        // limit of every wait
     bool stall;                           // failure-detection test hook
 };

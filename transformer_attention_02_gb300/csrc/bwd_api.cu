@@ -20,10 +20,34 @@ size_t align_up(size_t x) { return (x + kWorkspaceAlign - 1) / kWorkspaceAlign *
 
 bool is_additive(int mask_kind) { return mask_kind == ATTN_MASK_ADDITIVE || mask_kind == ATTN_MASK_CAUSAL_ADDITIVE; }
 
+// Where the tiles do not fill the device's SMs, their walks are cut into parts, as many as fill them and none shorter
+// than four blocks at the longest walk (a tile's beginning and end cost about as much as three).
+constexpr int kPartBlocks = 4;
+int parts_of(double tiles, double longest, int sms) {
+    if (tiles * 2 > sms) return 1;
+    return (int)std::max(1.0, std::min(std::floor(sms / tiles), std::ceil(longest / kPartBlocks)));
+}
+struct Parts {
+    int dq = 1, dkv = 1;
+    size_t bytes = 0;               // of the larger of the two sets of sums: they are used one after the other
+};
+Parts parts_for(int B, int Hq, int Hkv, int Sq, int Sk, int D, int mask_kind) {
+    const int sms = device_sm_count();
+    const double nq = (double)(bwd::padded_rows(Sq) / bwd::kBlock), nk = (double)(bwd::padded_rows(Sk) / bwd::kBlock);
+    Parts s;
+    if (!is_additive(mask_kind)) s.dq = parts_of(B * (double)Hq * nq, nk, sms);
+    s.dkv = parts_of(B * (double)Hkv * nk, nq * (Hq / Hkv), sms);
+    const size_t q = s.dq > 1 ? (size_t)s.dq * B * Sq * Hq * D * sizeof(float) : 0;
+    const size_t kv = s.dkv > 1 ? (size_t)s.dkv * 2 * B * Sk * Hkv * D * sizeof(float) : 0;
+    s.bytes = align_up(std::max(q, kv));
+    return s;
+}
+
 // Two tile counters, then three statistics for every query row, the third with an additive mask only.
 size_t stat_bytes(int B, int Hq, int Sq) { return align_up((size_t)B * Hq * bwd::padded_rows(Sq) * sizeof(float)); }
-size_t bwd_workspace(int B, int Hq, int Sq, int mask_kind) {
-    return kWorkspaceAlign + stat_bytes(B, Hq, Sq) * (is_additive(mask_kind) ? 3 : 2);
+size_t bwd_workspace(int B, int Hq, int Hkv, int Sq, int Sk, int D, int mask_kind) {
+    return kWorkspaceAlign + stat_bytes(B, Hq, Sq) * (is_additive(mask_kind) ? 3 : 2) +
+           parts_for(B, Hq, Hkv, Sq, Sk, D, mask_kind).bytes;
 }
 
 // A tensor of tokens: pointer, distance of tokens, H * D values a token. Null only where it is empty.
@@ -50,17 +74,45 @@ int zero_tokens(void* ptr, long long stride, int B, int S, int H, int D, cudaStr
 }
 
 template <int D, bool BF16, bool ADDITIVE>
-int launch_both(const DeviceState& dev, const CUtensorMap* maps, bwd::BwdParams& p, unsigned int* counters, cudaStream_t stream) {
-    bool* attr = dev.bwd_attr_set[D == 128][BF16][ADDITIVE];
-    p.n_tiles = p.B * p.Hq * p.n_qb;
+int launch_both(const DeviceState& dev, const CUtensorMap* maps, bwd::BwdParams& p, unsigned int* counters, const Parts& parts,
+                cudaStream_t stream) {
+    bool (*attr)[2] = dev.bwd_attr_set[D == 128][BF16][ADDITIVE];
+    p.splits = parts.dq;
+    p.n_tiles = p.B * p.Hq * p.n_qb * p.splits;
     p.counter = counters;
     int rc = bwd::launch_dq<D, BF16, ADDITIVE>(attr[0], maps[0], maps[1], maps[2], maps[3], p,
                                                std::min(p.n_tiles, dev.num_sms), stream);
     if (rc != ATTN_OK) return rc;
-    p.n_tiles = p.B * p.Hkv * p.n_kb;
+    if (p.splits > 1) {
+        bwd::JoinParams j{};
+        j.part = p.part;
+        j.apart = (long long)p.B * p.Sq * p.Hq * D;
+        j.splits = p.splits;
+        j.out = static_cast<uint16_t*>(p.dq);
+        j.tokens = (long long)p.B * p.Sq;
+        j.stride = p.dq_stride;
+        j.width = p.Hq * D;
+        j.factor = p.scale;
+        if ((rc = bwd::launch_join(&j, 1, BF16, dev.num_sms, stream)) != ATTN_OK) return rc;
+    }
+    p.splits = parts.dkv;
+    p.n_tiles = p.B * p.Hkv * p.n_kb * p.splits;
     p.counter = counters + 1;
-    return bwd::launch_dkv<D, BF16, ADDITIVE>(attr[1], maps[0], maps[1], maps[2], maps[3], p,
-                                              std::min(p.n_tiles, dev.num_sms), stream);
+    rc = bwd::launch_dkv<D, BF16, ADDITIVE>(attr[1], maps[0], maps[1], maps[2], maps[3], p, std::min(p.n_tiles, dev.num_sms), stream);
+    if (rc != ATTN_OK || p.splits == 1) return rc;
+    bwd::JoinParams j[2] = {};
+    for (int i = 0; i < 2; ++i) {                                 // dV, dK
+        const long long plane = (long long)p.B * p.Sk * p.Hkv * D;
+        j[i].part = p.part + i * plane;
+        j[i].apart = 2 * plane;
+        j[i].splits = p.splits;
+        j[i].out = static_cast<uint16_t*>(i ? p.dk : p.dv);
+        j[i].tokens = (long long)p.B * p.Sk;
+        j[i].stride = i ? p.dk_stride : p.dv_stride;
+        j[i].width = p.Hkv * D;
+        j[i].factor = i ? p.scale : 1.f;
+    }
+    return bwd::launch_join(j, 2, BF16, dev.num_sms, stream);
 }
 
 int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const void* o, const float* lse, void* dq,
@@ -91,7 +143,7 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
             return rc;
         return zero_tokens(dv, dv_stride, B, Sk, Hkv, D, stream);
     }
-    if (!workspace || !aligned(workspace, kWorkspaceAlign) || workspace_bytes < bwd_workspace(B, Hq, Sq, mask_kind))
+    if (!workspace || !aligned(workspace, kWorkspaceAlign) || workspace_bytes < bwd_workspace(B, Hq, Hkv, Sq, Sk, D, mask_kind))
         return ATTN_ERR_INVALID_ARG;
     if (check_only) return ATTN_OK;
 
@@ -108,6 +160,7 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
     unsigned int* const counters = static_cast<unsigned int*>(workspace);
     char* const ws = static_cast<char*>(workspace) + kWorkspaceAlign;
 
+    const Parts parts = parts_for(B, Hq, Hkv, Sq, Sk, D, mask_kind);
     rc = bwd::launch_begin(counters, stream);
     if (rc != ATTN_OK) return rc;
 
@@ -118,6 +171,7 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
     p.neg_lse = reinterpret_cast<float*>(ws);
     p.neg_delta = reinterpret_cast<float*>(ws + stat);
     p.inv_sum = additive ? reinterpret_cast<float*>(ws + 2 * stat) : nullptr;
+    p.part = reinterpret_cast<float*>(ws + (additive ? 3 : 2) * stat);
     p.mask = additive ? mask : nullptr;
     p.dq = dq;
     p.dk = dk;
@@ -146,11 +200,11 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
     p.timeout_ns = dev.timeout_ns;
     p.status = dev.status;
     if (D == 128) {
-        if (additive) return bf16 ? launch_both<128, true, true>(dev, maps, p, counters, stream) : launch_both<128, false, true>(dev, maps, p, counters, stream);
-        return bf16 ? launch_both<128, true, false>(dev, maps, p, counters, stream) : launch_both<128, false, false>(dev, maps, p, counters, stream);
+        if (additive) return bf16 ? launch_both<128, true, true>(dev, maps, p, counters, parts, stream) : launch_both<128, false, true>(dev, maps, p, counters, parts, stream);
+        return bf16 ? launch_both<128, true, false>(dev, maps, p, counters, parts, stream) : launch_both<128, false, false>(dev, maps, p, counters, parts, stream);
     }
-    if (additive) return bf16 ? launch_both<64, true, true>(dev, maps, p, counters, stream) : launch_both<64, false, true>(dev, maps, p, counters, stream);
-    return bf16 ? launch_both<64, true, false>(dev, maps, p, counters, stream) : launch_both<64, false, false>(dev, maps, p, counters, stream);
+    if (additive) return bf16 ? launch_both<64, true, true>(dev, maps, p, counters, parts, stream) : launch_both<64, false, true>(dev, maps, p, counters, parts, stream);
+    return bf16 ? launch_both<64, true, false>(dev, maps, p, counters, parts, stream) : launch_both<64, false, false>(dev, maps, p, counters, parts, stream);
 }
 
 // ----------------------------------------------------- 8-bit checkpoints
@@ -197,7 +251,7 @@ CheckpointLayout checkpoint_layout(int B, int Hq, int Hkv, int Sq, int Sk, int D
     l.o = l.v + kv;
     l.lse = l.o + q;
     l.bwd = l.lse + align_up((size_t)B * Hq * Sq * sizeof(float));
-    l.total = l.bwd + bwd_workspace(B, Hq, Sq, mask_kind);
+    l.total = l.bwd + bwd_workspace(B, Hq, Hkv, Sq, Sk, D, mask_kind);
     return l;
 }
 
@@ -319,7 +373,7 @@ size_t attn_bwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D, i
     if (check_sizes(B, Hq, Hkv, Sq, Sk, D) != ATTN_OK || mask_kind < ATTN_MASK_NONE || mask_kind > ATTN_MASK_CAUSAL_ADDITIVE)
         return 0;
     if ((long long)B * Sq * Hq == 0 || Sk == 0) return 0;
-    return bwd_workspace(B, Hq, Sq, mask_kind);
+    return bwd_workspace(B, Hq, Hkv, Sq, Sk, D, mask_kind);
 }
 
 }  // extern "C"

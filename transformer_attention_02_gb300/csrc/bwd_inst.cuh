@@ -20,23 +20,28 @@ int launch(bool& attr_set, Kernel kernel, int smem, const CUtensorMap& q, const 
 }
 
 template <int D, bool BF16, bool ADDITIVE>
-int launch_dq(bool& attr_set, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& d_o,
+int launch_dq(bool* attr_set, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& d_o,
               const BwdParams& p, int grid, cudaStream_t stream) {
-    return launch(attr_set, bwd_dq_kernel<D, BF16, ADDITIVE>, QCfg<D, ADDITIVE>::kSmemBytes, q, k, v, d_o, p, grid, stream);
+    constexpr int smem = QCfg<D, ADDITIVE>::kSmemBytes;
+    if constexpr (!ADDITIVE)                              // (the statistics of a masked row need its whole walk)
+        if (p.splits > 1)
+            return launch(attr_set[1], bwd_dq_kernel<D, BF16, ADDITIVE, true>, smem, q, k, v, d_o, p, grid, stream);
+    return launch(attr_set[0], bwd_dq_kernel<D, BF16, ADDITIVE, false>, smem, q, k, v, d_o, p, grid, stream);
 }
 
 template <int D, bool BF16, bool ADDITIVE>
-int launch_dkv(bool& attr_set, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& d_o,
+int launch_dkv(bool* attr_set, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& d_o,
                const BwdParams& p, int grid, cudaStream_t stream) {
-    return launch(attr_set, bwd_dkv_kernel<D, BF16, ADDITIVE>, KvCfg<D, ADDITIVE>::kSmemBytes, q, k, v, d_o, p, grid,
-                  stream);
+    constexpr int smem = KvCfg<D, ADDITIVE>::kSmemBytes;
+    if (p.splits > 1) return launch(attr_set[1], bwd_dkv_kernel<D, BF16, ADDITIVE, true>, smem, q, k, v, d_o, p, grid, stream);
+    return launch(attr_set[0], bwd_dkv_kernel<D, BF16, ADDITIVE, false>, smem, q, k, v, d_o, p, grid, stream);
 }
 
 }  // namespace bwd
 }  // namespace attn
 
 #define ATTN_BWD_ONE(LAUNCH, D, BF16, ADDITIVE)                                                               \
-    template int attn::bwd::LAUNCH<D, BF16, ADDITIVE>(bool&, const CUtensorMap&, const CUtensorMap&,          \
+    template int attn::bwd::LAUNCH<D, BF16, ADDITIVE>(bool*, const CUtensorMap&, const CUtensorMap&,          \
                                                       const CUtensorMap&, const CUtensorMap&,                 \
                                                       const attn::bwd::BwdParams&, int, cudaStream_t);
 

@@ -20,7 +20,7 @@
 //
 // Both are bound by the tensor cores: four (three) products of 512 cycles at D =
 // 128 stand against one exponential a pair (512 cycles of the SM's 32 a cycle).
-// Roles of a CTA (640 threads): warps 0-15 take the S and dP tiles from TMEM and
+// Roles of a CTA (576 threads): warps 0-15 take the S and dP tiles from TMEM and
 // put P and dS back in 16 bits (four warpgroups of 32 columns each; a warp's
 // lanes are 32 rows), warp 16 issues the products, warp 17 the loads.
 //
@@ -44,10 +44,10 @@
 namespace attn {
 namespace bwd {
 
-constexpr int kThreads = 640;
 constexpr int kGroups = 4, kCols = kBlock / kGroups;       // warpgroups of the element-wise work, columns of each
 constexpr int kWarps = 4 * kGroups;
 constexpr int kIssueWarp = kWarps, kLoadWarp = kWarps + 1;
+constexpr int kThreads = 32 * (kWarps + 2);                // 112 registers a thread
 constexpr uint32_t kRowBytes = kBlock * sizeof(float);     // 128 row statistics
 constexpr float kLog2E = 1.4426950408889634f;
 
@@ -191,12 +191,34 @@ __device__ __forceinline__ void store_row(uint32_t taddr, uint32_t freed, uint16
     }
 }
 
-// One warp writes zeros over rows row0 .. of a tile: `rows` of them, D values each, `stride` apart.
-template <int D>
-__device__ __forceinline__ void zero_rows(uint16_t* at, long long stride, int rows) {
-    constexpr int kPer = D / 8;                               // 16-byte pieces of a row
+// The same as FP32, of a part of a tile's walk (in pieces that leave the block's P its registers).
+template <int N>
+__device__ __forceinline__ void store_part(uint32_t taddr, uint32_t freed, float* row, bool there) {
+#pragma unroll 1
+    for (int c = 0; c < N; c += 16) {
+        uint32_t v[16];
+        ptx::tmem_ld16(taddr + c, v);
+        ptx::tmem_ld_wait();
+        ptx::reg_fence16(v);
+        if (there) {
+            ptx::st_global_v8(row + c, v);
+            ptx::st_global_v8(row + c + 8, v + 8);
+        }
+    }
+    warp_arrive_tmem(freed);
+}
+
+// One warp writes zeros over `rows` rows of D values (of a tile without a visible pair), `stride` apart.
+template <int D, typename Value>
+__device__ __forceinline__ void zero_rows(Value* at, long long stride, int rows) {
+    constexpr int kEach = 16 / sizeof(Value), kPer = D / kEach;                        // 16-byte pieces of a row
     for (int e = threadIdx.x & 31; e < rows * kPer; e += 32)
-        *reinterpret_cast<uint4*>(at + (e / kPer) * stride + 8 * (e % kPer)) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(at + (e / kPer) * stride + kEach * (e % kPer)) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Blocks [from, from + n) of a walk of `all` blocks that part `split` takes; part 0 is empty where the walk is.
+__device__ __forceinline__ int part_from(int all, int split, int splits) {
+    return min(all, split * ((all + splits - 1) / splits));
 }
 
 // Work tiles are handed out in order: a CTA's first is its own index, each further one comes from a counter in the
@@ -287,13 +309,19 @@ struct KvCfg {
 struct KvTile {
     int b, hk, k0;
     int lo, per_head;       // first query block that sees a key of the tile, and how many do
-    int n;                  // blocks of the walk: those of every head
+    int split, from, n;     // part of the walk over the blocks of every head, its first block and how many
 };
 
 // Tiles of a K/V head follow each other, so that its queries come from L2; with
 // a causal mask the first keys, which most queries see, come first.
+template <bool PARTS>
 __device__ __forceinline__ KvTile kv_tile(int t, const BwdParams& p) {
     KvTile w;
+    w.split = 0;
+    if (PARTS) {
+        w.split = t % p.splits;
+        t /= p.splits;
+    }
     const int bh = t / p.n_kb;
     w.k0 = (t - bh * p.n_kb) * kBlock;
     w.b = bh / p.Hkv;
@@ -304,10 +332,15 @@ __device__ __forceinline__ KvTile kv_tile(int t, const BwdParams& p) {
     w.lo = lo / kBlock;
     w.per_head = hi > lo ? (hi + kBlock - 1) / kBlock - w.lo : 0;
     w.n = w.per_head * p.group;
+    w.from = 0;
+    if (PARTS) {
+        w.from = part_from(w.n, w.split, p.splits);
+        w.n = part_from(w.n, w.split + 1, p.splits) - w.from;
+    }
     return w;
 }
 
-template <int D, bool BF16, bool ADDITIVE>
+template <int D, bool BF16, bool ADDITIVE, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG, const BwdParams p) {
@@ -361,10 +394,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         Place<C::kG> g;
         for (bool alive = true; alive;) {
             const int t = take_tile(taken, p);
-            const KvTile w = kv_tile(max(t, 0), p);
+            const KvTile w = kv_tile<PARTS>(max(t, 0), p);
             if (t >= 0 && w.n == 0) {
                 const long long token = (long long)w.b * p.Sk + w.k0;
                 const int rows = min(kBlock, p.Sk - w.k0);
+                if (PARTS) {
+                    const long long plane = (long long)p.B * p.Sk * p.Hkv * D;
+                    float* part = p.part + 2 * w.split * plane + (token * p.Hkv + w.hk) * D;
+                    zero_rows<D>(part, (long long)p.Hkv * D, rows);
+                    zero_rows<D>(part + plane, (long long)p.Hkv * D, rows);
+                    continue;
+                }
                 zero_rows<D>(static_cast<uint16_t*>(p.dk) + token * p.dk_stride + w.hk * D, p.dk_stride, rows);
                 zero_rows<D>(static_cast<uint16_t*>(p.dv) + token * p.dv_stride + w.hk * D, p.dv_stride, rows);
                 continue;
@@ -376,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load_tile<D>(smem + C::kKOff, &tmK, bar(C::bK), w.hk, w.k0, w.b);
             }
             ++tiles;
-            int h = w.hk * p.group, i = w.lo;
+            int h = w.hk * p.group + (PARTS ? w.from / w.per_head : 0), i = w.lo + (PARTS ? w.from % w.per_head : 0);
             for (int it = 0; it < w.n; ++it) {
                 const size_t row = ((size_t)w.b * p.Hq + h) * p.Sp + (size_t)i * kBlock;
                 if (q.round > 0 && !(alive = warp_wait(bar(C::bQEmpty + q.at), (q.round - 1) & 1u, sc))) break;
@@ -428,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Blocks of the next tile; 0: there is none.
         auto next_work = [&]() -> int {
             const int t = next_tile(k++, ring, sc);
-            return t < 0 ? 0 : kv_tile(t, p).n;
+            return t < 0 ? 0 : kv_tile<PARTS>(t, p).n;
         };
         auto s_half = [&](int half, uint32_t at) {
             half_over_d<D, BF16>(half, tmem + C::cS, smem + C::kKOff, smem + C::kQOff + at * T::kBytes);
@@ -536,14 +576,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Two warpgroups write dV, two dK, each half of the row: of the tile before, once the first P of the next one is done
         const bool is_k = wg >= 2;
         const int col = (wg & 1) * (D / 2);
-        uint16_t* done_row = nullptr;
+        void* done_row = nullptr;
         bool done_there = false;
         auto finish = [&]() -> bool {
             if (!done_row) return true;
             if (!warp_wait(bar(C::bAcc), tiles & 1u, sc)) return false;
             ptx::tc_fence_after_sync();
-            store_row<D / 2, BF16>(tmem + lane_base + (is_k ? C::cDK : C::cDV) + col, bar(C::bAccEmpty), done_row,
-                                   is_k ? p.scale : 1.f, done_there, p.vec8);
+            const uint32_t acc = tmem + lane_base + (is_k ? C::cDK : C::cDV) + col;
+            if (PARTS)
+                store_part<D / 2>(acc, bar(C::bAccEmpty), static_cast<float*>(done_row), done_there);
+            else
+                store_row<D / 2, BF16>(acc, bar(C::bAccEmpty), static_cast<uint16_t*>(done_row), is_k ? p.scale : 1.f, done_there,
+                                       p.vec8);
             done_row = nullptr;
             ++tiles;
             return true;
@@ -551,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t k = 0; alive; ++k) {
             const int t = next_tile(k, ring, sc);
             if (t < 0) break;
-            const KvTile w = kv_tile(t, p);
+            const KvTile w = kv_tile<PARTS>(t, p);
             const int key = w.k0 + r;
             // queries [see, end) see this key
             const int see = p.causal ? key - p.off : 0;
@@ -561,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int all_see = p.causal ? w.k0 + kBlock - 1 - p.off : 0;
             const int all_end = p.window && w.k0 + kBlock > p.sinks
                                     ? (int)min((long long)INT_MAX, (long long)max(w.k0, p.sinks) - p.off + p.window) : INT_MAX;
-            int i = w.lo;
+            int i = w.lo + (PARTS ? w.from % w.per_head : 0);
             for (int it = 0; it < w.n; ++it, ++use, q = q.next(), g = g.next()) {
                 const int m0 = i * kBlock + kCols * wg;              // this warp's first query
                 float x[kCols];
@@ -649,8 +693,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (++i == w.lo + w.per_head) i = w.lo;
             }
             if (!alive) break;
-            uint16_t* row = static_cast<uint16_t*>(is_k ? p.dk : p.dv) +
-                            ((long long)w.b * p.Sk + key) * (is_k ? p.dk_stride : p.dv_stride) + w.hk * D + col;
+            const long long token = (long long)w.b * p.Sk + key;
+            void* row = static_cast<uint16_t*>(is_k ? p.dk : p.dv) + token * (is_k ? p.dk_stride : p.dv_stride) + w.hk * D + col;
+            if (PARTS)
+                row = p.part + (2 * w.split + is_k) * ((long long)p.B * p.Sk * p.Hkv * D) + (token * p.Hkv + w.hk) * D + col;
             done_row = row;
             done_there = key < p.Sk;
         }
@@ -699,13 +745,19 @@ struct QCfg {
 struct QTile {
     int b, h, hk, m0;
     int first, gap;         // key blocks of the walk: 0 .. first - 1 (sinks), then on from first + gap
-    int n;
-    __device__ __forceinline__ int block(int j) const { return j < first ? j : j + gap; }
+    int split, from, n;     // part of the walk, its first block and how many
+    __device__ __forceinline__ int block(int j) const { return j + from < first ? j + from : j + from + gap; }    // (from 0: whole)
 };
 
 // Tiles of a head follow each other; with a causal mask the last queries, which see most keys, come first.
+template <bool PARTS>
 __device__ __forceinline__ QTile q_tile(int t, const BwdParams& p) {
     QTile w;
+    w.split = 0;
+    if (PARTS) {
+        w.split = t % p.splits;
+        t /= p.splits;
+    }
     const int bh = t / p.n_qb, m = t - bh * p.n_qb;
     w.m0 = (p.causal ? p.n_qb - 1 - m : m) * kBlock;
     w.b = bh / p.Hq;
@@ -723,10 +775,15 @@ __device__ __forceinline__ QTile q_tile(int t, const BwdParams& p) {
             w.n -= w.gap;
         }
     }
+    w.from = 0;
+    if (PARTS) {
+        w.from = part_from(w.n, w.split, p.splits);
+        w.n = part_from(w.n, w.split + 1, p.splits) - w.from;
+    }
     return w;
 }
 
-template <int D, bool BF16, bool ADDITIVE>
+template <int D, bool BF16, bool ADDITIVE, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG, const BwdParams p) {
@@ -779,10 +836,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t taken = 0, tiles = 0, g_fills = 0, kf = 0, vf = 0;
         for (bool alive = true; alive;) {
             const int t = take_tile(taken, p);
-            const QTile w = q_tile(max(t, 0), p);
+            const QTile w = q_tile<PARTS>(max(t, 0), p);
             if (t >= 0 && w.n == 0) {
-                zero_rows<D>(static_cast<uint16_t*>(p.dq) + ((long long)w.b * p.Sq + w.m0) * p.dq_stride + w.h * D, p.dq_stride,
-                             min(kBlock, p.Sq - w.m0));
+                const long long token = (long long)w.b * p.Sq + w.m0;
+                if (PARTS)
+                    zero_rows<D>(p.part + w.split * ((long long)p.B * p.Sq * p.Hq * D) + (token * p.Hq + w.h) * D,
+                                 (long long)p.Hq * D, min(kBlock, p.Sq - w.m0));
+                else
+                    zero_rows<D>(static_cast<uint16_t*>(p.dq) + token * p.dq_stride + w.h * D, p.dq_stride,
+                                 min(kBlock, p.Sq - w.m0));
+                if (w.split > 0) continue;
                 // the other kernel passes over these rows too
                 const size_t at = ((size_t)w.b * p.Hq + w.h) * p.Sp + w.m0;
                 for (int e = lane; e < kBlock; e += 32) {
@@ -862,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int kept0 = 0, kept1 = 0, kept2 = 0, kept3 = 0;
         auto next_work = [&]() {                              // at_s: the next tile, n = 0 behind the last
             const int t = next_tile(k++, ring, sc);
-            at_s.n = t < 0 ? 0 : kWalks * q_tile(t, p).n;
+            at_s.n = t < 0 ? 0 : kWalks * q_tile<PARTS>(t, p).n;
             at_s.j = 0;
             const uint32_t i = at_s.tile & 3u;
             kept0 = i == 0 ? at_s.n : kept0;
@@ -1005,15 +1068,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool alive = true;
         // Each warpgroup writes 32 columns of dQ: of the tile before, once the first block of the next one is in registers
         const bool writes = 32 * wg < D;
-        uint16_t* done_row = nullptr;
+        void* done_row = nullptr;
         bool done_there = false;
         auto finish = [&]() -> bool {
             if (!done_row) return true;
             if (!warp_wait(bar(C::bAcc), tiles & 1u, sc)) return false;
             ptx::tc_fence_after_sync();
-            if (writes)
-                store_row<32, BF16>(tmem + lane_base + C::cDQ + 32 * wg, bar(C::bAccEmpty), done_row, p.scale, done_there,
-                                    p.vec8);
+            if (PARTS && writes)
+                store_part<32>(tmem + lane_base + C::cDQ + 32 * wg, bar(C::bAccEmpty), static_cast<float*>(done_row), done_there);
+            else if (writes)
+                store_row<32, BF16>(tmem + lane_base + C::cDQ + 32 * wg, bar(C::bAccEmpty), static_cast<uint16_t*>(done_row),
+                                    p.scale, done_there, p.vec8);
             else
                 warp_arrive(bar(C::bAccEmpty));
             done_row = nullptr;
@@ -1023,7 +1088,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t k = 0; alive; ++k) {
             const int t = next_tile(k, ring, sc);
             if (t < 0) break;
-            const QTile w = q_tile(t, p);
+            const QTile w = q_tile<PARTS>(t, p);
             const int row = w.m0 + r;
             const bool there = row < p.Sq;
             const size_t at = ((size_t)w.b * p.Hq + w.h) * p.Sp + row;
@@ -1072,7 +1137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!warp_wait(bar(C::bDelta), k & 1u, sc)) return false;
                 nd = delta[r];
                 warp_arrive(bar(C::bGEmpty));                     // (the next tile's are written after its dO has come)
-                if (wg == 0) {
+                if (wg == 0 && w.split == 0) {
                     p.neg_delta[at] = nd;
                     if (!ADDITIVE) p.neg_lse[at] = nl;
                 }
@@ -1194,7 +1259,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             alive = block(0, std::true_type{});
             for (int j = 1; j < w.n && alive; ++j) alive = block(j, std::false_type{});
             if (!alive) break;
-            uint16_t* out = static_cast<uint16_t*>(p.dq) + ((long long)w.b * p.Sq + row) * p.dq_stride + w.h * D + 32 * wg;
+            const long long token = (long long)w.b * p.Sq + row;
+            void* out = static_cast<uint16_t*>(p.dq) + token * p.dq_stride + w.h * D + 32 * wg;
+            if (PARTS)
+                out = p.part + w.split * ((long long)p.B * p.Sq * p.Hq * D) + (token * p.Hq + w.h) * D + 32 * wg;
             done_row = out;
             done_there = there;
         }

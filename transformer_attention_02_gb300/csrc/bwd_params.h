@@ -1,5 +1,5 @@
 // Host-visible parameters of the attention's backward kernels and their
-// launchers (bwd_begin.cu, bwd_inst.cuh).
+// launchers (bwd_small.cu, bwd_inst.cuh).
 #pragma once
 
 #include <cuda.h>
@@ -30,7 +30,9 @@ struct BwdParams {
     int n_qb, n_kb;                 // blocks of 128 queries, of 128 keys
     int off;                        // Sk - Sq: query i sits at position i + off
     int causal, window, sinks;      // window 0: none (causal with it)
-    int n_tiles;
+    int splits;                     // parts of a tile's walk, each a tile of its own (not dQ with an additive mask)
+    float* part;                    // splits > 1: FP32 sums of the parts, [splits] (B, Sq, Hq, D) or [splits][dV, dK] (B, Sk, Hkv, D)
+    int n_tiles;                    // tiles times parts
     unsigned int* counter;          // tiles handed out beyond each CTA's first; launch_begin sets it to 0
     int vec8;                       // gradients may be written with 32-byte stores
     int stall;                      // failure-detection test hook, as in the forward kernel
@@ -39,13 +41,26 @@ struct BwdParams {
     unsigned int* status;
 };
 
-// Launchers; ATTN_OK or ATTN_ERR_CUDA. attr_set: per context and variant, that the kernel's shared memory is set.
+// The sum of a tensor's parts, times a factor, to 16 bits.
+struct JoinParams {
+    const float* part;              // the tensor's first part
+    long long apart;                // values from part to part
+    int splits;
+    uint16_t* out;                  // (tokens, width), `stride` from token to token
+    long long tokens, stride;
+    int width;
+    float factor;
+};
+
+// Launchers; ATTN_OK or ATTN_ERR_CUDA. attr_set: per context and variant, that the shared memory is set of the kernel of
+// whole walks, of the one of parts.
 int launch_begin(unsigned int* counters, cudaStream_t stream);        // two of them to 0
+int launch_join(const JoinParams* p, int n, bool bf16, int num_sms, cudaStream_t stream);        // one or two tensors
 template <int D, bool BF16, bool ADDITIVE>
-int launch_dq(bool& attr_set, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& d_o,
+int launch_dq(bool* attr_set, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& d_o,
               const BwdParams& p, int grid, cudaStream_t stream);
 template <int D, bool BF16, bool ADDITIVE>
-int launch_dkv(bool& attr_set, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& d_o,
+int launch_dkv(bool* attr_set, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& d_o,
                const BwdParams& p, int grid, cudaStream_t stream);
 
 }  // namespace bwd
