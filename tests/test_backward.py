@@ -104,6 +104,23 @@ def test_windows(shape, window, sinks):
     R.check(got, *R.backward(d_o, q, k, v, **w))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape,window,sinks", [
+    ((1, 8, 1, 2000, 2000, 128), 128, 4),              # a few tiles, the first of them twelve times as long as the others
+    ((3, 4, 1, 1000, 1900, 64), 60, 300),              # three blocks of sinks, in each sample
+    ((2, 64, 16, 2500, 2500, 64), 100, 130),           # many tiles
+])
+def test_sinks_that_every_query_sees(shape, window, sinks):
+    """The keys of the sinks take part in every query's sum: their tiles' walks are cut, and joined, apart from the others."""
+    d_o, q, k, v = _inputs(*shape, BF16, seed=12)
+    w = dict(causal=True, window=window, sinks=sinks)
+    o, lse = R.forward(q, k, v, **w)
+    got = ta.attention_backward(d_o, q, k, v, o.to(BF16), lse.float(), **w)
+    R.check(got, *R.backward(d_o, q, k, v, **w))
+    again = ta.attention_backward(d_o, q, k, v, o.to(BF16), lse.float(), **w)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
 def _mask(kind, B, Sq, Sk, dev="cuda"):
     g = torch.Generator(device=dev).manual_seed(5)
     m = torch.zeros((B, Sq, Sk), device=dev)

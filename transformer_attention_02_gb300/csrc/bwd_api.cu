@@ -22,41 +22,87 @@ bool is_additive(int mask_kind) { return mask_kind == ATTN_MASK_ADDITIVE || mask
 
 // Where there are few tiles their walks are cut into parts, as many as an estimate finds the quickest, in blocks of 128 x 128
 // pairs: a part costs its blocks and kTileCost for its beginning and end; walks of one length run in waves of the device's
-// SMs, those under a causal mask (from one block to the longest) fill each other's gaps, so that the longest part or an SM's
-// share of everything bounds them; joining costs a launch and two passes over the sums. Measured, bf16 heads of 128,
-// whole and cut: 4096 causal tokens of 8 heads on one K/V head 382 and 125 us, 1024 of 32 heads on one 362 and 79, 16384 of
-// one head 301 and 191, 128 queries of 8 heads over 16384 keys 182 and 75, window 512 over 8192 tokens 109 and 104.
-constexpr int kPartBlocks = 4;      // a part of the longest walk has no fewer
+// SMs, those of several lengths (under a causal mask, or with the sinks of a window) fill each other's gaps, so that the
+// longest part or an SM's share of everything bounds them; joining costs a launch and two passes over the sums. The keys of a
+// window's sinks are seen by all queries: with many tiles the walks of theirs alone are cut. Measured, bf16 heads of 128, whole
+// and cut: 4096 causal tokens of 8 heads on one K/V head 382 and 125 us, 1024 of 32 heads on one 362 and 79, 16384 of one head
+// 301 and 191, 128 queries of 8 heads over 16384 keys 182 and 75; with 4 sinks, window 128 over
+// 16384 tokens of 32 / 8 heads 1084 and 389, over 32768 of 16 heads of 64 on two 3328 and 330 (238 without sinks).
+constexpr int kPartBlocks = 4, kMaxParts = 64;      // a part of the longest walk has no fewer blocks
+constexpr int kSinkTiles = 2;                       // parts of the sinks' tiles, for each SM, at most
 constexpr double kTileCost = 3.0, kJoinCost = 2.0, kSumCost = 0.04;
-int parts_of(double tiles, double longest, int sms, bool triangle) {
-    int best = 1;
-    double least = 0.0;
-    if (tiles >= 4.0 * sms) return 1;
-    for (int s = 1; s <= 64 && (s == 1 || s <= longest / kPartBlocks); ++s) {
-        double cost = triangle ? std::max(longest / s + kTileCost, (tiles * longest / 2 + kTileCost * tiles * s) / sms)
-                               : std::ceil(tiles * s / sms) * (std::ceil(longest / s) + kTileCost);
-        if (s > 1) cost += kJoinCost + kSumCost * tiles * s;
-        if (s == 1 || cost < least) {
-            least = cost;
-            best = s;
-        }
+struct Walks {
+    double cut, longest;            // walks that may be cut, the longest of them
+    double tiles, other;            // all walks, the longest of those that stay whole
+    double total;                   // blocks of all walks together
+    bool even;                      // of one length
+};
+struct Choice {
+    int parts;
+    double cost;
+};
+Choice parts_of(const Walks& w, int sms, int most) {
+    Choice best{1, 0.0};
+    for (int s = 1; s <= most && (s == 1 || s <= w.longest / kPartBlocks); ++s) {
+        double cost = w.even ? std::ceil(w.cut * s / sms) * (std::ceil(w.longest / s) + kTileCost)
+                             : std::max(std::max(w.longest / s, w.other) + kTileCost,
+                                        (w.total + kTileCost * (w.tiles + w.cut * (s - 1))) / sms);
+        if (s > 1) cost += kJoinCost + kSumCost * w.cut * s;
+        if (s == 1 || cost < best.cost) best = {s, cost};
     }
     return best;
 }
+// All walks are cut, or none. (With as many tiles as these nothing is won.)
+Choice parts_of_all(double tiles, double longest, double total, bool even, int sms, int most = kMaxParts) {
+    return parts_of({tiles, longest, tiles, 0.0, total, even}, sms, tiles >= 4.0 * sms ? 1 : most);
+}
 struct Parts {
     int dq = 1, dkv = 1;
+    int sink_kb = 0;                // key blocks of the sinks, where theirs alone are cut
     size_t bytes = 0;               // of the larger of the two sets of sums: they are used one after the other
 };
+// Parts at most of each of the `kb` tiles of sinks that every K/V head has.
+int most_sink_parts(double heads, double kb, double walk, int sms) {
+    return (int)std::min({(double)kMaxParts, std::floor(walk / kPartBlocks), std::floor(kSinkTiles * sms / (heads * kb))});
+}
 Parts parts_for(int B, int Hq, int Hkv, int Sq, int Sk, int D, int mask_kind) {
     const int sms = device_sm_count();
     const double nq = (double)(bwd::padded_rows(Sq) / bwd::kBlock), nk = (double)(bwd::padded_rows(Sk) / bwd::kBlock);
+    const double q_tiles = B * (double)Hq * nq, kv_tiles = B * (double)Hkv * nk, kv_walk = nq * (Hq / Hkv);
     Parts s;
     const bool triangle = mask_kind == ATTN_MASK_CAUSAL || mask_kind == ATTN_MASK_CAUSAL_ADDITIVE;
-    if (!is_additive(mask_kind)) s.dq = parts_of(B * (double)Hq * nq, nk, sms, triangle);
-    s.dkv = parts_of(B * (double)Hkv * nk, nq * (Hq / Hkv), sms, triangle);
-    const size_t q = s.dq > 1 ? (size_t)s.dq * B * Sq * Hq * D * sizeof(float) : 0;
-    const size_t kv = s.dkv > 1 ? (size_t)s.dkv * 2 * B * Sk * Hkv * D * sizeof(float) : 0;
-    s.bytes = align_up(std::max(q, kv));
+    const double share = triangle ? 0.5 : 1.0;
+    if (!is_additive(mask_kind)) s.dq = parts_of_all(q_tiles, nk, share * q_tiles * nk, !triangle, sms).parts;
+    s.dkv = parts_of_all(kv_tiles, kv_walk, share * kv_tiles * kv_walk, !triangle, sms).parts;
+    const size_t vectors = (size_t)D * sizeof(float);
+    const size_t q = s.dq > 1 ? s.dq * vectors * B * Sq * Hq : 0, kv = s.dkv > 1 ? s.dkv * vectors * 2 * B * Sk * Hkv : 0;
+    // (of all sinks that a window may have: kb * most_sink_parts(.., kb, ..) tiles a head)
+    const double heads = B * (double)Hkv;
+    const double most = std::min(nk * std::min((double)kMaxParts, std::floor(kv_walk / kPartBlocks)), kSinkTiles * sms / heads);
+    const size_t sinks = mask_kind == ATTN_MASK_CAUSAL ? (size_t)(most * heads) * 2 * bwd::kBlock * vectors : 0;
+    s.bytes = align_up(std::max({q, kv, sinks}));
+    return s;
+}
+// With a window: all walks in no more parts than without, for which the workspace is, or the sinks' in as many as that holds.
+Parts parts_in_window(Parts s, int B, int Hq, int Hkv, int Sq, int Sk, int window, int sinks) {
+    const int sms = device_sm_count();
+    const double nq = (double)(bwd::padded_rows(Sq) / bwd::kBlock), nk = (double)(bwd::padded_rows(Sk) / bwd::kBlock);
+    const double seen = std::floor(((double)window + bwd::kBlock - 2) / bwd::kBlock) + 1;      // blocks that touch a tile's windows
+    const double sink_kb = std::min(nk, std::ceil((double)sinks / bwd::kBlock));
+    const double q_tiles = B * (double)Hq * nq, q_walk = std::min(nk, seen + sink_kb);
+    const double heads = B * (double)Hkv, G = Hq / Hkv, kv_walk = std::min(nq, seen) * G;
+    s.dq = parts_of_all(q_tiles, q_walk, q_tiles * q_walk, true, sms, s.dq).parts;
+    const double total = heads * ((nk - sink_kb) * kv_walk + sink_kb * nq * G);
+    const Choice all = parts_of_all(heads * nk, sink_kb > 0 ? nq * G : kv_walk, total, sink_kb == 0, sms, s.dkv);
+    s.dkv = all.parts;
+    if (sink_kb > 0 && sink_kb < nk) {
+        const Choice sink = parts_of({heads * sink_kb, nq * G, heads * nk, kv_walk, total, false}, sms,
+                                     std::max(1, most_sink_parts(heads, sink_kb, nq * G, sms)));
+        if (sink.parts > 1 && sink.cost < all.cost) {
+            s.dkv = sink.parts;
+            s.sink_kb = (int)sink_kb;
+        }
+    }
     return s;
 }
 
@@ -107,24 +153,29 @@ int launch_both(const DeviceState& dev, const CUtensorMap* maps, bwd::BwdParams&
         j.splits = p.splits;
         j.out = static_cast<uint16_t*>(p.dq);
         j.tokens = (long long)p.B * p.Sq;
+        j.rows = j.out_rows = p.Sq;
         j.stride = p.dq_stride;
         j.width = p.Hq * D;
         j.factor = p.scale;
         if ((rc = bwd::launch_join(&j, 1, BF16, dev.num_sms, stream)) != ATTN_OK) return rc;
     }
     p.splits = parts.dkv;
-    p.n_tiles = p.B * p.Hkv * p.n_kb * p.splits;
+    p.cut = p.B * p.Hkv * (parts.sink_kb ? parts.sink_kb : p.n_kb);
+    p.part_rows = parts.sink_kb ? parts.sink_kb * bwd::kBlock : p.Sk;
+    p.n_tiles = p.B * p.Hkv * p.n_kb + p.cut * (p.splits - 1);
     p.counter = counters + 1;
     rc = bwd::launch_dkv<D, BF16, ADDITIVE>(attr[1], maps[0], maps[1], maps[2], maps[3], p, std::min(p.n_tiles, dev.num_sms), stream);
     if (rc != ATTN_OK || p.splits == 1) return rc;
     bwd::JoinParams j[2] = {};
     for (int i = 0; i < 2; ++i) {                                 // dV, dK
-        const long long plane = (long long)p.B * p.Sk * p.Hkv * D;
+        const long long plane = (long long)p.B * p.part_rows * p.Hkv * D;
         j[i].part = p.part + i * plane;
         j[i].apart = 2 * plane;
         j[i].splits = p.splits;
         j[i].out = static_cast<uint16_t*>(i ? p.dk : p.dv);
-        j[i].tokens = (long long)p.B * p.Sk;
+        j[i].tokens = (long long)p.B * p.part_rows;
+        j[i].rows = p.part_rows;
+        j[i].out_rows = p.Sk;
         j[i].stride = i ? p.dk_stride : p.dv_stride;
         j[i].width = p.Hkv * D;
         j[i].factor = i ? p.scale : 1.f;
@@ -177,7 +228,8 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
     unsigned int* const counters = static_cast<unsigned int*>(workspace);
     char* const ws = static_cast<char*>(workspace) + kWorkspaceAlign;
 
-    const Parts parts = parts_for(B, Hq, Hkv, Sq, Sk, D, mask_kind);
+    Parts parts = parts_for(B, Hq, Hkv, Sq, Sk, D, mask_kind);
+    if (window > 0) parts = parts_in_window(parts, B, Hq, Hkv, Sq, Sk, window, sinks);
     rc = bwd::launch_begin(counters, stream);
     if (rc != ATTN_OK) return rc;
 
@@ -209,6 +261,7 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
     p.causal = mask_kind == ATTN_MASK_CAUSAL || mask_kind == ATTN_MASK_CAUSAL_ADDITIVE;
     p.window = std::min(window, kAllKeys);
     p.sinks = window > 0 ? std::min(sinks, kAllKeys) : 0;
+    p.sink_kb = std::min(p.n_kb, (p.sinks + bwd::kBlock - 1) / bwd::kBlock);
     p.vec8 = aligned(dq, 32) && aligned(dk, 32) && aligned(dv, 32) && dq_stride % 16 == 0 && dk_stride % 16 == 0 &&
              dv_stride % 16 == 0;
     p.stall = dev.stall;
@@ -229,6 +282,7 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
 int check_vectors(const void* x, long long stride, const void* codes, const float* scale, int B, int S, int H, int D) {
     if (B < 0 || S < 0 || H < 0 || D <= 0) return ATTN_ERR_INVALID_ARG;
     if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+    if ((double)B * S * H > (double)(1LL << 48)) return ATTN_ERR_INVALID_ARG;
     if ((long long)B * S * H == 0) return ATTN_OK;
     if (!x || !codes || !scale || !aligned(x, 16) || !aligned(codes, 16) || !aligned(scale, 4)) return ATTN_ERR_INVALID_ARG;
     return stride >= (long long)H * D && stride % 8 == 0 ? ATTN_OK : ATTN_ERR_INVALID_ARG;

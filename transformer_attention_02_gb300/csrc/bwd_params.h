@@ -28,11 +28,14 @@ struct BwdParams {
     int B, Hq, Hkv, Sq, Sk, Sp;
     int group;                      // Hq / Hkv
     int n_qb, n_kb;                 // blocks of 128 queries, of 128 keys
+    int sink_kb;                    // the first key blocks, which hold a window's sinks
     int off;                        // Sk - Sq: query i sits at position i + off
     int causal, window, sinks;      // window 0: none (causal with it)
     int splits;                     // parts of a tile's walk, each a tile of its own (not dQ with an additive mask)
-    float* part;                    // splits > 1: FP32 sums of the parts, [splits] (B, Sq, Hq, D) or [splits][dV, dK] (B, Sk, Hkv, D)
-    int n_tiles;                    // tiles times parts
+    int cut;                        // dK and dV, splits > 1: the first `cut` tiles are in parts, those of the first part_rows keys
+    int part_rows;
+    float* part;                    // splits > 1: FP32 sums of the parts, [splits] (B, Sq, Hq, D) or [splits][dV, dK] (B, part_rows, Hkv, D)
+    int n_tiles;                    // tiles, each part one
     unsigned int* counter;          // tiles handed out beyond each CTA's first; launch_begin sets it to 0
     int vec8;                       // gradients may be written with 32-byte stores
     int stall;                      // failure-detection test hook, as in the forward kernel
@@ -46,8 +49,9 @@ struct JoinParams {
     const float* part;              // the tensor's first part
     long long apart;                // values from part to part
     int splits;
-    uint16_t* out;                  // (tokens, width), `stride` from token to token
-    long long tokens, stride;
+    uint16_t* out;                  // (B, out_rows, width), `stride` from token to token; the first `rows` of each batch item
+    long long tokens, stride;       // B * rows
+    int rows, out_rows;
     int width;
     float factor;
 };

@@ -42,7 +42,8 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const JoinParams a, const
             w[i] = BF16 ? ptx::pack_bf16x2(lo, hi) : ptx::pack_f16x2(lo, hi);
         }
         const long long token = e / (p.width / 8);
-        *reinterpret_cast<uint4*>(p.out + token * p.stride + 8 * (e - token * (p.width / 8))) = make_uint4(w[0], w[1], w[2], w[3]);
+        const long long row = token + token / p.rows * (p.out_rows - p.rows);
+        *reinterpret_cast<uint4*>(p.out + row * p.stride + 8 * (e - token * (p.width / 8))) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
