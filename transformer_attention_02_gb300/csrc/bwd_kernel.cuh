@@ -208,6 +208,38 @@ __device__ __forceinline__ void store_part(uint32_t taddr, uint32_t freed, float
     warp_arrive_tmem(freed);
 }
 
+// The mask of a warp's 32 rows (those from `row0` on) and the kCols columns from `key0` on, a row a lane. Were each lane to read
+// its own row, every load would touch 32 lines; here a load touches four rows, eight lanes with four values each, and the eight
+// lanes exchange what they have in three steps. Rows and columns that are none get 0.
+__device__ __forceinline__ void load_mask(float (&x)[kCols], const float* mask, int row0, int rows, int key0, int keys) {
+    static_assert(kCols == 32, "eight lanes of four values");
+    const int lane = threadIdx.x & 31, first = row0 + (lane & 24), col = key0 + 4 * (lane & 7);
+    const float* at = mask + (size_t)first * keys + col;
+    const bool vec = key0 + kCols <= keys && keys % 4 == 0 && (reinterpret_cast<uintptr_t>(mask) & 15) == 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const bool there = first + i < rows;
+        if (vec) {
+            const float4 m = there ? *reinterpret_cast<const float4*>(at + (size_t)i * keys) : make_float4(0.f, 0.f, 0.f, 0.f);
+            x[4 * i] = m.x, x[4 * i + 1] = m.y, x[4 * i + 2] = m.z, x[4 * i + 3] = m.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[4 * i + e] = there && col + e < keys ? at[(size_t)i * keys + e] : 0.f;
+        }
+    }
+#pragma unroll
+    for (int m = 1; m < 8; m *= 2) {
+        const bool upper = lane & m;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            if (i & (4 * m)) continue;
+            const float got = __shfl_xor_sync(0xffffffffu, upper ? x[i] : x[i + 4 * m], m);
+            if (upper) x[i] = got;
+            else x[i + 4 * m] = got;
+        }
+    }
+}
+
 // One warp writes zeros over `rows` rows of D values (of a tile without a visible pair), `stride` apart.
 template <int D, typename Value>
 __device__ __forceinline__ void zero_rows(Value* at, long long stride, int rows) {
@@ -1101,7 +1133,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             // keys [low, lim) are visible, and those before sinks
             const int lim = p.causal ? min(p.Sk, max(0, row + p.off + 1)) : p.Sk;
             const int low = p.window ? row + p.off - p.window + 1 : 0;
-            const float* mrow = ADDITIVE && there ? p.mask + ((size_t)w.b * p.Sq + row) * p.Sk : nullptr;
             float nl = 0.f, is = 0.f, nd = 0.f;
             if (!ADDITIVE) {
                 const float l = there ? p.lse[((size_t)w.b * p.Hq + w.h) * p.Sq + row] : -INFINITY;
@@ -1153,27 +1184,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             // logits in log2 units of block j: S in the buffer of `su`, scaled, masked, hidden keys at -inf
             auto logits = [&](int j, float* x) -> bool {
                 const int key0 = w.block(j) * kBlock + kCols * wg;
-                if (ADDITIVE) {
-                    const bool vec = mrow != nullptr && key0 + kCols <= p.Sk && p.Sk % 4 == 0 &&
-                                     (reinterpret_cast<uintptr_t>(p.mask) & 15) == 0;
-                    if (vec) {
-#pragma unroll
-                        for (int c = 0; c < kCols; c += 4) {
-                            const float4 m = *reinterpret_cast<const float4*>(mrow + key0 + c);
-                            x[c] = m.x, x[c + 1] = m.y, x[c + 2] = m.z, x[c + 3] = m.w;
-                        }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < kCols; ++c) x[c] = mrow != nullptr && key0 + c < p.Sk ? mrow[key0 + c] : 0.f;
-                    }
-                }
+                float m[kCols];
+                if (ADDITIVE) load_mask(m, p.mask + (size_t)w.b * p.Sq * p.Sk, w.m0 + (warp & 3) * 32, p.Sq, key0, p.Sk);
                 if (!warp_wait(bar(C::bS + (su & 1u)), (su >> 1) & 1u, sc)) return false;
                 ptx::tc_fence_after_sync();
                 if (ADDITIVE) {
-                    float s[kCols];
-                    load32(tS + 128 * (su & 1u), s);
+                    load32(tS + 128 * (su & 1u), x);
 #pragma unroll
-                    for (int c = 0; c < kCols; ++c) x[c] = fmaf(x[c], kLog2E, s[c] * sl);
+                    for (int c = 0; c < kCols; ++c) x[c] = fmaf(m[c], kLog2E, x[c] * sl);
                 } else {
                     load32(tS + 128 * (su & 1u), x);
 #pragma unroll
