@@ -759,6 +759,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the keys are walked twice: first for the rows' maximum and sum, since a mask of
 // large values leaves lse without the logits' bits; both go to the other kernel.
 
+// With an additive mask a tile's keys are walked once where its rows' lse are in this range, whose rounding moves a
+// probability by 2^-16 of itself, little beside that to 16 bits; else twice: a mask of large values leaves lse without the
+// logits' bits, and the rows' maximum and sum are found anew.
+constexpr float kPlainLse = 256.f;
+
+// Ring entry of a tile that is walked twice.
+__device__ __forceinline__ int twice_entry(int t) { return -2 - t; }
+
 template <int D, bool ADDITIVE>
 struct QCfg {
     using T = Tile<D>;
@@ -893,7 +901,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 continue;
             }
-            if (!publish_tile(tiles, t, ring, sc) || t < 0) break;
+            bool twice = false;
+            if (ADDITIVE && t >= 0) {
+                for (int e = lane; e < min(kBlock, p.Sq - w.m0); e += 32) {
+                    const float l = p.lse[((size_t)w.b * p.Hq + w.h) * p.Sq + w.m0 + e];
+                    twice |= !(fabsf(l) <= kPlainLse) && l != -INFINITY;
+                }
+                twice = __any_sync(0xffffffffu, twice);
+            }
+            if (!publish_tile(tiles, twice ? twice_entry(t) : t, ring, sc) || t < 0) break;
             for (int e = lane; e < min(kBlock, p.Sq - w.m0); e += 32) {       // O, for delta: on its way to L2
                 const char* o = reinterpret_cast<const char*>(p.o + (((size_t)w.b * p.Sq + w.m0 + e) * p.Hq + w.h) * D);
 #pragma unroll
@@ -934,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++vf;
                 return true;
             };
-            if (ADDITIVE)
+            if (twice)
                 for (int j = 0; j < w.n && alive; ++j) alive = load_k(j);
             // in the order in which the products take them: K_0, dO, V_0, K_1, V_1, ...
             for (int j = 0; j < w.n && alive; ++j) alive = load_k(j) && (j > 0 || load_g()) && load_v(j);
@@ -947,14 +963,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (vf > s) drain_phase(bar(C::bV + s), ((vf - 1 - s) / C::kV) & 1u, sc);
     } else if (warp == kIssueWarp) {
         // --------------------------------------------------------- products
-        // One walk over the blocks of all tiles (with an additive mask each tile's keys come twice, the first time for S
-        // alone), with three places in it: dQ, dP one block ahead, S two blocks ahead. A place is a tile's number, the
+        // One walk over the blocks of all tiles (those walked twice have `skip` blocks of S alone before the others), with three places in it: dQ, dP one block ahead, S two blocks ahead. A place is a tile's number, the
         // block and the number of blocks; those of the last four tiles are kept for the places behind the first.
         struct At {
             uint32_t tile = 0;
-            int j = 0, n = 0;
+            int j = 0, n = 0, skip = 0;
+            // of a tile's entry below: its blocks, negative where it is walked twice
+            __device__ __forceinline__ void begin(int blocks) {
+                j = 0;
+                n = ADDITIVE && blocks < 0 ? -2 * blocks : blocks;
+                skip = ADDITIVE && blocks < 0 ? -blocks : 0;
+            }
         };
-        constexpr int kWalks = ADDITIVE ? 2 : 1;
         uint32_t k = 0, su = 0, ds = 0, dp = 0;               // ring entries, S issued, dS (or freed S) taken, dP issued
         At at_s, at_dp, at_dq;
         Place<C::kK> ka, kb;                                  // K of S, of dQ
@@ -962,21 +982,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool alive = true, issued = false;
         int kept0 = 0, kept1 = 0, kept2 = 0, kept3 = 0;
         auto next_work = [&]() {                              // at_s: the next tile, n = 0 behind the last
-            const int t = next_tile(k++, ring, sc);
-            at_s.n = t < 0 ? 0 : kWalks * q_tile<PARTS>(t, p).n;
-            at_s.j = 0;
+            const int e = next_tile(k++, ring, sc);
+            const bool twice = ADDITIVE && e < -1;
+            const int t = twice ? twice_entry(e) : e;
+            int n = t < 0 ? 0 : q_tile<PARTS>(t, p).n;
+            if (twice) n = -n;
+            at_s.begin(n);
             const uint32_t i = at_s.tile & 3u;
-            kept0 = i == 0 ? at_s.n : kept0;
-            kept1 = i == 1 ? at_s.n : kept1;
-            kept2 = i == 2 ? at_s.n : kept2;
-            kept3 = i == 3 ? at_s.n : kept3;
+            kept0 = i == 0 ? n : kept0;
+            kept1 = i == 1 ? n : kept1;
+            kept2 = i == 2 ? n : kept2;
+            kept3 = i == 3 ? n : kept3;
         };
         auto go_on = [&](At& a) {
             if (++a.j < a.n) return;
             ++a.tile;
-            a.j = 0;
             const uint32_t i = a.tile & 3u;
-            a.n = i == 0 ? kept0 : i == 1 ? kept1 : i == 2 ? kept2 : kept3;
+            a.begin(i == 0 ? kept0 : i == 1 ? kept1 : i == 2 ? kept2 : kept3);
         };
         // Second halves of the products that are half issued: of S (s_open), with its buffers and what follows it, of dP, dQ
         bool s_open = false, s_ends = false, dp_open = false, dp_ends = false, dq_open = false, dq_ends = false;
@@ -1029,9 +1051,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
         };
         auto begin_dp = [&]() -> bool {
-            if (!ADDITIVE || 2 * at_dp.j >= at_dp.n) {
+            if (!ADDITIVE || at_dp.j >= at_dp.skip) {
                 const uint32_t b = bar(C::bV + v.at), par = v.parity(), fb = bar(C::bDPFree), fpar = (dp - 1) & 1u;
-                const bool first = at_dp.j == at_dp.n - at_dp.n / kWalks;
+                const bool first = at_dp.j == at_dp.skip;
                 const uint32_t gpar = at_dp.tile & 1u;
                 if (!follow(
                         dp > 0 && !first && warp_test2(b, par, fb, fpar),
@@ -1054,13 +1076,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto begin_dq = [&]() -> bool {
             const uint32_t b = bar(C::bDS + (ds & 1u)), par = (ds >> 1) & 1u;
-            if (ADDITIVE && 2 * at_dq.j < at_dq.n) {          // S alone, which the warps have read
+            if (ADDITIVE && at_dq.j < at_dq.skip) {          // S alone, which the warps have read
                 if (ptx::elect_one()) rest();
                 close();
                 if (!warp_wait(b, par, sc)) return false;
                 commit(bar(C::bKEmpty + kb.at));
             } else {
-                const bool first = at_dq.j == at_dq.n - at_dq.n / kWalks, drained = !first || at_dq.tile == 0;
+                const bool first = at_dq.j == at_dq.skip, drained = !first || at_dq.tile == 0;
                 const uint32_t apar = (at_dq.tile - 1) & 1u;  // the warps have the last tile's dQ
                 if (!follow(
                         drained ? warp_test(b, par) : warp_test2(b, par, bar(C::bAccEmpty), apar),
@@ -1084,7 +1106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (p.stall) alive = warp_wait(bar(C::bStall), 0, sc);               // nothing ever arrives
         if (alive) {
             next_work();
-            at_dp.n = at_dq.n = at_s.n;
+            at_dp = at_dq = at_s;
             alive = at_s.n == 0 || (begin_s() && begin_dp() && (at_s.n == 0 || begin_s()));
         }
         while (alive && at_dq.n > 0)
@@ -1124,7 +1146,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
         };
         for (uint32_t k = 0; alive; ++k) {
-            const int t = next_tile(k, ring, sc);
+            const int e = next_tile(k, ring, sc);
+            const bool twice = ADDITIVE && e < -1;
+            const int t = twice ? twice_entry(e) : e;
             if (t < 0) break;
             const QTile w = q_tile<PARTS>(t, p);
             const int row = w.m0 + r;
@@ -1134,9 +1158,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int lim = p.causal ? min(p.Sk, max(0, row + p.off + 1)) : p.Sk;
             const int low = p.window ? row + p.off - p.window + 1 : 0;
             float nl = 0.f, is = 0.f, nd = 0.f;
-            if (!ADDITIVE) {
+            if (!twice) {
                 const float l = there ? p.lse[((size_t)w.b * p.Hq + w.h) * p.Sq + row] : -INFINITY;
-                nl = l == -INFINITY ? -INFINITY : -l * kLog2E;
+                const bool any = l != -INFINITY;
+                nl = any ? -l * kLog2E : ADDITIVE ? 0.f : -INFINITY;
+                is = any ? 1.f : 0.f;
             }
             // delta of the tile's rows, eight a warp, O from device memory (whole lines of it) and dO from its tile
             constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kPasses = 8 / kAtOnce;              // lanes of a row
@@ -1176,7 +1202,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 warp_arrive(bar(C::bGEmpty));                     // (the next tile's are written after its dO has come)
                 if (wg == 0 && w.split == 0) {
                     p.neg_delta[at] = nd;
-                    if (!ADDITIVE) p.neg_lse[at] = nl;
+                    if (!twice) p.neg_lse[at] = nl;
+                    if (ADDITIVE && !twice) p.inv_sum[at] = is;
                 }
                 return true;
             };
@@ -1206,7 +1233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return true;
             };
 
-            if (ADDITIVE) {
+            if (twice) {
                 float m = -INFINITY, l = 0.f;
                 for (int j = 0; j < w.n; ++j, ++su) {
                     float x[kCols];
@@ -1257,7 +1284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < kCols; ++c) x[c] = ptx::ex2(ADDITIVE ? x[c] + nl : x[c]);
                 if constexpr (decltype(begins)::value) {
-                    if (!ADDITIVE && !finish()) return false;
+                    if (!finish()) return false;
                     if (!find_delta(o)) return false;
                 }
                 if (!warp_wait(bar(C::bDP), dp & 1u, sc)) return false;
