@@ -1,12 +1,13 @@
 /*
- * attn.h — C ABI of the fused attention forward for NVIDIA GB300 (sm_103a).
+ * attn.h — C ABI of the fused attention for NVIDIA GB300 (sm_103a).
  *
  * One operation: O = softmax(scale * Q K^T + mask) V, computed in a single
  * kernel launch with the softmax done online, block by block, so that the
  * Sq x Sk score matrix never reaches device memory. The per-row running
  * maximum and sum stay in FP32 on chip; both matrix products accumulate in
  * FP32; the outputs are O in the input's 16-bit type and the FP32 row
- * log-sum-exp.
+ * log-sum-exp. Around it: its backward pass, rotary positions, a paged key/value
+ * cache, 8-bit activation checkpoints and the other parts of an attention block.
  *
  * Passages that define the operation (the pages are cited by title):
  *  [GUIDE]  "ATB engineering guide" (hwcomputing.csdn.net/6a59a88310ee7a33f28e5ce9):
@@ -530,8 +531,9 @@ size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, long lo
  *               other tensor, but may interleave in one packed tensor.
  *   scale, mask_kind, mask  as for attn_fwd. The mask has no gradient. Mask values
  *               below -2.3e38 hide a key as -inf does. With an additive mask the
- *               rows' statistics are found anew, in one more pass over the
- *               keys: a mask of large values leaves lse without the logits' bits.
+ *               statistics of rows whose |lse| is above 256 are found anew, in one
+ *               more pass over the keys (for all rows of a block of 128): a mask of
+ *               large values leaves lse without the logits' bits.
  *   window, sinks  window > 0 (causal mask only): as for attn_fwd_window; 0: none
  *   workspace   device scratch of attn_bwd_workspace_bytes(...) bytes, 256-byte
  *               aligned, contents overwritten. Calls that may run at the same
@@ -540,7 +542,10 @@ size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, long lo
  * to dK and dV. With Sq or Sk of 0 the gradients that exist are 0. Blocks of 128
  * keys and 128 queries that hide all of their pairs are not computed. Q, K, V and dO
  * must be finite in the others, hidden pairs included: those enter with weights of
- * zero. Results do not depend on the order of execution (no atomics).
+ * zero. In fp16, P and dS below 2^-14 lose bits and below 2^-25 vanish: gradients
+ * that small want a scaled loss, as everywhere in fp16. Sums are added up in an
+ * order that depends on the sizes and the device's number of SMs alone: the same
+ * call gives the same bits.
  * Errors as for attn_fwd.
  */
 int attn_bwd(const void *d_o, const void *q, const void *k, const void *v, const void *o, const float *lse,
@@ -556,8 +561,10 @@ int attn_bwd_f16(const void *d_o, const void *q, const void *k, const void *v, c
                  float scale, int mask_kind, const float *mask, int window, int sinks,
                  void *workspace, size_t workspace_bytes, attn_stream_t stream);
 
-/* attn_bwd_workspace_bytes — workspace bytes attn_bwd needs for these sizes
- * (host only; 0 for an empty problem or invalid sizes). */
+/* attn_bwd_workspace_bytes — workspace bytes attn_bwd needs for these sizes on the
+ * current device (with any window and sinks; host only; 0 for an empty problem or
+ * invalid sizes): row statistics, and FP32 sums where few blocks of 128 queries or
+ * keys would leave SMs idle and their work is divided. */
 size_t attn_bwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D, int mask_kind);
 
 /*
@@ -650,7 +657,8 @@ int attn_bwd_checkpoint_f16(const void *d_o, const void *q8, const void *k8, con
                             void *workspace, size_t workspace_bytes, attn_stream_t stream);
 
 /* attn_bwd_checkpoint_workspace_bytes — workspace bytes attn_bwd_checkpoint needs for
- * these sizes (host only; 0 for an empty problem or invalid sizes). */
+ * these sizes on the current device (host only; 0 for an empty problem or invalid
+ * sizes). */
 size_t attn_bwd_checkpoint_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D, int mask_kind);
 
 /*

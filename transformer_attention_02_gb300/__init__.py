@@ -1,4 +1,4 @@
-"""Fused attention forward for NVIDIA GB300 (sm_103a).
+"""Fused attention, forward and backward, for NVIDIA GB300 (sm_103a).
 
 The compute path is the CUDA library ``libattn.so`` (C ABI in
 ``include/attn.h``); ``attn`` is its thin ctypes binding and ``inputs`` the
