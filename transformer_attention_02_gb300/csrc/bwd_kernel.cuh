@@ -22,7 +22,7 @@
 // put P and dS back in 16 bits (four warpgroups of 32 columns each; a warp's
 // lanes are 32 rows), warp 16 issues the products, warp 17 the loads. Eight such
 // warps could not hide their own latencies (8 x 4096 causal tokens of 32 / 8 heads:
-// 3893 us with eight, 3496 with sixteen).
+// 3893 us with eight, 3496 with sixteen and the elected issuer below).
 //
 // Both are bound by the tensor cores: four (three) products of 512 cycles at D =
 // 128 stand against one exponential a pair (512 cycles of the SM's 32 a cycle).
