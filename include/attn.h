@@ -528,7 +528,8 @@ size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, long lo
  *               be slices of a packed projection
  *   k, v, dk, dv  device, (B, Sk, Hkv, D), with strides of their own
  *               The gradients are written whole and overlap no input and no
- *               other tensor, but may interleave in one packed tensor.
+ *               other tensor, but may interleave in one packed tensor. (One that
+ *               begins where another tensor does is refused.)
  *   scale, mask_kind, mask  as for attn_fwd. The mask has no gradient. Mask values
  *               below -2.3e38 hide a key as -inf does. With an additive mask the
  *               statistics of rows whose |lse| is above 256 are found anew, in one
@@ -577,7 +578,8 @@ size_t attn_bwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D, i
  *               values are contiguous and the strides (elements, a multiple of 8,
  *               at least H * D) lead from token to token of the flattened (B, S),
  *               so that they may be slices of a packed projection. q_out may be q
- *               (in place); otherwise inputs and outputs do not overlap
+ *               (in place, with its stride); otherwise inputs and outputs do not
+ *               overlap
  *   k, k_out    the same with Hkv heads. Either pair may be NULL with no heads
  *   D           a multiple of 8, at most 1024
  *   rope_table, max_pos  device, FP32, (max_pos, D/2, {cos, sin}), 8-byte aligned: of

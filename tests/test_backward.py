@@ -356,8 +356,8 @@ def test_a_wait_that_runs_out_is_reported():
 P = 0x10000
 
 
-def _raw(fn=A.attn_bwd, g=P, q=P, k=P, v=P, o=P, lse=P, dq=P, dk=P, dv=P, st=None, B=1, Hq=2, Hkv=2, Sq=16, Sk=16, D=64, kind=0,
-         mask=None, window=0, sinks=0, ws=P, ws_bytes=1 << 20):
+def _raw(fn=A.attn_bwd, g=2 * P, q=3 * P, k=4 * P, v=5 * P, o=6 * P, lse=7 * P, dq=8 * P, dk=9 * P, dv=10 * P, st=None, B=1, Hq=2,
+         Hkv=2, Sq=16, Sk=16, D=64, kind=0, mask=None, window=0, sinks=0, ws=P, ws_bytes=1 << 20):
     st = st or [Hq * D, Hkv * D, Hkv * D] * 2
     return fn(g, q, k, v, o, lse, dq, dk, dv, *st, B, Hq, Hkv, Sq, Sk, D, 0.0, kind, mask, window, sinks, ws, ws_bytes, None)
 
@@ -371,6 +371,8 @@ def _raw(fn=A.attn_bwd, g=P, q=P, k=P, v=P, o=P, lse=P, dq=P, dk=P, dv=P, st=Non
     (dict(kind=1, sinks=-1), 1), (dict(kind=0, window=3), 1), (dict(kind=3, mask=P, window=3), 1), (dict(ws_bytes=100), 1),
     (dict(st=[120, 128, 128, 128, 128, 128]), 1), (dict(st=[132, 128, 128, 128, 128, 128]), 1),
     (dict(st=[128, 128, 128, 128, 128, 64]), 1), (dict(D=96), 2), (dict(Sq=(1 << 30) + 1), 1),
+    *[({out: n * P}, 1) for out in ("dq", "dk", "dv") for n in range(1, 11) if n != 8 + ("dq", "dk", "dv").index(out)],
+    (dict(kind=2, mask=9 * P), 1),
     (dict(B=0), 0), (dict(Sq=0, Sk=0), 0), (dict(B=1 << 20, Sq=1 << 20, Sk=1 << 20), 1),
 ])
 def test_refusals_on_the_host(fn, kw, code):

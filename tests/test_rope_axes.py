@@ -177,8 +177,8 @@ def test_refusals_of_tensors():
 P = 0x10000
 
 
-def _raw(fn=A.attn_rope_axes, q=P, qo=P, qs=256, qos=256, k=P, ko=P, ks=128, kos=128, B=1, S=4, Hq=4, Hkv=2, D=64, table=P,
-         max_pos=16, pos=P, sections=(8, 24), n=None, inverse=0):
+def _raw(fn=A.attn_rope_axes, q=P, qo=2 * P, qs=256, qos=256, k=3 * P, ko=4 * P, ks=128, kos=128, B=1, S=4, Hq=4, Hkv=2, D=64,
+         table=5 * P, max_pos=16, pos=6 * P, sections=(8, 24), n=None, inverse=0):
     s = None if sections is None else (ctypes.c_int * max(1, len(sections)))(*sections)
     return fn(q, qo, qs, qos, k, ko, ks, kos, B, S, Hq, Hkv, D, table, max_pos, pos, s,
               len(sections or ()) if n is None else n, inverse, None)
@@ -190,6 +190,7 @@ def _raw(fn=A.attn_rope_axes, q=P, qo=P, qs=256, qos=256, k=P, ko=P, ks=128, kos
     *[({n: P + 8}, 1) for n in ("q", "qo", "k", "ko")], (dict(table=P + 4), 1), (dict(pos=P + 2), 1),
     (dict(qs=255), 1), (dict(qs=260), 1), (dict(kos=120), 1), (dict(B=-1), 1), (dict(S=-1), 1), (dict(Hq=-1), 1), (dict(D=60), 1),
     (dict(D=0), 1), (dict(D=2048), 1), (dict(max_pos=0), 1), (dict(sections=(8, 23)), 1), (dict(sections=(8, 25)), 1),
+    (dict(qo=3 * P), 1), (dict(ko=P), 1), (dict(ko=2 * P), 1), (dict(qo=P, qos=264), 1), (dict(ko=3 * P, kos=136), 1),
     (dict(sections=(-1, 33)), 1), (dict(n=0), 1), (dict(sections=(8, 8, 8, 4, 4)), 1), (dict(B=0), 0), (dict(S=0), 0),
     (dict(Hq=0, Hkv=0), 0),
 ])

@@ -204,6 +204,11 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
         !tokens_ok(dk, dk_stride, B, Sk, Hkv, D) || !tokens_ok(dv, dv_stride, B, Sk, Hkv, D) ||
         !tokens_ok(d_o, (long long)Hq * D, B, Sq, Hq, D) || !tokens_ok(o, (long long)Hq * D, B, Sq, Hq, D))
         return ATTN_ERR_INVALID_ARG;
+    if (q_values > 0 && kv_values > 0)                            // a result that begins where another tensor does
+        for (const void* out : {dq, dk, dv})
+            for (const void* in : {d_o, q, k, v, o, (const void*)lse, (const void*)mask, (const void*)workspace})
+                if (out == in) return ATTN_ERR_INVALID_ARG;
+    if (q_values > 0 && kv_values > 0 && (dq == dk || dq == dv || dk == dv)) return ATTN_ERR_INVALID_ARG;
     const bool additive = is_additive(mask_kind);
     if (q_values > 0 && (!lse || !aligned(lse, 4))) return ATTN_ERR_INVALID_ARG;
     if (additive && q_values > 0 && kv_values > 0 && (!mask || !aligned(mask, 4))) return ATTN_ERR_INVALID_ARG;

@@ -26,9 +26,10 @@
 //
 // Both are bound by the tensor cores: four (three) products of 512 cycles at D =
 // 128 stand against one exponential a pair (512 cycles of the SM's 32 a cycle).
-// Measured there: a block takes 2350 cycles (2120 in bwd_dq_kernel, whose products
-// alone, in this order, take 2030: shared memory feeds two operands of each S and
-// dP) and a tile 7000 more, for its first loads, its last chain and its results.
+// bwd_dq_kernel's products alone, in this order, take 2030 cycles a block, since
+// shared memory feeds two operands of each S and dP. Measured with all they wait
+// for: 2490 cycles a block where a tile has 16 of them, 3330 at 8; bwd_dkv_kernel
+// 2730 at 66, 3440 at 8 (delta and the results' stores stand between two tiles).
 // 8 x 4096 tokens take 2610 us: the seven products run at 1.47 PFLOP/s, near what
 // the tensor cores keep up at the clock that power leaves them in so long a call
 // (1.74 PFLOP/s for a library product); the five that are the work at 1.05.

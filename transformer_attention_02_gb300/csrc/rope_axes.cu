@@ -175,6 +175,10 @@ int rope_axes_impl(const void* q, void* q_out, long long q_stride, long long q_o
     if (!rows_ok(q, q_out, q_stride, q_out_stride, tokens, Hq, D) || !rows_ok(k, k_out, k_stride, k_out_stride, tokens, Hkv, D))
         return ATTN_ERR_INVALID_ARG;
     if (tokens == 0 || Hq + Hkv == 0) return ATTN_OK;
+    // In place is each on its own place; a result where the other tensor is read, or written, is none.
+    if (Hq > 0 && tokens > 1 && q == q_out && q_stride != q_out_stride) return ATTN_ERR_INVALID_ARG;
+    if (Hkv > 0 && tokens > 1 && k == k_out && k_stride != k_out_stride) return ATTN_ERR_INVALID_ARG;
+    if (Hq > 0 && Hkv > 0 && (q_out == k_out || q_out == k || k_out == q)) return ATTN_ERR_INVALID_ARG;
     if (!table || !aligned(table, 8) || !positions || !aligned(positions, 4)) return ATTN_ERR_INVALID_ARG;
     DeviceState dev{};
     const int rc = device_state(&dev);
