@@ -121,6 +121,30 @@ def test_sinks_that_every_query_sees(shape, window, sinks):
     assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("masked", [False, True])
+def test_fp16_keeps_its_bits_over_many_keys(masked):
+    """P of 1/6000 and dS of a few 1e-5 lie below fp16's normal numbers. A rounding is off by 2^-11 / sqrt(3) of the value (in the
+    mean square, at the worst mantissa); an operand's and the result's are independent, so that thousands of them together
+    are off by sqrt(2) of that."""
+    d_o, q, k, v = _inputs(1, 1, 1, 6000, 6000, 128, F16, seed=13)
+    d_o.mul_(0.01)
+    kw = dict(mask=torch.zeros((1, 6000, 6000), device="cuda")) if masked else {}
+    got = _run(d_o, q, k, v, **kw)
+    want, _ = R.backward(d_o, q, k, v, **kw)
+    for name, a, w in zip(("dq", "dk", "dv"), got, want):
+        assert float((a.double() - w).norm() / w.norm()) < 2 ** -11 * (2 / 3) ** 0.5, name
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("factor", [0.0, 2.0 ** -14, 1.0, 4000.0])
+def test_fp16_over_its_range(factor):
+    """dO from nothing to where a key alone in its row would leave fp16, among rows that see one key or two."""
+    d_o, q, k, v = _inputs(1, 4, 2, 200, 200, 64, F16, seed=14)
+    d_o.mul_(factor)
+    _check(d_o, q, k, v, causal=True, label=str(factor))
+
+
 def _mask(kind, B, Sq, Sk, dev="cuda"):
     g = torch.Generator(device=dev).manual_seed(5)
     m = torch.zeros((B, Sq, Sk), device=dev)
@@ -381,9 +405,9 @@ def test_refusals_on_the_host(fn, kw, code):
 
 def test_workspace_sizes():
     # (8 and 12 tiles of dQ and of dK, dV, too short to be cut)
-    assert A.attn_bwd_workspace_bytes(2, 4, 2, 100, 300, 64, 1) == 256 + 2 * 2 * 4 * 128 * 4
-    assert A.attn_bwd_workspace_bytes(2, 4, 2, 100, 300, 64, 2) == 256 + 3 * 2 * 4 * 128 * 4
+    assert A.attn_bwd_workspace_bytes(2, 4, 2, 100, 300, 64, 1) == 1024 + 2 * 2 * 4 * 128 * 4
+    assert A.attn_bwd_workspace_bytes(2, 4, 2, 100, 300, 64, 2) == 1024 + 3 * 2 * 4 * 128 * 4
     # one tile of 64 blocks of 128 keys: 16 parts of dQ of 1 x 128 x 64 FP32 values; the longer walk of dK and dV has one block
-    assert A.attn_bwd_workspace_bytes(1, 1, 1, 128, 8192, 64, 1) == 256 + 2 * 128 * 4 + 16 * 128 * 64 * 4
+    assert A.attn_bwd_workspace_bytes(1, 1, 1, 128, 8192, 64, 1) == 1024 + 2 * 128 * 4 + 16 * 128 * 64 * 4
     assert A.attn_bwd_workspace_bytes(2, 4, 3, 100, 300, 64, 1) == 0
     assert A.attn_bwd_workspace_bytes(2, 4, 2, 0, 300, 64, 1) == 0

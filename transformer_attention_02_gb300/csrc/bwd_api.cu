@@ -106,10 +106,12 @@ Parts parts_in_window(Parts s, int B, int Hq, int Hkv, int Sq, int Sk, int windo
     return s;
 }
 
-// Two tile counters, then three statistics for every query row, the third with an additive mask only.
+// The head: two tile counters, and in fp16 the ranges that the blocks of a pass find. Then three statistics for every query row, the third with an additive mask only.
+constexpr size_t kHead = 1024;
+static_assert(kHead >= (8 + bwd::kMostRanges) * sizeof(unsigned int), "the ranges lie in the head");
 size_t stat_bytes(int B, int Hq, int Sq) { return align_up((size_t)B * Hq * bwd::padded_rows(Sq) * sizeof(float)); }
 size_t bwd_workspace(int B, int Hq, int Hkv, int Sq, int Sk, int D, int mask_kind) {
-    return kWorkspaceAlign + stat_bytes(B, Hq, Sq) * (is_additive(mask_kind) ? 3 : 2) +
+    return kHead + stat_bytes(B, Hq, Sq) * (is_additive(mask_kind) ? 3 : 2) +
            parts_for(B, Hq, Hkv, Sq, Sk, D, mask_kind).bytes;
 }
 
@@ -146,7 +148,7 @@ int launch_both(const DeviceState& dev, const CUtensorMap* maps, bwd::BwdParams&
     const int dkv_tiles = p.B * p.Hkv * p.n_kb + p.cut * (parts.dkv - 1);
     int rc;
     // Where every tile has a CTA of its own, what the counters hold is of no account (100 tokens of 8 heads: 17.3 us with them set, 16.3 without).
-    if (std::max(dq_tiles, dkv_tiles) > dev.num_sms && (rc = bwd::launch_begin(counters, stream)) != ATTN_OK) return rc;
+    if (BF16 && std::max(dq_tiles, dkv_tiles) > dev.num_sms && (rc = bwd::launch_begin(counters, stream)) != ATTN_OK) return rc;
     p.splits = parts.dq;
     p.n_tiles = dq_tiles;
     p.counter = counters;
@@ -236,13 +238,21 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
         return ATTN_ERR_CUDA;
     const size_t stat = stat_bytes(B, Hq, Sq);
     unsigned int* const counters = static_cast<unsigned int*>(workspace);
-    char* const ws = static_cast<char*>(workspace) + kWorkspaceAlign;
+    char* const ws = static_cast<char*>(workspace) + kHead;
 
     Parts parts = parts_for(B, Hq, Hkv, Sq, Sk, D, mask_kind);
     if (window > 0) parts = parts_in_window(parts, B, Hq, Hkv, Sq, Sk, window, sinks);
 
     constexpr int kAllKeys = 1 << 30;                     // a longer window hides nothing; differences stay in 32 bits
     bwd::BwdParams p{};
+    if (!bf16) {
+        const long long pieces = std::max((long long)B * Sq * Hq, (long long)B * Sk * Hkv) * (D / 8);
+        p.n_range = (int)std::min({(pieces + 1023) / 1024, (long long)dev.num_sms, (long long)bwd::kMostRanges});
+        p.range = counters + 8;
+        rc = bwd::launch_range(counters, counters + 8, p.n_range, d_o, (long long)B * Sq * Hq * D, v, (long long)B * Sk, v_stride,
+                               Hkv * D, stream);
+        if (rc != ATTN_OK) return rc;
+    }
     p.o = static_cast<const uint16_t*>(o);
     p.lse = lse;
     p.neg_lse = reinterpret_cast<float*>(ws);

@@ -41,7 +41,12 @@
 // P enters its product in the inputs' 16-bit type, as in the forward pass, and
 // so does dS: the tensor cores take both operands in one type. Each is rounded
 // once, from FP32, so that a term is off by half a step of that type, as the
-// inputs themselves are; sums are FP32.
+// inputs themselves are; sums are FP32. fp16 has normal numbers from 2^-14 on only,
+// and over thousands of keys most of P and dS lie below: P enters as 2^14 P, and dS
+// as 2^s dS with the largest s >= 0 that keeps |dS| <= 2 D max|dO| max|V| within
+// 2^15, found by a pass over dO and V ahead (one s for the call); the powers are
+// taken back from the sums. (dV's error over 32000 keys: 4.4e-4 without, 3.0e-4
+// so, like dQ's and dK's; 3 x 777 queries over 1301 keys, 16 heads of 64: 82 and 89 us.)
 #pragma once
 
 #include "../../include/attn.h"
@@ -152,6 +157,29 @@ __device__ __forceinline__ void load32(uint32_t taddr, float* x) {
     ptx::reg_fence32(r);
 }
 
+// Exponents that P and dS carry in fp16 (see above), of the maxima that the blocks of the pass ahead have left.
+template <bool BF16>
+constexpr int kPShift = BF16 ? 0 : 14;
+template <int D, bool BF16>
+__device__ __forceinline__ int ds_shift(const BwdParams& p) {
+    if (BF16) return 0;
+    uint32_t m = 0, each[kMostRanges / 32];                    // (all on their way at once)
+#pragma unroll
+    for (int i = 0; i < kMostRanges / 32; ++i) {
+        const int at = 32 * i + (threadIdx.x & 31);
+        each[i] = at < p.n_range ? __ldcg(p.range + at) : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < kMostRanges / 32; ++i) m = __vmaxu2(m, each[i]);
+#pragma unroll
+    for (int e = 16; e > 0; e >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, e));
+    const float bound = 2.f * D * __half2float(__ushort_as_half((unsigned short)(m & 0xffffu))) *
+                        __half2float(__ushort_as_half((unsigned short)(m >> 16)));
+    const int above = (int)(__float_as_uint(bound) >> 23) - 126;               // bound < 2^above
+    return min(40, max(0, 15 - above));
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack(float a, float b) {
     return BF16 ? ptx::pack_bf16x2(a, b) : ptx::pack_f16x2(a, b);
@@ -203,13 +231,15 @@ __device__ __forceinline__ void store_row(uint32_t taddr, uint32_t freed, uint16
 
 // The same as FP32, of a part of a tile's walk (in pieces that leave the block's P its registers).
 template <int N>
-__device__ __forceinline__ void store_part(uint32_t taddr, uint32_t freed, float* row, bool there) {
+__device__ __forceinline__ void store_part(uint32_t taddr, uint32_t freed, float* row, float factor, bool there) {
 #pragma unroll 1
     for (int c = 0; c < N; c += 16) {
         uint32_t v[16];
         ptx::tmem_ld16(taddr + c, v);
         ptx::tmem_ld_wait();
         ptx::reg_fence16(v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * factor);
         if (there) {
             ptx::st_global_v8(row + c, v);
             ptx::st_global_v8(row + c + 8, v + 8);
@@ -615,6 +645,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_base + C::cS + kCols * wg, tDP = tmem + lane_base + C::cDP + kCols * wg;
         const float sl = p.scale_log2;
+        const int shift = ds_shift<D, BF16>(p);
+        const float more = power_of_two(shift - kPShift<BF16>);      // of dS over P
+        const float back = power_of_two(wg >= 2 ? -shift : -kPShift<BF16>);
         uint32_t tiles = 0, use = 0;
         Place<C::kQ> q;
         Place<C::kG> g;
@@ -630,9 +663,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::tc_fence_after_sync();
             const uint32_t acc = tmem + lane_base + (is_k ? C::cDK : C::cDV) + col;
             if (PARTS && done_part)
-                store_part<D / 2>(acc, bar(C::bAccEmpty), static_cast<float*>(done_row), done_there);
+                store_part<D / 2>(acc, bar(C::bAccEmpty), static_cast<float*>(done_row), back, done_there);
             else
-                store_row<D / 2, BF16>(acc, bar(C::bAccEmpty), static_cast<uint16_t*>(done_row), is_k ? p.scale : 1.f, done_there,
+                store_row<D / 2, BF16>(acc, bar(C::bAccEmpty), static_cast<uint16_t*>(done_row), is_k ? p.scale * back : back, done_there,
                                        p.vec8);
             done_row = nullptr;
             ++tiles;
@@ -724,8 +757,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < kCols; c += 4) {
                         const float4 n = nd[c / 4];
-                        ptx::add2(d[c], d[c + 1], d[c], d[c + 1], n.x, n.y);
-                        ptx::add2(d[c + 2], d[c + 3], d[c + 2], d[c + 3], n.z, n.w);
+                        if (BF16) {
+                            ptx::add2(d[c], d[c + 1], d[c], d[c + 1], n.x, n.y);
+                            ptx::add2(d[c + 2], d[c + 3], d[c + 2], d[c + 3], n.z, n.w);
+                        } else {                              // (delta comes with that factor)
+                            ptx::fma2(d[c], d[c + 1], d[c], d[c + 1], more, more, n.x, n.y);
+                            ptx::fma2(d[c + 2], d[c + 3], d[c + 2], d[c + 3], more, more, n.z, n.w);
+                        }
                         ptx::mul2(d[c], d[c + 1], d[c], d[c + 1], x[c], x[c + 1]);
                         ptx::mul2(d[c + 2], d[c + 3], d[c + 2], d[c + 3], x[c + 2], x[c + 3]);
                         pk[c / 2] = pack<BF16>(d[c], d[c + 1]);
@@ -1138,6 +1176,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_base + C::cS + kCols * wg, tDP = tmem + lane_base + C::cDP + kCols * wg;
         const float sl = p.scale_log2;
+        const int shift = ds_shift<D, BF16>(p);
+        const float more = power_of_two(shift), back = power_of_two(-shift);
         float2* stat = reinterpret_cast<float2*>(smem_ptr + C::kStatOff);
         uint32_t tiles = 0, su = 0, dp = 0, seen = 0;
         bool alive = true;
@@ -1150,10 +1190,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!warp_wait(bar(C::bAcc), tiles & 1u, sc)) return false;
             ptx::tc_fence_after_sync();
             if (PARTS && writes)
-                store_part<32>(tmem + lane_base + C::cDQ + 32 * wg, bar(C::bAccEmpty), static_cast<float*>(done_row), done_there);
+                store_part<32>(tmem + lane_base + C::cDQ + 32 * wg, bar(C::bAccEmpty), static_cast<float*>(done_row), back, done_there);
             else if (writes)
                 store_row<32, BF16>(tmem + lane_base + C::cDQ + 32 * wg, bar(C::bAccEmpty), static_cast<uint16_t*>(done_row),
-                                    p.scale, done_there, p.vec8);
+                                    p.scale * back, done_there, p.vec8);
             else
                 warp_arrive(bar(C::bAccEmpty));
             done_row = nullptr;
@@ -1177,7 +1217,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float l = there ? p.lse[((size_t)w.b * p.Hq + w.h) * p.Sq + row] : -INFINITY;
                 const bool any = l != -INFINITY;
                 nl = any ? -l * kLog2E : ADDITIVE ? 0.f : -INFINITY;
-                is = any ? 1.f : 0.f;
+                if (!ADDITIVE) nl += (float)shift;
+                is = any ? more : 0.f;
             }
             // delta of the tile's rows, eight a warp, O from device memory (whole lines of it) and dO from its tile
             constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kPasses = 8 / kAtOnce;              // lanes of a row
@@ -1216,9 +1257,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 nd = delta[r];
                 warp_arrive(bar(C::bGEmpty));                     // (the next tile's are written after its dO has come)
                 if (wg == 0 && w.split == 0) {
-                    p.neg_delta[at] = nd;
-                    if (!twice) p.neg_lse[at] = nl;
-                    if (ADDITIVE && !twice) p.inv_sum[at] = is;
+                    p.neg_delta[at] = nd * power_of_two(shift - kPShift<BF16>);
+                    if (!twice) p.neg_lse[at] = ADDITIVE ? nl : nl + (float)(kPShift<BF16> - shift);
+                    if (ADDITIVE && !twice) p.inv_sum[at] = is * power_of_two(kPShift<BF16> - shift);
                 }
                 return true;
             };
@@ -1283,12 +1324,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool any = there && l > 0.f;
                     stat[r] = make_float2(any ? -m : 0.f, any ? 1.f / l : 0.f);
                     p.neg_lse[at] = stat[r].x;
-                    p.inv_sum[at] = stat[r].y;
+                    p.inv_sum[at] = stat[r].y * power_of_two(kPShift<BF16>);
                     warp_arrive(bar(C::bWhole));
                 }
                 ++seen;
                 nl = stat[r].x;
-                is = stat[r].y;
+                is = stat[r].y * more;
             }
             // The first block of a tile is a copy of its own: it has the last tile's dQ and delta to see to.
             auto block = [&](int j, auto begins) -> bool {

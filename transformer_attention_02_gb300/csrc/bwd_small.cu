@@ -1,5 +1,6 @@
 // The small kernels around the products of the attention's backward pass: before
-// them the two counters are set from which their CTAs take work tiles; behind
+// them the two counters are set from which their CTAs take work tiles, and in fp16
+// the largest |dO| and |V| are found, which bound dS; behind
 // them, where few tiles were cut into parts, the parts' FP32 sums are joined, in
 // the parts' order.
 #include <algorithm>
@@ -17,6 +18,64 @@ __global__ void bwd_begin_kernel(unsigned int* counters) {
     wait_for_inputs();
     let_next_start();
     if (threadIdx.x < 2) counters[threadIdx.x] = 0u;
+}
+
+__device__ __forceinline__ uint32_t largest(uint32_t m, const uint4& w) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t a = x[i] & 0x7fff7fffu;
+        m = __vmaxu2(m, a & ~__vcmpgeu2(a, 0x7c007c00u));                    // (infinities and NaN set no range)
+    }
+    return m;
+}
+
+// Bound by memory, at small sizes by one wave's latency: eight values a load, two loads of each tensor in flight (13 MB: 6.8 us,
+// 3.5 more than the launch it takes the place of).
+constexpr int kRangeLoads = 2;
+__global__ void __launch_bounds__(1024) bwd_range_kernel(unsigned int* counters, unsigned int* range, const uint4* d_o,
+                                                        long long q_pieces, const uint16_t* v, long long kv_tokens,
+                                                        long long v_stride, int kv_pieces) {
+    wait_for_inputs();
+    let_next_start();
+    __shared__ uint32_t part[2][32];
+    if (blockIdx.x == 0 && threadIdx.x < 2) counters[threadIdx.x] = 0u;
+    const long long first = (long long)blockIdx.x * 1024 + threadIdx.x, step = (long long)gridDim.x * 1024;
+    uint32_t m[2] = {0u, 0u};
+    const long long pieces = kv_tokens * kv_pieces;
+    const bool whole = v_stride == 8LL * kv_pieces;
+    for (long long e = first; e < max(q_pieces, pieces); e += kRangeLoads * step) {
+        uint4 w[kRangeLoads], x[kRangeLoads];
+#pragma unroll
+        for (int i = 0; i < kRangeLoads; ++i) {
+            const long long at = e + i * step, token = whole || at >= pieces ? 0 : at / kv_pieces;
+            w[i] = at < q_pieces ? __ldcg(d_o + at) : make_uint4(0u, 0u, 0u, 0u);
+            x[i] = at < pieces ? __ldcg(reinterpret_cast<const uint4*>(v + token * v_stride + 8 * (at - token * kv_pieces)))
+                               : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < kRangeLoads; ++i) {
+            m[0] = largest(m[0], w[i]);
+            m[1] = largest(m[1], x[i]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m[k] = __vmaxu2(m[k], __shfl_xor_sync(0xffffffffu, m[k], d));
+        if (threadIdx.x % 32 == 0) part[k][threadIdx.x / 32] = m[k];
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            m[k] = part[k][threadIdx.x];
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) m[k] = __vmaxu2(m[k], __shfl_xor_sync(0xffffffffu, m[k], d));
+            m[k] = max(m[k] & 0xffffu, m[k] >> 16);
+        }
+        if (threadIdx.x == 0) range[blockIdx.x] = m[0] | m[1] << 16;
+    }
 }
 
 // Eight values a thread: bound by the parts' reads, which come from L2.
@@ -66,6 +125,13 @@ int launch_join(const JoinParams* p, int n, bool bf16, int num_sms, cudaStream_t
 
 int launch_begin(unsigned int* counters, cudaStream_t stream) {
     return launch_early(bwd_begin_kernel, 1u, 32u, (size_t)0, stream, counters) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int launch_range(unsigned int* counters, unsigned int* range, int blocks, const void* d_o, long long q_values, const void* v,
+                 long long kv_tokens, long long v_stride, int kv_width, cudaStream_t stream) {
+    return launch_early(bwd_range_kernel, (unsigned)blocks, 1024u, (size_t)0, stream, counters, range, static_cast<const uint4*>(d_o),
+                        q_values / 8, static_cast<const uint16_t*>(v), kv_tokens, v_stride, kv_width / 8) == cudaSuccess
+               ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace bwd
