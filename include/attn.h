@@ -543,9 +543,9 @@ size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, long lo
  * to dK and dV. With Sq or Sk of 0 the gradients that exist are 0. Blocks of 128
  * keys and 128 queries that hide all of their pairs are not computed. Q, K, V and dO
  * must be finite in the others, hidden pairs included: those enter with weights of
- * zero. In fp16 P and dS are held with powers of two that keep them within the
- * type (dS by the largest |dO| and |V|); results below 2^-14 lose bits, as everywhere
- * in fp16, and want a scaled loss. Sums are added up in an
+ * zero. In fp16 P and dS are held with powers of two, up or down, that keep them
+ * within the type (dS by the largest |dO| and |V|); results below 2^-14 lose bits, as
+ * everywhere in fp16, and want a scaled loss. Sums are added up in an
  * order that depends on the sizes and the device's number of SMs alone: the same
  * call gives the same bits.
  * Errors as for attn_fwd.
