@@ -544,8 +544,10 @@ size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, long lo
  * keys and 128 queries that hide all of their pairs are not computed. Q, K, V and dO
  * must be finite in the others, hidden pairs included: those enter with weights of
  * zero. In fp16 P and dS are held with powers of two, up or down, that keep them
- * within the type (dS by the largest |dO| and |V|); results below 2^-14 lose bits, as
- * everywhere in fp16, and want a scaled loss. Sums are added up in an
+ * within the type: dS by the largest norms of dO's and V's head vectors in a sample's
+ * K/V head (those of hidden tokens too), so that values of other samples and heads
+ * cost it no bits. Results below 2^-14 lose bits, as everywhere in fp16, and want a
+ * scaled loss. Sums are added up in an
  * order that depends on the sizes and the device's number of SMs alone: the same
  * call gives the same bits.
  * Errors as for attn_fwd.

@@ -106,12 +106,19 @@ Parts parts_in_window(Parts s, int B, int Hq, int Hkv, int Sq, int Sk, int windo
     return s;
 }
 
-// The head: two tile counters, and in fp16 the ranges that the blocks of a pass find. Then three statistics for every query row, the third with an additive mask only.
-constexpr size_t kHead = 1024;
-static_assert(kHead >= (8 + bwd::kMostRanges) * sizeof(unsigned int), "the ranges lie in the head");
+// The head: two tile counters, and behind 32 bytes the words of fp16's ranges. Then three statistics for every query row, the third
+// with an additive mask only.
+constexpr size_t kCounters = 8;                     // words
+int range_parts(int B, int Hkv) {                    // (two blocks an SM)
+    return (int)std::min<long long>(std::max(1LL, 2 * device_sm_count() / ((long long)B * Hkv)), bwd::kMostRanges);
+}
+size_t head_bytes(int B, int Hkv) {
+    const size_t words = kCounters + (size_t)B * Hkv * range_parts(B, Hkv);
+    return align_up(std::max<size_t>(1024, words * sizeof(unsigned int)));
+}
 size_t stat_bytes(int B, int Hq, int Sq) { return align_up((size_t)B * Hq * bwd::padded_rows(Sq) * sizeof(float)); }
 size_t bwd_workspace(int B, int Hq, int Hkv, int Sq, int Sk, int D, int mask_kind) {
-    return kHead + stat_bytes(B, Hq, Sq) * (is_additive(mask_kind) ? 3 : 2) +
+    return head_bytes(B, Hkv) + stat_bytes(B, Hq, Sq) * (is_additive(mask_kind) ? 3 : 2) +
            parts_for(B, Hq, Hkv, Sq, Sk, D, mask_kind).bytes;
 }
 
@@ -238,7 +245,7 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
         return ATTN_ERR_CUDA;
     const size_t stat = stat_bytes(B, Hq, Sq);
     unsigned int* const counters = static_cast<unsigned int*>(workspace);
-    char* const ws = static_cast<char*>(workspace) + kHead;
+    char* const ws = static_cast<char*>(workspace) + head_bytes(B, Hkv);
 
     Parts parts = parts_for(B, Hq, Hkv, Sq, Sk, D, mask_kind);
     if (window > 0) parts = parts_in_window(parts, B, Hq, Hkv, Sq, Sk, window, sinks);
@@ -246,11 +253,21 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
     constexpr int kAllKeys = 1 << 30;                     // a longer window hides nothing; differences stay in 32 bits
     bwd::BwdParams p{};
     if (!bf16) {
-        const long long pieces = std::max((long long)B * Sq * Hq, (long long)B * Sk * Hkv) * (D / 8);
-        p.n_range = (int)std::min({(pieces + 1023) / 1024, (long long)dev.num_sms, (long long)bwd::kMostRanges});
-        p.range = counters + 8;
-        rc = bwd::launch_range(counters, counters + 8, p.n_range, d_o, (long long)B * Sq * Hq * D, v, (long long)B * Sk, v_stride,
-                               Hkv * D, stream);
+        bwd::RangeParams r{};
+        r.counters = counters;
+        r.range = counters + kCounters;
+        r.d_o = static_cast<const uint16_t*>(d_o);
+        r.v = static_cast<const uint16_t*>(v);
+        r.v_stride = v_stride;
+        r.parts = range_parts(B, Hkv);
+        r.units = B * Hkv * r.parts;                              // (parts where B * Hkv is small)
+        r.Hkv = Hkv;
+        r.group = Hq / Hkv;
+        r.Sq = Sq;
+        r.Sk = Sk;
+        p.range = r.range;
+        p.n_range = r.parts;
+        rc = bwd::launch_range(r, D, dev.num_sms, stream);
         if (rc != ATTN_OK) return rc;
     }
     p.o = static_cast<const uint16_t*>(o);

@@ -44,9 +44,9 @@
 // inputs themselves are; sums are FP32. fp16 has normal numbers from 2^-14 to 2^16
 // only. Over thousands of keys most of P and dS lie below; with a scaled loss dS may
 // lie above where the gradients do not. P enters as 2^14 P, and dS as 2^s dS with
-// the largest s that keeps |dS| <= 2 D max|dO| max|V| within 2^15 (-25 to 40), found
-// by a pass over dO and V ahead (one s for the call); the powers are taken back from
-// the sums. (dV's error over 32000 keys: 4.4e-4 without, 3.0e-4
+// the largest s that keeps |dS| <= 2 |dO_i| max_j |v_j| (norms of head vectors) within
+// 2^15 (-26 to 40), for each (b, K/V head) from its largest norms, which a pass over
+// dO and V ahead finds; the powers are taken back from the sums. (dV's error over 32000 keys: 4.4e-4 without, 3.0e-4
 // so, like dQ's and dK's; 3 x 777 queries over 1301 keys, 16 heads of 64: 82 and 89 us.)
 #pragma once
 
@@ -158,26 +158,27 @@ __device__ __forceinline__ void load32(uint32_t taddr, float* x) {
     ptx::reg_fence32(r);
 }
 
-// Exponents that P and dS carry in fp16 (see above), of the maxima that the blocks of the pass ahead have left.
+// Exponents that P and dS carry in fp16 (see above). range_of fetches what the pass ahead has left of a (b, K/V head), a word a
+// lane; ds_shift, when it is needed, finds the exponent in it.
 template <bool BF16>
 constexpr int kPShift = BF16 ? 0 : 14;
-template <int D, bool BF16>
-__device__ __forceinline__ int ds_shift(const BwdParams& p) {
-    if (BF16) return 0;
-    uint32_t m = 0, each[kMostRanges / 32];                    // (all on their way at once)
+template <bool BF16>
+__device__ __forceinline__ uint32_t range_of(const BwdParams& p, int b, int hk) {
+    const int lane = threadIdx.x & 31;
+    return BF16 || lane >= p.n_range ? 0u : __ldcg(p.range + ((long long)b * p.Hkv + hk) * p.n_range + lane);
+}
+template <bool BF16>
+__device__ __forceinline__ int ds_shift(uint32_t m) {
+    if constexpr (BF16) {
+        return 0;
+    } else {
 #pragma unroll
-    for (int i = 0; i < kMostRanges / 32; ++i) {
-        const int at = 32 * i + (threadIdx.x & 31);
-        each[i] = at < p.n_range ? __ldcg(p.range + at) : 0u;
+        for (int d = 16; d > 0; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
+        // the squares of the norms, rounded up; the bound's, 4 |dO|^2 |V|^2, is below 2^e
+        const float bound = 4.f * __uint_as_float(((m & 0xffffu) + 1u) << 16) * __uint_as_float(((m >> 16) + 1u) << 16);
+        const int e = (int)(__float_as_uint(bound) >> 23) - 126;
+        return min(40, 15 - ((e + 1) >> 1));
     }
-#pragma unroll
-    for (int i = 0; i < kMostRanges / 32; ++i) m = __vmaxu2(m, each[i]);
-#pragma unroll
-    for (int e = 16; e > 0; e >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, e));
-    const float bound = 2.f * D * __half2float(__ushort_as_half((unsigned short)(m & 0xffffu))) *
-                        __half2float(__ushort_as_half((unsigned short)(m >> 16)));
-    const int above = (int)(__float_as_uint(bound) >> 23) - 126;               // bound < 2^above
-    return min(40, 15 - above);
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
@@ -646,9 +647,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_base + C::cS + kCols * wg, tDP = tmem + lane_base + C::cDP + kCols * wg;
         const float sl = p.scale_log2;
-        const int shift = ds_shift<D, BF16>(p);
-        const float more = power_of_two(shift - kPShift<BF16>);      // of dS over P
-        const float back = power_of_two(wg >= 2 ? -shift : -kPShift<BF16>);
+        int shift = 0;                                               // of the tile
+        float more = 1.f, back = 1.f;                                // of dS over P; of the tile before
         uint32_t tiles = 0, use = 0;
         Place<C::kQ> q;
         Place<C::kG> g;
@@ -676,6 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int t = next_tile(k, ring, sc);
             if (t < 0) break;
             const KvTile w = kv_tile<PARTS>(t, p);
+            const uint32_t range = range_of<BF16>(p, w.b, w.hk);
             const int key = w.k0 + r;
             // queries [see, end) see this key
             const int see = p.causal ? key - p.off : 0;
@@ -745,7 +746,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 warp_arrive_tmem(bar(C::bP));
                 if (lane == 0) ptx::mbar_arrive(bar(C::bQEmpty + q.at));
-                if (it == 0 && !(alive = finish())) break;
+                if (it == 0) {
+                    if (!(alive = finish())) break;
+                    shift = ds_shift<BF16>(range);
+                    more = power_of_two(shift - kPShift<BF16>);
+                }
                 // ---- dS = P (dP - delta)
                 alive = warp_wait2(bar(C::bG + g.at), g.parity(), bar(C::bDP), use & 1u, sc);
                 if (!alive) break;
@@ -786,6 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             done_part = PARTS && w.split >= 0;
             done_row = row;
             done_there = key < p.Sk;
+            back = power_of_two(is_k ? -shift : -kPShift<BF16>);
         }
         if (alive) finish();
     }
@@ -1177,8 +1183,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_base + C::cS + kCols * wg, tDP = tmem + lane_base + C::cDP + kCols * wg;
         const float sl = p.scale_log2;
-        const int shift = ds_shift<D, BF16>(p);
-        const float more = power_of_two(shift), back = power_of_two(-shift);
+        int shift = 0;                                            // of the tile
+        float more = 1.f, back = 1.f;                             // 2^shift; 2^-shift of the tile before
         float2* stat = reinterpret_cast<float2*>(smem_ptr + C::kStatOff);
         uint32_t tiles = 0, su = 0, dp = 0, seen = 0;
         bool alive = true;
@@ -1207,6 +1213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int t = twice ? twice_entry(e) : e;
             if (t < 0) break;
             const QTile w = q_tile<PARTS>(t, p);
+            const uint32_t range = range_of<BF16>(p, w.b, w.hk);
             const int row = w.m0 + r;
             const bool there = row < p.Sq;
             const size_t at = ((size_t)w.b * p.Hq + w.h) * p.Sp + row;
@@ -1218,8 +1225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float l = there ? p.lse[((size_t)w.b * p.Hq + w.h) * p.Sq + row] : -INFINITY;
                 const bool any = l != -INFINITY;
                 nl = any ? -l * kLog2E : ADDITIVE ? 0.f : -INFINITY;
-                if (!ADDITIVE) nl += (float)shift;
-                is = any ? more : 0.f;
+                is = any ? 1.f : 0.f;
             }
             // delta of the tile's rows, eight a warp, O from device memory (whole lines of it) and dO from its tile
             constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kPasses = 8 / kAtOnce;              // lanes of a row
@@ -1257,11 +1263,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!warp_wait(bar(C::bDelta), k & 1u, sc)) return false;
                 nd = delta[r];
                 warp_arrive(bar(C::bGEmpty));                     // (the next tile's are written after its dO has come)
+                more = power_of_two(shift);
                 if (wg == 0 && w.split == 0) {
                     p.neg_delta[at] = nd * power_of_two(shift - kPShift<BF16>);
-                    if (!twice) p.neg_lse[at] = ADDITIVE ? nl : nl + (float)(kPShift<BF16> - shift);
-                    if (ADDITIVE && !twice) p.inv_sum[at] = is * power_of_two(kPShift<BF16> - shift);
+                    if (!twice) p.neg_lse[at] = ADDITIVE ? nl : nl + (float)kPShift<BF16>;
+                    if (ADDITIVE && !twice) p.inv_sum[at] = is * power_of_two(kPShift<BF16>);
                 }
+                if (ADDITIVE) is *= more;
+                else nd *= more;
                 return true;
             };
 
@@ -1330,7 +1339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++seen;
                 nl = stat[r].x;
-                is = stat[r].y * more;
+                is = stat[r].y;
             }
             // The first block of a tile is a copy of its own: it has the last tile's dQ and delta to see to.
             auto block = [&](int j, auto begins) -> bool {
@@ -1338,6 +1347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint4 o[kPasses];
                 if constexpr (decltype(begins)::value) fetch_o(o);
                 if (!logits(j, x)) return false;
+                if constexpr (decltype(begins)::value) shift = ds_shift<BF16>(range);
 #pragma unroll
                 for (int c = 0; c < kCols; ++c) x[c] = ptx::ex2(ADDITIVE ? x[c] + nl : x[c]);
                 if constexpr (decltype(begins)::value) {
@@ -1352,7 +1362,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 warp_arrive_tmem(bar(C::bDPFree));
 #pragma unroll
                 for (int c = 0; c < kCols; c += 2) {
-                    ptx::add2(d[c], d[c + 1], d[c], d[c + 1], nd, nd);
+                    if (BF16 || ADDITIVE) ptx::add2(d[c], d[c + 1], d[c], d[c + 1], nd, nd);
+                    else ptx::fma2(d[c], d[c + 1], d[c], d[c + 1], more, more, nd, nd);
                     if (ADDITIVE) ptx::mul2(d[c], d[c + 1], d[c], d[c + 1], is, is);
                     ptx::mul2(d[c], d[c + 1], d[c], d[c + 1], x[c], x[c + 1]);
                     pk[c / 2] = pack<BF16>(d[c], d[c + 1]);
@@ -1373,6 +1384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 out = p.part + w.split * ((long long)p.B * p.Sq * p.Hq * D) + (token * p.Hq + w.h) * D + 32 * wg;
             done_row = out;
             done_there = there;
+            back = power_of_two(-shift);
         }
         if (alive) finish();
     }

@@ -11,7 +11,7 @@ namespace attn {
 namespace bwd {
 
 constexpr int kBlock = 128;         // queries and keys of a tile
-constexpr int kMostRanges = 160;    // blocks of launch_range
+constexpr int kMostRanges = 32;     // parts of a sample's K/V head in launch_range: a word a lane for those who read them
 
 // Rows of the row statistics: whole blocks of queries for each (b, query head).
 inline long long padded_rows(int Sq) { return ((long long)Sq + kBlock - 1) / kBlock * kBlock; }
@@ -38,13 +38,23 @@ struct BwdParams {
     float* part;                    // splits > 1: FP32 sums of the parts, [splits] (B, Sq, Hq, D) or [splits][dV, dK] (B, part_rows, Hkv, D)
     int n_tiles;                    // tiles, each part one
     unsigned int* counter;          // tiles handed out beyond each CTA's first; launch_begin or launch_range sets it to 0
-    const unsigned int* range;      // fp16: of each block of launch_range, max |dO| and, in the upper half, max |V|
+    const unsigned int* range;      // fp16: what launch_range has left, n_range words for each (b, K/V head)
     int n_range;
     int vec8;                       // gradients may be written with 32-byte stores
     int stall;                      // failure-detection test hook, as in the forward kernel
     float scale, scale_log2;
     unsigned long long timeout_ns;
     unsigned int* status;
+};
+
+// fp16: the counters to 0, and the largest norms of dO's and V's head vectors (infinities and NaN left out) of each (b, K/V
+// head), as `parts` words, which hold the upper 16 bits of the FP32 squares that a part of the tokens has: dO's low, V's high.
+struct RangeParams {
+    unsigned int *counters, *range;
+    const uint16_t *d_o, *v;        // (B, Sq, Hkv * group, D) contiguous; (B, Sk, Hkv, D), v_stride from token to token
+    long long v_stride;
+    int units;                      // B * Hkv * parts
+    int parts, Hkv, group, Sq, Sk;
 };
 
 // The sum of a tensor's parts, times a factor, to 16 bits.
@@ -62,10 +72,7 @@ struct JoinParams {
 // Launchers; ATTN_OK or ATTN_ERR_CUDA. attr_set: per context and variant, that the shared memory is set of the kernel of
 // whole walks, of the one of parts.
 int launch_begin(unsigned int* counters, cudaStream_t stream);        // two of them to 0
-// fp16: the same, and the largest finite |dO| ((tokens, width) contiguous) and |V| (v_stride from token to token) that each of
-// `blocks` blocks finds, as two 16-bit halves.
-int launch_range(unsigned int* counters, unsigned int* range, int blocks, const void* d_o, long long q_values, const void* v,
-                 long long kv_tokens, long long v_stride, int kv_width, cudaStream_t stream);
+int launch_range(const RangeParams& p, int D, int num_sms, cudaStream_t stream);
 int launch_join(const JoinParams* p, int n, bool bf16, int num_sms, cudaStream_t stream);        // one or two tensors
 template <int D, bool BF16, bool ADDITIVE>
 int launch_dq(bool* attr_set, const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const CUtensorMap& d_o,

@@ -1,12 +1,12 @@
 // The small kernels around the products of the attention's backward pass: before
 // them the two counters are set from which their CTAs take work tiles, and in fp16
-// the largest |dO| and |V| are found, which bound dS; behind
-// them, where few tiles were cut into parts, the parts' FP32 sums are joined, in
-// the parts' order.
+// the largest norms of dO and V are found, which bound dS; behind them, where few tiles were
+// cut into parts, the parts' FP32 sums are joined, in the parts' order.
 #include <algorithm>
 
 #include "../../include/attn.h"
 #include "bwd_params.h"
+#include "e4m3.cuh"
 #include "early_launch.h"
 #include "ptx.cuh"
 
@@ -20,61 +20,78 @@ __global__ void bwd_begin_kernel(unsigned int* counters) {
     if (threadIdx.x < 2) counters[threadIdx.x] = 0u;
 }
 
-__device__ __forceinline__ uint32_t largest(uint32_t m, const uint4& w) {
+// Sum of the squares of eight values, infinities and NaN left out.
+__device__ __forceinline__ float squares(const uint4& w) {
     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t a = x[i] & 0x7fff7fffu;
-        m = __vmaxu2(m, a & ~__vcmpgeu2(a, 0x7c007c00u));                    // (infinities and NaN set no range)
+        const float2 f = widen<false>(a & ~__vcmpgeu2(a, 0x7c007c00u));
+        s = fmaf(f.x, f.x, fmaf(f.y, f.y, s));
     }
-    return m;
+    return s;
 }
 
-// Bound by memory, at small sizes by one wave's latency: eight values a load, two loads of each tensor in flight (13 MB: 6.8 us,
-// 3.5 more than the launch it takes the place of).
-constexpr int kRangeLoads = 2;
-__global__ void __launch_bounds__(1024) bwd_range_kernel(unsigned int* counters, unsigned int* range, const uint4* d_o,
-                                                        long long q_pieces, const uint16_t* v, long long kv_tokens,
-                                                        long long v_stride, int kv_pieces) {
+// A block takes a part of the tokens of one (b, K/V head), D / 8 lanes a head vector. Bound by memory, at small sizes by one
+// wave's latency: two vectors of each tensor in flight.
+constexpr int kRangeThreads = 512;
+template <int D>
+__global__ void __launch_bounds__(kRangeThreads, 2) bwd_range_kernel(const RangeParams p) {
     wait_for_inputs();
     let_next_start();
-    __shared__ uint32_t part[2][32];
-    if (blockIdx.x == 0 && threadIdx.x < 2) counters[threadIdx.x] = 0u;
-    const long long first = (long long)blockIdx.x * 1024 + threadIdx.x, step = (long long)gridDim.x * 1024;
-    uint32_t m[2] = {0u, 0u};
-    const long long pieces = kv_tokens * kv_pieces;
-    const bool whole = v_stride == 8LL * kv_pieces;
-    for (long long e = first; e < max(q_pieces, pieces); e += kRangeLoads * step) {
-        uint4 w[kRangeLoads], x[kRangeLoads];
+    constexpr int kLanes = D / 8, kRows = kRangeThreads / kLanes, kWarps = kRangeThreads / 32;
+    __shared__ __align__(8) float part[kWarps][2];
+    if (blockIdx.x == 0 && threadIdx.x < 2) p.counters[threadIdx.x] = 0u;
+    const int lane = threadIdx.x % 32, piece = threadIdx.x % kLanes;
+    const long long q_rows = (long long)p.Sq * p.group, step = (long long)p.parts * kRows;
+    for (unsigned u = blockIdx.x; u < (unsigned)p.units; u += gridDim.x) {
+        const int bh = (int)(u / (unsigned)p.parts), b = bh / p.Hkv, hk = bh - b * p.Hkv;
+        const uint16_t* const d_o = p.d_o + ((long long)b * p.Sq * p.Hkv + hk) * p.group * D + 8 * piece;
+        const uint16_t* const v = p.v + (long long)b * p.Sk * p.v_stride + hk * D + 8 * piece;
+        const long long first = ((int)u - bh * p.parts) * kRows + threadIdx.x / kLanes;
+        float top = 0.f;                                          // of dO in even lanes, of V in odd ones
+        // (whole warps stay in the loop: its bound is a warp's first row)
+        for (long long r = first; r - lane / kLanes < max(q_rows, (long long)p.Sk); r += 2 * step) {
+            uint4 w[2][2];
 #pragma unroll
-        for (int i = 0; i < kRangeLoads; ++i) {
-            const long long at = e + i * step, token = whole || at >= pieces ? 0 : at / kv_pieces;
-            w[i] = at < q_pieces ? __ldcg(d_o + at) : make_uint4(0u, 0u, 0u, 0u);
-            x[i] = at < pieces ? __ldcg(reinterpret_cast<const uint4*>(v + token * v_stride + 8 * (at - token * kv_pieces)))
-                               : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < 2; ++i) {
+                const long long at = r + i * step;
+                w[i][0] = w[i][1] = make_uint4(0u, 0u, 0u, 0u);
+                if (at < q_rows) {
+                    const long long token = at <= 0x7fffffff ? (long long)((unsigned)at / (unsigned)p.group) : at / p.group;
+                    w[i][0] = __ldcg(reinterpret_cast<const uint4*>(
+                        d_o + (token * p.Hkv * p.group + (at - token * p.group)) * D));
+                }
+                if (at < p.Sk) w[i][1] = __ldcg(reinterpret_cast<const uint4*>(v + at * p.v_stride));
+            }
+            // four sums over a vector's lanes, each in the end in a quarter of them: 4 or 5 exchanges instead of 12 or 16
+            float s[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float a = squares(w[i][0]), c = squares(w[i][1]);
+                s[i] = (lane & 1 ? c : a) + __shfl_xor_sync(0xffffffffu, lane & 1 ? a : c, 1);
+            }
+            float t = (lane & 2 ? s[1] : s[0]) + __shfl_xor_sync(0xffffffffu, lane & 2 ? s[0] : s[1], 2);
+#pragma unroll
+            for (int d = 4; d < kLanes; d *= 2) t += __shfl_xor_sync(0xffffffffu, t, d);
+            top = fmaxf(top, t);
         }
 #pragma unroll
-        for (int i = 0; i < kRangeLoads; ++i) {
-            m[0] = largest(m[0], w[i]);
-            m[1] = largest(m[1], x[i]);
+        for (int d = 16; d > 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        if (lane < 2) part[threadIdx.x / 32][lane] = top;
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            const float2 both = *reinterpret_cast<const float2*>(part[lane % kWarps]);
+            float o = both.x, x = both.y;
+#pragma unroll
+            for (int d = kWarps / 2; d > 0; d >>= 1) {
+                o = fmaxf(o, __shfl_xor_sync(0xffffffffu, o, d));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+            }
+            if (lane == 0) p.range[u] = __float_as_uint(o) >> 16 | (__float_as_uint(x) & 0xffff0000u);
         }
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) m[k] = __vmaxu2(m[k], __shfl_xor_sync(0xffffffffu, m[k], d));
-        if (threadIdx.x % 32 == 0) part[k][threadIdx.x / 32] = m[k];
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            m[k] = part[k][threadIdx.x];
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) m[k] = __vmaxu2(m[k], __shfl_xor_sync(0xffffffffu, m[k], d));
-            m[k] = max(m[k] & 0xffffu, m[k] >> 16);
-        }
-        if (threadIdx.x == 0) range[blockIdx.x] = m[0] | m[1] << 16;
+        __syncthreads();
     }
 }
 
@@ -127,11 +144,10 @@ int launch_begin(unsigned int* counters, cudaStream_t stream) {
     return launch_early(bwd_begin_kernel, 1u, 32u, (size_t)0, stream, counters) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-int launch_range(unsigned int* counters, unsigned int* range, int blocks, const void* d_o, long long q_values, const void* v,
-                 long long kv_tokens, long long v_stride, int kv_width, cudaStream_t stream) {
-    return launch_early(bwd_range_kernel, (unsigned)blocks, 1024u, (size_t)0, stream, counters, range, static_cast<const uint4*>(d_o),
-                        q_values / 8, static_cast<const uint16_t*>(v), kv_tokens, v_stride, kv_width / 8) == cudaSuccess
-               ? ATTN_OK : ATTN_ERR_CUDA;
+int launch_range(const RangeParams& p, int D, int num_sms, cudaStream_t stream) {
+    const unsigned grid = (unsigned)std::min(p.units, 4 * num_sms);
+    return launch_early(D == 128 ? bwd_range_kernel<128> : bwd_range_kernel<64>, grid, (unsigned)kRangeThreads, (size_t)0,
+                        stream, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace bwd
