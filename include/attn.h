@@ -529,7 +529,8 @@ size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, long lo
  *   k, v, dk, dv  device, (B, Sk, Hkv, D), with strides of their own
  *               The gradients are written whole and overlap no input and no
  *               other tensor, but may interleave in one packed tensor. (One that
- *               begins where another tensor does is refused.)
+ *               begins where another tensor does is refused, and so is such a
+ *               workspace.)
  *   scale, mask_kind, mask  as for attn_fwd. The mask has no gradient. Mask values
  *               below -2.3e38 hide a key as -inf does. With an additive mask the
  *               statistics of rows whose |lse| is above 256 are found anew, in one
@@ -537,8 +538,8 @@ size_t attn_paged_workspace_bytes(int B, int Hq, int Hkv, int Sq, int D, long lo
  *               large values leaves lse without the logits' bits.
  *   window, sinks  window > 0 (causal mask only): as for attn_fwd_window; 0: none
  *   workspace   device scratch of attn_bwd_workspace_bytes(...) bytes, 256-byte
- *               aligned, contents overwritten. Calls that may run at the same
- *               time need one each.
+ *               aligned, contents overwritten; it overlaps no tensor. Calls that may
+ *               run at the same time need one each.
  * A row without a visible key gives no gradient: its dQ is 0 and it adds nothing
  * to dK and dV. With Sq or Sk of 0 the gradients that exist are 0. Blocks of 128
  * keys and 128 queries that hide all of their pairs are not computed. Q, K, V and dO
@@ -624,6 +625,7 @@ int attn_rope_axes_table(float *table, int max_pos, const int *sections, int n_a
  *               token (a multiple of 8, at least H * D)
  *   codes, scale  device, (B, S, H, D) bytes, 16-byte aligned, and FP32 (B, S, H);
  *               contiguous
+ * x, codes and scale do not overlap. (Two that begin at one address are refused.)
  * attn_checkpoint_store writes codes and scale, attn_checkpoint_load writes x:
  * code * scale, exact in bf16; in fp16 rounded, and cut to +-65504.
  */

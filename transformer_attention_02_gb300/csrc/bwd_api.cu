@@ -129,6 +129,15 @@ bool tokens_ok(const void* ptr, long long stride, int B, int S, int H, int D) {
     return ptr && aligned(ptr, 16) && stride >= (long long)H * D && stride % 8 == 0 && stride < (1LL << 39) / std::max(1, S);
 }
 
+// Whether one of the first `written` of these tensors begins where another of them does (null: no tensor).
+template <int N>
+bool any_begins_in(const void* const (&all)[N], int written) {
+    for (int i = 0; i < written; ++i)
+        for (int j = 0; j < N; ++j)
+            if (i != j && all[i] && all[i] == all[j]) return true;
+    return false;
+}
+
 int check_sizes(int B, int Hq, int Hkv, int Sq, int Sk, int D) {
     if (B < 0 || Hq < 0 || Hkv <= 0 || Sq < 0 || Sk < 0 || D <= 0 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
     if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
@@ -213,11 +222,10 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
         !tokens_ok(dk, dk_stride, B, Sk, Hkv, D) || !tokens_ok(dv, dv_stride, B, Sk, Hkv, D) ||
         !tokens_ok(d_o, (long long)Hq * D, B, Sq, Hq, D) || !tokens_ok(o, (long long)Hq * D, B, Sq, Hq, D))
         return ATTN_ERR_INVALID_ARG;
-    if (q_values > 0 && kv_values > 0)                            // a result that begins where another tensor does
-        for (const void* out : {dq, dk, dv})
-            for (const void* in : {d_o, q, k, v, o, (const void*)lse, (const void*)mask, (const void*)workspace})
-                if (out == in) return ATTN_ERR_INVALID_ARG;
-    if (q_values > 0 && kv_values > 0 && (dq == dk || dq == dv || dk == dv)) return ATTN_ERR_INVALID_ARG;
+    if (q_values > 0 && kv_values > 0) {                          // what is written begins where another tensor does
+        const void* const all[] = {dq, dk, dv, workspace, d_o, q, k, v, o, lse, mask};
+        if (any_begins_in(all, 4)) return ATTN_ERR_INVALID_ARG;
+    }
     const bool additive = is_additive(mask_kind);
     if (q_values > 0 && (!lse || !aligned(lse, 4))) return ATTN_ERR_INVALID_ARG;
     if (additive && q_values > 0 && kv_values > 0 && (!mask || !aligned(mask, 4))) return ATTN_ERR_INVALID_ARG;
@@ -338,6 +346,8 @@ int convert(bool store, const void* x, long long stride, const void* codes, cons
             cudaStream_t stream, bool bf16) {
     int rc = check_vectors(x, stride, codes, scale, B, S, H, D);
     if (rc != ATTN_OK || (long long)B * S * H == 0) return rc;
+    const void* const all[] = {x, codes, scale};
+    if (any_begins_in(all, 3)) return ATTN_ERR_INVALID_ARG;
     DeviceState dev{};
     if ((rc = device_state(&dev)) != ATTN_OK) return rc;
     const checkpoint::Tensor t = vectors_of(x, stride, codes, scale, B, S, H);
@@ -382,6 +392,8 @@ int bwd_checkpoint_impl(const void* d_o, const void* q8, const void* k8, const v
     if (mask_kind < ATTN_MASK_NONE || mask_kind > ATTN_MASK_CAUSAL_ADDITIVE) return ATTN_ERR_INVALID_ARG;
     const CheckpointLayout l = checkpoint_layout(B, Hq, Hkv, Sq, Sk, D, mask_kind);
     if (workspace_bytes < l.total) return ATTN_ERR_INVALID_ARG;
+    const void* const all[] = {dq, dk, dv, workspace, q8, k8, v8, q_scale, k_scale, v_scale, d_o, mask};
+    if (any_begins_in(all, 4)) return ATTN_ERR_INVALID_ARG;
     float* const lse = reinterpret_cast<float*>(ws + l.lse);
     // Everything is checked before the first launch: the backward pass's own arguments here, the forward pass's are among them.
     rc = bwd_impl(d_o, ws, ws + l.k, ws + l.v, ws + l.o, lse, dq, dk, dv, qs, ks, ks, dq_stride, dk_stride, dv_stride, B, Hq, Hkv,
