@@ -46,3 +46,43 @@ def test_gradients_onto_other_tensors_are_refused(fn, out, at):
     assert _backward(fn) != INVALID
     if at != out:
         assert _backward(fn, **{out: BACK[at]}) == INVALID
+
+
+@pytest.mark.parametrize("fn", CONVERSIONS)
+@pytest.mark.parametrize("kw,code", [
+    *[({n: None}, 1) for n in ("x", "codes", "scale")], *[({n: 15 * P + 8}, 1) for n in ("x", "codes")], (dict(scale=15 * P + 2), 1),
+    (dict(stride=120), 1), (dict(stride=132), 1), (dict(B=-1), 1), (dict(S=-1), 1), (dict(H=-1), 1), (dict(D=96), 2), (dict(D=0), 1),
+    (dict(B=1 << 30, S=1 << 30), 1), (dict(B=0), 0), (dict(S=0), 0), (dict(H=0), 0),
+])
+def test_conversions(fn, kw, code):
+    assert _store(fn) != INVALID
+    assert _store(fn, **kw) == code
+
+
+@pytest.mark.parametrize("fn", BACKWARDS)
+@pytest.mark.parametrize("kw,code", [
+    *[({n: None}, 1) for n in ("g", "q", "k", "v", "qs", "ks", "vs", "dq", "dk", "dv", "ws")],
+    *[({n: 15 * P + 8}, 1) for n in ("g", "q", "k", "v", "dq", "dk", "dv", "ws")],
+    *[({n: 15 * P + 1}, 1) for n in ("qs", "ks", "vs")], (dict(ws=15 * P + 128), 1),
+    *[(dict(st=[s if i == n else 128 for i in range(3)]), 1) for n in range(3) for s in (120, 132, 64)],
+    (dict(kind=-1), 1), (dict(kind=4), 1), (dict(kind=5), 1), (dict(window=2), 1), (dict(kind=1, window=-1), 1), (dict(kind=1, sinks=-1), 1),
+    (dict(kind=3, mask=14 * P, window=2), 1), (dict(kind=2), 1), (dict(kind=3), 1), (dict(kind=2, mask=14 * P + 1), 1),
+    (dict(size=1000), 1), (dict(B=-1), 1), (dict(Sq=-1), 1), (dict(Sk=-1), 1), (dict(Hkv=0), 1), (dict(Hq=3), 1), (dict(Sq=(1 << 30) + 1), 1),
+    (dict(D=32), 2), (dict(D=96), 2), (dict(B=0), 0), (dict(Sq=0, Sk=0), 0),
+])
+def test_backward(fn, kw, code):
+    assert _backward(fn) != INVALID
+    assert _backward(fn, **kw) == code
+
+
+@pytest.mark.parametrize("fn", BACKWARDS)
+@pytest.mark.parametrize("kw", [dict(kind=1), dict(kind=1, window=5, sinks=2), dict(kind=2, mask=14 * P), dict(kind=3, mask=14 * P),
+                                dict(D=128, st=[256, 256, 264]), dict(Hq=4, st=[256, 128, 128])])
+def test_other_calls_that_are_none_of_these(fn, kw):
+    assert _backward(fn, **kw) != INVALID
+
+
+@pytest.mark.parametrize("fn", BACKWARDS)
+def test_the_workspace_is_as_large_as_the_call_says(fn):
+    size = A.attn_bwd_checkpoint_workspace_bytes(1, 2, 2, 16, 16, 64, 0)
+    assert _backward(fn, size=size) != INVALID and _backward(fn, size=size - 1) == INVALID
