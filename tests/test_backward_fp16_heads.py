@@ -79,7 +79,8 @@ def test_infinities_and_nan_set_no_power(value):
     R.check(ta.attention_backward(d_o, q, k, v, o.to(F16), lse.float(), **kw), want, bounds)
 
 
-def test_the_workspace_holds_a_word_for_every_head():
-    # 320 heads, a word each behind eight others: 1312 bytes, in steps of 256; then two statistics for 128 rows of each
-    assert A.attn_bwd_workspace_bytes(40, 8, 8, 100, 100, 64, 0) == 1536 + 2 * 40 * 8 * 128 * 4
+def test_the_workspace_holds_the_words_of_every_head():
+    # 320 heads, eight to a block of 64 vectors of 64 values: 200 vectors a head in 7 parts of 4 x 8, a word each behind eight
+    # others, in steps of 256 bytes; then two statistics for 128 rows of each head
+    assert A.attn_bwd_workspace_bytes(40, 8, 8, 100, 100, 64, 0) == 9216 + 2 * 40 * 8 * 128 * 4
     assert A.attn_bwd_workspace_bytes(1, 1, 1, 100, 100, 64, 0) == 1024 + 2 * 128 * 4

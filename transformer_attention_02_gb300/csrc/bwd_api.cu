@@ -106,19 +106,31 @@ Parts parts_in_window(Parts s, int B, int Hq, int Hkv, int Sq, int Sk, int windo
     return s;
 }
 
-// The head: two tile counters, and behind 32 bytes the words of fp16's ranges. Then three statistics for every query row, the third
-// with an additive mask only.
-constexpr size_t kCounters = 8;                     // words
-int range_parts(int B, int Hkv) {                    // (two blocks an SM)
-    return (int)std::min<long long>(std::max(1LL, 2 * device_sm_count() / ((long long)B * Hkv)), bwd::kMostRanges);
+// The head: two tile counters, and behind 32 bytes the words of fp16's ranges, one for each part of a (b, K/V head). Then three
+// statistics for every query row, the third with an additive mask only.
+constexpr size_t kHead = 1024, kCounters = 8;       // bytes at least; words
+
+// Neighbouring K/V heads of a block (2^shift) and parts of each in fp16's pass over dO and V: two blocks an SM. More heads are
+// quicker, but a tile's warps read a head's parts at once where those are 32 at most. No part has less than a block's four vectors
+// a row of lanes.
+struct RangeSplit {
+    int shift, parts;
+};
+RangeSplit range_split(int B, int Hq, int Hkv, int Sq, int Sk, int D) {
+    const long long heads = (long long)B * Hkv, blocks = 2LL * device_sm_count();
+    RangeSplit s{0, 1};
+    while (s.shift < 3 && Hkv % (2 << s.shift) == 0 && (heads >> (s.shift + 1)) * 32 >= blocks) ++s.shift;
+    const long long rows = (long long)Sq * (Hq / Hkv) + Sk, each = 4 * (bwd::kRangeThreads / (D / 8) >> s.shift);
+    s.parts = (int)std::min({std::max(1LL, blocks / (heads >> s.shift)), (rows + each - 1) / each, 160LL});
+    return s;
 }
-size_t head_bytes(int B, int Hkv) {
-    const size_t words = kCounters + (size_t)B * Hkv * range_parts(B, Hkv);
-    return align_up(std::max<size_t>(1024, words * sizeof(unsigned int)));
+size_t head_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D) {
+    const size_t words = kCounters + (size_t)B * Hkv * range_split(B, Hq, Hkv, Sq, Sk, D).parts;
+    return std::max(kHead, align_up(words * sizeof(unsigned int)));
 }
 size_t stat_bytes(int B, int Hq, int Sq) { return align_up((size_t)B * Hq * bwd::padded_rows(Sq) * sizeof(float)); }
 size_t bwd_workspace(int B, int Hq, int Hkv, int Sq, int Sk, int D, int mask_kind) {
-    return head_bytes(B, Hkv) + stat_bytes(B, Hq, Sq) * (is_additive(mask_kind) ? 3 : 2) +
+    return head_bytes(B, Hq, Hkv, Sq, Sk, D) + stat_bytes(B, Hq, Sq) * (is_additive(mask_kind) ? 3 : 2) +
            parts_for(B, Hq, Hkv, Sq, Sk, D, mask_kind).bytes;
 }
 
@@ -253,7 +265,7 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
         return ATTN_ERR_CUDA;
     const size_t stat = stat_bytes(B, Hq, Sq);
     unsigned int* const counters = static_cast<unsigned int*>(workspace);
-    char* const ws = static_cast<char*>(workspace) + head_bytes(B, Hkv);
+    char* const ws = static_cast<char*>(workspace) + head_bytes(B, Hq, Hkv, Sq, Sk, D);
 
     Parts parts = parts_for(B, Hq, Hkv, Sq, Sk, D, mask_kind);
     if (window > 0) parts = parts_in_window(parts, B, Hq, Hkv, Sq, Sk, window, sinks);
@@ -267,8 +279,10 @@ int bwd_impl(const void* d_o, const void* q, const void* k, const void* v, const
         r.d_o = static_cast<const uint16_t*>(d_o);
         r.v = static_cast<const uint16_t*>(v);
         r.v_stride = v_stride;
-        r.parts = range_parts(B, Hkv);
-        r.units = B * Hkv * r.parts;                              // (parts where B * Hkv is small)
+        const RangeSplit split = range_split(B, Hq, Hkv, Sq, Sk, D);
+        r.shift = split.shift;
+        r.parts = split.parts;
+        r.units = (B * Hkv >> r.shift) * r.parts;                 // (parts where they are few)
         r.Hkv = Hkv;
         r.group = Hq / Hkv;
         r.Sq = Sq;

@@ -159,23 +159,29 @@ __device__ __forceinline__ void load32(uint32_t taddr, float* x) {
 }
 
 // Exponents that P and dS carry in fp16 (see above). range_of fetches what the pass ahead has left of a (b, K/V head), a word a
-// lane; ds_shift, when it is needed, finds the exponent in it.
+// lane (more where heads are few); ds_shift, when it is needed, finds the exponent in it.
 template <bool BF16>
 constexpr int kPShift = BF16 ? 0 : 14;
 template <bool BF16>
 __device__ __forceinline__ uint32_t range_of(const BwdParams& p, int b, int hk) {
-    const int lane = threadIdx.x & 31;
-    return BF16 || lane >= p.n_range ? 0u : __ldcg(p.range + ((long long)b * p.Hkv + hk) * p.n_range + lane);
+    if constexpr (BF16) {
+        return 0u;
+    } else {
+        const int lane = threadIdx.x & 31;
+        const unsigned int* const words = p.range + ((long long)b * p.Hkv + hk) * p.n_range;
+        uint32_t m = lane < p.n_range ? __ldcg(words + lane) : 0u;
+        for (int i = lane + 32; i < p.n_range; i += 32) m = __vmaxu2(m, __ldcg(words + i));
+        return m;
+    }
 }
 template <bool BF16>
 __device__ __forceinline__ int ds_shift(uint32_t m) {
     if constexpr (BF16) {
         return 0;
     } else {
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, d));
         // the squares of the norms, rounded up; the bound's, 4 |dO|^2 |V|^2, is below 2^e
-        const float bound = 4.f * __uint_as_float(((m & 0xffffu) + 1u) << 16) * __uint_as_float(((m >> 16) + 1u) << 16);
+        const uint32_t g = __reduce_max_sync(0xffffffffu, m & 0xffffu), v = __reduce_max_sync(0xffffffffu, m >> 16);
+        const float bound = 4.f * __uint_as_float((g + 1u) << 16) * __uint_as_float((v + 1u) << 16);
         const int e = (int)(__float_as_uint(bound) >> 23) - 126;
         return min(40, 15 - ((e + 1) >> 1));
     }

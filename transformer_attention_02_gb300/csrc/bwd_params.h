@@ -11,7 +11,7 @@ namespace attn {
 namespace bwd {
 
 constexpr int kBlock = 128;         // queries and keys of a tile
-constexpr int kMostRanges = 32;     // parts of a sample's K/V head in launch_range: a word a lane for those who read them
+constexpr int kRangeThreads = 512;  // of a block of launch_range
 
 // Rows of the row statistics: whole blocks of queries for each (b, query head).
 inline long long padded_rows(int Sq) { return ((long long)Sq + kBlock - 1) / kBlock * kBlock; }
@@ -53,7 +53,8 @@ struct RangeParams {
     unsigned int *counters, *range;
     const uint16_t *d_o, *v;        // (B, Sq, Hkv * group, D) contiguous; (B, Sk, Hkv, D), v_stride from token to token
     long long v_stride;
-    int units;                      // B * Hkv * parts
+    int shift;                      // a block takes 2^shift heads (a divisor of Hkv, at most 8)
+    int units;                      // (B * Hkv >> shift) * parts
     int parts, Hkv, group, Sq, Sk;
 };
 

@@ -26,70 +26,89 @@ __device__ __forceinline__ float squares(const uint4& w) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t a = x[i] & 0x7fff7fffu;
-        const float2 f = widen<false>(a & ~__vcmpgeu2(a, 0x7c007c00u));
+        const float2 f = widen<false>(x[i]);
         s = fmaf(f.x, f.x, fmaf(f.y, f.y, s));
+    }
+    if (!(s < INFINITY)) {
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = widen<false>(x[i]);
+            s += (fabsf(f.x) < INFINITY ? f.x * f.x : 0.f) + (fabsf(f.y) < INFINITY ? f.y * f.y : 0.f);
+        }
     }
     return s;
 }
 
-// A block takes a part of the tokens of one (b, K/V head), D / 8 lanes a head vector. Bound by memory, at small sizes by one
-// wave's latency: two vectors of each tensor in flight.
-constexpr int kRangeThreads = 512;
+// A block takes a part of the head vectors of 2^shift neighbouring K/V heads, dO's and then V's, D / 8 lanes a vector. Bound by
+// memory, which wants whole stretches of a token: with a head a block 4 x 2048 tokens of 32 heads of 128 take 38 us, with eight
+// 32, and 27 (134 MB, 5.0 TB/s) since infinities are looked for only where a sum has met one. At small sizes bound by one wave's
+// latency: four vectors in flight.
 template <int D>
 __global__ void __launch_bounds__(kRangeThreads, 2) bwd_range_kernel(const RangeParams p) {
     wait_for_inputs();
     let_next_start();
-    constexpr int kLanes = D / 8, kRows = kRangeThreads / kLanes, kWarps = kRangeThreads / 32;
-    __shared__ __align__(8) float part[kWarps][2];
+    constexpr int kLanes = D / 8, kVectors = kRangeThreads / kLanes;
+    __shared__ float2 part[kVectors];
     if (blockIdx.x == 0 && threadIdx.x < 2) p.counters[threadIdx.x] = 0u;
-    const int lane = threadIdx.x % 32, piece = threadIdx.x % kLanes;
-    const long long q_rows = (long long)p.Sq * p.group, step = (long long)p.parts * kRows;
+    const int lane = threadIdx.x % 32, piece = threadIdx.x % kLanes, vector = threadIdx.x / kLanes, heads = 1 << p.shift;
+    const int per_row = p.Hkv >> p.shift;                         // units of a token
+    const long long q_rows = (long long)p.Sq * p.group, rows = q_rows + p.Sk;
+    const long long step = (long long)p.parts * (kVectors >> p.shift);
     for (unsigned u = blockIdx.x; u < (unsigned)p.units; u += gridDim.x) {
-        const int bh = (int)(u / (unsigned)p.parts), b = bh / p.Hkv, hk = bh - b * p.Hkv;
+        const int at_heads = (int)(u / (unsigned)p.parts), split = (int)u - at_heads * p.parts, b = at_heads / per_row;
+        const int hk = ((at_heads - b * per_row) << p.shift) + (vector & (heads - 1));
         const uint16_t* const d_o = p.d_o + ((long long)b * p.Sq * p.Hkv + hk) * p.group * D + 8 * piece;
         const uint16_t* const v = p.v + (long long)b * p.Sk * p.v_stride + hk * D + 8 * piece;
-        const long long first = ((int)u - bh * p.parts) * kRows + threadIdx.x / kLanes;
-        float top = 0.f;                                          // of dO in even lanes, of V in odd ones
-        // (whole warps stay in the loop: its bound is a warp's first row)
-        for (long long r = first; r - lane / kLanes < max(q_rows, (long long)p.Sk); r += 2 * step) {
-            uint4 w[2][2];
+        const long long begin = (long long)split * (kVectors >> p.shift);
+        float2 top = make_float2(0.f, 0.f);
+        // (all warps stay in the loop)
+        for (long long r0 = begin; r0 < rows; r0 += 4 * step) {
+            const long long r = r0 + (vector >> p.shift);
+            uint4 w[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 const long long at = r + i * step;
-                w[i][0] = w[i][1] = make_uint4(0u, 0u, 0u, 0u);
+                const uint16_t* from = v + (at - q_rows) * p.v_stride;
                 if (at < q_rows) {
                     const long long token = at <= 0x7fffffff ? (long long)((unsigned)at / (unsigned)p.group) : at / p.group;
-                    w[i][0] = __ldcg(reinterpret_cast<const uint4*>(
-                        d_o + (token * p.Hkv * p.group + (at - token * p.group)) * D));
+                    from = d_o + (token * p.Hkv * p.group + (at - token * p.group)) * D;
                 }
-                if (at < p.Sk) w[i][1] = __ldcg(reinterpret_cast<const uint4*>(v + at * p.v_stride));
+                w[i] = at < rows ? __ldcg(reinterpret_cast<const uint4*>(from)) : make_uint4(0u, 0u, 0u, 0u);
             }
             // four sums over a vector's lanes, each in the end in a quarter of them: 4 or 5 exchanges instead of 12 or 16
             float s[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float a = squares(w[i][0]), c = squares(w[i][1]);
+                const float a = squares(w[2 * i]), c = squares(w[2 * i + 1]);
                 s[i] = (lane & 1 ? c : a) + __shfl_xor_sync(0xffffffffu, lane & 1 ? a : c, 1);
             }
             float t = (lane & 2 ? s[1] : s[0]) + __shfl_xor_sync(0xffffffffu, lane & 2 ? s[0] : s[1], 2);
 #pragma unroll
             for (int d = 4; d < kLanes; d *= 2) t += __shfl_xor_sync(0xffffffffu, t, d);
-            top = fmaxf(top, t);
+            if (r + (lane & 3) * step < q_rows) top.x = fmaxf(top.x, t);
+            else top.y = fmaxf(top.y, t);
         }
-#pragma unroll
-        for (int d = 16; d > 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        if (lane < 2) part[threadIdx.x / 32][lane] = top;
-        __syncthreads();
-        if (threadIdx.x < 32) {
-            const float2 both = *reinterpret_cast<const float2*>(part[lane % kWarps]);
-            float o = both.x, x = both.y;
-#pragma unroll
-            for (int d = kWarps / 2; d > 0; d >>= 1) {
-                o = fmaxf(o, __shfl_xor_sync(0xffffffffu, o, d));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+        auto over = [&](int lanes) {
+            for (int d = lanes / 2; d > 0; d >>= 1) {
+                top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, d));
+                top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, d));
             }
-            if (lane == 0) p.range[u] = __float_as_uint(o) >> 16 | (__float_as_uint(x) & 0xffff0000u);
+        };
+        over(4);
+        if (piece == 0) part[vector] = top;
+        __syncthreads();
+        const int head = threadIdx.x / 32;                        // a warp each
+        if (head < heads) {
+            top = make_float2(0.f, 0.f);
+            for (int e = head + lane * heads; e < kVectors; e += 32 * heads) {
+                const float2 x = part[e];
+                top = make_float2(fmaxf(top.x, x.x), fmaxf(top.y, x.y));
+            }
+            over(32);
+            if (lane == 0)
+                p.range[((long long)at_heads * heads + head) * p.parts + split] =
+                    __float_as_uint(top.x) >> 16 | (__float_as_uint(top.y) & 0xffff0000u);
         }
         __syncthreads();
     }
@@ -145,7 +164,7 @@ int launch_begin(unsigned int* counters, cudaStream_t stream) {
 }
 
 int launch_range(const RangeParams& p, int D, int num_sms, cudaStream_t stream) {
-    const unsigned grid = (unsigned)std::min(p.units, 4 * num_sms);
+    const unsigned grid = (unsigned)std::min(p.units, 2 * num_sms);
     return launch_early(D == 128 ? bwd_range_kernel<128> : bwd_range_kernel<64>, grid, (unsigned)kRangeThreads, (size_t)0,
                         stream, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
