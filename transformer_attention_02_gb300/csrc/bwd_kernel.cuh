@@ -12,11 +12,12 @@
 //   bwd_dq_kernel   a tile is (b, query head, 128 queries); it walks the keys
 //                   that they see and holds dQ in TMEM.
 // S and dP are computed in both, so seven products run where five would do. One
-// kernel with five would have to add dQ up in device memory from all key blocks,
-// with atomics (whose order changes the result) or behind a lock, 4 bytes x D a
-// query and key block; and dK, dV, dQ, S and dP of 128 x 128 x 128 tiles do not fit
-// TMEM together. With two kernels no sum is atomic, and results are the same
-// from run to run.
+// kernel with five would add dQ up in device memory from all key blocks, 4 bytes x D
+// a query and key block, with atomics (whose order changes the result) or in an
+// order that CTAs wait for, and its dQ would share TMEM columns with S or dP, since
+// dK, dV, dQ, S and dP of 128 x 128 x 128 tiles do not fit at once. That kernel was
+// not built: this is an argument, not a measurement. With two kernels no sum is
+// atomic, and results are the same from run to run.
 //
 // Roles of a CTA (576 threads): warps 0-15 take the S and dP tiles from TMEM and
 // put P and dS back in 16 bits (four warpgroups of 32 columns each; a warp's
@@ -24,19 +25,30 @@
 // warps could not hide their own latencies (8 x 4096 causal tokens of 32 / 8 heads:
 // 3893 us with eight, 3496 with sixteen and the elected issuer below).
 //
-// Both are bound by the tensor cores: four (three) products of 512 cycles at D =
-// 128 stand against one exponential a pair (512 cycles of the SM's 32 a cycle).
+// Five of a CTA's 18 warps share a quarter of the SM's registers, 96 a thread, and
+// some values spill: at D = 128 in bf16 bwd_dq_kernel stores 84 bytes a thread and
+// loads 64 (148 and 168 with a mask, 92 and 140 in parts), bwd_dkv_kernel 24 and 56
+// (none with a mask, 40 and 80 in parts).
+//
+// Over long walks at D = 128 both are bound by the tensor cores: four (three)
+// products of 512 cycles stand against one exponential a pair (512 cycles of the SM's
+// 32 a cycle). Over short walks and at D = 64 they are bound by the warps' chain from
+// S to dS, a block at a time, and by the tiles' ends (the tensor pipe is busy for 51%
+// and 65% of the time with 8.5 blocks a tile, at D = 64 for 27% and 37% with 11 and 7:
+// about 2800 and 3000 cycles a block, ends included).
 // bwd_dq_kernel's products alone, in this order, take 2030 cycles a block, since
 // shared memory feeds two operands of each S and dP. Measured with all they wait
 // for: 2490 cycles a block where a tile has 16 of them, 3330 at 8; bwd_dkv_kernel
 // 2730 at 66, 3440 at 8 (delta and the results' stores stand between two tiles).
-// 8 x 4096 tokens take 2610 us: the seven products run at 1.47 PFLOP/s, near what
-// the tensor cores keep up at the clock that power leaves them in so long a call
-// (1.74 PFLOP/s for a library product); the five that are the work at 1.05.
+// 8 x 4096 tokens take 2590 to 2640 us: the seven products run at 1.46 to 1.49 PFLOP/s,
+// near what the tensor cores keep up at the clock that power leaves them in so long a
+// call (1.73 PFLOP/s for a library product); the five that are the work at 1.05.
 //
 // delta and the log-sum-exp in log2 units, negated, are left for the other kernel by bwd_dq_kernel, which has dO at hand: as
 // (B, Hq, Sp) with the rows of a head next to each other and padded to whole blocks, so that 128 of them are one bulk copy.
-// Rows that are none, and rows without a visible key (lse = -inf), get -inf: their probabilities become 2^-inf = 0.
+// Rows that are none, and rows without a visible key (lse = -inf), get -inf: their probabilities become 2^-inf = 0. With an
+// additive mask -(row maximum) or -lse and 1 / (row sum) or 1 are left instead, and those rows get 0 and 0: the factor of 0 makes
+// their probabilities 0, beside logits that must stay finite or -inf.
 //
 // P enters its product in the inputs' 16-bit type, as in the forward pass, and
 // so does dS: the tensor cores take both operands in one type. Each is rounded
@@ -47,7 +59,7 @@
 // the largest s that keeps |dS| <= 2 |dO_i| max_j |v_j| (norms of head vectors) within
 // 2^15 (-26 to 40), for each (b, K/V head) from its largest norms, which a pass over
 // dO and V ahead finds; the powers are taken back from the sums. (dV's error over 32000 keys: 4.4e-4 without, 3.0e-4
-// so, like dQ's and dK's; 3 x 777 queries over 1301 keys, 16 heads of 64: 82 and 89 us.)
+// so, like dQ's and dK's; 3 x 777 queries over 1301 keys, 16 heads of 64: 8 us of 90.)
 #pragma once
 
 #include "../../include/attn.h"

@@ -19,10 +19,11 @@ inline long long padded_rows(int Sq) { return ((long long)Sq + kBlock - 1) / kBl
 struct BwdParams {
     const uint16_t* o;              // (B, Sq, Hq, D) contiguous
     const float* lse;               // (B, Hq, Sq)
-    // (B, Hq, Sp) FP32, Sp = padded_rows(Sq), from the dQ kernel to the other one; a row that is none holds -inf and 0
-    float* neg_lse;                 // -lse in log2 units; with an additive mask: -(row maximum)
-    float* neg_delta;               // -sum_d dO O (in fp16 times what dS carries more than P)
-    float* inv_sum;                 // additive mask only: 1 / row sum
+    // (B, Hq, Sp) FP32, Sp = padded_rows(Sq), from the dQ kernel to the other one
+    float* neg_lse;                 // -lse in log2 units (fp16: and 14, which P carries); a row that is none, or sees no key: -inf.
+                                    // With an additive mask -lse, or -(row maximum) where the rows are found anew; such a row: 0
+    float* neg_delta;               // -sum_d dO O (in fp16 times what dS carries more than P); a row that is none: 0
+    float* inv_sum;                 // additive mask only: 1, or 1 / row sum (fp16: times 2^14); a row that is none, or sees no key: 0
     const float* mask;              // (B, Sq, Sk) FP32 or null
     void *dq, *dk, *dv;             // gradients in the inputs' type
     long long dq_stride, dk_stride, dv_stride;   // elements from token to token
