@@ -119,3 +119,22 @@ def test_from_checkpoints():
     assert _ds_max(d_o, q, k, v, True) > 65504
     # (o and lse are the forward call's, with P's rounding: delta by that much again)
     _check(got, want, [2 * b for b in bounds])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape,kw", [
+    ((1, 8, 1, 1500, 1500, 64), dict(causal=True)),                          # walks of both kernels in parts
+    ((1, 1, 1, 40, 6000, 128), dict()),
+    ((1, 16, 1, 700, 100, 64), dict(causal=False)),
+    ((1, 8, 1, 2000, 2000, 128), dict(causal=True, window=128, sinks=4)),     # the sinks' tiles in parts, the others whole
+    ((2, 16, 8, 600, 600, 64), dict(causal=True, window=100, sinks=0)),
+])
+def test_in_parts_and_windows(shape, kw):
+    """Powers below zero, taken back before the parts are joined or as a tile is stored."""
+    B, Hq, Hkv, Sq, Sk, D = shape
+    d_o, q, k, v = _normal([(B, Sq, Hq, D), (B, Sq, Hq, D), (B, Sk, Hkv, D), (B, Sk, Hkv, D)], (3000.0, 1.0, 1.0, 30.0), 6)
+    want, bounds = _want(d_o, q, k, v, **kw)
+    got = _grads(d_o, q, k, v, **kw)
+    _check(got, want, bounds, str(shape))
+    again = _grads(d_o, q, k, v, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
