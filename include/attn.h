@@ -568,8 +568,9 @@ int attn_bwd_f16(const void *d_o, const void *q, const void *k, const void *v, c
 
 /* attn_bwd_workspace_bytes — workspace bytes attn_bwd needs for these sizes on the
  * current device (with any window and sinks; host only; 0 for an empty problem or
- * invalid sizes): row statistics, and FP32 sums where few blocks of 128 queries or
- * keys would leave SMs idle and their work is divided. */
+ * invalid sizes): row statistics, what fp16's powers of two are found from, and FP32
+ * sums where few blocks of 128 queries or keys would leave SMs idle and their work is
+ * divided. */
 size_t attn_bwd_workspace_bytes(int B, int Hq, int Hkv, int Sq, int Sk, int D, int mask_kind);
 
 /*
